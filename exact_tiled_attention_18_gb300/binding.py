@@ -20,9 +20,16 @@ FA_ERR_MISALIGNED = 3
 FA_ERR_LAUNCH = 4
 FA_ERR_TIMEOUT = 5
 FA_ERR_DEVICE_FAULT = 6
+FA_ERR_BAD_PAGE = 7
 FA_DECODE_MAX_Q = 8
 FA_DTYPE_F32 = 0
 FA_DTYPE_BF16 = 1
+FA_ROPE_HALF = 0
+FA_ROPE_INTERLEAVED = 1
+FA_ROPE_SCALE_NONE = 0
+FA_ROPE_SCALE_LINEAR = 1
+FA_ROPE_SCALE_NTK = 2
+FA_ROPE_SCALE_PARTS = 3
 
 _lock = threading.Lock()
 _lib = None
@@ -84,6 +91,23 @@ def lib() -> ctypes.CDLL:
         L.fa_bwd_noalloc.restype = st
         L.fa_bwd_workspace_bytes.argtypes = [i, i, i]
         L.fa_bwd_workspace_bytes.restype = ctypes.c_size_t
+        db = ctypes.c_double
+        L.fa_rope_turns.argtypes = [ctypes.POINTER(ll), i, db, i, db, db, db, db]
+        L.fa_rope_turns.restype = st
+        L.fa_rope.argtypes = [vp, i, ll, ll, ll, vp, i, ll, ll, ll, vp, ll, vp, i, i, f, i, i, i, i, i, vp]
+        L.fa_rope.restype = st
+        L.fa_kv_append.argtypes = [vp, ll, ll, ll, vp, ll, ll, ll, vp, ll, ll, ll, vp, vp, vp, i, i, vp, ll, i, vp, vp,
+                                   vp, ll, vp, i, i, f, i, i, i, i, i, vp]
+        L.fa_kv_append.restype = st
+        L.fa_fwd_paged.argtypes = [vp, vp, vp, i, i, vp, ll, i, vp, i, vp, vp, vp, vp, i, i, i, i, i, f, i, vp]
+        L.fa_fwd_paged.restype = st
+        L.fa_fwd_paged_workspace_bytes.argtypes = [i, i, i, i, i]
+        L.fa_fwd_paged_workspace_bytes.restype = ctypes.c_size_t
+        L.fa_fwd_shared_prefix.argtypes = [vp, vp, vp, i, i, vp, i, vp, ll, i, vp, i, vp, vp, vp, vp, i, i, i, i, i, f,
+                                           i, vp]
+        L.fa_fwd_shared_prefix.restype = st
+        L.fa_fwd_shared_prefix_workspace_bytes.argtypes = [i, i, i, i, i]
+        L.fa_fwd_shared_prefix_workspace_bytes.restype = ctypes.c_size_t
         L.fa_sync_status.argtypes = [vp]
         L.fa_sync_status.restype = st
         L.fa_test_set_stall.argtypes = [i]
@@ -208,6 +232,50 @@ FA_NOALLOC_MAX_ROWS = 1 << 20
 
 def fa_bwd_workspace_bytes(B: int, H: int, N: int) -> int:
     return int(lib().fa_bwd_workspace_bytes(B, H, N))
+
+
+def fa_rope(x: int, x_dtype: int, x_strides: tuple, y: int, y_dtype: int, y_strides: tuple, positions: int,
+            positions_stride_b: int, turns: int, rot_dim: int, layout: int, amplitude: float, inverse: int, B: int,
+            H: int, N: int, d: int, stream: int) -> int:
+    """Raw C call; strides are (b, h, n) triples in elements."""
+    return lib().fa_rope(x, x_dtype, *x_strides, y, y_dtype, *y_strides, positions, positions_stride_b, turns, rot_dim,
+                         layout, amplitude, inverse, B, H, N, d, stream)
+
+
+def fa_kv_append(k: int, k_strides: tuple, v: int, v_strides: tuple, q: int, q_strides: tuple, q_out: int,
+                 k_pages: int, v_pages: int, num_pages: int, page_size: int, block_table: int, table_stride: int,
+                 max_pages: int, seqlens_q: int, seqlens_k: int, positions: int, positions_stride_b: int, turns: int,
+                 rot_dim: int, layout: int, amplitude: float, B: int, Hq: int, Hkv: int, N: int, d: int,
+                 stream: int) -> int:
+    """Raw C call; strides are (b, h, n) triples in elements."""
+    return lib().fa_kv_append(k, *k_strides, v, *v_strides, q, *q_strides, q_out, k_pages, v_pages, num_pages,
+                              page_size, block_table, table_stride, max_pages, seqlens_q, seqlens_k, positions,
+                              positions_stride_b, turns, rot_dim, layout, amplitude, B, Hq, Hkv, N, d, stream)
+
+
+def fa_fwd_paged(q: int, k_pages: int, v_pages: int, num_pages: int, page_size: int, block_table: int,
+                 table_stride: int, max_pages: int, o: int, o_dtype: int, lse: int, seqlens_q: int, seqlens_k: int,
+                 workspace: int, B: int, Hq: int, Hkv: int, Nq: int, d: int, scale: float, causal: int,
+                 stream: int) -> int:
+    return lib().fa_fwd_paged(q, k_pages, v_pages, num_pages, page_size, block_table, table_stride, max_pages, o,
+                              o_dtype, lse, seqlens_q, seqlens_k, workspace, B, Hq, Hkv, Nq, d, scale, causal, stream)
+
+
+def fa_fwd_paged_workspace_bytes(B: int, Hq: int, Hkv: int, Nq: int, d: int) -> int:
+    return lib().fa_fwd_paged_workspace_bytes(B, Hq, Hkv, Nq, d)
+
+
+def fa_fwd_shared_prefix(q: int, k_pages: int, v_pages: int, num_pages: int, page_size: int, prefix_table: int,
+                         prefix_len: int, block_table: int, table_stride: int, max_pages: int, o: int, o_dtype: int,
+                         lse: int, seqlens_q: int, seqlens_k: int, workspace: int, B: int, Hq: int, Hkv: int, Nq: int,
+                         d: int, scale: float, causal: int, stream: int) -> int:
+    return lib().fa_fwd_shared_prefix(q, k_pages, v_pages, num_pages, page_size, prefix_table, prefix_len, block_table,
+                                      table_stride, max_pages, o, o_dtype, lse, seqlens_q, seqlens_k, workspace, B, Hq,
+                                      Hkv, Nq, d, scale, causal, stream)
+
+
+def fa_fwd_shared_prefix_workspace_bytes(B: int, Hq: int, Hkv: int, Nq: int, d: int) -> int:
+    return lib().fa_fwd_shared_prefix_workspace_bytes(B, Hq, Hkv, Nq, d)
 
 
 def fa_sync_status(stream: int) -> int:
@@ -560,9 +628,223 @@ def backward_stage(stage: int, q, k, v, o, lse, do, dq, dk, dv, workspace, causa
                         B, H, N, d, scale, int(bool(causal)), _stream_handle(q.device)))
 
 
+# ------------------------------------------- rotary positions, paged cache
+
+_ROPE_LAYOUTS = {"half": FA_ROPE_HALF, "interleaved": FA_ROPE_INTERLEAVED}
+_ROPE_SCALINGS = {None: FA_ROPE_SCALE_NONE, "linear": FA_ROPE_SCALE_LINEAR, "ntk": FA_ROPE_SCALE_NTK,
+                  "parts": FA_ROPE_SCALE_PARTS}
+
+
+def _need(ok: bool, message: str) -> None:
+    if not ok:
+        raise ValueError(message)
+
+
+def _call_on(index: int, call, *args) -> int:
+    """The C call with the tensors' device current (its kernels launch there)
+    on that device's current PyTorch stream."""
+    import torch
+    stream = torch.cuda.current_stream(index).cuda_stream
+    if torch.cuda.current_device() == index:
+        return call(*args, stream)
+    with torch.cuda.device(index):
+        return call(*args, stream)
+
+
+def rope_turns(rot_dim: int, base: float = 10000.0, scaling: str | None = None, factor: float = 1.0,
+               original_len: float = 1.0, low: float = 1.0, high: float = 32.0, device=None):
+    """The frequency table of the rotary calls through fa_rope_turns: int64
+    [rot_dim / 2], in units of 2^-64 turns per position, on ``device``.
+    ``scaling``: None, "linear", "ntk" or "parts" (see include/fa.h)."""
+    import torch
+    _need(scaling in _ROPE_SCALINGS, "scaling must be None, 'linear', 'ntk' or 'parts'")
+    out = (ctypes.c_longlong * max(int(rot_dim) // 2, 1))()
+    _check("fa_rope_turns", lib().fa_rope_turns(out, rot_dim, base, _ROPE_SCALINGS[scaling], factor, original_len, low,
+                                                high))
+    return torch.tensor(list(out), dtype=torch.int64, device=device)
+
+
+def _rope_args(turns, layout, positions, B, N, device):
+    """(turns, rot_dim, layout, positions, positions stride) of a rotary call."""
+    import torch
+    _need(layout in _ROPE_LAYOUTS, "layout must be 'half' or 'interleaved'")
+    _need(turns.dtype == torch.int64 and turns.dim() == 1 and turns.is_contiguous() and turns.device == device,
+          "turns must be a contiguous int64 tensor of rot_dim / 2 entries on the inputs' device")
+    pos, stride = 0, 0
+    if positions is not None:
+        _need(positions.dtype == torch.int32 and positions.device == device and positions.dim() in (1, 2)
+              and positions.shape[-1] == N and (N == 1 or positions.stride(-1) == 1)
+              and (positions.dim() == 1 or positions.shape[0] == B),
+              "positions must be int32 [N] or [B, N] on the inputs' device with contiguous rows")
+        pos = positions.data_ptr()
+        stride = positions.stride(0) if positions.dim() == 2 else 0
+    return turns.data_ptr(), 2 * turns.numel(), _ROPE_LAYOUTS[layout], pos, stride
+
+
+def _rope(x, turns, positions, layout, amplitude, inverse, out, out_dtype):
+    import torch
+    _need(x.is_cuda and x.dim() == 4 and x.dtype in (torch.bfloat16, torch.float32) and x.stride(3) == 1,
+          "x must be a bf16 or fp32 CUDA tensor [B, H, N, d] with contiguous d")
+    B, H, N, d = x.shape
+    t, rot_dim, lay, pos, pos_stride = _rope_args(turns, layout, positions, B, N, x.device)
+    if out is None:
+        out = torch.empty((B, H, N, d), dtype=out_dtype or x.dtype, device=x.device)
+    _need(out.shape == x.shape and out.device == x.device and out.dtype in (torch.bfloat16, torch.float32)
+          and out.stride(3) == 1 and out_dtype in (None, out.dtype),
+          "out must be a bf16 or fp32 tensor of x's shape and device with contiguous d")
+    xs, ys = x.stride(), out.stride()
+    _check("fa_rope", _call_on(x.device.index, lib().fa_rope, x.data_ptr(), int(x.dtype == torch.bfloat16), xs[0],
+                               xs[1], xs[2], out.data_ptr(), int(out.dtype == torch.bfloat16), ys[0], ys[1], ys[2],
+                               pos, pos_stride, t, rot_dim, lay, amplitude, inverse, B, H, N, d))
+    return out
+
+
+def rope_forward(x, turns, positions=None, layout: str = "half", amplitude: float = 1.0, out=None, out_dtype=None):
+    """x [B, H, N, d] (bf16 or fp32 CUDA, contiguous d, any other strides)
+    with its first 2 * len(turns) values rotated by their positions, through
+    fa_rope.  ``turns``: rope_turns(...) on x's device; ``positions``: int32
+    [N] or [B, N] (default 0 .. N - 1); ``layout``: "half" or "interleaved".
+    ``out`` may be x itself.  Returns ``out`` (contiguous if it is made here)."""
+    return _rope(x, turns, positions, layout, amplitude, 0, out, out_dtype)
+
+
+def rope_backward(dy, turns, positions=None, layout: str = "half", amplitude: float = 1.0, out=None, out_dtype=None):
+    """The gradient with respect to x of rope_forward with the same arguments,
+    given dy = dL/dy (bf16 or fp32)."""
+    return _rope(dy, turns, positions, layout, amplitude, 1, out, out_dtype)
+
+
+def _page_args(k_pages, v_pages, block_table, B, d, device):
+    """(num_pages, Hkv, page_size, max_pages) of a paged cache's tensors."""
+    import torch
+    _need(k_pages.dim() == 4 and k_pages.dtype == torch.bfloat16 and k_pages.is_contiguous()
+          and v_pages.dtype == torch.bfloat16 and v_pages.is_contiguous() and v_pages.shape == k_pages.shape
+          and k_pages.device == device and v_pages.device == device and k_pages.shape[3] == d,
+          "k_pages and v_pages must be contiguous bf16 [pages, Hkv, page_size, d] on the inputs' device")
+    _need(block_table.dim() == 2 and block_table.dtype == torch.int32 and block_table.shape[0] == B
+          and block_table.device == device and (block_table.shape[1] == 1 or block_table.stride(1) == 1),
+          "block_table must be int32 [B, max_pages] on the inputs' device with contiguous rows")
+    return k_pages.shape[0], k_pages.shape[1], k_pages.shape[2], block_table.shape[1]
+
+
+def _lens(t, B, device) -> int:
+    import torch
+    if t is None:
+        return 0
+    _need(t.dtype == torch.int32 and t.numel() == B and t.is_contiguous() and t.device == device,
+          "seqlens must be contiguous int32 tensors of B entries on the inputs' device")
+    return t.data_ptr()
+
+
+def kv_append(k, v, k_pages, v_pages, block_table, seqlens_k, seqlens_q=None, turns=None, layout: str = "half",
+              amplitude: float = 1.0, positions=None, q=None, q_out=None):
+    """Appends k and v [B, Hkv, N, d] (bf16 CUDA, contiguous d, any other
+    strides) to the paged cache through fa_kv_append, the keys rotated by
+    their positions if ``turns`` is given; with ``q`` [B, Hq, N, d] also
+    rotates the queries, into ``q_out`` (contiguous; made here by default, its
+    padding rows then unset).  ``seqlens_k``: int32 [B], each sequence's keys
+    with the new tokens; ``seqlens_q``: int32 [B], its new tokens (default N).
+    Returns q_out, or None without q."""
+    import torch
+    for t in (k, v) + ((q,) if q is not None else ()):
+        _need(t.is_cuda and t.dim() == 4 and t.dtype == torch.bfloat16 and t.stride(3) == 1 and t.device == k.device,
+              "q, k and v must be bf16 CUDA tensors [B, heads, N, d] of one device with contiguous d")
+    B, Hkv, N, d = k.shape
+    _need(v.shape == k.shape, "v must have k's shape")
+    num_pages, page_heads, page_size, max_pages = _page_args(k_pages, v_pages, block_table, B, d, k.device)
+    _need(page_heads == Hkv, "the pages must have k's heads")
+    _need(seqlens_k is not None, "seqlens_k is needed")
+    tp = rot_dim = lay = pos = pos_stride = 0
+    if turns is not None:
+        tp, rot_dim, lay, pos, pos_stride = _rope_args(turns, layout, positions, B, N, k.device)
+    else:
+        _need(positions is None, "positions without turns")
+    qp = op = Hq = 0
+    qs = (0, 0, 0)
+    if q is not None:
+        Hq = q.shape[1]
+        _need(q.shape == (B, Hq, N, d), "q must be [B, Hq, N, d] with the batch, length and d of k")
+        if q_out is None:
+            q_out = torch.empty((B, Hq, N, d), dtype=torch.bfloat16, device=k.device)
+        _need(q_out.shape == q.shape and q_out.dtype == torch.bfloat16 and q_out.is_contiguous()
+              and q_out.device == k.device, "q_out must be contiguous bf16 of q's shape")
+        qp, qs, op = q.data_ptr(), q.stride(), q_out.data_ptr()
+    else:
+        _need(q_out is None, "q_out without q")
+    ks, vs = k.stride(), v.stride()
+    _check("fa_kv_append",
+           _call_on(k.device.index, lib().fa_kv_append, k.data_ptr(), ks[0], ks[1], ks[2], v.data_ptr(), vs[0], vs[1],
+                    vs[2], qp, qs[0], qs[1], qs[2], op, k_pages.data_ptr(), v_pages.data_ptr(), num_pages, page_size,
+                    block_table.data_ptr(), block_table.stride(0), max_pages, _lens(seqlens_q, B, k.device),
+                    _lens(seqlens_k, B, k.device), pos, pos_stride, tp, rot_dim, lay, amplitude, B, Hq, Hkv, N, d))
+    return q_out
+
+
+def _paged(name, q, k_pages, v_pages, prefix, block_table, seqlens_k, seqlens_q, causal, scale, o_dtype, workspace,
+           out):
+    import torch
+    _need(q.is_cuda and q.dtype == torch.bfloat16 and q.is_contiguous() and q.dim() == 4,
+          "q must be a contiguous bf16 CUDA tensor [B, Hq, Nq, d]")
+    B, Hq, Nq, d = q.shape
+    dev = q.device
+    num_pages, Hkv, page_size, max_pages = _page_args(k_pages, v_pages, block_table, B, d, dev)
+    if scale is None:
+        scale = float(torch.tensor(d ** -0.5, dtype=torch.float32))
+    if out is None:
+        o = torch.empty((B, Hq, Nq, d), dtype=o_dtype or torch.float32, device=dev)
+        lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=dev)
+    else:
+        o, lse = out
+    _need(o.dtype in (torch.float32, torch.bfloat16), "O must be float32 or bfloat16")
+    _need(o.shape == q.shape and o.is_contiguous() and o.device == dev and lse.shape == q.shape[:3]
+          and lse.dtype == torch.float32 and lse.is_contiguous() and lse.device == dev,
+          "out must be contiguous O [B, Hq, Nq, d] and fp32 LSE [B, Hq, Nq] on q's device")
+    L = lib()
+    call = getattr(L, name)
+    need = getattr(L, name + "_workspace_bytes")(B, Hq, Hkv, Nq, d)
+    if workspace is None:
+        workspace = torch.empty(need // 4, dtype=torch.float32, device=dev)
+    _need(workspace.dtype == torch.float32 and workspace.is_contiguous() and workspace.device == dev
+          and 4 * workspace.numel() >= need, f"workspace must be fp32 on q's device, {name}_workspace_bytes(...) bytes")
+    _check(name, _call_on(dev.index, call, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), num_pages, page_size,
+                          *prefix, block_table.data_ptr(), block_table.stride(0), max_pages, o.data_ptr(),
+                          FA_DTYPE_BF16 if o.dtype == torch.bfloat16 else FA_DTYPE_F32, lse.data_ptr(),
+                          _lens(seqlens_q, B, dev), _lens(seqlens_k, B, dev), workspace.data_ptr(), B, Hq, Hkv, Nq, d,
+                          scale, int(bool(causal))))
+    return o, lse
+
+
+def forward_paged(q, k_pages, v_pages, block_table, seqlens_k=None, seqlens_q=None, causal: bool = True,
+                  scale: float | None = None, o_dtype=None, workspace=None, out=None):
+    """O, LSE through fa_fwd_paged: q [B, Hq, Nq, d] (bf16 CUDA, contiguous)
+    against the keys and values that ``block_table`` int32 [B, max_pages]
+    names in k_pages, v_pages [pages, Hkv, page_size, d]; Hq a multiple of
+    Hkv.  ``seqlens_k``, ``seqlens_q``: int32 [B] as kv_append.  ``workspace``:
+    an fp32 tensor of fa_fwd_paged_workspace_bytes(...) bytes, made here by
+    default."""
+    return _paged("fa_fwd_paged", q, k_pages, v_pages, (), block_table, seqlens_k, seqlens_q, causal, scale, o_dtype,
+                  workspace, out)
+
+
+def forward_shared_prefix(q, k_pages, v_pages, prefix_table, prefix_len: int, block_table, seqlens_k=None,
+                          seqlens_q=None, causal: bool = True, scale: float | None = None, o_dtype=None,
+                          workspace=None, out=None):
+    """forward_paged for a batch whose sequences share their first
+    ``prefix_len`` keys (a multiple of the page size), in the pages that
+    ``prefix_table`` int32 [prefix_len / page_size] names: that part is
+    computed once for all, through fa_fwd_shared_prefix."""
+    import torch
+    _need(prefix_table.dtype == torch.int32 and prefix_table.dim() == 1 and prefix_table.is_contiguous()
+          and prefix_table.device == q.device and prefix_len >= 1
+          and prefix_table.numel() * k_pages.shape[2] >= prefix_len,
+          "prefix_table must be contiguous int32 on q's device with an entry for every page of the prefix")
+    return _paged("fa_fwd_shared_prefix", q, k_pages, v_pages, (prefix_table.data_ptr(), int(prefix_len)), block_table,
+                  seqlens_k, seqlens_q, causal, scale, o_dtype, workspace, out)
+
+
 def sync_status(device=None) -> None:
     """Synchronise the current stream and raise if a kernel reported a failure."""
     status = fa_sync_status(_stream_handle(device))
     if status != FA_OK:
-        detail = fa_last_failure() if status == FA_ERR_TIMEOUT else None
+        detail = fa_last_failure() if status in (FA_ERR_TIMEOUT, FA_ERR_BAD_PAGE) else None
         raise FAError("fa_sync_status", status, fa_status_string(status) + (f" {detail}" if detail else ""))

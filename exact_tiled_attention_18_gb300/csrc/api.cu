@@ -14,6 +14,7 @@
 
 #include "../../include/fa.h"
 #include "internal.h"
+#include "serving.h"
 
 // Device status word written by the kernels when a bounded wait gives up:
 // [0] code, [1] wait site, [2] block, [3] work unit.  First failure wins.
@@ -364,6 +365,89 @@ fa_status bwd_launch(fa::BwdArgs& a, float* workspace, int B, int H, int Nq, fa_
   return e == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
 }
 
+// ------------------------------------------- rotary positions, paged cache
+
+// Strides of the dimensions that are walked; the stride of a dimension of
+// size one means nothing and is dropped.
+fa::Strides used_strides(long long sb, long long sh, long long sn, int B, int H, int N) {
+  return fa::Strides{B > 1 ? sb : 0, H > 1 ? sh : 0, N > 1 ? sn : 0};
+}
+
+fa_status check_strides(const fa::Strides& s, int elem_bytes) {
+  if (s.b < 0 || s.h < 0 || s.n < 0) return FA_ERR_INVALID_ARG;
+  const long long unit = 16 / elem_bytes;  // rows start on 16-byte boundaries
+  return s.b % unit || s.h % unit || s.n % unit ? FA_ERR_MISALIGNED : FA_OK;
+}
+
+fa_status check_rope(const long long* turns, int rot_dim, int layout, float amplitude, const int* positions,
+                     long long positions_sb, int d) {
+  if (rot_dim < 16 || rot_dim > d || rot_dim % 16 != 0 || !turns) return FA_ERR_INVALID_ARG;
+  if (layout != FA_ROPE_HALF && layout != FA_ROPE_INTERLEAVED) return FA_ERR_INVALID_ARG;
+  if (!std::isfinite(amplitude) || positions_sb < 0) return FA_ERR_INVALID_ARG;
+  if (!aligned(turns, 8) || (positions && !aligned(positions, 4))) return FA_ERR_MISALIGNED;
+  return FA_OK;
+}
+
+// The cache's own sizes: pages of whole 16-key groups, positions and head
+// rows of pages that fit 32 bits.
+fa_status check_pages(const void* k_pages, const void* v_pages, int num_pages, int page_size, const int* block_table,
+                      long long table_stride, int max_pages, int Hkv) {
+  if (!k_pages || !v_pages || !block_table) return FA_ERR_INVALID_ARG;
+  if (num_pages < 1 || max_pages < 1 || page_size < 16 || page_size % 16 != 0 || table_stride < 0)
+    return FA_ERR_INVALID_ARG;
+  const long long limit = 1LL << 31;
+  if (static_cast<long long>(max_pages) * page_size >= limit) return FA_ERR_INVALID_ARG;
+  if (static_cast<long long>(num_pages) * Hkv >= limit) return FA_ERR_INVALID_ARG;
+  if (!aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(block_table, 4)) return FA_ERR_MISALIGNED;
+  return FA_OK;
+}
+
+fa_status paged_common(const void* q, const void* k_pages, const void* v_pages, int num_pages, int page_size,
+                       const int* prefix_table, int prefix_len, const int* block_table, long long table_stride,
+                       int max_pages, void* o, int o_dtype, float* lse, const int* seqlens_q, const int* seqlens_k,
+                       float* workspace, int B, int Hq, int Hkv, int Nq, int d, float scale, int causal,
+                       fa_stream_t stream) {
+  if (!q || !o || !lse) return FA_ERR_INVALID_ARG;
+  if (o_dtype != FA_DTYPE_F32 && o_dtype != FA_DTYPE_BF16) return FA_ERR_INVALID_ARG;
+  fa_status st = check_sizes(B, Hq, Nq, d, causal);
+  if (st != FA_OK) return st;
+  if (Hkv < 1 || Hq % Hkv != 0) return FA_ERR_INVALID_ARG;
+  if (!std::isfinite(scale) || !(scale > 0.f)) return FA_ERR_INVALID_ARG;
+  st = check_pages(k_pages, v_pages, num_pages, page_size, block_table, table_stride, max_pages, Hkv);
+  if (st != FA_OK) return st;
+  if (!aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 4) || (workspace && !aligned(workspace, 16)) ||
+      (seqlens_q && !aligned(seqlens_q, 4)) || (seqlens_k && !aligned(seqlens_k, 4)) ||
+      (prefix_table && !aligned(prefix_table, 4)))
+    return FA_ERR_MISALIGNED;
+  DeviceInfo di;
+  if (device_info(di) != FA_OK) return FA_ERR_LAUNCH;
+  fa::PagedArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.q = static_cast<const uint16_t*>(q);
+  a.k_pages = static_cast<const uint16_t*>(k_pages);
+  a.v_pages = static_cast<const uint16_t*>(v_pages);
+  a.table = fa::PageTable{block_table, table_stride, max_pages, page_size, num_pages};
+  a.prefix_table = prefix_table;
+  a.prefix_len = prefix_len;
+  a.o = o;
+  a.o_bf16 = o_dtype == FA_DTYPE_BF16;
+  a.lse = lse;
+  a.part = workspace;
+  a.seqlens_q = seqlens_q;
+  a.seqlens_k = seqlens_k;
+  a.B = B;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.Nq = Nq;
+  a.d = d;
+  a.causal = causal;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.sms = di.sms;
+  a.status = di.status;
+  a.wait_limit_ns = wait_limit_ns();
+  a.stall_unit = test_stall_unit();
+  return fa::launch_paged(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
+}
 
 }  // namespace
 
@@ -671,6 +755,166 @@ fa_status fa_bwd_stage(int stage, const void* q, const void* k, const void* v, c
                                                                                               : FA_ERR_LAUNCH;
 }
 
+fa_status fa_rope_turns(long long* turns, int rot_dim, double base, int scaling, double factor, double original_len,
+                        double low, double high) {
+  if (!turns || rot_dim < 16 || rot_dim % 16 != 0 || !std::isfinite(base) || !(base > 1.0)) return FA_ERR_INVALID_ARG;
+  if (scaling < FA_ROPE_SCALE_NONE || scaling > FA_ROPE_SCALE_PARTS) return FA_ERR_INVALID_ARG;
+  if (scaling != FA_ROPE_SCALE_NONE && (!std::isfinite(factor) || !(factor >= 1.0))) return FA_ERR_INVALID_ARG;
+  if (scaling == FA_ROPE_SCALE_PARTS &&
+      (!std::isfinite(original_len) || !(original_len > 0.0) || !std::isfinite(low) || !std::isfinite(high) ||
+       !(low >= 0.0) || !(high > low)))
+    return FA_ERR_INVALID_ARG;
+  constexpr double kTwoPi = 6.283185307179586;
+  if (scaling == FA_ROPE_SCALE_NTK) base *= std::pow(factor, rot_dim / (rot_dim - 2.0));
+  if (!std::isfinite(base)) return FA_ERR_INVALID_ARG;
+  for (int i = 0; i < rot_dim / 2; ++i) {
+    double f = std::pow(base, -2.0 * i / rot_dim);  // radians per position
+    if (scaling == FA_ROPE_SCALE_LINEAR) f /= factor;
+    if (scaling == FA_ROPE_SCALE_PARTS) {
+      double keep = (f * original_len / kTwoPi - low) / (high - low);
+      keep = keep < 0.0 ? 0.0 : (keep > 1.0 ? 1.0 : keep);
+      f = f * keep + f / factor * (1.0 - keep);
+    }
+    turns[i] = std::llround(std::ldexp(f / kTwoPi, 64));  // f <= 1: below 2^62
+  }
+  return FA_OK;
+}
+
+fa_status fa_rope(const void* x, int x_dtype, long long x_stride_b, long long x_stride_h, long long x_stride_n,
+                  void* y, int y_dtype, long long y_stride_b, long long y_stride_h, long long y_stride_n,
+                  const int* positions, long long positions_stride_b, const long long* turns, int rot_dim, int layout,
+                  float amplitude, int inverse, int B, int H, int N, int d, fa_stream_t stream) {
+  if (!x || !y || (inverse != 0 && inverse != 1)) return FA_ERR_INVALID_ARG;
+  if ((x_dtype != FA_DTYPE_F32 && x_dtype != FA_DTYPE_BF16) || (y_dtype != FA_DTYPE_F32 && y_dtype != FA_DTYPE_BF16))
+    return FA_ERR_INVALID_ARG;
+  fa_status st = check_sizes(B, H, N, d, 0);
+  if (st != FA_OK) return st;
+  st = check_rope(turns, rot_dim, layout, amplitude, positions, positions_stride_b, d);
+  if (st != FA_OK) return st;
+  const int xe = x_dtype == FA_DTYPE_BF16 ? 2 : 4, ye = y_dtype == FA_DTYPE_BF16 ? 2 : 4;
+  const fa::Strides xs = used_strides(x_stride_b, x_stride_h, x_stride_n, B, H, N);
+  const fa::Strides ys = used_strides(y_stride_b, y_stride_h, y_stride_n, B, H, N);
+  // rows of y that fall on one another would race
+  if ((B > 1 && ys.b == 0) || (H > 1 && ys.h == 0) || (N > 1 && ys.n == 0)) return FA_ERR_INVALID_ARG;
+  // in place only element for element
+  if (x == y && (x_dtype != y_dtype || xs.b != ys.b || xs.h != ys.h || xs.n != ys.n)) return FA_ERR_INVALID_ARG;
+  if (!aligned(x, 16) || !aligned(y, 16)) return FA_ERR_MISALIGNED;
+  if ((st = check_strides(xs, xe)) != FA_OK || (st = check_strides(ys, ye)) != FA_OK) return st;
+  DeviceInfo di;
+  if (device_info(di) != FA_OK) return FA_ERR_LAUNCH;
+  fa::RopeArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.x = x;
+  a.y = y;
+  a.x_bf16 = x_dtype == FA_DTYPE_BF16;
+  a.y_bf16 = y_dtype == FA_DTYPE_BF16;
+  a.xs = xs;
+  a.ys = ys;
+  a.rope = fa::RopeRef{turns, positions, positions_stride_b, rot_dim, layout == FA_ROPE_INTERLEAVED, amplitude};
+  a.inverse = inverse;
+  a.B = B;
+  a.H = H;
+  a.N = N;
+  a.d = d;
+  a.sms = di.sms;
+  return fa::launch_rope(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
+}
+
+fa_status fa_kv_append(const void* k, long long k_stride_b, long long k_stride_h, long long k_stride_n, const void* v,
+                       long long v_stride_b, long long v_stride_h, long long v_stride_n, const void* q,
+                       long long q_stride_b, long long q_stride_h, long long q_stride_n, void* q_out, void* k_pages,
+                       void* v_pages, int num_pages, int page_size, const int* block_table, long long table_stride,
+                       int max_pages, const int* seqlens_q, const int* seqlens_k, const int* positions,
+                       long long positions_stride_b, const long long* turns, int rot_dim, int layout, float amplitude,
+                       int B, int Hq, int Hkv, int N, int d, fa_stream_t stream) {
+  if (!k || !v || !seqlens_k || (q != nullptr) != (q_out != nullptr)) return FA_ERR_INVALID_ARG;
+  fa_status st = check_sizes(B, Hkv, N, d, 0);
+  if (st != FA_OK) return st;
+  if (q) {
+    st = check_sizes(B, Hq, N, d, 0);
+    if (st != FA_OK) return st;
+  }
+  if (turns) {
+    st = check_rope(turns, rot_dim, layout, amplitude, positions, positions_stride_b, d);
+    if (st != FA_OK) return st;
+  } else if (positions) {
+    return FA_ERR_INVALID_ARG;  // positions of a rotation that is not asked for
+  }
+  st = check_pages(k_pages, v_pages, num_pages, page_size, block_table, table_stride, max_pages, Hkv);
+  if (st != FA_OK) return st;
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(seqlens_k, 4) || (seqlens_q && !aligned(seqlens_q, 4)))
+    return FA_ERR_MISALIGNED;
+  const fa::Strides ks = used_strides(k_stride_b, k_stride_h, k_stride_n, B, Hkv, N);
+  const fa::Strides vs = used_strides(v_stride_b, v_stride_h, v_stride_n, B, Hkv, N);
+  if ((st = check_strides(ks, 2)) != FA_OK || (st = check_strides(vs, 2)) != FA_OK) return st;
+  fa::Strides qs{0, 0, 0};
+  if (q) {
+    if (!aligned(q, 16) || !aligned(q_out, 16)) return FA_ERR_MISALIGNED;
+    qs = used_strides(q_stride_b, q_stride_h, q_stride_n, B, Hq, N);
+    if ((st = check_strides(qs, 2)) != FA_OK) return st;
+    // q_out is contiguous: in place only for a contiguous q
+    const fa::Strides cs = used_strides(static_cast<long long>(Hq) * N * d, static_cast<long long>(N) * d, d, B, Hq, N);
+    if (q == q_out && (qs.b != cs.b || qs.h != cs.h || qs.n != cs.n)) return FA_ERR_INVALID_ARG;
+  }
+  DeviceInfo di;
+  if (device_info(di) != FA_OK) return FA_ERR_LAUNCH;
+  fa::AppendArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.q = static_cast<const uint16_t*>(q);
+  a.k = static_cast<const uint16_t*>(k);
+  a.v = static_cast<const uint16_t*>(v);
+  a.qs = qs;
+  a.ks = ks;
+  a.vs = vs;
+  a.q_out = static_cast<uint16_t*>(q_out);
+  a.k_pages = static_cast<uint16_t*>(k_pages);
+  a.v_pages = static_cast<uint16_t*>(v_pages);
+  a.table = fa::PageTable{block_table, table_stride, max_pages, page_size, num_pages};
+  if (turns)
+    a.rope = fa::RopeRef{turns, positions, positions_stride_b, rot_dim, layout == FA_ROPE_INTERLEAVED, amplitude};
+  a.seqlens_q = seqlens_q;
+  a.seqlens_k = seqlens_k;
+  a.B = B;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.N = N;
+  a.d = d;
+  a.sms = di.sms;
+  a.status = di.status;
+  return fa::launch_kv_append(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
+}
+
+size_t fa_fwd_paged_workspace_bytes(int B, int Hq, int Hkv, int Nq, int d) {
+  if (B < 1 || Hq < 1 || Hkv < 1 || Nq < 1 || Hq % Hkv != 0 || (d != 64 && d != 128)) return 0;
+  if (static_cast<long long>(B) * Hq * Nq >= (1LL << 31)) return 0;
+  return 16;
+}
+
+fa_status fa_fwd_paged(const void* q, const void* k_pages, const void* v_pages, int num_pages, int page_size,
+                       const int* block_table, long long table_stride, int max_pages, void* o, int o_dtype,
+                       float* lse, const int* seqlens_q, const int* seqlens_k, float* workspace, int B, int Hq,
+                       int Hkv, int Nq, int d, float scale, int causal, fa_stream_t stream) {
+  return paged_common(q, k_pages, v_pages, num_pages, page_size, nullptr, 0, block_table, table_stride, max_pages, o,
+                      o_dtype, lse, seqlens_q, seqlens_k, workspace, B, Hq, Hkv, Nq, d, scale, causal, stream);
+}
+
+size_t fa_fwd_shared_prefix_workspace_bytes(int B, int Hq, int Hkv, int Nq, int d) {
+  return fa_fwd_paged_workspace_bytes(B, Hq, Hkv, Nq, d);
+}
+
+fa_status fa_fwd_shared_prefix(const void* q, const void* k_pages, const void* v_pages, int num_pages, int page_size,
+                               const int* prefix_table, int prefix_len, const int* block_table,
+                               long long table_stride, int max_pages, void* o, int o_dtype, float* lse,
+                               const int* seqlens_q, const int* seqlens_k, float* workspace, int B, int Hq, int Hkv,
+                               int Nq, int d, float scale, int causal, fa_stream_t stream) {
+  if (!prefix_table || page_size < 16 || prefix_len < page_size || prefix_len % page_size != 0)
+    return FA_ERR_INVALID_ARG;
+  if (prefix_len / page_size > max_pages) return FA_ERR_INVALID_ARG;
+  return paged_common(q, k_pages, v_pages, num_pages, page_size, prefix_table, prefix_len, block_table, table_stride,
+                      max_pages, o, o_dtype, lse, seqlens_q, seqlens_k, workspace, B, Hq, Hkv, Nq, d, scale, causal,
+                      stream);
+}
+
 fa_status fa_sync_status(fa_stream_t stream) {
   if (cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return FA_ERR_DEVICE_FAULT;
   int h[4] = {0, 0, 0, 0};
@@ -682,7 +926,7 @@ fa_status fa_sync_status(fa_stream_t stream) {
     }
     const int zero[4] = {0, 0, 0, 0};
     if (cudaMemcpyToSymbol(g_fa_status, zero, sizeof(zero)) != cudaSuccess) return FA_ERR_DEVICE_FAULT;
-    return h[0] == FA_ERR_TIMEOUT ? FA_ERR_TIMEOUT : FA_ERR_DEVICE_FAULT;
+    return h[0] == FA_ERR_TIMEOUT || h[0] == FA_ERR_BAD_PAGE ? static_cast<fa_status>(h[0]) : FA_ERR_DEVICE_FAULT;
   }
   return FA_OK;
 }
@@ -709,6 +953,7 @@ const char* fa_status_string(fa_status s) {
     case FA_ERR_LAUNCH: return "FA_ERR_LAUNCH: the CUDA runtime refused a launch or an allocation";
     case FA_ERR_TIMEOUT: return "FA_ERR_TIMEOUT: a kernel pipeline wait ran past its limit";
     case FA_ERR_DEVICE_FAULT: return "FA_ERR_DEVICE_FAULT: the stream reported a CUDA error";
+    case FA_ERR_BAD_PAGE: return "FA_ERR_BAD_PAGE: a block table names a page outside the cache";
   }
   return "unknown fa_status";
 }

@@ -1,0 +1,115 @@
+// Interface between the C-ABI translation unit and the kernels of rotary
+// positions, the paged key/value cache and the attention that reads it.  Not
+// part of the public boundary (that is include/fa.h).
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+namespace fa {
+
+// Status codes these kernels leave in the device status word, besides the
+// timeout of ptx.cuh.
+constexpr int FA_DEV_BAD_PAGE = 7;
+
+// Sites recorded with FA_DEV_BAD_PAGE.
+enum PageSite : int { SITE_PAGE_APPEND = 71, SITE_PAGE_READ = 72 };
+
+// A [B][H][N][d] tensor with contiguous d: element strides of the others.
+struct Strides {
+  long long b, h, n;
+};
+
+// Where position p of sequence b lives: page block_table[b * table_stride +
+// p / page_size], row p % page_size, of pages [num_pages][Hkv][page_size][d].
+struct PageTable {
+  const int* block_table;
+  long long table_stride;
+  int max_pages;   // entries per sequence that may be read
+  int page_size;   // a multiple of 16
+  int num_pages;   // page ids are valid in [0, num_pages)
+};
+
+// The rotation of a token at position p: pair i turns by p * turns[i] / 2^64
+// of a full turn, and the pair's values are multiplied by `amplitude`.
+struct RopeRef {
+  const long long* turns;  // [rot_dim / 2]; null: no rotation
+  const int* positions;    // [B][N] (stride positions_sb between sequences), or null
+  long long positions_sb;
+  int rot_dim;             // a multiple of 16, at most d; 0: no rotation
+  int interleaved;         // 0: pairs (i, i + rot_dim / 2), 1: pairs (2i, 2i + 1)
+  float amplitude;
+};
+
+struct RopeArgs {
+  const void* x;
+  void* y;
+  int x_bf16, y_bf16;
+  Strides xs, ys;
+  RopeRef rope;
+  int inverse;
+  int B, H, N, d;
+  int sms;
+};
+
+struct AppendArgs {
+  const uint16_t *q, *k, *v;  // q may be null
+  Strides qs, ks, vs;
+  uint16_t* q_out;            // [B][Hq][N][d]
+  uint16_t *k_pages, *v_pages;
+  PageTable table;
+  RopeRef rope;               // positions null: the cache position
+  const int *seqlens_q, *seqlens_k;
+  int B, Hq, Hkv, N, d;
+  int sms;
+  int* status;
+};
+
+struct PagedArgs {
+  CUtensorMap tm_k, tm_v;     // 3-D maps over [num_pages * Hkv][page_size][d] bf16, boxes of 64 columns x box_rows
+  const uint16_t *q;          // [B][Hq][Nq][d]
+  const uint16_t *k_pages, *v_pages;
+  PageTable table;
+  const int* prefix_table;    // pages of the shared prefix
+  int prefix_len;             // keys of the shared prefix, a multiple of page_size; 0: none
+  void* o;                    // [B][Hq][Nq][d] fp32, or bf16 when o_bf16
+  int o_bf16;
+  float* lse;                 // [B][Hq][Nq]
+  float* part;                // workspace
+  const int *seqlens_q, *seqlens_k;
+  int B, Hq, Hkv, Nq, d;
+  int causal;
+  float scale_log2;
+  int sms;
+  int* status;
+  unsigned long long wait_limit_ns;
+  int stall_unit;
+};
+
+cudaError_t launch_rope(const RopeArgs& a, cudaStream_t stream);
+cudaError_t launch_kv_append(const AppendArgs& a, cudaStream_t stream);
+cudaError_t launch_paged(const PagedArgs& a, cudaStream_t stream);
+
+#if defined(__CUDACC__)
+// Records an entry of a block table that names no page (first failure wins).
+__device__ __forceinline__ void record_bad_page(int* status, int site, int block, int page) {
+  if (atomicCAS(status, 0, FA_DEV_BAD_PAGE) == 0) {
+    volatile int* s = status;
+    s[1] = site;
+    s[2] = block;
+    s[3] = page;
+    __threadfence();
+  }
+}
+
+// Valid lengths of sequence b: new tokens and keys in the cache.
+__device__ __forceinline__ void paged_lens(const int* seqlens_q, const int* seqlens_k, int b, int nq, int capacity,
+                                           int& lq, int& lk) {
+  lq = seqlens_q ? min(max(__ldg(seqlens_q + b), 0), nq) : nq;
+  lk = seqlens_k ? min(max(__ldg(seqlens_k + b), 0), capacity) : capacity;
+}
+#endif
+
+}  // namespace fa

@@ -67,7 +67,8 @@ typedef enum {
   FA_ERR_MISALIGNED = 3,    /* a pointer breaks the alignment rules above */
   FA_ERR_LAUNCH = 4,        /* the CUDA runtime refused a launch or an allocation */
   FA_ERR_TIMEOUT = 5,       /* a kernel wait ran past its limit; the kernel returned early */
-  FA_ERR_DEVICE_FAULT = 6   /* the stream reported a CUDA error while synchronising */
+  FA_ERR_DEVICE_FAULT = 6,  /* the stream reported a CUDA error while synchronising */
+  FA_ERR_BAD_PAGE = 7       /* a block table names a page outside the cache (reported by fa_sync_status) */
 } fa_status;
 
 /* Element type of the forward output O (fa_fwd_ex, fa_bwd_ex). */
@@ -380,10 +381,173 @@ fa_status fa_bwd_stage(int stage, const void* q, const void* k, const void* v, c
  * for fa_bwd_varlen pass N = Nq. */
 size_t fa_bwd_workspace_bytes(int B, int H, int N);
 
+/* Pairing of the values that fa_rope and fa_kv_append rotate. */
+typedef enum {
+  FA_ROPE_HALF = 0,        /* pair i is (i, i + rot_dim / 2) */
+  FA_ROPE_INTERLEAVED = 1  /* pair i is (2i, 2i + 1) */
+} fa_rope_layout;
+
+/* How fa_rope_turns changes the frequencies for contexts longer than the
+ * trained one. */
+typedef enum {
+  FA_ROPE_SCALE_NONE = 0,
+  FA_ROPE_SCALE_LINEAR = 1,  /* every frequency divided by factor (interpolated positions) */
+  FA_ROPE_SCALE_NTK = 2,     /* base multiplied by factor^(rot_dim / (rot_dim - 2)): the slowest pair is
+                                stretched by factor, the fastest kept */
+  FA_ROPE_SCALE_PARTS = 3    /* by parts: pairs that turn more than `high` times within original_len keep
+                                their frequency, those below `low` turns are divided by factor, a linear
+                                ramp in the number of turns between */
+} fa_rope_scaling;
+
+/*
+ * The frequency table of the rotary calls, computed on the host: turns[i],
+ * i in [0, rot_dim / 2), is the angle that pair i turns by from one position
+ * to the next, in units of 2^-64 of a full turn.  Pair i's frequency is
+ * base^(-2i / rot_dim) radians per position, changed as `scaling` says.
+ *   turns    : host memory, rot_dim / 2 values; the device calls take a copy
+ *              in device memory.  A caller with frequencies f_i of its own
+ *              (radians per position) stores round(f_i / 2 pi * 2^64) mod 2^64.
+ *   rot_dim  : a multiple of 16.
+ *   factor >= 1 is read for every scaling but NONE; original_len > 0 and
+ *   0 <= low < high only for PARTS.
+ * Positions multiply these words modulo 2^64, that is modulo a full turn, so
+ * the angle is exact to 2^-32 turns at any 32-bit position.
+ */
+fa_status fa_rope_turns(long long* turns, int rot_dim, double base, int scaling, double factor, double original_len,
+                        double low, double high);
+
+/*
+ * Rotary positions: y = the first rot_dim values of every row of x rotated
+ * pair by pair by its position's angles, the other d - rot_dim values copied.
+ * For a pair (a, b) at position p with angle t = p * f_i:
+ *     a' = amplitude (a cos t - b sin t),  b' = amplitude (b cos t + a sin t).
+ *   x, y      : [B][H][N][d] of x_dtype / y_dtype (FA_DTYPE_F32, FA_DTYPE_BF16),
+ *               d contiguous, the other strides in elements (so that the q or
+ *               k part of a fused projection [B][N][heads][d] is read where it
+ *               lies); bases 16-byte aligned and rows starting on 16-byte
+ *               boundaries, strides >= 0, y's not 0.  y may be x itself, with
+ *               its type and strides; otherwise they must not overlap.
+ *   positions : device ints, position of token n of sequence b at
+ *               positions[b * positions_stride_b + n] (0: one row for all
+ *               sequences; negative positions turn the other way); or NULL:
+ *               token n is at position n.
+ *   turns     : device memory, rot_dim / 2 words of fa_rope_turns, 8-byte
+ *               aligned.  rot_dim: a multiple of 16, at most d.
+ *   amplitude : multiplies the rotated values (1 unless the scaling's
+ *               recipe calls for more); finite.
+ *   inverse   : 0 the forward rotation; 1 the rotation by -t, which is the
+ *               gradient with respect to x of the forward call with the same
+ *               arguments, given dL/dy as x (the rotation is orthogonal, and
+ *               amplitude enters both alike).
+ * Computed in fp32 from exact angles, rounded once when y is bf16.
+ */
+fa_status fa_rope(const void* x, int x_dtype, long long x_stride_b, long long x_stride_h, long long x_stride_n,
+                  void* y, int y_dtype, long long y_stride_b, long long y_stride_h, long long y_stride_n,
+                  const int* positions, long long positions_stride_b, const long long* turns, int rot_dim, int layout,
+                  float amplitude, int inverse, int B, int H, int N, int d, fa_stream_t stream);
+
+/*
+ * The paged key/value cache.  Keys and values live in pages,
+ *   k_pages, v_pages : bf16 [num_pages][Hkv][page_size][d], 16-byte aligned,
+ *   page_size a multiple of 16, and position p of sequence b is row
+ *   p % page_size of page block_table[b * table_stride + p / page_size].
+ *   block_table : device ints, max_pages entries a sequence are reachable
+ *               (table_stride >= 0 in elements); entries behind a sequence's
+ *               last page are never read.
+ *   seqlens_k : device ints, the keys of each sequence, the new tokens of
+ *               this step among them (clamped to [0, max_pages * page_size]).
+ *   seqlens_q : device ints, the new tokens of each sequence (clamped to
+ *               [0, N]); NULL: all N (Nq).
+ * Token t of a sequence with Lq new tokens and Lk keys is at position
+ * Lk - Lq + t, the bottom-right alignment of fa_fwd_varlen, so that one pair
+ * of length arrays serves the append and the attention of a step.
+ * A table entry outside [0, num_pages) reads or writes nothing: the call
+ * reports FA_ERR_BAD_PAGE through fa_sync_status, and the results of the
+ * sequences that name it are unspecified.  max_pages * page_size and
+ * num_pages * Hkv must be below 2^31.
+ */
+
+/*
+ * Appends the new tokens' keys and values to the paged cache, the keys
+ * rotated by their positions on the way, and (optionally) rotates the
+ * queries of the same tokens in the same launch.
+ *   k, v  : bf16 [B][Hkv][N][d] with strides as fa_rope's x (stride 0 allowed).
+ *   q     : bf16 [B][Hq][N][d] with strides; NULL: keys and values only (then
+ *           q_out is NULL and Hq is not read).
+ *   q_out : bf16 [B][Hq][N][d], contiguous; q itself if q is contiguous.
+ *   positions : as fa_rope, the angles' positions where they are not the
+ *           tokens' places in the cache; NULL: the cache position.
+ *   turns, rot_dim, layout, amplitude : as fa_rope; turns = NULL appends (and
+ *           copies q) without a rotation, and the other three are not read.
+ * Rows at or past Lq are padding: neither the cache nor q_out is written for
+ * them.  A token whose position is negative (Lq > Lk) has no place in the
+ * cache; its q_out row is written.  Two new tokens that a block table puts on
+ * one cache row leave either's value there, element by element.
+ */
+fa_status fa_kv_append(const void* k, long long k_stride_b, long long k_stride_h, long long k_stride_n, const void* v,
+                       long long v_stride_b, long long v_stride_h, long long v_stride_n, const void* q,
+                       long long q_stride_b, long long q_stride_h, long long q_stride_n, void* q_out, void* k_pages,
+                       void* v_pages, int num_pages, int page_size, const int* block_table, long long table_stride,
+                       int max_pages, const int* seqlens_q, const int* seqlens_k, const int* positions,
+                       long long positions_stride_b, const long long* turns, int rot_dim, int layout, float amplitude,
+                       int B, int Hq, int Hkv, int N, int d, fa_stream_t stream);
+
+/*
+ * Attention over the paged cache: fa_fwd_varlen for the lengths seqlens_q and
+ * seqlens_k, with keys and values read from their pages and query head h
+ * reading key head h / (Hq / Hkv) (Hq a multiple of Hkv).
+ *   q    : bf16 [B][Hq][Nq][d], contiguous, any Nq >= 1: single tokens,
+ *          drafted tokens, chunks of a prompt.
+ *   o    : [B][Hq][Nq][d] of o_dtype; lse: fp32 [B][Hq][Nq].
+ *   seqlens_k NULL: every sequence has max_pages * page_size keys.
+ *   workspace : fp32 scratch of fa_fwd_paged_workspace_bytes(...) bytes,
+ *          16-byte aligned, used by one call at a time; or NULL (a
+ *          stream-ordered allocation, freed on the same stream).
+ * Causal alignment, padding and empty rows as fa_fwd_varlen (O = 0,
+ * LSE = -inf).  Rows of a page behind a sequence's last key may hold anything,
+ * NaN included; the values of keys that some query of the sequence sees must
+ * be finite.
+ */
+fa_status fa_fwd_paged(const void* q, const void* k_pages, const void* v_pages, int num_pages, int page_size,
+                       const int* block_table, long long table_stride, int max_pages, void* o, int o_dtype,
+                       float* lse, const int* seqlens_q, const int* seqlens_k, float* workspace, int B, int Hq,
+                       int Hkv, int Nq, int d, float scale, int causal, fa_stream_t stream);
+
+/* Bytes of the fa_fwd_paged workspace (an upper bound that does not depend on
+ * the device or on the lengths); 0 on invalid sizes. */
+size_t fa_fwd_paged_workspace_bytes(int B, int Hq, int Hkv, int Nq, int d);
+
+/*
+ * Attention over the paged cache for a batch whose sequences all start with
+ * the same prefix_len keys: exactly what fa_fwd_paged computes when every
+ * sequence's first prefix_len / page_size block-table entries are
+ * prefix_table's, but the prefix's keys and values are read once for the rows
+ * of all sequences together, not once a sequence; the rest of each sequence
+ * is attended on its own and the two are merged by their log-sum-exp.
+ *   prefix_table : device ints, the prefix's prefix_len / page_size pages;
+ *                  block-table entries below prefix_len / page_size are not
+ *                  read by this call (positions stay those of the whole
+ *                  sequence, so one table serves the append as well).
+ *   prefix_len   : a positive multiple of page_size, at most
+ *                  max_pages * page_size.  Sequences shorter than it are
+ *                  allowed and see their own length's share of the prefix.
+ * Other arguments, results and errors as fa_fwd_paged.
+ */
+fa_status fa_fwd_shared_prefix(const void* q, const void* k_pages, const void* v_pages, int num_pages, int page_size,
+                               const int* prefix_table, int prefix_len, const int* block_table,
+                               long long table_stride, int max_pages, void* o, int o_dtype, float* lse,
+                               const int* seqlens_q, const int* seqlens_k, float* workspace, int B, int Hq, int Hkv,
+                               int Nq, int d, float scale, int causal, fa_stream_t stream);
+
+/* Bytes of the fa_fwd_shared_prefix workspace (an upper bound that does not
+ * depend on the device or on the lengths); 0 on invalid sizes. */
+size_t fa_fwd_shared_prefix_workspace_bytes(int B, int Hq, int Hkv, int Nq, int d);
+
 /*
  * Synchronises `stream`, then reads and clears the device status word of the
  * current device.  Returns FA_ERR_DEVICE_FAULT if the stream reported a CUDA
- * error, FA_ERR_TIMEOUT if a kernel wait ran out since the last call, FA_OK
+ * error, FA_ERR_TIMEOUT if a kernel wait ran out since the last call,
+ * FA_ERR_BAD_PAGE if a paged call met a table entry that names no page, FA_OK
  * otherwise.
  */
 fa_status fa_sync_status(fa_stream_t stream);
@@ -393,7 +557,8 @@ fa_status fa_sync_status(fa_stream_t stream);
  * out[0] status code, out[1] wait site, out[2] block index, out[3] work unit.
  * Wait sites: 1-7 forward, 11-20 dK/dV, 21-32 dQ, 35-36 decode, 41-47 FP8
  * forward, 51-59 the single-pass row-term pass, 61-63 the single-pass dK/dV
- * sweep (each kernel's source names them).
+ * sweep, 71-79 the paged calls (each kernel's source names them).  After
+ * FA_ERR_BAD_PAGE: out[2] the sequence, out[3] the table entry.
  * Returns FA_OK, or FA_ERR_INVALID_ARG if out is NULL.
  */
 fa_status fa_last_failure(int out[4]);
