@@ -1,14 +1,646 @@
-// Attention over the paged cache: one warp per query row, plain loops.
+// Attention over the paged cache for few rows a key head: single tokens and
+// drafted ones of every query head of its group.
+//
+// A step reads the keys and values of every sequence once, for G * Nq rows of
+// queries a key head: 2 G Nq FLOPs per byte, so with up to 32 rows it is bound
+// by HBM as long as the products run on the tensor cores (on the CUDA cores 8
+// heads a group already cost more than the reading).  The products are
+// 16 x 64 x d per 64 keys: a tcgen05 tile would be 128 rows high and its
+// result would have to come back through tensor memory before a row maximum
+// can be taken, so these use warp-wide mma with the fragments in registers,
+// fed by ldmatrix from the swizzled TMA tiles.
+//
+//   paged_steps_kernel    persistent CTAs of four compute warps and a TMA warp,
+//                         two an SM.  The key tiles (64 keys of one key head)
+//                         of all sequences form one line, cut into equal
+//                         ranges, one a CTA: the lengths stay on the device,
+//                         and a batch of very different lengths is balanced to
+//                         one tile.  Where a sequence's tiles fall into more
+//                         than one range each leaves a partial result.
+//   paged_combine_kernel  merges a row's partial results by their log-sum-exp.
+//
+// Within a tile each warp multiplies the rows with its 16 keys, the warps
+// agree on the row maxima through shared memory, exchange the probabilities
+// the same way, and each multiplies all 64 keys with its quarter of the value
+// columns: one accumulator and one set of statistics per CTA, so a CTA moves
+// from one sequence to the next without merging warps.
+//
+// Probabilities go into the product as a pair of bf16 (the value and what its
+// rounding left), 16 significand bits: the second product costs tensor time
+// that the kernel has to spare, and O is as exact as with fp32 products.
 #include <cuda_runtime.h>
 #include <math_constants.h>
 
+#include <atomic>
+
+#include "internal.h"
+#include "paged.cuh"
 #include "ptx.cuh"
 #include "serving.h"
 
 namespace fa {
 namespace {
 
+constexpr int kStepKeys = 64;         // keys a tile
+constexpr int kStepWarps = 4;         // compute warps, 16 keys of a tile each
+constexpr int kStepThreads = 32 * (kStepWarps + 1);
+constexpr float kTau = 8.f;           // the reference maximum moves when a row's grows by more than 2^8
 constexpr float kLn2 = 0.6931471805599453f;
+
+enum StepSite : int { SITE_STEP_EMPTY = 73, SITE_STEP_FULL = 74 };
+
+template <int D, int MB>
+struct StepLayout {
+  static constexpr int kBlock = kStepKeys * 128;        // 64 columns x 64 keys: 128-byte rows, swizzled
+  static constexpr int kHalf = (D / 64) * kBlock;       // K (or V) of a tile
+  static constexpr int kStage = 2 * kHalf;
+  static constexpr int kStages = D == 128 ? 3 : 6;
+  static constexpr int kPOff = kStages * kStage;        // probabilities: hi then lo, [16 MB rows][64 keys]
+  static constexpr int kPHalf = 16 * MB * 128;
+  static constexpr int kBarOff = kPOff + 2 * kPHalf;    // FULL[s] then EMPTY[s]
+  static constexpr int kMaxOff = kBarOff + 2 * kStages * 8;  // [warps][16 MB] row maxima, then row sums
+  static constexpr int kMiscOff = kMaxOff + 2 * kStepWarps * 16 * MB * 4;
+  static constexpr int kLineOff = kMiscOff + 16;        // first tile of every sequence
+  static constexpr int kSmemBytes = kLineOff + (kLineSequences + 1) * 4 + 1024;
+};
+
+__device__ __forceinline__ uint32_t sw128(int r, int c) {
+  return static_cast<uint32_t>(r * 128 + ((c ^ (r & 7)) << 4));
+}
+
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+
+__device__ __forceinline__ void ldmatrix4_t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+
+// c (16 x 8, fp32) += a (16 x 16) b (16 x 8), bf16
+__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void st_shared_u32(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
+// All four compute warps; true if every one of them passed true.
+__device__ __forceinline__ bool warps_agree(bool ok) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.and.pred q, 1, %2, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(ok ? 1u : 0u), "n"(32 * kStepWarps)
+      : "memory");
+  return r != 0;
+}
+
+__device__ __forceinline__ void warps_sync() {
+  asm volatile("barrier.cta.sync 1, %0;" ::"n"(32 * kStepWarps) : "memory");
+}
+
+// A walk over the pieces of sequences that a CTA's range of the line holds.
+struct Walk {
+  int b, head;      // sequence and key head of the piece
+  int tile, end;    // its tiles within the sequence: [tile, end)
+  int tiles;        // tiles of the sequence
+};
+
+__device__ __forceinline__ bool walk_begin(Walk& w, const int* line, int B, int Hkv, int at, int stop) {
+  if (at >= stop) return false;
+  // the last sequence that starts at or before `at` and has tiles
+  int lo = 0, hi = B - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (line[mid] * Hkv <= at) lo = mid; else hi = mid - 1;
+  }
+  w.b = lo;
+  w.tiles = line[lo + 1] - line[lo];
+  const int in = at - line[lo] * Hkv;
+  w.head = in / w.tiles;
+  w.tile = in - w.head * w.tiles;
+  w.end = min(w.tiles, w.tile + stop - at);
+  return true;
+}
+
+__device__ __forceinline__ bool walk_next(Walk& w, const int* line, int Hkv, int& at, int stop) {
+  at += w.end - w.tile;
+  if (at >= stop) return false;
+  if (++w.head == Hkv) {
+    w.head = 0;
+    do {
+      ++w.b;
+      w.tiles = line[w.b + 1] - line[w.b];
+    } while (w.tiles == 0);
+  }
+  w.tile = 0;
+  w.end = min(w.tiles, stop - at);
+  return true;
+}
+
+template <int D, int MB>
+__global__ void __launch_bounds__(kStepThreads, 2)
+    paged_steps_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                       const PagedStep p) {
+  using L = StepLayout<D, MB>;
+  constexpr int S = L::kStages;
+  constexpr int CB = D / 64;       // 64-column blocks of a head
+  constexpr int KS = D / 16;       // steps of the score product
+  constexpr int NT = D / 32;       // 8-column tiles of a warp's quarter of the values
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  const uint32_t bars = sbase + L::kBarOff;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMiscOff);
+  int* line = reinterpret_cast<int*>(smem + L::kLineOff);
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(bars + 8 * s, 1);
+      mbar_init(bars + 8 * (S + s), kStepWarps);
+    }
+    *abort_flag = 0;
+    mbar_fence_init();
+  }
+  if (warp == kStepWarps && lane == 0) {
+    prefetch_tensormap(&tm_k);
+    prefetch_tensormap(&tm_v);
+  }
+  // the scratch of the scan is the row-maxima area, unused so far
+  build_line<kStepThreads>(line, reinterpret_cast<int*>(smem + L::kMaxOff), p.seq, kStepKeys);
+  const int total = line[p.seq.B] * p.seq.Hkv;
+  if (blockIdx.x == 0) {
+    for (int i = threadIdx.x; i <= p.seq.B; i += kStepThreads) p.line_out[i] = line[i];
+  }
+  const int per = tiles_per_cta(total, gridDim.x);
+  int at = min(static_cast<int>(blockIdx.x) * per, total);
+  const int stop = min(at + per, total);
+  const WaitCtl wc{abort_flag, p.status, p.wait_limit_ns};
+  const int unit = static_cast<int>(blockIdx.x);
+  Walk w;
+  bool more = walk_begin(w, line, p.seq.B, p.seq.Hkv, at, stop);
+
+  if (warp == kStepWarps) {
+    // ------------------------------------------------------------ TMA producer
+    // lane i of a tile's loads: operand, 64-column block and box of rows
+    const int boxes = kStepKeys / p.box_rows;
+    const int mine = lane / boxes;                 // operand * CB + block
+    const int box = lane - mine * boxes;
+    const bool loads = mine < 2 * CB;
+    const uint32_t offset = static_cast<uint32_t>((mine / CB) * L::kHalf + (mine % CB) * L::kBlock + box * p.box_rows * 128);
+    const CUtensorMap* tm = mine / CB == 0 ? &tm_k : &tm_v;
+    int issued = 0;
+    bool ok = true;
+    while (more && ok) {
+      int lq, lk;
+      seq_lens(p.seq, w.b, lq, lk);
+      const int first = p.seq.prefix_len + w.tile * kStepKeys;
+      const int* pages = p.table.block_table + w.b * p.table.table_stride;
+      const int count = (w.end - w.tile) * boxes;
+      // page of box i of the piece; -1 behind the sequence's end
+      auto page_of = [&](int i) {
+        const int key = first + i * p.box_rows;
+        return i < count && key < lk ? __ldg(pages + key / p.table.page_size) : -1;
+      };
+      int cur = page_of(lane), next = page_of(32 + lane);
+      for (int t = 0; t < w.end - w.tile; ++t, ++issued) {
+        if (t > 0 && (t * boxes) % 32 == 0) {
+          cur = next;
+          next = page_of(t * boxes + 32 + lane);
+        }
+        const int s = issued % S;
+        ok = __all_sync(0xffffffffu,
+                        wait_bounded(bars + 8 * (S + s), ((issued / S) & 1) ^ 1, wc, SITE_STEP_EMPTY, unit));
+        if (!ok) break;
+        const int page = __shfl_sync(0xffffffffu, cur, (t * boxes + box) % 32);
+        if (unit == p.stall_unit && issued == 0) continue;  // testing hook: leave this tile unloaded
+        const uint32_t full = bars + 8 * s;
+        if (lane == 0) mbar_arrive_expect_tx(full, L::kStage);
+        __syncwarp();
+        if (loads) {
+          const int key = first + t * kStepKeys + box * p.box_rows;
+          // rows of no page: a coordinate past the map, which reads zeros
+          int outer = p.table.num_pages * p.seq.Hkv;
+          if (key < lk) {
+            if (page >= 0 && page < p.table.num_pages)
+              outer = page * p.seq.Hkv + w.head;
+            else
+              record_bad_page(p.status, SITE_PAGE_READ, p.b0 + w.b, page);
+          }
+          tma_load_3d(sbase + s * L::kStage + offset, tm, full, 64 * (mine % CB), key % p.table.page_size, outer);
+        }
+        __syncwarp();
+      }
+      if (ok) more = walk_next(w, line, p.seq.Hkv, at, stop);
+    }
+    if (!ok && lane == 0) {
+      // let the copies already issued land before the CTA can exit
+      for (int s = 0; s < S; ++s) {
+        if (issued > s) {
+          const int last = issued - 1 - ((issued - 1 - s) % S);
+          const uint64_t t0 = globaltimer_ns();
+          while (!mbar_try_wait(bars + 8 * s, (last / S) & 1)) {
+            if (globaltimer_ns() - t0 > p.wait_limit_ns) break;
+          }
+        }
+      }
+    }
+    return;
+  }
+
+  // ---------------------------------------------------------------- compute
+  float* maxima = reinterpret_cast<float*>(smem + L::kMaxOff);   // [warp][16 MB]
+  float* sums = maxima + kStepWarps * 16 * MB;
+  const int qr = lane >> 2;        // fragment row (and row + 8)
+  const int qc = (lane & 3) * 2;   // fragment column pair
+  const int rows = p.seq.G * p.seq.Nq;
+  // ldmatrix lane addresses: K (two 8-key tiles x two 8-column halves), P and
+  // V (16 keys x two 8-column tiles)
+  const int k_row = 16 * warp + ((lane >> 4) << 3) + (lane & 7);
+  const int k_half = (lane >> 3) & 1;
+  const int p_row = (((lane >> 3) & 1) << 3) + (lane & 7);
+  const int p_half = lane >> 4;
+  const int v_col = warp * (D / 4);  // first value column of this warp
+  const uint32_t p_hi = sbase + L::kPOff, p_lo = p_hi + L::kPHalf;
+  int done = 0;
+  bool ok = true;
+  while (more && ok) {
+    int lq, lk;
+    seq_lens(p.seq, w.b, lq, lk);
+    const size_t row0 = (static_cast<size_t>(w.b) * p.seq.Hkv + w.head) * rows;  // rows of the group lie together
+    uint32_t qf[MB][KS][4];
+    int kend[MB][2];
+#pragma unroll
+    for (int m = 0; m < MB; ++m) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = 16 * m + 8 * e + qr;
+        kend[m][e] = 0;
+        if (r < rows) {
+          const uint16_t* src = p.q + (row0 + r) * D + qc;
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks) {
+            qf[m][ks][e] = __ldg(reinterpret_cast<const uint32_t*>(src + 16 * ks));
+            qf[m][ks][2 + e] = __ldg(reinterpret_cast<const uint32_t*>(src + 16 * ks + 8));
+          }
+          const int i = r % p.seq.Nq;
+          if (i < lq) kend[m][e] = p.causal ? min(i + lk - lq + 1, lk) : lk;
+        } else {
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks) qf[m][ks][e] = qf[m][ks][2 + e] = 0u;
+        }
+      }
+    }
+    float m_ref[MB][2], l[MB][2], acc[MB][NT][4];
+#pragma unroll
+    for (int m = 0; m < MB; ++m) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        m_ref[m][e] = -CUDART_INF_F;
+        l[m][e] = 0.f;
+      }
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[m][n][e] = 0.f;
+    }
+    for (int t = w.tile; t < w.end; ++t, ++done) {
+      const int s = done % S;
+      const bool full = wait_bounded(bars + 8 * s, (done / S) & 1, wc, SITE_STEP_FULL, unit);
+      const uint32_t kb = sbase + s * L::kStage;
+      const uint32_t vb = kb + L::kHalf;
+      const int key0 = p.seq.prefix_len + t * kStepKeys;
+      // scores of this warp's 16 keys: fragment n holds keys 8 n + qc, + 1
+      float sc[MB][2][4];
+#pragma unroll
+      for (int m = 0; m < MB; ++m)
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sc[m][n][e] = 0.f;
+      if (__all_sync(0xffffffffu, full)) {
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          uint32_t kf[4];
+          ldmatrix4(kf, kb + (ks >> 2) * L::kBlock + sw128(k_row, 2 * (ks & 3) + k_half));
+#pragma unroll
+          for (int m = 0; m < MB; ++m) {
+            mma_bf16(sc[m][0], qf[m][ks], kf[0], kf[1]);
+            mma_bf16(sc[m][1], qf[m][ks], kf[2], kf[3]);
+          }
+        }
+        if (key0 + kStepKeys > lk) {
+          // rows behind the last key may hold anything: their weights are 0,
+          // so their values must be finite
+          for (int i = lane; i < 16 * 8 * CB; i += 32) {
+            const int r = 16 * warp + (i & 15);
+            if (key0 + r >= lk) st_shared_v4(vb + (i >> 7) * L::kBlock + sw128(r, (i >> 4) & 7), 0u, 0u, 0u, 0u);
+          }
+          fence_proxy_async_smem();  // before the slot's next TMA load
+        }
+      }
+      float mx[MB][2];
+#pragma unroll
+      for (int m = 0; m < MB; ++m) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int j = key0 + 16 * warp + qc;
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            if (j + 8 * n >= kend[m][e]) sc[m][n][2 * e] = -CUDART_INF_F;
+            if (j + 8 * n + 1 >= kend[m][e]) sc[m][n][2 * e + 1] = -CUDART_INF_F;
+          }
+          float x = fmaxf(fmaxf(sc[m][0][2 * e], sc[m][0][2 * e + 1]), fmaxf(sc[m][1][2 * e], sc[m][1][2 * e + 1]));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+          mx[m][e] = x;
+          if ((lane & 3) == 0) maxima[warp * 16 * MB + 16 * m + 8 * e + qr] = x;
+        }
+      }
+      ok = warps_agree(full);
+      if (!ok) break;
+#pragma unroll
+      for (int m = 0; m < MB; ++m) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int r = 16 * m + 8 * e + qr;
+          float x = mx[m][e];
+#pragma unroll
+          for (int o = 0; o < kStepWarps; ++o) x = fmaxf(x, maxima[o * 16 * MB + r]);
+          x *= p.scale_log2;
+          if (x > m_ref[m][e] + kTau) {  // the same in every warp
+            const float alpha = ex2_approx(m_ref[m][e] - x);  // 0 on the first visible key
+            m_ref[m][e] = x;
+            l[m][e] *= alpha;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              acc[m][n][2 * e] *= alpha;
+              acc[m][n][2 * e + 1] *= alpha;
+            }
+          }
+          const float mu = m_ref[m][e] == -CUDART_INF_F ? 0.f : m_ref[m][e];
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            const float a = ex2_approx(fmaf(sc[m][n][2 * e], p.scale_log2, -mu));
+            const float b = ex2_approx(fmaf(sc[m][n][2 * e + 1], p.scale_log2, -mu));
+            l[m][e] += a + b;
+            const uint32_t hi = pack_bf16x2(a, b);
+            const uint32_t lo = pack_bf16x2(a - __uint_as_float(hi << 16), b - __uint_as_float(hi & 0xFFFF0000u));
+            const uint32_t off = sw128(r, 2 * warp + n) + (lane & 3) * 4;
+            st_shared_u32(p_hi + off, hi);
+            st_shared_u32(p_lo + off, lo);
+          }
+        }
+      }
+      warps_sync();
+      // O += P V: all 64 keys, this warp's quarter of the columns
+#pragma unroll
+      for (int kk = 0; kk < kStepKeys / 16; ++kk) {
+        uint32_t vf[NT / 2][4];
+#pragma unroll
+        for (int n = 0; n < NT / 2; ++n) {
+          const int chunk = v_col / 8 + 2 * n + p_half;  // 16-byte chunk of the head's row
+          ldmatrix4_t(vf[n], vb + (chunk >> 3) * L::kBlock + sw128(16 * kk + p_row, chunk & 7));
+        }
+#pragma unroll
+        for (int m = 0; m < MB; ++m) {
+          uint32_t ph[4], pl[4];
+          const uint32_t off = sw128(16 * m + p_row, 2 * kk + p_half);
+          ldmatrix4(ph, p_hi + off);
+          ldmatrix4(pl, p_lo + off);
+#pragma unroll
+          for (int n = 0; n < NT / 2; ++n) {
+            mma_bf16(acc[m][2 * n], ph, vf[n][0], vf[n][1]);
+            mma_bf16(acc[m][2 * n + 1], ph, vf[n][2], vf[n][3]);
+            mma_bf16(acc[m][2 * n], pl, vf[n][0], vf[n][1]);
+            mma_bf16(acc[m][2 * n + 1], pl, vf[n][2], vf[n][3]);
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bars + 8 * (S + s));
+    }
+    if (!ok) break;
+    // the row sums of all warps
+#pragma unroll
+    for (int m = 0; m < MB; ++m) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float x = l[m][e];
+        x += __shfl_xor_sync(0xffffffffu, x, 1);
+        x += __shfl_xor_sync(0xffffffffu, x, 2);
+        if ((lane & 3) == 0) sums[warp * 16 * MB + 16 * m + 8 * e + qr] = x;
+      }
+    }
+    warps_sync();
+    const bool whole = p.direct && w.tile == 0 && w.end == w.tiles;
+    const size_t slot = static_cast<size_t>(w.b) * p.seq.Hkv + w.head + blockIdx.x;
+#pragma unroll
+    for (int m = 0; m < MB; ++m) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = 16 * m + 8 * e + qr;
+        if (r < rows) {
+          float sum = 0.f;
+#pragma unroll
+          for (int o = 0; o < kStepWarps; ++o) sum += sums[o * 16 * MB + r];
+          const bool live = sum > 0.f;
+          const float inv = live ? 1.0f / sum : 0.f;
+          const float lse2 = live ? m_ref[m][e] + log2f(sum) : -CUDART_INF_F;
+          const int col = v_col + qc;
+          if (whole) {
+            const size_t at_o = (row0 + r) * D + col;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              const float a = live ? acc[m][n][2 * e] * inv : 0.f, b = live ? acc[m][n][2 * e + 1] * inv : 0.f;
+              if (p.o_bf16)
+                *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.o) + at_o + 8 * n) = pack_bf16x2(a, b);
+              else
+                *reinterpret_cast<float2*>(static_cast<float*>(p.o) + at_o + 8 * n) = make_float2(a, b);
+            }
+            if (warp == 0 && (lane & 3) == 0) p.lse[row0 + r] = live ? lse2 * kLn2 : -CUDART_INF_F;
+          } else {
+            float* dst = p.part + (slot * rows + r) * D + col;
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+              *reinterpret_cast<float2*>(dst + 8 * n) =
+                  live ? make_float2(acc[m][n][2 * e] * inv, acc[m][n][2 * e + 1] * inv) : make_float2(0.f, 0.f);
+            if (warp == 0 && (lane & 3) == 0) p.part_lse[slot * rows + r] = lse2;
+          }
+        }
+      }
+    }
+    more = walk_next(w, line, p.seq.Hkv, at, stop);
+  }
+}
+
+// Merges a row's partial results.  WARPS warps share a row.
+template <int D, int WARPS>
+__global__ void __launch_bounds__(256) paged_combine_kernel(const PagedCombine p) {
+  constexpr int CW = D / 32;
+  constexpr int ROWS = 8 / WARPS;
+  __shared__ float s_max[8], s_sum[8], s_acc[8][D];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int sub = warp % WARPS;
+  const long long row = static_cast<long long>(blockIdx.x) * ROWS + warp / WARPS;
+  const bool in = row < static_cast<long long>(p.seq.B) * p.seq.Hkv * p.seq.G * p.seq.Nq;
+  const int rows = p.seq.G * p.seq.Nq;
+  const int group = in ? static_cast<int>(row / rows) : 0;  // (sequence, key head)
+  const int r = static_cast<int>(row - static_cast<long long>(group) * rows);
+  const int b = group / p.seq.Hkv, head = group - b * p.seq.Hkv;
+  // the line's partial results of the group: slots [first, first + n)
+  const int t0 = p.line[b], nt = p.line[b + 1] - t0;
+  const int per = tiles_per_cta(p.line[p.seq.B] * p.seq.Hkv, p.ctas);
+  const int from = t0 * p.seq.Hkv + head * nt;
+  const int c0 = from / per, n = nt ? (from + nt - 1) / per - c0 + 1 : 0;
+  const long long slot0 = group + c0;
+  const bool skip = !in || (p.direct && n == 1);  // written by the only CTA that had it
+  float M = -CUDART_INF_F, sum = 0.f, acc[CW];
+#pragma unroll
+  for (int c = 0; c < CW; ++c) acc[c] = 0.f;
+  auto add = [&](float lse, const float* src) {
+    if (lse == -CUDART_INF_F) return;  // the same in every lane
+    const float m = fmaxf(M, lse);
+    const float f = exp2f(lse - m), g = exp2f(M - m);
+    M = m;
+    sum = sum * g + f;
+#pragma unroll
+    for (int c = 0; c < CW; ++c) acc[c] = fmaf(f, src[c], acc[c] * g);
+  };
+  if (!skip) {
+    constexpr int U = 4;
+    for (int i = sub; i < n; i += WARPS * U) {
+      float lse[U], x[U][CW];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int k = i + u * WARPS;
+        const long long at = (slot0 + k) * rows + r;
+        lse[u] = k < n ? p.part_lse[at] : -CUDART_INF_F;
+#pragma unroll
+        for (int c = 0; c < CW; ++c) x[u][c] = k < n ? p.part[at * D + CW * lane + c] : 0.f;
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) add(lse[u], x[u]);
+    }
+  }
+  if constexpr (WARPS > 1) {
+#pragma unroll
+    for (int c = 0; c < CW; ++c) s_acc[warp][CW * lane + c] = acc[c];
+    if (lane == 0) {
+      s_max[warp] = M;
+      s_sum[warp] = sum;
+    }
+    __syncthreads();
+    if (sub != 0) return;
+    for (int o = 1; o < WARPS; ++o) {
+      const float m2 = s_max[warp + o];
+      if (m2 == -CUDART_INF_F) continue;
+      const float m = fmaxf(M, m2);
+      const float f = exp2f(m2 - m), g = exp2f(M - m);
+      M = m;
+      sum = sum * g + s_sum[warp + o] * f;
+#pragma unroll
+      for (int c = 0; c < CW; ++c) acc[c] = acc[c] * g + s_acc[warp + o][CW * lane + c] * f;
+    }
+  }
+  if (skip) return;
+  const bool live = sum > 0.f;
+  const float inv = live ? 1.0f / sum : 0.f;
+  const size_t at = static_cast<size_t>(row) * D + CW * lane;
+#pragma unroll
+  for (int c = 0; c < CW; c += 2) {
+    const float a = acc[c] * inv, e = acc[c + 1] * inv;
+    if (p.o_bf16)
+      *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.o) + at + c) = pack_bf16x2(a, e);
+    else
+      *reinterpret_cast<float2*>(static_cast<float*>(p.o) + at + c) = make_float2(a, e);
+  }
+  if (lane == 0) p.lse[row] = live ? (M + log2f(sum)) * kLn2 : -CUDART_INF_F;
+}
+
+template <int D, int MB>
+cudaError_t launch_steps(const PagedArgs& a, const PagedStep& p, int ctas, cudaStream_t stream) {
+  using L = StepLayout<D, MB>;
+  auto kern = paged_steps_kernel<D, MB>;
+  static std::atomic<unsigned long long> ready{0};
+  cudaError_t e = setup_kernel_once(kern, L::kSmemBytes, 0, ready);
+  if (e != cudaSuccess) return e;
+  kern<<<ctas, kStepThreads, L::kSmemBytes, stream>>>(a.tm_k, a.tm_v, p);
+  return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_combine(const PagedCombine& p, cudaStream_t stream) {
+  const long long rows = static_cast<long long>(p.seq.B) * p.seq.Hkv * p.seq.G * p.seq.Nq;
+  // few rows: four warps a row, whose partial results then number the most
+  if (rows <= 2048)
+    paged_combine_kernel<D, 4><<<static_cast<unsigned>((rows + 1) / 2), 256, 0, stream>>>(p);
+  else
+    paged_combine_kernel<D, 1><<<static_cast<unsigned>((rows + 7) / 8), 256, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_steps_d(const PagedArgs& a, cudaStream_t stream) {
+  const int G = a.Hq / a.Hkv, rows = G * a.Nq;
+  const int capacity = a.table.max_pages * a.table.page_size;
+  for (int b0 = 0; b0 < a.B; b0 += kLineSequences) {
+    const int B = a.B - b0 < kLineSequences ? a.B - b0 : kLineSequences;
+    const size_t first = static_cast<size_t>(b0) * a.Hq * a.Nq;
+    PagedStep p;
+    p.seq = PagedSeq{a.seqlens_q ? a.seqlens_q + b0 : nullptr, a.seqlens_k ? a.seqlens_k + b0 : nullptr, B, a.Hkv, G,
+                     a.Nq, capacity, a.prefix_len};
+    p.table = a.table;
+    p.table.block_table += b0 * a.table.table_stride;
+    p.q = a.q + first * D;
+    p.o = static_cast<uint8_t*>(a.o) + first * D * (a.o_bf16 ? 2 : 4);
+    p.o_bf16 = a.o_bf16;
+    p.lse = a.lse + first;
+    const size_t slots = static_cast<size_t>(B) * a.Hkv + kMaxCtas;
+    p.line_out = reinterpret_cast<int*>(a.part);
+    p.part = a.part + kLineWords;
+    p.part_lse = p.part + slots * rows * D;
+    p.direct = a.prefix_len == 0;
+    p.box_rows = a.box_rows;
+    p.b0 = b0;
+    p.causal = a.causal;
+    p.scale_log2 = a.scale_log2;
+    p.status = a.status;
+    p.wait_limit_ns = a.wait_limit_ns;
+    p.stall_unit = a.stall_unit;
+    const int ctas = 2 * a.sms < kMaxCtas ? 2 * a.sms : kMaxCtas;
+    cudaError_t e = rows <= 16 ? launch_steps<D, 1>(a, p, ctas, stream) : launch_steps<D, 2>(a, p, ctas, stream);
+    if (e != cudaSuccess) return e;
+    PagedCombine c;
+    c.seq = p.seq;
+    c.line = p.line_out;
+    c.ctas = ctas;
+    c.part = p.part;
+    c.part_lse = p.part_lse;
+    c.direct = p.direct;
+    c.o = p.o;
+    c.o_bf16 = p.o_bf16;
+    c.lse = p.lse;
+    e = launch_combine<D>(c, stream);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
 
 __device__ __forceinline__ float bf16_at(const uint16_t* p) {
   return __uint_as_float(static_cast<uint32_t>(__ldg(p)) << 16);
@@ -64,7 +696,16 @@ __global__ void __launch_bounds__(128) paged_rows_kernel(const PagedArgs a) {
 
 }  // namespace
 
+size_t paged_workspace_floats(int B, int Hkv, int G, int Nq, int d) {
+  const long long rows = static_cast<long long>(G) * Nq;
+  if (rows > kStepRows) return 4;
+  const size_t slots = static_cast<size_t>(B < kLineSequences ? B : kLineSequences) * Hkv + kMaxCtas;
+  return kLineWords + slots * rows * (d + 1);
+}
+
 cudaError_t launch_paged(const PagedArgs& a, cudaStream_t stream) {
+  if (a.prefix_len == 0 && static_cast<long long>(a.Hq / a.Hkv) * a.Nq <= kStepRows)
+    return a.d == 64 ? launch_steps_d<64>(a, stream) : launch_steps_d<128>(a, stream);
   const long long rows = static_cast<long long>(a.B) * a.Hq * a.Nq;
   const unsigned grid = static_cast<unsigned>((rows + 3) / 4);
   if (a.d == 64)

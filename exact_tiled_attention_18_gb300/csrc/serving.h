@@ -6,6 +6,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <cstddef>
 #include <cstdint>
 
 namespace fa {
@@ -82,6 +83,7 @@ struct PagedArgs {
   int B, Hq, Hkv, Nq, d;
   int causal;
   float scale_log2;
+  int box_rows;               // rows of a TMA box: the largest power of two up to 64 that divides page_size
   int sms;
   int* status;
   unsigned long long wait_limit_ns;
@@ -91,6 +93,9 @@ struct PagedArgs {
 cudaError_t launch_rope(const RopeArgs& a, cudaStream_t stream);
 cudaError_t launch_kv_append(const AppendArgs& a, cudaStream_t stream);
 cudaError_t launch_paged(const PagedArgs& a, cudaStream_t stream);
+
+// Workspace of launch_paged in 4-byte words.
+size_t paged_workspace_floats(int B, int Hkv, int G, int Nq, int d);
 
 #if defined(__CUDACC__)
 // Records an entry of a block table that names no page (first failure wins).
