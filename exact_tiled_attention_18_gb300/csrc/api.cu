@@ -391,15 +391,13 @@ fa_status check_rope(const long long* turns, int rot_dim, int layout, float ampl
 // The cache's own sizes: pages of whole 16-key groups, positions and head
 // rows of pages that fit 32 bits.
 fa_status check_pages(const void* k_pages, const void* v_pages, int num_pages, int page_size, const int* block_table,
-                      long long table_stride, int max_pages, int B, int Hkv) {
+                      long long table_stride, int max_pages, int Hkv) {
   if (!k_pages || !v_pages || !block_table) return FA_ERR_INVALID_ARG;
   if (num_pages < 1 || max_pages < 1 || page_size < 16 || page_size % 16 != 0 || table_stride < 0)
     return FA_ERR_INVALID_ARG;
   const long long limit = 1LL << 31;
   if (static_cast<long long>(max_pages) * page_size >= limit) return FA_ERR_INVALID_ARG;
   if (static_cast<long long>(num_pages) * Hkv >= limit) return FA_ERR_INVALID_ARG;
-  if (static_cast<long long>(B) * Hkv * ((static_cast<long long>(max_pages) * page_size + 63) / 64) >= limit)
-    return FA_ERR_INVALID_ARG;
   if (!aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(block_table, 4)) return FA_ERR_MISALIGNED;
   return FA_OK;
 }
@@ -415,8 +413,12 @@ fa_status paged_common(const void* q, const void* k_pages, const void* v_pages, 
   if (st != FA_OK) return st;
   if (Hkv < 1 || Hq % Hkv != 0) return FA_ERR_INVALID_ARG;
   if (!std::isfinite(scale) || !(scale > 0.f)) return FA_ERR_INVALID_ARG;
-  st = check_pages(k_pages, v_pages, num_pages, page_size, block_table, table_stride, max_pages, B, Hkv);
+  st = check_pages(k_pages, v_pages, num_pages, page_size, block_table, table_stride, max_pages, Hkv);
   if (st != FA_OK) return st;
+  // key tiles of all rows, in 32 bits
+  const double key_tiles = (static_cast<double>(max_pages) * page_size + 63) / 64;
+  const double row_tiles = static_cast<double>(B) * Hkv * (static_cast<double>(Hq / Hkv) * Nq / 256 + 1);
+  if (key_tiles * row_tiles >= 2147483648.0) return FA_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 4) || (workspace && !aligned(workspace, 16)) ||
       (seqlens_q && !aligned(seqlens_q, 4)) || (seqlens_k && !aligned(seqlens_k, 4)) ||
       (prefix_table && !aligned(prefix_table, 4)))
@@ -455,7 +457,7 @@ fa_status paged_common(const void* q, const void* k_pages, const void* v_pages, 
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (!workspace) {
     if (cudaMallocAsync(reinterpret_cast<void**>(&a.part),
-                        sizeof(float) * fa::paged_workspace_floats(B, Hkv, Hq / Hkv, Nq, d), s) != cudaSuccess)
+                        sizeof(float) * fa::paged_workspace_floats(B, Hkv, Hq / Hkv, Nq, d, prefix_len > 0), s) != cudaSuccess)
       return FA_ERR_LAUNCH;
   }
   cudaError_t e = fa::launch_paged(a, s);
@@ -857,7 +859,7 @@ fa_status fa_kv_append(const void* k, long long k_stride_b, long long k_stride_h
   } else if (positions) {
     return FA_ERR_INVALID_ARG;  // positions of a rotation that is not asked for
   }
-  st = check_pages(k_pages, v_pages, num_pages, page_size, block_table, table_stride, max_pages, B, Hkv);
+  st = check_pages(k_pages, v_pages, num_pages, page_size, block_table, table_stride, max_pages, Hkv);
   if (st != FA_OK) return st;
   if (!aligned(k, 16) || !aligned(v, 16) || !aligned(seqlens_k, 4) || (seqlens_q && !aligned(seqlens_q, 4)))
     return FA_ERR_MISALIGNED;
@@ -901,10 +903,14 @@ fa_status fa_kv_append(const void* k, long long k_stride_b, long long k_stride_h
   return fa::launch_kv_append(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
 }
 
-size_t fa_fwd_paged_workspace_bytes(int B, int Hq, int Hkv, int Nq, int d) {
+static size_t paged_workspace_bytes(int B, int Hq, int Hkv, int Nq, int d, bool with_prefix) {
   if (B < 1 || Hq < 1 || Hkv < 1 || Nq < 1 || Hq % Hkv != 0 || (d != 64 && d != 128)) return 0;
   if (static_cast<long long>(B) * Hq * Nq >= (1LL << 31)) return 0;
-  return sizeof(float) * fa::paged_workspace_floats(B, Hkv, Hq / Hkv, Nq, d);
+  return sizeof(float) * fa::paged_workspace_floats(B, Hkv, Hq / Hkv, Nq, d, with_prefix);
+}
+
+size_t fa_fwd_paged_workspace_bytes(int B, int Hq, int Hkv, int Nq, int d) {
+  return paged_workspace_bytes(B, Hq, Hkv, Nq, d, false);
 }
 
 fa_status fa_fwd_paged(const void* q, const void* k_pages, const void* v_pages, int num_pages, int page_size,
@@ -916,7 +922,7 @@ fa_status fa_fwd_paged(const void* q, const void* k_pages, const void* v_pages, 
 }
 
 size_t fa_fwd_shared_prefix_workspace_bytes(int B, int Hq, int Hkv, int Nq, int d) {
-  return fa_fwd_paged_workspace_bytes(B, Hq, Hkv, Nq, d);
+  return paged_workspace_bytes(B, Hq, Hkv, Nq, d, true);
 }
 
 fa_status fa_fwd_shared_prefix(const void* q, const void* k_pages, const void* v_pages, int num_pages, int page_size,

@@ -64,10 +64,6 @@ struct StepLayout {
   static constexpr int kSmemBytes = kLineOff + (kLineSequences + 1) * 4 + 1024;
 };
 
-__device__ __forceinline__ uint32_t sw128(int r, int c) {
-  return static_cast<uint32_t>(r * 128 + ((c ^ (r & 7)) << 4));
-}
-
 __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -112,45 +108,6 @@ __device__ __forceinline__ void warps_sync() {
   asm volatile("barrier.cta.sync 1, %0;" ::"n"(32 * kStepWarps) : "memory");
 }
 
-// A walk over the pieces of sequences that a CTA's range of the line holds.
-struct Walk {
-  int b, head;      // sequence and key head of the piece
-  int tile, end;    // its tiles within the sequence: [tile, end)
-  int tiles;        // tiles of the sequence
-};
-
-__device__ __forceinline__ bool walk_begin(Walk& w, const int* line, int B, int Hkv, int at, int stop) {
-  if (at >= stop) return false;
-  // the last sequence that starts at or before `at` and has tiles
-  int lo = 0, hi = B - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (line[mid] * Hkv <= at) lo = mid; else hi = mid - 1;
-  }
-  w.b = lo;
-  w.tiles = line[lo + 1] - line[lo];
-  const int in = at - line[lo] * Hkv;
-  w.head = in / w.tiles;
-  w.tile = in - w.head * w.tiles;
-  w.end = min(w.tiles, w.tile + stop - at);
-  return true;
-}
-
-__device__ __forceinline__ bool walk_next(Walk& w, const int* line, int Hkv, int& at, int stop) {
-  at += w.end - w.tile;
-  if (at >= stop) return false;
-  if (++w.head == Hkv) {
-    w.head = 0;
-    do {
-      ++w.b;
-      w.tiles = line[w.b + 1] - line[w.b];
-    } while (w.tiles == 0);
-  }
-  w.tile = 0;
-  w.end = min(w.tiles, stop - at);
-  return true;
-}
-
 template <int D, int MB>
 __global__ void __launch_bounds__(kStepThreads, 2)
     paged_steps_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
@@ -182,18 +139,23 @@ __global__ void __launch_bounds__(kStepThreads, 2)
     prefetch_tensormap(&tm_v);
   }
   // the scratch of the scan is the row-maxima area, unused so far
-  build_line<kStepThreads>(line, reinterpret_cast<int*>(smem + L::kMaxOff), p.seq, kStepKeys);
+  build_line<kStepThreads>(line, reinterpret_cast<int*>(smem + L::kMaxOff), p.seq.B, [&](int b) {
+    int lq, lk;
+    seq_lens(p.seq, b, lq, lk);
+    return lq > 0 && lk > p.seq.prefix_len ? (lk - p.seq.prefix_len + kStepKeys - 1) / kStepKeys : 0;
+  });
+  auto starts = [&](int b) { return line[b]; };
   const int total = line[p.seq.B] * p.seq.Hkv;
   if (blockIdx.x == 0) {
     for (int i = threadIdx.x; i <= p.seq.B; i += kStepThreads) p.line_out[i] = line[i];
   }
-  const int per = tiles_per_cta(total, gridDim.x);
+  const int per = tiles_per_cta(total, gridDim.x, p.part.min_tiles);
   int at = min(static_cast<int>(blockIdx.x) * per, total);
   const int stop = min(at + per, total);
   const WaitCtl wc{abort_flag, p.status, p.wait_limit_ns};
   const int unit = static_cast<int>(blockIdx.x);
   Walk w;
-  bool more = walk_begin(w, line, p.seq.B, p.seq.Hkv, at, stop);
+  bool more = walk_begin(w, starts, p.seq.B, p.seq.Hkv, at, stop);
 
   if (warp == kStepWarps) {
     // ------------------------------------------------------------ TMA producer
@@ -208,9 +170,9 @@ __global__ void __launch_bounds__(kStepThreads, 2)
     bool ok = true;
     while (more && ok) {
       int lq, lk;
-      seq_lens(p.seq, w.b, lq, lk);
+      seq_lens(p.seq, w.e, lq, lk);
       const int first = p.seq.prefix_len + w.tile * kStepKeys;
-      const int* pages = p.table.block_table + w.b * p.table.table_stride;
+      const int* pages = p.table.block_table + w.e * p.table.table_stride;
       const int count = (w.end - w.tile) * boxes;
       // page of box i of the piece; -1 behind the sequence's end
       auto page_of = [&](int i) {
@@ -240,13 +202,13 @@ __global__ void __launch_bounds__(kStepThreads, 2)
             if (page >= 0 && page < p.table.num_pages)
               outer = page * p.seq.Hkv + w.head;
             else
-              record_bad_page(p.status, SITE_PAGE_READ, p.b0 + w.b, page);
+              record_bad_page(p.status, SITE_PAGE_READ, p.b0 + w.e, page);
           }
           tma_load_3d(sbase + s * L::kStage + offset, tm, full, 64 * (mine % CB), key % p.table.page_size, outer);
         }
         __syncwarp();
       }
-      if (ok) more = walk_next(w, line, p.seq.Hkv, at, stop);
+      if (ok) more = walk_next(w, starts, p.seq.Hkv, at, stop);
     }
     if (!ok && lane == 0) {
       // let the copies already issued land before the CTA can exit
@@ -281,8 +243,8 @@ __global__ void __launch_bounds__(kStepThreads, 2)
   bool ok = true;
   while (more && ok) {
     int lq, lk;
-    seq_lens(p.seq, w.b, lq, lk);
-    const size_t row0 = (static_cast<size_t>(w.b) * p.seq.Hkv + w.head) * rows;  // rows of the group lie together
+    seq_lens(p.seq, w.e, lq, lk);
+    const size_t row0 = (static_cast<size_t>(w.e) * p.seq.Hkv + w.head) * rows;  // rows of the group lie together
     uint32_t qf[MB][KS][4];
     int kend[MB][2];
 #pragma unroll
@@ -449,7 +411,7 @@ __global__ void __launch_bounds__(kStepThreads, 2)
     }
     warps_sync();
     const bool whole = p.direct && w.tile == 0 && w.end == w.tiles;
-    const size_t slot = static_cast<size_t>(w.b) * p.seq.Hkv + w.head + blockIdx.x;
+    const size_t slot = static_cast<size_t>(w.e) * p.seq.Hkv + w.head + blockIdx.x;
 #pragma unroll
     for (int m = 0; m < MB; ++m) {
 #pragma unroll
@@ -475,67 +437,109 @@ __global__ void __launch_bounds__(kStepThreads, 2)
             }
             if (warp == 0 && (lane & 3) == 0) p.lse[row0 + r] = live ? lse2 * kLn2 : -CUDART_INF_F;
           } else {
-            float* dst = p.part + (slot * rows + r) * D + col;
+            float* dst = p.part.o + (slot * rows + r) * D + col;
 #pragma unroll
             for (int n = 0; n < NT; ++n)
               *reinterpret_cast<float2*>(dst + 8 * n) =
                   live ? make_float2(acc[m][n][2 * e] * inv, acc[m][n][2 * e + 1] * inv) : make_float2(0.f, 0.f);
-            if (warp == 0 && (lane & 3) == 0) p.part_lse[slot * rows + r] = lse2;
+            if (warp == 0 && (lane & 3) == 0) p.part.lse[slot * rows + r] = lse2;
           }
         }
       }
     }
-    more = walk_next(w, line, p.seq.Hkv, at, stop);
+    more = walk_next(w, starts, p.seq.Hkv, at, stop);
   }
 }
 
-// Merges a row's partial results.  WARPS warps share a row.
-template <int D, int WARPS>
+// Where row `in` of unit (entry, head) has its partial results.
+struct Pieces {
+  int n;              // pieces
+  int c0;             // first CTA
+  long long unit;
+  bool first_whole;   // the first piece starts its CTA's range
+};
+
+__device__ __forceinline__ Pieces pieces_of(const PartRef& r, int entry, int entries, int head, int Hkv) {
+  Pieces x;
+  const int t0 = r.line ? r.line[entry] : entry * *r.uniform;
+  const int nt = r.line ? r.line[entry + 1] - t0 : *r.uniform;
+  const int total = (r.line ? r.line[entries] : entries * *r.uniform) * Hkv;
+  const int per = tiles_per_cta(total, r.ctas, r.min_tiles);
+  const int from = t0 * Hkv + head * nt;
+  x.c0 = from / per;
+  x.n = nt ? (from + nt - 1) / per - x.c0 + 1 : 0;
+  x.unit = static_cast<long long>(entry) * Hkv + head;
+  x.first_whole = from == x.c0 * per;
+  return x;
+}
+
+__device__ __forceinline__ long long piece_row(const PartRef& r, const Pieces& x, int k, int in) {
+  const long long slot =
+      r.two_a_cta ? 2LL * (x.c0 + k) + (k > 0 || x.first_whole ? 0 : 1) : x.unit + x.c0 + k;
+  return slot * r.slot_rows + in;
+}
+
+// Merges a row's partial results: those of its sequence's own keys and those
+// of the shared prefix.  WARPS warps share a row.  TILES: the sequences' part
+// comes from the tile kernel, whose units are row pairs.
+template <int D, int WARPS, bool TILES>
 __global__ void __launch_bounds__(256) paged_combine_kernel(const PagedCombine p) {
   constexpr int CW = D / 32;
   constexpr int ROWS = 8 / WARPS;
-  __shared__ float s_max[8], s_sum[8], s_acc[8][D];
+  __shared__ float s_max[8], s_sum[8], s_acc[WARPS > 1 ? 8 : 1][D];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int sub = warp % WARPS;
-  const long long row = static_cast<long long>(blockIdx.x) * ROWS + warp / WARPS;
-  const bool in = row < static_cast<long long>(p.seq.B) * p.seq.Hkv * p.seq.G * p.seq.Nq;
+  const long long item = static_cast<long long>(blockIdx.x) * ROWS + warp / WARPS;
   const int rows = p.seq.G * p.seq.Nq;
-  const int group = in ? static_cast<int>(row / rows) : 0;  // (sequence, key head)
-  const int r = static_cast<int>(row - static_cast<long long>(group) * rows);
-  const int b = group / p.seq.Hkv, head = group - b * p.seq.Hkv;
-  // the line's partial results of the group: slots [first, first + n)
-  const int t0 = p.line[b], nt = p.line[b + 1] - t0;
-  const int per = tiles_per_cta(p.line[p.seq.B] * p.seq.Hkv, p.ctas);
-  const int from = t0 * p.seq.Hkv + head * nt;
-  const int c0 = from / per, n = nt ? (from + nt - 1) / per - c0 + 1 : 0;
-  const long long slot0 = group + c0;
-  const bool skip = !in || (p.direct && n == 1);  // written by the only CTA that had it
+  const int slot_rows = p.part.slot_rows;
+  bool in = item < static_cast<long long>(p.units) * slot_rows;
+  const int unit = in ? static_cast<int>(item / slot_rows) : 0;
+  const int at_row = in ? static_cast<int>(item - static_cast<long long>(unit) * slot_rows) : 0;
+  const int entry = unit / p.seq.Hkv, head = unit - entry * p.seq.Hkv;
+  int b = entry, r = at_row;
+  if constexpr (TILES) {
+    b = (p.e0 + entry) / p.pairs;
+    r = (p.e0 + entry - b * p.pairs) * kPairRows + at_row;
+    in = in && r < rows;
+  }
+  const Pieces own = pieces_of(p.part, entry, p.units / p.seq.Hkv, head, p.seq.Hkv);
+  const bool skip = !in || (p.direct && own.n == 1);  // written by the only CTA that had it
   float M = -CUDART_INF_F, sum = 0.f, acc[CW];
 #pragma unroll
   for (int c = 0; c < CW; ++c) acc[c] = 0.f;
-  auto add = [&](float lse, const float* src) {
-    if (lse == -CUDART_INF_F) return;  // the same in every lane
-    const float m = fmaxf(M, lse);
-    const float f = exp2f(lse - m), g = exp2f(M - m);
-    M = m;
-    sum = sum * g + f;
-#pragma unroll
-    for (int c = 0; c < CW; ++c) acc[c] = fmaf(f, src[c], acc[c] * g);
-  };
-  if (!skip) {
+  auto gather = [&](const PartRef& ref, const Pieces& x, int row_in) {
     constexpr int U = 4;
-    for (int i = sub; i < n; i += WARPS * U) {
-      float lse[U], x[U][CW];
+    for (int i = sub; i < x.n; i += WARPS * U) {
+      float lse[U], v[U][CW];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int k = i + u * WARPS;
-        const long long at = (slot0 + k) * rows + r;
-        lse[u] = k < n ? p.part_lse[at] : -CUDART_INF_F;
+        lse[u] = -CUDART_INF_F;
+        if (k < x.n) {
+          const long long at = piece_row(ref, x, k, row_in);
+          lse[u] = ref.lse[at];
 #pragma unroll
-        for (int c = 0; c < CW; ++c) x[u][c] = k < n ? p.part[at * D + CW * lane + c] : 0.f;
+          for (int c = 0; c < CW; ++c) v[u][c] = ref.o[at * D + CW * lane + c];
+        }
       }
 #pragma unroll
-      for (int u = 0; u < U; ++u) add(lse[u], x[u]);
+      for (int u = 0; u < U; ++u) {
+        if (lse[u] == -CUDART_INF_F) continue;  // the same in every lane
+        const float m = fmaxf(M, lse[u]);
+        const float f = exp2f(lse[u] - m), g = exp2f(M - m);
+        M = m;
+        sum = sum * g + f;
+#pragma unroll
+        for (int c = 0; c < CW; ++c) acc[c] = fmaf(f, v[u][c], acc[c] * g);
+      }
+    }
+  };
+  if (!skip) {
+    gather(p.part, own, at_row);
+    if (p.prefix.o) {
+      const long long all = static_cast<long long>(p.b0 + b) * rows + r;  // row among all sequences'
+      const int e = static_cast<int>(all / kPairRows);
+      gather(p.prefix, pieces_of(p.prefix, e, p.prefix_entries, head, p.seq.Hkv), static_cast<int>(all % kPairRows));
     }
   }
   if constexpr (WARPS > 1) {
@@ -561,14 +565,15 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const PagedCombine p
   if (skip) return;
   const bool live = sum > 0.f;
   const float inv = live ? 1.0f / sum : 0.f;
-  const size_t at = static_cast<size_t>(row) * D + CW * lane;
+  const size_t row = (static_cast<size_t>(b) * p.seq.Hkv + head) * rows + r;
+  const size_t at = row * D + CW * lane;
 #pragma unroll
   for (int c = 0; c < CW; c += 2) {
-    const float a = acc[c] * inv, e = acc[c + 1] * inv;
+    const float x = acc[c] * inv, y = acc[c + 1] * inv;
     if (p.o_bf16)
-      *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.o) + at + c) = pack_bf16x2(a, e);
+      *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.o) + at + c) = pack_bf16x2(x, y);
     else
-      *reinterpret_cast<float2*>(static_cast<float*>(p.o) + at + c) = make_float2(a, e);
+      *reinterpret_cast<float2*>(static_cast<float*>(p.o) + at + c) = make_float2(x, y);
   }
   if (lane == 0) p.lse[row] = live ? (M + log2f(sum)) * kLn2 : -CUDART_INF_F;
 }
@@ -585,134 +590,156 @@ cudaError_t launch_steps(const PagedArgs& a, const PagedStep& p, int ctas, cudaS
 }
 
 template <int D>
-cudaError_t launch_combine(const PagedCombine& p, cudaStream_t stream) {
-  const long long rows = static_cast<long long>(p.seq.B) * p.seq.Hkv * p.seq.G * p.seq.Nq;
-  // few rows: four warps a row, whose partial results then number the most
-  if (rows <= 2048)
-    paged_combine_kernel<D, 4><<<static_cast<unsigned>((rows + 1) / 2), 256, 0, stream>>>(p);
+cudaError_t launch_combine(const PagedCombine& p, bool tiles, cudaStream_t stream) {
+  const long long rows = static_cast<long long>(p.units) * p.part.slot_rows;
+  if (tiles)
+    paged_combine_kernel<D, 1, true><<<static_cast<unsigned>((rows + 7) / 8), 256, 0, stream>>>(p);
+  else if (rows <= 2048)  // few rows: four warps a row, whose partial results then number the most
+    paged_combine_kernel<D, 4, false><<<static_cast<unsigned>((rows + 1) / 2), 256, 0, stream>>>(p);
   else
-    paged_combine_kernel<D, 1><<<static_cast<unsigned>((rows + 7) / 8), 256, 0, stream>>>(p);
+    paged_combine_kernel<D, 1, false><<<static_cast<unsigned>((rows + 7) / 8), 256, 0, stream>>>(p);
   return cudaGetLastError();
 }
 
+// How a call is divided, and where its partial results lie in the workspace
+// (offsets in 4-byte words).
+struct Plan {
+  int rows, pairs;            // rows a key head of a sequence, and its row pairs
+  bool steps;                 // the sequences' own keys: the step kernel, else the tile kernel
+  int chunk;                  // sequences (steps) or entries (tiles) a launch
+  long long prefix_entries;   // row pairs of all sequences' rows
+  size_t own_slots, prefix_slots;
+  size_t own, prefix, words;
+};
+
+Plan make_plan(int B, int Hkv, int G, int Nq, int d, bool with_prefix) {
+  Plan x;
+  x.rows = G * Nq;
+  x.pairs = (x.rows + kPairRows - 1) / kPairRows;
+  x.steps = x.rows <= kStepRows;
+  const long long entries = x.steps ? B : static_cast<long long>(B) * x.pairs;
+  x.chunk = static_cast<int>(entries < kLineSequences ? entries : kLineSequences);
+  const size_t units = static_cast<size_t>(x.chunk) * Hkv;
+  x.own_slots = x.steps ? units + kMaxCtas : (with_prefix ? units + kMaxTileCtas : 2 * kMaxTileCtas);
+  const size_t own_words = x.own_slots * (x.steps ? x.rows : kPairRows) * (d + 1);
+  x.prefix_entries = (static_cast<long long>(B) * x.rows + kPairRows - 1) / kPairRows;
+  x.prefix_slots = with_prefix ? static_cast<size_t>(x.prefix_entries) * Hkv + kMaxTileCtas : 0;
+  x.own = 2 * kLineWords;     // the line's table, the prefix's word
+  x.prefix = x.own + (own_words + 3) / 4 * 4;
+  x.words = x.prefix + x.prefix_slots * kPairRows * (d + 1);
+  return x;
+}
+
 template <int D>
-cudaError_t launch_steps_d(const PagedArgs& a, cudaStream_t stream) {
-  const int G = a.Hq / a.Hkv, rows = G * a.Nq;
-  const int capacity = a.table.max_pages * a.table.page_size;
-  for (int b0 = 0; b0 < a.B; b0 += kLineSequences) {
-    const int B = a.B - b0 < kLineSequences ? a.B - b0 : kLineSequences;
-    const size_t first = static_cast<size_t>(b0) * a.Hq * a.Nq;
-    PagedStep p;
-    p.seq = PagedSeq{a.seqlens_q ? a.seqlens_q + b0 : nullptr, a.seqlens_k ? a.seqlens_k + b0 : nullptr, B, a.Hkv, G,
-                     a.Nq, capacity, a.prefix_len};
-    p.table = a.table;
-    p.table.block_table += b0 * a.table.table_stride;
-    p.q = a.q + first * D;
-    p.o = static_cast<uint8_t*>(a.o) + first * D * (a.o_bf16 ? 2 : 4);
-    p.o_bf16 = a.o_bf16;
-    p.lse = a.lse + first;
-    const size_t slots = static_cast<size_t>(B) * a.Hkv + kMaxCtas;
-    p.line_out = reinterpret_cast<int*>(a.part);
-    p.part = a.part + kLineWords;
-    p.part_lse = p.part + slots * rows * D;
-    p.direct = a.prefix_len == 0;
-    p.box_rows = a.box_rows;
-    p.b0 = b0;
-    p.causal = a.causal;
-    p.scale_log2 = a.scale_log2;
-    p.status = a.status;
-    p.wait_limit_ns = a.wait_limit_ns;
-    p.stall_unit = a.stall_unit;
-    const int ctas = 2 * a.sms < kMaxCtas ? 2 * a.sms : kMaxCtas;
-    cudaError_t e = rows <= 16 ? launch_steps<D, 1>(a, p, ctas, stream) : launch_steps<D, 2>(a, p, ctas, stream);
+cudaError_t launch_paged_d(const PagedArgs& a, cudaStream_t stream) {
+  const int G = a.Hq / a.Hkv;
+  const bool with_prefix = a.prefix_len > 0;
+  const Plan x = make_plan(a.B, a.Hkv, G, a.Nq, D, with_prefix);
+  const int step_ctas = 2 * a.sms < kMaxCtas ? 2 * a.sms : kMaxCtas;
+  const int tile_ctas = a.sms < kMaxTileCtas ? a.sms : kMaxTileCtas;
+  int* line = reinterpret_cast<int*>(a.part);
+  int* uniform = line + kLineWords;
+  const PagedSeq all{a.seqlens_q, a.seqlens_k, a.B, a.Hkv, G, a.Nq, a.table.max_pages * a.table.page_size,
+                     a.prefix_len};
+  PartRef prefix{};
+  PagedTiles t{};
+  t.seq = all;
+  t.table = a.table;
+  t.prefix_table = a.prefix_table;
+  t.q = a.q;
+  t.o = a.o;
+  t.o_bf16 = a.o_bf16;
+  t.lse = a.lse;
+  t.pairs = x.pairs;
+  t.box_rows = a.box_rows;
+  t.causal = a.causal;
+  t.scale_log2 = a.scale_log2;
+  t.status = a.status;
+  t.wait_limit_ns = a.wait_limit_ns;
+  t.stall_unit = a.stall_unit;
+  cudaError_t e;
+  if (with_prefix) {
+    prefix = PartRef{nullptr, uniform, tile_ctas, kMinTiles, 0, kPairRows, a.part + x.prefix,
+                     a.part + x.prefix + x.prefix_slots * kPairRows * D};
+    PagedTiles p = t;
+    p.line_out = uniform;
+    p.part = prefix;
+    p.e0 = 0;
+    p.entries = static_cast<int>(x.prefix_entries);
+    e = launch_tiles(p, a.tm_k, a.tm_v, D, tile_ctas, stream);
     if (e != cudaSuccess) return e;
-    PagedCombine c;
-    c.seq = p.seq;
-    c.line = p.line_out;
-    c.ctas = ctas;
-    c.part = p.part;
-    c.part_lse = p.part_lse;
-    c.direct = p.direct;
-    c.o = p.o;
-    c.o_bf16 = p.o_bf16;
-    c.lse = p.lse;
-    e = launch_combine<D>(c, stream);
+  }
+  const long long entries = x.steps ? a.B : static_cast<long long>(a.B) * x.pairs;
+  for (long long e0 = 0; e0 < entries; e0 += x.chunk) {
+    const int n = static_cast<int>(entries - e0 < x.chunk ? entries - e0 : x.chunk);
+    PagedCombine c{};
+    c.seq = all;
+    c.prefix = prefix;
+    c.direct = !with_prefix;
+    c.prefix_entries = static_cast<int>(x.prefix_entries);
+    c.pairs = x.pairs;
+    c.units = n * a.Hkv;
+    c.o = a.o;
+    c.o_bf16 = a.o_bf16;
+    c.lse = a.lse;
+    const int slot_rows = x.steps ? x.rows : kPairRows;
+    c.part = PartRef{line, nullptr, x.steps ? step_ctas : tile_ctas, x.steps ? kMinSteps : kMinTiles,
+                     !x.steps && !with_prefix, slot_rows, a.part + x.own, a.part + x.own + x.own_slots * slot_rows * D};
+    if (x.steps) {
+      const int b0 = static_cast<int>(e0);
+      const size_t first = static_cast<size_t>(b0) * a.Hq * a.Nq;
+      PagedStep p;
+      p.seq = all;
+      p.seq.B = n;
+      if (p.seq.seqlens_q) p.seq.seqlens_q += b0;
+      if (p.seq.seqlens_k) p.seq.seqlens_k += b0;
+      p.table = a.table;
+      p.table.block_table += b0 * a.table.table_stride;
+      p.q = a.q + first * D;
+      p.o = static_cast<uint8_t*>(a.o) + first * D * (a.o_bf16 ? 2 : 4);
+      p.o_bf16 = a.o_bf16;
+      p.lse = a.lse + first;
+      p.line_out = line;
+      p.part = c.part;
+      p.direct = c.direct;
+      p.box_rows = a.box_rows;
+      p.b0 = b0;
+      p.causal = a.causal;
+      p.scale_log2 = a.scale_log2;
+      p.status = a.status;
+      p.wait_limit_ns = a.wait_limit_ns;
+      p.stall_unit = a.stall_unit;
+      e = x.rows <= 16 ? launch_steps<D, 1>(a, p, step_ctas, stream) : launch_steps<D, 2>(a, p, step_ctas, stream);
+      c.seq = p.seq;
+      c.b0 = b0;
+      c.o = p.o;
+      c.lse = p.lse;
+    } else {
+      PagedTiles p = t;
+      p.prefix_table = nullptr;
+      p.line_out = line;
+      p.part = c.part;
+      p.direct = c.direct;
+      p.e0 = static_cast<int>(e0);
+      p.entries = n;
+      e = launch_tiles(p, a.tm_k, a.tm_v, D, tile_ctas, stream);
+      c.e0 = p.e0;
+    }
+    if (e != cudaSuccess) return e;
+    e = launch_combine<D>(c, !x.steps, stream);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
 }
 
-__device__ __forceinline__ float bf16_at(const uint16_t* p) {
-  return __uint_as_float(static_cast<uint32_t>(__ldg(p)) << 16);
-}
-
-template <int D>
-__global__ void __launch_bounds__(128) paged_rows_kernel(const PagedArgs a) {
-  constexpr int CW = D / 32;
-  const long long row = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  if (row >= static_cast<long long>(a.B) * a.Hq * a.Nq) return;
-  const int lane = threadIdx.x & 31;
-  const int i = static_cast<int>(row % a.Nq);
-  const int hq = static_cast<int>(row / a.Nq % a.Hq);
-  const int b = static_cast<int>(row / a.Nq / a.Hq);
-  const int kh = hq / (a.Hq / a.Hkv);
-  const int ps = a.table.page_size;
-  int lq, lk;
-  paged_lens(a.seqlens_q, a.seqlens_k, b, a.Nq, a.table.max_pages * ps, lq, lk);
-  const int end = i < lq ? (a.causal ? min(i + lk - lq + 1, lk) : lk) : 0;
-  float qv[CW], acc[CW];
-  for (int c = 0; c < CW; ++c) {
-    qv[c] = bf16_at(a.q + row * D + lane * CW + c) * a.scale_log2;
-    acc[c] = 0.f;
-  }
-  float m = -CUDART_INF_F, l = 0.f;
-  for (int j = 0; j < end; ++j) {
-    const int page = j < a.prefix_len ? __ldg(a.prefix_table + j / ps)
-                                      : __ldg(a.table.block_table + b * a.table.table_stride + j / ps);
-    if (page < 0 || page >= a.table.num_pages) {
-      if (lane == 0) record_bad_page(a.status, SITE_PAGE_READ, b, page);
-      continue;
-    }
-    const long long at = ((static_cast<long long>(page) * a.Hkv + kh) * ps + j % ps) * D + lane * CW;
-    float s = 0.f;
-    for (int c = 0; c < CW; ++c) s = fmaf(qv[c], bf16_at(a.k_pages + at + c), s);
-    for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-    const float mn = fmaxf(m, s);
-    const float alpha = exp2f(m - mn), p = exp2f(s - mn);
-    l = l * alpha + p;
-    for (int c = 0; c < CW; ++c) acc[c] = acc[c] * alpha + p * bf16_at(a.v_pages + at + c);
-    m = mn;
-  }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-  for (int c = 0; c < CW; ++c) {
-    const float o = acc[c] * inv;
-    if (a.o_bf16)
-      static_cast<uint16_t*>(a.o)[row * D + lane * CW + c] = static_cast<uint16_t>(pack_bf16x2(o, 0.f));
-    else
-      static_cast<float*>(a.o)[row * D + lane * CW + c] = o;
-  }
-  if (lane == 0) a.lse[row] = l > 0.f ? (m + log2f(l)) * kLn2 : -CUDART_INF_F;
-}
-
 }  // namespace
 
-size_t paged_workspace_floats(int B, int Hkv, int G, int Nq, int d) {
-  const long long rows = static_cast<long long>(G) * Nq;
-  if (rows > kStepRows) return 4;
-  const size_t slots = static_cast<size_t>(B < kLineSequences ? B : kLineSequences) * Hkv + kMaxCtas;
-  return kLineWords + slots * rows * (d + 1);
+size_t paged_workspace_floats(int B, int Hkv, int G, int Nq, int d, bool with_prefix) {
+  return make_plan(B, Hkv, G, Nq, d, with_prefix).words;
 }
 
 cudaError_t launch_paged(const PagedArgs& a, cudaStream_t stream) {
-  if (a.prefix_len == 0 && static_cast<long long>(a.Hq / a.Hkv) * a.Nq <= kStepRows)
-    return a.d == 64 ? launch_steps_d<64>(a, stream) : launch_steps_d<128>(a, stream);
-  const long long rows = static_cast<long long>(a.B) * a.Hq * a.Nq;
-  const unsigned grid = static_cast<unsigned>((rows + 3) / 4);
-  if (a.d == 64)
-    paged_rows_kernel<64><<<grid, 128, 0, stream>>>(a);
-  else
-    paged_rows_kernel<128><<<grid, 128, 0, stream>>>(a);
-  return cudaGetLastError();
+  return a.d == 64 ? launch_paged_d<64>(a, stream) : launch_paged_d<128>(a, stream);
 }
 
 }  // namespace fa

@@ -12,7 +12,10 @@ constexpr int kStepRows = 32;          // rows a key head that the step kernel t
 constexpr int kLineSequences = 1024;   // sequences a launch: the line's table is in shared memory
 constexpr int kLineWords = 1040;       // 4-byte words of the line in the workspace, a multiple of 4
 constexpr int kMaxCtas = 512;
-constexpr int kMinTiles = 4;           // key tiles a CTA takes at least
+constexpr int kMinSteps = 4;           // key tiles (64 keys) a CTA of the step kernel takes at least
+constexpr int kMinTiles = 2;           // key tiles (128 keys) a CTA of the tile kernel takes at least
+constexpr int kMaxTileCtas = 256;
+constexpr int kPairRows = 256;         // query rows a unit of the tile kernel: two 128-row tiles
 static_assert(kLineWords >= kLineSequences + 1 && kLineWords % 4 == 0, "the line's room");
 
 struct PagedSeq {
@@ -20,6 +23,19 @@ struct PagedSeq {
   int B, Hkv, G, Nq;
   int capacity;     // positions that the table reaches
   int prefix_len;   // keys that are not these tiles' work
+};
+
+// Partial results of the units (a sequence's or row pair's part and a key
+// head) that CTAs cut out of a line of key tiles.  Unit u's piece of CTA c is
+// in slot u + c, which no other piece has; with two_a_cta, where only a CTA's
+// first and last pieces are partial, in slot 2 c (its first) or 2 c + 1.
+struct PartRef {
+  const int* line;     // first tile of every entry, in tiles of one key head; null: `uniform` tiles each
+  const int* uniform;  // tiles of every entry (one word)
+  int ctas, min_tiles;
+  int two_a_cta;
+  int slot_rows;
+  float *o, *lse;      // [slot][slot_rows][d], [slot][slot_rows] (log2 units)
 };
 
 struct PagedStep {
@@ -30,8 +46,8 @@ struct PagedStep {
   int o_bf16;
   float* lse;
   int* line_out;     // the line's table, for the combine
-  float *part, *part_lse;  // [slot][G * Nq][d] outputs and [slot][G * Nq] log2-sum-exp
-  int direct;        // 1: a piece that is a whole sequence's writes o and lse
+  PartRef part;
+  int direct;        // 1: a piece that is a whole unit's writes o and lse
   int box_rows;
   int b0;            // first sequence of this launch, for error reports
   int causal;
@@ -41,42 +57,73 @@ struct PagedStep {
   int stall_unit;
 };
 
+// The tile kernel: entries are row pairs (256 rows) of a sequence, or of all
+// sequences' rows together against the shared prefix.
+struct PagedTiles {
+  PagedSeq seq;
+  PageTable table;
+  const int* prefix_table;
+  const uint16_t* q;
+  void* o;
+  int o_bf16;
+  float* lse;
+  int* line_out;     // the line's table, or the one word of a prefix
+  PartRef part;
+  int direct;
+  int pairs;         // row pairs a sequence
+  int e0, entries;   // entries of this launch
+  int box_rows;
+  int causal;
+  float scale_log2;
+  int* status;
+  unsigned long long wait_limit_ns;
+  int stall_unit;
+};
+
 struct PagedCombine {
   PagedSeq seq;
-  const int* line;
-  int ctas;
-  const float *part, *part_lse;
+  PartRef part;      // the sequences' own keys
+  PartRef prefix;    // the shared prefix (o null: none)
   int direct;
+  int pairs, e0;     // the tile kernel's entries
+  int units;         // units of this launch
+  int b0;            // sequences before this launch's first (rows of the prefix)
+  int prefix_entries;
   void* o;
   int o_bf16;
   float* lse;
 };
+
+cudaError_t launch_tiles(const PagedTiles& p, const CUtensorMap& tm_k, const CUtensorMap& tm_v, int d, int ctas,
+                         cudaStream_t stream);
 
 #if defined(__CUDACC__)
 __device__ __forceinline__ void seq_lens(const PagedSeq& s, int b, int& lq, int& lk) {
   paged_lens(s.seqlens_q, s.seqlens_k, b, s.Nq, s.capacity, lq, lk);
 }
 
-// Tiles of the line that each CTA takes.
-__device__ __forceinline__ int tiles_per_cta(int total, int ctas) {
-  return max((total + ctas - 1) / ctas, kMinTiles);
+// Byte offset of 16-byte chunk c of row r inside a 128-byte-swizzled box
+// (the chunk index is XORed with the row index modulo 8).
+__device__ __forceinline__ uint32_t sw128(int r, int c) {
+  return static_cast<uint32_t>(r * 128 + ((c ^ (r & 7)) << 4));
 }
 
-// line[b] = tiles of one key head of all sequences before b, for b in
-// [0, B]; `scratch` holds one word a warp.  Ends with a CTA-wide barrier.
-template <int THREADS>
-__device__ __forceinline__ void build_line(int* line, int* scratch, const PagedSeq& s, int tile_keys) {
+// Tiles of the line that each CTA takes.
+__device__ __forceinline__ int tiles_per_cta(int total, int ctas, int least) {
+  return max((total + ctas - 1) / ctas, least);
+}
+
+// line[e] = tiles of one key head of all entries before e, for e in
+// [0, entries]; tiles_of(e) counts an entry's; `scratch` holds one word a
+// warp.  Ends with a CTA-wide barrier.
+template <int THREADS, typename F>
+__device__ __forceinline__ void build_line(int* line, int* scratch, int entries, F tiles_of) {
   constexpr int WARPS = THREADS / 32;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int base = 0;
-  for (int b0 = 0; b0 < s.B; b0 += THREADS) {
-    const int b = b0 + static_cast<int>(threadIdx.x);
-    int n = 0;
-    if (b < s.B) {
-      int lq, lk;
-      seq_lens(s, b, lq, lk);
-      if (lq > 0 && lk > s.prefix_len) n = (lk - s.prefix_len + tile_keys - 1) / tile_keys;
-    }
+  for (int e0 = 0; e0 < entries; e0 += THREADS) {
+    const int e = e0 + static_cast<int>(threadIdx.x);
+    const int n = e < entries ? tiles_of(e) : 0;
     int x = n;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -92,10 +139,53 @@ __device__ __forceinline__ void build_line(int* line, int* scratch, const PagedS
       if (i < warp) before += scratch[i];
       base += scratch[i];
     }
-    if (b < s.B) line[b] = before + x - n;
+    if (e < entries) line[e] = before + x - n;
   }
-  if (threadIdx.x == 0) line[s.B] = base;
+  if (threadIdx.x == 0) line[entries] = base;
   __syncthreads();
+}
+
+// A walk over the pieces of units that a CTA's range [at, stop) of the line
+// holds.  starts(e) is the first tile of entry e in tiles of one key head.
+struct Walk {
+  int e, head;      // entry and key head of the piece
+  int tile, end;    // its tiles within the unit: [tile, end)
+  int tiles;        // tiles of the unit
+};
+
+template <typename F>
+__device__ __forceinline__ bool walk_begin(Walk& w, F starts, int entries, int Hkv, int at, int stop) {
+  if (at >= stop) return false;
+  // the last entry that starts at or before `at` (one with tiles: an empty
+  // one starts where its successor does)
+  int lo = 0, hi = entries - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (starts(mid) * Hkv <= at) lo = mid; else hi = mid - 1;
+  }
+  w.e = lo;
+  w.tiles = starts(lo + 1) - starts(lo);
+  const int in = at - starts(lo) * Hkv;
+  w.head = in / w.tiles;
+  w.tile = in - w.head * w.tiles;
+  w.end = min(w.tiles, w.tile + stop - at);
+  return true;
+}
+
+template <typename F>
+__device__ __forceinline__ bool walk_next(Walk& w, F starts, int Hkv, int& at, int stop) {
+  at += w.end - w.tile;
+  if (at >= stop) return false;
+  if (++w.head == Hkv) {
+    w.head = 0;
+    do {
+      ++w.e;
+      w.tiles = starts(w.e + 1) - starts(w.e);
+    } while (w.tiles == 0);
+  }
+  w.tile = 0;
+  w.end = min(w.tiles, stop - at);
+  return true;
 }
 #endif
 

@@ -95,7 +95,7 @@ cudaError_t launch_kv_append(const AppendArgs& a, cudaStream_t stream);
 cudaError_t launch_paged(const PagedArgs& a, cudaStream_t stream);
 
 // Workspace of launch_paged in 4-byte words.
-size_t paged_workspace_floats(int B, int Hkv, int G, int Nq, int d);
+size_t paged_workspace_floats(int B, int Hkv, int G, int Nq, int d, bool with_prefix);
 
 #if defined(__CUDACC__)
 // Records an entry of a block table that names no page (first failure wins).

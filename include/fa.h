@@ -463,9 +463,9 @@ fa_status fa_rope(const void* x, int x_dtype, long long x_stride_b, long long x_
  * of length arrays serves the append and the attention of a step.
  * A table entry outside [0, num_pages) reads or writes nothing: the call
  * reports FA_ERR_BAD_PAGE through fa_sync_status, and the results of the
- * sequences that name it are unspecified.  max_pages * page_size,
- * num_pages * Hkv and B * Hkv * (max_pages * page_size / 64) must be below
- * 2^31.
+ * sequences that name it are unspecified.  max_pages * page_size
+ * and num_pages * Hkv must be below 2^31; for the attention calls so must
+ * B * Hkv * (Hq / Hkv * Nq / 256 + 1) * (max_pages * page_size / 64 + 1).
  */
 
 /*

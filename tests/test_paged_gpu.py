@@ -118,6 +118,9 @@ CHUNKS = [
     (2, 1, 1, 257, 64, 16, [300, 100], [257, 257]),              # second: 157 rows see nothing
     (1, 3, 1, 129, 128, 256, [5000], None),
     (1, 16, 2, 33, 64, 64, [2000], None),
+    (1, 1, 1, 140, 128, 16, [41000], None),                      # long ranges: the ring goes round
+    (2, 2, 1, 700, 128, 64, [3001, 9001], [700, 600]),           # heads of 700 rows: tiles across two heads
+    (3, 3, 3, 200, 64, 32, [6001, 12007, 300], None),
 ]
 
 
