@@ -635,17 +635,15 @@ _ROPE_SCALINGS = {None: FA_ROPE_SCALE_NONE, "linear": FA_ROPE_SCALE_LINEAR, "ntk
                   "parts": FA_ROPE_SCALE_PARTS}
 
 
-def _need(ok: bool, message: str) -> None:
-    if not ok:
-        raise ValueError(message)
-
+# A decoding step is a few microseconds of kernels, so these calls keep their
+# checks to a few attribute reads, and name what is wrong only when something is.
 
 def _call_on(index: int, call, *args) -> int:
     """The C call with the tensors' device current (its kernels launch there)
     on that device's current PyTorch stream."""
     import torch
-    stream = torch.cuda.current_stream(index).cuda_stream
-    if torch.cuda.current_device() == index:
+    stream = torch._C._cuda_getCurrentRawStream(index)
+    if torch._C._cuda_getDevice() == index:
         return call(*args, stream)
     with torch.cuda.device(index):
         return call(*args, stream)
@@ -657,45 +655,56 @@ def rope_turns(rot_dim: int, base: float = 10000.0, scaling: str | None = None, 
     [rot_dim / 2], in units of 2^-64 turns per position, on ``device``.
     ``scaling``: None, "linear", "ntk" or "parts" (see include/fa.h)."""
     import torch
-    _need(scaling in _ROPE_SCALINGS, "scaling must be None, 'linear', 'ntk' or 'parts'")
+    if scaling not in _ROPE_SCALINGS:
+        raise ValueError("scaling must be None, 'linear', 'ntk' or 'parts'")
     out = (ctypes.c_longlong * max(int(rot_dim) // 2, 1))()
     _check("fa_rope_turns", lib().fa_rope_turns(out, rot_dim, base, _ROPE_SCALINGS[scaling], factor, original_len, low,
                                                 high))
     return torch.tensor(list(out), dtype=torch.int64, device=device)
 
 
-def _rope_args(turns, layout, positions, B, N, device):
-    """(turns, rot_dim, layout, positions, positions stride) of a rotary call."""
+def _rope_args(turns, layout, positions, B, N, index):
+    """(positions, positions stride, turns, rot_dim, layout) of a rotary call."""
     import torch
-    _need(layout in _ROPE_LAYOUTS, "layout must be 'half' or 'interleaved'")
-    _need(turns.dtype == torch.int64 and turns.dim() == 1 and turns.is_contiguous() and turns.device == device,
-          "turns must be a contiguous int64 tensor of rot_dim / 2 entries on the inputs' device")
-    pos, stride = 0, 0
-    if positions is not None:
-        _need(positions.dtype == torch.int32 and positions.device == device and positions.dim() in (1, 2)
-              and positions.shape[-1] == N and (N == 1 or positions.stride(-1) == 1)
-              and (positions.dim() == 1 or positions.shape[0] == B),
-              "positions must be int32 [N] or [B, N] on the inputs' device with contiguous rows")
-        pos = positions.data_ptr()
-        stride = positions.stride(0) if positions.dim() == 2 else 0
-    return turns.data_ptr(), 2 * turns.numel(), _ROPE_LAYOUTS[layout], pos, stride
+    lay = _ROPE_LAYOUTS.get(layout)
+    if lay is None:
+        raise ValueError("layout must be 'half' or 'interleaved'")
+    if turns.dtype != torch.int64 or turns.dim() != 1 or not turns.is_contiguous() or turns.get_device() != index:
+        raise ValueError("turns must be a contiguous int64 tensor of rot_dim / 2 entries on the inputs' device")
+    if positions is None:
+        return 0, 0, turns.data_ptr(), 2 * turns.numel(), lay
+    if positions.dtype != torch.int32 or positions.get_device() != index or (
+            positions.shape != (B, N) and positions.shape != (N,)) or (N > 1 and positions.stride(-1) != 1):
+        raise ValueError("positions must be int32 [N] or [B, N] on the inputs' device with contiguous rows")
+    return (positions.data_ptr(), positions.stride(0) if positions.dim() == 2 else 0, turns.data_ptr(),
+            2 * turns.numel(), lay)
 
 
 def _rope(x, turns, positions, layout, amplitude, inverse, out, out_dtype):
     import torch
-    _need(x.is_cuda and x.dim() == 4 and x.dtype in (torch.bfloat16, torch.float32) and x.stride(3) == 1,
-          "x must be a bf16 or fp32 CUDA tensor [B, H, N, d] with contiguous d")
+    if x.dim() != 4 or not x.is_cuda:
+        raise ValueError("x must be a bf16 or fp32 CUDA tensor [B, H, N, d] with contiguous d")
     B, H, N, d = x.shape
-    t, rot_dim, lay, pos, pos_stride = _rope_args(turns, layout, positions, B, N, x.device)
+    xb, xh, xn, one = x.stride()
+    index, dtype = x.get_device(), x.dtype
+    if one != 1 or (dtype != torch.bfloat16 and dtype != torch.float32):
+        raise ValueError("x must be a bf16 or fp32 CUDA tensor [B, H, N, d] with contiguous d")
+    pos, pos_stride, t, rot_dim, lay = _rope_args(turns, layout, positions, B, N, index)
     if out is None:
-        out = torch.empty((B, H, N, d), dtype=out_dtype or x.dtype, device=x.device)
-    _need(out.shape == x.shape and out.device == x.device and out.dtype in (torch.bfloat16, torch.float32)
-          and out.stride(3) == 1 and out_dtype in (None, out.dtype),
-          "out must be a bf16 or fp32 tensor of x's shape and device with contiguous d")
-    xs, ys = x.stride(), out.stride()
-    _check("fa_rope", _call_on(x.device.index, lib().fa_rope, x.data_ptr(), int(x.dtype == torch.bfloat16), xs[0],
-                               xs[1], xs[2], out.data_ptr(), int(out.dtype == torch.bfloat16), ys[0], ys[1], ys[2],
-                               pos, pos_stride, t, rot_dim, lay, amplitude, inverse, B, H, N, d))
+        if out_dtype is None:
+            out_dtype = dtype
+        out = torch.empty((B, H, N, d), dtype=out_dtype, device=x.device)
+    if out_dtype is None:
+        out_dtype = out.dtype
+    yb, yh, yn, one = out.stride()
+    if (one != 1 or out.shape != x.shape or out.get_device() != index or out.dtype != out_dtype
+            or (out_dtype != torch.bfloat16 and out_dtype != torch.float32)):
+        raise ValueError("out must be a bf16 or fp32 tensor of x's shape and device with contiguous d")
+    st = _call_on(index, (_lib or lib()).fa_rope, x.data_ptr(), dtype == torch.bfloat16, xb, xh, xn, out.data_ptr(),
+                  out_dtype == torch.bfloat16, yb, yh, yn, pos, pos_stride, t, rot_dim, lay, amplitude, inverse, B, H,
+                  N, d)
+    if st:
+        _check("fa_rope", st)
     return out
 
 
@@ -714,25 +723,28 @@ def rope_backward(dy, turns, positions=None, layout: str = "half", amplitude: fl
     return _rope(dy, turns, positions, layout, amplitude, 1, out, out_dtype)
 
 
-def _page_args(k_pages, v_pages, block_table, B, d, device):
-    """(num_pages, Hkv, page_size, max_pages) of a paged cache's tensors."""
+def _page_args(k_pages, v_pages, block_table, B, d, index):
+    """(k_pages, v_pages, num_pages, page_size) and (block_table, its stride,
+    max_pages) of the C calls, and Hkv."""
     import torch
-    _need(k_pages.dim() == 4 and k_pages.dtype == torch.bfloat16 and k_pages.is_contiguous()
-          and v_pages.dtype == torch.bfloat16 and v_pages.is_contiguous() and v_pages.shape == k_pages.shape
-          and k_pages.device == device and v_pages.device == device and k_pages.shape[3] == d,
-          "k_pages and v_pages must be contiguous bf16 [pages, Hkv, page_size, d] on the inputs' device")
-    _need(block_table.dim() == 2 and block_table.dtype == torch.int32 and block_table.shape[0] == B
-          and block_table.device == device and (block_table.shape[1] == 1 or block_table.stride(1) == 1),
-          "block_table must be int32 [B, max_pages] on the inputs' device with contiguous rows")
-    return k_pages.shape[0], k_pages.shape[1], k_pages.shape[2], block_table.shape[1]
+    shape = k_pages.shape
+    if (len(shape) != 4 or shape[3] != d or v_pages.shape != shape or k_pages.dtype != torch.bfloat16
+            or v_pages.dtype != torch.bfloat16 or not k_pages.is_contiguous() or not v_pages.is_contiguous()
+            or k_pages.get_device() != index or v_pages.get_device() != index):
+        raise ValueError("k_pages and v_pages must be contiguous bf16 [pages, Hkv, page_size, d] on the inputs' device")
+    if (block_table.dim() != 2 or block_table.dtype != torch.int32 or block_table.shape[0] != B
+            or block_table.get_device() != index or (block_table.shape[1] != 1 and block_table.stride(1) != 1)):
+        raise ValueError("block_table must be int32 [B, max_pages] on the inputs' device with contiguous rows")
+    return ((k_pages.data_ptr(), v_pages.data_ptr(), shape[0], shape[2]),
+            (block_table.data_ptr(), block_table.stride(0), block_table.shape[1]), shape[1])
 
 
-def _lens(t, B, device) -> int:
+def _lens(t, B, index) -> int:
     import torch
     if t is None:
         return 0
-    _need(t.dtype == torch.int32 and t.numel() == B and t.is_contiguous() and t.device == device,
-          "seqlens must be contiguous int32 tensors of B entries on the inputs' device")
+    if t.dtype != torch.int32 or t.numel() != B or not t.is_contiguous() or t.get_device() != index:
+        raise ValueError("seqlens must be contiguous int32 tensors of B entries on the inputs' device")
     return t.data_ptr()
 
 
@@ -746,72 +758,94 @@ def kv_append(k, v, k_pages, v_pages, block_table, seqlens_k, seqlens_q=None, tu
     with the new tokens; ``seqlens_q``: int32 [B], its new tokens (default N).
     Returns q_out, or None without q."""
     import torch
-    for t in (k, v) + ((q,) if q is not None else ()):
-        _need(t.is_cuda and t.dim() == 4 and t.dtype == torch.bfloat16 and t.stride(3) == 1 and t.device == k.device,
-              "q, k and v must be bf16 CUDA tensors [B, heads, N, d] of one device with contiguous d")
+    if k.dim() != 4 or not k.is_cuda:
+        raise ValueError("k must be a bf16 CUDA tensor [B, Hkv, N, d] with contiguous d")
     B, Hkv, N, d = k.shape
-    _need(v.shape == k.shape, "v must have k's shape")
-    num_pages, page_heads, page_size, max_pages = _page_args(k_pages, v_pages, block_table, B, d, k.device)
-    _need(page_heads == Hkv, "the pages must have k's heads")
-    _need(seqlens_k is not None, "seqlens_k is needed")
-    tp = rot_dim = lay = pos = pos_stride = 0
+    index = k.get_device()
+    kb, kh, kn, k1 = k.stride()
+    if v.shape != k.shape:
+        raise ValueError("v must have k's shape")
+    vb, vh, vn, v1 = v.stride()
+    if (k1 != 1 or v1 != 1 or k.dtype != torch.bfloat16 or v.dtype != torch.bfloat16 or v.get_device() != index):
+        raise ValueError("k and v must be bf16 CUDA tensors [B, Hkv, N, d] of one device with contiguous d")
+    pages, table, page_heads = _page_args(k_pages, v_pages, block_table, B, d, index)
+    if page_heads != Hkv:
+        raise ValueError("the pages must have k's heads")
+    if seqlens_k is None:
+        raise ValueError("seqlens_k is needed")
     if turns is not None:
-        tp, rot_dim, lay, pos, pos_stride = _rope_args(turns, layout, positions, B, N, k.device)
+        rope = _rope_args(turns, layout, positions, B, N, index)
+    elif positions is None:
+        rope = (0, 0, 0, 0, 0)
     else:
-        _need(positions is None, "positions without turns")
-    qp = op = Hq = 0
-    qs = (0, 0, 0)
-    if q is not None:
+        raise ValueError("positions without turns")
+    if q is None:
+        if q_out is not None:
+            raise ValueError("q_out without q")
+        qp = op = Hq = qb = qh = qn = 0
+    else:
+        if q.dim() != 4 or q.get_device() != index or q.dtype != torch.bfloat16:
+            raise ValueError("q must be a bf16 tensor [B, Hq, N, d] with the batch, length, d and device of k")
         Hq = q.shape[1]
-        _need(q.shape == (B, Hq, N, d), "q must be [B, Hq, N, d] with the batch, length and d of k")
+        qb, qh, qn, q1 = q.stride()
+        if q.shape != (B, Hq, N, d) or q1 != 1:
+            raise ValueError("q must be a bf16 tensor [B, Hq, N, d] with the batch, length, d and device of k")
         if q_out is None:
             q_out = torch.empty((B, Hq, N, d), dtype=torch.bfloat16, device=k.device)
-        _need(q_out.shape == q.shape and q_out.dtype == torch.bfloat16 and q_out.is_contiguous()
-              and q_out.device == k.device, "q_out must be contiguous bf16 of q's shape")
-        qp, qs, op = q.data_ptr(), q.stride(), q_out.data_ptr()
-    else:
-        _need(q_out is None, "q_out without q")
-    ks, vs = k.stride(), v.stride()
-    _check("fa_kv_append",
-           _call_on(k.device.index, lib().fa_kv_append, k.data_ptr(), ks[0], ks[1], ks[2], v.data_ptr(), vs[0], vs[1],
-                    vs[2], qp, qs[0], qs[1], qs[2], op, k_pages.data_ptr(), v_pages.data_ptr(), num_pages, page_size,
-                    block_table.data_ptr(), block_table.stride(0), max_pages, _lens(seqlens_q, B, k.device),
-                    _lens(seqlens_k, B, k.device), pos, pos_stride, tp, rot_dim, lay, amplitude, B, Hq, Hkv, N, d))
+        elif (q_out.shape != q.shape or q_out.dtype != torch.bfloat16 or not q_out.is_contiguous()
+              or q_out.get_device() != index):
+            raise ValueError("q_out must be contiguous bf16 of q's shape and device")
+        qp, op = q.data_ptr(), q_out.data_ptr()
+    st = _call_on(index, (_lib or lib()).fa_kv_append, k.data_ptr(), kb, kh, kn, v.data_ptr(), vb, vh, vn, qp, qb, qh,
+                  qn, op, *pages, *table, _lens(seqlens_q, B, index), _lens(seqlens_k, B, index), *rope, amplitude, B,
+                  Hq, Hkv, N, d)
+    if st:
+        _check("fa_kv_append", st)
     return q_out
 
 
 def _paged(name, q, k_pages, v_pages, prefix, block_table, seqlens_k, seqlens_q, causal, scale, o_dtype, workspace,
            out):
     import torch
-    _need(q.is_cuda and q.dtype == torch.bfloat16 and q.is_contiguous() and q.dim() == 4,
-          "q must be a contiguous bf16 CUDA tensor [B, Hq, Nq, d]")
+    if q.dim() != 4 or not q.is_cuda or q.dtype != torch.bfloat16 or not q.is_contiguous():
+        raise ValueError("q must be a contiguous bf16 CUDA tensor [B, Hq, Nq, d]")
     B, Hq, Nq, d = q.shape
-    dev = q.device
-    num_pages, Hkv, page_size, max_pages = _page_args(k_pages, v_pages, block_table, B, d, dev)
+    index = q.get_device()
+    pages, table, Hkv = _page_args(k_pages, v_pages, block_table, B, d, index)
     if scale is None:
-        scale = float(torch.tensor(d ** -0.5, dtype=torch.float32))
+        scale = d ** -0.5
     if out is None:
-        o = torch.empty((B, Hq, Nq, d), dtype=o_dtype or torch.float32, device=dev)
-        lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=dev)
+        dtype = torch.float32 if o_dtype is None else o_dtype
+        o = torch.empty((B, Hq, Nq, d), dtype=dtype, device=q.device)
+        lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=q.device)
     else:
         o, lse = out
-    _need(o.dtype in (torch.float32, torch.bfloat16), "O must be float32 or bfloat16")
-    _need(o.shape == q.shape and o.is_contiguous() and o.device == dev and lse.shape == q.shape[:3]
-          and lse.dtype == torch.float32 and lse.is_contiguous() and lse.device == dev,
-          "out must be contiguous O [B, Hq, Nq, d] and fp32 LSE [B, Hq, Nq] on q's device")
-    L = lib()
-    call = getattr(L, name)
-    need = getattr(L, name + "_workspace_bytes")(B, Hq, Hkv, Nq, d)
+        dtype = o.dtype
+        if (o.shape != q.shape or not o.is_contiguous() or o.get_device() != index or lse.shape != (B, Hq, Nq)
+                or lse.dtype != torch.float32 or not lse.is_contiguous() or lse.get_device() != index):
+            raise ValueError("out must be contiguous O [B, Hq, Nq, d] and fp32 LSE [B, Hq, Nq] on q's device")
+    if dtype != torch.float32 and dtype != torch.bfloat16:
+        raise ValueError("O must be float32 or bfloat16")
+    call, bytes_of = _paged_calls(name)
+    need = bytes_of(B, Hq, Hkv, Nq, d) // 4
     if workspace is None:
-        workspace = torch.empty(need // 4, dtype=torch.float32, device=dev)
-    _need(workspace.dtype == torch.float32 and workspace.is_contiguous() and workspace.device == dev
-          and 4 * workspace.numel() >= need, f"workspace must be fp32 on q's device, {name}_workspace_bytes(...) bytes")
-    _check(name, _call_on(dev.index, call, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), num_pages, page_size,
-                          *prefix, block_table.data_ptr(), block_table.stride(0), max_pages, o.data_ptr(),
-                          FA_DTYPE_BF16 if o.dtype == torch.bfloat16 else FA_DTYPE_F32, lse.data_ptr(),
-                          _lens(seqlens_q, B, dev), _lens(seqlens_k, B, dev), workspace.data_ptr(), B, Hq, Hkv, Nq, d,
-                          scale, int(bool(causal))))
+        workspace = torch.empty(need, dtype=torch.float32, device=q.device)
+    elif (workspace.dtype != torch.float32 or not workspace.is_contiguous() or workspace.get_device() != index
+          or workspace.numel() < need):
+        raise ValueError(f"workspace must be fp32 on q's device, {name}_workspace_bytes(...) bytes")
+    st = _call_on(index, call, q.data_ptr(), *pages, *prefix, *table, o.data_ptr(), dtype == torch.bfloat16,
+                  lse.data_ptr(), _lens(seqlens_q, B, index), _lens(seqlens_k, B, index), workspace.data_ptr(), B, Hq,
+                  Hkv, Nq, d, scale, bool(causal))
+    if st:
+        _check(name, st)
     return o, lse
+
+
+def _paged_calls(name):
+    L = _lib or lib()
+    if name == "fa_fwd_paged":
+        return L.fa_fwd_paged, L.fa_fwd_paged_workspace_bytes
+    return L.fa_fwd_shared_prefix, L.fa_fwd_shared_prefix_workspace_bytes
 
 
 def forward_paged(q, k_pages, v_pages, block_table, seqlens_k=None, seqlens_q=None, causal: bool = True,
@@ -834,10 +868,11 @@ def forward_shared_prefix(q, k_pages, v_pages, prefix_table, prefix_len: int, bl
     ``prefix_table`` int32 [prefix_len / page_size] names: that part is
     computed once for all, through fa_fwd_shared_prefix."""
     import torch
-    _need(prefix_table.dtype == torch.int32 and prefix_table.dim() == 1 and prefix_table.is_contiguous()
-          and prefix_table.device == q.device and prefix_len >= 1
-          and prefix_table.numel() * k_pages.shape[2] >= prefix_len,
-          "prefix_table must be contiguous int32 on q's device with an entry for every page of the prefix")
+    if (prefix_table.dtype != torch.int32 or prefix_table.dim() != 1 or not prefix_table.is_contiguous()
+            or prefix_table.get_device() != q.get_device() or prefix_len < 1 or k_pages.dim() != 4
+            or prefix_table.numel() * k_pages.shape[2] < prefix_len):
+        raise ValueError("prefix_table must be contiguous int32 on q's device with an entry for every page of the "
+                         "prefix")
     return _paged("fa_fwd_shared_prefix", q, k_pages, v_pages, (prefix_table.data_ptr(), int(prefix_len)), block_table,
                   seqlens_k, seqlens_q, causal, scale, o_dtype, workspace, out)
 

@@ -60,8 +60,8 @@ struct StepLayout {
   static constexpr int kBarOff = kPOff + 2 * kPHalf;    // FULL[s] then EMPTY[s]
   static constexpr int kMaxOff = kBarOff + 2 * kStages * 8;  // [warps][16 MB] row maxima, then row sums
   static constexpr int kMiscOff = kMaxOff + 2 * kStepWarps * 16 * MB * 4;
-  static constexpr int kLineOff = kMiscOff + 16;        // first tile of every sequence
-  static constexpr int kSmemBytes = kLineOff + (kLineSequences + 1) * 4 + 1024;
+  static constexpr int kLineOff = kMiscOff + 16;        // first tile of every sequence, then lq, then lk
+  static constexpr int kSmemBytes = kLineOff + (3 * kLineSequences + 1) * 4 + 1024;
 };
 
 __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
@@ -138,10 +138,16 @@ __global__ void __launch_bounds__(kStepThreads, 2)
     prefetch_tensormap(&tm_k);
     prefetch_tensormap(&tm_v);
   }
+  if (p.wait_first) grid_wait();
+  grid_trigger();
   // the scratch of the scan is the row-maxima area, unused so far
+  int* len_q = line + kLineSequences + 1;
+  int* len_k = len_q + kLineSequences;
   build_line<kStepThreads>(line, reinterpret_cast<int*>(smem + L::kMaxOff), p.seq.B, [&](int b) {
     int lq, lk;
     seq_lens(p.seq, b, lq, lk);
+    len_q[b] = lq;
+    len_k[b] = lk;
     return lq > 0 && lk > p.seq.prefix_len ? (lk - p.seq.prefix_len + kStepKeys - 1) / kStepKeys : 0;
   });
   auto starts = [&](int b) { return line[b]; };
@@ -168,22 +174,27 @@ __global__ void __launch_bounds__(kStepThreads, 2)
     const CUtensorMap* tm = mine / CB == 0 ? &tm_k : &tm_v;
     int issued = 0;
     bool ok = true;
+    // page of box i of a piece; -1 behind the sequence's end
+    auto page_of = [&](const Walk& x, int i) {
+      const int key = p.seq.prefix_len + x.tile * kStepKeys + i * p.box_rows;
+      return i < (x.end - x.tile) * boxes && key < len_k[x.e]
+                 ? __ldg(p.table.block_table + x.e * p.table.table_stride + key / p.table.page_size)
+                 : -1;
+    };
+    // pages are looked up 32 boxes ahead: the next ones of this piece, and the
+    // first of the piece after it
+    int ahead = more ? page_of(w, lane) : -1;
     while (more && ok) {
-      int lq, lk;
-      seq_lens(p.seq, w.e, lq, lk);
+      const int lk = len_k[w.e];
       const int first = p.seq.prefix_len + w.tile * kStepKeys;
-      const int* pages = p.table.block_table + w.e * p.table.table_stride;
-      const int count = (w.end - w.tile) * boxes;
-      // page of box i of the piece; -1 behind the sequence's end
-      auto page_of = [&](int i) {
-        const int key = first + i * p.box_rows;
-        return i < count && key < lk ? __ldg(pages + key / p.table.page_size) : -1;
-      };
-      int cur = page_of(lane), next = page_of(32 + lane);
+      int cur = ahead, next = page_of(w, 32 + lane);
+      Walk after = w;
+      int after_at = at;
+      if (walk_next(after, starts, p.seq.Hkv, after_at, stop)) ahead = page_of(after, lane);
       for (int t = 0; t < w.end - w.tile; ++t, ++issued) {
         if (t > 0 && (t * boxes) % 32 == 0) {
           cur = next;
-          next = page_of(t * boxes + 32 + lane);
+          next = page_of(w, t * boxes + 32 + lane);
         }
         const int s = issued % S;
         ok = __all_sync(0xffffffffu,
@@ -210,6 +221,7 @@ __global__ void __launch_bounds__(kStepThreads, 2)
       }
       if (ok) more = walk_next(w, starts, p.seq.Hkv, at, stop);
     }
+    if (!p.wait_first && lane == 0) grid_wait();
     if (!ok && lane == 0) {
       // let the copies already issued land before the CTA can exit
       for (int s = 0; s < S; ++s) {
@@ -239,35 +251,41 @@ __global__ void __launch_bounds__(kStepThreads, 2)
   const int p_half = lane >> 4;
   const int v_col = warp * (D / 4);  // first value column of this warp
   const uint32_t p_hi = sbase + L::kPOff, p_lo = p_hi + L::kPHalf;
+  uint32_t qf[MB][KS][4];
+  // the rows of a piece as fragments (rows of the group lie together)
+  auto load_q = [&](const Walk& x, auto& f) {
+    const uint16_t* base = p.q + (static_cast<size_t>(x.e) * p.seq.Hkv + x.head) * rows * D + qc;
+#pragma unroll
+    for (int m = 0; m < MB; ++m) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = 16 * m + 8 * e + qr;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          f[m][ks][e] = r < rows ? __ldg(reinterpret_cast<const uint32_t*>(base + r * D + 16 * ks)) : 0u;
+          f[m][ks][2 + e] = r < rows ? __ldg(reinterpret_cast<const uint32_t*>(base + r * D + 16 * ks + 8)) : 0u;
+        }
+      }
+    }
+  };
+  if (more) load_q(w, qf);
   int done = 0;
   bool ok = true;
   while (more && ok) {
-    int lq, lk;
-    seq_lens(p.seq, w.e, lq, lk);
-    const size_t row0 = (static_cast<size_t>(w.e) * p.seq.Hkv + w.head) * rows;  // rows of the group lie together
-    uint32_t qf[MB][KS][4];
+    const int lq = len_q[w.e], lk = len_k[w.e];
     int kend[MB][2];
 #pragma unroll
     for (int m = 0; m < MB; ++m) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int r = 16 * m + 8 * e + qr;
-        kend[m][e] = 0;
-        if (r < rows) {
-          const uint16_t* src = p.q + (row0 + r) * D + qc;
-#pragma unroll
-          for (int ks = 0; ks < KS; ++ks) {
-            qf[m][ks][e] = __ldg(reinterpret_cast<const uint32_t*>(src + 16 * ks));
-            qf[m][ks][2 + e] = __ldg(reinterpret_cast<const uint32_t*>(src + 16 * ks + 8));
-          }
-          const int i = r % p.seq.Nq;
-          if (i < lq) kend[m][e] = p.causal ? min(i + lk - lq + 1, lk) : lk;
-        } else {
-#pragma unroll
-          for (int ks = 0; ks < KS; ++ks) qf[m][ks][e] = qf[m][ks][2 + e] = 0u;
-        }
+        const int i = r % p.seq.Nq;
+        kend[m][e] = r < rows && i < lq ? (p.causal ? min(i + lk - lq + 1, lk) : lk) : 0;
       }
     }
+    Walk after = w;
+    int after_at = at;
+    const bool another = walk_next(after, starts, p.seq.Hkv, after_at, stop);
     float m_ref[MB][2], l[MB][2], acc[MB][NT][4];
 #pragma unroll
     for (int m = 0; m < MB; ++m) {
@@ -398,6 +416,8 @@ __global__ void __launch_bounds__(kStepThreads, 2)
       if (lane == 0) mbar_arrive(bars + 8 * (S + s));
     }
     if (!ok) break;
+    if (another) load_q(after, qf);  // in flight while this piece's results are written
+    const size_t row0 = (static_cast<size_t>(w.e) * p.seq.Hkv + w.head) * rows;
     // the row sums of all warps
 #pragma unroll
     for (int m = 0; m < MB; ++m) {
@@ -447,7 +467,9 @@ __global__ void __launch_bounds__(kStepThreads, 2)
         }
       }
     }
-    more = walk_next(w, starts, p.seq.Hkv, at, stop);
+    w = after;
+    at = after_at;
+    more = another;
   }
 }
 
@@ -479,103 +501,129 @@ __device__ __forceinline__ long long piece_row(const PartRef& r, const Pieces& x
   return slot * r.slot_rows + in;
 }
 
-// Merges a row's partial results: those of its sequence's own keys and those
-// of the shared prefix.  WARPS warps share a row.  TILES: the sequences' part
-// comes from the tile kernel, whose units are row pairs.
-template <int D, int WARPS, bool TILES>
-__global__ void __launch_bounds__(256) paged_combine_kernel(const PagedCombine p) {
+// Merges rows' partial results: those of the sequence's own keys and those of
+// the shared prefix.  A warp takes RPW rows of one unit (their pieces are the
+// same) or, where rows are few and pieces many, WARPS warps share one row.
+// TILES: the sequences' part comes from the tile kernel, whose units are row
+// pairs.
+template <int D, int WARPS, int RPW, bool TILES>
+__global__ void __launch_bounds__(256) paged_combine_kernel(const __grid_constant__ PagedCombine p) {
+  static_assert(WARPS == 1 || RPW == 1, "one or the other");
   constexpr int CW = D / 32;
-  constexpr int ROWS = 8 / WARPS;
+  constexpr int U = WARPS > 1 ? 4 : 2;  // pieces in flight
   __shared__ float s_max[8], s_sum[8], s_acc[WARPS > 1 ? 8 : 1][D];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int sub = warp % WARPS;
-  const long long item = static_cast<long long>(blockIdx.x) * ROWS + warp / WARPS;
   const int rows = p.seq.G * p.seq.Nq;
   const int slot_rows = p.part.slot_rows;
-  bool in = item < static_cast<long long>(p.units) * slot_rows;
-  const int unit = in ? static_cast<int>(item / slot_rows) : 0;
-  const int at_row = in ? static_cast<int>(item - static_cast<long long>(unit) * slot_rows) : 0;
+  const int groups = (slot_rows + RPW - 1) / RPW;  // of rows, in a unit
+  const long long item = static_cast<long long>(blockIdx.x) * (8 / WARPS) + warp / WARPS;
+  bool in = item < static_cast<long long>(p.units) * groups;
+  const int unit = in ? static_cast<int>(item / groups) : 0;
+  const int row_in = in ? static_cast<int>(item - static_cast<long long>(unit) * groups) * RPW : 0;
   const int entry = unit / p.seq.Hkv, head = unit - entry * p.seq.Hkv;
-  int b = entry, r = at_row;
+  int b = entry, r0 = row_in;
   if constexpr (TILES) {
     b = (p.e0 + entry) / p.pairs;
-    r = (p.e0 + entry - b * p.pairs) * kPairRows + at_row;
-    in = in && r < rows;
+    r0 = (p.e0 + entry - b * p.pairs) * kPairRows + row_in;
+    in = in && r0 < rows;
   }
+  grid_wait();
   const Pieces own = pieces_of(p.part, entry, p.units / p.seq.Hkv, head, p.seq.Hkv);
   const bool skip = !in || (p.direct && own.n == 1);  // written by the only CTA that had it
-  float M = -CUDART_INF_F, sum = 0.f, acc[CW];
+  const int count = skip ? 0 : min(RPW, (TILES ? min(rows - r0, slot_rows - row_in) : slot_rows - row_in));
+  float M[RPW], sum[RPW], acc[RPW][CW];
 #pragma unroll
-  for (int c = 0; c < CW; ++c) acc[c] = 0.f;
-  auto gather = [&](const PartRef& ref, const Pieces& x, int row_in) {
-    constexpr int U = 4;
+  for (int q = 0; q < RPW; ++q) {
+    M[q] = -CUDART_INF_F;
+    sum[q] = 0.f;
+#pragma unroll
+    for (int c = 0; c < CW; ++c) acc[q][c] = 0.f;
+  }
+  const long long all = static_cast<long long>(p.b0 + b) * rows + r0;  // row among all sequences'
+  auto gather = [&](const PartRef& ref, const Pieces& x, int in_slot, int q0, int qn) {
     for (int i = sub; i < x.n; i += WARPS * U) {
-      float lse[U], v[U][CW];
+      float lse[RPW][U], v[RPW][U][CW];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int k = i + u * WARPS;
-        lse[u] = -CUDART_INF_F;
-        if (k < x.n) {
-          const long long at = piece_row(ref, x, k, row_in);
-          lse[u] = ref.lse[at];
+        const long long at = piece_row(ref, x, k, in_slot);
 #pragma unroll
-          for (int c = 0; c < CW; ++c) v[u][c] = ref.o[at * D + CW * lane + c];
+        for (int q = 0; q < RPW; ++q) {
+          lse[q][u] = -CUDART_INF_F;
+          if (k < x.n && q >= q0 && q < qn) {
+            lse[q][u] = ref.lse[at + q];
+            const float* src = ref.o + (at + q) * D + CW * lane;
+            if constexpr (CW == 4)
+              *reinterpret_cast<float4*>(v[q][u]) = *reinterpret_cast<const float4*>(src);
+            else
+              *reinterpret_cast<float2*>(v[q][u]) = *reinterpret_cast<const float2*>(src);
+          }
         }
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        if (lse[u] == -CUDART_INF_F) continue;  // the same in every lane
-        const float m = fmaxf(M, lse[u]);
-        const float f = exp2f(lse[u] - m), g = exp2f(M - m);
-        M = m;
-        sum = sum * g + f;
 #pragma unroll
-        for (int c = 0; c < CW; ++c) acc[c] = fmaf(f, v[u][c], acc[c] * g);
+        for (int q = 0; q < RPW; ++q) {
+          if (lse[q][u] == -CUDART_INF_F) continue;  // the same in every lane
+          const float m = fmaxf(M[q], lse[q][u]);
+          const float f = exp2f(lse[q][u] - m), g = exp2f(M[q] - m);
+          M[q] = m;
+          sum[q] = sum[q] * g + f;
+#pragma unroll
+          for (int c = 0; c < CW; ++c) acc[q][c] = fmaf(f, v[q][u][c], acc[q][c] * g);
+        }
       }
     }
   };
-  if (!skip) {
-    gather(p.part, own, at_row);
+  if (count > 0) {
+    gather(p.part, own, row_in, 0, count);
     if (p.prefix.o) {
-      const long long all = static_cast<long long>(p.b0 + b) * rows + r;  // row among all sequences'
-      const int e = static_cast<int>(all / kPairRows);
-      gather(p.prefix, pieces_of(p.prefix, e, p.prefix_entries, head, p.seq.Hkv), static_cast<int>(all % kPairRows));
+      // the rows may cross from one row pair of the prefix into the next
+      const int e = static_cast<int>(all / kPairRows), in_pair = static_cast<int>(all % kPairRows);
+      const int here = min(count, kPairRows - in_pair);
+      gather(p.prefix, pieces_of(p.prefix, e, p.prefix_entries, head, p.seq.Hkv), in_pair, 0, here);
+      if (here < count)
+        gather(p.prefix, pieces_of(p.prefix, e + 1, p.prefix_entries, head, p.seq.Hkv), -here, here, count);
     }
   }
   if constexpr (WARPS > 1) {
 #pragma unroll
-    for (int c = 0; c < CW; ++c) s_acc[warp][CW * lane + c] = acc[c];
+    for (int c = 0; c < CW; ++c) s_acc[warp][CW * lane + c] = acc[0][c];
     if (lane == 0) {
-      s_max[warp] = M;
-      s_sum[warp] = sum;
+      s_max[warp] = M[0];
+      s_sum[warp] = sum[0];
     }
     __syncthreads();
     if (sub != 0) return;
     for (int o = 1; o < WARPS; ++o) {
       const float m2 = s_max[warp + o];
       if (m2 == -CUDART_INF_F) continue;
-      const float m = fmaxf(M, m2);
-      const float f = exp2f(m2 - m), g = exp2f(M - m);
-      M = m;
-      sum = sum * g + s_sum[warp + o] * f;
+      const float m = fmaxf(M[0], m2);
+      const float f = exp2f(m2 - m), g = exp2f(M[0] - m);
+      M[0] = m;
+      sum[0] = sum[0] * g + s_sum[warp + o] * f;
 #pragma unroll
-      for (int c = 0; c < CW; ++c) acc[c] = acc[c] * g + s_acc[warp + o][CW * lane + c] * f;
+      for (int c = 0; c < CW; ++c) acc[0][c] = acc[0][c] * g + s_acc[warp + o][CW * lane + c] * f;
     }
   }
-  if (skip) return;
-  const bool live = sum > 0.f;
-  const float inv = live ? 1.0f / sum : 0.f;
-  const size_t row = (static_cast<size_t>(b) * p.seq.Hkv + head) * rows + r;
-  const size_t at = row * D + CW * lane;
 #pragma unroll
-  for (int c = 0; c < CW; c += 2) {
-    const float x = acc[c] * inv, y = acc[c + 1] * inv;
-    if (p.o_bf16)
-      *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.o) + at + c) = pack_bf16x2(x, y);
-    else
-      *reinterpret_cast<float2*>(static_cast<float*>(p.o) + at + c) = make_float2(x, y);
+  for (int q = 0; q < RPW; ++q) {
+    if (q >= count) break;
+    const bool live = sum[q] > 0.f;
+    const float inv = live ? 1.0f / sum[q] : 0.f;
+    const size_t row = (static_cast<size_t>(b) * p.seq.Hkv + head) * rows + r0 + q;
+    const size_t at = row * D + CW * lane;
+#pragma unroll
+    for (int c = 0; c < CW; c += 2) {
+      const float x = acc[q][c] * inv, y = acc[q][c + 1] * inv;
+      if (p.o_bf16)
+        *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.o) + at + c) = pack_bf16x2(x, y);
+      else
+        *reinterpret_cast<float2*>(static_cast<float*>(p.o) + at + c) = make_float2(x, y);
+    }
+    if (lane == 0) p.lse[row] = live ? (M[q] + log2f(sum[q])) * kLn2 : -CUDART_INF_F;
   }
-  if (lane == 0) p.lse[row] = live ? (M + log2f(sum)) * kLn2 : -CUDART_INF_F;
 }
 
 template <int D, int MB>
@@ -585,20 +633,22 @@ cudaError_t launch_steps(const PagedArgs& a, const PagedStep& p, int ctas, cudaS
   static std::atomic<unsigned long long> ready{0};
   cudaError_t e = setup_kernel_once(kern, L::kSmemBytes, 0, ready);
   if (e != cudaSuccess) return e;
-  kern<<<ctas, kStepThreads, L::kSmemBytes, stream>>>(a.tm_k, a.tm_v, p);
-  return cudaGetLastError();
+  return launch_overlapped(kern, dim3(ctas), kStepThreads, L::kSmemBytes, stream, a.tm_k, a.tm_v, p);
 }
 
 template <int D>
 cudaError_t launch_combine(const PagedCombine& p, bool tiles, cudaStream_t stream) {
+  constexpr int RPW = 4;
   const long long rows = static_cast<long long>(p.units) * p.part.slot_rows;
+  const long long groups = static_cast<long long>(p.units) * ((p.part.slot_rows + RPW - 1) / RPW);
   if (tiles)
-    paged_combine_kernel<D, 1, true><<<static_cast<unsigned>((rows + 7) / 8), 256, 0, stream>>>(p);
-  else if (rows <= 2048)  // few rows: four warps a row, whose partial results then number the most
-    paged_combine_kernel<D, 4, false><<<static_cast<unsigned>((rows + 1) / 2), 256, 0, stream>>>(p);
-  else
-    paged_combine_kernel<D, 1, false><<<static_cast<unsigned>((rows + 7) / 8), 256, 0, stream>>>(p);
-  return cudaGetLastError();
+    return launch_overlapped(paged_combine_kernel<D, 1, RPW, true>, dim3(static_cast<unsigned>((groups + 7) / 8)), 256,
+                             0, stream, p);
+  if (rows <= 2048)  // few rows: four warps a row, whose partial results then number the most
+    return launch_overlapped(paged_combine_kernel<D, 4, 1, false>, dim3(static_cast<unsigned>((rows + 1) / 2)), 256, 0,
+                             stream, p);
+  return launch_overlapped(paged_combine_kernel<D, 1, RPW, false>, dim3(static_cast<unsigned>((groups + 7) / 8)), 256,
+                           0, stream, p);
 }
 
 // How a call is divided, and where its partial results lie in the workspace
@@ -664,6 +714,7 @@ cudaError_t launch_paged_d(const PagedArgs& a, cudaStream_t stream) {
     PagedTiles p = t;
     p.line_out = uniform;
     p.part = prefix;
+    p.wait_first = 1;
     p.e0 = 0;
     p.entries = static_cast<int>(x.prefix_entries);
     e = launch_tiles(p, a.tm_k, a.tm_v, D, tile_ctas, stream);
@@ -702,6 +753,7 @@ cudaError_t launch_paged_d(const PagedArgs& a, cudaStream_t stream) {
       p.line_out = line;
       p.part = c.part;
       p.direct = c.direct;
+      p.wait_first = !with_prefix || e0 > 0;
       p.box_rows = a.box_rows;
       p.b0 = b0;
       p.causal = a.causal;
@@ -720,6 +772,7 @@ cudaError_t launch_paged_d(const PagedArgs& a, cudaStream_t stream) {
       p.line_out = line;
       p.part = c.part;
       p.direct = c.direct;
+      p.wait_first = !with_prefix || e0 > 0;
       p.e0 = static_cast<int>(e0);
       p.entries = n;
       e = launch_tiles(p, a.tm_k, a.tm_v, D, tile_ctas, stream);

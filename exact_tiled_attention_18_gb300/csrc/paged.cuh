@@ -9,8 +9,8 @@
 namespace fa {
 
 constexpr int kStepRows = 32;          // rows a key head that the step kernel takes
-constexpr int kLineSequences = 1024;   // sequences a launch: the line's table is in shared memory
-constexpr int kLineWords = 1040;       // 4-byte words of the line in the workspace, a multiple of 4
+constexpr int kLineSequences = 512;    // sequences (or row pairs) a launch: the line's table is in shared memory
+constexpr int kLineWords = 528;        // 4-byte words of the line in the workspace, a multiple of 4
 constexpr int kMaxCtas = 512;
 constexpr int kMinSteps = 4;           // key tiles (64 keys) a CTA of the step kernel takes at least
 constexpr int kMinTiles = 2;           // key tiles (128 keys) a CTA of the tile kernel takes at least
@@ -48,6 +48,7 @@ struct PagedStep {
   int* line_out;     // the line's table, for the combine
   PartRef part;
   int direct;        // 1: a piece that is a whole unit's writes o and lse
+  int wait_first;    // 1: wait for the kernels before this one at the start; 0: before the end
   int box_rows;
   int b0;            // first sequence of this launch, for error reports
   int causal;
@@ -72,6 +73,7 @@ struct PagedTiles {
   int direct;
   int pairs;         // row pairs a sequence
   int e0, entries;   // entries of this launch
+  int wait_first;    // as PagedStep's
   int box_rows;
   int causal;
   float scale_log2;

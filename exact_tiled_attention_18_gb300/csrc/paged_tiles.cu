@@ -165,6 +165,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefetch_tensormap(&tm_k);
     prefetch_tensormap(&tm_v);
   }
+  if (p.wait_first) grid_wait();
+  grid_trigger();
   // the line: for the prefix every entry has the tiles of its keys that some
   // sequence reaches
   int reach = 0, total;
@@ -663,6 +665,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
 
+  if (!p.wait_first && threadIdx.x == 0) grid_wait();
   tc_fence_before();
   __syncthreads();
   if (warp == 9) {
@@ -680,8 +683,7 @@ cudaError_t launch_t(const PagedTiles& p, const CUtensorMap& tm_k, const CUtenso
   static std::atomic<unsigned long long> ready{0};
   cudaError_t e = setup_kernel_once(kern, L::kSmemBytes, kLaunchRegs, ready);
   if (e != cudaSuccess) return e;
-  kern<<<ctas, kThreads, L::kSmemBytes, stream>>>(tm_k, tm_v, p);
-  return cudaGetLastError();
+  return launch_overlapped(kern, dim3(ctas), kThreads, L::kSmemBytes, stream, tm_k, tm_v, p);
 }
 
 }  // namespace

@@ -147,6 +147,7 @@ __device__ __forceinline__ void turn(const Lane& l, bool interleaved, float (&lo
 template <int D, bool XBF, bool YBF>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a, const int heads_per_thread) {
   constexpr int LANES = D / 16;
+  grid_trigger();
   const long long item = static_cast<long long>(blockIdx.x) * (kRopeThreads / LANES) + threadIdx.x / LANES;
   if (item >= static_cast<long long>(a.B) * a.N) return;
   const int c = threadIdx.x % LANES;
@@ -187,6 +188,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a, co
 template <int D>
 __global__ void __launch_bounds__(kRopeThreads) append_kernel(const AppendArgs a, const int heads_per_thread) {
   constexpr int LANES = D / 16;
+  grid_trigger();
   const long long item = static_cast<long long>(blockIdx.x) * (kRopeThreads / LANES) + threadIdx.x / LANES;
   if (item >= static_cast<long long>(a.B) * a.N) return;
   const int c = threadIdx.x % LANES;

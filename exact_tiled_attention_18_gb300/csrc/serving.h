@@ -97,7 +97,33 @@ cudaError_t launch_paged(const PagedArgs& a, cudaStream_t stream);
 // Workspace of launch_paged in 4-byte words.
 size_t paged_workspace_floats(int B, int Hkv, int G, int Nq, int d, bool with_prefix);
 
+// Launches a kernel that may start while the one before it in the stream
+// still runs, provided that one has let its dependents go (grid_trigger); it
+// waits for it itself (grid_wait).
+template <typename... Params, typename... Args>
+cudaError_t launch_overlapped(void (*kern)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t stream,
+                              Args... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, static_cast<Params>(args)...);
+}
+
 #if defined(__CUDACC__)
+// The kernel behind this one in the stream may start its CTAs from here on
+// (once every CTA of this grid has said so or ended).
+__device__ __forceinline__ void grid_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// Until the kernels before this one have ended and their writes are visible.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // Records an entry of a block table that names no page (first failure wins).
 __device__ __forceinline__ void record_bad_page(int* status, int site, int block, int page) {
   if (atomicCAS(status, 0, FA_DEV_BAD_PAGE) == 0) {

@@ -94,6 +94,7 @@ STEPS = [
     (70, 2, 1, 1, 64, 16, [(i * 37) % 211 for i in range(70)], None),
     (2, 3, 1, 4, 128, 80, [333, 200], None),
     (1, 8, 8, 1, 128, 64, [9000], None),
+    (600, 2, 1, 1, 64, 16, [(i * 53) % 97 for i in range(600)], None),  # more sequences than a launch takes
 ]
 
 
@@ -121,6 +122,7 @@ CHUNKS = [
     (1, 1, 1, 140, 128, 16, [41000], None),                      # long ranges: the ring goes round
     (2, 2, 1, 700, 128, 64, [3001, 9001], [700, 600]),           # heads of 700 rows: tiles across two heads
     (3, 3, 3, 200, 64, 32, [6001, 12007, 300], None),
+    (530, 1, 1, 40, 64, 16, [40 + (i * 31) % 60 for i in range(530)], None),  # more row pairs than a launch takes
 ]
 
 
@@ -146,6 +148,8 @@ PREFIXES = [
     (130, 2, 2, 1, 128, 64, 256, [257] * 130, None),             # more rows than one tile
     (20, 16, 1, 1, 128, 48, 960, [961 + i for i in range(20)], [1] * 19 + [0]),
     (3, 2, 1, 150, 64, 128, 128, [278, 200, 150], None),         # new tokens inside the prefix
+    (520, 3, 1, 1, 64, 16, 32, [33 + i % 40 for i in range(520)], None),  # groups of rows cross row pairs
+    (515, 1, 1, 35, 64, 16, 64, [99 + i % 50 for i in range(515)], None),
 ]
 
 
