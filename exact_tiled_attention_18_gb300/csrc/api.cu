@@ -452,7 +452,9 @@ fa_status paged_common(const void* q, const void* k_pages, const void* v_pages, 
   a.stall_unit = test_stall_unit();
   a.box_rows = page_size % 64 == 0 ? 64 : (page_size % 32 == 0 ? 32 : 16);
   if (!encode_bf16_map(&a.tm_k, k_pages, num_pages * Hkv, page_size, d, a.box_rows) ||
-      !encode_bf16_map(&a.tm_v, v_pages, num_pages * Hkv, page_size, d, a.box_rows))
+      !encode_bf16_map(&a.tm_v, v_pages, num_pages * Hkv, page_size, d, a.box_rows) ||
+      !encode_bf16_map(&a.tm_k16, k_pages, num_pages * Hkv, page_size, d, 16) ||
+      !encode_bf16_map(&a.tm_v16, v_pages, num_pages * Hkv, page_size, d, 16))
     return FA_ERR_LAUNCH;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (!workspace) {

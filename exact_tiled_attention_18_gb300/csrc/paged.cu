@@ -2,13 +2,15 @@
 // drafted ones of every query head of its group.
 //
 // A step reads the keys and values of every sequence once, for G * Nq rows of
-// queries a key head: 2 G Nq FLOPs per byte, so with up to 32 rows it is bound
-// by HBM as long as the products run on the tensor cores (on the CUDA cores 8
-// heads a group already cost more than the reading).  The products are
-// 16 x 64 x d per 64 keys: a tcgen05 tile would be 128 rows high and its
-// result would have to come back through tensor memory before a row maximum
-// can be taken, so these use warp-wide mma with the fragments in registers,
-// fed by ldmatrix from the swizzled TMA tiles.
+// queries a key head: 2 G Nq FLOPs per byte, so it is bound by HBM as long as
+// the products run on the tensor cores (on the CUDA cores 8 heads a group
+// already cost more than the reading).  A tcgen05 tile would be 128 rows high
+// and its result would have to come back through tensor memory before a row
+// maximum can be taken, so these use warp-wide mma with the fragments in
+// registers, fed by ldmatrix from the swizzled TMA tiles.  Keys and value
+// columns are the 16-high side of each mma, query rows the 8-wide side
+// (S^T = K Q^T, O^T = V^T P^T): up to 8 rows cost half of what they would as
+// rows of a 16-high tile, and the mma rate is what comes next after HBM.
 //
 //   paged_steps_kernel    persistent CTAs of four compute warps and a TMA warp,
 //                         two an SM.  The key tiles (64 keys of one key head)
@@ -49,17 +51,27 @@ constexpr float kLn2 = 0.6931471805599453f;
 
 enum StepSite : int { SITE_STEP_EMPTY = 73, SITE_STEP_FULL = 74 };
 
-template <int D, int MB>
+// CTAs an SM: three with up to 8 rows, whose registers and rings (two tiles of
+// 32 KB at d = 128) leave room for it; two with more (three tiles).  The
+// bytes in flight an SM are the same; a third CTA fills the gaps that the
+// others leave between sequences.
+template <int RB>
+constexpr int step_ctas_per_sm() { return RB <= 1 ? 3 : 2; }
+
+// RB: blocks of 8 query rows.
+template <int D, int RB>
 struct StepLayout {
   static constexpr int kBlock = kStepKeys * 128;        // 64 columns x 64 keys: 128-byte rows, swizzled
   static constexpr int kHalf = (D / 64) * kBlock;       // K (or V) of a tile
   static constexpr int kStage = 2 * kHalf;
-  static constexpr int kStages = D == 128 ? 3 : 6;
-  static constexpr int kPOff = kStages * kStage;        // probabilities: hi then lo, [16 MB rows][64 keys]
-  static constexpr int kPHalf = 16 * MB * 128;
-  static constexpr int kBarOff = kPOff + 2 * kPHalf;    // FULL[s] then EMPTY[s]
-  static constexpr int kMaxOff = kBarOff + 2 * kStages * 8;  // [warps][16 MB] row maxima, then row sums
-  static constexpr int kMiscOff = kMaxOff + 2 * kStepWarps * 16 * MB * 4;
+  static constexpr int kStages = (step_ctas_per_sm<RB>() == 3 ? 2 : 3) * (128 / D);
+  // probabilities: hi then lo, [RB][64 keys][8 rows] bf16, so that eight keys
+  // of a block are 128 contiguous bytes
+  static constexpr int kPOff = kStages * kStage;
+  static constexpr int kPBlock = kStepKeys * 16;
+  static constexpr int kBarOff = kPOff + 2 * RB * kPBlock;   // FULL[s] then EMPTY[s]
+  static constexpr int kMaxOff = kBarOff + 2 * kStages * 8;  // [warps][8 RB] row maxima, then row sums
+  static constexpr int kMiscOff = kMaxOff + 2 * kStepWarps * 8 * RB * 4;
   static constexpr int kLineOff = kMiscOff + 16;        // first tile of every sequence, then lq, then lk
   static constexpr int kSmemBytes = kLineOff + (3 * kLineSequences + 1) * 4 + 1024;
 };
@@ -108,15 +120,16 @@ __device__ __forceinline__ void warps_sync() {
   asm volatile("barrier.cta.sync 1, %0;" ::"n"(32 * kStepWarps) : "memory");
 }
 
-template <int D, int MB>
-__global__ void __launch_bounds__(kStepThreads, 2)
+template <int D, int RB>
+__global__ void __launch_bounds__(kStepThreads, step_ctas_per_sm<RB>())
     paged_steps_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                       const PagedStep p) {
-  using L = StepLayout<D, MB>;
+                       const __grid_constant__ CUtensorMap tm_k16, const __grid_constant__ CUtensorMap tm_v16,
+                       const __grid_constant__ PagedStep p) {
+  using L = StepLayout<D, RB>;
   constexpr int S = L::kStages;
   constexpr int CB = D / 64;       // 64-column blocks of a head
   constexpr int KS = D / 16;       // steps of the score product
-  constexpr int NT = D / 32;       // 8-column tiles of a warp's quarter of the values
+  constexpr int MT = D / 64;       // 16-column tiles of a warp's quarter of the values
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
@@ -137,6 +150,8 @@ __global__ void __launch_bounds__(kStepThreads, 2)
   if (warp == kStepWarps && lane == 0) {
     prefetch_tensormap(&tm_k);
     prefetch_tensormap(&tm_v);
+    prefetch_tensormap(&tm_k16);
+    prefetch_tensormap(&tm_v16);
   }
   if (p.wait_first) grid_wait();
   grid_trigger();
@@ -167,11 +182,6 @@ __global__ void __launch_bounds__(kStepThreads, 2)
     // ------------------------------------------------------------ TMA producer
     // lane i of a tile's loads: operand, 64-column block and box of rows
     const int boxes = kStepKeys / p.box_rows;
-    const int mine = lane / boxes;                 // operand * CB + block
-    const int box = lane - mine * boxes;
-    const bool loads = mine < 2 * CB;
-    const uint32_t offset = static_cast<uint32_t>((mine / CB) * L::kHalf + (mine % CB) * L::kBlock + box * p.box_rows * 128);
-    const CUtensorMap* tm = mine / CB == 0 ? &tm_k : &tm_v;
     int issued = 0;
     bool ok = true;
     // page of box i of a piece; -1 behind the sequence's end
@@ -200,13 +210,20 @@ __global__ void __launch_bounds__(kStepThreads, 2)
         ok = __all_sync(0xffffffffu,
                         wait_bounded(bars + 8 * (S + s), ((issued / S) & 1) ^ 1, wc, SITE_STEP_EMPTY, unit));
         if (!ok) break;
-        const int page = __shfl_sync(0xffffffffu, cur, (t * boxes + box) % 32);
+        // a sequence's last tile comes in boxes of 16 rows, so that at most 15
+        // rows behind its last key are read
+        const bool tail = first + (t + 1) * kStepKeys > lk;
+        const int rows_box = tail ? 16 : p.box_rows;
+        const int per_block = kStepKeys / rows_box;      // boxes a 64-column block
+        const int mine = lane / per_block;               // operand * CB + block
+        const int row = (lane - mine * per_block) * rows_box;
+        const int page = __shfl_sync(0xffffffffu, cur, (t * boxes + row / p.box_rows) % 32);
         if (unit == p.stall_unit && issued == 0) continue;  // testing hook: leave this tile unloaded
         const uint32_t full = bars + 8 * s;
         if (lane == 0) mbar_arrive_expect_tx(full, L::kStage);
         __syncwarp();
-        if (loads) {
-          const int key = first + t * kStepKeys + box * p.box_rows;
+        if (mine < 2 * CB) {
+          const int key = first + t * kStepKeys + row;
           // rows of no page: a coordinate past the map, which reads zeros
           int outer = p.table.num_pages * p.seq.Hkv;
           if (key < lk) {
@@ -215,7 +232,10 @@ __global__ void __launch_bounds__(kStepThreads, 2)
             else
               record_bad_page(p.status, SITE_PAGE_READ, p.b0 + w.e, page);
           }
-          tma_load_3d(sbase + s * L::kStage + offset, tm, full, 64 * (mine % CB), key % p.table.page_size, outer);
+          const int block = mine % CB;
+          const CUtensorMap* tm = mine < CB ? (tail ? &tm_k16 : &tm_k) : (tail ? &tm_v16 : &tm_v);
+          tma_load_3d(sbase + s * L::kStage + (mine / CB) * L::kHalf + block * L::kBlock + row * 128, tm, full,
+                      64 * block, key % p.table.page_size, outer);
         }
         __syncwarp();
       }
@@ -238,233 +258,230 @@ __global__ void __launch_bounds__(kStepThreads, 2)
   }
 
   // ---------------------------------------------------------------- compute
-  float* maxima = reinterpret_cast<float*>(smem + L::kMaxOff);   // [warp][16 MB]
-  float* sums = maxima + kStepWarps * 16 * MB;
-  const int qr = lane >> 2;        // fragment row (and row + 8)
-  const int qc = (lane & 3) * 2;   // fragment column pair
+  float* maxima = reinterpret_cast<float*>(smem + L::kMaxOff);   // [warp][8 RB]
+  float* sums = maxima + kStepWarps * 8 * RB;
+  const int fr = lane >> 2;        // fragment line: key (or value column) fr and fr + 8
+  const int fc = (lane & 3) * 2;   // fragment columns: query rows fc, fc + 1 of a block
   const int rows = p.seq.G * p.seq.Nq;
-  // ldmatrix lane addresses: K (two 8-key tiles x two 8-column halves), P and
-  // V (16 keys x two 8-column tiles)
-  const int k_row = 16 * warp + ((lane >> 4) << 3) + (lane & 7);
-  const int k_half = (lane >> 3) & 1;
-  const int p_row = (((lane >> 3) & 1) << 3) + (lane & 7);
-  const int p_half = lane >> 4;
+  // ldmatrix lane addresses: K (16 keys x 16 columns), V and P transposed
+  const int k_row = 16 * warp + (lane & 15), k_half = lane >> 4;
+  const int v_row = ((lane >> 4) << 3) + (lane & 7), v_half = (lane >> 3) & 1;
   const int v_col = warp * (D / 4);  // first value column of this warp
-  const uint32_t p_hi = sbase + L::kPOff, p_lo = p_hi + L::kPHalf;
-  uint32_t qf[MB][KS][4];
+  const uint32_t p_hi = sbase + L::kPOff, p_lo = p_hi + RB * L::kPBlock;
+  uint32_t qf[RB][KS][2];
   // the rows of a piece as fragments (rows of the group lie together)
-  auto load_q = [&](const Walk& x, auto& f) {
-    const uint16_t* base = p.q + (static_cast<size_t>(x.e) * p.seq.Hkv + x.head) * rows * D + qc;
+  auto load_q = [&](const Walk& x) {
+    const uint16_t* base = p.q + (static_cast<size_t>(x.e) * p.seq.Hkv + x.head) * rows * D + fc;
 #pragma unroll
-    for (int m = 0; m < MB; ++m) {
+    for (int m = 0; m < RB; ++m) {
+      const int r = 8 * m + fr;
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int r = 16 * m + 8 * e + qr;
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-          f[m][ks][e] = r < rows ? __ldg(reinterpret_cast<const uint32_t*>(base + r * D + 16 * ks)) : 0u;
-          f[m][ks][2 + e] = r < rows ? __ldg(reinterpret_cast<const uint32_t*>(base + r * D + 16 * ks + 8)) : 0u;
-        }
+      for (int ks = 0; ks < KS; ++ks) {
+        qf[m][ks][0] = r < rows ? __ldg(reinterpret_cast<const uint32_t*>(base + r * D + 16 * ks)) : 0u;
+        qf[m][ks][1] = r < rows ? __ldg(reinterpret_cast<const uint32_t*>(base + r * D + 16 * ks + 8)) : 0u;
       }
     }
   };
-  if (more) load_q(w, qf);
+  if (more) load_q(w);
   int done = 0;
   bool ok = true;
   while (more && ok) {
     const int lq = len_q[w.e], lk = len_k[w.e];
-    int kend[MB][2];
+    int kend[RB][2];               // last visible key + 1 of rows fc, fc + 1
+    float m_ref[RB][2], l[RB][2], acc[RB][MT][4];
 #pragma unroll
-    for (int m = 0; m < MB; ++m) {
+    for (int m = 0; m < RB; ++m) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int r = 16 * m + 8 * e + qr;
+        const int r = 8 * m + fc + e;
         const int i = r % p.seq.Nq;
         kend[m][e] = r < rows && i < lq ? (p.causal ? min(i + lk - lq + 1, lk) : lk) : 0;
-      }
-    }
-    Walk after = w;
-    int after_at = at;
-    const bool another = walk_next(after, starts, p.seq.Hkv, after_at, stop);
-    float m_ref[MB][2], l[MB][2], acc[MB][NT][4];
-#pragma unroll
-    for (int m = 0; m < MB; ++m) {
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
         m_ref[m][e] = -CUDART_INF_F;
         l[m][e] = 0.f;
       }
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+      for (int n = 0; n < MT; ++n)
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[m][n][e] = 0.f;
     }
+    Walk after = w;
+    int after_at = at;
+    const bool another = walk_next(after, starts, p.seq.Hkv, after_at, stop);
     for (int t = w.tile; t < w.end; ++t, ++done) {
       const int s = done % S;
       const bool full = wait_bounded(bars + 8 * s, (done / S) & 1, wc, SITE_STEP_FULL, unit);
       const uint32_t kb = sbase + s * L::kStage;
       const uint32_t vb = kb + L::kHalf;
       const int key0 = p.seq.prefix_len + t * kStepKeys;
-      // scores of this warp's 16 keys: fragment n holds keys 8 n + qc, + 1
-      float sc[MB][2][4];
+      // scores of this warp's 16 keys: keys fr (elements 0, 1) and fr + 8 (2, 3)
+      float sc[RB][4];
 #pragma unroll
-      for (int m = 0; m < MB; ++m)
+      for (int m = 0; m < RB; ++m)
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) sc[m][n][e] = 0.f;
+        for (int e = 0; e < 4; ++e) sc[m][e] = 0.f;
       if (__all_sync(0xffffffffu, full)) {
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
           uint32_t kf[4];
           ldmatrix4(kf, kb + (ks >> 2) * L::kBlock + sw128(k_row, 2 * (ks & 3) + k_half));
 #pragma unroll
-          for (int m = 0; m < MB; ++m) {
-            mma_bf16(sc[m][0], qf[m][ks], kf[0], kf[1]);
-            mma_bf16(sc[m][1], qf[m][ks], kf[2], kf[3]);
-          }
+          for (int m = 0; m < RB; ++m) mma_bf16(sc[m], kf, qf[m][ks][0], qf[m][ks][1]);
         }
         if (key0 + kStepKeys > lk) {
           // rows behind the last key may hold anything: their weights are 0,
           // so their values must be finite
-          for (int i = lane; i < 16 * 8 * CB; i += 32) {
-            const int r = 16 * warp + (i & 15);
-            if (key0 + r >= lk) st_shared_v4(vb + (i >> 7) * L::kBlock + sw128(r, (i >> 4) & 7), 0u, 0u, 0u, 0u);
+          // (whole boxes behind it were read as zeros)
+          if ((lk - key0) / 16 == warp) {
+            for (int i = lane; i < 16 * 8 * CB; i += 32) {
+              const int r = 16 * warp + (i & 15);
+              if (key0 + r >= lk) st_shared_v4(vb + (i >> 7) * L::kBlock + sw128(r, (i >> 4) & 7), 0u, 0u, 0u, 0u);
+            }
           }
           fence_proxy_async_smem();  // before the slot's next TMA load
         }
       }
-      float mx[MB][2];
+      const int j = key0 + 16 * warp + fr;
 #pragma unroll
-      for (int m = 0; m < MB; ++m) {
+      for (int m = 0; m < RB; ++m) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const int j = key0 + 16 * warp + qc;
-#pragma unroll
-          for (int n = 0; n < 2; ++n) {
-            if (j + 8 * n >= kend[m][e]) sc[m][n][2 * e] = -CUDART_INF_F;
-            if (j + 8 * n + 1 >= kend[m][e]) sc[m][n][2 * e + 1] = -CUDART_INF_F;
-          }
-          float x = fmaxf(fmaxf(sc[m][0][2 * e], sc[m][0][2 * e + 1]), fmaxf(sc[m][1][2 * e], sc[m][1][2 * e + 1]));
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-          mx[m][e] = x;
-          if ((lane & 3) == 0) maxima[warp * 16 * MB + 16 * m + 8 * e + qr] = x;
+          if (j >= kend[m][e]) sc[m][e] = -CUDART_INF_F;
+          if (j + 8 >= kend[m][e]) sc[m][2 + e] = -CUDART_INF_F;
+          float x = fmaxf(sc[m][e], sc[m][2 + e]);
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+          if (lane < 4) maxima[warp * 8 * RB + 8 * m + fc + e] = x;
         }
       }
       ok = warps_agree(full);
       if (!ok) break;
 #pragma unroll
-      for (int m = 0; m < MB; ++m) {
+      for (int m = 0; m < RB; ++m) {
+        float2 x = *reinterpret_cast<const float2*>(maxima + 8 * m + fc);
+#pragma unroll
+        for (int o = 1; o < kStepWarps; ++o) {
+          const float2 y = *reinterpret_cast<const float2*>(maxima + o * 8 * RB + 8 * m + fc);
+          x.x = fmaxf(x.x, y.x);
+          x.y = fmaxf(x.y, y.y);
+        }
+        const float top[2] = {x.x * p.scale_log2, x.y * p.scale_log2};
+        float pr[4];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const int r = 16 * m + 8 * e + qr;
-          float x = mx[m][e];
-#pragma unroll
-          for (int o = 0; o < kStepWarps; ++o) x = fmaxf(x, maxima[o * 16 * MB + r]);
-          x *= p.scale_log2;
-          if (x > m_ref[m][e] + kTau) {  // the same in every warp
-            const float alpha = ex2_approx(m_ref[m][e] - x);  // 0 on the first visible key
-            m_ref[m][e] = x;
+          if (top[e] > m_ref[m][e] + kTau) {  // the same in every warp
+            const float alpha = ex2_approx(m_ref[m][e] - top[e]);  // 0 on the first visible key
+            m_ref[m][e] = top[e];
             l[m][e] *= alpha;
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              acc[m][n][2 * e] *= alpha;
-              acc[m][n][2 * e + 1] *= alpha;
+            for (int n = 0; n < MT; ++n) {
+              acc[m][n][e] *= alpha;
+              acc[m][n][2 + e] *= alpha;
             }
           }
           const float mu = m_ref[m][e] == -CUDART_INF_F ? 0.f : m_ref[m][e];
+          pr[e] = ex2_approx(fmaf(sc[m][e], p.scale_log2, -mu));
+          pr[2 + e] = ex2_approx(fmaf(sc[m][2 + e], p.scale_log2, -mu));
+          l[m][e] += pr[e] + pr[2 + e];
+        }
 #pragma unroll
-          for (int n = 0; n < 2; ++n) {
-            const float a = ex2_approx(fmaf(sc[m][n][2 * e], p.scale_log2, -mu));
-            const float b = ex2_approx(fmaf(sc[m][n][2 * e + 1], p.scale_log2, -mu));
-            l[m][e] += a + b;
-            const uint32_t hi = pack_bf16x2(a, b);
-            const uint32_t lo = pack_bf16x2(a - __uint_as_float(hi << 16), b - __uint_as_float(hi & 0xFFFF0000u));
-            const uint32_t off = sw128(r, 2 * warp + n) + (lane & 3) * 4;
-            st_shared_u32(p_hi + off, hi);
-            st_shared_u32(p_lo + off, lo);
-          }
+        for (int h = 0; h < 2; ++h) {  // keys fr and fr + 8
+          const uint32_t hi = pack_bf16x2(pr[2 * h], pr[2 * h + 1]);
+          const uint32_t lo = pack_bf16x2(pr[2 * h] - __uint_as_float(hi << 16),
+                                          pr[2 * h + 1] - __uint_as_float(hi & 0xFFFF0000u));
+          const uint32_t off = m * L::kPBlock + (16 * warp + 8 * h + fr) * 16 + fc * 2;
+          st_shared_u32(p_hi + off, hi);
+          st_shared_u32(p_lo + off, lo);
         }
       }
       warps_sync();
-      // O += P V: all 64 keys, this warp's quarter of the columns
+      // O^T += V^T P^T: all 64 keys, this warp's quarter of the columns
 #pragma unroll
-      for (int kk = 0; kk < kStepKeys / 16; ++kk) {
-        uint32_t vf[NT / 2][4];
+      for (int kk = 0; kk < kStepKeys / 16; kk += 2) {
+        uint32_t vf[2][MT][4];
 #pragma unroll
-        for (int n = 0; n < NT / 2; ++n) {
-          const int chunk = v_col / 8 + 2 * n + p_half;  // 16-byte chunk of the head's row
-          ldmatrix4_t(vf[n], vb + (chunk >> 3) * L::kBlock + sw128(16 * kk + p_row, chunk & 7));
-        }
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int m = 0; m < MB; ++m) {
-          uint32_t ph[4], pl[4];
-          const uint32_t off = sw128(16 * m + p_row, 2 * kk + p_half);
-          ldmatrix4(ph, p_hi + off);
-          ldmatrix4(pl, p_lo + off);
-#pragma unroll
-          for (int n = 0; n < NT / 2; ++n) {
-            mma_bf16(acc[m][2 * n], ph, vf[n][0], vf[n][1]);
-            mma_bf16(acc[m][2 * n + 1], ph, vf[n][2], vf[n][3]);
-            mma_bf16(acc[m][2 * n], pl, vf[n][0], vf[n][1]);
-            mma_bf16(acc[m][2 * n + 1], pl, vf[n][2], vf[n][3]);
+          for (int n = 0; n < MT; ++n) {
+            const int chunk = v_col / 8 + 2 * n + v_half;  // 16-byte chunk of the head's row
+            ldmatrix4_t(vf[h][n], vb + (chunk >> 3) * L::kBlock + sw128(16 * (kk + h) + v_row, chunk & 7));
           }
+#pragma unroll
+        for (int m = 0; m < RB; ++m) {
+          uint32_t ph[4], pl[4];  // keys 16 kk .. + 32, eight a matrix
+          const uint32_t off = m * L::kPBlock + (16 * kk + lane) * 16;
+          ldmatrix4_t(ph, p_hi + off);
+          ldmatrix4_t(pl, p_lo + off);
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int n = 0; n < MT; ++n) {
+              mma_bf16(acc[m][n], vf[h][n], ph[2 * h], ph[2 * h + 1]);
+              mma_bf16(acc[m][n], vf[h][n], pl[2 * h], pl[2 * h + 1]);
+            }
         }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(bars + 8 * (S + s));
     }
     if (!ok) break;
-    if (another) load_q(after, qf);  // in flight while this piece's results are written
+    if (another) load_q(after);  // in flight while this piece's results are written
     const size_t row0 = (static_cast<size_t>(w.e) * p.seq.Hkv + w.head) * rows;
     // the row sums of all warps
 #pragma unroll
-    for (int m = 0; m < MB; ++m) {
+    for (int m = 0; m < RB; ++m) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         float x = l[m][e];
-        x += __shfl_xor_sync(0xffffffffu, x, 1);
-        x += __shfl_xor_sync(0xffffffffu, x, 2);
-        if ((lane & 3) == 0) sums[warp * 16 * MB + 16 * m + 8 * e + qr] = x;
+        x += __shfl_xor_sync(0xffffffffu, x, 4);
+        x += __shfl_xor_sync(0xffffffffu, x, 8);
+        x += __shfl_xor_sync(0xffffffffu, x, 16);
+        if (lane < 4) sums[warp * 8 * RB + 8 * m + fc + e] = x;
       }
     }
     warps_sync();
     const bool whole = p.direct && w.tile == 0 && w.end == w.tiles;
     const size_t slot = static_cast<size_t>(w.e) * p.seq.Hkv + w.head + blockIdx.x;
+    const int odd = fr & 1;
 #pragma unroll
-    for (int m = 0; m < MB; ++m) {
+    for (int m = 0; m < RB; ++m) {
+      float scale[2], lse2[2];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int r = 16 * m + 8 * e + qr;
-        if (r < rows) {
-          float sum = 0.f;
+        float sum = 0.f;
 #pragma unroll
-          for (int o = 0; o < kStepWarps; ++o) sum += sums[o * 16 * MB + r];
-          const bool live = sum > 0.f;
-          const float inv = live ? 1.0f / sum : 0.f;
-          const float lse2 = live ? m_ref[m][e] + log2f(sum) : -CUDART_INF_F;
-          const int col = v_col + qc;
-          if (whole) {
-            const size_t at_o = (row0 + r) * D + col;
+        for (int o = 0; o < kStepWarps; ++o) sum += sums[o * 8 * RB + 8 * m + fc + e];
+        scale[e] = sum > 0.f ? 1.0f / sum : 0.f;
+        lse2[e] = sum > 0.f ? m_ref[m][e] + log2f(sum) : -CUDART_INF_F;
+      }
+      // neighbours in the column exchange rows: a lane then holds two adjacent
+      // columns of row fc (even columns' lanes) or fc + 1 (odd ones')
+      const int r = 8 * m + fc + odd;
+      float* dst_p = p.part.o + (slot * rows + r) * D;
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              const float a = live ? acc[m][n][2 * e] * inv : 0.f, b = live ? acc[m][n][2 * e + 1] * inv : 0.f;
-              if (p.o_bf16)
-                *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.o) + at_o + 8 * n) = pack_bf16x2(a, b);
-              else
-                *reinterpret_cast<float2*>(static_cast<float*>(p.o) + at_o + 8 * n) = make_float2(a, b);
-            }
-            if (warp == 0 && (lane & 3) == 0) p.lse[row0 + r] = live ? lse2 * kLn2 : -CUDART_INF_F;
-          } else {
-            float* dst = p.part.o + (slot * rows + r) * D + col;
+      for (int n = 0; n < MT; ++n) {
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-              *reinterpret_cast<float2*>(dst + 8 * n) =
-                  live ? make_float2(acc[m][n][2 * e] * inv, acc[m][n][2 * e + 1] * inv) : make_float2(0.f, 0.f);
-            if (warp == 0 && (lane & 3) == 0) p.part.lse[slot * rows + r] = lse2;
+        for (int h = 0; h < 2; ++h) {
+          const float a = acc[m][n][2 * h] * scale[0], b = acc[m][n][2 * h + 1] * scale[1];
+          const float got = __shfl_xor_sync(0xffffffffu, odd ? a : b, 4);
+          const float x = odd ? got : a, y = odd ? b : got;
+          const int col = v_col + 16 * n + 8 * h + (fr & ~1);
+          if (r < rows) {
+            if (!whole)
+              *reinterpret_cast<float2*>(dst_p + col) = make_float2(x, y);
+            else if (p.o_bf16)
+              *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.o) + (row0 + r) * D + col) = pack_bf16x2(x, y);
+            else
+              *reinterpret_cast<float2*>(static_cast<float*>(p.o) + (row0 + r) * D + col) = make_float2(x, y);
           }
         }
+      }
+      if (warp == 0 && fr < 2 && r < rows) {
+        const float v = odd ? lse2[1] : lse2[0];
+        if (whole)
+          p.lse[row0 + r] = v == -CUDART_INF_F ? v : v * kLn2;
+        else
+          p.part.lse[slot * rows + r] = v;
       }
     }
     w = after;
@@ -626,14 +643,14 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const __grid_constan
   }
 }
 
-template <int D, int MB>
+template <int D, int RB>
 cudaError_t launch_steps(const PagedArgs& a, const PagedStep& p, int ctas, cudaStream_t stream) {
-  using L = StepLayout<D, MB>;
-  auto kern = paged_steps_kernel<D, MB>;
+  using L = StepLayout<D, RB>;
+  auto kern = paged_steps_kernel<D, RB>;
   static std::atomic<unsigned long long> ready{0};
   cudaError_t e = setup_kernel_once(kern, L::kSmemBytes, 0, ready);
   if (e != cudaSuccess) return e;
-  return launch_overlapped(kern, dim3(ctas), kStepThreads, L::kSmemBytes, stream, a.tm_k, a.tm_v, p);
+  return launch_overlapped(kern, dim3(ctas), kStepThreads, L::kSmemBytes, stream, a.tm_k, a.tm_v, a.tm_k16, a.tm_v16, p);
 }
 
 template <int D>
@@ -644,8 +661,8 @@ cudaError_t launch_combine(const PagedCombine& p, bool tiles, cudaStream_t strea
   if (tiles)
     return launch_overlapped(paged_combine_kernel<D, 1, RPW, true>, dim3(static_cast<unsigned>((groups + 7) / 8)), 256,
                              0, stream, p);
-  if (rows <= 2048)  // few rows: four warps a row, whose partial results then number the most
-    return launch_overlapped(paged_combine_kernel<D, 4, 1, false>, dim3(static_cast<unsigned>((rows + 1) / 2)), 256, 0,
+  if (rows <= 2048)  // few rows: eight warps a row, whose partial results then number the most
+    return launch_overlapped(paged_combine_kernel<D, 8, 1, false>, dim3(static_cast<unsigned>(rows)), 256, 0,
                              stream, p);
   return launch_overlapped(paged_combine_kernel<D, 1, RPW, false>, dim3(static_cast<unsigned>((groups + 7) / 8)), 256,
                            0, stream, p);
@@ -685,7 +702,8 @@ cudaError_t launch_paged_d(const PagedArgs& a, cudaStream_t stream) {
   const int G = a.Hq / a.Hkv;
   const bool with_prefix = a.prefix_len > 0;
   const Plan x = make_plan(a.B, a.Hkv, G, a.Nq, D, with_prefix);
-  const int step_ctas = 2 * a.sms < kMaxCtas ? 2 * a.sms : kMaxCtas;
+  const int per_sm = x.rows <= 8 ? step_ctas_per_sm<1>() : step_ctas_per_sm<4>();
+  const int step_ctas = per_sm * a.sms < kMaxCtas ? per_sm * a.sms : kMaxCtas;
   const int tile_ctas = a.sms < kMaxTileCtas ? a.sms : kMaxTileCtas;
   int* line = reinterpret_cast<int*>(a.part);
   int* uniform = line + kLineWords;
@@ -761,7 +779,10 @@ cudaError_t launch_paged_d(const PagedArgs& a, cudaStream_t stream) {
       p.status = a.status;
       p.wait_limit_ns = a.wait_limit_ns;
       p.stall_unit = a.stall_unit;
-      e = x.rows <= 16 ? launch_steps<D, 1>(a, p, step_ctas, stream) : launch_steps<D, 2>(a, p, step_ctas, stream);
+      e = x.rows <= 8    ? launch_steps<D, 1>(a, p, step_ctas, stream)
+          : x.rows <= 16 ? launch_steps<D, 2>(a, p, step_ctas, stream)
+          : x.rows <= 24 ? launch_steps<D, 3>(a, p, step_ctas, stream)
+                         : launch_steps<D, 4>(a, p, step_ctas, stream);
       c.seq = p.seq;
       c.b0 = b0;
       c.o = p.o;

@@ -9,10 +9,10 @@
 namespace fa {
 
 constexpr int kStepRows = 32;          // rows a key head that the step kernel takes
-constexpr int kLineSequences = 512;    // sequences (or row pairs) a launch: the line's table is in shared memory
-constexpr int kLineWords = 528;        // 4-byte words of the line in the workspace, a multiple of 4
+constexpr int kLineSequences = 256;    // sequences (or row pairs) a launch: the line's table is in shared memory
+constexpr int kLineWords = 272;        // 4-byte words of the line in the workspace, a multiple of 4
 constexpr int kMaxCtas = 512;
-constexpr int kMinSteps = 4;           // key tiles (64 keys) a CTA of the step kernel takes at least
+constexpr int kMinSteps = 1;           // key tiles (64 keys) a CTA of the step kernel takes at least
 constexpr int kMinTiles = 2;           // key tiles (128 keys) a CTA of the tile kernel takes at least
 constexpr int kMaxTileCtas = 256;
 constexpr int kPairRows = 256;         // query rows a unit of the tile kernel: two 128-row tiles

@@ -70,6 +70,7 @@ struct AppendArgs {
 
 struct PagedArgs {
   CUtensorMap tm_k, tm_v;     // 3-D maps over [num_pages * Hkv][page_size][d] bf16, boxes of 64 columns x box_rows
+  CUtensorMap tm_k16, tm_v16; // the same, boxes of 16 rows
   const uint16_t *q;          // [B][Hq][Nq][d]
   const uint16_t *k_pages, *v_pages;
   PageTable table;
