@@ -490,31 +490,46 @@ __global__ void __launch_bounds__(kStepThreads, step_ctas_per_sm<RB>())
   }
 }
 
-// Where row `in` of unit (entry, head) has its partial results.
+// Where a unit has its partial results.
 struct Pieces {
   int n;              // pieces
   int c0;             // first CTA
-  long long unit;
+  long long slot;     // slot of a piece of CTA 0
   bool first_whole;   // the first piece starts its CTA's range
 };
 
-__device__ __forceinline__ Pieces pieces_of(const PartRef& r, int entry, int entries, int head, int Hkv) {
+// `tile`: the unit's first tile on the line; nt: its tiles; total: the line's.
+__device__ __forceinline__ Pieces pieces_on_line(const PartRef& r, int unit, int tile, int nt, int total) {
   Pieces x;
-  const int t0 = r.line ? r.line[entry] : entry * *r.uniform;
-  const int nt = r.line ? r.line[entry + 1] - t0 : *r.uniform;
-  const int total = (r.line ? r.line[entries] : entries * *r.uniform) * Hkv;
   const int per = tiles_per_cta(total, r.ctas, r.min_tiles);
-  const int from = t0 * Hkv + head * nt;
-  x.c0 = from / per;
-  x.n = nt ? (from + nt - 1) / per - x.c0 + 1 : 0;
-  x.unit = static_cast<long long>(entry) * Hkv + head;
-  x.first_whole = from == x.c0 * per;
+  x.c0 = tile / per;
+  x.n = nt ? (tile + nt - 1) / per - x.c0 + 1 : 0;
+  x.slot = unit;
+  x.first_whole = tile == x.c0 * per;
   return x;
 }
 
+// Unit (entry, head) of the step kernel.
+__device__ __forceinline__ Pieces step_pieces(const PartRef& r, int entry, int entries, int head, int Hkv) {
+  const int t0 = r.line[entry], nt = r.line[entry + 1] - t0;
+  return pieces_on_line(r, entry * Hkv + head, t0 * Hkv + head * nt, nt, r.line[entries] * Hkv);
+}
+
+// Unit u of the tile kernel.
+__device__ __forceinline__ Pieces tile_pieces(const PartRef& r, int u) {
+  if (u >= r.cut) return Pieces{1, 0, u + r.ctas, true};
+  return pieces_on_line(r, u, r.line[u], r.line[u + 1] - r.line[u], r.line[r.cut]);
+}
+
+// The tile kernel's unit of (sequence, head) bh and row pair `pair`.
+__device__ __forceinline__ int tile_unit(const PartRef& r, int bh, int pair) {
+  const int g = bh / r.group;
+  const int hs = min(r.group, r.heads - g * r.group);
+  return g * r.group * r.pairs + (r.pairs - 1 - pair) * hs + bh - g * r.group;
+}
+
 __device__ __forceinline__ long long piece_row(const PartRef& r, const Pieces& x, int k, int in) {
-  const long long slot =
-      r.two_a_cta ? 2LL * (x.c0 + k) + (k > 0 || x.first_whole ? 0 : 1) : x.unit + x.c0 + k;
+  const long long slot = r.two_a_cta ? 2LL * (x.c0 + k) + (k > 0 || x.first_whole ? 0 : 1) : x.slot + x.c0 + k;
   return slot * r.slot_rows + in;
 }
 
@@ -537,16 +552,26 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const __grid_constan
   const long long item = static_cast<long long>(blockIdx.x) * (8 / WARPS) + warp / WARPS;
   bool in = item < static_cast<long long>(p.units) * groups;
   const int unit = in ? static_cast<int>(item / groups) : 0;
-  const int row_in = in ? static_cast<int>(item - static_cast<long long>(unit) * groups) * RPW : 0;
-  const int entry = unit / p.seq.Hkv, head = unit - entry * p.seq.Hkv;
-  int b = entry, r0 = row_in;
+  const int row_in = in ? static_cast<int>(item % groups) * RPW : 0;
+  int b, head, r0;
   if constexpr (TILES) {
-    b = (p.e0 + entry) / p.pairs;
-    r0 = (p.e0 + entry - b * p.pairs) * kPairRows + row_in;
+    const int g = unit / (p.part.group * p.part.pairs);
+    const int i = unit - g * p.part.group * p.part.pairs;
+    const int hs = min(p.part.group, p.part.heads - g * p.part.group);
+    const int level = i / hs;
+    const int bh = g * p.part.group + i - level * hs;
+    b = bh / p.seq.Hkv;
+    head = bh - b * p.seq.Hkv;
+    r0 = (p.part.pairs - 1 - level) * kPairRows + row_in;
     in = in && r0 < rows;
+  } else {
+    b = unit / p.seq.Hkv;
+    head = unit - b * p.seq.Hkv;
+    r0 = row_in;
   }
   grid_wait();
-  const Pieces own = pieces_of(p.part, entry, p.units / p.seq.Hkv, head, p.seq.Hkv);
+  const Pieces own =
+      TILES ? tile_pieces(p.part, unit) : step_pieces(p.part, b, p.part.units / p.seq.Hkv, head, p.seq.Hkv);
   const bool skip = !in || (p.direct && own.n == 1);  // written by the only CTA that had it
   const int count = skip ? 0 : min(RPW, (TILES ? min(rows - r0, slot_rows - row_in) : slot_rows - row_in));
   float M[RPW], sum[RPW], acc[RPW][CW];
@@ -599,9 +624,8 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const __grid_constan
       // the rows may cross from one row pair of the prefix into the next
       const int e = static_cast<int>(all / kPairRows), in_pair = static_cast<int>(all % kPairRows);
       const int here = min(count, kPairRows - in_pair);
-      gather(p.prefix, pieces_of(p.prefix, e, p.prefix_entries, head, p.seq.Hkv), in_pair, 0, here);
-      if (here < count)
-        gather(p.prefix, pieces_of(p.prefix, e + 1, p.prefix_entries, head, p.seq.Hkv), -here, here, count);
+      gather(p.prefix, tile_pieces(p.prefix, tile_unit(p.prefix, head, e)), in_pair, 0, here);
+      if (here < count) gather(p.prefix, tile_pieces(p.prefix, tile_unit(p.prefix, head, e + 1)), -here, here, count);
     }
   }
   if constexpr (WARPS > 1) {
@@ -656,8 +680,9 @@ cudaError_t launch_steps(const PagedArgs& a, const PagedStep& p, int ctas, cudaS
 template <int D>
 cudaError_t launch_combine(const PagedCombine& p, bool tiles, cudaStream_t stream) {
   constexpr int RPW = 4;
-  const long long rows = static_cast<long long>(p.units) * p.part.slot_rows;
-  const long long groups = static_cast<long long>(p.units) * ((p.part.slot_rows + RPW - 1) / RPW);
+  const long long units = p.units;
+  const long long rows = units * p.part.slot_rows;
+  const long long groups = units * ((p.part.slot_rows + RPW - 1) / RPW);
   if (tiles)
     return launch_overlapped(paged_combine_kernel<D, 1, RPW, true>, dim3(static_cast<unsigned>((groups + 7) / 8)), 256,
                              0, stream, p);
@@ -673,8 +698,8 @@ cudaError_t launch_combine(const PagedCombine& p, bool tiles, cudaStream_t strea
 struct Plan {
   int rows, pairs;            // rows a key head of a sequence, and its row pairs
   bool steps;                 // the sequences' own keys: the step kernel, else the tile kernel
-  int chunk;                  // sequences (steps) or entries (tiles) a launch
-  long long prefix_entries;   // row pairs of all sequences' rows
+  int chunk;                  // sequences a launch of the step kernel
+  int prefix_pairs;           // row pairs of all sequences' rows
   size_t own_slots, prefix_slots;
   size_t own, prefix, words;
 };
@@ -684,17 +709,28 @@ Plan make_plan(int B, int Hkv, int G, int Nq, int d, bool with_prefix) {
   x.rows = G * Nq;
   x.pairs = (x.rows + kPairRows - 1) / kPairRows;
   x.steps = x.rows <= kStepRows;
-  const long long entries = x.steps ? B : static_cast<long long>(B) * x.pairs;
-  x.chunk = static_cast<int>(entries < kLineSequences ? entries : kLineSequences);
-  const size_t units = static_cast<size_t>(x.chunk) * Hkv;
-  x.own_slots = x.steps ? units + kMaxCtas : (with_prefix ? units + kMaxTileCtas : 2 * kMaxTileCtas);
+  x.chunk = B < kLineSequences ? B : kLineSequences;
+  if (x.steps)
+    x.own_slots = static_cast<size_t>(x.chunk) * Hkv + kMaxCtas;
+  else
+    x.own_slots = with_prefix ? static_cast<size_t>(B) * Hkv * x.pairs + kMaxTileCtas : 2 * kMaxTileCtas;
   const size_t own_words = x.own_slots * (x.steps ? x.rows : kPairRows) * (d + 1);
-  x.prefix_entries = (static_cast<long long>(B) * x.rows + kPairRows - 1) / kPairRows;
-  x.prefix_slots = with_prefix ? static_cast<size_t>(x.prefix_entries) * Hkv + kMaxTileCtas : 0;
-  x.own = 2 * kLineWords;     // the line's table, the prefix's word
+  x.prefix_pairs = static_cast<int>((static_cast<long long>(B) * x.rows + kPairRows - 1) / kPairRows);
+  x.prefix_slots = with_prefix ? static_cast<size_t>(x.prefix_pairs) * Hkv + kMaxTileCtas : 0;
+  x.own = 2 * kLineWords;     // the lines' tables
   x.prefix = x.own + (own_words + 3) / 4 * 4;
   x.words = x.prefix + x.prefix_slots * kPairRows * (d + 1);
   return x;
+}
+
+// Heads whose units are dealt out together: as many as keep their keys and
+// values (of at most `keys` keys a head) within 32 MB of L2, and at least one
+// round's.
+int head_group(long long heads, int pairs, long long keys, int d, int ctas) {
+  long long g = (32LL << 20) / (keys * d * 4);
+  const long long round = (ctas + pairs - 1) / pairs;
+  if (g < round) g = round;
+  return static_cast<int>(g > heads ? heads : g);
 }
 
 template <int D>
@@ -706,101 +742,101 @@ cudaError_t launch_paged_d(const PagedArgs& a, cudaStream_t stream) {
   const int step_ctas = per_sm * a.sms < kMaxCtas ? per_sm * a.sms : kMaxCtas;
   const int tile_ctas = a.sms < kMaxTileCtas ? a.sms : kMaxTileCtas;
   int* line = reinterpret_cast<int*>(a.part);
-  int* uniform = line + kLineWords;
-  const PagedSeq all{a.seqlens_q, a.seqlens_k, a.B, a.Hkv, G, a.Nq, a.table.max_pages * a.table.page_size,
-                     a.prefix_len};
-  PartRef prefix{};
-  PagedTiles t{};
-  t.seq = all;
-  t.table = a.table;
-  t.prefix_table = a.prefix_table;
-  t.q = a.q;
-  t.o = a.o;
-  t.o_bf16 = a.o_bf16;
-  t.lse = a.lse;
-  t.pairs = x.pairs;
-  t.box_rows = a.box_rows;
-  t.causal = a.causal;
-  t.scale_log2 = a.scale_log2;
-  t.status = a.status;
-  t.wait_limit_ns = a.wait_limit_ns;
-  t.stall_unit = a.stall_unit;
+  const int capacity = a.table.max_pages * a.table.page_size;
+  const PagedSeq all{a.seqlens_q, a.seqlens_k, a.B, a.Hkv, G, a.Nq, capacity, a.prefix_len};
+  // the tile kernel on `heads` row spaces of `pairs` row pairs; the workspace
+  // from `at` on holds `slots` slots
+  auto tiles = [&](PagedTiles& t, int heads, int pairs, int keys, bool two_a_cta, size_t at, size_t slots,
+                   int* table) -> cudaError_t {
+    t.seq = all;
+    t.table = a.table;
+    t.q = a.q;
+    t.o = a.o;
+    t.o_bf16 = a.o_bf16;
+    t.lse = a.lse;
+    const int units = heads * pairs;
+    const int cut = units < 2 * tile_ctas ? units : tile_ctas + units % tile_ctas;
+    t.line_out = table;
+    t.counter = table + kTileLine + 1;
+    t.part = PartRef{table, tile_ctas, kMinTiles, cut, two_a_cta, kPairRows, units, heads, pairs,
+                     head_group(heads, pairs, keys, D, tile_ctas), a.part + at,
+                     a.part + at + slots * kPairRows * D};
+    t.box_rows = a.box_rows;
+    t.causal = a.causal;
+    t.scale_log2 = a.scale_log2;
+    t.status = a.status;
+    t.wait_limit_ns = a.wait_limit_ns;
+    t.stall_unit = a.stall_unit;
+    return cut < units ? cudaMemsetAsync(t.counter, 0, sizeof(int), stream) : cudaSuccess;
+  };
+  PagedCombine c{};
+  c.direct = !with_prefix;
+  c.o_bf16 = a.o_bf16;
   cudaError_t e;
   if (with_prefix) {
-    prefix = PartRef{nullptr, uniform, tile_ctas, kMinTiles, 0, kPairRows, a.part + x.prefix,
-                     a.part + x.prefix + x.prefix_slots * kPairRows * D};
-    PagedTiles p = t;
-    p.line_out = uniform;
-    p.part = prefix;
-    p.wait_first = 1;
-    p.e0 = 0;
-    p.entries = static_cast<int>(x.prefix_entries);
-    e = launch_tiles(p, a.tm_k, a.tm_v, D, tile_ctas, stream);
+    PagedTiles t{};
+    e = tiles(t, a.Hkv, x.prefix_pairs, a.prefix_len, false, x.prefix, x.prefix_slots, line + kLineWords);
     if (e != cudaSuccess) return e;
+    t.prefix_table = a.prefix_table;
+    t.wait_first = 1;
+    e = launch_tiles(t, a.tm_k, a.tm_v, D, tile_ctas, stream);
+    if (e != cudaSuccess) return e;
+    c.prefix = t.part;
   }
-  const long long entries = x.steps ? a.B : static_cast<long long>(a.B) * x.pairs;
-  for (long long e0 = 0; e0 < entries; e0 += x.chunk) {
-    const int n = static_cast<int>(entries - e0 < x.chunk ? entries - e0 : x.chunk);
-    PagedCombine c{};
-    c.seq = all;
-    c.prefix = prefix;
-    c.direct = !with_prefix;
-    c.prefix_entries = static_cast<int>(x.prefix_entries);
-    c.pairs = x.pairs;
-    c.units = n * a.Hkv;
-    c.o = a.o;
-    c.o_bf16 = a.o_bf16;
-    c.lse = a.lse;
-    const int slot_rows = x.steps ? x.rows : kPairRows;
-    c.part = PartRef{line, nullptr, x.steps ? step_ctas : tile_ctas, x.steps ? kMinSteps : kMinTiles,
-                     !x.steps && !with_prefix, slot_rows, a.part + x.own, a.part + x.own + x.own_slots * slot_rows * D};
-    if (x.steps) {
-      const int b0 = static_cast<int>(e0);
-      const size_t first = static_cast<size_t>(b0) * a.Hq * a.Nq;
-      PagedStep p;
-      p.seq = all;
-      p.seq.B = n;
-      if (p.seq.seqlens_q) p.seq.seqlens_q += b0;
-      if (p.seq.seqlens_k) p.seq.seqlens_k += b0;
-      p.table = a.table;
-      p.table.block_table += b0 * a.table.table_stride;
-      p.q = a.q + first * D;
-      p.o = static_cast<uint8_t*>(a.o) + first * D * (a.o_bf16 ? 2 : 4);
-      p.o_bf16 = a.o_bf16;
-      p.lse = a.lse + first;
-      p.line_out = line;
-      p.part = c.part;
-      p.direct = c.direct;
-      p.wait_first = !with_prefix || e0 > 0;
-      p.box_rows = a.box_rows;
-      p.b0 = b0;
-      p.causal = a.causal;
-      p.scale_log2 = a.scale_log2;
-      p.status = a.status;
-      p.wait_limit_ns = a.wait_limit_ns;
-      p.stall_unit = a.stall_unit;
-      e = x.rows <= 8    ? launch_steps<D, 1>(a, p, step_ctas, stream)
-          : x.rows <= 16 ? launch_steps<D, 2>(a, p, step_ctas, stream)
-          : x.rows <= 24 ? launch_steps<D, 3>(a, p, step_ctas, stream)
-                         : launch_steps<D, 4>(a, p, step_ctas, stream);
-      c.seq = p.seq;
-      c.b0 = b0;
-      c.o = p.o;
-      c.lse = p.lse;
-    } else {
-      PagedTiles p = t;
-      p.prefix_table = nullptr;
-      p.line_out = line;
-      p.part = c.part;
-      p.direct = c.direct;
-      p.wait_first = !with_prefix || e0 > 0;
-      p.e0 = static_cast<int>(e0);
-      p.entries = n;
-      e = launch_tiles(p, a.tm_k, a.tm_v, D, tile_ctas, stream);
-      c.e0 = p.e0;
-    }
+  if (!x.steps) {
+    PagedTiles t{};
+    e = tiles(t, a.B * a.Hkv, x.pairs, capacity, !with_prefix, x.own, x.own_slots, line);
     if (e != cudaSuccess) return e;
-    e = launch_combine<D>(c, !x.steps, stream);
+    t.direct = c.direct;
+    // (behind a memset the launch does not overlap with the prefix's)
+    t.wait_first = !with_prefix || t.part.cut < t.part.units;
+    e = launch_tiles(t, a.tm_k, a.tm_v, D, tile_ctas, stream);
+    if (e != cudaSuccess) return e;
+    c.seq = all;
+    c.part = t.part;
+    c.units = c.direct ? t.part.cut : t.part.units;
+    c.o = a.o;
+    c.lse = a.lse;
+    return launch_combine<D>(c, true, stream);
+  }
+  for (int b0 = 0; b0 < a.B; b0 += x.chunk) {
+    const int n = a.B - b0 < x.chunk ? a.B - b0 : x.chunk;
+    const size_t first = static_cast<size_t>(b0) * a.Hq * a.Nq;
+    PagedStep p;
+    p.seq = all;
+    p.seq.B = n;
+    if (p.seq.seqlens_q) p.seq.seqlens_q += b0;
+    if (p.seq.seqlens_k) p.seq.seqlens_k += b0;
+    p.table = a.table;
+    p.table.block_table += b0 * a.table.table_stride;
+    p.q = a.q + first * D;
+    p.o = static_cast<uint8_t*>(a.o) + first * D * (a.o_bf16 ? 2 : 4);
+    p.o_bf16 = a.o_bf16;
+    p.lse = a.lse + first;
+    p.line_out = line;
+    p.part = PartRef{line,        step_ctas, kMinSteps, 0, 0, x.rows, n * a.Hkv, 0, 0, 0, a.part + x.own,
+                     a.part + x.own + x.own_slots * x.rows * D};
+    p.direct = c.direct;
+    p.wait_first = !with_prefix || b0 > 0;
+    p.box_rows = a.box_rows;
+    p.b0 = b0;
+    p.causal = a.causal;
+    p.scale_log2 = a.scale_log2;
+    p.status = a.status;
+    p.wait_limit_ns = a.wait_limit_ns;
+    p.stall_unit = a.stall_unit;
+    e = x.rows <= 8    ? launch_steps<D, 1>(a, p, step_ctas, stream)
+        : x.rows <= 16 ? launch_steps<D, 2>(a, p, step_ctas, stream)
+        : x.rows <= 24 ? launch_steps<D, 3>(a, p, step_ctas, stream)
+                       : launch_steps<D, 4>(a, p, step_ctas, stream);
+    if (e != cudaSuccess) return e;
+    c.seq = p.seq;
+    c.part = p.part;
+    c.units = p.part.units;
+    c.b0 = b0;
+    c.o = p.o;
+    c.lse = p.lse;
+    e = launch_combine<D>(c, false, stream);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;

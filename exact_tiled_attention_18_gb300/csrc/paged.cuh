@@ -10,13 +10,14 @@ namespace fa {
 
 constexpr int kStepRows = 32;          // rows a key head that the step kernel takes
 constexpr int kLineSequences = 256;    // sequences (or row pairs) a launch: the line's table is in shared memory
-constexpr int kLineWords = 272;        // 4-byte words of the line in the workspace, a multiple of 4
+constexpr int kLineWords = 528;        // 4-byte words of a line in the workspace, a multiple of 4
 constexpr int kMaxCtas = 512;
 constexpr int kMinSteps = 1;           // key tiles (64 keys) a CTA of the step kernel takes at least
 constexpr int kMinTiles = 2;           // key tiles (128 keys) a CTA of the tile kernel takes at least
 constexpr int kMaxTileCtas = 256;
+constexpr int kTileLine = 2 * kMaxTileCtas;  // units of the tile kernel's line
 constexpr int kPairRows = 256;         // query rows a unit of the tile kernel: two 128-row tiles
-static_assert(kLineWords >= kLineSequences + 1 && kLineWords % 4 == 0, "the line's room");
+static_assert(kLineWords >= kLineSequences + 1 && kLineWords >= kTileLine + 1 && kLineWords % 4 == 0, "the line's room");
 
 struct PagedSeq {
   const int *seqlens_q, *seqlens_k;
@@ -25,16 +26,20 @@ struct PagedSeq {
   int prefix_len;   // keys that are not these tiles' work
 };
 
-// Partial results of the units (a sequence's or row pair's part and a key
-// head) that CTAs cut out of a line of key tiles.  Unit u's piece of CTA c is
-// in slot u + c, which no other piece has; with two_a_cta, where only a CTA's
-// first and last pieces are partial, in slot 2 c (its first) or 2 c + 1.
+// Partial results of units (the step kernel: a sequence's keys of one key
+// head; the tile kernel: 256 rows of one) that CTAs cut out of a line of key
+// tiles.  Unit u's piece of CTA c is in slot u + c, which no other piece has
+// (units from `cut` on are whole and in slot u + ctas); with two_a_cta, where
+// only a CTA's first and last pieces of the line are partial, in slot 2 c (its
+// first) or 2 c + 1.
 struct PartRef {
-  const int* line;     // first tile of every entry, in tiles of one key head; null: `uniform` tiles each
-  const int* uniform;  // tiles of every entry (one word)
+  const int* line;     // first tile of every unit before `cut` (the step kernel: of every sequence, a head)
   int ctas, min_tiles;
+  int cut;
   int two_a_cta;
   int slot_rows;
+  int units;
+  int heads, pairs, group;  // the tile kernel: (sequence, head)s, row pairs of each, heads dealt out together
   float *o, *lse;      // [slot][slot_rows][d], [slot][slot_rows] (log2 units)
 };
 
@@ -58,8 +63,8 @@ struct PagedStep {
   int stall_unit;
 };
 
-// The tile kernel: entries are row pairs (256 rows) of a sequence, or of all
-// sequences' rows together against the shared prefix.
+// The tile kernel: units are 256 rows of a key head, of one sequence or (the
+// shared prefix) of all sequences' rows together.
 struct PagedTiles {
   PagedSeq seq;
   PageTable table;
@@ -68,11 +73,10 @@ struct PagedTiles {
   void* o;
   int o_bf16;
   float* lse;
-  int* line_out;     // the line's table, or the one word of a prefix
+  int* line_out;     // the line's table, for the combine
   PartRef part;
   int direct;
-  int pairs;         // row pairs a sequence
-  int e0, entries;   // entries of this launch
+  int* counter;      // draws units from part.cut on; zero at the start
   int wait_first;    // as PagedStep's
   int box_rows;
   int causal;
@@ -87,10 +91,8 @@ struct PagedCombine {
   PartRef part;      // the sequences' own keys
   PartRef prefix;    // the shared prefix (o null: none)
   int direct;
-  int pairs, e0;     // the tile kernel's entries
-  int units;         // units of this launch
+  int units;         // units to merge: those behind them are written already
   int b0;            // sequences before this launch's first (rows of the prefix)
-  int prefix_entries;
   void* o;
   int o_bf16;
   float* lse;

@@ -16,9 +16,12 @@
 //  - Keys come from pages: a tile of 128 keys is 128 / box_rows TMA boxes a
 //    64-column block, issued by the lanes of the producer warp, page ids read
 //    32 boxes ahead.
-//  - Division.  The (row pair, key head, key tile) line is cut into equal
-//    ranges, one a CTA, as in the step kernel; pieces of a unit leave
-//    normalised outputs and log-sum-exps that paged_combine_kernel merges.
+//  - Division.  The first one to two units (256 rows of a key head) for every
+//    CTA form a line of key tiles that is cut into equal ranges, one a CTA, as
+//    in the step kernel; the others are drawn whole from a counter, heaviest
+//    first within groups of heads whose keys stay in L2.  So few units fill
+//    the GPU, and many end together, on their lightest.  Pieces of a unit leave normalised outputs
+//    and log-sum-exps that paged_combine_kernel merges.
 //  - Rows of a page behind the last key may hold anything, NaN included, and
 //    0 * NaN would poison the product with V: a spare warp zeroes them in the
 //    last tile before that product is issued.
@@ -26,10 +29,12 @@
 //   warps 0-3  softmax of tile A     warp 8   TMA producer
 //   warps 4-7  softmax of tile B     warp 9   MMA issuer, owns tensor memory
 //                                    warp 10  zeroes the values behind the last key
+//                                    warp 11  draws the whole units
 #include <cuda_runtime.h>
 #include <math_constants.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "internal.h"
 #include "paged.cuh"
@@ -49,7 +54,8 @@ static_assert(2 * 128 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * kLaunchReg
               "register split exceeds the launch allocation");
 constexpr float kTau = 8.f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kRows = 128;   // rows and keys a tile
+constexpr int kRows = 128;        // rows and keys a tile
+constexpr int kUnitReaders = 11;  // warps that follow the drawn units: softmax, producer, issuer, cleaner
 
 enum TileSite : int {
   SITE_TILE_LOAD = 75,
@@ -57,6 +63,7 @@ enum TileSite : int {
   SITE_TILE_S = 77,
   SITE_TILE_O = 78,
   SITE_TILE_CLEAN = 79,
+  SITE_TILE_UNIT = 80,
 };
 
 template <int D>
@@ -73,12 +80,14 @@ struct TileLayout {
   static constexpr int O_FULL = P_FULL + 2;
   static constexpr int DIRTY = O_FULL + 2;
   static constexpr int CLEAN = DIRTY + 1;
-  static constexpr int DRAIN = CLEAN + 1;
+  static constexpr int UNIT_FULL = CLEAN + 1;
+  static constexpr int UNIT_EMPTY = UNIT_FULL + 2;
+  static constexpr int DRAIN = UNIT_EMPTY + 2;
   static constexpr int kNumBars = DRAIN + 1;
   static constexpr int kMiscOff = kBarOff + kNumBars * 8;
-  static constexpr int kScratchOff = kMiscOff + 16;  // one word a warp
+  static constexpr int kScratchOff = kMiscOff + 16;  // one word a warp, then the two drawn units
   static constexpr int kLineOff = kScratchOff + 64;
-  static constexpr int kSmemBytes = kLineOff + (kLineSequences + 1) * 4 + 1024;
+  static constexpr int kSmemBytes = kLineOff + (kTileLine + 1) * 4 + 1024;
   static constexpr uint32_t kColO = 256;
 };
 
@@ -153,6 +162,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(bars + 8 * L::DIRTY, 1);
     mbar_init(bars + 8 * L::CLEAN, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bars + 8 * (L::UNIT_FULL + i), 1);
+      mbar_init(bars + 8 * (L::UNIT_EMPTY + i), kUnitReaders);
+    }
     mbar_init(bars + 8 * L::DRAIN, 1);
     *abort_flag = 0;
     mbar_fence_init();
@@ -167,10 +180,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (p.wait_first) grid_wait();
   grid_trigger();
-  // the line: for the prefix every entry has the tiles of its keys that some
-  // sequence reaches
-  int reach = 0, total;
-  int uniform = 0;
+  // the prefix's keys that some sequence reaches
+  int reach = 0;
   if constexpr (PREFIX) {
     for (int b = threadIdx.x; b < p.seq.B; b += kThreads) {
       int lq, lk;
@@ -181,63 +192,117 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) scratch[warp] = reach;
     __syncthreads();
     for (int i = 0; i < kThreads / 32; ++i) reach = max(reach, scratch[i]);
-    uniform = (reach + kRows - 1) / kRows;
-    total = p.entries * uniform * Hkv;
-    if (blockIdx.x == 0 && threadIdx.x == 0) *p.line_out = uniform;
-  } else {
-    build_line<kThreads>(line, scratch, p.entries, [&](int e) {
-      const int b = (p.e0 + e) / p.pairs;
-      const int r0 = (p.e0 + e - b * p.pairs) * kPairRows;
-      int lq, lk;
-      seq_lens(p.seq, b, lq, lk);
-      const int keys = max(tile_keys(r0, rows, p.seq.Nq, lq, lk, origin, p.causal),
-                           tile_keys(r0 + kRows, rows, p.seq.Nq, lq, lk, origin, p.causal));
-      return (keys + kRows - 1) / kRows;
-    });
-    total = line[p.entries] * Hkv;
-    if (blockIdx.x == 0)
-      for (int i = threadIdx.x; i <= p.entries; i += kThreads) p.line_out[i] = line[i];
+    __syncthreads();
   }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
-  auto BAR = [&](int i) -> uint32_t { return bars + 8u * static_cast<uint32_t>(i); };
-  auto starts = [&](int e) -> int { return PREFIX ? e * uniform : line[e]; };
-  const int per = tiles_per_cta(total, gridDim.x, p.part.min_tiles);
-  int at = min(static_cast<int>(blockIdx.x) * per, total);
-  const int stop = min(at + per, total);
-  Walk w;
-  const WaitCtl wc{abort_flag, p.status, p.wait_limit_ns};
-  // A row tile without keys in a piece, and the cleaner, wait while the other
-  // tile's whole pieces go by: their limit grows with the range.  The producer
-  // and the issuer notice a stall within the limit itself and end all waits.
-  const WaitCtl wc_idle{abort_flag, p.status, p.wait_limit_ns * static_cast<unsigned long long>(stop - at + 1)};
-
-  auto entry_of = [&](int e, int& b, int& r0) {  // sequence (0 for the prefix) and first row of entry e
-    if constexpr (PREFIX) {
-      b = 0;
-      r0 = e * kPairRows;
-    } else {
-      b = (p.e0 + e) / p.pairs;
-      r0 = (p.e0 + e - b * p.pairs) * kPairRows;
-    }
+  // sequence (0 for the prefix), key head and first row of unit u: groups of
+  // `group` (sequence, head)s; in a group the row pairs from the last, which
+  // under the causal rule sees the most keys, each for every head
+  auto unit_at = [&](int u, int& b, int& head, int& r0) {
+    const int g = u / (p.part.group * p.part.pairs);
+    const int in = u - g * p.part.group * p.part.pairs;
+    const int hs = min(p.part.group, p.part.heads - g * p.part.group);
+    const int level = in / hs;
+    const int bh = g * p.part.group + in - level * hs;
+    b = PREFIX ? 0 : bh / Hkv;
+    head = bh - b * Hkv;
+    r0 = (p.part.pairs - 1 - level) * kPairRows;
   };
-  auto piece_of = [&](int& b, int& r0) {
-    Piece x;
-    entry_of(w.e, b, r0);
-    int ka, kb;
+  // keys (from the origin) that tiles A and B of a unit need
+  auto unit_keys = [&](int b, int r0, int& ka, int& kb, int& limit) {
     if constexpr (PREFIX) {
-      ka = reach;
+      ka = limit = reach;
       kb = r0 + kRows < space ? reach : 0;
-      x.limit = reach;
     } else {
       int lq, lk;
       seq_lens(p.seq, b, lq, lk);
       ka = tile_keys(r0, rows, p.seq.Nq, lq, lk, origin, p.causal);
       kb = tile_keys(r0 + kRows, rows, p.seq.Nq, lq, lk, origin, p.causal);
-      x.limit = lk - origin;
+      limit = lk - origin;
     }
+  };
+  auto unit_tiles = [&](int u) {
+    int b, head, r0, ka, kb, limit;
+    unit_at(u, b, head, r0);
+    unit_keys(b, r0, ka, kb, limit);
+    return (max(ka, kb) + kRows - 1) / kRows;
+  };
+  const int cut = p.part.cut;  // units of the line
+  build_line<kThreads>(line, scratch, cut, [&](int e) { return unit_tiles(e); });
+  const int total = line[cut];
+  if (blockIdx.x == 0)
+    for (int i = threadIdx.x; i <= cut; i += kThreads) p.line_out[i] = line[i];
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  auto BAR = [&](int i) -> uint32_t { return bars + 8u * static_cast<uint32_t>(i); };
+  // A CTA's work: its range of the line (place x: from tile x on), then the
+  // units it draws (place -1 - n: the n-th).
+  volatile int* drawn = scratch + 14;
+  const int per = tiles_per_cta(total, gridDim.x, p.part.min_tiles);
+  const int at0 = min(static_cast<int>(blockIdx.x) * per, total);
+  const int stop = min(at0 + per, total);
+  int at = at0;
+  struct Place {
+    int u;           // unit
+    int tile, end;   // its tiles in this piece: [tile, end)
+    bool whole;      // all of the unit's
+  };
+  auto locate = [&](int place) {
+    Place w;
+    if (place < 0) {
+      w.u = drawn[(-1 - place) & 1];
+      w.tile = 0;
+      w.end = unit_tiles(w.u);
+      w.whole = true;
+      return w;
+    }
+    // the last unit that starts at or before the tile (one with tiles: an
+    // empty one starts where its successor does)
+    int lo = 0, hi = cut - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (line[mid] <= place) lo = mid; else hi = mid - 1;
+    }
+    w.u = lo;
+    w.tile = place - line[lo];
+    const int tiles = line[lo + 1] - line[lo];
+    w.end = min(tiles, w.tile + stop - place);
+    w.whole = w.tile == 0 && w.end == tiles;
+    return w;
+  };
+  const WaitCtl wc{abort_flag, p.status, p.wait_limit_ns};
+  // A row tile without keys in a piece, and the cleaner, wait while the other
+  // tile's whole pieces go by: their limit grows with the range.  The producer
+  // and the issuer notice a stall within the limit itself and end all waits.
+  const WaitCtl wc_idle{abort_flag, p.status, p.wait_limit_ns * 64};
+
+  // Every role that follows the work calls this before a piece, with all lanes
+  // of its warp (`true`: there is one), and done() behind it.
+  auto another = [&](bool& ok) {
+    if (at >= 0) {
+      if (at < stop) return true;
+      if (cut == p.part.units) return false;
+      at = -1;
+    }
+    const int n = -1 - at;
+    ok = tile_wait(BAR(L::UNIT_FULL + (n & 1)), (n >> 1) & 1, wc_idle, SITE_TILE_UNIT, at);
+    return ok && drawn[n & 1] < p.part.units;
+  };
+  auto done = [&](int tiles) {
+    if (at < 0) {
+      mbar_arrive_warp(BAR(L::UNIT_EMPTY + ((-1 - at) & 1)));
+      --at;
+    } else {
+      at += tiles;
+    }
+  };
+
+  auto piece_of = [&](const Place& w, int& b, int& head, int& r0) {
+    Piece x;
+    unit_at(w.u, b, head, r0);
+    int ka, kb;
+    unit_keys(b, r0, ka, kb, x.limit);
     const int len = w.end - w.tile;
     x.na = max(0, min((ka + kRows - 1) / kRows - w.tile, len));
     x.nb = max(0, min((kb + kRows - 1) / kRows - w.tile, len));
@@ -267,12 +332,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     uint32_t sn = 0, on = 0;
     bool ok = true;
-    while (at < stop) {
+    while (another(ok)) {
       int nt, lim0 = 0;  // key tiles; this row's visible keys from the piece's first
       {
-        int b, r0, rb, rr;
-        walk_begin(w, starts, p.entries, Hkv, at, stop);
-        const Piece x = piece_of(b, r0);
+        int b, head, r0, rb, rr;
+        const Place w = locate(at);
+        const Piece x = piece_of(w, b, head, r0);
         nt = t ? x.nb : x.na;
         unsigned long long grow = 0;
         const bool valid = row_of(b, r0, rb, rr);
@@ -283,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (i < lq) lim0 = (p.causal ? min(i + lk - lq + 1, lk) : lk) - origin;
           if (PREFIX) lim0 = min(lim0, p.seq.prefix_len);
           lim0 -= w.tile * kRows;
-          grow = (static_cast<unsigned long long>(rb) * Hkv + w.head) * rows + rr;
+          grow = (static_cast<unsigned long long>(rb) * Hkv + head) * rows + rr;
         }
         if (nt > 0) {
           // gather the tile's 128 rows: a warp its 32, whole rows at a time.
@@ -407,14 +472,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const bool live = l > 0.f;
       const float inv = live ? 1.0f / (l + dl) : 0.f;
-      int b, r0, rb, rr;
-      walk_begin(w, starts, p.entries, Hkv, at, stop);
-      entry_of(w.e, b, r0);
+      int b, head, r0, rb, rr;
+      const Place w = locate(at);
+      unit_at(w.u, b, head, r0);
       const bool valid = row_of(b, r0, rb, rr);
-      const bool whole = p.direct && w.tile == 0 && w.end == w.tiles;
-      const size_t grow = (static_cast<size_t>(rb) * Hkv + w.head) * rows + rr;
-      const long long slot = p.part.two_a_cta ? 2LL * blockIdx.x + (at == static_cast<int>(blockIdx.x) * tiles_per_cta(starts(p.entries) * Hkv, gridDim.x, p.part.min_tiles) ? 0 : 1)
-                                              : static_cast<long long>(w.e) * Hkv + w.head + blockIdx.x;
+      const bool whole = p.direct && w.whole;
+      const size_t grow = (static_cast<size_t>(rb) * Hkv + head) * rows + rr;
+      const long long slot = p.part.two_a_cta ? 2LL * blockIdx.x + (at == at0 ? 0 : 1)
+                                              : static_cast<long long>(w.u) + (at < 0 ? gridDim.x : blockIdx.x);
       const long long prow = slot * kPairRows + t * kRows + r;
       float* dst = whole ? static_cast<float*>(p.o) + grow * D : p.part.o + prow * D;
       const bool half = whole && p.o_bf16;
@@ -458,24 +523,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         else
           p.part.lse[prow] = lse2;
       }
-      at += w.end - w.tile;
+      done(w.end - w.tile);
     }
   } else {
     regs_decrease<kOtherRegs>();
     if (warp == 8) {
       // -------------------------------------------------------- TMA producer
       const int boxes = kRows / p.box_rows;
-      const bool loads = lane < CB * boxes;
-      const int block = lane / boxes, box = lane - block * boxes;
+      const int block = lane / boxes, box = lane - block * boxes;  // this lane's load of a tile
+      const bool loads = block < CB;
       const uint32_t offset = static_cast<uint32_t>(block * 16384 + box * p.box_rows * 128);
       const uint64_t policy = l2_policy_evict_last();
       uint32_t kvpos = 0;
       int piece = 0;
-      bool ok = true, more = walk_begin(w, starts, p.entries, Hkv, at, stop);
-      while (more && ok) {
-        int b, r0;
-        const Piece x = piece_of(b, r0);
-        const int unit = w.e * Hkv + w.head;
+      bool ok = true;
+      while (another(ok)) {
+        int b, head, r0;
+        const Place w = locate(at);
+        const Piece x = piece_of(w, b, head, r0);
         const int* pages = PREFIX ? p.prefix_table : p.table.block_table + b * p.table.table_stride;
         const int first = origin + w.tile * kRows;
         const int last = origin + x.limit;
@@ -495,30 +560,30 @@ __global__ void __launch_bounds__(kThreads, 1)
           int outer = p.table.num_pages * Hkv;  // past the map: zeros
           if (loads && key < last) {
             if (page >= 0 && page < p.table.num_pages)
-              outer = page * Hkv + w.head;
+              outer = page * Hkv + head;
             else
               record_bad_page(p.status, SITE_PAGE_READ, b, page);
           }
+          const int row = key % p.table.page_size;
 #pragma unroll 1
           for (int kv = 0; kv < 2; ++kv) {
             const uint32_t s = kvpos % S, use = kvpos / S;
-            ok = tile_wait(BAR(L::KV_EMPTY + s), (use & 1) ^ 1, wc, SITE_TILE_LOAD, unit);
+            ok = tile_wait(BAR(L::KV_EMPTY + s), (use & 1) ^ 1, wc, SITE_TILE_LOAD, at);
             if (!ok) break;
-            if (blockIdx.x == 0 && piece == p.stall_unit && j == 0 && kv == 0) {
-              ++kvpos;  // testing hook: leave this tile unloaded
-              continue;
-            }
+            ++kvpos;
+            if (blockIdx.x == 0 && piece == p.stall_unit && j == 0 && kv == 0)
+              continue;  // testing hook: leave this tile unloaded
             if (lane == 0) mbar_arrive_expect_tx(BAR(L::KV_FULL + s), L::kTileBytes);
             __syncwarp();
             if (loads)
               tma_load_3d_hint(sbase + L::kRingOff + s * L::kTileBytes + offset, kv == 0 ? &tm_k : &tm_v,
-                               BAR(L::KV_FULL + s), block * 64, key % p.table.page_size, outer, policy);
+                               BAR(L::KV_FULL + s), block * 64, row, outer, policy);
             __syncwarp();
-            ++kvpos;
           }
         }
+        if (!ok) break;
         ++piece;
-        if (ok) more = walk_next(w, starts, Hkv, at, stop);
+        done(w.end - w.tile);
       }
       if (!ok && lane == 0) {
         for (uint32_t s = 0; s < static_cast<uint32_t>(S); ++s) {
@@ -530,7 +595,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else if (warp == 9) {
       // ---------------------------------------------------------- MMA issuer
-      if (lane == 0) {
+      {
         constexpr uint32_t id_s = idesc_bf16_f32(128, 128, false, false);
         constexpr uint32_t id_pv = idesc_bf16_f32(128, D, false, true);
         const SDesc qdesc0 = sdesc_sw128(sbase, 16, 1024);
@@ -555,12 +620,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         };
         uint32_t qa = 0, qb = 0, kvbase = 0, pa = 0, pb = 0, cleaned = 0;
-        bool ok = true, more = walk_begin(w, starts, p.entries, Hkv, at, stop);
-        while (more && ok) {
-          int b, r0;
-          const Piece x = piece_of(b, r0);
-          const int unit = w.e * Hkv + w.head;
+        bool ok = true;
+        while (another(ok)) {
+          int b, head, r0;
+          const Place w = locate(at);
+          const Piece x = piece_of(w, b, head, r0);
+          const int unit = at;
           const int na = x.na, nb = x.nb;
+          if (lane == 0) {
+          do {
           if (x.nmax > 0) {
             ok = wait_bounded(BAR(L::KV_FULL + kvbase % S), (kvbase / S) & 1, wc, SITE_TILE_MMA, unit);
             if (!ok) break;
@@ -581,69 +649,81 @@ __global__ void __launch_bounds__(kThreads, 1)
               umma_commit(BAR(L::S_FULL + 1));
             }
           }
-          for (int j = 0; j < x.nmax; ++j) {
+          // One key tile.  STEADY: both row tiles have it and the next one, and
+          // its values need no zeroing -- all but the last steps of most
+          // pieces, with nothing to decide in them: this thread's instructions
+          // are on every step's critical path.
+          auto step = [&](auto steady_tag, int j) -> bool {
+            constexpr bool STEADY = decltype(steady_tag)::value;
             const uint32_t kpos = kvbase + 2 * j, vpos = kpos + 1, knext = kpos + 2;
-            const bool has_a = j < na, next_a = j + 1 < na, has_b = j < nb, next_b = j + 1 < nb;
+            const bool has_a = STEADY || j < na, next_a = STEADY || j + 1 < na;
+            const bool has_b = STEADY || j < nb, next_b = STEADY || j + 1 < nb;
+            const bool dirty = !STEADY && j == x.clean;
             umma_commit(BAR(L::KV_EMPTY + kpos % S));  // K_j is free once S(j) of both tiles completes
-            ok = wait_bounded(BAR(L::KV_FULL + vpos % S), (vpos / S) & 1, wc, SITE_TILE_MMA, unit);
-            if (!ok) break;
+            if (!wait_bounded(BAR(L::KV_FULL + vpos % S), (vpos / S) & 1, wc, SITE_TILE_MMA, unit)) return false;
             // the last keys' values: zeroed behind the last key by warp 10
             // while the softmax of this tile runs
-            if (j == x.clean) mbar_arrive(BAR(L::DIRTY));
+            if (dirty) mbar_arrive(BAR(L::DIRTY));
             auto values_ready = [&]() {
-              if (j != x.clean) return true;
-              return wait_bounded(BAR(L::CLEAN), cleaned & 1, wc, SITE_TILE_CLEAN, unit);
+              return !dirty || wait_bounded(BAR(L::CLEAN), cleaned & 1, wc, SITE_TILE_CLEAN, unit);
             };
             if (has_a) {
-              ok = wait_bounded(BAR(L::P_FULL + 0), pa & 1, wc, SITE_TILE_MMA, unit) && values_ready();
-              if (!ok) break;
+              if (!wait_bounded(BAR(L::P_FULL + 0), pa & 1, wc, SITE_TILE_MMA, unit) || !values_ready()) return false;
               ++pa;
               tc_fence_after();
               issue_pv(0, vpos % S, j > 0);
               if (!next_a) umma_commit(BAR(L::O_FULL + 0));
               if (next_a) {
-                ok = wait_bounded(BAR(L::KV_FULL + knext % S), (knext / S) & 1, wc, SITE_TILE_MMA, unit);
-                if (!ok) break;
+                if (!wait_bounded(BAR(L::KV_FULL + knext % S), (knext / S) & 1, wc, SITE_TILE_MMA, unit)) return false;
                 tc_fence_after();
                 issue_s(0, knext % S);
                 umma_commit(BAR(L::S_FULL + 0));
               }
             }
             if (has_b) {
-              ok = wait_bounded(BAR(L::P_FULL + 1), pb & 1, wc, SITE_TILE_MMA, unit) && values_ready();
-              if (!ok) break;
+              if (!wait_bounded(BAR(L::P_FULL + 1), pb & 1, wc, SITE_TILE_MMA, unit) || !values_ready()) return false;
               ++pb;
               tc_fence_after();
               issue_pv(1, vpos % S, j > 0);
               if (!next_b) umma_commit(BAR(L::O_FULL + 1));
             }
-            if (j == x.clean) ++cleaned;
+            if (dirty) ++cleaned;
             umma_commit(BAR(L::KV_EMPTY + vpos % S));  // V_j is free once PV(j) of both tiles completes
             if (next_b) {
               if (!(has_a && next_a)) {  // otherwise tile A's S(j+1) already waited for K_{j+1}
-                ok = wait_bounded(BAR(L::KV_FULL + knext % S), (knext / S) & 1, wc, SITE_TILE_MMA, unit);
-                if (!ok) break;
+                if (!wait_bounded(BAR(L::KV_FULL + knext % S), (knext / S) & 1, wc, SITE_TILE_MMA, unit)) return false;
                 tc_fence_after();
               }
               issue_s(1, knext % S);
               umma_commit(BAR(L::S_FULL + 1));
             }
+            return true;
+          };
+          const int both = min(na, nb) - 1;
+          for (int j = 0; j < x.nmax && ok; ++j)
+            ok = j < both && j != x.clean ? step(std::true_type{}, j) : step(std::false_type{}, j);
+          } while (false);
           }
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
           kvbase += 2 * x.nmax;
-          if (ok) more = walk_next(w, starts, Hkv, at, stop);
+          done(w.end - w.tile);
         }
         // every MMA this thread issued completes before tensor memory is freed
-        umma_commit(BAR(L::DRAIN));
-        drain_wait(BAR(L::DRAIN), 0, p.wait_limit_ns);
+        if (lane == 0) {
+          umma_commit(BAR(L::DRAIN));
+          drain_wait(BAR(L::DRAIN), 0, p.wait_limit_ns);
+        }
       }
     } else if (warp == 10) {
       // ------------------------------------------- values behind the last key
       uint32_t kvbase = 0, cleaned = 0;
-      bool ok = true, more = walk_begin(w, starts, p.entries, Hkv, at, stop);
-      while (more && ok) {
-        int b, r0;
-        const Piece x = piece_of(b, r0);
-        const int unit = w.e * Hkv + w.head;
+      bool ok = true;
+      while (another(ok)) {
+        int b, head, r0;
+        const Place w = locate(at);
+        const Piece x = piece_of(w, b, head, r0);
+        const int unit = at;
         if (x.clean >= 0) {
           const uint32_t vpos = kvbase + 2 * x.clean + 1;
           ok = tile_wait(BAR(L::DIRTY), cleaned & 1, wc_idle, SITE_TILE_CLEAN, unit);
@@ -660,7 +740,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++cleaned;
         }
         kvbase += 2 * x.nmax;
-        more = walk_next(w, starts, Hkv, at, stop);
+        done(w.end - w.tile);
+      }
+    } else if (lane == 0 && cut < p.part.units) {
+      // ------------------------------------------------------ whole units
+      // drawn two ahead: the draw's latency passes behind the work before
+      for (int n = 0;; ++n) {
+        if (!wait_bounded(BAR(L::UNIT_EMPTY + (n & 1)), ((n >> 1) & 1) ^ 1, wc_idle, SITE_TILE_UNIT, n)) break;
+        const int u = cut + atomicAdd(p.counter, 1);
+        drawn[n & 1] = u;
+        mbar_arrive(BAR(L::UNIT_FULL + (n & 1)));
+        if (u >= p.part.units) break;
       }
     }
   }

@@ -558,7 +558,7 @@ fa_status fa_sync_status(fa_stream_t stream);
  * out[0] status code, out[1] wait site, out[2] block index, out[3] work unit.
  * Wait sites: 1-7 forward, 11-20 dK/dV, 21-32 dQ, 35-36 decode, 41-47 FP8
  * forward, 51-59 the single-pass row-term pass, 61-63 the single-pass dK/dV
- * sweep, 71-79 the paged calls (each kernel's source names them).  After
+ * sweep, 71-80 the paged calls (each kernel's source names them).  After
  * FA_ERR_BAD_PAGE: out[2] the sequence, out[3] the table entry.
  * Returns FA_OK, or FA_ERR_INVALID_ARG if out is NULL.
  */
