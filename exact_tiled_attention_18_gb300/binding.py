@@ -804,48 +804,58 @@ def kv_append(k, v, k_pages, v_pages, block_table, seqlens_k, seqlens_q=None, tu
     return q_out
 
 
-def _paged(name, q, k_pages, v_pages, prefix, block_table, seqlens_k, seqlens_q, causal, scale, o_dtype, workspace,
+def _paged(shared, q, k_pages, v_pages, prefix, block_table, seqlens_k, seqlens_q, causal, scale, o_dtype, workspace,
            out):
     import torch
-    if q.dim() != 4 or not q.is_cuda or q.dtype != torch.bfloat16 or not q.is_contiguous():
+    if q.dtype != torch.bfloat16 or not q.is_cuda or q.dim() != 4 or not q.is_contiguous():
         raise ValueError("q must be a contiguous bf16 CUDA tensor [B, Hq, Nq, d]")
     B, Hq, Nq, d = q.shape
     index = q.get_device()
     pages, table, Hkv = _page_args(k_pages, v_pages, block_table, B, d, index)
-    if scale is None:
-        scale = d ** -0.5
     if out is None:
-        dtype = torch.float32 if o_dtype is None else o_dtype
-        o = torch.empty((B, Hq, Nq, d), dtype=dtype, device=q.device)
+        if o_dtype is None:
+            o_dtype = torch.float32
+        if o_dtype == torch.bfloat16:
+            o = torch.empty_like(q)
+        elif o_dtype == torch.float32:
+            o = torch.empty_like(q, dtype=o_dtype)
+        else:
+            raise ValueError("O must be float32 or bfloat16")
         lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=q.device)
     else:
         o, lse = out
-        dtype = o.dtype
+        o_dtype = o.dtype
+        if o_dtype != torch.float32 and o_dtype != torch.bfloat16:
+            raise ValueError("O must be float32 or bfloat16")
         if (o.shape != q.shape or not o.is_contiguous() or o.get_device() != index or lse.shape != (B, Hq, Nq)
                 or lse.dtype != torch.float32 or not lse.is_contiguous() or lse.get_device() != index):
             raise ValueError("out must be contiguous O [B, Hq, Nq, d] and fp32 LSE [B, Hq, Nq] on q's device")
-    if dtype != torch.float32 and dtype != torch.bfloat16:
-        raise ValueError("O must be float32 or bfloat16")
-    call, bytes_of = _paged_calls(name)
-    need = bytes_of(B, Hq, Hkv, Nq, d) // 4
+    L = _lib or lib()
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.float32, device=q.device)
-    elif (workspace.dtype != torch.float32 or not workspace.is_contiguous() or workspace.get_device() != index
-          or workspace.numel() < need):
-        raise ValueError(f"workspace must be fp32 on q's device, {name}_workspace_bytes(...) bytes")
-    st = _call_on(index, call, q.data_ptr(), *pages, *prefix, *table, o.data_ptr(), dtype == torch.bfloat16,
-                  lse.data_ptr(), _lens(seqlens_q, B, index), _lens(seqlens_k, B, index), workspace.data_ptr(), B, Hq,
-                  Hkv, Nq, d, scale, bool(causal))
+        # the library's own, unless a graph is being captured: the graph then
+        # keeps a tensor of PyTorch's graph pool
+        ws = 0
+        if torch.cuda.is_current_stream_capturing():
+            workspace = torch.empty(_paged_workspace(L, shared, B, Hq, Hkv, Nq, d), dtype=torch.float32,
+                                    device=q.device)
+            ws = workspace.data_ptr()
+    else:
+        if (workspace.dtype != torch.float32 or not workspace.is_contiguous() or workspace.get_device() != index
+                or workspace.numel() < _paged_workspace(L, shared, B, Hq, Hkv, Nq, d)):
+            raise ValueError("workspace must be fp32 on q's device, of the call's workspace_bytes(...) bytes")
+        ws = workspace.data_ptr()
+    st = _call_on(index, L.fa_fwd_shared_prefix if shared else L.fa_fwd_paged, q.data_ptr(), *pages, *prefix, *table,
+                  o.data_ptr(), o_dtype == torch.bfloat16, lse.data_ptr(), _lens(seqlens_q, B, index),
+                  _lens(seqlens_k, B, index), ws, B, Hq, Hkv, Nq, d, d ** -0.5 if scale is None else scale,
+                  bool(causal))
     if st:
-        _check(name, st)
+        _check("fa_fwd_shared_prefix" if shared else "fa_fwd_paged", st)
     return o, lse
 
 
-def _paged_calls(name):
-    L = _lib or lib()
-    if name == "fa_fwd_paged":
-        return L.fa_fwd_paged, L.fa_fwd_paged_workspace_bytes
-    return L.fa_fwd_shared_prefix, L.fa_fwd_shared_prefix_workspace_bytes
+def _paged_workspace(L, shared, B, Hq, Hkv, Nq, d) -> int:
+    size = L.fa_fwd_shared_prefix_workspace_bytes if shared else L.fa_fwd_paged_workspace_bytes
+    return size(B, Hq, Hkv, Nq, d) // 4
 
 
 def forward_paged(q, k_pages, v_pages, block_table, seqlens_k=None, seqlens_q=None, causal: bool = True,
@@ -854,9 +864,9 @@ def forward_paged(q, k_pages, v_pages, block_table, seqlens_k=None, seqlens_q=No
     against the keys and values that ``block_table`` int32 [B, max_pages]
     names in k_pages, v_pages [pages, Hkv, page_size, d]; Hq a multiple of
     Hkv.  ``seqlens_k``, ``seqlens_q``: int32 [B] as kv_append.  ``workspace``:
-    an fp32 tensor of fa_fwd_paged_workspace_bytes(...) bytes, made here by
-    default."""
-    return _paged("fa_fwd_paged", q, k_pages, v_pages, (), block_table, seqlens_k, seqlens_q, causal, scale, o_dtype,
+    an fp32 tensor of fa_fwd_paged_workspace_bytes(...) bytes; by default a
+    stream-ordered one of the library's."""
+    return _paged(False, q, k_pages, v_pages, (), block_table, seqlens_k, seqlens_q, causal, scale, o_dtype,
                   workspace, out)
 
 
@@ -873,7 +883,7 @@ def forward_shared_prefix(q, k_pages, v_pages, prefix_table, prefix_len: int, bl
             or prefix_table.numel() * k_pages.shape[2] < prefix_len):
         raise ValueError("prefix_table must be contiguous int32 on q's device with an entry for every page of the "
                          "prefix")
-    return _paged("fa_fwd_shared_prefix", q, k_pages, v_pages, (prefix_table.data_ptr(), int(prefix_len)), block_table,
+    return _paged(True, q, k_pages, v_pages, (prefix_table.data_ptr(), int(prefix_len)), block_table,
                   seqlens_k, seqlens_q, causal, scale, o_dtype, workspace, out)
 
 

@@ -72,9 +72,10 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
 struct MapKey {
   const void* base;
   int elem_bytes, heads, rows, inner, box_inner, box_rows;
+  bool blocked = false;  // 4-D: a box takes all the 64-column blocks of its rows
   bool operator==(const MapKey& o) const {
     return base == o.base && elem_bytes == o.elem_bytes && heads == o.heads && rows == o.rows && inner == o.inner &&
-           box_inner == o.box_inner && box_rows == o.box_rows;
+           box_inner == o.box_inner && box_rows == o.box_rows && blocked == o.blocked;
   }
 };
 
@@ -84,9 +85,26 @@ MapKey g_map_keys[kMapCacheSize];
 CUtensorMap g_maps[kMapCacheSize];
 int g_map_count = 0, g_map_next = 0;
 
+bool remember_map(const MapKey& key, const CUtensorMap& m) {
+  std::lock_guard<std::mutex> lock(g_map_mu);
+  int slot;
+  if (g_map_count < kMapCacheSize) {
+    slot = g_map_count++;
+  } else {
+    slot = g_map_next;
+    g_map_next = (g_map_next + 1) % kMapCacheSize;
+  }
+  g_map_keys[slot] = key;
+  g_maps[slot] = m;
+  return true;
+}
+
 // 3-D map over [heads][rows][inner] elements of `elem_bytes` (2: bf16, 1:
 // E4M3 bytes), box = box_inner x box_rows x 1 with the 128-byte swizzle (the
 // layout the MMA descriptors expect).  Rows past `rows` read as zeros.
+// Blocked (bf16): a 4-D map over [heads][inner / 64][rows][64] of the same
+// memory, box = 64 x box_rows x (inner / 64) x 1, so that one load brings the
+// box's rows block by block.
 bool encode_map(CUtensorMap* m, const MapKey& key) {
   {
     std::lock_guard<std::mutex> lock(g_map_mu);
@@ -105,22 +123,22 @@ bool encode_map(CUtensorMap* m, const MapKey& key) {
   cuuint64_t strides[2] = {static_cast<cuuint64_t>(key.inner) * eb,
                            static_cast<cuuint64_t>(key.rows) * key.inner * eb};
   cuuint32_t box[3] = {static_cast<cuuint32_t>(key.box_inner), static_cast<cuuint32_t>(key.box_rows), 1};
-  cuuint32_t estride[3] = {1, 1, 1};
+  cuuint32_t estride[4] = {1, 1, 1, 1};
+  if (key.blocked) {
+    cuuint64_t dims4[4] = {64, dims[1], static_cast<cuuint64_t>(key.inner / 64), dims[2]};
+    cuuint64_t strides4[3] = {strides[0], 128, strides[1]};
+    cuuint32_t box4[4] = {64, box[1], static_cast<cuuint32_t>(key.inner / 64), 1};
+    if (fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(key.base), dims4, strides4, box4, estride,
+           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return false;
+    return remember_map(key, *m);
+  }
   CUresult r = fn(m, key.elem_bytes == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 3,
                   const_cast<void*>(key.base), dims, strides, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return false;
-  std::lock_guard<std::mutex> lock(g_map_mu);
-  int slot;
-  if (g_map_count < kMapCacheSize) {
-    slot = g_map_count++;
-  } else {
-    slot = g_map_next;
-    g_map_next = (g_map_next + 1) % kMapCacheSize;
-  }
-  g_map_keys[slot] = key;
-  g_maps[slot] = *m;
-  return true;
+  return remember_map(key, *m);
 }
 
 // bf16 [heads][n][d], boxes of 64 columns x box_rows rows.
@@ -367,6 +385,32 @@ fa_status bwd_launch(fa::BwdArgs& a, float* workspace, int B, int H, int Nq, fa_
 
 // ------------------------------------------- rotary positions, paged cache
 
+// Pool of the paged calls' own workspaces on the current device.  The
+// device's default pool gives freed memory back at the next synchronisation,
+// and taking it anew then costs a small call more than its kernels; this one
+// keeps what the calls have used, up to kPoolKeep bytes.
+constexpr unsigned long long kPoolKeep = 256ULL << 20;
+
+cudaMemPool_t workspace_pool() {
+  static std::mutex mu;
+  static cudaMemPool_t pools[kMaxDevices];
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return nullptr;
+  std::lock_guard<std::mutex> lock(mu);
+  if (!pools[dev]) {
+    cudaMemPoolProps props{};
+    props.allocType = cudaMemAllocationTypePinned;
+    props.location.type = cudaMemLocationTypeDevice;
+    props.location.id = dev;
+    cudaMemPool_t pool;
+    if (cudaMemPoolCreate(&pool, &props) != cudaSuccess) return nullptr;
+    unsigned long long keep = kPoolKeep;
+    if (cudaMemPoolSetAttribute(pool, cudaMemPoolAttrReleaseThreshold, &keep) != cudaSuccess) return nullptr;
+    pools[dev] = pool;
+  }
+  return pools[dev];
+}
+
 // Strides of the dimensions that are walked; the stride of a dimension of
 // size one means nothing and is dropped.
 fa::Strides used_strides(long long sb, long long sh, long long sn, int B, int H, int N) {
@@ -451,15 +495,21 @@ fa_status paged_common(const void* q, const void* k_pages, const void* v_pages, 
   a.wait_limit_ns = wait_limit_ns();
   a.stall_unit = test_stall_unit();
   a.box_rows = page_size % 64 == 0 ? 64 : (page_size % 32 == 0 ? 32 : 16);
-  if (!encode_bf16_map(&a.tm_k, k_pages, num_pages * Hkv, page_size, d, a.box_rows) ||
-      !encode_bf16_map(&a.tm_v, v_pages, num_pages * Hkv, page_size, d, a.box_rows) ||
-      !encode_bf16_map(&a.tm_k16, k_pages, num_pages * Hkv, page_size, d, 16) ||
-      !encode_bf16_map(&a.tm_v16, v_pages, num_pages * Hkv, page_size, d, 16))
+  const int page_heads = num_pages * Hkv;
+  const bool steps = fa::paged_uses_steps(Hq / Hkv, Nq);
+  if ((!steps || prefix_len > 0) && (!encode_bf16_map(&a.tm_k, k_pages, page_heads, page_size, d, a.box_rows) ||
+                                     !encode_bf16_map(&a.tm_v, v_pages, page_heads, page_size, d, a.box_rows)))
+    return FA_ERR_LAUNCH;
+  if (steps && (!encode_map(&a.st_k, MapKey{k_pages, 2, page_heads, page_size, d, 64, a.box_rows, true}) ||
+                !encode_map(&a.st_v, MapKey{v_pages, 2, page_heads, page_size, d, 64, a.box_rows, true}) ||
+                !encode_map(&a.st_k16, MapKey{k_pages, 2, page_heads, page_size, d, 64, 16, true}) ||
+                !encode_map(&a.st_v16, MapKey{v_pages, 2, page_heads, page_size, d, 64, 16, true})))
     return FA_ERR_LAUNCH;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (!workspace) {
-    if (cudaMallocAsync(reinterpret_cast<void**>(&a.part),
-                        sizeof(float) * fa::paged_workspace_floats(B, Hkv, Hq / Hkv, Nq, d, prefix_len > 0), s) != cudaSuccess)
+    cudaMemPool_t pool = workspace_pool();
+    const size_t bytes = sizeof(float) * fa::paged_workspace_floats(B, Hkv, Hq / Hkv, Nq, d, prefix_len > 0);
+    if (!pool || cudaMallocFromPoolAsync(reinterpret_cast<void**>(&a.part), bytes, pool, s) != cudaSuccess)
       return FA_ERR_LAUNCH;
   }
   cudaError_t e = fa::launch_paged(a, s);

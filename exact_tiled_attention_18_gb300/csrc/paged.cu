@@ -61,8 +61,9 @@ constexpr int step_ctas_per_sm() { return RB <= 1 ? 3 : 2; }
 // RB: blocks of 8 query rows.
 template <int D, int RB>
 struct StepLayout {
-  static constexpr int kBlock = kStepKeys * 128;        // 64 columns x 64 keys: 128-byte rows, swizzled
-  static constexpr int kHalf = (D / 64) * kBlock;       // K (or V) of a tile
+  // K (or V) of a tile: box by box, in a box its 64-column blocks, in a block
+  // one 128-byte row a key, swizzled
+  static constexpr int kHalf = (D / 64) * kStepKeys * 128;
   static constexpr int kStage = 2 * kHalf;
   static constexpr int kStages = (step_ctas_per_sm<RB>() == 3 ? 2 : 3) * (128 / D);
   // probabilities: hi then lo, [RB][64 keys][8 rows] bf16, so that eight keys
@@ -100,6 +101,14 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], 
 
 __device__ __forceinline__ void st_shared_u32(uint32_t addr, uint32_t v) {
   asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
+__device__ __forceinline__ void store_pair(float* p, float x, float y) {
+  *reinterpret_cast<float2*>(p) = make_float2(x, y);
+}
+
+__device__ __forceinline__ void store_pair(uint16_t* p, float x, float y) {
+  *reinterpret_cast<uint32_t*>(p) = pack_bf16x2(x, y);
 }
 
 // All four compute warps; true if every one of them passed true.
@@ -170,9 +179,9 @@ __global__ void __launch_bounds__(kStepThreads, step_ctas_per_sm<RB>())
   if (blockIdx.x == 0) {
     for (int i = threadIdx.x; i <= p.seq.B; i += kStepThreads) p.line_out[i] = line[i];
   }
-  const int per = tiles_per_cta(total, gridDim.x, p.part.min_tiles);
-  int at = min(static_cast<int>(blockIdx.x) * per, total);
-  const int stop = min(at + per, total);
+  const Ranges ranges = make_ranges(total, gridDim.x, p.part.min_tiles);
+  int at = range_start(ranges, blockIdx.x);
+  const int stop = range_start(ranges, blockIdx.x + 1);
   const WaitCtl wc{abort_flag, p.status, p.wait_limit_ns};
   const int unit = static_cast<int>(blockIdx.x);
   Walk w;
@@ -214,15 +223,15 @@ __global__ void __launch_bounds__(kStepThreads, step_ctas_per_sm<RB>())
         // rows behind its last key are read
         const bool tail = first + (t + 1) * kStepKeys > lk;
         const int rows_box = tail ? 16 : p.box_rows;
-        const int per_block = kStepKeys / rows_box;      // boxes a 64-column block
-        const int mine = lane / per_block;               // operand * CB + block
-        const int row = (lane - mine * per_block) * rows_box;
+        const int count = kStepKeys / rows_box;          // boxes an operand; one lane loads each
+        const int value = lane >= count;
+        const int row = (lane - value * count) * rows_box;
         const int page = __shfl_sync(0xffffffffu, cur, (t * boxes + row / p.box_rows) % 32);
         if (unit == p.stall_unit && issued == 0) continue;  // testing hook: leave this tile unloaded
         const uint32_t full = bars + 8 * s;
         if (lane == 0) mbar_arrive_expect_tx(full, L::kStage);
         __syncwarp();
-        if (mine < 2 * CB) {
+        if (lane < 2 * count) {
           const int key = first + t * kStepKeys + row;
           // rows of no page: a coordinate past the map, which reads zeros
           int outer = p.table.num_pages * p.seq.Hkv;
@@ -232,10 +241,9 @@ __global__ void __launch_bounds__(kStepThreads, step_ctas_per_sm<RB>())
             else
               record_bad_page(p.status, SITE_PAGE_READ, p.b0 + w.e, page);
           }
-          const int block = mine % CB;
-          const CUtensorMap* tm = mine < CB ? (tail ? &tm_k16 : &tm_k) : (tail ? &tm_v16 : &tm_v);
-          tma_load_3d(sbase + s * L::kStage + (mine / CB) * L::kHalf + block * L::kBlock + row * 128, tm, full,
-                      64 * block, key % p.table.page_size, outer);
+          const CUtensorMap* tm = value ? (tail ? &tm_v16 : &tm_v) : (tail ? &tm_k16 : &tm_k);
+          tma_load_4d(sbase + s * L::kStage + value * L::kHalf + row * (CB * 128), tm, full, 0,
+                      key % p.table.page_size, 0, outer);
         }
         __syncwarp();
       }
@@ -264,7 +272,7 @@ __global__ void __launch_bounds__(kStepThreads, step_ctas_per_sm<RB>())
   const int fc = (lane & 3) * 2;   // fragment columns: query rows fc, fc + 1 of a block
   const int rows = p.seq.G * p.seq.Nq;
   // ldmatrix lane addresses: K (16 keys x 16 columns), V and P transposed
-  const int k_row = 16 * warp + (lane & 15), k_half = lane >> 4;
+  const int k_row = lane & 15, k_half = lane >> 4;
   const int v_row = ((lane >> 4) << 3) + (lane & 7), v_half = (lane >> 3) & 1;
   const int v_col = warp * (D / 4);  // first value column of this warp
   const uint32_t p_hi = sbase + L::kPOff, p_lo = p_hi + RB * L::kPBlock;
@@ -274,14 +282,20 @@ __global__ void __launch_bounds__(kStepThreads, step_ctas_per_sm<RB>())
     const uint16_t* base = p.q + (static_cast<size_t>(x.e) * p.seq.Hkv + x.head) * rows * D + fc;
 #pragma unroll
     for (int m = 0; m < RB; ++m) {
-      const int r = 8 * m + fr;
+      const uint16_t* src = base + min(8 * m + fr, rows - 1) * D;  // rows of the block behind the last see no key
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) {
-        qf[m][ks][0] = r < rows ? __ldg(reinterpret_cast<const uint32_t*>(base + r * D + 16 * ks)) : 0u;
-        qf[m][ks][1] = r < rows ? __ldg(reinterpret_cast<const uint32_t*>(base + r * D + 16 * ks + 8)) : 0u;
+        qf[m][ks][0] = __ldg(reinterpret_cast<const uint32_t*>(src + 16 * ks));
+        qf[m][ks][1] = __ldg(reinterpret_cast<const uint32_t*>(src + 16 * ks + 8));
       }
     }
   };
+  int query[RB];  // query index of rows fc (low half) and fc + 1 of each block; past lq where there is no row
+#pragma unroll
+  for (int m = 0; m < RB; ++m) {
+    const int r = 8 * m + fc;
+    query[m] = (r < rows ? r % p.seq.Nq : 0x7fff) | (r + 1 < rows ? (r + 1) % p.seq.Nq : 0x7fff) << 16;
+  }
   if (more) load_q(w);
   int done = 0;
   bool ok = true;
@@ -293,9 +307,8 @@ __global__ void __launch_bounds__(kStepThreads, step_ctas_per_sm<RB>())
     for (int m = 0; m < RB; ++m) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int r = 8 * m + fc + e;
-        const int i = r % p.seq.Nq;
-        kend[m][e] = r < rows && i < lq ? (p.causal ? min(i + lk - lq + 1, lk) : lk) : 0;
+        const int i = (query[m] >> (16 * e)) & 0x7fff;
+        kend[m][e] = i < lq ? (p.causal ? min(i + lk - lq + 1, lk) : lk) : 0;
         m_ref[m][e] = -CUDART_INF_F;
         l[m][e] = 0.f;
       }
@@ -313,6 +326,10 @@ __global__ void __launch_bounds__(kStepThreads, step_ctas_per_sm<RB>())
       const uint32_t kb = sbase + s * L::kStage;
       const uint32_t vb = kb + L::kHalf;
       const int key0 = p.seq.prefix_len + t * kStepKeys;
+      // bytes of a 64-column block of a box; the 16 keys from 16 g on start at
+      // box (16 g / its rows), row (16 g modulo them)
+      const uint32_t block = (key0 + kStepKeys > lk ? 16 : p.box_rows) * 128;
+      auto keys_at = [&](int g) { return (g * 2048 & ~(block - 1)) * CB + (g * 2048 & (block - 1)); };
       // scores of this warp's 16 keys: keys fr (elements 0, 1) and fr + 8 (2, 3)
       float sc[RB][4];
 #pragma unroll
@@ -320,10 +337,11 @@ __global__ void __launch_bounds__(kStepThreads, step_ctas_per_sm<RB>())
 #pragma unroll
         for (int e = 0; e < 4; ++e) sc[m][e] = 0.f;
       if (__all_sync(0xffffffffu, full)) {
+        const uint32_t k16 = kb + keys_at(warp);
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
           uint32_t kf[4];
-          ldmatrix4(kf, kb + (ks >> 2) * L::kBlock + sw128(k_row, 2 * (ks & 3) + k_half));
+          ldmatrix4(kf, k16 + (ks >> 2) * block + sw128(k_row, 2 * (ks & 3) + k_half));
 #pragma unroll
           for (int m = 0; m < RB; ++m) mma_bf16(sc[m], kf, qf[m][ks][0], qf[m][ks][1]);
         }
@@ -333,8 +351,9 @@ __global__ void __launch_bounds__(kStepThreads, step_ctas_per_sm<RB>())
           // (whole boxes behind it were read as zeros)
           if ((lk - key0) / 16 == warp) {
             for (int i = lane; i < 16 * 8 * CB; i += 32) {
-              const int r = 16 * warp + (i & 15);
-              if (key0 + r >= lk) st_shared_v4(vb + (i >> 7) * L::kBlock + sw128(r, (i >> 4) & 7), 0u, 0u, 0u, 0u);
+              const int r = i & 15;
+              if (key0 + 16 * warp + r >= lk)
+                st_shared_v4(vb + keys_at(warp) + (i >> 7) * block + sw128(r, (i >> 4) & 7), 0u, 0u, 0u, 0u);
             }
           }
           fence_proxy_async_smem();  // before the slot's next TMA load
@@ -404,7 +423,7 @@ __global__ void __launch_bounds__(kStepThreads, step_ctas_per_sm<RB>())
 #pragma unroll
           for (int n = 0; n < MT; ++n) {
             const int chunk = v_col / 8 + 2 * n + v_half;  // 16-byte chunk of the head's row
-            ldmatrix4_t(vf[h][n], vb + (chunk >> 3) * L::kBlock + sw128(16 * (kk + h) + v_row, chunk & 7));
+            ldmatrix4_t(vf[h][n], vb + keys_at(kk + h) + (chunk >> 3) * block + sw128(v_row, chunk & 7));
           }
 #pragma unroll
         for (int m = 0; m < RB; ++m) {
@@ -443,47 +462,43 @@ __global__ void __launch_bounds__(kStepThreads, step_ctas_per_sm<RB>())
     const bool whole = p.direct && w.tile == 0 && w.end == w.tiles;
     const size_t slot = static_cast<size_t>(w.e) * p.seq.Hkv + w.head + blockIdx.x;
     const int odd = fr & 1;
+    auto write = [&](auto* dst, float* lse, const float unit) {  // rows of d outputs; log-sum-exps in units of ln 2
 #pragma unroll
-    for (int m = 0; m < RB; ++m) {
-      float scale[2], lse2[2];
+      for (int m = 0; m < RB; ++m) {
+        float2 sum = *reinterpret_cast<const float2*>(sums + 8 * m + fc);
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float sum = 0.f;
+        for (int o = 1; o < kStepWarps; ++o) {
+          const float2 y = *reinterpret_cast<const float2*>(sums + o * 8 * RB + 8 * m + fc);
+          sum.x += y.x;
+          sum.y += y.y;
+        }
+        const float s0 = sum.x > 0.f ? __fdividef(1.f, sum.x) : 0.f, s1 = sum.y > 0.f ? __fdividef(1.f, sum.y) : 0.f;
+        // neighbours in the column exchange rows: a lane then holds two
+        // adjacent columns of row fc (even columns' lanes) or fc + 1 (odd ones')
+        const int r = 8 * m + fc + odd;
+        const bool valid = r < rows;
 #pragma unroll
-        for (int o = 0; o < kStepWarps; ++o) sum += sums[o * 8 * RB + 8 * m + fc + e];
-        scale[e] = sum > 0.f ? 1.0f / sum : 0.f;
-        lse2[e] = sum > 0.f ? m_ref[m][e] + log2f(sum) : -CUDART_INF_F;
-      }
-      // neighbours in the column exchange rows: a lane then holds two adjacent
-      // columns of row fc (even columns' lanes) or fc + 1 (odd ones')
-      const int r = 8 * m + fc + odd;
-      float* dst_p = p.part.o + (slot * rows + r) * D;
+        for (int n = 0; n < MT; ++n) {
 #pragma unroll
-      for (int n = 0; n < MT; ++n) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float a = acc[m][n][2 * h] * scale[0], b = acc[m][n][2 * h + 1] * scale[1];
-          const float got = __shfl_xor_sync(0xffffffffu, odd ? a : b, 4);
-          const float x = odd ? got : a, y = odd ? b : got;
-          const int col = v_col + 16 * n + 8 * h + (fr & ~1);
-          if (r < rows) {
-            if (!whole)
-              *reinterpret_cast<float2*>(dst_p + col) = make_float2(x, y);
-            else if (p.o_bf16)
-              *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.o) + (row0 + r) * D + col) = pack_bf16x2(x, y);
-            else
-              *reinterpret_cast<float2*>(static_cast<float*>(p.o) + (row0 + r) * D + col) = make_float2(x, y);
+          for (int h = 0; h < 2; ++h) {
+            const float a = acc[m][n][2 * h] * s0, b = acc[m][n][2 * h + 1] * s1;
+            const float got = __shfl_xor_sync(0xffffffffu, odd ? a : b, 4);
+            const float x = odd ? got : a, y = odd ? b : got;
+            if (valid) store_pair(dst + r * D + v_col + 16 * n + 8 * h + (fr & ~1), x, y);
           }
         }
+        if (warp == 0 && fr < 2 && valid) {
+          const float total = odd ? sum.y : sum.x;
+          lse[r] = total > 0.f ? ((odd ? m_ref[m][1] : m_ref[m][0]) + __log2f(total)) * unit : -CUDART_INF_F;
+        }
       }
-      if (warp == 0 && fr < 2 && r < rows) {
-        const float v = odd ? lse2[1] : lse2[0];
-        if (whole)
-          p.lse[row0 + r] = v == -CUDART_INF_F ? v : v * kLn2;
-        else
-          p.part.lse[slot * rows + r] = v;
-      }
-    }
+    };
+    if (!whole)
+      write(p.part.o + slot * rows * D, p.part.lse + slot * rows, 1.f);
+    else if (p.o_bf16)
+      write(static_cast<uint16_t*>(p.o) + row0 * D, p.lse + row0, kLn2);
+    else
+      write(static_cast<float*>(p.o) + row0 * D, p.lse + row0, kLn2);
     w = after;
     at = after_at;
     more = another;
@@ -501,11 +516,15 @@ struct Pieces {
 // `tile`: the unit's first tile on the line; nt: its tiles; total: the line's.
 __device__ __forceinline__ Pieces pieces_on_line(const PartRef& r, int unit, int tile, int nt, int total) {
   Pieces x;
-  const int per = tiles_per_cta(total, r.ctas, r.min_tiles);
-  x.c0 = tile / per;
-  x.n = nt ? (tile + nt - 1) / per - x.c0 + 1 : 0;
   x.slot = unit;
-  x.first_whole = tile == x.c0 * per;
+  x.c0 = x.n = 0;
+  x.first_whole = false;
+  if (nt > 0) {
+    const Ranges ranges = make_ranges(total, r.ctas, r.min_tiles);
+    x.c0 = range_of(ranges, tile);
+    x.n = range_of(ranges, tile + nt - 1) - x.c0 + 1;
+    x.first_whole = tile == range_start(ranges, x.c0);
+  }
   return x;
 }
 
@@ -674,23 +693,25 @@ cudaError_t launch_steps(const PagedArgs& a, const PagedStep& p, int ctas, cudaS
   static std::atomic<unsigned long long> ready{0};
   cudaError_t e = setup_kernel_once(kern, L::kSmemBytes, 0, ready);
   if (e != cudaSuccess) return e;
-  return launch_overlapped(kern, dim3(ctas), kStepThreads, L::kSmemBytes, stream, a.tm_k, a.tm_v, a.tm_k16, a.tm_v16, p);
+  return launch_overlapped(kern, dim3(ctas), kStepThreads, L::kSmemBytes, stream, a.st_k, a.st_v, a.st_k16, a.st_v16, p);
 }
 
+// Warps a row: as many as the rows leave room for on the GPU at once, for the
+// rows with the most partial results are those of the smallest batches.  Where
+// most rows may have none (direct), launching the blocks counts as well.
 template <int D>
-cudaError_t launch_combine(const PagedCombine& p, bool tiles, cudaStream_t stream) {
+cudaError_t launch_combine(const PagedCombine& p, bool tiles, int sms, cudaStream_t stream) {
   constexpr int RPW = 4;
-  const long long units = p.units;
-  const long long rows = units * p.part.slot_rows;
-  const long long groups = units * ((p.part.slot_rows + RPW - 1) / RPW);
-  if (tiles)
-    return launch_overlapped(paged_combine_kernel<D, 1, RPW, true>, dim3(static_cast<unsigned>((groups + 7) / 8)), 256,
-                             0, stream, p);
-  if (rows <= 2048)  // few rows: eight warps a row, whose partial results then number the most
-    return launch_overlapped(paged_combine_kernel<D, 8, 1, false>, dim3(static_cast<unsigned>(rows)), 256, 0,
-                             stream, p);
-  return launch_overlapped(paged_combine_kernel<D, 1, RPW, false>, dim3(static_cast<unsigned>((groups + 7) / 8)), 256,
-                           0, stream, p);
+  const long long rows = static_cast<long long>(p.units) * p.part.slot_rows;
+  auto launch = [&](auto kern, long long items, int per_block) {
+    return launch_overlapped(kern, dim3(static_cast<unsigned>((items + per_block - 1) / per_block)), 256, 0, stream, p);
+  };
+  const long long groups = static_cast<long long>(p.units) * ((p.part.slot_rows + RPW - 1) / RPW);
+  if (tiles) return launch(paged_combine_kernel<D, 1, RPW, true>, groups, 8);
+  const long long room = (p.direct ? 4LL : 8LL) * sms;
+  if (rows <= room) return launch(paged_combine_kernel<D, 8, 1, false>, rows, 1);
+  if (rows <= 2 * room) return launch(paged_combine_kernel<D, 4, 1, false>, rows, 2);
+  return launch(paged_combine_kernel<D, 1, RPW, false>, groups, 8);
 }
 
 // How a call is divided, and where its partial results lie in the workspace
@@ -708,7 +729,7 @@ Plan make_plan(int B, int Hkv, int G, int Nq, int d, bool with_prefix) {
   Plan x;
   x.rows = G * Nq;
   x.pairs = (x.rows + kPairRows - 1) / kPairRows;
-  x.steps = x.rows <= kStepRows;
+  x.steps = paged_uses_steps(G, Nq);
   x.chunk = B < kLineSequences ? B : kLineSequences;
   if (x.steps)
     x.own_slots = static_cast<size_t>(x.chunk) * Hkv + kMaxCtas;
@@ -797,7 +818,7 @@ cudaError_t launch_paged_d(const PagedArgs& a, cudaStream_t stream) {
     c.units = c.direct ? t.part.cut : t.part.units;
     c.o = a.o;
     c.lse = a.lse;
-    return launch_combine<D>(c, true, stream);
+    return launch_combine<D>(c, true, a.sms, stream);
   }
   for (int b0 = 0; b0 < a.B; b0 += x.chunk) {
     const int n = a.B - b0 < x.chunk ? a.B - b0 : x.chunk;
@@ -836,13 +857,15 @@ cudaError_t launch_paged_d(const PagedArgs& a, cudaStream_t stream) {
     c.b0 = b0;
     c.o = p.o;
     c.lse = p.lse;
-    e = launch_combine<D>(c, false, stream);
+    e = launch_combine<D>(c, false, a.sms, stream);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
 }
 
 }  // namespace
+
+bool paged_uses_steps(int G, int Nq) { return static_cast<long long>(G) * Nq <= kStepRows; }
 
 size_t paged_workspace_floats(int B, int Hkv, int G, int Nq, int d, bool with_prefix) {
   return make_plan(B, Hkv, G, Nq, d, with_prefix).words;

@@ -112,9 +112,27 @@ __device__ __forceinline__ uint32_t sw128(int r, int c) {
   return static_cast<uint32_t>(r * 128 + ((c ^ (r & 7)) << 4));
 }
 
-// Tiles of the line that each CTA takes.
-__device__ __forceinline__ int tiles_per_cta(int total, int ctas, int least) {
-  return max((total + ctas - 1) / ctas, least);
+// The line's tiles in equal ranges, one a CTA (the first `more` CTAs have one
+// tile more than `base`), for no more CTAs than leave each `least` tiles.
+struct Ranges {
+  int base, more, total;
+};
+
+__device__ __forceinline__ Ranges make_ranges(int total, int ctas, int least) {
+  const int n = max(1, min(ctas, total / least));
+  const int base = total / n;
+  return Ranges{base, total - base * n, total};
+}
+
+__device__ __forceinline__ int range_start(const Ranges& r, int c) {
+  // (in 64 bits: c * base passes 2^31 for CTAs behind the last that has work)
+  return static_cast<int>(min(static_cast<long long>(c) * r.base + min(c, r.more), static_cast<long long>(r.total)));
+}
+
+// The CTA whose range holds a tile.
+__device__ __forceinline__ int range_of(const Ranges& r, int tile) {
+  const int longer = r.more * (r.base + 1);
+  return tile < longer ? tile / (r.base + 1) : r.more + (tile - longer) / r.base;
 }
 
 // line[e] = tiles of one key head of all entries before e, for e in

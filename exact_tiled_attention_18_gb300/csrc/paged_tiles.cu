@@ -192,7 +192,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) scratch[warp] = reach;
     __syncthreads();
     for (int i = 0; i < kThreads / 32; ++i) reach = max(reach, scratch[i]);
-    __syncthreads();
   }
   // sequence (0 for the prefix), key head and first row of unit u: groups of
   // `group` (sequence, head)s; in a group the row pairs from the last, which
@@ -227,7 +226,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     return (max(ka, kb) + kRows - 1) / kRows;
   };
   const int cut = p.part.cut;  // units of the line
-  build_line<kThreads>(line, scratch, cut, [&](int e) { return unit_tiles(e); });
+  if constexpr (PREFIX) {  // the same for every unit
+    const int n = (reach + kRows - 1) / kRows;
+    for (int i = threadIdx.x; i <= cut; i += kThreads) line[i] = i * n;
+    __syncthreads();
+  } else {
+    build_line<kThreads>(line, scratch, cut, [&](int e) { return unit_tiles(e); });
+  }
   const int total = line[cut];
   if (blockIdx.x == 0)
     for (int i = threadIdx.x; i <= cut; i += kThreads) p.line_out[i] = line[i];
@@ -239,9 +244,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   // A CTA's work: its range of the line (place x: from tile x on), then the
   // units it draws (place -1 - n: the n-th).
   volatile int* drawn = scratch + 14;
-  const int per = tiles_per_cta(total, gridDim.x, p.part.min_tiles);
-  const int at0 = min(static_cast<int>(blockIdx.x) * per, total);
-  const int stop = min(at0 + per, total);
+  const Ranges ranges = make_ranges(total, gridDim.x, p.part.min_tiles);
+  const int at0 = range_start(ranges, blockIdx.x);
+  const int stop = range_start(ranges, blockIdx.x + 1);
   int at = at0;
   struct Place {
     int u;           // unit

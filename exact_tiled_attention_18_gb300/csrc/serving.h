@@ -69,8 +69,9 @@ struct AppendArgs {
 };
 
 struct PagedArgs {
-  CUtensorMap tm_k, tm_v;     // 3-D maps over [num_pages * Hkv][page_size][d] bf16, boxes of 64 columns x box_rows
-  CUtensorMap tm_k16, tm_v16; // the same, boxes of 16 rows
+  CUtensorMap tm_k, tm_v;     // tile kernel: 3-D maps over [num_pages * Hkv][page_size][d], boxes 64 x box_rows
+  CUtensorMap st_k, st_v;     // step kernel: blocked maps of the same, boxes of box_rows whole rows
+  CUtensorMap st_k16, st_v16; // and of 16
   const uint16_t *q;          // [B][Hq][Nq][d]
   const uint16_t *k_pages, *v_pages;
   PageTable table;
@@ -94,6 +95,10 @@ struct PagedArgs {
 cudaError_t launch_rope(const RopeArgs& a, cudaStream_t stream);
 cudaError_t launch_kv_append(const AppendArgs& a, cudaStream_t stream);
 cudaError_t launch_paged(const PagedArgs& a, cudaStream_t stream);
+
+// Whether the sequences' own keys are the step kernel's work (few rows a key
+// head) or the tile kernel's.
+bool paged_uses_steps(int G, int Nq);
 
 // Workspace of launch_paged in 4-byte words.
 size_t paged_workspace_floats(int B, int Hkv, int G, int Nq, int d, bool with_prefix);
