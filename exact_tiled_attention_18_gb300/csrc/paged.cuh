@@ -14,7 +14,7 @@ constexpr int kLineWords = 528;        // 4-byte words of a line in the workspac
 constexpr int kMaxCtas = 512;
 constexpr int kMinSteps = 1;           // key tiles (64 keys) a CTA of the step kernel takes at least
 constexpr int kMinTiles = 2;           // key tiles (128 keys) a CTA of the tile kernel takes at least
-constexpr int kMaxTileCtas = 256;
+constexpr int kMaxTileCtas = 160;
 constexpr int kTileLine = 2 * kMaxTileCtas;  // units of the tile kernel's line
 constexpr int kPairRows = 256;         // query rows a unit of the tile kernel: two 128-row tiles
 static_assert(kLineWords >= kLineSequences + 1 && kLineWords >= kTileLine + 1 && kLineWords % 4 == 0, "the line's room");

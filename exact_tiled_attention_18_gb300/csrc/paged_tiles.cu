@@ -10,9 +10,8 @@
 //
 //  - Rows.  The G * Nq rows of a key head are one row space (or B * G * Nq for
 //    the prefix: the queries of every sequence side by side, which is what
-//    lets its keys be read once).  Rows are gathered from q by the softmax
-//    warps themselves with plain loads into the swizzled tile; each row has
-//    its own last visible key.
+//    lets its keys be read once).  A warp gathers them from q into the swizzled
+//    tiles, a piece ahead; each row has its own last visible key.
 //  - Keys come from pages: a tile of 128 keys is 128 / box_rows TMA boxes a
 //    64-column block, issued by the lanes of the producer warp, page ids read
 //    32 boxes ahead.
@@ -20,16 +19,18 @@
 //    CTA form a line of key tiles that is cut into equal ranges, one a CTA, as
 //    in the step kernel; the others are drawn whole from a counter, heaviest
 //    first within groups of heads whose keys stay in L2.  So few units fill
-//    the GPU, and many end together, on their lightest.  Pieces of a unit leave normalised outputs
-//    and log-sum-exps that paged_combine_kernel merges.
+//    the GPU, and many end together, on their lightest.  Pieces of a unit leave
+//    normalised outputs and log-sum-exps that paged_combine_kernel merges.  One
+//    warp works out what the next pieces are and the others read it, so that
+//    none of it stands between two pieces.
 //  - Rows of a page behind the last key may hold anything, NaN included, and
 //    0 * NaN would poison the product with V: a spare warp zeroes them in the
 //    last tile before that product is issued.
 //
 //   warps 0-3  softmax of tile A     warp 8   TMA producer
 //   warps 4-7  softmax of tile B     warp 9   MMA issuer, owns tensor memory
-//                                    warp 10  zeroes the values behind the last key
-//                                    warp 11  draws the whole units
+//                                    warp 10  gathers rows; zeroes values behind the last key
+//                                    warp 11  works out the pieces
 #include <cuda_runtime.h>
 #include <math_constants.h>
 
@@ -55,7 +56,7 @@ static_assert(2 * 128 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * kLaunchReg
 constexpr float kTau = 8.f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kRows = 128;        // rows and keys a tile
-constexpr int kUnitReaders = 11;  // warps that follow the drawn units: softmax, producer, issuer, cleaner
+constexpr int kReaders = 11;      // warps that follow the pieces: all but the one that works them out
 
 enum TileSite : int {
   SITE_TILE_LOAD = 75,
@@ -63,7 +64,18 @@ enum TileSite : int {
   SITE_TILE_S = 77,
   SITE_TILE_O = 78,
   SITE_TILE_CLEAN = 79,
-  SITE_TILE_UNIT = 80,
+  SITE_TILE_PIECE = 80,
+};
+
+// A piece of a unit, as the roles read it.
+struct Piece {
+  int na, nb;      // key tiles that row tiles A and B take; na < 0: there is no further piece
+  int tile;        // the unit's first of them
+  int limit;       // keys (from the origin) whose values are the sequence's own
+  int clean;       // the piece's tile that the limit falls into, or -1
+  int b, head, r0; // sequence, key head, first row
+  int whole;       // all of the unit, and its result is the row's
+  int slot;        // of the partial result
 };
 
 template <int D>
@@ -71,35 +83,34 @@ struct TileLayout {
   static constexpr int kTileBytes = kRows * D * 2;
   static constexpr int kSlots = (D == 128) ? 4 : 8;
   static constexpr int kRingOff = 2 * kTileBytes;
-  static constexpr int kBarOff = kRingOff + kSlots * kTileBytes;
+  // a warp's staging of its output rows: 32 rows of 64 bytes, so that rows
+  // leave in 64-byte runs instead of a 16-byte store a row
+  static constexpr int kStageOff = kRingOff + kSlots * kTileBytes;
+  static constexpr int kBarOff = kStageOff + 8 * 2048;
   static constexpr int KV_FULL = 0;
   static constexpr int KV_EMPTY = KV_FULL + kSlots;
   static constexpr int Q_FULL = KV_EMPTY + kSlots;
-  static constexpr int S_FULL = Q_FULL + 2;
+  static constexpr int Q_EMPTY = Q_FULL + 2;
+  static constexpr int S_FULL = Q_EMPTY + 2;
   static constexpr int P_FULL = S_FULL + 2;
   static constexpr int O_FULL = P_FULL + 2;
   static constexpr int DIRTY = O_FULL + 2;
   static constexpr int CLEAN = DIRTY + 1;
-  static constexpr int UNIT_FULL = CLEAN + 1;
-  static constexpr int UNIT_EMPTY = UNIT_FULL + 2;
-  static constexpr int DRAIN = UNIT_EMPTY + 2;
+  static constexpr int PIECE_FULL = CLEAN + 1;
+  static constexpr int PIECE_EMPTY = PIECE_FULL + 2;
+  static constexpr int ROWS_FULL = PIECE_EMPTY + 2;
+  static constexpr int DRAIN = ROWS_FULL + 2;
   static constexpr int kNumBars = DRAIN + 1;
   static constexpr int kMiscOff = kBarOff + kNumBars * 8;
-  static constexpr int kScratchOff = kMiscOff + 16;  // one word a warp, then the two drawn units
-  static constexpr int kLineOff = kScratchOff + 64;
+  static constexpr int kScratchOff = kMiscOff + 16;            // one word a warp
+  static constexpr int kPieceOff = kScratchOff + 64;           // two pieces
+  static constexpr int kRowOff = kPieceOff + 2 * 48;           // [2 pieces][256 rows] place in q and o, then last key
+  static constexpr int kLineOff = kRowOff + 2 * kPairRows * 8;
   static constexpr int kSmemBytes = kLineOff + (kTileLine + 1) * 4 + 1024;
   static constexpr uint32_t kColO = 256;
 };
+static_assert(sizeof(Piece) <= 48, "a piece's room");
 
-// One piece of a unit: how many key tiles of it each row tile needs.
-struct Piece {
-  int na, nb;     // key tiles from w.tile on
-  int nmax;
-  int limit;      // first key (from the origin) whose values may be anything
-  int clean;      // piece tile that holds it, or -1
-};
-
-// Row space of a unit: rows [256 pair, 256 pair + 256) of `total`.
 __device__ __forceinline__ bool tile_wait(uint32_t bar, uint32_t parity, const WaitCtl& w, int site, int unit) {
   return __all_sync(0xffffffffu, wait_bounded(bar, parity, w, site, unit));
 }
@@ -155,7 +166,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bars + 8 * (L::KV_EMPTY + s), 1);
     }
     for (int t = 0; t < 2; ++t) {
-      mbar_init(bars + 8 * (L::Q_FULL + t), 4);
+      mbar_init(bars + 8 * (L::Q_FULL + t), 1);
+      mbar_init(bars + 8 * (L::Q_EMPTY + t), 1);
       mbar_init(bars + 8 * (L::S_FULL + t), 1);
       mbar_init(bars + 8 * (L::P_FULL + t), 4);
       mbar_init(bars + 8 * (L::O_FULL + t), 1);
@@ -163,8 +175,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(bars + 8 * L::DIRTY, 1);
     mbar_init(bars + 8 * L::CLEAN, 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(bars + 8 * (L::UNIT_FULL + i), 1);
-      mbar_init(bars + 8 * (L::UNIT_EMPTY + i), kUnitReaders);
+      mbar_init(bars + 8 * (L::PIECE_FULL + i), 1);
+      mbar_init(bars + 8 * (L::PIECE_EMPTY + i), kReaders);
+      mbar_init(bars + 8 * (L::ROWS_FULL + i), 1);
     }
     mbar_init(bars + 8 * L::DRAIN, 1);
     *abort_flag = 0;
@@ -241,81 +254,23 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   auto BAR = [&](int i) -> uint32_t { return bars + 8u * static_cast<uint32_t>(i); };
-  // A CTA's work: its range of the line (place x: from tile x on), then the
-  // units it draws (place -1 - n: the n-th).
-  volatile int* drawn = scratch + 14;
-  const Ranges ranges = make_ranges(total, gridDim.x, p.part.min_tiles);
-  const int at0 = range_start(ranges, blockIdx.x);
-  const int stop = range_start(ranges, blockIdx.x + 1);
-  int at = at0;
-  struct Place {
-    int u;           // unit
-    int tile, end;   // its tiles in this piece: [tile, end)
-    bool whole;      // all of the unit's
-  };
-  auto locate = [&](int place) {
-    Place w;
-    if (place < 0) {
-      w.u = drawn[(-1 - place) & 1];
-      w.tile = 0;
-      w.end = unit_tiles(w.u);
-      w.whole = true;
-      return w;
-    }
-    // the last unit that starts at or before the tile (one with tiles: an
-    // empty one starts where its successor does)
-    int lo = 0, hi = cut - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (line[mid] <= place) lo = mid; else hi = mid - 1;
-    }
-    w.u = lo;
-    w.tile = place - line[lo];
-    const int tiles = line[lo + 1] - line[lo];
-    w.end = min(tiles, w.tile + stop - place);
-    w.whole = w.tile == 0 && w.end == tiles;
-    return w;
-  };
   const WaitCtl wc{abort_flag, p.status, p.wait_limit_ns};
-  // A row tile without keys in a piece, and the cleaner, wait while the other
-  // tile's whole pieces go by: their limit grows with the range.  The producer
-  // and the issuer notice a stall within the limit itself and end all waits.
+  // A row tile without keys in a piece, and the spare warps, wait while whole
+  // pieces go by: their limit is longer.  The producer and the issuer notice a
+  // stall within the limit itself and end all waits.
   const WaitCtl wc_idle{abort_flag, p.status, p.wait_limit_ns * 64};
-
-  // Every role that follows the work calls this before a piece, with all lanes
-  // of its warp (`true`: there is one), and done() behind it.
-  auto another = [&](bool& ok) {
-    if (at >= 0) {
-      if (at < stop) return true;
-      if (cut == p.part.units) return false;
-      at = -1;
-    }
-    const int n = -1 - at;
-    ok = tile_wait(BAR(L::UNIT_FULL + (n & 1)), (n >> 1) & 1, wc_idle, SITE_TILE_UNIT, at);
-    return ok && drawn[n & 1] < p.part.units;
+  const volatile Piece* pieces = reinterpret_cast<const volatile Piece*>(smem + L::kPieceOff);
+  static_assert(sizeof(Piece) == 40, "pieces lie 40 bytes apart");
+  const volatile uint32_t* row_at = reinterpret_cast<const volatile uint32_t*>(smem + L::kRowOff);
+  const volatile int* row_end = reinterpret_cast<const volatile int*>(smem + L::kRowOff + 2 * kPairRows * 4);
+  constexpr uint32_t kNoRow = 0xffffffffu;
+  // Every role but warp 11 calls this before its n-th piece, with all lanes of
+  // its warp (false: none left, or a wait ran out), and piece_done behind it.
+  auto next_piece = [&](uint32_t n, bool& ok) {
+    ok = tile_wait(BAR(L::PIECE_FULL + (n & 1)), (n >> 1) & 1, wc_idle, SITE_TILE_PIECE, n);
+    return ok && pieces[n & 1].na >= 0;
   };
-  auto done = [&](int tiles) {
-    if (at < 0) {
-      mbar_arrive_warp(BAR(L::UNIT_EMPTY + ((-1 - at) & 1)));
-      --at;
-    } else {
-      at += tiles;
-    }
-  };
-
-  auto piece_of = [&](const Place& w, int& b, int& head, int& r0) {
-    Piece x;
-    unit_at(w.u, b, head, r0);
-    int ka, kb;
-    unit_keys(b, r0, ka, kb, x.limit);
-    const int len = w.end - w.tile;
-    x.na = max(0, min((ka + kRows - 1) / kRows - w.tile, len));
-    x.nb = max(0, min((kb + kRows - 1) / kRows - w.tile, len));
-    x.nmax = max(x.na, x.nb);
-    const int at_tile = x.limit / kRows - w.tile;
-    x.clean = x.limit % p.box_rows != 0 && at_tile >= 0 && at_tile < x.nmax ? at_tile : -1;
-    return x;
-  };
+  auto piece_done = [&](uint32_t n) { mbar_arrive_warp(BAR(L::PIECE_EMPTY + (n & 1))); };
 
   if (warp < 8) {
     // ------------------------------------------------------------ softmax
@@ -326,62 +281,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tS = tmem + lane_off + static_cast<uint32_t>(t * 128);
     const uint32_t tO = tmem + lane_off + L::kColO + static_cast<uint32_t>(t * D);
     const float scale_log2 = p.scale_log2;
-    // A row's whole register budget is its 128 scores, so a piece is described
-    // by its place `at` on the line alone; the rest is worked out again from
-    // shared memory before and after the sweep.
-    auto row_of = [&](int b, int r0, int& rb, int& rr) {  // sequence and row of this thread's row; false: none
-      const int row = r0 + t * kRows + r;
-      rb = PREFIX ? row / rows : b;
-      rr = PREFIX ? row - rb * rows : row;
-      return row < space;
-    };
     uint32_t sn = 0, on = 0;
     bool ok = true;
-    while (another(ok)) {
-      int nt, lim0 = 0;  // key tiles; this row's visible keys from the piece's first
-      {
-        int b, head, r0, rb, rr;
-        const Place w = locate(at);
-        const Piece x = piece_of(w, b, head, r0);
-        nt = t ? x.nb : x.na;
-        unsigned long long grow = 0;
-        const bool valid = row_of(b, r0, rb, rr);
-        if (valid) {
-          const int i = rr % p.seq.Nq;
-          int lq, lk;
-          seq_lens(p.seq, rb, lq, lk);
-          if (i < lq) lim0 = (p.causal ? min(i + lk - lq + 1, lk) : lk) - origin;
-          if (PREFIX) lim0 = min(lim0, p.seq.prefix_len);
-          lim0 -= w.tile * kRows;
-          grow = (static_cast<unsigned long long>(rb) * Hkv + head) * rows + rr;
-        }
-        if (nt > 0) {
-          // gather the tile's 128 rows: a warp its 32, whole rows at a time.
-          // The tile is free: its last product completed before O was read.
-          constexpr int LPR = D / 8;            // lanes a row, 16 bytes each
-          constexpr int RPI = 32 / LPR;         // rows an iteration
-          const int chunk = lane % LPR;
-          const uint32_t qt = sbase + t * L::kTileBytes + (chunk >> 3) * 16384;
-          uint4 v[32 / RPI];
-#pragma unroll
-          for (int k = 0; k < 32 / RPI; ++k) {
-            const int src = k * RPI + lane / LPR;   // lane of the warp that owns the row
-            const unsigned long long g = __shfl_sync(0xffffffffu, grow, src);
-            const int live = __shfl_sync(0xffffffffu, static_cast<int>(valid), src);
-            v[k] = live ? __ldg(reinterpret_cast<const uint4*>(p.q + g * D) + chunk) : make_uint4(0u, 0u, 0u, 0u);
-          }
-#pragma unroll
-          for (int k = 0; k < 32 / RPI; ++k) {
-            const int rr2 = ((warp & 3) << 5) + k * RPI + lane / LPR;
-            st_shared_v4(qt + sw128(rr2, chunk & 7), v[k].x, v[k].y, v[k].z, v[k].w);
-          }
-          fence_proxy_async_smem();
-          mbar_arrive_warp(BAR(L::Q_FULL + t));
-        }
-      }
+    for (uint32_t n = 0; next_piece(n, ok); ++n) {
+      ok = tile_wait(BAR(L::ROWS_FULL + (n & 1)), (n >> 1) & 1, wc_idle, SITE_TILE_PIECE, n);
+      if (!ok) break;
+      const int nt = t ? pieces[n & 1].nb : pieces[n & 1].na;
+      // this row's visible keys from the piece's first
+      const int lim0 = row_end[(n & 1) * kPairRows + t * kRows + r];
       float m_ref = 0.f, l = 0.f, dl = 0.f;
       for (int j = 0; j < nt; ++j) {
-        ok = tile_wait(BAR(L::S_FULL + t), sn & 1, wc_idle, SITE_TILE_S, at);
+        ok = tile_wait(BAR(L::S_FULL + t), sn & 1, wc_idle, SITE_TILE_S, n);
         if (!ok) break;
         ++sn;
         tc_fence_after();
@@ -470,65 +380,75 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       if (nt > 0) {
-        ok = tile_wait(BAR(L::O_FULL + t), on & 1, wc, SITE_TILE_O, at);
+        ok = tile_wait(BAR(L::O_FULL + t), on & 1, wc, SITE_TILE_O, n);
         if (!ok) break;
         ++on;
         tc_fence_after();
       }
+      // rows leave through the warp's staging area, 64 bytes at a time: each
+      // lane writes a run of its own row there, then the lanes take the runs
+      // of eight rows at once (a tile without keys reads what was left in
+      // tensor memory, and drops it)
       const bool live = l > 0.f;
       const float inv = live ? 1.0f / (l + dl) : 0.f;
-      int b, head, r0, rb, rr;
-      const Place w = locate(at);
-      unit_at(w.u, b, head, r0);
-      const bool valid = row_of(b, r0, rb, rr);
-      const bool whole = p.direct && w.whole;
-      const size_t grow = (static_cast<size_t>(rb) * Hkv + head) * rows + rr;
-      const long long slot = p.part.two_a_cta ? 2LL * blockIdx.x + (at == at0 ? 0 : 1)
-                                              : static_cast<long long>(w.u) + (at < 0 ? gridDim.x : blockIdx.x);
-      const long long prow = slot * kPairRows + t * kRows + r;
-      float* dst = whole ? static_cast<float*>(p.o) + grow * D : p.part.o + prow * D;
+      const bool whole = pieces[n & 1].whole;
       const bool half = whole && p.o_bf16;
-      uint16_t* dst_h = static_cast<uint16_t*>(p.o) + grow * D;
+      const long long prow0 = static_cast<long long>(pieces[n & 1].slot) * kPairRows + t * kRows + (r - lane);
+      const volatile uint32_t* at = row_at + (n & 1) * kPairRows + t * kRows + (r - lane);
+      const uint32_t stage = sbase + L::kStageOff + warp * 2048;
+      const uint32_t put = stage + lane * 64, put_x = (lane >> 1) & 3;
+      const int from = lane >> 2, run = lane & 3;  // read: rows from, from + 8, ..., 16 bytes each
+      uint8_t* dst[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t g = at[8 * k + from];
+        uint8_t* base = whole ? static_cast<uint8_t*>(p.o) + static_cast<size_t>(g) * D * (half ? 2 : 4)
+                              : reinterpret_cast<uint8_t*>(p.part.o + (prow0 + 8 * k + from) * D);
+        dst[k] = g == kNoRow ? nullptr : base + 16 * run;
+      }
+      const int runs = half ? D / 32 : D / 16;
 #pragma unroll 1
-      for (int c = 0; c < D / 32; ++c) {
-        uint32_t v[32];
-        // (a tile without keys reads what was left there, and drops it)
-        tmem_ld32(tO + 32 * c, v);
-        tmem_ld_wait();
+      for (int c = 0; c < runs; ++c) {
+        uint32_t w[16];
+        if (half) {
+          uint32_t v[32];
+          tmem_ld32(tO + 32 * c, v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            w[i] = pack_bf16x2(__uint_as_float(v[2 * i]) * inv, __uint_as_float(v[2 * i + 1]) * inv);
+        } else {
+          tmem_ld16(tO + 16 * c, w);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) * inv);
+        }
         if (!live) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = 0u;
+          for (int i = 0; i < 16; ++i) w[i] = 0u;
         }
-        if (valid && half) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint4 h;
-            h.x = pack_bf16x2(__uint_as_float(v[8 * i + 0]) * inv, __uint_as_float(v[8 * i + 1]) * inv);
-            h.y = pack_bf16x2(__uint_as_float(v[8 * i + 2]) * inv, __uint_as_float(v[8 * i + 3]) * inv);
-            h.z = pack_bf16x2(__uint_as_float(v[8 * i + 4]) * inv, __uint_as_float(v[8 * i + 5]) * inv);
-            h.w = pack_bf16x2(__uint_as_float(v[8 * i + 6]) * inv, __uint_as_float(v[8 * i + 7]) * inv);
-            *reinterpret_cast<uint4*>(dst_h + 32 * c + 8 * i) = h;
-          }
-        } else if (valid) {
+        for (int i = 0; i < 4; ++i)
+          st_shared_v4(put + ((i ^ put_x) << 4), w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+        __syncwarp();
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            float4 f;
-            f.x = __uint_as_float(v[4 * i + 0]) * inv;
-            f.y = __uint_as_float(v[4 * i + 1]) * inv;
-            f.z = __uint_as_float(v[4 * i + 2]) * inv;
-            f.w = __uint_as_float(v[4 * i + 3]) * inv;
-            *reinterpret_cast<float4*>(dst + 32 * c + 4 * i) = f;
-          }
+        for (int k = 0; k < 4; ++k) {
+          uint32_t x[4];
+          const int row = 8 * k + from;
+          ld_shared_v4(stage + row * 64 + ((run ^ ((row >> 1) & 3)) << 4), x);
+          if (dst[k]) *reinterpret_cast<uint4*>(dst[k] + 64 * c) = make_uint4(x[0], x[1], x[2], x[3]);
         }
+        __syncwarp();
       }
-      if (valid) {
+      const uint32_t mine = at[lane];
+      if (mine != kNoRow) {
         const float lse2 = live ? m_ref + log2f(l) : -CUDART_INF_F;
         if (whole)
-          p.lse[grow] = live ? lse2 * kLn2 : -CUDART_INF_F;
+          p.lse[mine] = live ? lse2 * kLn2 : -CUDART_INF_F;
         else
-          p.part.lse[prow] = lse2;
+          p.part.lse[prow0 + lane] = lse2;
       }
-      done(w.end - w.tile);
+      piece_done(n);
     }
   } else {
     regs_decrease<kOtherRegs>();
@@ -540,22 +460,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t offset = static_cast<uint32_t>(block * 16384 + box * p.box_rows * 128);
       const uint64_t policy = l2_policy_evict_last();
       uint32_t kvpos = 0;
-      int piece = 0;
       bool ok = true;
-      while (another(ok)) {
-        int b, head, r0;
-        const Place w = locate(at);
-        const Piece x = piece_of(w, b, head, r0);
+      for (uint32_t n = 0; next_piece(n, ok); ++n) {
+        const volatile Piece& x = pieces[n & 1];
+        const int head = x.head, b = x.b, tiles = max(x.na, x.nb);
         const int* pages = PREFIX ? p.prefix_table : p.table.block_table + b * p.table.table_stride;
-        const int first = origin + w.tile * kRows;
+        const int first = origin + x.tile * kRows;
         const int last = origin + x.limit;
-        const int count = x.nmax * boxes;
+        const int count = tiles * boxes;
         auto page_of = [&](int i) {
           const int key = first + i * p.box_rows;
           return i < count && key < last ? __ldg(pages + key / p.table.page_size) : -1;
         };
         int cur = page_of(lane), next = page_of(32 + lane);
-        for (int j = 0; j < x.nmax && ok; ++j) {
+        for (int j = 0; j < tiles && ok; ++j) {
           if (j > 0 && (j * boxes) % 32 == 0) {
             cur = next;
             next = page_of(j * boxes + 32 + lane);
@@ -573,10 +491,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
           for (int kv = 0; kv < 2; ++kv) {
             const uint32_t s = kvpos % S, use = kvpos / S;
-            ok = tile_wait(BAR(L::KV_EMPTY + s), (use & 1) ^ 1, wc, SITE_TILE_LOAD, at);
+            ok = tile_wait(BAR(L::KV_EMPTY + s), (use & 1) ^ 1, wc, SITE_TILE_LOAD, n);
             if (!ok) break;
             ++kvpos;
-            if (blockIdx.x == 0 && piece == p.stall_unit && j == 0 && kv == 0)
+            if (blockIdx.x == 0 && static_cast<int>(n) == p.stall_unit && j == 0 && kv == 0)
               continue;  // testing hook: leave this tile unloaded
             if (lane == 0) mbar_arrive_expect_tx(BAR(L::KV_FULL + s), L::kTileBytes);
             __syncwarp();
@@ -587,8 +505,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (!ok) break;
-        ++piece;
-        done(w.end - w.tile);
+        piece_done(n);
       }
       if (!ok && lane == 0) {
         for (uint32_t s = 0; s < static_cast<uint32_t>(S); ++s) {
@@ -626,15 +543,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         uint32_t qa = 0, qb = 0, kvbase = 0, pa = 0, pb = 0, cleaned = 0;
         bool ok = true;
-        while (another(ok)) {
-          int b, head, r0;
-          const Place w = locate(at);
-          const Piece x = piece_of(w, b, head, r0);
-          const int unit = at;
-          const int na = x.na, nb = x.nb;
+        for (uint32_t n = 0; next_piece(n, ok); ++n) {
+          const int unit = static_cast<int>(n);
+          const int na = pieces[n & 1].na, nb = pieces[n & 1].nb, clean = pieces[n & 1].clean;
+          const int tiles = max(na, nb);
           if (lane == 0) {
           do {
-          if (x.nmax > 0) {
+          if (tiles > 0) {
             ok = wait_bounded(BAR(L::KV_FULL + kvbase % S), (kvbase / S) & 1, wc, SITE_TILE_MMA, unit);
             if (!ok) break;
             if (na > 0) {
@@ -644,6 +559,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               tc_fence_after();
               issue_s(0, kvbase % S);
               umma_commit(BAR(L::S_FULL + 0));
+              if (na == 1) umma_commit(BAR(L::Q_EMPTY + 0));  // the piece's last use of Q
             }
             if (nb > 0) {
               ok = wait_bounded(BAR(L::Q_FULL + 1), qb & 1, wc, SITE_TILE_MMA, unit);
@@ -652,18 +568,18 @@ __global__ void __launch_bounds__(kThreads, 1)
               tc_fence_after();
               issue_s(1, kvbase % S);
               umma_commit(BAR(L::S_FULL + 1));
+              if (nb == 1) umma_commit(BAR(L::Q_EMPTY + 1));
             }
           }
-          // One key tile.  STEADY: both row tiles have it and the next one, and
-          // its values need no zeroing -- all but the last steps of most
-          // pieces, with nothing to decide in them: this thread's instructions
+          // One key tile.  STEADY: both row tiles have it and two more, and its
+          // values need no zeroing -- all but the last steps of most pieces, with nothing to decide in them: this thread's instructions
           // are on every step's critical path.
           auto step = [&](auto steady_tag, int j) -> bool {
             constexpr bool STEADY = decltype(steady_tag)::value;
             const uint32_t kpos = kvbase + 2 * j, vpos = kpos + 1, knext = kpos + 2;
             const bool has_a = STEADY || j < na, next_a = STEADY || j + 1 < na;
             const bool has_b = STEADY || j < nb, next_b = STEADY || j + 1 < nb;
-            const bool dirty = !STEADY && j == x.clean;
+            const bool dirty = !STEADY && j == clean;
             umma_commit(BAR(L::KV_EMPTY + kpos % S));  // K_j is free once S(j) of both tiles completes
             if (!wait_bounded(BAR(L::KV_FULL + vpos % S), (vpos / S) & 1, wc, SITE_TILE_MMA, unit)) return false;
             // the last keys' values: zeroed behind the last key by warp 10
@@ -683,6 +599,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_after();
                 issue_s(0, knext % S);
                 umma_commit(BAR(L::S_FULL + 0));
+                if (!STEADY && j + 2 == na) umma_commit(BAR(L::Q_EMPTY + 0));
               }
             }
             if (has_b) {
@@ -701,18 +618,19 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
               issue_s(1, knext % S);
               umma_commit(BAR(L::S_FULL + 1));
+              if (!STEADY && j + 2 == nb) umma_commit(BAR(L::Q_EMPTY + 1));
             }
             return true;
           };
-          const int both = min(na, nb) - 1;
-          for (int j = 0; j < x.nmax && ok; ++j)
-            ok = j < both && j != x.clean ? step(std::true_type{}, j) : step(std::false_type{}, j);
+          const int steady = min(na, nb) - 2;
+          for (int j = 0; j < tiles && ok; ++j)
+            ok = j < steady && j != clean ? step(std::true_type{}, j) : step(std::false_type{}, j);
           } while (false);
           }
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
-          kvbase += 2 * x.nmax;
-          done(w.end - w.tile);
+          kvbase += 2 * tiles;
+          piece_done(n);
         }
         // every MMA this thread issued completes before tensor memory is freed
         if (lane == 0) {
@@ -721,20 +639,60 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     } else if (warp == 10) {
-      // ------------------------------------------- values behind the last key
-      uint32_t kvbase = 0, cleaned = 0;
+      // ------------------------------ rows in, and values behind the last key
+      volatile uint32_t* at_w = const_cast<volatile uint32_t*>(row_at);
+      volatile int* end_w = const_cast<volatile int*>(row_end);
+      uint32_t kvbase = 0, cleaned = 0, qn[2] = {0, 0};
       bool ok = true;
-      while (another(ok)) {
-        int b, head, r0;
-        const Place w = locate(at);
-        const Piece x = piece_of(w, b, head, r0);
-        const int unit = at;
-        if (x.clean >= 0) {
-          const uint32_t vpos = kvbase + 2 * x.clean + 1;
-          ok = tile_wait(BAR(L::DIRTY), cleaned & 1, wc_idle, SITE_TILE_CLEAN, unit);
+      for (uint32_t n = 0; next_piece(n, ok); ++n) {
+        const volatile Piece& x = pieces[n & 1];
+        const int r0 = x.r0, head = x.head, tile0 = x.tile * kRows, clean = x.clean, limit = x.limit;
+        const int nt[2] = {x.na, x.nb};
+        const int buf = (n & 1) * kPairRows;
+        for (int i = lane; i < kPairRows; i += 32) {
+          const int row = r0 + i;
+          uint32_t at = kNoRow;
+          int end = 0;
+          if (row < space) {
+            const int rb = PREFIX ? row / rows : x.b;
+            const int rr = PREFIX ? row - rb * rows : row;
+            const int qi = rr % p.seq.Nq;
+            int lq, lk;
+            seq_lens(p.seq, rb, lq, lk);
+            if (qi < lq) end = (p.causal ? min(qi + lk - lq + 1, lk) : lk) - origin;
+            if (PREFIX) end = min(end, p.seq.prefix_len);
+            at = (static_cast<uint32_t>(rb) * Hkv + head) * rows + rr;
+          }
+          at_w[buf + i] = at;
+          end_w[buf + i] = end - tile0;
+        }
+        mbar_arrive_warp(BAR(L::ROWS_FULL + (n & 1)));
+        constexpr int LPR = D / 8;     // lanes a row, 16 bytes each
+        const int chunk = lane % LPR;
+        for (int t = 0; t < 2 && ok; ++t) {
+          if (nt[t] == 0) continue;
+          ok = tile_wait(BAR(L::Q_EMPTY + t), (qn[t] & 1) ^ 1, wc_idle, SITE_TILE_PIECE, n);
+          if (!ok) break;
+          ++qn[t];
+          const uint32_t qt = sbase + t * L::kTileBytes + (chunk >> 3) * 16384;
+#pragma unroll 8
+          for (int i = lane / LPR; i < kRows; i += 32 / LPR) {
+            const uint32_t at = row_at[buf + t * kRows + i];
+            const bool live = at != kNoRow;
+            cp_async16(qt + sw128(i, chunk & 7), p.q + (live ? static_cast<size_t>(at) * D + chunk * 8 : 0),
+                       live ? 16u : 0u);
+          }
+          cp_async_wait();
+          fence_proxy_async_smem();
+          mbar_arrive_warp(BAR(L::Q_FULL + t));
+        }
+        if (!ok) break;
+        if (clean >= 0) {
+          const uint32_t vpos = kvbase + 2 * clean + 1;
+          ok = tile_wait(BAR(L::DIRTY), cleaned & 1, wc_idle, SITE_TILE_CLEAN, n);
           if (!ok) break;
           // the rest of the last key's box; whole boxes behind it were read as zeros
-          const int from = x.limit % kRows, rest = p.box_rows - from % p.box_rows;
+          const int from = limit % kRows, rest = p.box_rows - from % p.box_rows;
           const uint32_t vt = sbase + L::kRingOff + (vpos % S) * L::kTileBytes;
           for (int i = lane; i < rest * (D / 8); i += 32) {
             const int row = from + i / (D / 8), c = i % (D / 8);
@@ -744,18 +702,57 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive_warp(BAR(L::CLEAN));
           ++cleaned;
         }
-        kvbase += 2 * x.nmax;
-        done(w.end - w.tile);
+        kvbase += 2 * max(nt[0], nt[1]);
+        piece_done(n);
       }
-    } else if (lane == 0 && cut < p.part.units) {
-      // ------------------------------------------------------ whole units
-      // drawn two ahead: the draw's latency passes behind the work before
-      for (int n = 0;; ++n) {
-        if (!wait_bounded(BAR(L::UNIT_EMPTY + (n & 1)), ((n >> 1) & 1) ^ 1, wc_idle, SITE_TILE_UNIT, n)) break;
-        const int u = cut + atomicAdd(p.counter, 1);
-        drawn[n & 1] = u;
-        mbar_arrive(BAR(L::UNIT_FULL + (n & 1)));
-        if (u >= p.part.units) break;
+    } else {
+      // ------------------------------------------------------------- pieces
+      const Ranges ranges = make_ranges(total, gridDim.x, p.part.min_tiles);
+      const int at0 = range_start(ranges, blockIdx.x), stop = range_start(ranges, blockIdx.x + 1);
+      int at = at0;  // on the line; then units are drawn
+      for (uint32_t n = 0;; ++n) {
+        if (!tile_wait(BAR(L::PIECE_EMPTY + (n & 1)), ((n >> 1) & 1) ^ 1, wc_idle, SITE_TILE_PIECE, n)) break;
+        int u = -1, len = 0;
+        Piece x{};
+        x.na = -1;
+        if (at < stop) {
+          // the last unit that starts at or before the tile (one with tiles:
+          // an empty one starts where its successor does)
+          int lo = 0, hi = cut - 1;
+          while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (line[mid] <= at) lo = mid; else hi = mid - 1;
+          }
+          u = lo;
+          x.tile = at - line[lo];
+          const int tiles = line[lo + 1] - line[lo];
+          len = min(tiles - x.tile, stop - at);
+          x.whole = p.direct && len == tiles;
+          x.slot = p.part.two_a_cta ? 2 * blockIdx.x + (at == at0 ? 0 : 1) : u + blockIdx.x;
+          at += len;
+        } else if (cut < p.part.units) {
+          if (lane == 0) u = cut + atomicAdd(p.counter, 1);
+          u = __shfl_sync(0xffffffffu, u, 0);
+          if (u < p.part.units) {
+            len = unit_tiles(u);
+            x.whole = p.direct;
+            x.slot = u + gridDim.x;
+          } else {
+            u = -1;
+          }
+        }
+        if (u >= 0) {
+          int ka, kb;
+          unit_at(u, x.b, x.head, x.r0);
+          unit_keys(x.b, x.r0, ka, kb, x.limit);
+          x.na = max(0, min((ka + kRows - 1) / kRows - x.tile, len));
+          x.nb = max(0, min((kb + kRows - 1) / kRows - x.tile, len));
+          const int at_tile = x.limit / kRows - x.tile;
+          x.clean = x.limit % p.box_rows != 0 && at_tile >= 0 && at_tile < max(x.na, x.nb) ? at_tile : -1;
+        }
+        if (lane == 0) *reinterpret_cast<Piece*>(smem + L::kPieceOff + (n & 1) * sizeof(Piece)) = x;
+        mbar_arrive_warp(BAR(L::PIECE_FULL + (n & 1)));
+        if (u < 0) break;
       }
     }
   }
