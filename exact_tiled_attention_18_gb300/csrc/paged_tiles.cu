@@ -431,13 +431,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < 4; ++i)
           st_shared_v4(put + ((i ^ put_x) << 4), w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
         __syncwarp();
+        uint32_t x[4][4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          uint32_t x[4];
           const int row = 8 * k + from;
-          ld_shared_v4(stage + row * 64 + ((run ^ ((row >> 1) & 3)) << 4), x);
-          if (dst[k]) *reinterpret_cast<uint4*>(dst[k] + 64 * c) = make_uint4(x[0], x[1], x[2], x[3]);
+          ld_shared_v4(stage + row * 64 + ((run ^ ((row >> 1) & 3)) << 4), x[k]);
         }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (dst[k]) *reinterpret_cast<uint4*>(dst[k] + 64 * c) = make_uint4(x[k][0], x[k][1], x[k][2], x[k][3]);
         __syncwarp();
       }
       const uint32_t mine = at[lane];
@@ -649,44 +651,62 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int r0 = x.r0, head = x.head, tile0 = x.tile * kRows, clean = x.clean, limit = x.limit;
         const int nt[2] = {x.na, x.nb};
         const int buf = (n & 1) * kPairRows;
-        for (int i = lane; i < kPairRows; i += 32) {
-          const int row = r0 + i;
-          uint32_t at = kNoRow;
+        constexpr int RL = kPairRows / 32;  // rows a lane
+        int lq[RL], lk[RL], rb[RL];
+        const int xb = x.b;
+#pragma unroll
+        for (int k = 0; k < RL; ++k) {  // all the lengths' loads in flight at once
+          rb[k] = PREFIX ? min((r0 + 32 * k + lane) / rows, p.seq.B - 1) : xb;
+          seq_lens(p.seq, rb[k], lq[k], lk[k]);
+        }
+#pragma unroll
+        for (int k = 0; k < RL; ++k) {
+          const int i = 32 * k + lane, row = r0 + i;
+          const int rr = PREFIX ? row - rb[k] * rows : row;
+          const int qi = rr % p.seq.Nq;
           int end = 0;
-          if (row < space) {
-            const int rb = PREFIX ? row / rows : x.b;
-            const int rr = PREFIX ? row - rb * rows : row;
-            const int qi = rr % p.seq.Nq;
-            int lq, lk;
-            seq_lens(p.seq, rb, lq, lk);
-            if (qi < lq) end = (p.causal ? min(qi + lk - lq + 1, lk) : lk) - origin;
-            if (PREFIX) end = min(end, p.seq.prefix_len);
-            at = (static_cast<uint32_t>(rb) * Hkv + head) * rows + rr;
-          }
-          at_w[buf + i] = at;
-          end_w[buf + i] = end - tile0;
+          if (qi < lq[k]) end = (p.causal ? min(qi + lk[k] - lq[k] + 1, lk[k]) : lk[k]) - origin;
+          if (PREFIX) end = min(end, p.seq.prefix_len);
+          const bool in = row < space;
+          at_w[buf + i] = in ? (static_cast<uint32_t>(rb[k]) * Hkv + head) * rows + rr : kNoRow;
+          end_w[buf + i] = (in ? end : 0) - tile0;
         }
         mbar_arrive_warp(BAR(L::ROWS_FULL + (n & 1)));
         constexpr int LPR = D / 8;     // lanes a row, 16 bytes each
         const int chunk = lane % LPR;
-        for (int t = 0; t < 2 && ok; ++t) {
-          if (nt[t] == 0) continue;
-          ok = tile_wait(BAR(L::Q_EMPTY + t), (qn[t] & 1) ^ 1, wc_idle, SITE_TILE_PIECE, n);
-          if (!ok) break;
-          ++qn[t];
-          const uint32_t qt = sbase + t * L::kTileBytes + (chunk >> 3) * 16384;
-#pragma unroll 8
-          for (int i = lane / LPR; i < kRows; i += 32 / LPR) {
-            const uint32_t at = row_at[buf + t * kRows + i];
-            const bool live = at != kNoRow;
-            cp_async16(qt + sw128(i, chunk & 7), p.q + (live ? static_cast<size_t>(at) * D + chunk * 8 : 0),
-                       live ? 16u : 0u);
+        for (int t = 0; t < 2; ++t) {
+          if (nt[t] > 0) {
+            ok = tile_wait(BAR(L::Q_EMPTY + t), (qn[t] & 1) ^ 1, wc_idle, SITE_TILE_PIECE, n);
+            if (!ok) break;
+            ++qn[t];
+            const uint32_t qt = sbase + t * L::kTileBytes + (chunk >> 3) * 16384;
+            constexpr int RPI = 32 / LPR, IN = 16;  // rows an instruction, instructions whose rows are looked up at once
+#pragma unroll 1
+            for (int i0 = lane / LPR; i0 < kRows; i0 += RPI * IN) {
+              uint32_t at[IN];
+#pragma unroll
+              for (int k = 0; k < IN; ++k) at[k] = row_at[buf + t * kRows + i0 + RPI * k];
+#pragma unroll
+              for (int k = 0; k < IN; ++k) {
+                const bool live = at[k] != kNoRow;
+                cp_async16(qt + sw128(i0 + RPI * k, chunk & 7), p.q + (live ? static_cast<size_t>(at[k]) * D : 0) + chunk * 8,
+                           live ? 16u : 0u);
+              }
+            }
           }
-          cp_async_wait();
-          fence_proxy_async_smem();
-          mbar_arrive_warp(BAR(L::Q_FULL + t));
+          cp_async_commit();
         }
-        if (!ok) break;
+        if (!ok) {
+          cp_async_wait<0>();
+          break;
+        }
+        // tile A's rows may go while tile B's arrive
+        cp_async_wait<1>();
+        fence_proxy_async_smem();
+        if (nt[0] > 0) mbar_arrive_warp(BAR(L::Q_FULL + 0));
+        cp_async_wait<0>();
+        fence_proxy_async_smem();
+        if (nt[1] > 0) mbar_arrive_warp(BAR(L::Q_FULL + 1));
         if (clean >= 0) {
           const uint32_t vpos = kvbase + 2 * clean + 1;
           ok = tile_wait(BAR(L::DIRTY), cleaned & 1, wc_idle, SITE_TILE_CLEAN, n);
