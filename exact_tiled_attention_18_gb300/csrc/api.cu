@@ -500,6 +500,7 @@ fa_status paged_common(const void* q, const void* k_pages, const void* v_pages, 
   if ((!steps || prefix_len > 0) && (!encode_bf16_map(&a.tm_k, k_pages, page_heads, page_size, d, a.box_rows) ||
                                      !encode_bf16_map(&a.tm_v, v_pages, page_heads, page_size, d, a.box_rows)))
     return FA_ERR_LAUNCH;
+  if (!steps && !encode_bf16_map(&a.tm_q, q, 1, B * Hq * Nq, d)) return FA_ERR_LAUNCH;
   if (steps && (!encode_map(&a.st_k, MapKey{k_pages, 2, page_heads, page_size, d, 64, a.box_rows, true}) ||
                 !encode_map(&a.st_v, MapKey{v_pages, 2, page_heads, page_size, d, 64, a.box_rows, true}) ||
                 !encode_map(&a.st_k16, MapKey{k_pages, 2, page_heads, page_size, d, 64, 16, true}) ||

@@ -176,10 +176,14 @@ __global__ void __launch_bounds__(kStepThreads, step_ctas_per_sm<RB>())
   });
   auto starts = [&](int b) { return line[b]; };
   const int total = line[p.seq.B] * p.seq.Hkv;
+  const Ranges ranges = make_ranges(total, gridDim.x, p.part.min_tiles);
   if (blockIdx.x == 0) {
     for (int i = threadIdx.x; i <= p.seq.B; i += kStepThreads) p.line_out[i] = line[i];
+    if (threadIdx.x == 0) {
+      p.line_out[p.seq.B + 1] = ranges.base;
+      p.line_out[p.seq.B + 2] = ranges.more;
+    }
   }
-  const Ranges ranges = make_ranges(total, gridDim.x, p.part.min_tiles);
   int at = range_start(ranges, blockIdx.x);
   const int stop = range_start(ranges, blockIdx.x + 1);
   const WaitCtl wc{abort_flag, p.status, p.wait_limit_ns};
@@ -197,7 +201,7 @@ __global__ void __launch_bounds__(kStepThreads, step_ctas_per_sm<RB>())
     auto page_of = [&](const Walk& x, int i) {
       const int key = p.seq.prefix_len + x.tile * kStepKeys + i * p.box_rows;
       return i < (x.end - x.tile) * boxes && key < len_k[x.e]
-                 ? __ldg(p.table.block_table + x.e * p.table.table_stride + key / p.table.page_size)
+                 ? p.table.block_table[x.e * p.table.table_stride + key / p.table.page_size]
                  : -1;
     };
     // pages are looked up 32 boxes ahead: the next ones of this piece, and the
@@ -285,8 +289,8 @@ __global__ void __launch_bounds__(kStepThreads, step_ctas_per_sm<RB>())
       const uint16_t* src = base + min(8 * m + fr, rows - 1) * D;  // rows of the block behind the last see no key
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) {
-        qf[m][ks][0] = __ldg(reinterpret_cast<const uint32_t*>(src + 16 * ks));
-        qf[m][ks][1] = __ldg(reinterpret_cast<const uint32_t*>(src + 16 * ks + 8));
+        qf[m][ks][0] = *reinterpret_cast<const uint32_t*>(src + 16 * ks);
+        qf[m][ks][1] = *reinterpret_cast<const uint32_t*>(src + 16 * ks + 8);
       }
     }
   };
@@ -509,18 +513,14 @@ __global__ void __launch_bounds__(kStepThreads, step_ctas_per_sm<RB>())
 struct Pieces {
   int n;              // pieces
   int c0;             // first CTA
-  long long slot;     // slot of a piece of CTA 0
+  int slot;           // slot of a piece of CTA 0
   bool first_whole;   // the first piece starts its CTA's range
 };
 
-// `tile`: the unit's first tile on the line; nt: its tiles; total: the line's.
-__device__ __forceinline__ Pieces pieces_on_line(const PartRef& r, int unit, int tile, int nt, int total) {
-  Pieces x;
-  x.slot = unit;
-  x.c0 = x.n = 0;
-  x.first_whole = false;
+// `tile`: the unit's first tile on the line; nt: its tiles.
+__device__ __forceinline__ Pieces pieces_on_line(const Ranges& ranges, int unit, int tile, int nt) {
+  Pieces x{0, 0, unit, false};
   if (nt > 0) {
-    const Ranges ranges = make_ranges(total, r.ctas, r.min_tiles);
     x.c0 = range_of(ranges, tile);
     x.n = range_of(ranges, tile + nt - 1) - x.c0 + 1;
     x.first_whole = tile == range_start(ranges, x.c0);
@@ -528,16 +528,24 @@ __device__ __forceinline__ Pieces pieces_on_line(const PartRef& r, int unit, int
   return x;
 }
 
+// The ranges stand behind the line's table of `entries` entries.
+__device__ __forceinline__ Ranges line_ranges(const int* line, int entries) {
+  return Ranges{line[entries + 1], line[entries + 2], line[entries]};
+}
+
 // Unit (entry, head) of the step kernel.
-__device__ __forceinline__ Pieces step_pieces(const PartRef& r, int entry, int entries, int head, int Hkv) {
+__device__ __forceinline__ Pieces step_pieces(const PartRef& r, int entry, int head, int Hkv) {
   const int t0 = r.line[entry], nt = r.line[entry + 1] - t0;
-  return pieces_on_line(r, entry * Hkv + head, t0 * Hkv + head * nt, nt, r.line[entries] * Hkv);
+  Ranges ranges = line_ranges(r.line, r.cut);
+  ranges.total *= Hkv;
+  return pieces_on_line(ranges, entry * Hkv + head, t0 * Hkv + head * nt, nt);
 }
 
 // Unit u of the tile kernel.
 __device__ __forceinline__ Pieces tile_pieces(const PartRef& r, int u) {
   if (u >= r.cut) return Pieces{1, 0, u + r.ctas, true};
-  return pieces_on_line(r, u, r.line[u], r.line[u + 1] - r.line[u], r.line[r.cut]);
+  const int t0 = r.line[u], nt = r.line[u + 1] - t0;
+  return pieces_on_line(line_ranges(r.line, r.cut), u, t0, nt);
 }
 
 // The tile kernel's unit of (sequence, head) bh and row pair `pair`.
@@ -548,15 +556,16 @@ __device__ __forceinline__ int tile_unit(const PartRef& r, int bh, int pair) {
 }
 
 __device__ __forceinline__ long long piece_row(const PartRef& r, const Pieces& x, int k, int in) {
-  const long long slot = r.two_a_cta ? 2LL * (x.c0 + k) + (k > 0 || x.first_whole ? 0 : 1) : x.slot + x.c0 + k;
-  return slot * r.slot_rows + in;
+  const int slot = r.two_a_cta ? 2 * (x.c0 + k) + (k > 0 || x.first_whole ? 0 : 1) : x.slot + x.c0 + k;
+  return static_cast<long long>(slot) * r.slot_rows + in;
 }
 
 // Merges rows' partial results: those of the sequence's own keys and those of
-// the shared prefix.  A warp takes RPW rows of one unit (their pieces are the
-// same) or, where rows are few and pieces many, WARPS warps share one row.
-// TILES: the sequences' part comes from the tile kernel, whose units are row
-// pairs.
+// the shared prefix.  A warp takes RPW neighbouring rows of one unit (their
+// pieces are the same) or, where rows are few and pieces many, WARPS warps
+// share one row.  TILES: the sequences' part comes from the tile kernel, whose
+// units are row pairs.  Bound by instructions and by the latency of two rounds
+// of loads (where the pieces are, the pieces).
 template <int D, int WARPS, int RPW, bool TILES>
 __global__ void __launch_bounds__(256) paged_combine_kernel(const __grid_constant__ PagedCombine p) {
   static_assert(WARPS == 1 || RPW == 1, "one or the other");
@@ -567,11 +576,11 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const __grid_constan
   const int sub = warp % WARPS;
   const int rows = p.seq.G * p.seq.Nq;
   const int slot_rows = p.part.slot_rows;
-  const int groups = (slot_rows + RPW - 1) / RPW;  // of rows, in a unit
-  const long long item = static_cast<long long>(blockIdx.x) * (8 / WARPS) + warp / WARPS;
-  bool in = item < static_cast<long long>(p.units) * groups;
-  const int unit = in ? static_cast<int>(item / groups) : 0;
-  const int row_in = in ? static_cast<int>(item % groups) * RPW : 0;
+  const unsigned groups = (slot_rows + RPW - 1) / RPW;  // of rows, in a unit
+  const unsigned item = blockIdx.x * (8 / WARPS) + warp / WARPS;
+  const int unit = static_cast<int>(min(item / groups, static_cast<unsigned>(p.units - 1)));
+  const int row_in = static_cast<int>(item % groups) * RPW;
+  bool in = item < p.units * groups;
   int b, head, r0;
   if constexpr (TILES) {
     const int g = unit / (p.part.group * p.part.pairs);
@@ -588,11 +597,15 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const __grid_constan
     head = unit - b * p.seq.Hkv;
     r0 = row_in;
   }
+  const bool with_prefix = p.prefix.o != nullptr;
+  const int all = (p.b0 + b) * rows + r0;  // row among all sequences'
+  const int prefix_pair = all / kPairRows, prefix_row = all % kPairRows;
   grid_wait();
-  const Pieces own =
-      TILES ? tile_pieces(p.part, unit) : step_pieces(p.part, b, p.part.units / p.seq.Hkv, head, p.seq.Hkv);
+  const Pieces own = TILES ? tile_pieces(p.part, unit) : step_pieces(p.part, b, head, p.seq.Hkv);
+  Pieces pre{0, 0, 0, false};
+  if (with_prefix) pre = tile_pieces(p.prefix, tile_unit(p.prefix, head, prefix_pair));
   const bool skip = !in || (p.direct && own.n == 1);  // written by the only CTA that had it
-  const int count = skip ? 0 : min(RPW, (TILES ? min(rows - r0, slot_rows - row_in) : slot_rows - row_in));
+  const int count = skip ? 0 : min(RPW, TILES ? min(rows - r0, slot_rows - row_in) : slot_rows - row_in);
   float M[RPW], sum[RPW], acc[RPW][CW];
 #pragma unroll
   for (int q = 0; q < RPW; ++q) {
@@ -601,7 +614,7 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const __grid_constan
 #pragma unroll
     for (int c = 0; c < CW; ++c) acc[q][c] = 0.f;
   }
-  const long long all = static_cast<long long>(p.b0 + b) * rows + r0;  // row among all sequences'
+  // rows [q0, qn) of the warp's, the first of which is row in_slot + q0 of x
   auto gather = [&](const PartRef& ref, const Pieces& x, int in_slot, int q0, int qn) {
     for (int i = sub; i < x.n; i += WARPS * U) {
       float lse[RPW][U], v[RPW][U][CW];
@@ -609,42 +622,50 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const __grid_constan
       for (int u = 0; u < U; ++u) {
         const int k = i + u * WARPS;
         const long long at = piece_row(ref, x, k, in_slot);
+        const float* src = ref.o + at * D + CW * lane;
+        const float* src_lse = ref.lse + at;
 #pragma unroll
         for (int q = 0; q < RPW; ++q) {
           lse[q][u] = -CUDART_INF_F;
           if (k < x.n && q >= q0 && q < qn) {
-            lse[q][u] = ref.lse[at + q];
-            const float* src = ref.o + (at + q) * D + CW * lane;
+            lse[q][u] = src_lse[q];
             if constexpr (CW == 4)
-              *reinterpret_cast<float4*>(v[q][u]) = *reinterpret_cast<const float4*>(src);
+              *reinterpret_cast<float4*>(v[q][u]) = *reinterpret_cast<const float4*>(src + q * D);
             else
-              *reinterpret_cast<float2*>(v[q][u]) = *reinterpret_cast<const float2*>(src);
+              *reinterpret_cast<float2*>(v[q][u]) = *reinterpret_cast<const float2*>(src + q * D);
           }
         }
       }
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
+      for (int q = 0; q < RPW; ++q) {
+        float m = M[q];
 #pragma unroll
-        for (int q = 0; q < RPW; ++q) {
-          if (lse[q][u] == -CUDART_INF_F) continue;  // the same in every lane
-          const float m = fmaxf(M[q], lse[q][u]);
-          const float f = exp2f(lse[q][u] - m), g = exp2f(M[q] - m);
-          M[q] = m;
-          sum[q] = sum[q] * g + f;
+        for (int u = 0; u < U; ++u) m = fmaxf(m, lse[q][u]);
+        if (m == -CUDART_INF_F) continue;  // the same in every lane
+        const float g = ex2_approx(M[q] - m);
+        M[q] = m;
+        sum[q] *= g;
 #pragma unroll
-          for (int c = 0; c < CW; ++c) acc[q][c] = fmaf(f, v[q][u][c], acc[q][c] * g);
+        for (int c = 0; c < CW; ++c) acc[q][c] *= g;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          if (lse[q][u] == -CUDART_INF_F) continue;
+          const float f = ex2_approx(lse[q][u] - m);
+          sum[q] += f;
+#pragma unroll
+          for (int c = 0; c < CW; ++c) acc[q][c] = fmaf(f, v[q][u][c], acc[q][c]);
         }
       }
     }
   };
   if (count > 0) {
     gather(p.part, own, row_in, 0, count);
-    if (p.prefix.o) {
+    if (with_prefix) {
       // the rows may cross from one row pair of the prefix into the next
-      const int e = static_cast<int>(all / kPairRows), in_pair = static_cast<int>(all % kPairRows);
-      const int here = min(count, kPairRows - in_pair);
-      gather(p.prefix, tile_pieces(p.prefix, tile_unit(p.prefix, head, e)), in_pair, 0, here);
-      if (here < count) gather(p.prefix, tile_pieces(p.prefix, tile_unit(p.prefix, head, e + 1)), -here, here, count);
+      const int here = min(count, kPairRows - prefix_row);
+      gather(p.prefix, pre, prefix_row, 0, here);
+      if (RPW > 1 && here < count)
+        gather(p.prefix, tile_pieces(p.prefix, tile_unit(p.prefix, head, prefix_pair + 1)), -here, here, count);
     }
   }
   if constexpr (WARPS > 1) {
@@ -656,11 +677,12 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const __grid_constan
     }
     __syncthreads();
     if (sub != 0) return;
+#pragma unroll
     for (int o = 1; o < WARPS; ++o) {
       const float m2 = s_max[warp + o];
       if (m2 == -CUDART_INF_F) continue;
       const float m = fmaxf(M[0], m2);
-      const float f = exp2f(m2 - m), g = exp2f(M[0] - m);
+      const float f = ex2_approx(m2 - m), g = ex2_approx(M[0] - m);
       M[0] = m;
       sum[0] = sum[0] * g + s_sum[warp + o] * f;
 #pragma unroll
@@ -671,18 +693,18 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const __grid_constan
   for (int q = 0; q < RPW; ++q) {
     if (q >= count) break;
     const bool live = sum[q] > 0.f;
-    const float inv = live ? 1.0f / sum[q] : 0.f;
+    const float inv = live ? __fdividef(1.f, sum[q]) : 0.f;
     const size_t row = (static_cast<size_t>(b) * p.seq.Hkv + head) * rows + r0 + q;
     const size_t at = row * D + CW * lane;
 #pragma unroll
     for (int c = 0; c < CW; c += 2) {
       const float x = acc[q][c] * inv, y = acc[q][c + 1] * inv;
       if (p.o_bf16)
-        *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.o) + at + c) = pack_bf16x2(x, y);
+        store_pair(static_cast<uint16_t*>(p.o) + at + c, x, y);
       else
-        *reinterpret_cast<float2*>(static_cast<float*>(p.o) + at + c) = make_float2(x, y);
+        store_pair(static_cast<float*>(p.o) + at + c, x, y);
     }
-    if (lane == 0) p.lse[row] = live ? (M[q] + log2f(sum[q])) * kLn2 : -CUDART_INF_F;
+    if (lane == 0) p.lse[row] = live ? (M[q] + __log2f(sum[q])) * kLn2 : -CUDART_INF_F;
   }
 }
 
@@ -701,11 +723,11 @@ cudaError_t launch_steps(const PagedArgs& a, const PagedStep& p, int ctas, cudaS
 // most rows may have none (direct), launching the blocks counts as well.
 template <int D>
 cudaError_t launch_combine(const PagedCombine& p, bool tiles, int sms, cudaStream_t stream) {
-  constexpr int RPW = 4;
   const long long rows = static_cast<long long>(p.units) * p.part.slot_rows;
   auto launch = [&](auto kern, long long items, int per_block) {
     return launch_overlapped(kern, dim3(static_cast<unsigned>((items + per_block - 1) / per_block)), 256, 0, stream, p);
   };
+  constexpr int RPW = 4;
   const long long groups = static_cast<long long>(p.units) * ((p.part.slot_rows + RPW - 1) / RPW);
   if (tiles) return launch(paged_combine_kernel<D, 1, RPW, true>, groups, 8);
   const long long room = (p.direct ? 4LL : 8LL) * sms;
@@ -778,7 +800,7 @@ cudaError_t launch_paged_d(const PagedArgs& a, cudaStream_t stream) {
     const int units = heads * pairs;
     const int cut = units < 2 * tile_ctas ? units : tile_ctas + units % tile_ctas;
     t.line_out = table;
-    t.counter = table + kTileLine + 1;
+    t.counter = table + kTileLine + 3;
     t.part = PartRef{table, tile_ctas, kMinTiles, cut, two_a_cta, kPairRows, units, heads, pairs,
                      head_group(heads, pairs, keys, D, tile_ctas), a.part + at,
                      a.part + at + slots * kPairRows * D};
@@ -800,7 +822,7 @@ cudaError_t launch_paged_d(const PagedArgs& a, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     t.prefix_table = a.prefix_table;
     t.wait_first = 1;
-    e = launch_tiles(t, a.tm_k, a.tm_v, D, tile_ctas, stream);
+    e = launch_tiles(t, a.tm_q, a.tm_k, a.tm_v, D, tile_ctas, stream);
     if (e != cudaSuccess) return e;
     c.prefix = t.part;
   }
@@ -811,7 +833,7 @@ cudaError_t launch_paged_d(const PagedArgs& a, cudaStream_t stream) {
     t.direct = c.direct;
     // (behind a memset the launch does not overlap with the prefix's)
     t.wait_first = !with_prefix || t.part.cut < t.part.units;
-    e = launch_tiles(t, a.tm_k, a.tm_v, D, tile_ctas, stream);
+    e = launch_tiles(t, a.tm_q, a.tm_k, a.tm_v, D, tile_ctas, stream);
     if (e != cudaSuccess) return e;
     c.seq = all;
     c.part = t.part;
@@ -835,7 +857,7 @@ cudaError_t launch_paged_d(const PagedArgs& a, cudaStream_t stream) {
     p.o_bf16 = a.o_bf16;
     p.lse = a.lse + first;
     p.line_out = line;
-    p.part = PartRef{line,        step_ctas, kMinSteps, 0, 0, x.rows, n * a.Hkv, 0, 0, 0, a.part + x.own,
+    p.part = PartRef{line,        step_ctas, kMinSteps, n, 0, x.rows, n * a.Hkv, 0, 0, 0, a.part + x.own,
                      a.part + x.own + x.own_slots * x.rows * D};
     p.direct = c.direct;
     p.wait_first = !with_prefix || b0 > 0;

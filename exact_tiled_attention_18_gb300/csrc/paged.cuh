@@ -17,7 +17,7 @@ constexpr int kMinTiles = 2;           // key tiles (128 keys) a CTA of the tile
 constexpr int kMaxTileCtas = 160;
 constexpr int kTileLine = 2 * kMaxTileCtas;  // units of the tile kernel's line
 constexpr int kPairRows = 256;         // query rows a unit of the tile kernel: two 128-row tiles
-static_assert(kLineWords >= kLineSequences + 1 && kLineWords >= kTileLine + 1 && kLineWords % 4 == 0, "the line's room");
+static_assert(kLineWords >= kLineSequences + 3 && kLineWords >= kTileLine + 4 && kLineWords % 4 == 0, "the line's room");
 
 struct PagedSeq {
   const int *seqlens_q, *seqlens_k;
@@ -33,7 +33,8 @@ struct PagedSeq {
 // only a CTA's first and last pieces of the line are partial, in slot 2 c (its
 // first) or 2 c + 1.
 struct PartRef {
-  const int* line;     // first tile of every unit before `cut` (the step kernel: of every sequence, a head)
+  const int* line;     // first tile of every unit before `cut` (the step kernel: of its `cut` sequences, a head),
+                       // their sum, then the ranges' base and more
   int ctas, min_tiles;
   int cut;
   int two_a_cta;
@@ -98,8 +99,8 @@ struct PagedCombine {
   float* lse;
 };
 
-cudaError_t launch_tiles(const PagedTiles& p, const CUtensorMap& tm_k, const CUtensorMap& tm_v, int d, int ctas,
-                         cudaStream_t stream);
+cudaError_t launch_tiles(const PagedTiles& p, const CUtensorMap& tm_q, const CUtensorMap& tm_k,
+                         const CUtensorMap& tm_v, int d, int ctas, cudaStream_t stream);
 
 #if defined(__CUDACC__)
 __device__ __forceinline__ void seq_lens(const PagedSeq& s, int b, int& lq, int& lk) {

@@ -140,8 +140,8 @@ __device__ __forceinline__ int tile_keys(int r0, int rows, int nq, int lq, int l
 
 template <int D, bool PREFIX>
 __global__ void __launch_bounds__(kThreads, 1)
-    paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                       const __grid_constant__ PagedTiles p) {
+    paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                       const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ PagedTiles p) {
   using L = TileLayout<D>;
   constexpr int S = L::kSlots;
   constexpr int CB = D / 64;
@@ -188,6 +188,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_relinquish();
   }
   if (warp == 8 && lane == 0) {
+    if (!PREFIX) prefetch_tensormap(&tm_q);
     prefetch_tensormap(&tm_k);
     prefetch_tensormap(&tm_v);
   }
@@ -247,8 +248,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     build_line<kThreads>(line, scratch, cut, [&](int e) { return unit_tiles(e); });
   }
   const int total = line[cut];
-  if (blockIdx.x == 0)
+  if (blockIdx.x == 0) {
     for (int i = threadIdx.x; i <= cut; i += kThreads) p.line_out[i] = line[i];
+    if (threadIdx.x == 0) {
+      const Ranges ranges = make_ranges(total, gridDim.x, p.part.min_tiles);
+      p.line_out[cut + 1] = ranges.base;
+      p.line_out[cut + 2] = ranges.more;
+    }
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -472,7 +479,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int count = tiles * boxes;
         auto page_of = [&](int i) {
           const int key = first + i * p.box_rows;
-          return i < count && key < last ? __ldg(pages + key / p.table.page_size) : -1;
+          return i < count && key < last ? pages[key / p.table.page_size] : -1;
         };
         int cur = page_of(lane), next = page_of(32 + lane);
         for (int j = 0; j < tiles && ok; ++j) {
@@ -651,6 +658,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int r0 = x.r0, head = x.head, tile0 = x.tile * kRows, clean = x.clean, limit = x.limit;
         const int nt[2] = {x.na, x.nb};
         const int buf = (n & 1) * kPairRows;
+        // a sequence's rows of a key head lie together (rows of the tile behind
+        // the last are the next head's, and see no key); the prefix's are
+        // gathered, one row of every sequence's after the other
+        if constexpr (!PREFIX) {
+          for (int t = 0; t < 2; ++t) {
+            if (nt[t] == 0) continue;
+            ok = tile_wait(BAR(L::Q_EMPTY + t), (qn[t] & 1) ^ 1, wc_idle, SITE_TILE_PIECE, n);
+            if (!ok) break;
+            ++qn[t];
+            if (lane == 0) {
+              mbar_arrive_expect_tx(BAR(L::Q_FULL + t), L::kTileBytes);
+              const int row = (x.b * Hkv + head) * rows + r0 + t * kRows;
+#pragma unroll
+              for (int c = 0; c < CB; ++c)
+                tma_load_3d(sbase + t * L::kTileBytes + c * 16384, &tm_q, BAR(L::Q_FULL + t), c * 64, row, 0);
+            }
+            __syncwarp();
+          }
+          if (!ok) break;
+        }
         constexpr int RL = kPairRows / 32;  // rows a lane
         int lq[RL], lk[RL], rb[RL];
         const int xb = x.b;
@@ -663,50 +690,61 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int k = 0; k < RL; ++k) {
           const int i = 32 * k + lane, row = r0 + i;
           const int rr = PREFIX ? row - rb[k] * rows : row;
-          const int qi = rr % p.seq.Nq;
-          int end = 0;
-          if (qi < lq[k]) end = (p.causal ? min(qi + lk[k] - lq[k] + 1, lk[k]) : lk[k]) - origin;
-          if (PREFIX) end = min(end, p.seq.prefix_len);
-          const bool in = row < space;
-          at_w[buf + i] = in ? (static_cast<uint32_t>(rb[k]) * Hkv + head) * rows + rr : kNoRow;
-          end_w[buf + i] = (in ? end : 0) - tile0;
+          at_w[buf + i] = row < space ? (static_cast<uint32_t>(rb[k]) * Hkv + head) * rows + rr : kNoRow;
         }
-        mbar_arrive_warp(BAR(L::ROWS_FULL + (n & 1)));
-        constexpr int LPR = D / 8;     // lanes a row, 16 bytes each
-        const int chunk = lane % LPR;
-        for (int t = 0; t < 2; ++t) {
-          if (nt[t] > 0) {
-            ok = tile_wait(BAR(L::Q_EMPTY + t), (qn[t] & 1) ^ 1, wc_idle, SITE_TILE_PIECE, n);
-            if (!ok) break;
-            ++qn[t];
-            const uint32_t qt = sbase + t * L::kTileBytes + (chunk >> 3) * 16384;
-            constexpr int RPI = 32 / LPR, IN = 16;  // rows an instruction, instructions whose rows are looked up at once
+        __syncwarp();
+        if constexpr (PREFIX) {
+          constexpr int LPR = D / 8;     // lanes a row, 16 bytes each
+          const int chunk = lane % LPR;
+          for (int t = 0; t < 2; ++t) {
+            if (nt[t] > 0) {
+              ok = tile_wait(BAR(L::Q_EMPTY + t), (qn[t] & 1) ^ 1, wc_idle, SITE_TILE_PIECE, n);
+              if (!ok) break;
+              ++qn[t];
+              const uint32_t qt = sbase + t * L::kTileBytes + (chunk >> 3) * 16384;
+              constexpr int RPI = 32 / LPR, IN = 16;  // rows an instruction, instructions looked up at once
 #pragma unroll 1
-            for (int i0 = lane / LPR; i0 < kRows; i0 += RPI * IN) {
-              uint32_t at[IN];
+              for (int i0 = lane / LPR; i0 < kRows; i0 += RPI * IN) {
+                uint32_t at[IN];
 #pragma unroll
-              for (int k = 0; k < IN; ++k) at[k] = row_at[buf + t * kRows + i0 + RPI * k];
+                for (int k = 0; k < IN; ++k) at[k] = row_at[buf + t * kRows + i0 + RPI * k];
 #pragma unroll
-              for (int k = 0; k < IN; ++k) {
-                const bool live = at[k] != kNoRow;
-                cp_async16(qt + sw128(i0 + RPI * k, chunk & 7), p.q + (live ? static_cast<size_t>(at[k]) * D : 0) + chunk * 8,
-                           live ? 16u : 0u);
+                for (int k = 0; k < IN; ++k) {
+                  const bool live = at[k] != kNoRow;
+                  cp_async16(qt + sw128(i0 + RPI * k, chunk & 7),
+                             p.q + (live ? static_cast<size_t>(at[k]) * D : 0) + chunk * 8, live ? 16u : 0u);
+                }
               }
             }
+            cp_async_commit();
           }
-          cp_async_commit();
         }
-        if (!ok) {
+        // the rows' last keys, while their values arrive
+        if (ok) {
+#pragma unroll
+          for (int k = 0; k < RL; ++k) {
+            const int i = 32 * k + lane, row = r0 + i;
+            const int qi = (PREFIX ? row - rb[k] * rows : row) % p.seq.Nq;
+            int end = 0;
+            if (row < space && qi < lq[k]) end = (p.causal ? min(qi + lk[k] - lq[k] + 1, lk[k]) : lk[k]) - origin;
+            if (PREFIX) end = min(end, p.seq.prefix_len);
+            end_w[buf + i] = end - tile0;
+          }
+          mbar_arrive_warp(BAR(L::ROWS_FULL + (n & 1)));
+        }
+        if constexpr (PREFIX) {
+          if (!ok) {
+            cp_async_wait<0>();
+            break;
+          }
+          // tile A's rows may go while tile B's arrive
+          cp_async_wait<1>();
+          fence_proxy_async_smem();
+          if (nt[0] > 0) mbar_arrive_warp(BAR(L::Q_FULL + 0));
           cp_async_wait<0>();
-          break;
+          fence_proxy_async_smem();
+          if (nt[1] > 0) mbar_arrive_warp(BAR(L::Q_FULL + 1));
         }
-        // tile A's rows may go while tile B's arrive
-        cp_async_wait<1>();
-        fence_proxy_async_smem();
-        if (nt[0] > 0) mbar_arrive_warp(BAR(L::Q_FULL + 0));
-        cp_async_wait<0>();
-        fence_proxy_async_smem();
-        if (nt[1] > 0) mbar_arrive_warp(BAR(L::Q_FULL + 1));
         if (clean >= 0) {
           const uint32_t vpos = kvbase + 2 * clean + 1;
           ok = tile_wait(BAR(L::DIRTY), cleaned & 1, wc_idle, SITE_TILE_CLEAN, n);
@@ -724,6 +762,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         kvbase += 2 * max(nt[0], nt[1]);
         piece_done(n);
+      }
+      if (!PREFIX && !ok && lane == 0) {
+        // let the copies already issued land before the CTA can exit
+        for (int t = 0; t < 2; ++t)
+          if (qn[t] > 0) drain_wait(BAR(L::Q_FULL + t), (qn[t] - 1) & 1, p.wait_limit_ns);
       }
     } else {
       // ------------------------------------------------------------- pieces
@@ -788,25 +831,25 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <int D, bool PREFIX>
-cudaError_t launch_t(const PagedTiles& p, const CUtensorMap& tm_k, const CUtensorMap& tm_v, int ctas,
-                     cudaStream_t stream) {
+cudaError_t launch_t(const PagedTiles& p, const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
+                     int ctas, cudaStream_t stream) {
   using L = TileLayout<D>;
   auto kern = paged_tiles_kernel<D, PREFIX>;
   static std::atomic<unsigned long long> ready{0};
   cudaError_t e = setup_kernel_once(kern, L::kSmemBytes, kLaunchRegs, ready);
   if (e != cudaSuccess) return e;
-  return launch_overlapped(kern, dim3(ctas), kThreads, L::kSmemBytes, stream, tm_k, tm_v, p);
+  return launch_overlapped(kern, dim3(ctas), kThreads, L::kSmemBytes, stream, tm_q, tm_k, tm_v, p);
 }
 
 }  // namespace
 
-cudaError_t launch_tiles(const PagedTiles& p, const CUtensorMap& tm_k, const CUtensorMap& tm_v, int d, int ctas,
-                         cudaStream_t stream) {
+cudaError_t launch_tiles(const PagedTiles& p, const CUtensorMap& tm_q, const CUtensorMap& tm_k,
+                         const CUtensorMap& tm_v, int d, int ctas, cudaStream_t stream) {
   if (d == 64)
-    return p.prefix_table ? launch_t<64, true>(p, tm_k, tm_v, ctas, stream)
-                          : launch_t<64, false>(p, tm_k, tm_v, ctas, stream);
-  return p.prefix_table ? launch_t<128, true>(p, tm_k, tm_v, ctas, stream)
-                        : launch_t<128, false>(p, tm_k, tm_v, ctas, stream);
+    return p.prefix_table ? launch_t<64, true>(p, tm_q, tm_k, tm_v, ctas, stream)
+                          : launch_t<64, false>(p, tm_q, tm_k, tm_v, ctas, stream);
+  return p.prefix_table ? launch_t<128, true>(p, tm_q, tm_k, tm_v, ctas, stream)
+                        : launch_t<128, false>(p, tm_q, tm_k, tm_v, ctas, stream);
 }
 
 }  // namespace fa

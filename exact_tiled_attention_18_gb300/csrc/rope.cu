@@ -15,9 +15,9 @@
 //
 // Both kernels are copies with a little arithmetic: bound by HBM bandwidth
 // (two bytes in and two out per bf16 value) when large and by launch latency
-// when small.  A thread owns 16 values of a token's head (8 pairs) in 16-byte
-// loads, computes their 8 sines and cosines once, and walks over heads with
-// them, four heads' loads in flight at a time.
+// when small.  A thread owns 16 values of a token's head (8 pairs), computes
+// their 8 sines and cosines once, and walks over heads with them, several
+// heads' loads in flight at a time.
 #include <cuda_runtime.h>
 
 #include "ptx.cuh"
@@ -27,90 +27,45 @@ namespace fa {
 namespace {
 
 constexpr int kRopeThreads = 256;
-constexpr int kHeadsInFlight = 4;
 
-// Eight consecutive values as fp32.
-template <bool BF16>
-struct Eight {
-  uint4 w[BF16 ? 1 : 2];
-};
-
-template <bool BF16>
-__device__ __forceinline__ Eight<BF16> load8(const void* base, long long i) {
-  Eight<BF16> e;
-  if constexpr (BF16) {
-    e.w[0] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + i);
-  } else {
-    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const float*>(base) + i);
-    e.w[0] = p[0];
-    e.w[1] = p[1];
-  }
-  return e;
-}
-
-template <bool BF16>
-__device__ __forceinline__ void unpack8(const Eight<BF16>& e, float (&f)[8]) {
-  if constexpr (BF16) {
-    const uint32_t w[4] = {e.w[0].x, e.w[0].y, e.w[0].z, e.w[0].w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      f[2 * i] = __uint_as_float(w[i] << 16);
-      f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      f[4 * i] = __uint_as_float(e.w[i].x);
-      f[4 * i + 1] = __uint_as_float(e.w[i].y);
-      f[4 * i + 2] = __uint_as_float(e.w[i].z);
-      f[4 * i + 3] = __uint_as_float(e.w[i].w);
-    }
-  }
-}
-
-// Eight fp32 values, rounded once when the output is bf16.
-template <bool BF16>
-__device__ __forceinline__ void store8(void* base, long long i, const float (&f)[8]) {
-  if constexpr (BF16) {
-    uint4 w;
-    w.x = pack_bf16x2(f[0], f[1]);
-    w.y = pack_bf16x2(f[2], f[3]);
-    w.z = pack_bf16x2(f[4], f[5]);
-    w.w = pack_bf16x2(f[6], f[7]);
-    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + i) = w;
-  } else {
-    float4* p = reinterpret_cast<float4*>(static_cast<float*>(base) + i);
-    p[0] = make_float4(f[0], f[1], f[2], f[3]);
-    p[1] = make_float4(f[4], f[5], f[6], f[7]);
-  }
-}
-
-// The 16 values of a head that lane c of its d / 16 lanes owns, as two runs of
-// eight, and the pairs it turns.
+// A lane's 16 values of a head are RUNS runs of as many bytes as one load
+// takes, spread over the rotated part (or the part behind it) so that
+// neighbouring lanes' runs are neighbours: run k of lane c is elements
+//     base + k * span / RUNS + c * PER, ...      (PER = 16 / RUNS).
+// Pairs never leave a lane: with the half layout element i of the first half
+// of the runs belongs to element i of the second half, span / 2 further on;
+// interleaved pairs are neighbours inside a run.  Eight values a run (16 bytes
+// of bf16), four where fp32 is read or written.
+template <int RUNS>
 struct Lane {
-  int lo, hi;       // first element of either run
+  int at;           // first element of run 0
+  int step;         // from run to run
   bool turns;       // false: the values behind rot_dim, copied
-  float cs[8], sn[8];
+  float cs[8], sn[8];  // of pair i of the lane
 };
 
-__device__ __forceinline__ Lane make_lane(const RopeRef& r, int c, bool turn) {
-  Lane l;
-  l.turns = turn && 16 * c < r.rot_dim;
-  if (l.turns && !r.interleaved) {
-    l.lo = 8 * c;
-    l.hi = r.rot_dim / 2 + 8 * c;
-  } else {
-    l.lo = 16 * c;
-    l.hi = 16 * c + 8;
-  }
+template <int RUNS>
+__device__ __forceinline__ Lane<RUNS> make_lane(const RopeRef& r, int d, int c, bool rotate) {
+  constexpr int PER = 16 / RUNS;
+  Lane<RUNS> l;
+  const int turned = rotate ? r.rot_dim : 0;
+  l.turns = 16 * c < turned;
+  const int span = l.turns ? turned : d - turned;
+  l.at = l.turns ? PER * c : turned + PER * (c - turned / 16);
+  l.step = span / RUNS;
   return l;
 }
 
-__device__ __forceinline__ void set_angles(Lane& l, const RopeRef& r, int c, int position, float sign) {
+template <int RUNS>
+__device__ __forceinline__ void set_angles(Lane<RUNS>& l, const RopeRef& r, int position, float sign) {
   if (!l.turns) return;
+  constexpr int PER = 16 / RUNS;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const unsigned long long f = static_cast<unsigned long long>(__ldg(r.turns + 8 * c + i));
+    // pair i: element i of the lane's first eight (half), or elements 2i, 2i+1
+    const int e = r.interleaved ? 2 * i : i;
+    const int element = l.at + (e / PER) * l.step + e % PER;
+    const unsigned long long f = static_cast<unsigned long long>(__ldg(r.turns + (r.interleaved ? element / 2 : element)));
     const unsigned long long phase = static_cast<unsigned long long>(static_cast<long long>(position)) * f;
     const float half_turns = static_cast<float>(static_cast<int>(phase >> 32)) * 4.656612873077393e-10f;  // 2^-31
     float s, co;
@@ -120,33 +75,101 @@ __device__ __forceinline__ void set_angles(Lane& l, const RopeRef& r, int c, int
   }
 }
 
-// Turns the lane's pairs: interleaved pairs are neighbours inside a run,
-// otherwise pair i is (lo[i], hi[i]).
-__device__ __forceinline__ void turn(const Lane& l, bool interleaved, float (&lo)[8], float (&hi)[8]) {
+template <int RUNS>
+__device__ __forceinline__ void turn(const Lane<RUNS>& l, bool interleaved, float (&v)[16]) {
   if (!l.turns) return;
   if (interleaved) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float a = lo[2 * i], b = lo[2 * i + 1];
-      lo[2 * i] = a * l.cs[i] - b * l.sn[i];
-      lo[2 * i + 1] = b * l.cs[i] + a * l.sn[i];
-      const float e = hi[2 * i], f = hi[2 * i + 1];
-      hi[2 * i] = e * l.cs[4 + i] - f * l.sn[4 + i];
-      hi[2 * i + 1] = f * l.cs[4 + i] + e * l.sn[4 + i];
+    for (int i = 0; i < 8; ++i) {
+      const float a = v[2 * i], b = v[2 * i + 1];
+      v[2 * i] = a * l.cs[i] - b * l.sn[i];
+      v[2 * i + 1] = b * l.cs[i] + a * l.sn[i];
     }
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float a = lo[i], b = hi[i];
-      lo[i] = a * l.cs[i] - b * l.sn[i];
-      hi[i] = b * l.cs[i] + a * l.sn[i];
+      const float a = v[i], b = v[8 + i];
+      v[i] = a * l.cs[i] - b * l.sn[i];
+      v[8 + i] = b * l.cs[i] + a * l.sn[i];
     }
   }
 }
 
+// A lane's values as they lie in memory: 8 words of bf16, 16 of fp32.
+template <bool BF16>
+struct Raw {
+  uint32_t w[BF16 ? 8 : 16];
+};
+
+template <bool BF16, int RUNS>
+__device__ __forceinline__ Raw<BF16> load(const void* base, long long row, const Lane<RUNS>& l) {
+  constexpr int PER = 16 / RUNS;
+  Raw<BF16> x;
+#pragma unroll
+  for (int k = 0; k < RUNS; ++k) {
+    const long long i = row + l.at + k * l.step;
+    if constexpr (!BF16) {
+      static_assert(BF16 || PER == 4, "fp32 comes in runs of four");
+      const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const float*>(base) + i);
+      x.w[4 * k] = v.x, x.w[4 * k + 1] = v.y, x.w[4 * k + 2] = v.z, x.w[4 * k + 3] = v.w;
+    } else if constexpr (PER == 8) {
+      const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + i);
+      x.w[4 * k] = v.x, x.w[4 * k + 1] = v.y, x.w[4 * k + 2] = v.z, x.w[4 * k + 3] = v.w;
+    } else {
+      const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(base) + i);
+      x.w[2 * k] = v.x, x.w[2 * k + 1] = v.y;
+    }
+  }
+  return x;
+}
+
+template <bool BF16>
+__device__ __forceinline__ void unpack(const Raw<BF16>& x, float (&v)[16]) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    if constexpr (BF16)
+      v[i] = __uint_as_float(i & 1 ? x.w[i / 2] & 0xFFFF0000u : x.w[i / 2] << 16);
+    else
+      v[i] = __uint_as_float(x.w[i]);
+  }
+}
+
+// The values rounded once when the output is bf16.
+template <bool BF16>
+__device__ __forceinline__ Raw<BF16> pack(const float (&v)[16]) {
+  Raw<BF16> x;
+#pragma unroll
+  for (int i = 0; i < (BF16 ? 8 : 16); ++i) {
+    if constexpr (BF16)
+      x.w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+    else
+      x.w[i] = __float_as_uint(v[i]);
+  }
+  return x;
+}
+
+template <bool BF16, int RUNS>
+__device__ __forceinline__ void store(void* base, long long row, const Lane<RUNS>& l, const Raw<BF16>& x) {
+  constexpr int PER = 16 / RUNS;
+#pragma unroll
+  for (int k = 0; k < RUNS; ++k) {
+    const long long i = row + l.at + k * l.step;
+    if constexpr (!BF16)
+      *reinterpret_cast<uint4*>(static_cast<float*>(base) + i) =
+          make_uint4(x.w[4 * k], x.w[4 * k + 1], x.w[4 * k + 2], x.w[4 * k + 3]);
+    else if constexpr (PER == 8)
+      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + i) =
+          make_uint4(x.w[4 * k], x.w[4 * k + 1], x.w[4 * k + 2], x.w[4 * k + 3]);
+    else
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(base) + i) = make_uint2(x.w[2 * k], x.w[2 * k + 1]);
+  }
+}
+
 template <int D, bool XBF, bool YBF>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a, const int heads_per_thread) {
+__global__ void __launch_bounds__(kRopeThreads, 3) rope_kernel(const RopeArgs a, const int heads_per_thread) {
   constexpr int LANES = D / 16;
+  constexpr int RUNS = XBF && YBF ? 2 : 4;
+  constexpr int HEADS = XBF ? 4 : 2;  // heads in flight: 128 bytes a thread
   grid_trigger();
   const long long item = static_cast<long long>(blockIdx.x) * (kRopeThreads / LANES) + threadIdx.x / LANES;
   if (item >= static_cast<long long>(a.B) * a.N) return;
@@ -156,28 +179,22 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a, co
   const int h0 = blockIdx.y * heads_per_thread;
   const int h1 = min(h0 + heads_per_thread, a.H);
   const int position = a.rope.positions ? __ldg(a.rope.positions + b * a.rope.positions_sb + n) : n;
-  Lane l = make_lane(a.rope, c, true);
-  set_angles(l, a.rope, c, position, a.inverse ? -1.f : 1.f);
+  Lane<RUNS> l = make_lane<RUNS>(a.rope, D, c, true);
+  set_angles(l, a.rope, position, a.inverse ? -1.f : 1.f);
   const long long xo = b * a.xs.b + n * a.xs.n;
   const long long yo = b * a.ys.b + n * a.ys.n;
-  for (int h = h0; h < h1; h += kHeadsInFlight) {
-    Eight<XBF> lo[kHeadsInFlight], hi[kHeadsInFlight];
+  for (int h = h0; h < h1; h += HEADS) {
+    Raw<XBF> raw[HEADS];
 #pragma unroll
-    for (int u = 0; u < kHeadsInFlight; ++u) {
-      if (h + u < h1) {
-        lo[u] = load8<XBF>(a.x, xo + (h + u) * a.xs.h + l.lo);
-        hi[u] = load8<XBF>(a.x, xo + (h + u) * a.xs.h + l.hi);
-      }
-    }
+    for (int u = 0; u < HEADS; ++u)
+      if (h + u < h1) raw[u] = load<XBF>(a.x, xo + (h + u) * a.xs.h, l);
 #pragma unroll
-    for (int u = 0; u < kHeadsInFlight; ++u) {
+    for (int u = 0; u < HEADS; ++u) {
       if (h + u < h1) {
-        float p[8], q[8];
-        unpack8<XBF>(lo[u], p);
-        unpack8<XBF>(hi[u], q);
-        turn(l, a.rope.interleaved, p, q);
-        store8<YBF>(a.y, yo + (h + u) * a.ys.h + l.lo, p);
-        store8<YBF>(a.y, yo + (h + u) * a.ys.h + l.hi, q);
+        float v[16];
+        unpack<XBF>(raw[u], v);
+        turn(l, a.rope.interleaved, v);
+        store<YBF>(a.y, yo + (h + u) * a.ys.h, l, pack<YBF>(v));
       }
     }
   }
@@ -188,6 +205,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a, co
 template <int D>
 __global__ void __launch_bounds__(kRopeThreads) append_kernel(const AppendArgs a, const int heads_per_thread) {
   constexpr int LANES = D / 16;
+  constexpr int RUNS = 2, HEADS = 4;
   grid_trigger();
   const long long item = static_cast<long long>(blockIdx.x) * (kRopeThreads / LANES) + threadIdx.x / LANES;
   if (item >= static_cast<long long>(a.B) * a.N) return;
@@ -213,17 +231,16 @@ __global__ void __launch_bounds__(kRopeThreads) append_kernel(const AppendArgs a
     else if (c == 0)
       record_bad_page(a.status, SITE_PAGE_APPEND, b, page);
   }
-  const bool rotate = a.rope.rot_dim > 0;
-  Lane l = make_lane(a.rope, c, rotate);
+  Lane<RUNS> l = make_lane<RUNS>(a.rope, D, c, a.rope.rot_dim > 0);
   if (h0 < hq + a.Hkv) {
     const int position = a.rope.positions ? __ldg(a.rope.positions + b * a.rope.positions_sb + t) : place;
-    set_angles(l, a.rope, c, position, 1.f);
+    set_angles(l, a.rope, position, 1.f);
   }
-  for (int h = h0; h < h1; h += kHeadsInFlight) {
-    Eight<true> lo[kHeadsInFlight], hi[kHeadsInFlight];
-    uint16_t* dst[kHeadsInFlight];
+  for (int h = h0; h < h1; h += HEADS) {
+    Raw<true> raw[HEADS];
+    uint16_t* dst[HEADS];  // null: no such head, or no row of the cache
 #pragma unroll
-    for (int u = 0; u < kHeadsInFlight; ++u) {
+    for (int u = 0; u < HEADS; ++u) {
       const int g = h + u;
       dst[u] = nullptr;
       if (g < h1) {
@@ -238,24 +255,19 @@ __global__ void __launch_bounds__(kRopeThreads) append_kernel(const AppendArgs a
           if (row >= 0)
             dst[u] = (value ? a.v_pages : a.k_pages) + (row + static_cast<long long>(kh) * a.table.page_size) * D;
         }
-        lo[u] = load8<true>(src, l.lo);
-        hi[u] = load8<true>(src, l.hi);
+        raw[u] = load<true>(src, 0, l);
       }
     }
 #pragma unroll
-    for (int u = 0; u < kHeadsInFlight; ++u) {
+    for (int u = 0; u < HEADS; ++u) {
       if (dst[u]) {
         if (h + u < hq + a.Hkv && l.turns) {
-          float p[8], q[8];
-          unpack8<true>(lo[u], p);
-          unpack8<true>(hi[u], q);
-          turn(l, a.rope.interleaved, p, q);
-          store8<true>(dst[u], l.lo, p);
-          store8<true>(dst[u], l.hi, q);
-        } else {
-          *reinterpret_cast<uint4*>(dst[u] + l.lo) = lo[u].w[0];
-          *reinterpret_cast<uint4*>(dst[u] + l.hi) = hi[u].w[0];
+          float v[16];
+          unpack<true>(raw[u], v);
+          turn(l, a.rope.interleaved, v);
+          raw[u] = pack<true>(v);
         }
+        store<true>(dst[u], 0, l, raw[u]);
       }
     }
   }

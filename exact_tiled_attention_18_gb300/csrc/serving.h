@@ -70,6 +70,7 @@ struct AppendArgs {
 
 struct PagedArgs {
   CUtensorMap tm_k, tm_v;     // tile kernel: 3-D maps over [num_pages * Hkv][page_size][d], boxes 64 x box_rows
+  CUtensorMap tm_q;           // and over q's rows [B * Hq * Nq][d], boxes 64 x 128 (chunks only)
   CUtensorMap st_k, st_v;     // step kernel: blocked maps of the same, boxes of box_rows whole rows
   CUtensorMap st_k16, st_v16; // and of 16
   const uint16_t *q;          // [B][Hq][Nq][d]
@@ -128,6 +129,8 @@ cudaError_t launch_overlapped(void (*kern)(Params...), dim3 grid, int threads, s
 __device__ __forceinline__ void grid_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // Until the kernels before this one have ended and their writes are visible.
+// What they wrote is read behind it with ordinary loads, never with __ldg,
+// which the compiler may move before it.
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // Records an entry of a block table that names no page (first failure wins).
@@ -144,8 +147,8 @@ __device__ __forceinline__ void record_bad_page(int* status, int site, int block
 // Valid lengths of sequence b: new tokens and keys in the cache.
 __device__ __forceinline__ void paged_lens(const int* seqlens_q, const int* seqlens_k, int b, int nq, int capacity,
                                            int& lq, int& lk) {
-  lq = seqlens_q ? min(max(__ldg(seqlens_q + b), 0), nq) : nq;
-  lk = seqlens_k ? min(max(__ldg(seqlens_k + b), 0), capacity) : capacity;
+  lq = seqlens_q ? min(max(seqlens_q[b], 0), nq) : nq;
+  lk = seqlens_k ? min(max(seqlens_k[b], 0), capacity) : capacity;
 }
 #endif
 
