@@ -403,3 +403,94 @@ def test_long_cache_offsets_past_32_bits():
         assert (o - o2).abs().max() <= 2e-2 and (lse - lse2).abs().max() <= 1e-4
     assert torch.equal(kp[pages - 1, :, :page], k[0, :, :page])
     assert torch.equal(kp[pages - 2, :, :n - page], k[0, :, page:])
+
+
+@pytest.mark.parametrize("Hq,Hkv,N,d", [(20, 20, 4096, 64), (24, 8, 3500, 128)])
+def test_many_units_agree_with_the_square_call(Hq, Hkv, N, d):
+    """More units than two for every CTA, so that most are drawn from the
+    counter: a whole prompt against its own cache agrees with fa_fwd on the
+    same tensors, and two runs are equal bit for bit."""
+    page = 64
+    g = torch.Generator().manual_seed(2)
+    q, k, v = (torch.randn(1, h, N, d, generator=g).to(BF16).cuda() for h in (Hq, Hkv, Hkv))
+    kp, vp, table = (t.cuda() for t in make_cache(1, Hkv, d, page, [N]))
+    lk = torch.tensor([N], dtype=torch.int32, device="cuda")
+    fa.kv_append(k, v, kp, vp, table, lk)
+    a = fa.forward_paged(q, kp, vp, table, lk)
+    b = fa.forward_paged(q, kp, vp, table, lk)
+    G = Hq // Hkv
+    o, lse = fa.forward(q, k.repeat_interleave(G, 1), v.repeat_interleave(G, 1), causal=True)
+    fa.sync_status()
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    # both round P to bf16 (8 bits) against their own running maximum: |v| below 6, sum of P 1
+    assert (a[0] - o).abs().max() <= 2 * 2.0 ** -8 * 6 and (a[1] - lse).abs().max() <= 1e-4
+
+
+def test_many_units_behind_a_prefix():
+    """Drawn units of both parts: the prefix's row pairs and the sequences'."""
+    B, Hq, Hkv, Nq, d, page, prefix = 300, 4, 2, 128, 64, 16, 64
+    lens = [prefix + Nq + i % 50 for i in range(B)]
+    q, kp, vp, table = make_batch(B, Hq, Hkv, Nq, d, page, lens, seed=3)
+    n = prefix // page
+    for b in range(1, B):
+        table[b, :n] = table[0, :n]
+    o, lse = run(q, kp, vp, table, lens, prefix=prefix, prefix_table=table[0, :n].clone())
+    o2, lse2 = run(q, kp, vp, table, lens, prefix=prefix, prefix_table=table[0, :n].clone())
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    some = [0, 1, 77, 150, 151, 299]
+    ref = reference(q[some], kp, vp, table[some], [lens[b] for b in some], None, True)
+    check(o[some], lse[some], ref, q, kp, scale_for(d), 8)
+
+
+@pytest.mark.parametrize("Nq", [1, 40])
+def test_graphs_with_their_own_workspaces_replay_at_once(Nq):
+    """Two captured calls without a given workspace, replayed on two streams
+    at once beside eager calls."""
+    lens = [2500, 100, 900, 64]
+    q, kp, vp, table = make_batch(4, 8, 2, Nq, 128, 64, lens, seed=5)
+    dev = [t.cuda() for t in (q, kp, vp, table)]
+    lk = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    want = fa.forward_paged(*dev, lk)
+    torch.cuda.synchronize()
+    graphs, outs, streams = [], [], [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(2):
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            outs.append(fa.forward_paged(*dev, lk))
+        graphs.append(gr)
+    for _ in range(5):
+        for gr, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                gr.replay()
+        eager = fa.forward_paged(*dev, lk)
+    torch.cuda.synchronize()
+    fa.sync_status()
+    for o, lse in outs + [eager]:
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+
+
+def test_two_host_threads():
+    """Calls from two threads on their own streams."""
+    import threading
+    lens = [1500, 33]
+    q, kp, vp, table = make_batch(2, 8, 2, 1, 128, 64, lens, seed=6)
+    dev = [t.cuda() for t in (q, kp, vp, table)]
+    lk = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    want = fa.forward_paged(*dev, lk)
+    torch.cuda.synchronize()
+    bad = []
+
+    def work():
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            for _ in range(50):
+                o, lse = fa.forward_paged(*dev, lk)
+                s.synchronize()
+                if not (torch.equal(o, want[0]) and torch.equal(lse, want[1])):
+                    bad.append(1)
+
+    threads = [threading.Thread(target=work) for _ in range(2)]
+    [t.start() for t in threads]
+    [t.join() for t in threads]
+    fa.sync_status()
+    assert not bad
