@@ -693,13 +693,17 @@ def _rope(x, turns, positions, layout, amplitude, inverse, out, out_dtype):
     if out is None:
         if out_dtype is None:
             out_dtype = dtype
+        elif out_dtype != torch.bfloat16 and out_dtype != torch.float32:
+            raise ValueError("out_dtype must be bfloat16 or float32")
         out = torch.empty((B, H, N, d), dtype=out_dtype, device=x.device)
-    if out_dtype is None:
-        out_dtype = out.dtype
-    yb, yh, yn, one = out.stride()
-    if (one != 1 or out.shape != x.shape or out.get_device() != index or out.dtype != out_dtype
-            or (out_dtype != torch.bfloat16 and out_dtype != torch.float32)):
-        raise ValueError("out must be a bf16 or fp32 tensor of x's shape and device with contiguous d")
+        yb, yh, yn = H * N * d, N * d, d
+    else:
+        if out_dtype is None:
+            out_dtype = out.dtype
+        if (out.shape != x.shape or out.get_device() != index or out.dtype != out_dtype
+                or (out_dtype != torch.bfloat16 and out_dtype != torch.float32) or out.stride(3) != 1):
+            raise ValueError("out must be a bf16 or fp32 tensor of x's shape and device with contiguous d")
+        yb, yh, yn, _ = out.stride()
     st = _call_on(index, (_lib or lib()).fa_rope, x.data_ptr(), dtype == torch.bfloat16, xb, xh, xn, out.data_ptr(),
                   out_dtype == torch.bfloat16, yb, yh, yn, pos, pos_stride, t, rot_dim, lay, amplitude, inverse, B, H,
                   N, d)
