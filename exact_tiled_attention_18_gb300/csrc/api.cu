@@ -73,9 +73,12 @@ struct MapKey {
   const void* base;
   int elem_bytes, heads, rows, inner, box_inner, box_rows;
   bool blocked = false;  // 4-D: a box takes all the 64-column blocks of its rows
+  int batch = 0;         // > 0, 4-D: over [batch][heads][rows][inner], a box takes box_batch sequences' rows
+  int box_batch = 0;
   bool operator==(const MapKey& o) const {
     return base == o.base && elem_bytes == o.elem_bytes && heads == o.heads && rows == o.rows && inner == o.inner &&
-           box_inner == o.box_inner && box_rows == o.box_rows && blocked == o.blocked;
+           box_inner == o.box_inner && box_rows == o.box_rows && blocked == o.blocked && batch == o.batch &&
+           box_batch == o.box_batch;
   }
 };
 
@@ -104,7 +107,9 @@ bool remember_map(const MapKey& key, const CUtensorMap& m) {
 // layout the MMA descriptors expect).  Rows past `rows` read as zeros.
 // Blocked (bf16): a 4-D map over [heads][inner / 64][rows][64] of the same
 // memory, box = 64 x box_rows x (inner / 64) x 1, so that one load brings the
-// box's rows block by block.
+// box's rows block by block.  With a batch (bf16): a 4-D map over
+// [batch][heads][rows][inner], box = 64 x box_rows x 1 x box_batch, for the
+// rows of several sequences' same head one behind the other.
 bool encode_map(CUtensorMap* m, const MapKey& key) {
   {
     std::lock_guard<std::mutex> lock(g_map_mu);
@@ -124,10 +129,19 @@ bool encode_map(CUtensorMap* m, const MapKey& key) {
                            static_cast<cuuint64_t>(key.rows) * key.inner * eb};
   cuuint32_t box[3] = {static_cast<cuuint32_t>(key.box_inner), static_cast<cuuint32_t>(key.box_rows), 1};
   cuuint32_t estride[4] = {1, 1, 1, 1};
-  if (key.blocked) {
+  if (key.blocked || key.batch > 0) {
     cuuint64_t dims4[4] = {64, dims[1], static_cast<cuuint64_t>(key.inner / 64), dims[2]};
     cuuint64_t strides4[3] = {strides[0], 128, strides[1]};
     cuuint32_t box4[4] = {64, box[1], static_cast<cuuint32_t>(key.inner / 64), 1};
+    if (key.batch > 0) {
+      dims4[0] = dims[0];
+      dims4[2] = dims[2];
+      dims4[3] = static_cast<cuuint64_t>(key.batch);
+      strides4[1] = strides[1];
+      strides4[2] = strides[1] * key.heads;
+      box4[2] = 1;
+      box4[3] = static_cast<cuuint32_t>(key.box_batch);
+    }
     if (fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(key.base), dims4, strides4, box4, estride,
            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
@@ -500,7 +514,17 @@ fa_status paged_common(const void* q, const void* k_pages, const void* v_pages, 
   if ((!steps || prefix_len > 0) && (!encode_bf16_map(&a.tm_k, k_pages, page_heads, page_size, d, a.box_rows) ||
                                      !encode_bf16_map(&a.tm_v, v_pages, page_heads, page_size, d, a.box_rows)))
     return FA_ERR_LAUNCH;
+  const int rows = Hq / Hkv * Nq;  // below 2^31: checked above
   if (!steps && !encode_bf16_map(&a.tm_q, q, 1, B * Hq * Nq, d)) return FA_ERR_LAUNCH;
+  // the prefix's row tiles in boxes, where 128 rows are whole sequences' rows
+  // or a part of one's
+  a.boxed_rows = prefix_len > 0 && (fa::kTileRows % rows == 0 || rows % fa::kTileRows == 0);
+  if (a.boxed_rows) {
+    MapKey key{q, 2, Hkv, rows, d, 64, rows < fa::kTileRows ? rows : fa::kTileRows};
+    key.batch = B;
+    key.box_batch = rows < fa::kTileRows ? fa::kTileRows / rows : 1;
+    if (!encode_map(&a.tm_qp, key)) return FA_ERR_LAUNCH;
+  }
   if (steps && (!encode_map(&a.st_k, MapKey{k_pages, 2, page_heads, page_size, d, 64, a.box_rows, true}) ||
                 !encode_map(&a.st_v, MapKey{v_pages, 2, page_heads, page_size, d, 64, a.box_rows, true}) ||
                 !encode_map(&a.st_k16, MapKey{k_pages, 2, page_heads, page_size, d, 64, 16, true}) ||

@@ -821,8 +821,9 @@ cudaError_t launch_paged_d(const PagedArgs& a, cudaStream_t stream) {
     e = tiles(t, a.Hkv, x.prefix_pairs, a.prefix_len, false, x.prefix, x.prefix_slots, line + kLineWords);
     if (e != cudaSuccess) return e;
     t.prefix_table = a.prefix_table;
+    t.boxed_rows = a.boxed_rows;
     t.wait_first = 1;
-    e = launch_tiles(t, a.tm_q, a.tm_k, a.tm_v, D, tile_ctas, stream);
+    e = launch_tiles(t, a.tm_qp, a.tm_k, a.tm_v, D, tile_ctas, stream);
     if (e != cudaSuccess) return e;
     c.prefix = t.part;
   }
@@ -831,6 +832,7 @@ cudaError_t launch_paged_d(const PagedArgs& a, cudaStream_t stream) {
     e = tiles(t, a.B * a.Hkv, x.pairs, capacity, !with_prefix, x.own, x.own_slots, line);
     if (e != cudaSuccess) return e;
     t.direct = c.direct;
+    t.boxed_rows = 1;
     // (behind a memset the launch does not overlap with the prefix's)
     t.wait_first = !with_prefix || t.part.cut < t.part.units;
     e = launch_tiles(t, a.tm_q, a.tm_k, a.tm_v, D, tile_ctas, stream);

@@ -77,6 +77,7 @@ struct PagedTiles {
   int* line_out;     // the line's table, for the combine
   PartRef part;
   int direct;
+  int boxed_rows;    // tiles of rows come by TMA (always but for some prefixes)
   int* counter;      // draws units from part.cut on; zero at the start
   int wait_first;    // as PagedStep's
   int box_rows;

@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_relinquish();
   }
   if (warp == 8 && lane == 0) {
-    if (!PREFIX) prefetch_tensormap(&tm_q);
+    if (p.boxed_rows) prefetch_tensormap(&tm_q);
     prefetch_tensormap(&tm_k);
     prefetch_tensormap(&tm_v);
   }
@@ -659,9 +659,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int nt[2] = {x.na, x.nb};
         const int buf = (n & 1) * kPairRows;
         // a sequence's rows of a key head lie together (rows of the tile behind
-        // the last are the next head's, and see no key); the prefix's are
-        // gathered, one row of every sequence's after the other
-        if constexpr (!PREFIX) {
+        // the last are the next head's, and see no key), the prefix's rows in
+        // as many runs as it has sequences: boxes where those divide 128 rows,
+        // gathered row by row where not
+        const bool boxed = !PREFIX || p.boxed_rows;
+        if (boxed) {
           for (int t = 0; t < 2; ++t) {
             if (nt[t] == 0) continue;
             ok = tile_wait(BAR(L::Q_EMPTY + t), (qn[t] & 1) ^ 1, wc_idle, SITE_TILE_PIECE, n);
@@ -669,10 +671,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             ++qn[t];
             if (lane == 0) {
               mbar_arrive_expect_tx(BAR(L::Q_FULL + t), L::kTileBytes);
-              const int row = (x.b * Hkv + head) * rows + r0 + t * kRows;
+              const int row = r0 + t * kRows;
 #pragma unroll
-              for (int c = 0; c < CB; ++c)
-                tma_load_3d(sbase + t * L::kTileBytes + c * 16384, &tm_q, BAR(L::Q_FULL + t), c * 64, row, 0);
+              for (int c = 0; c < CB; ++c) {
+                const uint32_t dst = sbase + t * L::kTileBytes + c * 16384;
+                if constexpr (PREFIX)
+                  tma_load_4d(dst, &tm_q, BAR(L::Q_FULL + t), c * 64, row % rows, head, row / rows);
+                else
+                  tma_load_3d(dst, &tm_q, BAR(L::Q_FULL + t), c * 64, (x.b * Hkv + head) * rows + row, 0);
+              }
             }
             __syncwarp();
           }
@@ -693,7 +700,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           at_w[buf + i] = row < space ? (static_cast<uint32_t>(rb[k]) * Hkv + head) * rows + rr : kNoRow;
         }
         __syncwarp();
-        if constexpr (PREFIX) {
+        if (PREFIX && !boxed) {
           constexpr int LPR = D / 8;     // lanes a row, 16 bytes each
           const int chunk = lane % LPR;
           for (int t = 0; t < 2; ++t) {
@@ -732,7 +739,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           mbar_arrive_warp(BAR(L::ROWS_FULL + (n & 1)));
         }
-        if constexpr (PREFIX) {
+        if (PREFIX && !boxed) {
           if (!ok) {
             cp_async_wait<0>();
             break;
@@ -763,7 +770,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         kvbase += 2 * max(nt[0], nt[1]);
         piece_done(n);
       }
-      if (!PREFIX && !ok && lane == 0) {
+      if ((!PREFIX || p.boxed_rows) && !ok && lane == 0) {
         // let the copies already issued land before the CTA can exit
         for (int t = 0; t < 2; ++t)
           if (qn[t] > 0) drain_wait(BAR(L::Q_FULL + t), (qn[t] - 1) & 1, p.wait_limit_ns);

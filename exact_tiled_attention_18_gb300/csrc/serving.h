@@ -71,6 +71,7 @@ struct AppendArgs {
 struct PagedArgs {
   CUtensorMap tm_k, tm_v;     // tile kernel: 3-D maps over [num_pages * Hkv][page_size][d], boxes 64 x box_rows
   CUtensorMap tm_q;           // and over q's rows [B * Hq * Nq][d], boxes 64 x 128 (chunks only)
+  CUtensorMap tm_qp;          // and over [B][Hkv][G * Nq][d], boxes of 128 rows (prefix, where boxed_rows)
   CUtensorMap st_k, st_v;     // step kernel: blocked maps of the same, boxes of box_rows whole rows
   CUtensorMap st_k16, st_v16; // and of 16
   const uint16_t *q;          // [B][Hq][Nq][d]
@@ -78,6 +79,7 @@ struct PagedArgs {
   PageTable table;
   const int* prefix_table;    // pages of the shared prefix
   int prefix_len;             // keys of the shared prefix, a multiple of page_size; 0: none
+  int boxed_rows;             // the prefix's row tiles come in boxes of tm_qp, else row by row
   void* o;                    // [B][Hq][Nq][d] fp32, or bf16 when o_bf16
   int o_bf16;
   float* lse;                 // [B][Hq][Nq]
