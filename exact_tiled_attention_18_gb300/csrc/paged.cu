@@ -27,9 +27,13 @@
 // columns: one accumulator and one set of statistics per CTA, so a CTA moves
 // from one sequence to the next without merging warps.
 //
-// Probabilities go into the product as a pair of bf16 (the value and what its
-// rounding left), 16 significand bits: the second product costs tensor time
-// that the kernel has to spare, and O is as exact as with fp32 products.
+// Up to 16 rows the probabilities go into the product as a pair of bf16 (the
+// value and what its rounding left), 16 significand bits: the second product
+// costs tensor time that the kernel has to spare, and O is as exact as with
+// fp32 products.  From 17 rows on they are one bf16, as in the other kernels,
+// and O is divided by the sum of the rounded weights, so that their rounding
+// does not scale a row; the queries then stay in shared memory instead of
+// registers.
 #include <cuda_runtime.h>
 #include <math_constants.h>
 
@@ -66,15 +70,22 @@ struct StepLayout {
   static constexpr int kHalf = (D / 64) * kStepKeys * 128;
   static constexpr int kStage = 2 * kHalf;
   static constexpr int kStages = (step_ctas_per_sm<RB>() == 3 ? 2 : 3) * (128 / D);
-  // probabilities: hi then lo, [RB][64 keys][8 rows] bf16, so that eight keys
-  // of a block are 128 contiguous bytes
+  static constexpr bool kMany = RB > 2;   // 17 rows or more
+  // probabilities: hi, then lo (up to 16 rows), [RB][64 keys][8 rows] bf16, so
+  // that eight keys of a block are 128 contiguous bytes
   static constexpr int kPOff = kStages * kStage;
   static constexpr int kPBlock = kStepKeys * 16;
-  static constexpr int kBarOff = kPOff + 2 * RB * kPBlock;   // FULL[s] then EMPTY[s]
-  static constexpr int kMaxOff = kBarOff + 2 * kStages * 8;  // [warps][8 RB] row maxima, then row sums
-  static constexpr int kMiscOff = kMaxOff + 2 * kStepWarps * 8 * RB * 4;
-  static constexpr int kLineOff = kMiscOff + 16;        // first tile of every sequence, then lq, then lk
-  static constexpr int kSmemBytes = kLineOff + (3 * kLineSequences + 1) * 4 + 1024;
+  // queries (17 rows or more): 64-column blocks of 32 rows of 128 bytes, swizzled
+  static constexpr int kQOff = kPOff + (kMany ? 1 : 2) * RB * kPBlock;
+  static constexpr int kQBytes = kMany ? 32 * D * 2 : 0;
+  static constexpr int kBarOff = kQOff + kQBytes;            // FULL[s] then EMPTY[s]
+  // [warps][8 RB] row maxima, row sums, and (17 rows or more) sums of rounded weights
+  static constexpr int kMaxOff = kBarOff + 2 * kStages * 8;
+  static constexpr int kMiscOff = kMaxOff + (kMany ? 3 : 2) * kStepWarps * 8 * RB * 4;
+  // first tile of every sequence, then lk, then lq (a byte: at most 32 here)
+  static constexpr int kLineOff = kMiscOff + 16;
+  static constexpr int kSmemBytes = kLineOff + (2 * kLineSequences + 1) * 4 + kLineSequences + 1024;
+  static_assert(step_ctas_per_sm<RB>() * (kSmemBytes + 1024) <= 228 * 1024, "resident CTAs an SM");
 };
 
 __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
@@ -165,12 +176,12 @@ __global__ void __launch_bounds__(kStepThreads, step_ctas_per_sm<RB>())
   if (p.wait_first) grid_wait();
   grid_trigger();
   // the scratch of the scan is the row-maxima area, unused so far
-  int* len_q = line + kLineSequences + 1;
-  int* len_k = len_q + kLineSequences;
+  int* len_k = line + kLineSequences + 1;
+  uint8_t* len_q = reinterpret_cast<uint8_t*>(len_k + kLineSequences);
   build_line<kStepThreads>(line, reinterpret_cast<int*>(smem + L::kMaxOff), p.seq.B, [&](int b) {
     int lq, lk;
     seq_lens(p.seq, b, lq, lk);
-    len_q[b] = lq;
+    len_q[b] = static_cast<uint8_t>(lq);
     len_k[b] = lk;
     return lq > 0 && lk > p.seq.prefix_len ? (lk - p.seq.prefix_len + kStepKeys - 1) / kStepKeys : 0;
   });
@@ -280,12 +291,26 @@ __global__ void __launch_bounds__(kStepThreads, step_ctas_per_sm<RB>())
   const int v_row = ((lane >> 4) << 3) + (lane & 7), v_half = (lane >> 3) & 1;
   const int v_col = warp * (D / 4);  // first value column of this warp
   const uint32_t p_hi = sbase + L::kPOff, p_lo = p_hi + RB * L::kPBlock;
-  uint32_t qf[RB][KS][2];
-  // the rows of a piece as fragments (rows of the group lie together)
+  constexpr bool MANY = L::kMany;
+  constexpr int QC = 32 * D / 8 / (32 * kStepWarps);  // 16-byte chunks of 32 rows of queries, a thread
+  uint32_t qf[MANY ? 1 : RB][MANY ? 1 : KS][2];
+  uint4 qs[MANY ? QC : 1];
+  // the rows of a piece (rows of the group lie together): as fragments, or on
+  // their way to shared memory
   auto load_q = [&](const Walk& x) {
-    const uint16_t* base = p.q + (static_cast<size_t>(x.e) * p.seq.Hkv + x.head) * rows * D + fc;
+    const uint16_t* base = p.q + (static_cast<size_t>(x.e) * p.seq.Hkv + x.head) * rows * D;
+    if constexpr (MANY) {
 #pragma unroll
-    for (int m = 0; m < RB; ++m) {
+      for (int i = 0; i < QC; ++i) {
+        const int at = static_cast<int>(threadIdx.x) + i * 32 * kStepWarps;
+        const int r = min(at / (D / 8), rows - 1);  // rows behind the last see no key
+        qs[i] = *reinterpret_cast<const uint4*>(base + r * D + at % (D / 8) * 8);
+      }
+      return;
+    }
+    base += fc;
+#pragma unroll
+    for (int m = 0; m < (MANY ? 0 : RB); ++m) {
       const uint16_t* src = base + min(8 * m + fr, rows - 1) * D;  // rows of the block behind the last see no key
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) {
@@ -300,13 +325,32 @@ __global__ void __launch_bounds__(kStepThreads, step_ctas_per_sm<RB>())
     const int r = 8 * m + fc;
     query[m] = (r < rows ? r % p.seq.Nq : 0x7fff) | (r + 1 < rows ? (r + 1) % p.seq.Nq : 0x7fff) << 16;
   }
+  // ... and from there into it, when every warp is through with the last ones
+  auto place_q = [&]() {
+    if constexpr (MANY) {
+#pragma unroll
+      for (int i = 0; i < QC; ++i) {
+        const int at = static_cast<int>(threadIdx.x) + i * 32 * kStepWarps;
+        const int c = at % (D / 8);
+        st_shared_v4(sbase + L::kQOff + (c >> 3) * 4096 + sw128(at / (D / 8), c & 7), qs[i].x, qs[i].y, qs[i].z,
+                     qs[i].w);
+      }
+    }
+  };
   if (more) load_q(w);
+  if (more) place_q();
   int done = 0;
   bool ok = true;
   while (more && ok) {
     const int lq = len_q[w.e], lk = len_k[w.e];
     int kend[RB][2];               // last visible key + 1 of rows fc, fc + 1
     float m_ref[RB][2], l[RB][2], acc[RB][MT][4];
+    float lr[MANY ? RB : 1][2];    // sums of the rounded weights
+    if constexpr (MANY) {
+#pragma unroll
+      for (int m = 0; m < RB; ++m) lr[m][0] = lr[m][1] = 0.f;
+      warps_sync();                // the queries are in place
+    }
 #pragma unroll
     for (int m = 0; m < RB; ++m) {
 #pragma unroll
@@ -346,8 +390,19 @@ __global__ void __launch_bounds__(kStepThreads, step_ctas_per_sm<RB>())
         for (int ks = 0; ks < KS; ++ks) {
           uint32_t kf[4];
           ldmatrix4(kf, k16 + (ks >> 2) * block + sw128(k_row, 2 * (ks & 3) + k_half));
+          if constexpr (MANY) {
 #pragma unroll
-          for (int m = 0; m < RB; ++m) mma_bf16(sc[m], kf, qf[m][ks][0], qf[m][ks][1]);
+            for (int m = 0; m < RB; m += 2) {  // 16 rows a load (of 24 the last eight are not used)
+              uint32_t qv[4];
+              ldmatrix4(qv, sbase + L::kQOff + (ks >> 2) * 4096 +
+                                sw128(8 * m + ((lane >> 4) << 3) + (lane & 7), 2 * (ks & 3) + ((lane >> 3) & 1)));
+              mma_bf16(sc[m], kf, qv[0], qv[1]);
+              if (m + 1 < RB) mma_bf16(sc[m + 1 < RB ? m + 1 : m], kf, qv[2], qv[3]);
+            }
+          } else {
+#pragma unroll
+            for (int m = 0; m < RB; ++m) mma_bf16(sc[m], kf, qf[m][ks][0], qf[m][ks][1]);
+          }
         }
         if (key0 + kStepKeys > lk) {
           // rows behind the last key may hold anything: their weights are 0,
@@ -396,6 +451,7 @@ __global__ void __launch_bounds__(kStepThreads, step_ctas_per_sm<RB>())
             const float alpha = ex2_approx(m_ref[m][e] - top[e]);  // 0 on the first visible key
             m_ref[m][e] = top[e];
             l[m][e] *= alpha;
+            if constexpr (MANY) lr[m][e] *= alpha;
 #pragma unroll
             for (int n = 0; n < MT; ++n) {
               acc[m][n][e] *= alpha;
@@ -410,11 +466,15 @@ __global__ void __launch_bounds__(kStepThreads, step_ctas_per_sm<RB>())
 #pragma unroll
         for (int h = 0; h < 2; ++h) {  // keys fr and fr + 8
           const uint32_t hi = pack_bf16x2(pr[2 * h], pr[2 * h + 1]);
-          const uint32_t lo = pack_bf16x2(pr[2 * h] - __uint_as_float(hi << 16),
-                                          pr[2 * h + 1] - __uint_as_float(hi & 0xFFFF0000u));
+          const float h0 = __uint_as_float(hi << 16), h1 = __uint_as_float(hi & 0xFFFF0000u);
           const uint32_t off = m * L::kPBlock + (16 * warp + 8 * h + fr) * 16 + fc * 2;
           st_shared_u32(p_hi + off, hi);
-          st_shared_u32(p_lo + off, lo);
+          if constexpr (MANY) {
+            lr[m][0] += h0;
+            lr[m][1] += h1;
+          } else {
+            st_shared_u32(p_lo + off, pack_bf16x2(pr[2 * h] - h0, pr[2 * h + 1] - h1));
+          }
         }
       }
       warps_sync();
@@ -434,13 +494,13 @@ __global__ void __launch_bounds__(kStepThreads, step_ctas_per_sm<RB>())
           uint32_t ph[4], pl[4];  // keys 16 kk .. + 32, eight a matrix
           const uint32_t off = m * L::kPBlock + (16 * kk + lane) * 16;
           ldmatrix4_t(ph, p_hi + off);
-          ldmatrix4_t(pl, p_lo + off);
+          if constexpr (!MANY) ldmatrix4_t(pl, p_lo + off);
 #pragma unroll
           for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int n = 0; n < MT; ++n) {
               mma_bf16(acc[m][n], vf[h][n], ph[2 * h], ph[2 * h + 1]);
-              mma_bf16(acc[m][n], vf[h][n], pl[2 * h], pl[2 * h + 1]);
+              if constexpr (!MANY) mma_bf16(acc[m][n], vf[h][n], pl[2 * h], pl[2 * h + 1]);
             }
         }
       }
@@ -460,9 +520,17 @@ __global__ void __launch_bounds__(kStepThreads, step_ctas_per_sm<RB>())
         x += __shfl_xor_sync(0xffffffffu, x, 8);
         x += __shfl_xor_sync(0xffffffffu, x, 16);
         if (lane < 4) sums[warp * 8 * RB + 8 * m + fc + e] = x;
+        if constexpr (MANY) {
+          float y = lr[m][e];
+          y += __shfl_xor_sync(0xffffffffu, y, 4);
+          y += __shfl_xor_sync(0xffffffffu, y, 8);
+          y += __shfl_xor_sync(0xffffffffu, y, 16);
+          if (lane < 4) sums[(kStepWarps + warp) * 8 * RB + 8 * m + fc + e] = y;
+        }
       }
     }
     warps_sync();
+    if (another) place_q();
     const bool whole = p.direct && w.tile == 0 && w.end == w.tiles;
     const size_t slot = static_cast<size_t>(w.e) * p.seq.Hkv + w.head + blockIdx.x;
     const int odd = fr & 1;
@@ -476,7 +544,18 @@ __global__ void __launch_bounds__(kStepThreads, step_ctas_per_sm<RB>())
           sum.x += y.x;
           sum.y += y.y;
         }
-        const float s0 = sum.x > 0.f ? __fdividef(1.f, sum.x) : 0.f, s1 = sum.y > 0.f ? __fdividef(1.f, sum.y) : 0.f;
+        float2 weights = sum;  // what O is divided by
+        if constexpr (MANY) {
+          weights = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int o = 0; o < kStepWarps; ++o) {
+            const float2 y = *reinterpret_cast<const float2*>(sums + (kStepWarps + o) * 8 * RB + 8 * m + fc);
+            weights.x += y.x;
+            weights.y += y.y;
+          }
+        }
+        const float s0 = weights.x > 0.f ? __fdividef(1.f, weights.x) : 0.f;
+        const float s1 = weights.y > 0.f ? __fdividef(1.f, weights.y) : 0.f;
         // neighbours in the column exchange rows: a lane then holds two
         // adjacent columns of row fc (even columns' lanes) or fc + 1 (odd ones')
         const int r = 8 * m + fc + odd;
@@ -727,7 +806,7 @@ cudaError_t launch_combine(const PagedCombine& p, bool tiles, int sms, cudaStrea
   auto launch = [&](auto kern, long long items, int per_block) {
     return launch_overlapped(kern, dim3(static_cast<unsigned>((items + per_block - 1) / per_block)), 256, 0, stream, p);
   };
-  constexpr int RPW = 4;
+  constexpr int RPW = 2;
   const long long groups = static_cast<long long>(p.units) * ((p.part.slot_rows + RPW - 1) / RPW);
   if (tiles) return launch(paged_combine_kernel<D, 1, RPW, true>, groups, 8);
   const long long room = (p.direct ? 4LL : 8LL) * sms;

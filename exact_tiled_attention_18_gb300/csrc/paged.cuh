@@ -9,7 +9,7 @@
 namespace fa {
 
 constexpr int kStepRows = 32;          // rows a key head that the step kernel takes
-constexpr int kLineSequences = 256;    // sequences (or row pairs) a launch: the line's table is in shared memory
+constexpr int kLineSequences = 256;    // sequences a launch of the step kernel: the line's table is in shared memory
 constexpr int kLineWords = 528;        // 4-byte words of a line in the workspace, a multiple of 4
 constexpr int kMaxCtas = 512;
 constexpr int kMinSteps = 1;           // key tiles (64 keys) a CTA of the step kernel takes at least
