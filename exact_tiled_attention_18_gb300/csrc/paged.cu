@@ -683,7 +683,7 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const __grid_constan
   const Pieces own = TILES ? tile_pieces(p.part, unit) : step_pieces(p.part, b, head, p.seq.Hkv);
   Pieces pre{0, 0, 0, false};
   if (with_prefix) pre = tile_pieces(p.prefix, tile_unit(p.prefix, head, prefix_pair));
-  const bool skip = !in || (p.direct && own.n == 1);  // written by the only CTA that had it
+  const bool skip = !in || (p.direct && !p.part.dual && own.n == 1);  // written by the only CTA that had it
   const int count = skip ? 0 : min(RPW, TILES ? min(rows - r0, slot_rows - row_in) : slot_rows - row_in);
   float M[RPW], sum[RPW], acc[RPW][CW];
 #pragma unroll
@@ -695,18 +695,19 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const __grid_constan
   }
   // rows [q0, qn) of the warp's, the first of which is row in_slot + q0 of x
   auto gather = [&](const PartRef& ref, const Pieces& x, int in_slot, int q0, int qn) {
-    for (int i = sub; i < x.n; i += WARPS * U) {
+    const int n = ref.dual ? 2 * x.n : x.n;  // (dual: a piece's two halves)
+    for (int i = sub; i < n; i += WARPS * U) {
       float lse[RPW][U], v[RPW][U][CW];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int k = i + u * WARPS;
-        const long long at = piece_row(ref, x, k, in_slot);
+        const long long at = ref.dual ? piece_row(ref, x, k >> 1, in_slot + (k & 1) * 128) : piece_row(ref, x, k, in_slot);
         const float* src = ref.o + at * D + CW * lane;
         const float* src_lse = ref.lse + at;
 #pragma unroll
         for (int q = 0; q < RPW; ++q) {
           lse[q][u] = -CUDART_INF_F;
-          if (k < x.n && q >= q0 && q < qn) {
+          if (k < n && q >= q0 && q < qn) {
             lse[q][u] = src_lse[q];
             if constexpr (CW == 4)
               *reinterpret_cast<float4*>(v[q][u]) = *reinterpret_cast<const float4*>(src + q * D);
@@ -834,8 +835,10 @@ Plan make_plan(int B, int Hkv, int G, int Nq, int d, bool with_prefix) {
   x.chunk = B < kLineSequences ? B : kLineSequences;
   if (x.steps)
     x.own_slots = static_cast<size_t>(x.chunk) * Hkv + kMaxCtas;
+  else if (with_prefix || x.rows <= kTileRows)
+    x.own_slots = static_cast<size_t>(B) * Hkv * x.pairs + kMaxTileCtas;
   else
-    x.own_slots = with_prefix ? static_cast<size_t>(B) * Hkv * x.pairs + kMaxTileCtas : 2 * kMaxTileCtas;
+    x.own_slots = 2 * kMaxTileCtas;
   const size_t own_words = x.own_slots * (x.steps ? x.rows : kPairRows) * (d + 1);
   x.prefix_pairs = static_cast<int>((static_cast<long long>(B) * x.rows + kPairRows - 1) / kPairRows);
   x.prefix_slots = with_prefix ? static_cast<size_t>(x.prefix_pairs) * Hkv + kMaxTileCtas : 0;
@@ -868,7 +871,7 @@ cudaError_t launch_paged_d(const PagedArgs& a, cudaStream_t stream) {
   const PagedSeq all{a.seqlens_q, a.seqlens_k, a.B, a.Hkv, G, a.Nq, capacity, a.prefix_len};
   // the tile kernel on `heads` row spaces of `pairs` row pairs; the workspace
   // from `at` on holds `slots` slots
-  auto tiles = [&](PagedTiles& t, int heads, int pairs, int keys, bool two_a_cta, size_t at, size_t slots,
+  auto tiles = [&](PagedTiles& t, int heads, int pairs, int keys, bool direct, bool dual, size_t at, size_t slots,
                    int* table) -> cudaError_t {
     t.seq = all;
     t.table = a.table;
@@ -880,7 +883,8 @@ cudaError_t launch_paged_d(const PagedArgs& a, cudaStream_t stream) {
     const int cut = units < 2 * tile_ctas ? units : tile_ctas + units % tile_ctas;
     t.line_out = table;
     t.counter = table + kTileLine + 3;
-    t.part = PartRef{table, tile_ctas, kMinTiles, cut, two_a_cta, kPairRows, units, heads, pairs,
+    t.dual = dual;
+    t.part = PartRef{table, tile_ctas, kMinTiles, cut, direct && !dual, kPairRows, dual, units, heads, pairs,
                      head_group(heads, pairs, keys, D, tile_ctas), a.part + at,
                      a.part + at + slots * kPairRows * D};
     t.box_rows = a.box_rows;
@@ -897,7 +901,8 @@ cudaError_t launch_paged_d(const PagedArgs& a, cudaStream_t stream) {
   cudaError_t e;
   if (with_prefix) {
     PagedTiles t{};
-    e = tiles(t, a.Hkv, x.prefix_pairs, a.prefix_len, false, x.prefix, x.prefix_slots, line + kLineWords);
+    e = tiles(t, a.Hkv, x.prefix_pairs, a.prefix_len, false, static_cast<long long>(a.B) * x.rows <= kTileRows,
+              x.prefix, x.prefix_slots, line + kLineWords);
     if (e != cudaSuccess) return e;
     t.prefix_table = a.prefix_table;
     t.boxed_rows = a.boxed_rows;
@@ -908,7 +913,7 @@ cudaError_t launch_paged_d(const PagedArgs& a, cudaStream_t stream) {
   }
   if (!x.steps) {
     PagedTiles t{};
-    e = tiles(t, a.B * a.Hkv, x.pairs, capacity, !with_prefix, x.own, x.own_slots, line);
+    e = tiles(t, a.B * a.Hkv, x.pairs, capacity, !with_prefix, x.rows <= kTileRows, x.own, x.own_slots, line);
     if (e != cudaSuccess) return e;
     t.direct = c.direct;
     t.boxed_rows = 1;
@@ -918,7 +923,7 @@ cudaError_t launch_paged_d(const PagedArgs& a, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     c.seq = all;
     c.part = t.part;
-    c.units = c.direct ? t.part.cut : t.part.units;
+    c.units = c.direct && !t.dual ? t.part.cut : t.part.units;
     c.o = a.o;
     c.lse = a.lse;
     return launch_combine<D>(c, true, a.sms, stream);
@@ -938,7 +943,7 @@ cudaError_t launch_paged_d(const PagedArgs& a, cudaStream_t stream) {
     p.o_bf16 = a.o_bf16;
     p.lse = a.lse + first;
     p.line_out = line;
-    p.part = PartRef{line,        step_ctas, kMinSteps, n, 0, x.rows, n * a.Hkv, 0, 0, 0, a.part + x.own,
+    p.part = PartRef{line,        step_ctas, kMinSteps, n, 0, x.rows, 0, n * a.Hkv, 0, 0, 0, a.part + x.own,
                      a.part + x.own + x.own_slots * x.rows * D};
     p.direct = c.direct;
     p.wait_first = !with_prefix || b0 > 0;

@@ -39,6 +39,7 @@ struct PartRef {
   int cut;
   int two_a_cta;
   int slot_rows;
+  int dual;            // the tile kernel's dual mode: two partial results a piece
   int units;
   int heads, pairs, group;  // the tile kernel: (sequence, head)s, row pairs of each, heads dealt out together
   float *o, *lse;      // [slot][slot_rows][d], [slot][slot_rows] (log2 units)
@@ -77,6 +78,9 @@ struct PagedTiles {
   int* line_out;     // the line's table, for the combine
   PartRef part;
   int direct;
+  // 1: a unit's rows all fit into tile A; tile B takes the same rows and every
+  // other key tile, and leaves its partial result in the slot's second half
+  int dual;
   int boxed_rows;    // tiles of rows come by TMA (always but for some prefixes)
   int* counter;      // draws units from part.cut on; zero at the start
   int wait_first;    // as PagedStep's

@@ -70,6 +70,7 @@ enum TileSite : int {
 // A piece of a unit, as the roles read it.
 struct Piece {
   int na, nb;      // key tiles that row tiles A and B take; na < 0: there is no further piece
+  int tiles;       // key tiles
   int tile;        // the unit's first of them
   int limit;       // keys (from the origin) whose values are the sequence's own
   int clean;       // the piece's tile that the limit falls into, or -1
@@ -267,7 +268,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // stall within the limit itself and end all waits.
   const WaitCtl wc_idle{abort_flag, p.status, p.wait_limit_ns * 64};
   const volatile Piece* pieces = reinterpret_cast<const volatile Piece*>(smem + L::kPieceOff);
-  static_assert(sizeof(Piece) == 40, "pieces lie 40 bytes apart");
+  static_assert(sizeof(Piece) == 44, "pieces lie 44 bytes apart");
   const volatile uint32_t* row_at = reinterpret_cast<const volatile uint32_t*>(smem + L::kRowOff);
   const volatile int* row_end = reinterpret_cast<const volatile int*>(smem + L::kRowOff + 2 * kPairRows * 4);
   constexpr uint32_t kNoRow = 0xffffffffu;
@@ -294,8 +295,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = tile_wait(BAR(L::ROWS_FULL + (n & 1)), (n >> 1) & 1, wc_idle, SITE_TILE_PIECE, n);
       if (!ok) break;
       const int nt = t ? pieces[n & 1].nb : pieces[n & 1].na;
-      // this row's visible keys from the piece's first
+      // this row's visible keys from the tile's first, and how far its key
+      // tiles are apart
       const int lim0 = row_end[(n & 1) * kPairRows + t * kRows + r];
+      const int stride = p.dual ? 2 * kRows : kRows;
       float m_ref = 0.f, l = 0.f, dl = 0.f;
       for (int j = 0; j < nt; ++j) {
         ok = tile_wait(BAR(L::S_FULL + t), sn & 1, wc_idle, SITE_TILE_S, n);
@@ -311,7 +314,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int c = 0; c < 128; ++c) s[c] = __uint_as_float(sr[c]);
         }
-        const int lim = lim0 - j * kRows;
+        const int lim = lim0 - j * stride;
         if (__any_sync(0xffffffffu, lim < kRows)) {
 #pragma unroll
           for (int c = 0; c < 128; ++c) s[c] = (c < lim) ? s[c] : -CUDART_INF_F;
@@ -472,7 +475,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       for (uint32_t n = 0; next_piece(n, ok); ++n) {
         const volatile Piece& x = pieces[n & 1];
-        const int head = x.head, b = x.b, tiles = max(x.na, x.nb);
+        const int head = x.head, b = x.b, tiles = x.tiles;
         const int* pages = PREFIX ? p.prefix_table : p.table.block_table + b * p.table.table_stride;
         const int first = origin + x.tile * kRows;
         const int last = origin + x.limit;
@@ -555,9 +558,54 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (uint32_t n = 0; next_piece(n, ok); ++n) {
           const int unit = static_cast<int>(n);
           const int na = pieces[n & 1].na, nb = pieces[n & 1].nb, clean = pieces[n & 1].clean;
-          const int tiles = max(na, nb);
+          const int tiles = pieces[n & 1].tiles;
           if (lane == 0) {
           do {
+          if (p.dual) {
+            // key tile j belongs to row tile j & 1, whose chain S -> softmax ->
+            // P V -> next S runs beside the other's
+            auto start = [&](int t, int j) -> bool {
+              const uint32_t kpos = kvbase + 2 * j;
+              if (!wait_bounded(BAR(L::KV_FULL + kpos % S), (kpos / S) & 1, wc, SITE_TILE_MMA, unit)) return false;
+              tc_fence_after();
+              issue_s(t, kpos % S);
+              umma_commit(BAR(L::S_FULL + t));
+              umma_commit(BAR(L::KV_EMPTY + kpos % S));
+              if (j + 2 >= tiles) umma_commit(BAR(L::Q_EMPTY + t));  // the piece's last use of Q
+              return true;
+            };
+            if (na > 0) {
+              ok = wait_bounded(BAR(L::Q_FULL + 0), qa & 1, wc, SITE_TILE_MMA, unit) && start(0, 0);
+              if (!ok) break;
+              ++qa;
+            }
+            if (nb > 0) {
+              ok = wait_bounded(BAR(L::Q_FULL + 1), qb & 1, wc, SITE_TILE_MMA, unit) && start(1, 1);
+              if (!ok) break;
+              ++qb;
+            }
+            for (int j = 0; j < tiles && ok; ++j) {
+              const int t = j & 1;
+              const uint32_t vpos = kvbase + 2 * j + 1;
+              ok = wait_bounded(BAR(L::KV_FULL + vpos % S), (vpos / S) & 1, wc, SITE_TILE_MMA, unit);
+              if (!ok) break;
+              if (j == clean) mbar_arrive(BAR(L::DIRTY));
+              ok = wait_bounded(BAR(L::P_FULL + t), (t ? pb : pa) & 1, wc, SITE_TILE_MMA, unit);
+              if (!ok) break;
+              if (t) ++pb; else ++pa;
+              if (j == clean) {
+                ok = wait_bounded(BAR(L::CLEAN), cleaned & 1, wc, SITE_TILE_CLEAN, unit);
+                if (!ok) break;
+                ++cleaned;
+              }
+              tc_fence_after();
+              issue_pv(t, vpos % S, j > 1);
+              if (j + 2 >= tiles) umma_commit(BAR(L::O_FULL + t));
+              umma_commit(BAR(L::KV_EMPTY + vpos % S));
+              if (j + 2 < tiles) ok = start(t, j + 2);
+            }
+            break;
+          }
           if (tiles > 0) {
             ok = wait_bounded(BAR(L::KV_FULL + kvbase % S), (kvbase / S) & 1, wc, SITE_TILE_MMA, unit);
             if (!ok) break;
@@ -671,7 +719,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ++qn[t];
             if (lane == 0) {
               mbar_arrive_expect_tx(BAR(L::Q_FULL + t), L::kTileBytes);
-              const int row = r0 + t * kRows;
+              const int row = r0 + (p.dual ? 0 : t * kRows);
 #pragma unroll
               for (int c = 0; c < CB; ++c) {
                 const uint32_t dst = sbase + t * L::kTileBytes + c * 16384;
@@ -686,16 +734,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
         }
         constexpr int RL = kPairRows / 32;  // rows a lane
+        auto row_of = [&](int i) { return p.dual ? i & (kRows - 1) : i; };
         int lq[RL], lk[RL], rb[RL];
         const int xb = x.b;
 #pragma unroll
         for (int k = 0; k < RL; ++k) {  // all the lengths' loads in flight at once
-          rb[k] = PREFIX ? min((r0 + 32 * k + lane) / rows, p.seq.B - 1) : xb;
+          rb[k] = PREFIX ? min((r0 + row_of(32 * k + lane)) / rows, p.seq.B - 1) : xb;
           seq_lens(p.seq, rb[k], lq[k], lk[k]);
         }
 #pragma unroll
         for (int k = 0; k < RL; ++k) {
-          const int i = 32 * k + lane, row = r0 + i;
+          const int i = 32 * k + lane, row = r0 + row_of(i);
           const int rr = PREFIX ? row - rb[k] * rows : row;
           at_w[buf + i] = row < space ? (static_cast<uint32_t>(rb[k]) * Hkv + head) * rows + rr : kNoRow;
         }
@@ -730,12 +779,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ok) {
 #pragma unroll
           for (int k = 0; k < RL; ++k) {
-            const int i = 32 * k + lane, row = r0 + i;
+            const int i = 32 * k + lane, row = r0 + row_of(i);
             const int qi = (PREFIX ? row - rb[k] * rows : row) % p.seq.Nq;
             int end = 0;
             if (row < space && qi < lq[k]) end = (p.causal ? min(qi + lk[k] - lq[k] + 1, lk[k]) : lk[k]) - origin;
             if (PREFIX) end = min(end, p.seq.prefix_len);
-            end_w[buf + i] = end - tile0;
+            end_w[buf + i] = end - tile0 - (p.dual ? i & kRows : 0);  // tile B of two begins a key tile later
           }
           mbar_arrive_warp(BAR(L::ROWS_FULL + (n & 1)));
         }
@@ -767,7 +816,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive_warp(BAR(L::CLEAN));
           ++cleaned;
         }
-        kvbase += 2 * max(nt[0], nt[1]);
+        kvbase += 2 * x.tiles;
         piece_done(n);
       }
       if ((!PREFIX || p.boxed_rows) && !ok && lane == 0) {
@@ -797,7 +846,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           x.tile = at - line[lo];
           const int tiles = line[lo + 1] - line[lo];
           len = min(tiles - x.tile, stop - at);
-          x.whole = p.direct && len == tiles;
+          x.whole = p.direct && !p.dual && len == tiles;
           x.slot = p.part.two_a_cta ? 2 * blockIdx.x + (at == at0 ? 0 : 1) : u + blockIdx.x;
           at += len;
         } else if (cut < p.part.units) {
@@ -805,7 +854,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           u = __shfl_sync(0xffffffffu, u, 0);
           if (u < p.part.units) {
             len = unit_tiles(u);
-            x.whole = p.direct;
+            x.whole = p.direct && !p.dual;
             x.slot = u + gridDim.x;
           } else {
             u = -1;
@@ -817,8 +866,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           unit_keys(x.b, x.r0, ka, kb, x.limit);
           x.na = max(0, min((ka + kRows - 1) / kRows - x.tile, len));
           x.nb = max(0, min((kb + kRows - 1) / kRows - x.tile, len));
+          x.tiles = max(x.na, x.nb);
+          if (p.dual) {
+            x.nb = x.tiles / 2;
+            x.na = x.tiles - x.nb;
+          }
           const int at_tile = x.limit / kRows - x.tile;
-          x.clean = x.limit % p.box_rows != 0 && at_tile >= 0 && at_tile < max(x.na, x.nb) ? at_tile : -1;
+          x.clean = x.limit % p.box_rows != 0 && at_tile >= 0 && at_tile < x.tiles ? at_tile : -1;
         }
         if (lane == 0) *reinterpret_cast<Piece*>(smem + L::kPieceOff + (n & 1) * sizeof(Piece)) = x;
         mbar_arrive_warp(BAR(L::PIECE_FULL + (n & 1)));

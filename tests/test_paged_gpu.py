@@ -122,6 +122,9 @@ CHUNKS = [
     (1, 1, 1, 140, 128, 16, [41000], None),                      # long ranges: the ring goes round
     (2, 2, 1, 700, 128, 64, [3001, 9001], [700, 600]),           # heads of 700 rows: tiles across two heads
     (3, 3, 3, 200, 64, 32, [6001, 12007, 300], None),
+    (1, 4, 1, 32, 128, 64, [9000], None),                        # 128 rows: both row tiles take them
+    (2, 5, 1, 21, 64, 32, [1000, 130], [21, 3]),
+    (1, 8, 2, 11, 128, 16, [129], None),
     (530, 1, 1, 40, 64, 16, [40 + (i * 31) % 60 for i in range(530)], None),  # more row pairs than a launch takes
 ]
 
