@@ -634,6 +634,9 @@ __device__ __forceinline__ int tile_unit(const PartRef& r, int bh, int pair) {
   return g * r.group * r.pairs + (r.pairs - 1 - pair) * hs + bh - g * r.group;
 }
 
+// Rows of a unit.
+__host__ __device__ __forceinline__ int rows_of_unit(const PartRef& r) { return r.dual ? kTileRows : r.slot_rows; }
+
 __device__ __forceinline__ long long piece_row(const PartRef& r, const Pieces& x, int k, int in) {
   const int slot = r.two_a_cta ? 2 * (x.c0 + k) + (k > 0 || x.first_whole ? 0 : 1) : x.slot + x.c0 + k;
   return static_cast<long long>(slot) * r.slot_rows + in;
@@ -654,8 +657,8 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const __grid_constan
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int sub = warp % WARPS;
   const int rows = p.seq.G * p.seq.Nq;
-  const int slot_rows = p.part.slot_rows;
-  const unsigned groups = (slot_rows + RPW - 1) / RPW;  // of rows, in a unit
+  const int unit_rows = rows_of_unit(p.part);
+  const unsigned groups = (unit_rows + RPW - 1) / RPW;  // of rows, in a unit
   const unsigned item = blockIdx.x * (8 / WARPS) + warp / WARPS;
   const int unit = static_cast<int>(min(item / groups, static_cast<unsigned>(p.units - 1)));
   const int row_in = static_cast<int>(item % groups) * RPW;
@@ -684,7 +687,7 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const __grid_constan
   Pieces pre{0, 0, 0, false};
   if (with_prefix) pre = tile_pieces(p.prefix, tile_unit(p.prefix, head, prefix_pair));
   const bool skip = !in || (p.direct && !p.part.dual && own.n == 1);  // written by the only CTA that had it
-  const int count = skip ? 0 : min(RPW, TILES ? min(rows - r0, slot_rows - row_in) : slot_rows - row_in);
+  const int count = skip ? 0 : min(RPW, TILES ? min(rows - r0, unit_rows - row_in) : unit_rows - row_in);
   float M[RPW], sum[RPW], acc[RPW][CW];
 #pragma unroll
   for (int q = 0; q < RPW; ++q) {
@@ -701,7 +704,7 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const __grid_constan
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int k = i + u * WARPS;
-        const long long at = ref.dual ? piece_row(ref, x, k >> 1, in_slot + (k & 1) * 128) : piece_row(ref, x, k, in_slot);
+        const long long at = ref.dual ? piece_row(ref, x, k >> 1, in_slot + (k & 1) * kTileRows) : piece_row(ref, x, k, in_slot);
         const float* src = ref.o + at * D + CW * lane;
         const float* src_lse = ref.lse + at;
 #pragma unroll
@@ -803,14 +806,18 @@ cudaError_t launch_steps(const PagedArgs& a, const PagedStep& p, int ctas, cudaS
 // most rows may have none (direct), launching the blocks counts as well.
 template <int D>
 cudaError_t launch_combine(const PagedCombine& p, bool tiles, int sms, cudaStream_t stream) {
-  const long long rows = static_cast<long long>(p.units) * p.part.slot_rows;
+  constexpr int RPW = 2;
+  const int unit_rows = rows_of_unit(p.part);
+  const long long rows = static_cast<long long>(p.units) * unit_rows;
+  const long long groups = static_cast<long long>(p.units) * ((unit_rows + RPW - 1) / RPW);
+  const long long room = (p.direct ? 4LL : 8LL) * sms;
   auto launch = [&](auto kern, long long items, int per_block) {
     return launch_overlapped(kern, dim3(static_cast<unsigned>((items + per_block - 1) / per_block)), 256, 0, stream, p);
   };
-  constexpr int RPW = 2;
-  const long long groups = static_cast<long long>(p.units) * ((p.part.slot_rows + RPW - 1) / RPW);
-  if (tiles) return launch(paged_combine_kernel<D, 1, RPW, true>, groups, 8);
-  const long long room = (p.direct ? 4LL : 8LL) * sms;
+  if (tiles) {
+    if (rows <= 2 * room) return launch(paged_combine_kernel<D, 8, 1, true>, rows, 1);
+    return launch(paged_combine_kernel<D, 1, RPW, true>, groups, 8);
+  }
   if (rows <= room) return launch(paged_combine_kernel<D, 8, 1, false>, rows, 1);
   if (rows <= 2 * room) return launch(paged_combine_kernel<D, 4, 1, false>, rows, 2);
   return launch(paged_combine_kernel<D, 1, RPW, false>, groups, 8);
