@@ -43,9 +43,10 @@
  *    returns instead of hanging.  For tests of that path only,
  *    fa_test_set_stall(n) (initial value: the FA_TEST_STALL_UNIT environment
  *    variable, read once per process) makes the first CTA of every later
- *    launch leave one tile of its n-th work unit unloaded (fa_fwd_decode:
- *    CTA n leaves its first stage unloaded): its waits run out and
- *    fa_sync_status() then reports FA_ERR_TIMEOUT.
+ *    launch leave one tile of its n-th work unit unloaded (fa_fwd_decode and
+ *    the few-rows kernel of the paged calls: CTA n leaves its first stage
+ *    unloaded): its waits run out and fa_sync_status() then reports
+ *    FA_ERR_TIMEOUT.
  *  - Thread safety: calls may be made from several host threads; calls on
  *    different devices are independent.
  */
@@ -463,9 +464,9 @@ fa_status fa_rope(const void* x, int x_dtype, long long x_stride_b, long long x_
  * of length arrays serves the append and the attention of a step.
  * A table entry outside [0, num_pages) reads or writes nothing: the call
  * reports FA_ERR_BAD_PAGE through fa_sync_status, and the results of the
- * sequences that name it are unspecified.  max_pages * page_size
- * and num_pages * Hkv must be below 2^31; for the attention calls so must
- * B * Hkv * (Hq / Hkv * Nq / 256 + 1) * (max_pages * page_size / 64 + 1).
+ * sequences that name it are unspecified.  max_pages * page_size may be up to
+ * 2^30; num_pages * Hkv must be below 2^31, and for the attention calls so
+ * must B * Hkv * (Hq / Hkv * Nq / 256 + 1) * (max_pages * page_size / 64 + 1).
  */
 
 /*
@@ -503,7 +504,11 @@ fa_status fa_kv_append(const void* k, long long k_stride_b, long long k_stride_h
  *   seqlens_k NULL: every sequence has max_pages * page_size keys.
  *   workspace : fp32 scratch of fa_fwd_paged_workspace_bytes(...) bytes,
  *          16-byte aligned, used by one call at a time; or NULL (a
- *          stream-ordered allocation, freed on the same stream).
+ *          stream-ordered allocation from a pool of the library's that keeps
+ *          up to 256 MB a device between calls, freed on the same stream;
+ *          inside a stream capture an allocation of the graph's).
+ * With up to 16 rows a key head (Hq / Hkv * Nq) the probabilities enter the
+ * product with V in 16 significand bits, with more in 8 (bf16, as in fa_fwd).
  * Causal alignment, padding and empty rows as fa_fwd_varlen (O = 0,
  * LSE = -inf).  Rows of a page behind a sequence's last key may hold anything,
  * NaN included; the values of keys that some query of the sequence sees must
@@ -532,7 +537,8 @@ size_t fa_fwd_paged_workspace_bytes(int B, int Hq, int Hkv, int Nq, int d);
  *   prefix_len   : a positive multiple of page_size, at most
  *                  max_pages * page_size.  Sequences shorter than it are
  *                  allowed and see their own length's share of the prefix.
- * Other arguments, results and errors as fa_fwd_paged.
+ * The prefix's probabilities are bf16, as in fa_fwd, whatever the number of
+ * rows.  Other arguments, results and errors as fa_fwd_paged.
  */
 fa_status fa_fwd_shared_prefix(const void* q, const void* k_pages, const void* v_pages, int num_pages, int page_size,
                                const int* prefix_table, int prefix_len, const int* block_table,
@@ -559,7 +565,8 @@ fa_status fa_sync_status(fa_stream_t stream);
  * Wait sites: 1-7 forward, 11-20 dK/dV, 21-32 dQ, 35-36 decode, 41-47 FP8
  * forward, 51-59 the single-pass row-term pass, 61-63 the single-pass dK/dV
  * sweep, 71-80 the paged calls (each kernel's source names them).  After
- * FA_ERR_BAD_PAGE: out[2] the sequence, out[3] the table entry.
+ * FA_ERR_BAD_PAGE: out[2] the sequence (0 for a prefix), out[3] the table
+ * entry.
  * Returns FA_OK, or FA_ERR_INVALID_ARG if out is NULL.
  */
 fa_status fa_last_failure(int out[4]);

@@ -497,3 +497,34 @@ def test_two_host_threads():
     [t.join() for t in threads]
     fa.sync_status()
     assert not bad
+
+
+def test_captured_call_with_the_librarys_workspace():
+    """The C call without a workspace inside a capture: an allocation of the
+    graph's, replayed on new contents."""
+    lens = [1500, 200]
+    q, kp, vp, table = make_batch(2, 8, 2, 1, 128, 64, lens, seed=7)
+    dev = [t.cuda() for t in (q, kp, vp, table)]
+    lk = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    o = torch.zeros(2, 8, 1, 128, device="cuda")
+    lse = torch.zeros(2, 8, 1, device="cuda")
+
+    def call():
+        assert fa.fa_fwd_paged(dev[0].data_ptr(), dev[1].data_ptr(), dev[2].data_ptr(), kp.shape[0], 64,
+                               dev[3].data_ptr(), dev[3].stride(0), dev[3].shape[1], o.data_ptr(), 0, lse.data_ptr(), 0,
+                               lk.data_ptr(), 0, 2, 8, 2, 1, 128, 128 ** -0.5, 1,
+                               torch.cuda.current_stream().cuda_stream) == 0
+
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    dev[0].copy_(torch.randn(2, 8, 1, 128).to(BF16))
+    lk.sub_(3)
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    want = fa.forward_paged(*dev, lk)
+    fa.sync_status()
+    assert torch.equal(o, want[0]) and torch.equal(lse, want[1])

@@ -74,7 +74,7 @@ PAGED_ERRORS = [
     (dict(o_dtype=2), 1), (dict(causal=2), 1), (dict(scale=0.0), 1), (dict(scale=float("nan")), 1),
     (dict(pages=0), 1), (dict(page=20), 1), (dict(max_pages=0), 1), (dict(stride=-4), 1),
     (dict(Hkv=3), 1), (dict(Hkv=0), 1), (dict(B=0), 1), (dict(Nq=0), 1), (dict(B=BIG, Nq=4), 1), (dict(d=256), 2),
-    (dict(max_pages=BIG), 1), (dict(pages=BIG), 1),
+    (dict(max_pages=BIG), 1), (dict(max_pages=(BIG >> 4) + 1), 1), (dict(pages=BIG), 1),
     (dict(q=FAKE + 8), 3), (dict(o=FAKE + 4), 3), (dict(lse=FAKE + 2), 3), (dict(ws=FAKE + 8), 3),
     (dict(lk=FAKE + 1), 3), (dict(lq=FAKE + 1), 3), (dict(kp=FAKE + 2), 3), (dict(table=FAKE + 1), 3),
 ]
