@@ -890,7 +890,6 @@ cudaError_t launch_paged_d(const PagedArgs& a, cudaStream_t stream) {
     const int cut = units < 2 * tile_ctas ? units : tile_ctas + units % tile_ctas;
     t.line_out = table;
     t.counter = table + kTileLine + 3;
-    t.dual = dual;
     t.part = PartRef{table, tile_ctas, kMinTiles, cut, direct && !dual, kPairRows, dual, units, heads, pairs,
                      head_group(heads, pairs, keys, D, tile_ctas), a.part + at,
                      a.part + at + slots * kPairRows * D};
@@ -930,7 +929,7 @@ cudaError_t launch_paged_d(const PagedArgs& a, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     c.seq = all;
     c.part = t.part;
-    c.units = c.direct && !t.dual ? t.part.cut : t.part.units;
+    c.units = c.direct && !t.part.dual ? t.part.cut : t.part.units;
     c.o = a.o;
     c.lse = a.lse;
     return launch_combine<D>(c, true, a.sms, stream);

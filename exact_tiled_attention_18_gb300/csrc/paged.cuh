@@ -80,7 +80,6 @@ struct PagedTiles {
   int direct;
   // 1: a unit's rows all fit into tile A; tile B takes the same rows and every
   // other key tile, and leaves its partial result in the slot's second half
-  int dual;
   int boxed_rows;    // tiles of rows come by TMA (always but for some prefixes)
   int* counter;      // draws units from part.cut on; zero at the start
   int wait_first;    // as PagedStep's

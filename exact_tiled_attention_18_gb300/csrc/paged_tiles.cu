@@ -139,7 +139,7 @@ __device__ __forceinline__ int tile_keys(int r0, int rows, int nq, int lq, int l
   return max(keys, 0);
 }
 
-template <int D, bool PREFIX>
+template <int D, bool PREFIX, bool DUAL>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ PagedTiles p) {
@@ -298,7 +298,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // this row's visible keys from the tile's first, and how far its key
       // tiles are apart
       const int lim0 = row_end[(n & 1) * kPairRows + t * kRows + r];
-      const int stride = p.dual ? 2 * kRows : kRows;
+      constexpr int stride = DUAL ? 2 * kRows : kRows;
       float m_ref = 0.f, l = 0.f, dl = 0.f;
       for (int j = 0; j < nt; ++j) {
         ok = tile_wait(BAR(L::S_FULL + t), sn & 1, wc_idle, SITE_TILE_S, n);
@@ -559,131 +559,125 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int unit = static_cast<int>(n);
           const int na = pieces[n & 1].na, nb = pieces[n & 1].nb, clean = pieces[n & 1].clean;
           const int tiles = pieces[n & 1].tiles;
-          if (lane == 0) {
-          do {
-          if (p.dual) {
-            // key tile j belongs to row tile j & 1, whose chain S -> softmax ->
-            // P V -> next S runs beside the other's
-            auto start = [&](int t, int j) -> bool {
-              const uint32_t kpos = kvbase + 2 * j;
-              if (!wait_bounded(BAR(L::KV_FULL + kpos % S), (kpos / S) & 1, wc, SITE_TILE_MMA, unit)) return false;
-              tc_fence_after();
-              issue_s(t, kpos % S);
-              umma_commit(BAR(L::S_FULL + t));
-              umma_commit(BAR(L::KV_EMPTY + kpos % S));
-              if (j + 2 >= tiles) umma_commit(BAR(L::Q_EMPTY + t));  // the piece's last use of Q
-              return true;
-            };
-            if (na > 0) {
-              ok = wait_bounded(BAR(L::Q_FULL + 0), qa & 1, wc, SITE_TILE_MMA, unit) && start(0, 0);
-              if (!ok) break;
-              ++qa;
-            }
-            if (nb > 0) {
-              ok = wait_bounded(BAR(L::Q_FULL + 1), qb & 1, wc, SITE_TILE_MMA, unit) && start(1, 1);
-              if (!ok) break;
-              ++qb;
-            }
-            for (int j = 0; j < tiles && ok; ++j) {
-              const int t = j & 1;
-              const uint32_t vpos = kvbase + 2 * j + 1;
-              ok = wait_bounded(BAR(L::KV_FULL + vpos % S), (vpos / S) & 1, wc, SITE_TILE_MMA, unit);
-              if (!ok) break;
-              if (j == clean) mbar_arrive(BAR(L::DIRTY));
-              ok = wait_bounded(BAR(L::P_FULL + t), (t ? pb : pa) & 1, wc, SITE_TILE_MMA, unit);
-              if (!ok) break;
-              if (t) ++pb; else ++pa;
-              if (j == clean) {
-                ok = wait_bounded(BAR(L::CLEAN), cleaned & 1, wc, SITE_TILE_CLEAN, unit);
-                if (!ok) break;
-                ++cleaned;
-              }
-              tc_fence_after();
-              issue_pv(t, vpos % S, j > 1);
-              if (j + 2 >= tiles) umma_commit(BAR(L::O_FULL + t));
-              umma_commit(BAR(L::KV_EMPTY + vpos % S));
-              if (j + 2 < tiles) ok = start(t, j + 2);
-            }
-            break;
-          }
-          if (tiles > 0) {
-            ok = wait_bounded(BAR(L::KV_FULL + kvbase % S), (kvbase / S) & 1, wc, SITE_TILE_MMA, unit);
-            if (!ok) break;
-            if (na > 0) {
-              ok = wait_bounded(BAR(L::Q_FULL + 0), qa & 1, wc, SITE_TILE_MMA, unit);
-              if (!ok) break;
-              ++qa;
-              tc_fence_after();
-              issue_s(0, kvbase % S);
-              umma_commit(BAR(L::S_FULL + 0));
-              if (na == 1) umma_commit(BAR(L::Q_EMPTY + 0));  // the piece's last use of Q
-            }
-            if (nb > 0) {
-              ok = wait_bounded(BAR(L::Q_FULL + 1), qb & 1, wc, SITE_TILE_MMA, unit);
-              if (!ok) break;
-              ++qb;
-              tc_fence_after();
-              issue_s(1, kvbase % S);
-              umma_commit(BAR(L::S_FULL + 1));
-              if (nb == 1) umma_commit(BAR(L::Q_EMPTY + 1));
-            }
-          }
-          // One key tile.  STEADY: both row tiles have it and two more, and its
-          // values need no zeroing -- all but the last steps of most pieces, with nothing to decide in them: this thread's instructions
-          // are on every step's critical path.
-          auto step = [&](auto steady_tag, int j) -> bool {
-            constexpr bool STEADY = decltype(steady_tag)::value;
-            const uint32_t kpos = kvbase + 2 * j, vpos = kpos + 1, knext = kpos + 2;
-            const bool has_a = STEADY || j < na, next_a = STEADY || j + 1 < na;
-            const bool has_b = STEADY || j < nb, next_b = STEADY || j + 1 < nb;
-            const bool dirty = !STEADY && j == clean;
-            umma_commit(BAR(L::KV_EMPTY + kpos % S));  // K_j is free once S(j) of both tiles completes
-            if (!wait_bounded(BAR(L::KV_FULL + vpos % S), (vpos / S) & 1, wc, SITE_TILE_MMA, unit)) return false;
-            // the last keys' values: zeroed behind the last key by warp 10
-            // while the softmax of this tile runs
-            if (dirty) mbar_arrive(BAR(L::DIRTY));
-            auto values_ready = [&]() {
-              return !dirty || wait_bounded(BAR(L::CLEAN), cleaned & 1, wc, SITE_TILE_CLEAN, unit);
-            };
-            if (has_a) {
-              if (!wait_bounded(BAR(L::P_FULL + 0), pa & 1, wc, SITE_TILE_MMA, unit) || !values_ready()) return false;
-              ++pa;
-              tc_fence_after();
-              issue_pv(0, vpos % S, j > 0);
-              if (!next_a) umma_commit(BAR(L::O_FULL + 0));
-              if (next_a) {
-                if (!wait_bounded(BAR(L::KV_FULL + knext % S), (knext / S) & 1, wc, SITE_TILE_MMA, unit)) return false;
+          // all of a piece, by one thread
+          auto issue_piece = [&]() -> bool {
+            if constexpr (DUAL) {
+              // key tile j belongs to row tile j & 1, whose chain S -> softmax ->
+              // P V -> next S runs beside the other's
+              auto start = [&](int t, int j) -> bool {
+                const uint32_t kpos = kvbase + 2 * j;
+                if (!wait_bounded(BAR(L::KV_FULL + kpos % S), (kpos / S) & 1, wc, SITE_TILE_MMA, unit)) return false;
                 tc_fence_after();
-                issue_s(0, knext % S);
-                umma_commit(BAR(L::S_FULL + 0));
-                if (!STEADY && j + 2 == na) umma_commit(BAR(L::Q_EMPTY + 0));
+                issue_s(t, kpos % S);
+                umma_commit(BAR(L::S_FULL + t));
+                umma_commit(BAR(L::KV_EMPTY + kpos % S));
+                if (j + 2 >= tiles) umma_commit(BAR(L::Q_EMPTY + t));  // the piece's last use of Q
+                return true;
+              };
+              if (na > 0) {
+                if (!wait_bounded(BAR(L::Q_FULL + 0), qa & 1, wc, SITE_TILE_MMA, unit) || !start(0, 0)) return false;
+                ++qa;
               }
-            }
-            if (has_b) {
-              if (!wait_bounded(BAR(L::P_FULL + 1), pb & 1, wc, SITE_TILE_MMA, unit) || !values_ready()) return false;
-              ++pb;
-              tc_fence_after();
-              issue_pv(1, vpos % S, j > 0);
-              if (!next_b) umma_commit(BAR(L::O_FULL + 1));
-            }
-            if (dirty) ++cleaned;
-            umma_commit(BAR(L::KV_EMPTY + vpos % S));  // V_j is free once PV(j) of both tiles completes
-            if (next_b) {
-              if (!(has_a && next_a)) {  // otherwise tile A's S(j+1) already waited for K_{j+1}
-                if (!wait_bounded(BAR(L::KV_FULL + knext % S), (knext / S) & 1, wc, SITE_TILE_MMA, unit)) return false;
+              if (nb > 0) {
+                if (!wait_bounded(BAR(L::Q_FULL + 1), qb & 1, wc, SITE_TILE_MMA, unit) || !start(1, 1)) return false;
+                ++qb;
+              }
+              for (int j = 0; j < tiles; ++j) {
+                const int t = j & 1;
+                const uint32_t vpos = kvbase + 2 * j + 1;
+                if (!wait_bounded(BAR(L::KV_FULL + vpos % S), (vpos / S) & 1, wc, SITE_TILE_MMA, unit)) return false;
+                if (j == clean) mbar_arrive(BAR(L::DIRTY));
+                if (!wait_bounded(BAR(L::P_FULL + t), (t ? pb : pa) & 1, wc, SITE_TILE_MMA, unit)) return false;
+                if (t) ++pb; else ++pa;
+                if (j == clean) {
+                  if (!wait_bounded(BAR(L::CLEAN), cleaned & 1, wc, SITE_TILE_CLEAN, unit)) return false;
+                  ++cleaned;
+                }
                 tc_fence_after();
+                issue_pv(t, vpos % S, j > 1);
+                if (j + 2 >= tiles) umma_commit(BAR(L::O_FULL + t));
+                umma_commit(BAR(L::KV_EMPTY + vpos % S));
+                if (j + 2 < tiles && !start(t, j + 2)) return false;
               }
-              issue_s(1, knext % S);
-              umma_commit(BAR(L::S_FULL + 1));
-              if (!STEADY && j + 2 == nb) umma_commit(BAR(L::Q_EMPTY + 1));
+            } else {
+              if (tiles > 0) {
+                if (!wait_bounded(BAR(L::KV_FULL + kvbase % S), (kvbase / S) & 1, wc, SITE_TILE_MMA, unit)) return false;
+                if (na > 0) {
+                  if (!wait_bounded(BAR(L::Q_FULL + 0), qa & 1, wc, SITE_TILE_MMA, unit)) return false;
+                  ++qa;
+                  tc_fence_after();
+                  issue_s(0, kvbase % S);
+                  umma_commit(BAR(L::S_FULL + 0));
+                  if (na == 1) umma_commit(BAR(L::Q_EMPTY + 0));  // the piece's last use of Q
+                }
+                if (nb > 0) {
+                  if (!wait_bounded(BAR(L::Q_FULL + 1), qb & 1, wc, SITE_TILE_MMA, unit)) return false;
+                  ++qb;
+                  tc_fence_after();
+                  issue_s(1, kvbase % S);
+                  umma_commit(BAR(L::S_FULL + 1));
+                  if (nb == 1) umma_commit(BAR(L::Q_EMPTY + 1));
+                }
+              }
+              // One key tile.  STEADY: both row tiles have it and two more, and its
+              // values need no zeroing: all but the last steps of most pieces.
+              // Nothing is decided in such a step, since this thread's
+              // instructions are on every step's critical path.
+              auto step = [&](auto steady_tag, int j) -> bool {
+                constexpr bool STEADY = decltype(steady_tag)::value;
+                const uint32_t kpos = kvbase + 2 * j, vpos = kpos + 1, knext = kpos + 2;
+                const bool has_a = STEADY || j < na, next_a = STEADY || j + 1 < na;
+                const bool has_b = STEADY || j < nb, next_b = STEADY || j + 1 < nb;
+                const bool dirty = !STEADY && j == clean;
+                umma_commit(BAR(L::KV_EMPTY + kpos % S));  // K_j is free once S(j) of both tiles completes
+                if (!wait_bounded(BAR(L::KV_FULL + vpos % S), (vpos / S) & 1, wc, SITE_TILE_MMA, unit)) return false;
+                // the last keys' values: zeroed behind the last key by warp 10
+                // while the softmax of this tile runs
+                if (dirty) mbar_arrive(BAR(L::DIRTY));
+                auto values_ready = [&]() {
+                  return !dirty || wait_bounded(BAR(L::CLEAN), cleaned & 1, wc, SITE_TILE_CLEAN, unit);
+                };
+                if (has_a) {
+                  if (!wait_bounded(BAR(L::P_FULL + 0), pa & 1, wc, SITE_TILE_MMA, unit) || !values_ready()) return false;
+                  ++pa;
+                  tc_fence_after();
+                  issue_pv(0, vpos % S, j > 0);
+                  if (!next_a) umma_commit(BAR(L::O_FULL + 0));
+                  if (next_a) {
+                    if (!wait_bounded(BAR(L::KV_FULL + knext % S), (knext / S) & 1, wc, SITE_TILE_MMA, unit)) return false;
+                    tc_fence_after();
+                    issue_s(0, knext % S);
+                    umma_commit(BAR(L::S_FULL + 0));
+                    if (!STEADY && j + 2 == na) umma_commit(BAR(L::Q_EMPTY + 0));
+                  }
+                }
+                if (has_b) {
+                  if (!wait_bounded(BAR(L::P_FULL + 1), pb & 1, wc, SITE_TILE_MMA, unit) || !values_ready()) return false;
+                  ++pb;
+                  tc_fence_after();
+                  issue_pv(1, vpos % S, j > 0);
+                  if (!next_b) umma_commit(BAR(L::O_FULL + 1));
+                }
+                if (dirty) ++cleaned;
+                umma_commit(BAR(L::KV_EMPTY + vpos % S));  // V_j is free once PV(j) of both tiles completes
+                if (next_b) {
+                  if (!(has_a && next_a)) {  // otherwise tile A's S(j+1) already waited for K_{j+1}
+                    if (!wait_bounded(BAR(L::KV_FULL + knext % S), (knext / S) & 1, wc, SITE_TILE_MMA, unit)) return false;
+                    tc_fence_after();
+                  }
+                  issue_s(1, knext % S);
+                  umma_commit(BAR(L::S_FULL + 1));
+                  if (!STEADY && j + 2 == nb) umma_commit(BAR(L::Q_EMPTY + 1));
+                }
+                return true;
+              };
+              const int steady = min(na, nb) - 2;
+              for (int j = 0; j < tiles; ++j)
+                if (!(j < steady && j != clean ? step(std::true_type{}, j) : step(std::false_type{}, j))) return false;
             }
             return true;
           };
-          const int steady = min(na, nb) - 2;
-          for (int j = 0; j < tiles && ok; ++j)
-            ok = j < steady && j != clean ? step(std::true_type{}, j) : step(std::false_type{}, j);
-          } while (false);
-          }
+          if (lane == 0) ok = issue_piece();
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           kvbase += 2 * tiles;
@@ -719,7 +713,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ++qn[t];
             if (lane == 0) {
               mbar_arrive_expect_tx(BAR(L::Q_FULL + t), L::kTileBytes);
-              const int row = r0 + (p.dual ? 0 : t * kRows);
+              const int row = r0 + (DUAL ? 0 : t * kRows);
 #pragma unroll
               for (int c = 0; c < CB; ++c) {
                 const uint32_t dst = sbase + t * L::kTileBytes + c * 16384;
@@ -734,7 +728,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
         }
         constexpr int RL = kPairRows / 32;  // rows a lane
-        auto row_of = [&](int i) { return p.dual ? i & (kRows - 1) : i; };
+        auto row_of = [&](int i) { return DUAL ? i & (kRows - 1) : i; };
         int lq[RL], lk[RL], rb[RL];
         const int xb = x.b;
 #pragma unroll
@@ -784,7 +778,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             int end = 0;
             if (row < space && qi < lq[k]) end = (p.causal ? min(qi + lk[k] - lq[k] + 1, lk[k]) : lk[k]) - origin;
             if (PREFIX) end = min(end, p.seq.prefix_len);
-            end_w[buf + i] = end - tile0 - (p.dual ? i & kRows : 0);  // tile B of two begins a key tile later
+            end_w[buf + i] = end - tile0 - (DUAL ? i & kRows : 0);  // tile B of two begins a key tile later
           }
           mbar_arrive_warp(BAR(L::ROWS_FULL + (n & 1)));
         }
@@ -846,7 +840,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           x.tile = at - line[lo];
           const int tiles = line[lo + 1] - line[lo];
           len = min(tiles - x.tile, stop - at);
-          x.whole = p.direct && !p.dual && len == tiles;
+          x.whole = p.direct && !DUAL && len == tiles;
           x.slot = p.part.two_a_cta ? 2 * blockIdx.x + (at == at0 ? 0 : 1) : u + blockIdx.x;
           at += len;
         } else if (cut < p.part.units) {
@@ -854,7 +848,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           u = __shfl_sync(0xffffffffu, u, 0);
           if (u < p.part.units) {
             len = unit_tiles(u);
-            x.whole = p.direct && !p.dual;
+            x.whole = p.direct && !DUAL;
             x.slot = u + gridDim.x;
           } else {
             u = -1;
@@ -867,7 +861,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           x.na = max(0, min((ka + kRows - 1) / kRows - x.tile, len));
           x.nb = max(0, min((kb + kRows - 1) / kRows - x.tile, len));
           x.tiles = max(x.na, x.nb);
-          if (p.dual) {
+          if constexpr (DUAL) {
             x.nb = x.tiles / 2;
             x.na = x.tiles - x.nb;
           }
@@ -891,11 +885,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int D, bool PREFIX>
+template <int D, bool PREFIX, bool DUAL>
 cudaError_t launch_t(const PagedTiles& p, const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                      int ctas, cudaStream_t stream) {
   using L = TileLayout<D>;
-  auto kern = paged_tiles_kernel<D, PREFIX>;
+  auto kern = paged_tiles_kernel<D, PREFIX, DUAL>;
   static std::atomic<unsigned long long> ready{0};
   cudaError_t e = setup_kernel_once(kern, L::kSmemBytes, kLaunchRegs, ready);
   if (e != cudaSuccess) return e;
@@ -906,11 +900,14 @@ cudaError_t launch_t(const PagedTiles& p, const CUtensorMap& tm_q, const CUtenso
 
 cudaError_t launch_tiles(const PagedTiles& p, const CUtensorMap& tm_q, const CUtensorMap& tm_k,
                          const CUtensorMap& tm_v, int d, int ctas, cudaStream_t stream) {
-  if (d == 64)
-    return p.prefix_table ? launch_t<64, true>(p, tm_q, tm_k, tm_v, ctas, stream)
-                          : launch_t<64, false>(p, tm_q, tm_k, tm_v, ctas, stream);
-  return p.prefix_table ? launch_t<128, true>(p, tm_q, tm_k, tm_v, ctas, stream)
-                        : launch_t<128, false>(p, tm_q, tm_k, tm_v, ctas, stream);
+  auto launch = [&](auto prefix, auto dual) {
+    return d == 64 ? launch_t<64, prefix.value, dual.value>(p, tm_q, tm_k, tm_v, ctas, stream)
+                   : launch_t<128, prefix.value, dual.value>(p, tm_q, tm_k, tm_v, ctas, stream);
+  };
+  const std::true_type yes;
+  const std::false_type no;
+  if (p.prefix_table) return p.part.dual ? launch(yes, yes) : launch(yes, no);
+  return p.part.dual ? launch(no, yes) : launch(no, no);
 }
 
 }  // namespace fa
