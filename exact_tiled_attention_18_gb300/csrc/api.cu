@@ -487,8 +487,6 @@ fa_status paged_common(const void* q, const void* k_pages, const void* v_pages, 
   fa::PagedArgs a;
   std::memset(&a, 0, sizeof(a));
   a.q = static_cast<const uint16_t*>(q);
-  a.k_pages = static_cast<const uint16_t*>(k_pages);
-  a.v_pages = static_cast<const uint16_t*>(v_pages);
   a.table = fa::PageTable{block_table, table_stride, max_pages, page_size, num_pages};
   a.prefix_table = prefix_table;
   a.prefix_len = prefix_len;
@@ -896,7 +894,7 @@ fa_status fa_rope(const void* x, int x_dtype, long long x_stride_b, long long x_
   const fa::Strides xs = used_strides(x_stride_b, x_stride_h, x_stride_n, B, H, N);
   const fa::Strides ys = used_strides(y_stride_b, y_stride_h, y_stride_n, B, H, N);
   // rows of y that fall on one another would race
-  if ((B > 1 && ys.b == 0) || (H > 1 && ys.h == 0) || (N > 1 && ys.n == 0)) return FA_ERR_INVALID_ARG;
+  if ((B > 1 && ys.b < d) || (H > 1 && ys.h < d) || (N > 1 && ys.n < d)) return FA_ERR_INVALID_ARG;
   // in place only element for element
   if (x == y && (x_dtype != y_dtype || xs.b != ys.b || xs.h != ys.h || xs.n != ys.n)) return FA_ERR_INVALID_ARG;
   if (!aligned(x, 16) || !aligned(y, 16)) return FA_ERR_MISALIGNED;

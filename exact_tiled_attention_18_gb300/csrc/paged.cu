@@ -13,7 +13,7 @@
 // rows of a 16-high tile, and the mma rate is what comes next after HBM.
 //
 //   paged_steps_kernel    persistent CTAs of four compute warps and a TMA warp,
-//                         two an SM.  The key tiles (64 keys of one key head)
+//                         two or three an SM.  The key tiles (64 keys of one key head)
 //                         of all sequences form one line, cut into equal
 //                         ranges, one a CTA: the lengths stay on the device,
 //                         and a batch of very different lengths is balanced to
@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(kStepThreads, step_ctas_per_sm<RB>())
     prefetch_tensormap(&tm_k16);
     prefetch_tensormap(&tm_v16);
   }
-  if (p.wait_first) grid_wait();
+  if (p.wait_first) grid_wait(); else grid_overlap();
   grid_trigger();
   // the scratch of the scan is the row-maxima area, unused so far
   int* len_k = line + kLineSequences + 1;

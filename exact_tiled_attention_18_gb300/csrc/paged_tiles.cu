@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefetch_tensormap(&tm_k);
     prefetch_tensormap(&tm_v);
   }
-  if (p.wait_first) grid_wait();
+  if (p.wait_first) grid_wait(); else grid_overlap();
   grid_trigger();
   // the prefix's keys that some sequence reaches
   int reach = 0;

@@ -283,6 +283,7 @@ int heads_per_thread(long long tokens, int lanes, int heads, int sms, int most) 
   long long n = tokens * lanes * heads / (static_cast<long long>(sms) * 1024);
   if (n < 1) n = 1;
   if (n > most) n = most;
+  if (n < (heads + 65534) / 65535) n = (heads + 65534) / 65535;  // the grid's second axis
   if (n > heads) n = heads;
   const int groups = static_cast<int>((heads + n - 1) / n);
   return (heads + groups - 1) / groups;

@@ -75,7 +75,6 @@ struct PagedArgs {
   CUtensorMap st_k, st_v;     // step kernel: blocked maps of the same, boxes of box_rows whole rows
   CUtensorMap st_k16, st_v16; // and of 16
   const uint16_t *q;          // [B][Hq][Nq][d]
-  const uint16_t *k_pages, *v_pages;
   PageTable table;
   const int* prefix_table;    // pages of the shared prefix
   int prefix_len;             // keys of the shared prefix, a multiple of page_size; 0: none
@@ -145,6 +144,12 @@ __device__ __forceinline__ void record_bad_page(int* status, int site, int block
     __threadfence();
   }
 }
+
+// For a kernel that does not wait for the one before it at its start, because
+// that one has nothing for it: what it reads was written by kernels further
+// back, which that one has waited for before it let this one start; a fence
+// keeps this SM's L1 from answering with what it held before.
+__device__ __forceinline__ void grid_overlap() { __threadfence(); }
 
 // Valid lengths of sequence b: new tokens and keys in the cache.
 __device__ __forceinline__ void paged_lens(const int* seqlens_q, const int* seqlens_k, int b, int nq, int capacity,

@@ -320,3 +320,19 @@ def test_append_captured_steps():
         want_v = serving.place_tokens(want_v, to64(nv), table.numpy(), [1] * B, lens)
     torch.cuda.synchronize()
     assert np.array_equal(to64(a.cpu()), want_k) and np.array_equal(to64(b.cpu()), want_v)
+
+
+def test_many_heads_of_one_token():
+    """More heads than a grid's second axis has blocks."""
+    H, d = 70000, 64
+    x = torch.randn(1, H, 1, d, dtype=BF16, device="cuda")
+    turns = fa.rope_turns(d, device="cuda")
+    pos = torch.tensor([77], dtype=torch.int32, device="cuda")
+    y = fa.rope_forward(x, turns, pos)
+    assert torch.equal(y.view(H, 1, 1, d), fa.rope_forward(x.view(H, 1, 1, d), turns, pos))
+    kp, vp = (torch.zeros(1, H, 16, d, dtype=BF16, device="cuda") for _ in range(2))
+    fa.kv_append(x, x, kp, vp, torch.zeros(1, 1, dtype=torch.int32, device="cuda"),
+                 torch.tensor([5], dtype=torch.int32, device="cuda"), turns=turns, positions=pos.view(1, 1))
+    fa.sync_status()
+    assert torch.equal(kp[:, :, 4:5], y) and torch.equal(vp[:, :, 4:5], x)
+    assert not kp[:, :, :4].any() and not vp[:, :, 5:].any()

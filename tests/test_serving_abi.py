@@ -34,7 +34,7 @@ ROPE = dict(x=FAKE, x_dtype=1, xs=(4096, 1024, 64), y=FAKE + 65536, y_dtype=1, y
     (dict(B=0), 1), (dict(H=0), 1), (dict(N=-1), 1), (dict(B=BIG, H=2), 1), (dict(d=96), 2), (dict(d=32), 2),
     (dict(x=FAKE + 8), 3), (dict(y=FAKE + 2), 3), (dict(turns=FAKE + 4), 3), (dict(positions=FAKE + 2), 3),
     (dict(xs=(4096, 1024, 65)), 3), (dict(ys=(4096, 1028, 64)), 3), (dict(xs=(-4096, 1024, 64)), 1),
-    (dict(ys=(0, 1024, 64)), 1), (dict(psb=-1), 1),
+    (dict(ys=(0, 1024, 64)), 1), (dict(psb=-1), 1), (dict(ys=(4096, 1024, 48)), 1), (dict(ys=(4096, 32, 256)), 1),
     (dict(y=FAKE, ys=(8192, 1024, 64)), 1),      # in place with other strides
     (dict(y=FAKE, y_dtype=0), 1),                # in place with another type
 ])
