@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(kStepThreads, step_ctas_per_sm<RB>())
   });
   auto starts = [&](int b) { return line[b]; };
   const int total = line[p.seq.B] * p.seq.Hkv;
-  const Ranges ranges = make_ranges(total, gridDim.x, p.part.min_tiles);
+  const Ranges ranges = make_ranges<kEvenSteps>(total, gridDim.x, p.part.min_tiles);
   if (blockIdx.x == 0) {
     for (int i = threadIdx.x; i <= p.seq.B; i += kStepThreads) p.line_out[i] = line[i];
     if (threadIdx.x == 0) {

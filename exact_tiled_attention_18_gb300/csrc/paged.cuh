@@ -12,8 +12,12 @@ constexpr int kStepRows = 32;          // rows a key head that the step kernel t
 constexpr int kLineSequences = 256;    // sequences a launch of the step kernel: the line's table is in shared memory
 constexpr int kLineWords = 528;        // 4-byte words of a line in the workspace, a multiple of 4
 constexpr int kMaxCtas = 512;
-constexpr int kMinSteps = 1;           // key tiles (64 keys) a CTA of the step kernel takes at least
-constexpr int kMinTiles = 2;           // key tiles (128 keys) a CTA of the tile kernel takes at least
+// Key tiles a CTA takes at least.  Step kernel (64 keys): 1000 keys of 8 key
+// heads 6.9 us with 1, 7.3 with 2, 8.5 with 4.  Tile kernel (128 keys): 64 rows of 8
+// heads on 8, 512 keys 15.0 / 15.5 / 16.8 us with 1 / 2 / 4, 4096 keys 18.1 / 17.4 /
+// 19.0, 64 sequences behind a prefix of 1024 keys 30.3 / 27.2 / 29.8.
+constexpr int kMinSteps = 1, kMinTiles = 2;
+constexpr int kEvenSteps = 2, kEvenTiles = 8;  // (make_ranges)
 constexpr int kMaxTileCtas = 160;
 constexpr int kTileLine = 2 * kMaxTileCtas;  // units of the tile kernel's line
 constexpr int kPairRows = 256;         // query rows a unit of the tile kernel: two 128-row tiles
@@ -118,13 +122,27 @@ __device__ __forceinline__ uint32_t sw128(int r, int c) {
 }
 
 // The line's tiles in equal ranges, one a CTA (the first `more` CTAs have one
-// tile more than `base`), for no more CTAs than leave each `least` tiles.
+// tile more than `base`), for no more CTAs than leave each `least` tiles and,
+// where the longest range has at most EVEN tiles, for no more than ranges of
+// that length need: as quick, with fewer partial results, and units more often
+// cut into equal parts.  (One sequence of 30000 keys, one key head, 469 tiles
+// for 456 CTAs: 14.6 us without, 10.4 with it; 4 chunks of 100 tokens over 1500
+// keys, 32 heads on 8: 33.4 and 28.1 us.  The shared prefix's tiles do without:
+// drafted tokens behind 8208 keys 33.5 us, 34.2 with it, for CTAs that end
+// early make room for the step kernel's.)
 struct Ranges {
   int base, more, total;
 };
 
+template <int EVEN>
 __device__ __forceinline__ Ranges make_ranges(int total, int ctas, int least) {
-  const int n = max(1, min(ctas, total / least));
+  int n = max(1, min(ctas, total / least));
+  if constexpr (EVEN == 2) {  // (without a division, which a step of few keys would notice)
+    if (total > n && total <= 2 * n) n = (total + 1) >> 1;
+  } else if constexpr (EVEN > 2) {
+    const int longest = (total + n - 1) / n;
+    if (longest > 0 && longest <= EVEN) n = (total + longest - 1) / longest;
+  }
   const int base = total / n;
   return Ranges{base, total - base * n, total};
 }

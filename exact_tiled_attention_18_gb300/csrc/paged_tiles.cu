@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (blockIdx.x == 0) {
     for (int i = threadIdx.x; i <= cut; i += kThreads) p.line_out[i] = line[i];
     if (threadIdx.x == 0) {
-      const Ranges ranges = make_ranges(total, gridDim.x, p.part.min_tiles);
+      const Ranges ranges = make_ranges<PREFIX ? 0 : kEvenTiles>(total, gridDim.x, p.part.min_tiles);
       p.line_out[cut + 1] = ranges.base;
       p.line_out[cut + 2] = ranges.more;
     }
@@ -820,7 +820,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else {
       // ------------------------------------------------------------- pieces
-      const Ranges ranges = make_ranges(total, gridDim.x, p.part.min_tiles);
+      const Ranges ranges = make_ranges<PREFIX ? 0 : kEvenTiles>(total, gridDim.x, p.part.min_tiles);
       const int at0 = range_start(ranges, blockIdx.x), stop = range_start(ranges, blockIdx.x + 1);
       int at = at0;  // on the line; then units are drawn
       for (uint32_t n = 0;; ++n) {
