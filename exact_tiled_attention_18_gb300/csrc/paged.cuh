@@ -8,14 +8,18 @@
 
 namespace fa {
 
-constexpr int kStepRows = 32;          // rows a key head that the step kernel takes
+// Rows a key head that the step kernel takes; more are the tile kernel's, which
+// takes 128 whether they are there or not.  (8 sequences x 8 heads x 8192 keys: 24
+// rows 54 us here, 64 there; 32 rows 61 and 63; 38 sequences of 512 keys, 32
+// rows, 21 and 37.  64 rows are 65 us there.)
+constexpr int kStepRows = 32;
 constexpr int kLineSequences = 256;    // sequences a launch of the step kernel: the line's table is in shared memory
 constexpr int kLineWords = 528;        // 4-byte words of a line in the workspace, a multiple of 4
 constexpr int kMaxCtas = 512;
 // Key tiles a CTA takes at least.  Step kernel (64 keys): 1000 keys of 8 key
-// heads 6.9 us with 1, 7.3 with 2, 8.5 with 4.  Tile kernel (128 keys): 64 rows of 8
-// heads on 8, 512 keys 15.0 / 15.5 / 16.8 us with 1 / 2 / 4, 4096 keys 18.1 / 17.4 /
-// 19.0, 64 sequences behind a prefix of 1024 keys 30.3 / 27.2 / 29.8.
+// heads 6.9 us with 1, 7.3 with 2, 8.5 with 4.  Tile kernel (128 keys): 64 rows
+// of 8 heads on 8, 512 keys 15.0 / 15.5 / 16.8 us with 1 / 2 / 4, 4096 keys
+// 18.1 / 17.4 / 19.0, 64 sequences behind a prefix of 1024 keys 30.3 / 27.2 / 29.8.
 constexpr int kMinSteps = 1, kMinTiles = 2;
 constexpr int kEvenSteps = 2, kEvenTiles = 8;  // (make_ranges)
 constexpr int kMaxTileCtas = 160;
@@ -43,7 +47,11 @@ struct PartRef {
   int cut;
   int two_a_cta;
   int slot_rows;
-  int dual;            // the tile kernel's dual mode: two partial results a piece
+  // 1: a unit of the tile kernel has at most 128 rows, so that its tile B would
+  // be empty: tile B takes the same rows and every other key tile, and leaves
+  // its partial result in the slot's second half.  (8 sequences x 8 heads x 64
+  // rows x 8192 keys: 65 us, 71 with tile A alone.)
+  int dual;
   int units;
   int heads, pairs, group;  // the tile kernel: (sequence, head)s, row pairs of each, heads dealt out together
   float *o, *lse;      // [slot][slot_rows][d], [slot][slot_rows] (log2 units)
@@ -82,8 +90,6 @@ struct PagedTiles {
   int* line_out;     // the line's table, for the combine
   PartRef part;
   int direct;
-  // 1: a unit's rows all fit into tile A; tile B takes the same rows and every
-  // other key tile, and leaves its partial result in the slot's second half
   int boxed_rows;    // tiles of rows come by TMA (always but for some prefixes)
   int* counter;      // draws units from part.cut on; zero at the start
   int wait_first;    // as PagedStep's
@@ -111,6 +117,44 @@ cudaError_t launch_tiles(const PagedTiles& p, const CUtensorMap& tm_q, const CUt
                          const CUtensorMap& tm_v, int d, int ctas, cudaStream_t stream);
 
 #if defined(__CUDACC__)
+// 4-D form of tma_load_3d (ptx.cuh).
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1,
+                                            int c2, int c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
+      : "memory");
+}
+
+__device__ __forceinline__ void ld_shared_v4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+
+// 16 bytes global -> shared without registers; `bytes` 0 writes zeros.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+
+// Until at most N of this thread's committed groups are in flight.
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+
 __device__ __forceinline__ void seq_lens(const PagedSeq& s, int b, int& lq, int& lk) {
   paged_lens(s.seqlens_q, s.seqlens_k, b, s.Nq, s.capacity, lq, lk);
 }

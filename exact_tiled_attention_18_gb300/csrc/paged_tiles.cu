@@ -27,6 +27,15 @@
 //    0 * NaN would poison the product with V: a spare warp zeroes them in the
 //    last tile before that product is issued.
 //
+// Measured (whole calls): a square prompt of 16 heads x 16384 tokens 1574
+// TFLOP/s, 32 heads under the causal rule 1409 to 1442; two chunks of 1000
+// tokens, 32 heads on 8, over 9001 and 16384 keys 332 us = 1200 TFLOP/s (this
+// kernel 317, of which a piece's beginning and end cost about 2.7 us each); 2048
+// rows of 8 heads behind 32768 shared keys 190 us in this kernel.  The tensor
+// pipe is 54 to 58% busy in the last two; with pages of 16 keys a square
+// prompt runs at 1316 TFLOP/s, bound by the issue of its eight boxes a tile and
+// block.
+//
 //   warps 0-3  softmax of tile A     warp 8   TMA producer
 //   warps 4-7  softmax of tile B     warp 9   MMA issuer, owns tensor memory
 //                                    warp 10  gathers rows; zeroes values behind the last key
