@@ -810,7 +810,8 @@ cudaError_t launch_steps(const PagedArgs& a, const PagedStep& p, int ctas, cudaS
   static std::atomic<unsigned long long> ready{0};
   cudaError_t e = setup_kernel_once(kern, L::kSmemBytes, 0, ready);
   if (e != cudaSuccess) return e;
-  return launch_overlapped(kern, dim3(ctas), kStepThreads, L::kSmemBytes, stream, a.st_k, a.st_v, a.st_k16, a.st_v16, p);
+  return launch_overlapped(kern, dim3(ctas), kStepThreads, L::kSmemBytes, stream, a.st_k, a.st_v, a.st_k16, a.st_v16,
+                           p);
 }
 
 // Warps a row: as many as the rows leave room for on the GPU at once, for the

@@ -568,6 +568,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int unit = static_cast<int>(n);
           const int na = pieces[n & 1].na, nb = pieces[n & 1].nb, clean = pieces[n & 1].clean;
           const int tiles = pieces[n & 1].tiles;
+          auto arrived = [&](int bar, uint32_t phase) {
+            return wait_bounded(BAR(bar), phase & 1, wc, SITE_TILE_MMA, unit);
+          };
           // all of a piece, by one thread
           auto issue_piece = [&]() -> bool {
             if constexpr (DUAL) {
@@ -575,7 +578,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               // P V -> next S runs beside the other's
               auto start = [&](int t, int j) -> bool {
                 const uint32_t kpos = kvbase + 2 * j;
-                if (!wait_bounded(BAR(L::KV_FULL + kpos % S), (kpos / S) & 1, wc, SITE_TILE_MMA, unit)) return false;
+                if (!arrived(L::KV_FULL + kpos % S, kpos / S)) return false;
                 tc_fence_after();
                 issue_s(t, kpos % S);
                 umma_commit(BAR(L::S_FULL + t));
@@ -584,19 +587,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                 return true;
               };
               if (na > 0) {
-                if (!wait_bounded(BAR(L::Q_FULL + 0), qa & 1, wc, SITE_TILE_MMA, unit) || !start(0, 0)) return false;
+                if (!arrived(L::Q_FULL + 0, qa) || !start(0, 0)) return false;
                 ++qa;
               }
               if (nb > 0) {
-                if (!wait_bounded(BAR(L::Q_FULL + 1), qb & 1, wc, SITE_TILE_MMA, unit) || !start(1, 1)) return false;
+                if (!arrived(L::Q_FULL + 1, qb) || !start(1, 1)) return false;
                 ++qb;
               }
               for (int j = 0; j < tiles; ++j) {
                 const int t = j & 1;
                 const uint32_t vpos = kvbase + 2 * j + 1;
-                if (!wait_bounded(BAR(L::KV_FULL + vpos % S), (vpos / S) & 1, wc, SITE_TILE_MMA, unit)) return false;
+                if (!arrived(L::KV_FULL + vpos % S, vpos / S)) return false;
                 if (j == clean) mbar_arrive(BAR(L::DIRTY));
-                if (!wait_bounded(BAR(L::P_FULL + t), (t ? pb : pa) & 1, wc, SITE_TILE_MMA, unit)) return false;
+                if (!arrived(L::P_FULL + t, t ? pb : pa)) return false;
                 if (t) ++pb; else ++pa;
                 if (j == clean) {
                   if (!wait_bounded(BAR(L::CLEAN), cleaned & 1, wc, SITE_TILE_CLEAN, unit)) return false;
@@ -610,9 +613,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             } else {
               if (tiles > 0) {
-                if (!wait_bounded(BAR(L::KV_FULL + kvbase % S), (kvbase / S) & 1, wc, SITE_TILE_MMA, unit)) return false;
+                if (!arrived(L::KV_FULL + kvbase % S, kvbase / S)) return false;
                 if (na > 0) {
-                  if (!wait_bounded(BAR(L::Q_FULL + 0), qa & 1, wc, SITE_TILE_MMA, unit)) return false;
+                  if (!arrived(L::Q_FULL + 0, qa)) return false;
                   ++qa;
                   tc_fence_after();
                   issue_s(0, kvbase % S);
@@ -620,7 +623,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                   if (na == 1) umma_commit(BAR(L::Q_EMPTY + 0));  // the piece's last use of Q
                 }
                 if (nb > 0) {
-                  if (!wait_bounded(BAR(L::Q_FULL + 1), qb & 1, wc, SITE_TILE_MMA, unit)) return false;
+                  if (!arrived(L::Q_FULL + 1, qb)) return false;
                   ++qb;
                   tc_fence_after();
                   issue_s(1, kvbase % S);
@@ -639,7 +642,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool has_b = STEADY || j < nb, next_b = STEADY || j + 1 < nb;
                 const bool dirty = !STEADY && j == clean;
                 umma_commit(BAR(L::KV_EMPTY + kpos % S));  // K_j is free once S(j) of both tiles completes
-                if (!wait_bounded(BAR(L::KV_FULL + vpos % S), (vpos / S) & 1, wc, SITE_TILE_MMA, unit)) return false;
+                if (!arrived(L::KV_FULL + vpos % S, vpos / S)) return false;
                 // the last keys' values: zeroed behind the last key by warp 10
                 // while the softmax of this tile runs
                 if (dirty) mbar_arrive(BAR(L::DIRTY));
@@ -647,13 +650,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                   return !dirty || wait_bounded(BAR(L::CLEAN), cleaned & 1, wc, SITE_TILE_CLEAN, unit);
                 };
                 if (has_a) {
-                  if (!wait_bounded(BAR(L::P_FULL + 0), pa & 1, wc, SITE_TILE_MMA, unit) || !values_ready()) return false;
+                  if (!arrived(L::P_FULL + 0, pa) || !values_ready()) return false;
                   ++pa;
                   tc_fence_after();
                   issue_pv(0, vpos % S, j > 0);
                   if (!next_a) umma_commit(BAR(L::O_FULL + 0));
                   if (next_a) {
-                    if (!wait_bounded(BAR(L::KV_FULL + knext % S), (knext / S) & 1, wc, SITE_TILE_MMA, unit)) return false;
+                    if (!arrived(L::KV_FULL + knext % S, knext / S)) return false;
                     tc_fence_after();
                     issue_s(0, knext % S);
                     umma_commit(BAR(L::S_FULL + 0));
@@ -661,7 +664,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                   }
                 }
                 if (has_b) {
-                  if (!wait_bounded(BAR(L::P_FULL + 1), pb & 1, wc, SITE_TILE_MMA, unit) || !values_ready()) return false;
+                  if (!arrived(L::P_FULL + 1, pb) || !values_ready()) return false;
                   ++pb;
                   tc_fence_after();
                   issue_pv(1, vpos % S, j > 0);
@@ -671,7 +674,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 umma_commit(BAR(L::KV_EMPTY + vpos % S));  // V_j is free once PV(j) of both tiles completes
                 if (next_b) {
                   if (!(has_a && next_a)) {  // otherwise tile A's S(j+1) already waited for K_{j+1}
-                    if (!wait_bounded(BAR(L::KV_FULL + knext % S), (knext / S) & 1, wc, SITE_TILE_MMA, unit)) return false;
+                    if (!arrived(L::KV_FULL + knext % S, knext / S)) return false;
                     tc_fence_after();
                   }
                   issue_s(1, knext % S);
