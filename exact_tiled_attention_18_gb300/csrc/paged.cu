@@ -20,7 +20,8 @@
 //                         balanced to one tile.  Where a sequence's tiles fall
 //                         into more than one range each leaves a partial
 //                         result.
-//   paged_combine_kernel  merges a row's partial results by their log-sum-exp.
+//   merge_rows_kernel     merges a row's partial results by their log-sum-exp
+//                         (merge_lanes_kernel: with a prefix, or the tile kernel's).
 //
 // Within a tile each warp multiplies the rows with its 16 keys, the warps
 // agree on the row maxima through shared memory, exchange the probabilities
@@ -47,6 +48,7 @@
 #include <math_constants.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "internal.h"
 #include "paged.cuh"
@@ -648,19 +650,61 @@ __device__ __forceinline__ int tile_unit(const PartRef& r, int bh, int pair) {
 // Rows of a unit.
 __host__ __device__ __forceinline__ int rows_of_unit(const PartRef& r) { return r.dual ? kTileRows : r.slot_rows; }
 
+// Where column `col` (a multiple of 4) of row `row` of the tile kernel's lies.
+__device__ __forceinline__ long long tile_part(long long row, int col, int d) {
+  return (row & ~31LL) * d + (col >> 2) * 128 + (row & 31) * 4;
+}
+
 __device__ __forceinline__ long long piece_row(const PartRef& r, const Pieces& x, int k, int in) {
   const int slot = r.two_a_cta ? 2 * (x.c0 + k) + (k > 0 || x.first_whole ? 0 : 1) : x.slot + x.c0 + k;
   return static_cast<long long>(slot) * r.slot_rows + in;
 }
 
-// Merges rows' partial results: those of the sequence's own keys and those of
-// the shared prefix.  A warp takes RPW neighbouring rows of one unit (their
-// pieces are the same) or, where rows are few and pieces many, WARPS warps
-// share one row.  TILES: the sequences' part comes from the tile kernel, whose
-// units are row pairs.  Bound by instructions and by the latency of two rounds
-// of loads (where the pieces are, the pieces).
-template <int D, int WARPS, int RPW, bool TILES>
-__global__ void __launch_bounds__(256) paged_combine_kernel(const __grid_constant__ PagedCombine p) {
+// The running merge of partial results: maximum, sum and C columns.
+template <int C>
+struct Merged {
+  float top, sum, acc[C];
+
+  __device__ __forceinline__ void clear() {
+    top = -CUDART_INF_F;
+    sum = 0.f;
+#pragma unroll
+    for (int c = 0; c < C; ++c) acc[c] = 0.f;
+  }
+
+  // `lse` (U of them, -inf: none) and their columns
+  template <int U>
+  __device__ __forceinline__ void add(const float (&lse)[U], const float (&v)[U][C]) {
+    float m = top;
+#pragma unroll
+    for (int u = 0; u < U; ++u) m = fmaxf(m, lse[u]);
+    if (m == -CUDART_INF_F) return;
+    const float g = ex2_approx(top - m);
+    top = m;
+    sum *= g;
+#pragma unroll
+    for (int c = 0; c < C; ++c) acc[c] *= g;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (lse[u] == -CUDART_INF_F) continue;
+      const float f = ex2_approx(lse[u] - m);
+      sum += f;
+#pragma unroll
+      for (int c = 0; c < C; ++c) acc[c] = fmaf(f, v[u][c], acc[c]);
+    }
+  }
+
+  __device__ __forceinline__ float lse() const { return sum > 0.f ? (top + __log2f(sum)) * kLn2 : -CUDART_INF_F; }
+  __device__ __forceinline__ float scale() const { return sum > 0.f ? __fdividef(1.f, sum) : 0.f; }
+};
+
+// Merges the rows of the step kernel's units where there is no prefix.  A warp
+// takes RPW neighbouring rows of one unit (their pieces are the same) or, where
+// rows are few and pieces many, WARPS warps share one row; a lane takes D / 32
+// columns.  Bound by instructions and by the latency of two rounds of loads
+// (where the pieces are, the pieces).
+template <int D, int WARPS, int RPW>
+__global__ void __launch_bounds__(256) merge_rows_kernel(const __grid_constant__ PagedCombine p) {
   static_assert(WARPS == 1 || RPW == 1, "one or the other");
   constexpr int CW = D / 32;
   constexpr int U = WARPS > 1 ? 4 : 2;  // pieces in flight
@@ -668,107 +712,50 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const __grid_constan
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int sub = warp % WARPS;
   const int rows = p.seq.G * p.seq.Nq;
-  const int unit_rows = rows_of_unit(p.part);
-  const unsigned groups = (unit_rows + RPW - 1) / RPW;  // of rows, in a unit
+  const unsigned groups = (rows + RPW - 1) / RPW;  // of rows, in a unit
   const unsigned item = blockIdx.x * (8 / WARPS) + warp / WARPS;
   const int unit = static_cast<int>(min(item / groups, static_cast<unsigned>(p.units - 1)));
-  const int row_in = static_cast<int>(item % groups) * RPW;
-  bool in = item < p.units * groups;
-  int b, head, r0;
-  if constexpr (TILES) {
-    const int g = unit / (p.part.group * p.part.pairs);
-    const int i = unit - g * p.part.group * p.part.pairs;
-    const int hs = min(p.part.group, p.part.heads - g * p.part.group);
-    const int level = i / hs;
-    const int bh = g * p.part.group + i - level * hs;
-    b = bh / p.seq.Hkv;
-    head = bh - b * p.seq.Hkv;
-    r0 = (p.part.pairs - 1 - level) * kPairRows + row_in;
-    in = in && r0 < rows;
-  } else {
-    b = unit / p.seq.Hkv;
-    head = unit - b * p.seq.Hkv;
-    r0 = row_in;
-  }
-  const bool with_prefix = p.prefix.o != nullptr;
-  const int all = (p.b0 + b) * rows + r0;  // row among all sequences'
-  const int prefix_pair = all / kPairRows, prefix_row = all % kPairRows;
+  const int r0 = static_cast<int>(item % groups) * RPW;
+  const bool in = item < p.units * groups;
+  const int b = unit / p.seq.Hkv, head = unit - b * p.seq.Hkv;
   grid_wait();
-  const Pieces own = TILES ? tile_pieces(p.part, unit) : step_pieces(p.part, b, head, p.seq.Hkv);
-  Pieces pre{0, 0, 0, false};
-  if (with_prefix) pre = tile_pieces(p.prefix, tile_unit(p.prefix, head, prefix_pair));
-  const bool skip = !in || (p.direct && !p.part.dual && own.n == 1);  // written by the only CTA that had it
-  const int count = skip ? 0 : min(RPW, TILES ? min(rows - r0, unit_rows - row_in) : unit_rows - row_in);
-  float M[RPW], sum[RPW], acc[RPW][CW];
+  const Pieces own = step_pieces(p.part, b, head, p.seq.Hkv);
+  const bool skip = !in || (p.direct && own.n == 1);  // written by the only CTA that had it
+  const int count = skip ? 0 : min(RPW, rows - r0);
+  Merged<CW> m[RPW];
 #pragma unroll
-  for (int q = 0; q < RPW; ++q) {
-    M[q] = -CUDART_INF_F;
-    sum[q] = 0.f;
+  for (int q = 0; q < RPW; ++q) m[q].clear();
+  auto load = [&](const float* src, float (&v)[CW]) {
+    if constexpr (CW == 4)
+      *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(src);
+    else
+      *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(src);
+  };
+  const int n = count > 0 ? own.n : 0;
+  for (int i = sub; i < n; i += WARPS * U) {
+    float lse[RPW][U], v[RPW][U][CW];
 #pragma unroll
-    for (int c = 0; c < CW; ++c) acc[q][c] = 0.f;
-  }
-  // rows [q0, qn) of the warp's, the first of which is row in_slot + q0 of x
-  auto gather = [&](const PartRef& ref, const Pieces& x, int in_slot, int q0, int qn) {
-    const int n = ref.dual ? 2 * x.n : x.n;  // (dual: a piece's two halves)
-    for (int i = sub; i < n; i += WARPS * U) {
-      float lse[RPW][U], v[RPW][U][CW];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int k = i + u * WARPS;
-        const long long at =
-            ref.dual ? piece_row(ref, x, k >> 1, in_slot + (k & 1) * kTileRows) : piece_row(ref, x, k, in_slot);
-        const float* src = ref.o + at * D + CW * lane;
-        const float* src_lse = ref.lse + at;
-#pragma unroll
-        for (int q = 0; q < RPW; ++q) {
-          lse[q][u] = -CUDART_INF_F;
-          if (k < n && q >= q0 && q < qn) {
-            lse[q][u] = src_lse[q];
-            if constexpr (CW == 4)
-              *reinterpret_cast<float4*>(v[q][u]) = *reinterpret_cast<const float4*>(src + q * D);
-            else
-              *reinterpret_cast<float2*>(v[q][u]) = *reinterpret_cast<const float2*>(src + q * D);
-          }
-        }
-      }
+    for (int u = 0; u < U; ++u) {
+      const int k = i + u * WARPS;
+      const long long at = piece_row(p.part, own, k, r0);
 #pragma unroll
       for (int q = 0; q < RPW; ++q) {
-        float m = M[q];
-#pragma unroll
-        for (int u = 0; u < U; ++u) m = fmaxf(m, lse[q][u]);
-        if (m == -CUDART_INF_F) continue;  // the same in every lane
-        const float g = ex2_approx(M[q] - m);
-        M[q] = m;
-        sum[q] *= g;
-#pragma unroll
-        for (int c = 0; c < CW; ++c) acc[q][c] *= g;
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          if (lse[q][u] == -CUDART_INF_F) continue;
-          const float f = ex2_approx(lse[q][u] - m);
-          sum[q] += f;
-#pragma unroll
-          for (int c = 0; c < CW; ++c) acc[q][c] = fmaf(f, v[q][u][c], acc[q][c]);
+        lse[q][u] = -CUDART_INF_F;
+        if (k < n && q < count) {
+          lse[q][u] = p.part.lse[at + q];
+          load(p.part.o + (at + q) * D + CW * lane, v[q][u]);
         }
       }
     }
-  };
-  if (count > 0) {
-    gather(p.part, own, row_in, 0, count);
-    if (with_prefix) {
-      // the rows may cross from one row pair of the prefix into the next
-      const int here = min(count, kPairRows - prefix_row);
-      gather(p.prefix, pre, prefix_row, 0, here);
-      if (RPW > 1 && here < count)
-        gather(p.prefix, tile_pieces(p.prefix, tile_unit(p.prefix, head, prefix_pair + 1)), -here, here, count);
-    }
+#pragma unroll
+    for (int q = 0; q < RPW; ++q) m[q].add(lse[q], v[q]);
   }
   if constexpr (WARPS > 1) {
 #pragma unroll
-    for (int c = 0; c < CW; ++c) s_acc[warp][CW * lane + c] = acc[0][c];
+    for (int c = 0; c < CW; ++c) s_acc[warp][CW * lane + c] = m[0].acc[c];
     if (lane == 0) {
-      s_max[warp] = M[0];
-      s_sum[warp] = sum[0];
+      s_max[warp] = m[0].top;
+      s_sum[warp] = m[0].sum;
     }
     __syncthreads();
     if (sub != 0) return;
@@ -776,31 +763,150 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const __grid_constan
     for (int o = 1; o < WARPS; ++o) {
       const float m2 = s_max[warp + o];
       if (m2 == -CUDART_INF_F) continue;
-      const float m = fmaxf(M[0], m2);
-      const float f = ex2_approx(m2 - m), g = ex2_approx(M[0] - m);
-      M[0] = m;
-      sum[0] = sum[0] * g + s_sum[warp + o] * f;
+      const float top = fmaxf(m[0].top, m2);
+      const float f = ex2_approx(m2 - top), g = ex2_approx(m[0].top - top);
+      m[0].top = top;
+      m[0].sum = m[0].sum * g + s_sum[warp + o] * f;
 #pragma unroll
-      for (int c = 0; c < CW; ++c) acc[0][c] = acc[0][c] * g + s_acc[warp + o][CW * lane + c] * f;
+      for (int c = 0; c < CW; ++c) m[0].acc[c] = m[0].acc[c] * g + s_acc[warp + o][CW * lane + c] * f;
     }
   }
 #pragma unroll
   for (int q = 0; q < RPW; ++q) {
     if (q >= count) break;
-    const bool live = sum[q] > 0.f;
-    const float inv = live ? __fdividef(1.f, sum[q]) : 0.f;
-    const size_t row = (static_cast<size_t>(b) * p.seq.Hkv + head) * rows + r0 + q;
+    const float inv = m[q].scale();
+    const size_t row = static_cast<size_t>(unit) * rows + r0 + q;
     const size_t at = row * D + CW * lane;
 #pragma unroll
     for (int c = 0; c < CW; c += 2) {
-      const float x = acc[q][c] * inv, y = acc[q][c + 1] * inv;
+      const float x = m[q].acc[c] * inv, y = m[q].acc[c + 1] * inv;
       if (p.o_bf16)
         store_pair(static_cast<uint16_t*>(p.o) + at + c, x, y);
       else
         store_pair(static_cast<float*>(p.o) + at + c, x, y);
     }
-    if (lane == 0) p.lse[row] = live ? (M[q] + __log2f(sum[q])) * kLn2 : -CUDART_INF_F;
+    if (lane == 0) p.lse[row] = m[q].lse();
   }
+}
+
+// Merges the rows of the tile kernel's units (STEPS = false) or of the step
+// kernel's, and those of the shared prefix.  A lane takes one of 32 rows that
+// lie together, and 16 of its columns; a CTA's warps take the row group's other
+// columns (WARPS = 1) or, where rows are few and pieces many, every WARPS-th
+// piece each.
+template <int D, int WARPS, bool STEPS>
+__global__ void __launch_bounds__(256) merge_lanes_kernel(const __grid_constant__ PagedCombine p) {
+  constexpr int C = 16;                          // columns a warp
+  constexpr int BLOCKS = D / C * WARPS / 8;      // CTAs a row group; 0: a CTA takes several
+  constexpr int PER = BLOCKS ? 1 : 8 * C / D;    // row groups a CTA
+  constexpr int COLS = D / C;                    // column parts of a row group
+  __shared__ float s_max[WARPS > 1 ? 8 : 1][32], s_sum[WARPS > 1 ? 8 : 1][32], s_acc[WARPS > 1 ? 8 : 1][C][32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rows = p.seq.G * p.seq.Nq;
+  // row groups of a unit, or (STEPS) of all sequences' rows of a key head
+  const int groups = STEPS ? (p.seq.B * rows + 31) / 32 : rows_of_unit(p.part) / 32;
+  const int part = WARPS > 1 ? static_cast<int>(blockIdx.x % BLOCKS) : warp % COLS;
+  const int sub = WARPS > 1 ? warp : 0;
+  const unsigned item = WARPS > 1 ? blockIdx.x / BLOCKS : blockIdx.x * PER + warp / COLS;
+  const int units = STEPS ? p.seq.Hkv : p.units;
+  const int unit = static_cast<int>(min(item / groups, static_cast<unsigned>(units - 1)));
+  const int in_unit = static_cast<int>(item % groups) * 32 + lane;
+  int b, head, row_in;  // sequence, key head, row of its rows
+  bool live = item < static_cast<unsigned>(units) * groups;
+  if constexpr (STEPS) {
+    head = unit;
+    live = live && in_unit < p.seq.B * rows;
+    b = live ? in_unit / rows : 0;
+    row_in = live ? in_unit - b * rows : 0;
+  } else {
+    // paged_tiles_kernel's order of units
+    const int g = unit / (p.part.group * p.part.pairs);
+    const int i = unit - g * p.part.group * p.part.pairs;
+    const int hs = min(p.part.group, p.part.heads - g * p.part.group);
+    const int level = i / hs;
+    const int bh = g * p.part.group + i - level * hs;
+    b = bh / p.seq.Hkv;
+    head = bh - b * p.seq.Hkv;
+    row_in = (p.part.pairs - 1 - level) * kPairRows + in_unit;
+    live = live && row_in < rows;
+  }
+  grid_wait();
+  Pieces own;
+  if constexpr (STEPS)
+    own = step_pieces(p.part, b, head, p.seq.Hkv);
+  else
+    own = tile_pieces(p.part, unit);
+  if (p.direct && !p.part.dual && own.n == 1) live = false;  // written by the only CTA that had it
+  Merged<C> m;
+  m.clear();
+  auto gather = [&](auto steps_tag, const PartRef& ref, const Pieces& x, int row) {
+    constexpr bool ROWS = decltype(steps_tag)::value;  // the step kernel's layout
+    constexpr int U = 2;  // pieces in flight
+    const bool dual = !ROWS && ref.dual;
+    const int n = live ? (dual ? 2 * x.n : x.n) : 0;
+    for (int k0 = sub; k0 < n; k0 += WARPS * U) {
+      float lse[U], v[U][C];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int k = k0 + u * WARPS;
+        lse[u] = -CUDART_INF_F;
+        if (k < n) {
+          const long long at =
+              dual ? piece_row(ref, x, k >> 1, row + (k & 1) * kTileRows) : piece_row(ref, x, k, row);
+          lse[u] = ref.lse[at];
+          const float* src = ref.o + (ROWS ? at * D + C * part : tile_part(at, C * part, D));
+#pragma unroll
+          for (int c = 0; c < C; c += 4)
+            *reinterpret_cast<float4*>(v[u] + c) = *reinterpret_cast<const float4*>(src + (ROWS ? c : c * 32));
+        }
+      }
+      m.add(lse, v);
+    }
+  };
+  gather(std::bool_constant<STEPS>{}, p.part, own, STEPS ? row_in : in_unit);
+  if (STEPS || p.prefix.o) {
+    const int all = (p.b0 + b) * rows + row_in;  // row among all sequences'
+    gather(std::false_type{}, p.prefix, tile_pieces(p.prefix, tile_unit(p.prefix, head, min(all / kPairRows, p.prefix.pairs - 1))),
+           all % kPairRows);
+  }
+  if constexpr (WARPS > 1) {
+    s_max[warp][lane] = m.top;
+    s_sum[warp][lane] = m.sum;
+#pragma unroll
+    for (int c = 0; c < C; ++c) s_acc[warp][c][lane] = m.acc[c];
+    __syncthreads();
+    if (warp != 0) return;
+#pragma unroll 1
+    for (int o = 1; o < WARPS; ++o) {
+      const float m2 = s_max[o][lane];
+      const float top = fmaxf(m.top, m2);
+      if (top == -CUDART_INF_F) continue;
+      const float f = ex2_approx(m2 - top), g2 = ex2_approx(m.top - top);
+      m.top = top;
+      m.sum = m.sum * g2 + s_sum[o][lane] * f;
+#pragma unroll
+      for (int c = 0; c < C; ++c) m.acc[c] = m.acc[c] * g2 + s_acc[o][c][lane] * f;
+    }
+  }
+  if (!live) return;
+  const float inv = m.scale();
+  const size_t row = (static_cast<size_t>(b) * p.seq.Hkv + head) * rows + row_in;
+  const size_t at = row * D + C * part;
+  if (p.o_bf16) {
+    uint32_t w[C / 2];
+#pragma unroll
+    for (int c = 0; c < C; c += 2) w[c / 2] = pack_bf16x2(m.acc[c] * inv, m.acc[c + 1] * inv);
+#pragma unroll
+    for (int c = 0; c < C / 2; c += 4)
+      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + at + 2 * c) =
+          make_uint4(w[c], w[c + 1], w[c + 2], w[c + 3]);
+  } else {
+#pragma unroll
+    for (int c = 0; c < C; c += 4)
+      *reinterpret_cast<float4*>(static_cast<float*>(p.o) + at + c) =
+          make_float4(m.acc[c] * inv, m.acc[c + 1] * inv, m.acc[c + 2] * inv, m.acc[c + 3] * inv);
+  }
+  if (part == 0) p.lse[row] = m.lse();
 }
 
 template <int D, int RB>
@@ -815,28 +921,34 @@ cudaError_t launch_steps(const PagedArgs& a, const PagedStep& p, int ctas, cudaS
 }
 
 // Warps a row: as many as the rows leave room for on the GPU at once, for the
-// rows with the most partial results are those of the smallest batches.  Where
-// most rows may have none (direct), launching the blocks counts as well.
-// (128 rows of tile units, 32768 keys: 52.7 us a call with one warp a row, 44.8
-// with eight.  32000 rows of a chunk: one warp for two rows 18 us, with six
-// pieces in flight instead of two slower.)
+// rows with the most partial results are those of the smallest batches.
 template <int D>
-cudaError_t launch_combine(const PagedCombine& p, bool tiles, int sms, cudaStream_t stream) {
+cudaError_t launch_merge_rows(const PagedCombine& p, int sms, cudaStream_t stream) {
   constexpr int RPW = 2;
-  const int unit_rows = rows_of_unit(p.part);
-  const long long rows = static_cast<long long>(p.units) * unit_rows;
-  const long long groups = static_cast<long long>(p.units) * ((unit_rows + RPW - 1) / RPW);
-  const long long room = (p.direct ? 4LL : 8LL) * sms;
+  const long long rows = static_cast<long long>(p.units) * p.part.slot_rows;
+  const long long groups = static_cast<long long>(p.units) * ((p.part.slot_rows + RPW - 1) / RPW);
+  const long long room = 4LL * sms;
   auto launch = [&](auto kern, long long items, int per_block) {
     return launch_overlapped(kern, dim3(static_cast<unsigned>((items + per_block - 1) / per_block)), 256, 0, stream, p);
   };
-  if (tiles) {
-    if (rows <= 2 * room) return launch(paged_combine_kernel<D, 8, 1, true>, rows, 1);
-    return launch(paged_combine_kernel<D, 1, RPW, true>, groups, 8);
-  }
-  if (rows <= room) return launch(paged_combine_kernel<D, 8, 1, false>, rows, 1);
-  if (rows <= 2 * room) return launch(paged_combine_kernel<D, 4, 1, false>, rows, 2);
-  return launch(paged_combine_kernel<D, 1, RPW, false>, groups, 8);
+  if (rows <= room) return launch(merge_rows_kernel<D, 8, 1>, rows, 1);
+  if (rows <= 2 * room) return launch(merge_rows_kernel<D, 4, 1>, rows, 2);
+  return launch(merge_rows_kernel<D, 1, RPW>, groups, 8);
+}
+
+// Eight warps to a row group's 16 columns while that leaves every CTA its own
+// room on the GPU.
+template <int D, bool STEPS>
+cudaError_t launch_merge_lanes(const PagedCombine& p, int sms, cudaStream_t stream) {
+  const long long rows = static_cast<long long>(p.seq.B) * p.seq.G * p.seq.Nq;
+  const long long groups = STEPS ? p.seq.Hkv * ((rows + 31) / 32)
+                                 : static_cast<long long>(p.units) * (rows_of_unit(p.part) / 32);
+  auto launch = [&](auto kern, long long blocks) {
+    return launch_overlapped(kern, dim3(static_cast<unsigned>(blocks)), 256, 0, stream, p);
+  };
+  if (groups * (D / 16) <= 4LL * sms) return launch(merge_lanes_kernel<D, 8, STEPS>, groups * (D / 16));
+  constexpr int PER = 128 / D;  // row groups a CTA
+  return launch(merge_lanes_kernel<D, 1, STEPS>, (groups + PER - 1) / PER);
 }
 
 // How a call is divided, and where its partial results lie in the workspace
@@ -948,7 +1060,7 @@ cudaError_t launch_paged_d(const PagedArgs& a, cudaStream_t stream) {
     c.units = c.direct && !t.part.dual ? t.part.cut : t.part.units;
     c.o = a.o;
     c.lse = a.lse;
-    return launch_combine<D>(c, true, a.sms, stream);
+    return launch_merge_lanes<D, false>(c, a.sms, stream);
   }
   for (int b0 = 0; b0 < a.B; b0 += x.chunk) {
     const int n = a.B - b0 < x.chunk ? a.B - b0 : x.chunk;
@@ -987,7 +1099,7 @@ cudaError_t launch_paged_d(const PagedArgs& a, cudaStream_t stream) {
     c.b0 = b0;
     c.o = p.o;
     c.lse = p.lse;
-    e = launch_combine<D>(c, false, a.sms, stream);
+    e = with_prefix ? launch_merge_lanes<D, true>(c, a.sms, stream) : launch_merge_rows<D>(c, a.sms, stream);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;

@@ -40,6 +40,11 @@ struct PagedSeq {
 // (units from `cut` on are whole and in slot u + ctas); with two_a_cta, where
 // only a CTA's first and last pieces of the line are partial, in slot 2 c (its
 // first) or 2 c + 1.
+//
+// A row of the step kernel's is d floats in one run.  The tile kernel writes a
+// row a lane, so its 32 rows of a warp lie as [d / 4][32 rows][4]: every store
+// is then 512 bytes in one piece, and so is every load of a merge that takes a
+// row a lane.
 struct PartRef {
   const int* line;     // first tile of every unit before `cut` (the step kernel: of its `cut` sequences, a head),
                        // their sum, then the ranges' base and more
@@ -54,7 +59,7 @@ struct PartRef {
   int dual;
   int units;
   int heads, pairs, group;  // the tile kernel: (sequence, head)s, row pairs of each, heads dealt out together
-  float *o, *lse;      // [slot][slot_rows][d], [slot][slot_rows] (log2 units)
+  float *o, *lse;      // [slot] of slot_rows rows of d; [slot][slot_rows] (log2 units)
 };
 
 struct PagedStep {
@@ -64,7 +69,7 @@ struct PagedStep {
   void* o;
   int o_bf16;
   float* lse;
-  int* line_out;     // the line's table, for the combine
+  int* line_out;     // the line's table, for the merge
   PartRef part;
   int direct;        // 1: a piece that is a whole unit's writes o and lse
   int wait_first;    // 1: wait for the kernels before this one at the start; 0: before the end
@@ -87,7 +92,7 @@ struct PagedTiles {
   void* o;
   int o_bf16;
   float* lse;
-  int* line_out;     // the line's table, for the combine
+  int* line_out;     // the line's table, for the merge
   PartRef part;
   int direct;
   int boxed_rows;    // tiles of rows come by TMA (always but for some prefixes)

@@ -20,7 +20,7 @@
 //    in the step kernel; the others are drawn whole from a counter, heaviest
 //    first within groups of heads whose keys stay in L2.  So few units fill
 //    the GPU, and many end together, on their lightest.  Pieces of a unit leave
-//    normalised outputs and log-sum-exps that paged_combine_kernel merges.  One
+//    normalised outputs and log-sum-exps that the merge kernels of paged.cu take up.  One
 //    warp works out what the next pieces are and the others read it, so that
 //    none of it stands between two pieces.
 //  - Rows of a page behind the last key may hold anything, NaN included, and
@@ -404,62 +404,83 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++on;
         tc_fence_after();
       }
-      // rows leave through the warp's staging area, 64 bytes at a time: each
-      // lane writes a run of its own row there, then the lanes take the runs
-      // of eight rows at once (a tile without keys reads what was left in
-      // tensor memory, and drops it)
+      // (a tile without keys reads what was left in tensor memory, and drops it)
       const bool live = l > 0.f;
       const float inv = live ? 1.0f / (l + dl) : 0.f;
       const bool whole = pieces[n & 1].whole;
-      const bool half = whole && p.o_bf16;
       const long long prow0 = static_cast<long long>(pieces[n & 1].slot) * kPairRows + t * kRows + (r - lane);
       const volatile uint32_t* at = row_at + (n & 1) * kPairRows + t * kRows + (r - lane);
-      const uint32_t stage = sbase + L::kStageOff + warp * 2048;
-      const uint32_t put = stage + lane * 64, put_x = (lane >> 1) & 3;
-      const int from = lane >> 2, run = lane & 3;  // read: rows from, from + 8, ..., 16 bytes each
-      uint8_t* dst[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const uint32_t g = at[8 * k + from];
-        uint8_t* base = whole ? static_cast<uint8_t*>(p.o) + static_cast<size_t>(g) * D * (half ? 2 : 4)
-                              : reinterpret_cast<uint8_t*>(p.part.o + (prow0 + 8 * k + from) * D);
-        dst[k] = g == kNoRow ? nullptr : base + 16 * run;
-      }
-      const int runs = half ? D / 32 : D / 16;
+      if (!whole) {
+        // a partial result lies in runs of 16 bytes, a row group's 32 rows side
+        // by side (PartRef), so a store is 512 bytes in one piece
+        float4* dst = reinterpret_cast<float4*>(p.part.o + prow0 * D) + lane;
+        const bool keep = at[lane] != kNoRow;
 #pragma unroll 1
-      for (int c = 0; c < runs; ++c) {
-        uint32_t w[16];
-        if (half) {
-          uint32_t v[32];
-          tmem_ld32(tO + 32 * c, v);
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t w[32];
+          tmem_ld32(tO + 32 * c, w);
           tmem_ld_wait();
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            w[i] = pack_bf16x2(__uint_as_float(v[2 * i]) * inv, __uint_as_float(v[2 * i + 1]) * inv);
-        } else {
-          tmem_ld16(tO + 16 * c, w);
-          tmem_ld_wait();
-#pragma unroll
-          for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) * inv);
+          for (int i = 0; i < 8; ++i) {
+            float4 x;
+            x.x = live ? __uint_as_float(w[4 * i]) * inv : 0.f;
+            x.y = live ? __uint_as_float(w[4 * i + 1]) * inv : 0.f;
+            x.z = live ? __uint_as_float(w[4 * i + 2]) * inv : 0.f;
+            x.w = live ? __uint_as_float(w[4 * i + 3]) * inv : 0.f;
+            if (keep) dst[(8 * c + i) * 32] = x;
+          }
         }
-        if (!live) {
-#pragma unroll
-          for (int i = 0; i < 16; ++i) w[i] = 0u;
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          st_shared_v4(put + ((i ^ put_x) << 4), w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-        __syncwarp();
-        uint32_t x[4][4];
+      } else {
+        // rows leave through the warp's staging area, 64 bytes at a time: each
+        // lane writes a run of its own row there, then the lanes take the runs
+        // of eight rows at once
+        const bool half = p.o_bf16;
+        const uint32_t stage = sbase + L::kStageOff + warp * 2048;
+        const uint32_t put = stage + lane * 64, put_x = (lane >> 1) & 3;
+        const int from = lane >> 2, run = lane & 3;  // read: rows from, from + 8, ..., 16 bytes each
+        uint8_t* dst[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const int row = 8 * k + from;
-          ld_shared_v4(stage + row * 64 + ((run ^ ((row >> 1) & 3)) << 4), x[k]);
+          const uint32_t g = at[8 * k + from];
+          dst[k] = g == kNoRow ? nullptr
+                               : static_cast<uint8_t*>(p.o) + static_cast<size_t>(g) * D * (half ? 2 : 4) + 16 * run;
         }
+        const int runs = half ? D / 32 : D / 16;
+#pragma unroll 1
+        for (int c = 0; c < runs; ++c) {
+          uint32_t w[16];
+          if (half) {
+            uint32_t v[32];
+            tmem_ld32(tO + 32 * c, v);
+            tmem_ld_wait();
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (dst[k]) *reinterpret_cast<uint4*>(dst[k] + 64 * c) = make_uint4(x[k][0], x[k][1], x[k][2], x[k][3]);
-        __syncwarp();
+            for (int i = 0; i < 16; ++i)
+              w[i] = pack_bf16x2(__uint_as_float(v[2 * i]) * inv, __uint_as_float(v[2 * i + 1]) * inv);
+          } else {
+            tmem_ld16(tO + 16 * c, w);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) * inv);
+          }
+          if (!live) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) w[i] = 0u;
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            st_shared_v4(put + ((i ^ put_x) << 4), w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+          __syncwarp();
+          uint32_t x[4][4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int row = 8 * k + from;
+            ld_shared_v4(stage + row * 64 + ((run ^ ((row >> 1) & 3)) << 4), x[k]);
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (dst[k]) *reinterpret_cast<uint4*>(dst[k] + 64 * c) = make_uint4(x[k][0], x[k][1], x[k][2], x[k][3]);
+          __syncwarp();
+        }
       }
       const uint32_t mine = at[lane];
       if (mine != kNoRow) {
