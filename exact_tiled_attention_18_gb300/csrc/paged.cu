@@ -921,7 +921,10 @@ cudaError_t launch_steps(const PagedArgs& a, const PagedStep& p, int ctas, cudaS
 }
 
 // Warps a row: as many as the rows leave room for on the GPU at once, for the
-// rows with the most partial results are those of the smallest batches.
+// rows with the most partial results are those of the smallest batches.  (Whole
+// calls with 8 / 4 / 1 warps: one sequence of 16384 keys, one key head, 10.1 /
+// 13.2 / 54.7 us; one of 4000 keys, 8 key heads, 8.3 / 8.6 / 14.9; 64 of 300 keys 17.0
+// / 15.1 / 14.1.)
 template <int D>
 cudaError_t launch_merge_rows(const PagedCombine& p, int sms, cudaStream_t stream) {
   constexpr int RPW = 2;
@@ -937,7 +940,9 @@ cudaError_t launch_merge_rows(const PagedCombine& p, int sms, cudaStream_t strea
 }
 
 // Eight warps to a row group's 16 columns while that leaves every CTA its own
-// room on the GPU.
+// room on the GPU.  (Whole calls with 8 / 1: 64 rows of 8 heads, 4096 keys, 15.5 and
+// 27.2 us; 16 sequences behind a prefix of 2048 keys 16.4 and 21.5; the long
+// chunk 388 and 323, 256 sequences behind a prefix 270 and 247.)
 template <int D, bool STEPS>
 cudaError_t launch_merge_lanes(const PagedCombine& p, int sms, cudaStream_t stream) {
   const long long rows = static_cast<long long>(p.seq.B) * p.seq.G * p.seq.Nq;

@@ -29,12 +29,14 @@
 //
 // Measured (whole calls): a square prompt of 16 heads x 16384 tokens 1574
 // TFLOP/s, 32 heads under the causal rule 1409 to 1442; two chunks of 1000
-// tokens, 32 heads on 8, over 9001 and 16384 keys 332 us = 1200 TFLOP/s (this
-// kernel 317, of which a piece's beginning and end cost about 2.7 us each); 2048
+// tokens, 32 heads on 8, over 9001 and 16384 keys 323 us = 1240 TFLOP/s; 2048
 // rows of 8 heads behind 32768 shared keys 190 us in this kernel.  The tensor
-// pipe is 54 to 58% busy in the last two; with pages of 16 keys a square
-// prompt runs at 1316 TFLOP/s, bound by the issue of its eight boxes a tile and
-// block.
+// pipe is 54 to 58% busy in the last two, DRAM 9 to 12%.  The smallest call, 64
+// rows of 8 heads over 512 keys, is 12.8 us: 1.7 until the line is there, 1.8 until a
+// piece is worked out, 1.5 until its first scores, 2 for the softmax and the second
+// product, 2 for writing the rows, then the merge.  With pages of 16 keys a
+// square prompt runs at 1316 TFLOP/s, bound by the issue of its eight boxes a
+// tile and block.
 //
 //   warps 0-3  softmax of tile A     warp 8   TMA producer
 //   warps 4-7  softmax of tile B     warp 9   MMA issuer, owns tensor memory
