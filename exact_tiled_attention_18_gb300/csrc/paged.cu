@@ -39,7 +39,7 @@
 // and pairs, 54 us so; 32 rows 87 and 61).
 //
 // Measured (whole calls; HBM read rate of keys and values): 8 sequences x 32
-// heads x 32768 keys, one row a head, 604 us = 7.1 TB/s; 32 sequences of 100 to
+// heads x 32768 keys, one row a head, 604 to 616 us = 7.0 to 7.1 TB/s; 32 sequences of 100 to
 // 16384 keys, 32 heads on 4, 42 us = 5.3 TB/s, of which 6 us pass before the
 // first tiles are there; one sequence of 1000 keys 6.9 us in a graph.  A pass
 // over a quarter of the first keeps DRAM 85% of its peak busy, the tensor pipe
@@ -866,8 +866,8 @@ __global__ void __launch_bounds__(256) merge_lanes_kernel(const __grid_constant_
   gather(std::bool_constant<STEPS>{}, p.part, own, STEPS ? row_in : in_unit);
   if (STEPS || p.prefix.o) {
     const int all = (p.b0 + b) * rows + row_in;  // row among all sequences'
-    gather(std::false_type{}, p.prefix, tile_pieces(p.prefix, tile_unit(p.prefix, head, min(all / kPairRows, p.prefix.pairs - 1))),
-           all % kPairRows);
+    const int pair = min(all / kPairRows, p.prefix.pairs - 1);
+    gather(std::false_type{}, p.prefix, tile_pieces(p.prefix, tile_unit(p.prefix, head, pair)), all % kPairRows);
   }
   if constexpr (WARPS > 1) {
     s_max[warp][lane] = m.top;

@@ -25,7 +25,8 @@ constexpr int kEvenSteps = 2, kEvenTiles = 8;  // (make_ranges)
 constexpr int kMaxTileCtas = 160;
 constexpr int kTileLine = 2 * kMaxTileCtas;  // units of the tile kernel's line
 constexpr int kPairRows = 256;         // query rows a unit of the tile kernel: two 128-row tiles
-static_assert(kLineWords >= kLineSequences + 3 && kLineWords >= kTileLine + 4 && kLineWords % 4 == 0, "the line's room");
+static_assert(kLineWords >= kLineSequences + 3 && kLineWords >= kTileLine + 4, "the line's room");
+static_assert(kLineWords % 4 == 0, "what lies behind it is read 16 bytes at a time");
 
 struct PagedSeq {
   const int *seqlens_q, *seqlens_k;
