@@ -72,7 +72,7 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
 struct MapKey {
   const void* base;
   int elem_bytes, heads, rows, inner, box_inner, box_rows;
-  bool blocked = false;  // 4-D: a box takes all the 64-column blocks of its rows
+  int blocked = 0;       // 1, 4-D: a box takes all the 64-column blocks of its rows; 2, 5-D: of 8 rows at a time
   int batch = 0;         // > 0, 4-D: over [batch][heads][rows][inner], a box takes box_batch sequences' rows
   int box_batch = 0;
   bool operator==(const MapKey& o) const {
@@ -107,7 +107,10 @@ bool remember_map(const MapKey& key, const CUtensorMap& m) {
 // layout the MMA descriptors expect).  Rows past `rows` read as zeros.
 // Blocked (bf16): a 4-D map over [heads][inner / 64][rows][64] of the same
 // memory, box = 64 x box_rows x (inner / 64) x 1, so that one load brings the
-// box's rows block by block.  With a batch (bf16): a 4-D map over
+// box's rows block by block (blocked = 1), or a 5-D map over
+// [heads][rows / 8][inner / 64][8][64], box = 64 x 8 x (inner / 64) x box_rows / 8
+// x 1, so that it brings them 8 rows at a time, block by block (blocked = 2; rows
+// a multiple of 8).  With a batch (bf16): a 4-D map over
 // [batch][heads][rows][inner], box = 64 x box_rows x 1 x box_batch, for the
 // rows of several sequences' same head one behind the other.
 bool encode_map(CUtensorMap* m, const MapKey& key) {
@@ -128,7 +131,18 @@ bool encode_map(CUtensorMap* m, const MapKey& key) {
   cuuint64_t strides[2] = {static_cast<cuuint64_t>(key.inner) * eb,
                            static_cast<cuuint64_t>(key.rows) * key.inner * eb};
   cuuint32_t box[3] = {static_cast<cuuint32_t>(key.box_inner), static_cast<cuuint32_t>(key.box_rows), 1};
-  cuuint32_t estride[4] = {1, 1, 1, 1};
+  cuuint32_t estride[5] = {1, 1, 1, 1, 1};
+  if (key.blocked == 2) {
+    const cuuint64_t blocks = static_cast<cuuint64_t>(key.inner / 64);
+    cuuint64_t dims5[5] = {64, 8, blocks, dims[1] / 8, dims[2]};
+    cuuint64_t strides5[4] = {strides[0], 128, 8 * strides[0], strides[1]};
+    cuuint32_t box5[5] = {64, 8, static_cast<cuuint32_t>(blocks), box[1] / 8, 1};
+    if (fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(key.base), dims5, strides5, box5, estride,
+           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return false;
+    return remember_map(key, *m);
+  }
   if (key.blocked || key.batch > 0) {
     cuuint64_t dims4[4] = {64, dims[1], static_cast<cuuint64_t>(key.inner / 64), dims[2]};
     cuuint64_t strides4[3] = {strides[0], 128, strides[1]};
@@ -510,8 +524,11 @@ fa_status paged_common(const void* q, const void* k_pages, const void* v_pages, 
   a.box_rows = page_size % 64 == 0 ? 64 : (page_size % 32 == 0 ? 32 : 16);
   const int page_heads = num_pages * Hkv;
   const bool steps = fa::paged_uses_steps(Hq / Hkv, Nq);
-  if ((!steps || prefix_len > 0) && (!encode_bf16_map(&a.tm_k, k_pages, page_heads, page_size, d, a.box_rows) ||
-                                     !encode_bf16_map(&a.tm_v, v_pages, page_heads, page_size, d, a.box_rows)))
+  auto page_map = [&](CUtensorMap* m, const void* pages, int box_rows, int blocked) {
+    return encode_map(m, MapKey{pages, 2, page_heads, page_size, d, 64, box_rows, blocked});
+  };
+  if ((!steps || prefix_len > 0) &&
+      (!page_map(&a.tm_k, k_pages, a.box_rows, 2) || !page_map(&a.tm_v, v_pages, a.box_rows, 2)))
     return FA_ERR_LAUNCH;
   const int rows = Hq / Hkv * Nq;  // below 2^31: checked above
   if (!steps && !encode_bf16_map(&a.tm_q, q, 1, B * Hq * Nq, d)) return FA_ERR_LAUNCH;
@@ -524,10 +541,8 @@ fa_status paged_common(const void* q, const void* k_pages, const void* v_pages, 
     key.box_batch = rows < fa::kTileRows ? fa::kTileRows / rows : 1;
     if (!encode_map(&a.tm_qp, key)) return FA_ERR_LAUNCH;
   }
-  if (steps && (!encode_map(&a.st_k, MapKey{k_pages, 2, page_heads, page_size, d, 64, a.box_rows, true}) ||
-                !encode_map(&a.st_v, MapKey{v_pages, 2, page_heads, page_size, d, 64, a.box_rows, true}) ||
-                !encode_map(&a.st_k16, MapKey{k_pages, 2, page_heads, page_size, d, 64, 16, true}) ||
-                !encode_map(&a.st_v16, MapKey{v_pages, 2, page_heads, page_size, d, 64, 16, true})))
+  if (steps && (!page_map(&a.st_k, k_pages, a.box_rows, 1) || !page_map(&a.st_v, v_pages, a.box_rows, 1) ||
+                !page_map(&a.st_k16, k_pages, 16, 1) || !page_map(&a.st_v16, v_pages, 16, 1)))
     return FA_ERR_LAUNCH;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (!workspace) {

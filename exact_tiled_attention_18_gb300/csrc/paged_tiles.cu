@@ -12,17 +12,19 @@
 //    the prefix: the queries of every sequence side by side, which is what
 //    lets its keys be read once).  A warp gathers them from q into the swizzled
 //    tiles, a piece ahead; each row has its own last visible key.
-//  - Keys come from pages: a tile of 128 keys is 128 / box_rows TMA boxes a
-//    64-column block, issued by the lanes of the producer warp, page ids read
-//    32 boxes ahead.
+//  - Keys come from pages: a tile of 128 keys is 128 / box_rows TMA boxes, one a
+//    lane of the producer warp, page ids read 32 boxes ahead.  A box brings all
+//    columns of its rows, in groups of 8 rows whose 64-column blocks lie one
+//    behind the other: a layout that the MMA descriptors know as well as blocks
+//    of all rows, and half the loads at d = 128.
 //  - Division.  The first one to two units (256 rows of a key head) for every
 //    CTA form a line of key tiles that is cut into equal ranges, one a CTA, as
 //    in the step kernel; the others are drawn whole from a counter, heaviest
 //    first within groups of heads whose keys stay in L2.  So few units fill
 //    the GPU, and many end together, on their lightest.  Pieces of a unit leave
-//    normalised outputs and log-sum-exps that the merge kernels of paged.cu take up.  One
-//    warp works out what the next pieces are and the others read it, so that
-//    none of it stands between two pieces.
+//    normalised outputs and log-sum-exps that the merge kernels of paged.cu take
+//    up.  One warp works out what the next pieces are and the others read it,
+//    so that none of it stands between two pieces.
 //  - Rows of a page behind the last key may hold anything, NaN included, and
 //    0 * NaN would poison the product with V: a spare warp zeroes them in the
 //    last tile before that product is issued.
@@ -34,9 +36,9 @@
 // pipe is 54 to 58% busy in the last two, DRAM 9 to 12%.  The smallest call, 64
 // rows of 8 heads over 512 keys, is 12.8 us: 1.7 until the line is there, 1.8 until a
 // piece is worked out, 1.5 until its first scores, 2 for the softmax and the second
-// product, 2 for writing the rows, then the merge.  With pages of 16 keys a
-// square prompt runs at 1316 TFLOP/s, bound by the issue of its eight boxes a
-// tile and block.
+// product, 2 for writing the rows, then the merge.  (A prompt of 8192 tokens, 16
+// heads, pages of 16 / 32 / 64 / 128 keys: 279 / 275 / 277 / 276 us; with a box a
+// 64-column block 324 / 278 / 277 / 276, the first bound by their issue.)
 //
 //   warps 0-3  softmax of tile A     warp 8   TMA producer
 //   warps 4-7  softmax of tile B     warp 9   MMA issuer, owns tensor memory
@@ -125,6 +127,16 @@ static_assert(sizeof(Piece) <= 48, "a piece's room");
 
 __device__ __forceinline__ bool tile_wait(uint32_t bar, uint32_t parity, const WaitCtl& w, int site, int unit) {
   return __all_sync(0xffffffffu, wait_bounded(bar, parity, w, site, unit));
+}
+
+// A box of whole rows of a page, in groups of 8 rows from `group` on.
+__device__ __forceinline__ void tma_load_groups(uint32_t dst, const CUtensorMap* map, uint32_t bar, int group,
+                                                int outer, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%2, %2, %2, %3, %4}], [%5], %6;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(group), "r"(outer), "r"(bar), "l"(policy)
+      : "memory");
 }
 
 __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
@@ -499,9 +511,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 8) {
       // -------------------------------------------------------- TMA producer
       const int boxes = kRows / p.box_rows;
-      const int block = lane / boxes, box = lane - block * boxes;  // this lane's load of a tile
-      const bool loads = block < CB;
-      const uint32_t offset = static_cast<uint32_t>(block * 16384 + box * p.box_rows * 128);
+      const int box = lane & (boxes - 1);  // this lane's load of a tile
+      const bool loads = lane < boxes;
+      const uint32_t offset = static_cast<uint32_t>(box * p.box_rows * CB * 128);
       const uint64_t policy = l2_policy_evict_last();
       uint32_t kvpos = 0;
       bool ok = true;
@@ -543,8 +555,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) mbar_arrive_expect_tx(BAR(L::KV_FULL + s), L::kTileBytes);
             __syncwarp();
             if (loads)
-              tma_load_3d_hint(sbase + L::kRingOff + s * L::kTileBytes + offset, kv == 0 ? &tm_k : &tm_v,
-                               BAR(L::KV_FULL + s), block * 64, row, outer, policy);
+              tma_load_groups(sbase + L::kRingOff + s * L::kTileBytes + offset, kv == 0 ? &tm_k : &tm_v,
+                              BAR(L::KV_FULL + s), row / 8, outer, policy);
             __syncwarp();
           }
         }
@@ -565,16 +577,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr uint32_t id_s = idesc_bf16_f32(128, 128, false, false);
         constexpr uint32_t id_pv = idesc_bf16_f32(128, D, false, true);
         const SDesc qdesc0 = sdesc_sw128(sbase, 16, 1024);
-        const SDesc kdesc0 = sdesc_sw128(sbase + L::kRingOff, 16, 1024);
-        const SDesc vdesc0 = sdesc_sw128(sbase + L::kRingOff, kRows * 128, 1024);
+        // keys and values: groups of 8 rows, in a group its 64-column blocks
+        const SDesc kdesc0 = sdesc_sw128(sbase + L::kRingOff, 16, CB * 1024);
+        const SDesc vdesc0 = sdesc_sw128(sbase + L::kRingOff, 1024, CB * 1024);
         constexpr uint32_t kTileUnits = L::kTileBytes >> 4;
         auto issue_s = [&](int t, uint32_t slot) {
           const SDesc qd = qdesc0 + static_cast<uint32_t>(t) * kTileUnits;
           const SDesc kd = kdesc0 + slot * kTileUnits;
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks) {
-            const uint32_t off = ((ks >> 2) * 16384 + (ks & 3) * 32) >> 4;
-            umma_ss(tmem + static_cast<uint32_t>(t * 128), qd + off, kd + off, id_s, ks > 0 ? 1u : 0u);
+            const uint32_t q_off = ((ks >> 2) * 16384 + (ks & 3) * 32) >> 4;
+            const uint32_t k_off = ((ks >> 2) * 1024 + (ks & 3) * 32) >> 4;
+            umma_ss(tmem + static_cast<uint32_t>(t * 128), qd + q_off, kd + k_off, id_s, ks > 0 ? 1u : 0u);
           }
         };
         auto issue_pv = [&](int t, uint32_t slot, bool acc) {
@@ -582,7 +596,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int ks = 0; ks < 8; ++ks) {
             umma_ts(tmem + L::kColO + static_cast<uint32_t>(t * D), tmem + static_cast<uint32_t>(t * 128 + ks * 8),
-                    vd + static_cast<uint32_t>((ks * 2048) >> 4), id_pv, (acc || ks > 0) ? 1u : 0u);
+                    vd + static_cast<uint32_t>((ks * CB * 2048) >> 4), id_pv, (acc || ks > 0) ? 1u : 0u);
           }
         };
         uint32_t qa = 0, qb = 0, kvbase = 0, pa = 0, pb = 0, cleaned = 0;
@@ -839,7 +853,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t vt = sbase + L::kRingOff + (vpos % S) * L::kTileBytes;
           for (int i = lane; i < rest * (D / 8); i += 32) {
             const int row = from + i / (D / 8), c = i % (D / 8);
-            st_shared_v4(vt + (c >> 3) * 16384 + sw128(row, c & 7), 0u, 0u, 0u, 0u);
+            st_shared_v4(vt + ((row >> 3) * CB + (c >> 3)) * 1024 + sw128(row & 7, c & 7), 0u, 0u, 0u, 0u);
           }
           fence_proxy_async_smem();
           mbar_arrive_warp(BAR(L::CLEAN));

@@ -69,7 +69,7 @@ struct AppendArgs {
 };
 
 struct PagedArgs {
-  CUtensorMap tm_k, tm_v;     // tile kernel: 3-D maps over [num_pages * Hkv][page_size][d], boxes 64 x box_rows
+  CUtensorMap tm_k, tm_v;     // tile kernel: maps of [num_pages * Hkv][page_size][d], boxes of box_rows rows, 8 at a time
   CUtensorMap tm_q;           // and over q's rows [B * Hq * Nq][d], boxes 64 x 128 (chunks only)
   CUtensorMap tm_qp;          // and over [B][Hkv][G * Nq][d], boxes of 128 rows (prefix, where boxed_rows)
   CUtensorMap st_k, st_v;     // step kernel: blocked maps of the same, boxes of box_rows whole rows
