@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(kStepThreads, step_ctas_per_sm<RB>())
 
   if (warp == kStepWarps) {
     // ------------------------------------------------------------ TMA producer
-    // lane i of a tile's loads: operand, 64-column block and box of rows
+    // lane i of a tile's loads: operand and box of rows
     const int boxes = kStepKeys / p.box_rows;
     int issued = 0;
     bool ok = true;
