@@ -606,16 +606,14 @@ struct Pieces {
   int n;              // pieces
   int c0;             // first CTA
   int slot;           // slot of a piece of CTA 0
-  bool first_whole;   // the first piece starts its CTA's range
 };
 
 // `tile`: the unit's first tile on the line; nt: its tiles.
 __device__ __forceinline__ Pieces pieces_on_line(const Ranges& ranges, int unit, int tile, int nt) {
-  Pieces x{0, 0, unit, false};
+  Pieces x{0, 0, unit};
   if (nt > 0) {
     x.c0 = range_of(ranges, tile);
     x.n = range_of(ranges, tile + nt - 1) - x.c0 + 1;
-    x.first_whole = tile == range_start(ranges, x.c0);
   }
   return x;
 }
@@ -635,9 +633,11 @@ __device__ __forceinline__ Pieces step_pieces(const PartRef& r, int entry, int h
 
 // Unit u of the tile kernel.
 __device__ __forceinline__ Pieces tile_pieces(const PartRef& r, int u) {
-  if (u >= r.cut) return Pieces{1, 0, u + r.ctas, true};
-  const int t0 = r.line[u], nt = r.line[u + 1] - t0;
-  return pieces_on_line(line_ranges(r.line, r.cut), u, t0, nt);
+  if (u >= r.cut) return Pieces{1, 0, u + r.ctas};
+  const int t0 = r.line[u], nt = r.line[u + 1] - t0 - r.piece_cost;
+  const Ranges ranges = line_ranges(r.line, r.cut);
+  if (ranges.base == kWholeUnits) return Pieces{1, 0, 0};
+  return pieces_on_line(ranges, u, t0, nt);
 }
 
 // The tile kernel's unit of (sequence, head) bh and row pair `pair`.
@@ -656,7 +656,7 @@ __device__ __forceinline__ long long tile_part(long long row, int col, int d) {
 }
 
 __device__ __forceinline__ long long piece_row(const PartRef& r, const Pieces& x, int k, int in) {
-  const int slot = r.two_a_cta ? 2 * (x.c0 + k) + (k > 0 || x.first_whole ? 0 : 1) : x.slot + x.c0 + k;
+  const int slot = r.two_a_cta ? 2 * (x.c0 + k) + (k > 0 ? 0 : 1) : x.slot + x.c0 + k;
   return static_cast<long long>(slot) * r.slot_rows + in;
 }
 
@@ -1011,8 +1011,8 @@ cudaError_t launch_paged_d(const PagedArgs& a, cudaStream_t stream) {
   const PagedSeq all{a.seqlens_q, a.seqlens_k, a.B, a.Hkv, G, a.Nq, capacity, a.prefix_len};
   // the tile kernel on `heads` row spaces of `pairs` row pairs; the workspace
   // from `at` on holds `slots` slots
-  auto tiles = [&](PagedTiles& t, int heads, int pairs, int keys, bool direct, bool dual, size_t at, size_t slots,
-                   int* table) -> cudaError_t {
+  auto tiles = [&](PagedTiles& t, bool prefix, int heads, int pairs, int keys, bool direct, bool dual, size_t at,
+                   size_t slots, int* table) -> cudaError_t {
     t.seq = all;
     t.table = a.table;
     t.q = a.q;
@@ -1023,8 +1023,9 @@ cudaError_t launch_paged_d(const PagedArgs& a, cudaStream_t stream) {
     const int cut = units < 2 * tile_ctas ? units : tile_ctas + units % tile_ctas;
     t.line_out = table;
     t.counter = table + kTileLine + 3;
-    t.part = PartRef{table, tile_ctas, kMinTiles, cut, direct && !dual, kPairRows, dual, units, heads, pairs,
-                     head_group(heads, pairs, keys, D, tile_ctas), a.part + at,
+    const int piece_cost = !prefix && !dual && 2 * units >= tile_ctas ? kTilePieceCost : 0;
+    t.part = PartRef{table, tile_ctas, kMinTiles, cut, direct && !dual, piece_cost, kPairRows, dual, units, heads,
+                     pairs, head_group(heads, pairs, keys, D, tile_ctas), a.part + at,
                      a.part + at + slots * kPairRows * D};
     t.box_rows = a.box_rows;
     t.causal = a.causal;
@@ -1040,7 +1041,7 @@ cudaError_t launch_paged_d(const PagedArgs& a, cudaStream_t stream) {
   cudaError_t e;
   if (with_prefix) {
     PagedTiles t{};
-    e = tiles(t, a.Hkv, x.prefix_pairs, a.prefix_len, false, static_cast<long long>(a.B) * x.rows <= kTileRows,
+    e = tiles(t, true, a.Hkv, x.prefix_pairs, a.prefix_len, false, static_cast<long long>(a.B) * x.rows <= kTileRows,
               x.prefix, x.prefix_slots, line + kLineWords);
     if (e != cudaSuccess) return e;
     t.prefix_table = a.prefix_table;
@@ -1052,7 +1053,7 @@ cudaError_t launch_paged_d(const PagedArgs& a, cudaStream_t stream) {
   }
   if (!x.steps) {
     PagedTiles t{};
-    e = tiles(t, a.B * a.Hkv, x.pairs, capacity, !with_prefix, x.rows <= kTileRows, x.own, x.own_slots, line);
+    e = tiles(t, false, a.B * a.Hkv, x.pairs, capacity, !with_prefix, x.rows <= kTileRows, x.own, x.own_slots, line);
     if (e != cudaSuccess) return e;
     t.direct = c.direct;
     t.boxed_rows = 1;
@@ -1082,7 +1083,7 @@ cudaError_t launch_paged_d(const PagedArgs& a, cudaStream_t stream) {
     p.o_bf16 = a.o_bf16;
     p.lse = a.lse + first;
     p.line_out = line;
-    p.part = PartRef{line,        step_ctas, kMinSteps, n, 0, x.rows, 0, n * a.Hkv, 0, 0, 0, a.part + x.own,
+    p.part = PartRef{line,        step_ctas, kMinSteps, n, 0, 0, x.rows, 0, n * a.Hkv, 0, 0, 0, a.part + x.own,
                      a.part + x.own + x.own_slots * x.rows * D};
     p.direct = c.direct;
     p.wait_first = !with_prefix || b0 > 0;

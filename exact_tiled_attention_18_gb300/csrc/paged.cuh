@@ -22,6 +22,10 @@ constexpr int kMaxCtas = 512;
 // 18.1 / 17.4 / 19.0, 64 sequences behind a prefix of 1024 keys 30.3 / 27.2 / 29.8.
 constexpr int kMinSteps = 1, kMinTiles = 2;
 constexpr int kEvenSteps = 2, kEvenTiles = 8;  // (make_ranges)
+// A piece's beginning and end in the tile kernel, in key tiles, where there are
+// units enough for a CTA to have several.
+constexpr int kTilePieceCost = 2;
+constexpr int kWholeUnits = -1;     // in the place of the ranges' base: no unit has been cut
 constexpr int kMaxTileCtas = 160;
 constexpr int kTileLine = 2 * kMaxTileCtas;  // units of the tile kernel's line
 constexpr int kPairRows = 256;         // query rows a unit of the tile kernel: two 128-row tiles
@@ -39,8 +43,11 @@ struct PagedSeq {
 // head; the tile kernel: 256 rows of one) that CTAs cut out of a line of key
 // tiles.  Unit u's piece of CTA c is in slot u + c, which no other piece has
 // (units from `cut` on are whole and in slot u + ctas); with two_a_cta, where
-// only a CTA's first and last pieces of the line are partial, in slot 2 c (its
-// first) or 2 c + 1.
+// only a CTA's first and last pieces of the line are partial, in slot 2 c (one
+// that goes on from the CTA before) or 2 c + 1.
+//
+// A unit of the tile kernel ends on the line with piece_cost places that hold
+// no tile: what the beginning and the end of a piece cost.
 //
 // A row of the step kernel's is d floats in one run.  The tile kernel writes a
 // row a lane, so its 32 rows of a warp lie as [d / 4][32 rows][4]: every store
@@ -52,6 +59,7 @@ struct PartRef {
   int ctas, min_tiles;
   int cut;
   int two_a_cta;
+  int piece_cost;
   int slot_rows;
   // 1: a unit of the tile kernel has at most 128 rows, so that its tile B would
   // be empty: tile B takes the same rows and every other key tile, and leaves

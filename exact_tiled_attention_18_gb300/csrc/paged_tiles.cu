@@ -21,7 +21,9 @@
 //    CTA form a line of key tiles that is cut into equal ranges, one a CTA, as
 //    in the step kernel; the others are drawn whole from a counter, heaviest
 //    first within groups of heads whose keys stay in L2.  So few units fill
-//    the GPU, and many end together, on their lightest.  Pieces of a unit leave
+//    the GPU, and many end together, on their lightest.  Where units differ so
+//    much that they end together anyway (prompts under the causal rule), none
+//    is cut; the kernel finds that out from the lengths.  Pieces of a unit leave
 //    normalised outputs and log-sum-exps that the merge kernels of paged.cu take
 //    up.  One warp works out what the next pieces are and the others read it,
 //    so that none of it stands between two pieces.
@@ -31,14 +33,15 @@
 //
 // Measured (whole calls): a square prompt of 16 heads x 16384 tokens 1574
 // TFLOP/s, 32 heads under the causal rule 1409 to 1442; two chunks of 1000
-// tokens, 32 heads on 8, over 9001 and 16384 keys 323 us = 1240 TFLOP/s; 2048
+// tokens, 32 heads on 8, over 9001 and 16384 keys 320 us = 1250 TFLOP/s; 2048
 // rows of 8 heads behind 32768 shared keys 190 us in this kernel.  The tensor
 // pipe is 54 to 58% busy in the last two, DRAM 9 to 12%.  The smallest call, 64
 // rows of 8 heads over 512 keys, is 12.8 us: 1.7 until the line is there, 1.8 until a
 // piece is worked out, 1.5 until its first scores, 2 for the softmax and the second
-// product, 2 for writing the rows, then the merge.  (A prompt of 8192 tokens, 16
-// heads, pages of 16 / 32 / 64 / 128 keys: 279 / 275 / 277 / 276 us; with a box a
-// 64-column block 324 / 278 / 277 / 276, the first bound by their issue.)
+// product, 2 for writing the rows, then the merge.  Prompts under the causal
+// rule: 16 heads x 4096 tokens 68 us, 8 x 8192 121, 16 x 8192 233 with pages of 16,
+// 32, 64 or 128 keys.  (With a box a 64-column block pages of 16 keys cost a sixth
+// more, bound by the issue of the boxes.)
 //
 //   warps 0-3  softmax of tile A     warp 8   TMA producer
 //   warps 4-7  softmax of tile B     warp 9   MMA issuer, owns tensor memory
@@ -69,6 +72,10 @@ static_assert(2 * 128 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * kLaunchReg
 constexpr float kTau = 8.f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kRows = 128;        // rows and keys a tile
+// Key tiles before a piece's end that the next one is drawn.  (16 heads x 8192
+// tokens 233 us with 0 or 2, 231 with 4, 279 at the piece's beginning; 2 x 12 heads
+// x 5000 tokens 167, 167, 172 and 205.)
+constexpr int kTellTiles = 2;
 constexpr int kReaders = 11;      // warps that follow the pieces: all but the one that works them out
 
 enum TileSite : int {
@@ -113,7 +120,8 @@ struct TileLayout {
   static constexpr int PIECE_FULL = CLEAN + 1;
   static constexpr int PIECE_EMPTY = PIECE_FULL + 2;
   static constexpr int ROWS_FULL = PIECE_EMPTY + 2;
-  static constexpr int DRAIN = ROWS_FULL + 2;
+  static constexpr int LOADED = ROWS_FULL + 2;
+  static constexpr int DRAIN = LOADED + 1;
   static constexpr int kNumBars = DRAIN + 1;
   static constexpr int kMiscOff = kBarOff + kNumBars * 8;
   static constexpr int kScratchOff = kMiscOff + 16;            // one word a warp
@@ -203,6 +211,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bars + 8 * (L::PIECE_EMPTY + i), kReaders);
       mbar_init(bars + 8 * (L::ROWS_FULL + i), 1);
     }
+    mbar_init(bars + 8 * L::LOADED, 1);
     mbar_init(bars + 8 * L::DRAIN, 1);
     *abort_flag = 0;
     mbar_fence_init();
@@ -264,19 +273,47 @@ __global__ void __launch_bounds__(kThreads, 1)
     return (max(ka, kb) + kRows - 1) / kRows;
   };
   const int cut = p.part.cut;  // units of the line
+  auto cost = [&](int tiles) { return tiles > 0 ? tiles + p.part.piece_cost : 0; };
   if constexpr (PREFIX) {  // the same for every unit
-    const int n = (reach + kRows - 1) / kRows;
+    const int n = cost((reach + kRows - 1) / kRows);
     for (int i = threadIdx.x; i <= cut; i += kThreads) line[i] = i * n;
     __syncthreads();
   } else {
-    build_line<kThreads>(line, scratch, cut, [&](int e) { return unit_tiles(e); });
+    build_line<kThreads>(line, scratch, cut, [&](int e) { return cost(unit_tiles(e)); });
   }
   const int total = line[cut];
+  // Whole units instead of the line, where that ends as early or nearly so
+  // (partial results and their merge are worth four tiles and an eighth): with
+  // fewer than two units a CTA one from either end of their order, else all
+  // drawn, if the last ones are light.  Prompts under the causal rule: 16 heads x
+  // 4096 tokens 135 us on the line, 68 so; 8 heads x 8192 149 and 123; 16 heads x
+  // 8192, drawn, 276 and 233.  4 chunks of 100 tokens over 1500 keys, 32 heads on 8,
+  // are 27 us on the line and would be 34.
+  bool whole_units = false;
+  if constexpr (!PREFIX && !DUAL) {
+    if (p.direct && p.part.piece_cost > 0) {  // (not with few units)
+      const int ctas = gridDim.x, c = threadIdx.x;
+      int last = 0;  // of one CTA: its two units, or the one that it may draw last
+      if (cut == p.part.units) {
+        const int u2 = 2 * ctas - 1 - c;
+        if (c < ctas && c < cut) last = line[c + 1] - line[c] + (u2 < cut ? line[u2 + 1] - line[u2] : 0);
+      } else if (c < ctas) {
+        last = cost(unit_tiles(p.part.units - 1 - c));
+      }
+      last = __reduce_max_sync(0xffffffffu, last);
+      __syncthreads();
+      if (lane == 0) scratch[warp] = last;
+      __syncthreads();
+      for (int i = 0; i < kThreads / 32; ++i) last = max(last, scratch[i]);
+      const int mean = total / ctas;
+      whole_units = cut == p.part.units ? last <= mean + mean / 8 + 4 : last <= total / cut / 2;
+    }
+  }
   if (blockIdx.x == 0) {
     for (int i = threadIdx.x; i <= cut; i += kThreads) p.line_out[i] = line[i];
     if (threadIdx.x == 0) {
       const Ranges ranges = make_ranges<PREFIX ? 0 : kEvenTiles>(total, gridDim.x, p.part.min_tiles);
-      p.line_out[cut + 1] = ranges.base;
+      p.line_out[cut + 1] = whole_units ? kWholeUnits : ranges.base;
       p.line_out[cut + 2] = ranges.more;
     }
   }
@@ -529,7 +566,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           return i < count && key < last ? pages[key / p.table.page_size] : -1;
         };
         int cur = page_of(lane), next = page_of(32 + lane);
+        const int tell = max(0, tiles - kTellTiles);
         for (int j = 0; j < tiles && ok; ++j) {
+          if (j == tell && lane == 0) mbar_arrive(BAR(L::LOADED));
           if (j > 0 && (j * boxes) % 32 == 0) {
             cur = next;
             next = page_of(j * boxes + 32 + lane);
@@ -561,6 +600,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (!ok) break;
+        if (tell >= tiles && lane == 0) mbar_arrive(BAR(L::LOADED));
         piece_done(n);
       }
       if (!ok && lane == 0) {
@@ -877,8 +917,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         int u = -1, len = 0;
         Piece x{};
         x.na = -1;
-        if (at < stop) {
-          // the last unit that starts at or before the tile (one with tiles:
+        while (!whole_units && at < stop && len == 0) {
+          // the last unit that starts at or before this place (one with tiles:
           // an empty one starts where its successor does)
           int lo = 0, hi = cut - 1;
           while (lo < hi) {
@@ -886,21 +926,31 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (line[mid] <= at) lo = mid; else hi = mid - 1;
           }
           u = lo;
-          x.tile = at - line[lo];
-          const int tiles = line[lo + 1] - line[lo];
-          len = min(tiles - x.tile, stop - at);
+          const int in = at - line[lo], out = min(line[lo + 1], stop) - line[lo];
+          const int tiles = line[lo + 1] - line[lo] - p.part.piece_cost;
+          x.tile = min(in, tiles);
+          len = min(out, tiles) - x.tile;  // 0: the range begins behind the unit's last tile
           x.whole = p.direct && !DUAL && len == tiles;
-          x.slot = p.part.two_a_cta ? 2 * blockIdx.x + (at == at0 ? 0 : 1) : u + blockIdx.x;
-          at += len;
-        } else if (cut < p.part.units) {
-          if (lane == 0) u = cut + atomicAdd(p.counter, 1);
-          u = __shfl_sync(0xffffffffu, u, 0);
-          if (u < p.part.units) {
+          x.slot = p.part.two_a_cta ? 2 * blockIdx.x + (x.tile > 0 ? 0 : 1) : u + blockIdx.x;
+          at += out - in;
+        }
+        if (len == 0) {
+          u = -1;
+          if (whole_units && cut == p.part.units) {
+            if (n < 2) u = n == 0 ? blockIdx.x : 2 * gridDim.x - 1 - blockIdx.x;
+          } else if (cut < p.part.units) {
+            // as late as the next piece can be begun without a pause: when the
+            // last one's tiles are on their way
+            if (n > 0 && !tile_wait(BAR(L::LOADED), (n - 1) & 1, wc_idle, SITE_TILE_PIECE, n)) break;
+            if (lane == 0) u = (whole_units ? 0 : cut) + atomicAdd(p.counter, 1);
+            u = __shfl_sync(0xffffffffu, u, 0);
+          }
+          if (u >= p.part.units) u = -1;
+          if (u >= 0) {
             len = unit_tiles(u);
+            x.tile = 0;
             x.whole = p.direct && !DUAL;
             x.slot = u + gridDim.x;
-          } else {
-            u = -1;
           }
         }
         if (u >= 0) {

@@ -528,3 +528,36 @@ def test_captured_call_with_the_librarys_workspace():
     want = fa.forward_paged(*dev, lk)
     fa.sync_status()
     assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+
+
+@pytest.mark.parametrize("Hq,Hkv,d,lens_q,lens_k", [
+    (16, 16, 128, [2560], [2560]),                       # one or two whole units a CTA
+    (10, 10, 64, [2048, 700], [2048, 3000]),             # the same, one sequence shorter
+    (10, 5, 128, [2100, 1], [2100, 2100]),
+    (8, 8, 128, [3000], [3000]),                         # fewer units than CTAs, all cut
+    (16, 8, 64, [1800, 900, 0], [1800, 2000, 50]),       # all drawn, one sequence without a query
+    (40, 40, 64, [1000, 1000], [9000, 8000]),            # units of one length: some cut, the others drawn
+    (32, 32, 64, [1300, 1300], [1300, 600]),             # the second: rows that see nothing
+])
+def test_prompts_agree_with_the_padded_call(Hq, Hkv, d, lens_q, lens_k):
+    """Prompts whose units are cut, dealt out whole or drawn, against
+    fa_fwd_varlen on the same tensors; two runs equal bit for bit."""
+    B, Nq, Nk, page = len(lens_q), max(lens_q), max(lens_k), 64
+    g = torch.Generator().manual_seed(len(lens_q) + d + Hq)
+    q = torch.randn(B, Hq, Nq, d, generator=g).to(BF16).cuda()
+    k, v = (torch.randn(B, Hkv, Nk, d, generator=g).to(BF16).cuda() for _ in range(2))
+    kp, vp, table = (t.cuda() for t in make_cache(B, Hkv, d, page, [max(n, 1) for n in lens_k]))
+    lk, lq = (torch.tensor(n, dtype=torch.int32, device="cuda") for n in (lens_k, lens_q))
+    fa.kv_append(k, v, kp, vp, table, lk, lk)
+    G = Hq // Hkv
+    o, lse = fa.forward_varlen(q, k.repeat_interleave(G, 1), v.repeat_interleave(G, 1), lq, lk, causal=True)
+    for o_dtype in (F32, BF16):
+        a = fa.forward_paged(q, kp, vp, table, lk, lq, o_dtype=o_dtype)
+        b = fa.forward_paged(q, kp, vp, table, lk, lq, o_dtype=o_dtype)
+        fa.sync_status()
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+        # both round P to bf16 (8 bits) against their own running maximum: |v| below 6, sum of P 1; O once more
+        assert (a[0].float() - o).abs().max() <= 2 * 2.0 ** -8 * 6 + (2.0 ** -8 * 6 if o_dtype == BF16 else 0)
+        seen = torch.isfinite(lse)
+        assert torch.equal(seen, torch.isfinite(a[1])) and (a[1] - lse)[seen].abs().max() <= 1e-4
+        assert not a[0][~seen].any()
