@@ -836,14 +836,13 @@ __global__ void __launch_bounds__(256) merge_lanes_kernel(const __grid_constant_
     own = step_pieces(p.part, b, head, p.seq.Hkv);
   else
     own = tile_pieces(p.part, unit);
-  if (p.direct && !p.part.dual && own.n == 1) live = false;  // written by the only CTA that had it
+  if (p.direct && own.n == 1) live = false;  // written by the only CTA that had it
   Merged<C> m;
   m.clear();
   auto gather = [&](auto steps_tag, const PartRef& ref, const Pieces& x, int row) {
     constexpr bool ROWS = decltype(steps_tag)::value;  // the step kernel's layout
     constexpr int U = 2;  // pieces in flight
-    const bool dual = !ROWS && ref.dual;
-    const int n = live ? (dual ? 2 * x.n : x.n) : 0;
+    const int n = live ? x.n : 0;
     for (int k0 = sub; k0 < n; k0 += WARPS * U) {
       float lse[U], v[U][C];
 #pragma unroll
@@ -851,8 +850,7 @@ __global__ void __launch_bounds__(256) merge_lanes_kernel(const __grid_constant_
         const int k = k0 + u * WARPS;
         lse[u] = -CUDART_INF_F;
         if (k < n) {
-          const long long at =
-              dual ? piece_row(ref, x, k >> 1, row + (k & 1) * kTileRows) : piece_row(ref, x, k, row);
+          const long long at = piece_row(ref, x, k, row);
           lse[u] = ref.lse[at];
           const float* src = ref.o + (ROWS ? at * D + C * part : tile_part(at, C * part, D));
 #pragma unroll
@@ -975,7 +973,7 @@ Plan make_plan(int B, int Hkv, int G, int Nq, int d, bool with_prefix) {
   x.chunk = B < kLineSequences ? B : kLineSequences;
   if (x.steps)
     x.own_slots = static_cast<size_t>(x.chunk) * Hkv + kMaxCtas;
-  else if (with_prefix || x.rows <= kTileRows)
+  else if (with_prefix)
     x.own_slots = static_cast<size_t>(B) * Hkv * x.pairs + kMaxTileCtas;
   else
     x.own_slots = 2 * kMaxTileCtas;
@@ -1024,7 +1022,7 @@ cudaError_t launch_paged_d(const PagedArgs& a, cudaStream_t stream) {
     t.line_out = table;
     t.counter = table + kTileLine + 3;
     const int piece_cost = !prefix && !dual && 2 * units >= tile_ctas ? kTilePieceCost : 0;
-    t.part = PartRef{table, tile_ctas, kMinTiles, cut, direct && !dual, piece_cost, kPairRows, dual, units, heads,
+    t.part = PartRef{table, tile_ctas, kMinTiles, cut, direct, piece_cost, kPairRows, dual, units, heads,
                      pairs, head_group(heads, pairs, keys, D, tile_ctas), a.part + at,
                      a.part + at + slots * kPairRows * D};
     t.box_rows = a.box_rows;
@@ -1063,7 +1061,7 @@ cudaError_t launch_paged_d(const PagedArgs& a, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     c.seq = all;
     c.part = t.part;
-    c.units = c.direct && !t.part.dual ? t.part.cut : t.part.units;
+    c.units = c.direct ? t.part.cut : t.part.units;
     c.o = a.o;
     c.lse = a.lse;
     return launch_merge_lanes<D, false>(c, a.sms, stream);

@@ -62,9 +62,9 @@ struct PartRef {
   int piece_cost;
   int slot_rows;
   // 1: a unit of the tile kernel has at most 128 rows, so that its tile B would
-  // be empty: tile B takes the same rows and every other key tile, and leaves
-  // its partial result in the slot's second half.  (8 sequences x 8 heads x 64
-  // rows x 8192 keys: 65 us, 71 with tile A alone.)
+  // be empty: tile B takes the same rows and every other key tile, and the two
+  // are put together in the CTA.  (8 sequences x 8 heads x 64 rows x 8192 keys:
+  // 65 us, 71 with tile A alone.)
   int dual;
   int units;
   int heads, pairs, group;  // the tile kernel: (sequence, head)s, row pairs of each, heads dealt out together

@@ -73,9 +73,9 @@ constexpr float kTau = 8.f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kRows = 128;        // rows and keys a tile
 // Key tiles before a piece's end that the next one is drawn.  (16 heads x 8192
-// tokens 233 us with 0 or 2, 231 with 4, 279 at the piece's beginning; 2 x 12 heads
-// x 5000 tokens 167, 167, 172 and 205.)
-constexpr int kTellTiles = 2;
+// tokens 231 us with 2, 230 with 4, 228 with 6, 284 at the piece's beginning; 2 x
+// 12 heads x 5000 tokens 169, 167, 169 and 204; 4 x 16 x 4096 262, 256, 258, 278.)
+constexpr int kTellTiles = 4;
 constexpr int kReaders = 11;      // warps that follow the pieces: all but the one that works them out
 
 enum TileSite : int {
@@ -121,13 +121,16 @@ struct TileLayout {
   static constexpr int PIECE_EMPTY = PIECE_FULL + 2;
   static constexpr int ROWS_FULL = PIECE_EMPTY + 2;
   static constexpr int LOADED = ROWS_FULL + 2;
-  static constexpr int DRAIN = LOADED + 1;
+  static constexpr int PAIR = LOADED + 1;    // two row tiles on the same rows: warps w and w + 4 have their statistics
+  static constexpr int PAIR_DONE = PAIR + 4; // ... and have read both accumulators
+  static constexpr int DRAIN = PAIR_DONE + 4;
   static constexpr int kNumBars = DRAIN + 1;
   static constexpr int kMiscOff = kBarOff + kNumBars * 8;
   static constexpr int kScratchOff = kMiscOff + 16;            // one word a warp
   static constexpr int kPieceOff = kScratchOff + 64;           // two pieces
   static constexpr int kRowOff = kPieceOff + 2 * 48;           // [2 pieces][256 rows] place in q and o, then last key
-  static constexpr int kLineOff = kRowOff + 2 * kPairRows * 8;
+  static constexpr int kStatOff = kRowOff + 2 * kPairRows * 8; // [2 row tiles][maximum, sum, correction][128]
+  static constexpr int kLineOff = kStatOff + 2 * 3 * kRows * 4;
   static constexpr int kSmemBytes = kLineOff + (kTileLine + 1) * 4 + 1024;
   static constexpr uint32_t kColO = 256;
 };
@@ -212,6 +215,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bars + 8 * (L::ROWS_FULL + i), 1);
     }
     mbar_init(bars + 8 * L::LOADED, 1);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(bars + 8 * (L::PAIR + i), 2);
+      mbar_init(bars + 8 * (L::PAIR_DONE + i), 2);
+    }
     mbar_init(bars + 8 * L::DRAIN, 1);
     *abort_flag = 0;
     mbar_fence_init();
@@ -349,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tS = tmem + lane_off + static_cast<uint32_t>(t * 128);
     const uint32_t tO = tmem + lane_off + L::kColO + static_cast<uint32_t>(t * D);
     const float scale_log2 = p.scale_log2;
-    uint32_t sn = 0, on = 0;
+    uint32_t sn = 0, on = 0, on2 = 0;
     bool ok = true;
     for (uint32_t n = 0; next_piece(n, ok); ++n) {
       ok = tile_wait(BAR(L::ROWS_FULL + (n & 1)), (n >> 1) & 1, wc_idle, SITE_TILE_PIECE, n);
@@ -455,11 +462,61 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++on;
         tc_fence_after();
       }
-      // (a tile without keys reads what was left in tensor memory, and drops it)
-      const bool live = l > 0.f;
-      const float inv = live ? 1.0f / (l + dl) : 0.f;
+      // The row is acc_own * f_own + acc_other * f_other (a tile without keys
+      // reads what was left in tensor memory, and drops it).
+      bool live = l > 0.f;
+      float f_own = live ? 1.0f / (l + dl) : 0.f, f_other = 0.f;
+      if constexpr (DUAL) {
+        // the other row tile's warp has the same rows, in the same lanes of
+        // tensor memory: each writes half of the columns of both together
+        float* stat = reinterpret_cast<float*>(smem + L::kStatOff) + r;
+        stat[t * 3 * kRows] = m_ref;
+        stat[t * 3 * kRows + kRows] = l;
+        stat[t * 3 * kRows + 2 * kRows] = dl;
+        if ((t ? pieces[n & 1].na : pieces[n & 1].nb) > 0) {
+          ok = tile_wait(BAR(L::O_FULL + 1 - t), on2 & 1, wc, SITE_TILE_O, n);
+          if (!ok) break;
+          ++on2;
+        }
+        mbar_arrive_warp(BAR(L::PAIR + (warp & 3)));
+        ok = tile_wait(BAR(L::PAIR + (warp & 3)), n & 1, wc_idle, SITE_TILE_O, n);
+        if (!ok) break;
+        tc_fence_after();
+        const float m2 = stat[(1 - t) * 3 * kRows], l2 = stat[(1 - t) * 3 * kRows + kRows];
+        const float dl2 = stat[(1 - t) * 3 * kRows + 2 * kRows];
+        const float m = l > 0.f ? (l2 > 0.f ? fmaxf(m_ref, m2) : m_ref) : m2;
+        const float a = l > 0.f ? ex2_approx(m_ref - m) : 0.f, a2 = l2 > 0.f ? ex2_approx(m2 - m) : 0.f;
+        live = live || l2 > 0.f;
+        const float inv = live ? 1.0f / (a * (l + dl) + a2 * (l2 + dl2)) : 0.f;
+        f_own = a * inv;
+        f_other = a2 * inv;
+        l = a * l + a2 * l2;
+        m_ref = m;
+      }
+      // columns c0 .. c0 + N - 1 of the row
+      auto columns = [&](int c0, auto& w) {
+        constexpr int N = sizeof(w) / 4;
+        auto fetch = [&](uint32_t from, uint32_t (&x)[N]) {
+          if constexpr (N == 32)
+            tmem_ld32(from + c0, x);
+          else
+            tmem_ld16(from + c0, x);
+        };
+        uint32_t x[N], y[DUAL ? N : 1];
+        fetch(tO, x);
+        if constexpr (DUAL) fetch(tmem + lane_off + L::kColO + static_cast<uint32_t>((1 - t) * D), y);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          w[i] = f_own > 0.f ? __uint_as_float(x[i]) * f_own : 0.f;
+          if constexpr (DUAL) w[i] += f_other > 0.f ? __uint_as_float(y[i]) * f_other : 0.f;
+        }
+      };
+      constexpr int kShare = DUAL ? 2 : 1;           // warps that write a row
+      const int share = DUAL ? t : 0;
       const bool whole = pieces[n & 1].whole;
-      const long long prow0 = static_cast<long long>(pieces[n & 1].slot) * kPairRows + t * kRows + (r - lane);
+      const long long prow0 =
+          static_cast<long long>(pieces[n & 1].slot) * kPairRows + (DUAL ? 0 : t * kRows) + (r - lane);
       const volatile uint32_t* at = row_at + (n & 1) * kPairRows + t * kRows + (r - lane);
       if (!whole) {
         // a partial result lies in runs of 16 bytes, a row group's 32 rows side
@@ -467,19 +524,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         float4* dst = reinterpret_cast<float4*>(p.part.o + prow0 * D) + lane;
         const bool keep = at[lane] != kNoRow;
 #pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t w[32];
-          tmem_ld32(tO + 32 * c, w);
-          tmem_ld_wait();
+        for (int c = share * D / 32 / kShare; c < (share + 1) * D / 32 / kShare; ++c) {
+          float w[32];
+          columns(32 * c, w);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            float4 x;
-            x.x = live ? __uint_as_float(w[4 * i]) * inv : 0.f;
-            x.y = live ? __uint_as_float(w[4 * i + 1]) * inv : 0.f;
-            x.z = live ? __uint_as_float(w[4 * i + 2]) * inv : 0.f;
-            x.w = live ? __uint_as_float(w[4 * i + 3]) * inv : 0.f;
-            if (keep) dst[(8 * c + i) * 32] = x;
-          }
+          for (int i = 0; i < 8; ++i)
+            if (keep) dst[(8 * c + i) * 32] = make_float4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
         }
       } else {
         // rows leave through the warp's staging area, 64 bytes at a time: each
@@ -496,26 +546,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           dst[k] = g == kNoRow ? nullptr
                                : static_cast<uint8_t*>(p.o) + static_cast<size_t>(g) * D * (half ? 2 : 4) + 16 * run;
         }
-        const int runs = half ? D / 32 : D / 16;
+        const int runs = (half ? D / 32 : D / 16) / kShare;
 #pragma unroll 1
-        for (int c = 0; c < runs; ++c) {
+        for (int c = share * runs; c < (share + 1) * runs; ++c) {
           uint32_t w[16];
           if (half) {
-            uint32_t v[32];
-            tmem_ld32(tO + 32 * c, v);
-            tmem_ld_wait();
+            float v[32];
+            columns(32 * c, v);
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-              w[i] = pack_bf16x2(__uint_as_float(v[2 * i]) * inv, __uint_as_float(v[2 * i + 1]) * inv);
+            for (int i = 0; i < 16; ++i) w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
           } else {
-            tmem_ld16(tO + 16 * c, w);
-            tmem_ld_wait();
+            float v[16];
+            columns(16 * c, v);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) * inv);
-          }
-          if (!live) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) w[i] = 0u;
+            for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(v[i]);
           }
 #pragma unroll
           for (int i = 0; i < 4; ++i)
@@ -534,12 +578,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       const uint32_t mine = at[lane];
-      if (mine != kNoRow) {
+      if (share == 0 && mine != kNoRow) {
         const float lse2 = live ? m_ref + log2f(l) : -CUDART_INF_F;
         if (whole)
           p.lse[mine] = live ? lse2 * kLn2 : -CUDART_INF_F;
         else
           p.part.lse[prow0 + lane] = lse2;
+      }
+      if constexpr (DUAL) {  // before the next product overwrites what the other warp reads
+        tc_fence_before();
+        mbar_arrive_warp(BAR(L::PAIR_DONE + (warp & 3)));
+        ok = tile_wait(BAR(L::PAIR_DONE + (warp & 3)), n & 1, wc_idle, SITE_TILE_O, n);
+        if (!ok) break;
+        tc_fence_after();
       }
       piece_done(n);
     }
@@ -930,7 +981,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int tiles = line[lo + 1] - line[lo] - p.part.piece_cost;
           x.tile = min(in, tiles);
           len = min(out, tiles) - x.tile;  // 0: the range begins behind the unit's last tile
-          x.whole = p.direct && !DUAL && len == tiles;
+          x.whole = p.direct && len == tiles;
           x.slot = p.part.two_a_cta ? 2 * blockIdx.x + (x.tile > 0 ? 0 : 1) : u + blockIdx.x;
           at += out - in;
         }
@@ -949,7 +1000,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (u >= 0) {
             len = unit_tiles(u);
             x.tile = 0;
-            x.whole = p.direct && !DUAL;
+            x.whole = p.direct;
             x.slot = u + gridDim.x;
           }
         }
