@@ -99,11 +99,15 @@ struct Piece {
   int slot;        // of the partial result
 };
 
-template <int D>
+template <int D, bool DUAL>
 struct TileLayout {
   static constexpr int kTileBytes = kRows * D * 2;
-  static constexpr int kSlots = (D == 128) ? 4 : 8;
-  static constexpr int kRingOff = 2 * kTileBytes;
+  // two tiles of rows; where both row tiles have the same rows one, and one
+  // more key or value tile on its way (64 sequences x 8 heads x 64 rows x 1000
+  // keys: 85 us with four, 80 with five)
+  static constexpr int kQTiles = DUAL ? 1 : 2;
+  static constexpr int kSlots = ((D == 128) ? 6 : 12) - kQTiles * (D == 128 ? 1 : 2);
+  static constexpr int kRingOff = kQTiles * kTileBytes;
   // a warp's staging of its output rows: 32 rows of 64 bytes, so that rows
   // leave in 64-byte runs instead of a 16-byte store a row
   static constexpr int kStageOff = kRingOff + kSlots * kTileBytes;
@@ -177,7 +181,7 @@ template <int D, bool PREFIX, bool DUAL>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ PagedTiles p) {
-  using L = TileLayout<D>;
+  using L = TileLayout<D, DUAL>;
   constexpr int S = L::kSlots;
   constexpr int CB = D / 64;
   extern __shared__ uint8_t smem_raw[];
@@ -673,7 +677,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const SDesc vdesc0 = sdesc_sw128(sbase + L::kRingOff, 1024, CB * 1024);
         constexpr uint32_t kTileUnits = L::kTileBytes >> 4;
         auto issue_s = [&](int t, uint32_t slot) {
-          const SDesc qd = qdesc0 + static_cast<uint32_t>(t) * kTileUnits;
+          const SDesc qd = qdesc0 + static_cast<uint32_t>(DUAL ? 0 : t) * kTileUnits;
           const SDesc kd = kdesc0 + slot * kTileUnits;
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks) {
@@ -711,17 +715,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 issue_s(t, kpos % S);
                 umma_commit(BAR(L::S_FULL + t));
                 umma_commit(BAR(L::KV_EMPTY + kpos % S));
-                if (j + 2 >= tiles) umma_commit(BAR(L::Q_EMPTY + t));  // the piece's last use of Q
+                if (j + 1 == tiles) umma_commit(BAR(L::Q_EMPTY + 0));  // the piece's last use of Q
                 return true;
               };
               if (na > 0) {
                 if (!arrived(L::Q_FULL + 0, qa) || !start(0, 0)) return false;
                 ++qa;
               }
-              if (nb > 0) {
-                if (!arrived(L::Q_FULL + 1, qb) || !start(1, 1)) return false;
-                ++qb;
-              }
+              if (nb > 0 && !start(1, 1)) return false;
               for (int j = 0; j < tiles; ++j) {
                 const int t = j & 1;
                 const uint32_t vpos = kvbase + 2 * j + 1;
@@ -838,7 +839,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (uint32_t n = 0; next_piece(n, ok); ++n) {
         const volatile Piece& x = pieces[n & 1];
         const int r0 = x.r0, head = x.head, tile0 = x.tile * kRows, clean = x.clean, limit = x.limit;
-        const int nt[2] = {x.na, x.nb};
+        const int nt[2] = {x.na, DUAL ? 0 : x.nb};  // key tiles of what each tile of rows is for
         const int buf = (n & 1) * kPairRows;
         // a sequence's rows of a key head lie together (rows of the tile behind
         // the last are the next head's, and see no key), the prefix's rows in
@@ -1038,7 +1039,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <int D, bool PREFIX, bool DUAL>
 cudaError_t launch_t(const PagedTiles& p, const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                      int ctas, cudaStream_t stream) {
-  using L = TileLayout<D>;
+  using L = TileLayout<D, DUAL>;
   auto kern = paged_tiles_kernel<D, PREFIX, DUAL>;
   static std::atomic<unsigned long long> ready{0};
   cudaError_t e = setup_kernel_once(kern, L::kSmemBytes, kLaunchRegs, ready);
