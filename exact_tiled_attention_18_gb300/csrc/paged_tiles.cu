@@ -45,7 +45,7 @@
 //
 //   warps 0-3  softmax of tile A     warp 8   TMA producer
 //   warps 4-7  softmax of tile B     warp 9   MMA issuer, owns tensor memory
-//                                    warp 10  gathers rows; zeroes values behind the last key
+//                                    warp 10  brings rows in; zeroes values behind the last key
 //                                    warp 11  works out the pieces
 #include <cuda_runtime.h>
 #include <math_constants.h>
@@ -506,7 +506,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           else
             tmem_ld16(from + c0, x);
         };
-        uint32_t x[N], y[DUAL ? N : 1];
+        uint32_t x[N];
+        [[maybe_unused]] uint32_t y[DUAL ? N : 1];
         fetch(tO, x);
         if constexpr (DUAL) fetch(tmem + lane_off + L::kColO + static_cast<uint32_t>((1 - t) * D), y);
         tmem_ld_wait();

@@ -538,6 +538,8 @@ def test_captured_call_with_the_librarys_workspace():
     (16, 8, 64, [1800, 900, 0], [1800, 2000, 50]),       # all drawn, one sequence without a query
     (40, 40, 64, [1000, 1000], [9000, 8000]),            # units of one length: some cut, the others drawn
     (32, 32, 64, [1300, 1300], [1300, 600]),             # the second: rows that see nothing
+    (16, 8, 128, [24 - i % 3 for i in range(48)], [30 + 7 * i for i in range(48)]),  # 48 rows: two row tiles on them
+    (64, 8, 128, [16] * 3, [5000, 2100, 17]),            # 128 rows, few units: cut
 ])
 def test_prompts_agree_with_the_padded_call(Hq, Hkv, d, lens_q, lens_k):
     """Prompts whose units are cut, dealt out whole or drawn, against
