@@ -760,7 +760,8 @@ def kv_append(k, v, k_pages, v_pages, block_table, seqlens_k, seqlens_q=None, tu
     rotates the queries, into ``q_out`` (contiguous; made here by default, its
     padding rows then unset).  ``seqlens_k``: int32 [B], each sequence's keys
     with the new tokens; ``seqlens_q``: int32 [B], its new tokens (default N).
-    Returns q_out, or None without q."""
+    Tokens past the end of their row of ``block_table`` are not stored, which
+    sync_status reports.  Returns q_out, or None without q."""
     import torch
     if k.dim() != 4 or not k.is_cuda:
         raise ValueError("k must be a bf16 CUDA tensor [B, Hkv, N, d] with contiguous d")

@@ -1071,7 +1071,8 @@ const char* fa_status_string(fa_status s) {
     case FA_ERR_LAUNCH: return "FA_ERR_LAUNCH: the CUDA runtime refused a launch or an allocation";
     case FA_ERR_TIMEOUT: return "FA_ERR_TIMEOUT: a kernel pipeline wait ran past its limit";
     case FA_ERR_DEVICE_FAULT: return "FA_ERR_DEVICE_FAULT: the stream reported a CUDA error";
-    case FA_ERR_BAD_PAGE: return "FA_ERR_BAD_PAGE: a block table names a page outside the cache";
+    case FA_ERR_BAD_PAGE:
+      return "FA_ERR_BAD_PAGE: a block table names a page outside the cache, or ends before an appended token";
   }
   return "unknown fa_status";
 }

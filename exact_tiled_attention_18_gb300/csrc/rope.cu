@@ -28,6 +28,8 @@
 // blocks an SM 86.5.
 #include <cuda_runtime.h>
 
+#include <climits>
+
 #include "ptx.cuh"
 #include "serving.h"
 
@@ -220,19 +222,22 @@ __global__ void __launch_bounds__(kRopeThreads) append_kernel(const AppendArgs a
   const int c = threadIdx.x % LANES;
   const int b = static_cast<int>(item / a.N);
   const int t = static_cast<int>(item - static_cast<long long>(b) * a.N);
-  const int capacity = a.table.max_pages * a.table.page_size;
+  // (the keys' number as it is given, not cut to what the table holds: a token
+  // past the table's end must not come to lie on an earlier one's row)
   int lq, lk;
-  paged_lens(a.seqlens_q, a.seqlens_k, b, a.N, capacity, lq, lk);
+  paged_lens(a.seqlens_q, a.seqlens_k, b, a.N, INT_MAX, lq, lk);
   if (t >= lq) return;  // padding: nothing of it is written
   const int place = lk - lq + t;
   const int hq = a.q ? a.Hq : 0;
   const int heads = hq + 2 * a.Hkv;
   const int h0 = blockIdx.y * heads_per_thread;
   const int h1 = min(h0 + heads_per_thread, heads);
-  // the row of the cache; a token before position 0, or one whose page does
-  // not exist, has none
+  // the row of the cache; a token before position 0 or past the table's end,
+  // or one whose page does not exist, has none
   long long row = -1;
-  if (h1 > hq && place >= 0) {
+  if (h1 > hq && place >= a.table.max_pages * a.table.page_size) {
+    if (c == 0) record_bad_page(a.status, SITE_PAGE_PAST_TABLE, b, place);
+  } else if (h1 > hq && place >= 0) {
     const int page = __ldg(a.table.block_table + b * a.table.table_stride + place / a.table.page_size);
     if (page >= 0 && page < a.table.num_pages)
       row = (static_cast<long long>(page) * a.Hkv) * a.table.page_size + place % a.table.page_size;

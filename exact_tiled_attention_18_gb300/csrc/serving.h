@@ -16,7 +16,7 @@ namespace fa {
 constexpr int FA_DEV_BAD_PAGE = 7;
 
 // Sites recorded with FA_DEV_BAD_PAGE.
-enum PageSite : int { SITE_PAGE_APPEND = 71, SITE_PAGE_READ = 72 };
+enum PageSite : int { SITE_PAGE_APPEND = 71, SITE_PAGE_READ = 72, SITE_PAGE_PAST_TABLE = 81 };
 
 // A [B][H][N][d] tensor with contiguous d: element strides of the others.
 struct Strides {
@@ -134,13 +134,14 @@ __device__ __forceinline__ void grid_trigger() { asm volatile("griddepcontrol.la
 // which the compiler may move before it.
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
-// Records an entry of a block table that names no page (first failure wins).
-__device__ __forceinline__ void record_bad_page(int* status, int site, int block, int page) {
+// Records an entry of a block table that names no page, or a position behind
+// the table's last one (first failure wins).
+__device__ __forceinline__ void record_bad_page(int* status, int site, int sequence, int what) {
   if (atomicCAS(status, 0, FA_DEV_BAD_PAGE) == 0) {
     volatile int* s = status;
     s[1] = site;
-    s[2] = block;
-    s[3] = page;
+    s[2] = sequence;
+    s[3] = what;
     __threadfence();
   }
 }

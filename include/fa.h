@@ -69,7 +69,8 @@ typedef enum {
   FA_ERR_LAUNCH = 4,        /* the CUDA runtime refused a launch or an allocation */
   FA_ERR_TIMEOUT = 5,       /* a kernel wait ran past its limit; the kernel returned early */
   FA_ERR_DEVICE_FAULT = 6,  /* the stream reported a CUDA error while synchronising */
-  FA_ERR_BAD_PAGE = 7       /* a block table names a page outside the cache (reported by fa_sync_status) */
+  FA_ERR_BAD_PAGE = 7       /* a block table names a page outside the cache, or ends before an appended token
+                               (reported by fa_sync_status) */
 } fa_status;
 
 /* Element type of the forward output O (fa_fwd_ex, fa_bwd_ex). */
@@ -457,7 +458,9 @@ fa_status fa_rope(const void* x, int x_dtype, long long x_stride_b, long long x_
  *               (table_stride >= 0 in elements); entries behind a sequence's
  *               last page are never read.
  *   seqlens_k : device ints, the keys of each sequence, the new tokens of
- *               this step among them (clamped to [0, max_pages * page_size]).
+ *               this step among them (negative: 0).  More than max_pages *
+ *               page_size: the attention calls read that many; the append
+ *               writes the tokens that have a place and reports the others.
  *   seqlens_q : device ints, the new tokens of each sequence (clamped to
  *               [0, N]); NULL: all N (Nq).
  * Token t of a sequence with Lq new tokens and Lk keys is at position
@@ -484,8 +487,11 @@ fa_status fa_rope(const void* x, int x_dtype, long long x_stride_b, long long x_
  *           copies q) without a rotation, and the other three are not read.
  * Rows at or past Lq are padding: neither the cache nor q_out is written for
  * them.  A token whose position is negative (Lq > Lk) has no place in the
- * cache; its q_out row is written.  Two new tokens that a block table puts on
- * one cache row leave either's value there, element by element.
+ * cache; its q_out row is written.  A token whose position is max_pages *
+ * page_size or more has none either, and is reported as FA_ERR_BAD_PAGE; its
+ * q_out row is rotated by the position that it would have had.  Two new tokens
+ * that a block table puts on one cache row leave either's value there, element
+ * by element.
  */
 fa_status fa_kv_append(const void* k, long long k_stride_b, long long k_stride_h, long long k_stride_n, const void* v,
                        long long v_stride_b, long long v_stride_h, long long v_stride_n, const void* q,
@@ -565,9 +571,10 @@ fa_status fa_sync_status(fa_stream_t stream);
  * out[0] status code, out[1] wait site, out[2] block index, out[3] work unit.
  * Wait sites: 1-7 forward, 11-20 dK/dV, 21-32 dQ, 35-36 decode, 41-47 FP8
  * forward, 51-59 the single-pass row-term pass, 61-63 the single-pass dK/dV
- * sweep, 71-80 the paged calls (each kernel's source names them).  After
+ * sweep, 71-81 the paged calls (each kernel's source names them).  After
  * FA_ERR_BAD_PAGE: out[2] the sequence (0 for a prefix), out[3] the table
- * entry.
+ * entry, or where out[1] is 81 the position of an appended token that is
+ * behind the table's last one.
  * Returns FA_OK, or FA_ERR_INVALID_ARG if out is NULL.
  */
 fa_status fa_last_failure(int out[4]);

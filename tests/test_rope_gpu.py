@@ -336,3 +336,70 @@ def test_many_heads_of_one_token():
     fa.sync_status()
     assert torch.equal(kp[:, :, 4:5], y) and torch.equal(vp[:, :, 4:5], x)
     assert not kp[:, :, :4].any() and not vp[:, :, 5:].any()
+
+
+@pytest.mark.parametrize("N,lens_k,lens_q", [
+    (1, [97, 96, 300], None),                 # one token past six pages of 16, the last place, far behind the end
+    (40, [100, 130, 96], None),               # across the end, 34 tokens past it, up to it
+    (3, [2 ** 31 - 1, 2, 98], [3, 3, 1]),     # the largest length; a token before position 0; one past the end
+])
+def test_append_past_the_table_keeps_the_cache_and_is_reported(N, lens_k, lens_q):
+    """Tokens behind the last place that the table reaches: no row of the cache
+    changes for them, q is rotated by their own positions, and the call is
+    reported; the other tokens are where they belong."""
+    B, Hq, Hkv, d, page, pages = 3, 4, 2, 64, 16, 6
+    g = torch.Generator().manual_seed(N)
+    kp, vp = (torch.randn(B * pages + 1, Hkv, page, d, generator=g).to(BF16) for _ in range(2))
+    table = torch.randperm(B * pages, generator=g).to(torch.int32).view(B, pages)
+    q, k, v = (torch.randn(B, h, N, d, generator=g).to(BF16) for h in (Hq, Hkv, Hkv))
+    turns = fa.rope_turns(d, device="cuda")
+    a, b = kp.cuda(), vp.cuda()
+    lk = torch.tensor(lens_k, dtype=torch.int32, device="cuda")
+    lq = torch.tensor(lens_q, dtype=torch.int32, device="cuda") if lens_q else None
+    q_out = torch.full((B, Hq, N, d), 9.0, dtype=BF16, device="cuda")
+    fa.kv_append(k.cuda(), v.cuda(), a, b, table.cuda(), lk, lq, turns=turns, q=q.cuda(), q_out=q_out)
+    with pytest.raises(fa.FAError) as e:
+        fa.sync_status()
+    assert e.value.status == fa.FA_ERR_BAD_PAGE
+    ql = lens_q or [N] * B
+    pos = [[lens_k[i] - ql[i] + t for t in range(N)] for i in range(B)]
+    _, site, sequence, position = fa.fa_last_failure()
+    assert site == 81 and position in [p for p in pos[sequence][:ql[sequence]] if p >= pages * page]
+    fa.sync_status()  # reported once
+    p = torch.tensor(pos, dtype=torch.int32, device="cuda")
+    rk, rq = fa.rope_forward(k.cuda(), turns, p).cpu(), fa.rope_forward(q.cuda(), turns, p).cpu()
+    for i in range(B):
+        for t in range(ql[i]):
+            if 0 <= pos[i][t] < pages * page:
+                at = table[i, pos[i][t] // page], slice(None), pos[i][t] % page
+                kp[at], vp[at] = rk[i, :, t], v[i, :, t]
+            assert torch.equal(q_out[i, :, t].cpu(), rq[i, :, t])
+        assert bool((q_out[i, :, ql[i]:] == 9.0).all())
+    assert torch.equal(a.cpu(), kp) and torch.equal(b.cpu(), vp)
+
+
+def test_append_loop_runs_over_the_end_of_its_table():
+    """A captured decoding loop replayed past the table's end: the last rows
+    stay what the last tokens with a place were."""
+    kp, vp = (torch.zeros(2, 1, 16, 64, dtype=BF16, device="cuda") for _ in range(2))
+    table = torch.tensor([[1, 0]], dtype=torch.int32, device="cuda")
+    lk = torch.tensor([0], dtype=torch.int32, device="cuda")
+    x = torch.zeros(1, 1, 1, 64, dtype=BF16, device="cuda")
+    fa.kv_append(x, x, kp, vp, table, lk)  # a first call: position -1, nothing written
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        lk.add_(1)
+        x.add_(1)
+        fa.kv_append(x, x, kp, vp, table, lk)
+    lk.zero_(), x.zero_()
+    for _ in range(32):
+        graph.replay()
+    fa.sync_status()
+    want = torch.arange(1, 33).to(BF16).view(2, 16).flip(0)  # page 1 first
+    assert torch.equal(kp[:, 0, :, 0].cpu(), want)
+    for _ in range(5):
+        graph.replay()
+    with pytest.raises(fa.FAError):
+        fa.sync_status()
+    assert torch.equal(kp[:, 0, :, 0].cpu(), want) and torch.equal(vp[:, 0, :, 5].cpu(), want)
