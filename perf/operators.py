@@ -89,7 +89,10 @@ def draw(rng):
     Nq = rng.choice([1, 1, rng.randint(2, 8), _log(rng, 9, 200)])
     B = _log(rng, 2, 256)
     while B * Hkv * G * Nq > 16384:
-        B = (B + 1) // 2
+        if B > 1:
+            B = (B + 1) // 2
+        else:  # one sequence's rows alone
+            Nq = (Nq + 1) // 2
     P = page * _log(rng, 4, 32768 // page)
     return dict(op=op, B=B, Hq=G * Hkv, Hkv=Hkv, Nq=Nq, d=d, page=page, P=P, Lmin=Nq,
                 Lmax=Nq + _log(rng, 1, 1024))
