@@ -567,8 +567,9 @@ __global__ void __launch_bounds__(kStepThreads, step_ctas_per_sm<RB>())
             weights.y += y.y;
           }
         }
-        const float s0 = weights.x > 0.f ? __fdividef(1.f, weights.x) : 0.f;
-        const float s1 = weights.y > 0.f ? __fdividef(1.f, weights.y) : 0.f;
+        // (sums are 0 only where no key is seen; a NaN goes through)
+        const float s0 = weights.x != 0.f ? __fdividef(1.f, weights.x) : 0.f;
+        const float s1 = weights.y != 0.f ? __fdividef(1.f, weights.y) : 0.f;
         // neighbours in the column exchange rows: a lane then holds two
         // adjacent columns of row fc (even columns' lanes) or fc + 1 (odd ones')
         const int r = 8 * m + fc + odd;
@@ -585,7 +586,7 @@ __global__ void __launch_bounds__(kStepThreads, step_ctas_per_sm<RB>())
         }
         if (warp == 0 && fr < 2 && valid) {
           const float total = odd ? sum.y : sum.x;
-          lse[r] = total > 0.f ? ((odd ? m_ref[m][1] : m_ref[m][0]) + __log2f(total)) * unit : -CUDART_INF_F;
+          lse[r] = total != 0.f ? ((odd ? m_ref[m][1] : m_ref[m][0]) + __log2f(total)) * unit : -CUDART_INF_F;
         }
       }
     };
@@ -660,7 +661,8 @@ __device__ __forceinline__ long long piece_row(const PartRef& r, const Pieces& x
   return static_cast<long long>(slot) * r.slot_rows + in;
 }
 
-// The running merge of partial results: maximum, sum and C columns.
+// The running merge of partial results: maximum, sum (0: no key seen so far)
+// and C columns.
 template <int C>
 struct Merged {
   float top, sum, acc[C];
@@ -677,7 +679,7 @@ struct Merged {
   __device__ __forceinline__ void add(const float (&lse)[U], const float (&v)[U][C]) {
     float m = top;
 #pragma unroll
-    for (int u = 0; u < U; ++u) m = fmaxf(m, lse[u]);
+    for (int u = 0; u < U; ++u) m = max_nan(m, lse[u]);
     if (m == -CUDART_INF_F) return;
     const float g = ex2_approx(top - m);
     top = m;
@@ -694,8 +696,8 @@ struct Merged {
     }
   }
 
-  __device__ __forceinline__ float lse() const { return sum > 0.f ? (top + __log2f(sum)) * kLn2 : -CUDART_INF_F; }
-  __device__ __forceinline__ float scale() const { return sum > 0.f ? __fdividef(1.f, sum) : 0.f; }
+  __device__ __forceinline__ float lse() const { return sum != 0.f ? (top + __log2f(sum)) * kLn2 : -CUDART_INF_F; }
+  __device__ __forceinline__ float scale() const { return sum != 0.f ? __fdividef(1.f, sum) : 0.f; }
 };
 
 // Merges the rows of the step kernel's units where there is no prefix.  A warp
@@ -763,7 +765,7 @@ __global__ void __launch_bounds__(256) merge_rows_kernel(const __grid_constant__
     for (int o = 1; o < WARPS; ++o) {
       const float m2 = s_max[warp + o];
       if (m2 == -CUDART_INF_F) continue;
-      const float top = fmaxf(m[0].top, m2);
+      const float top = max_nan(m[0].top, m2);
       const float f = ex2_approx(m2 - top), g = ex2_approx(m[0].top - top);
       m[0].top = top;
       m[0].sum = m[0].sum * g + s_sum[warp + o] * f;
@@ -877,7 +879,7 @@ __global__ void __launch_bounds__(256) merge_lanes_kernel(const __grid_constant_
 #pragma unroll 1
     for (int o = 1; o < WARPS; ++o) {
       const float m2 = s_max[o][lane];
-      const float top = fmaxf(m.top, m2);
+      const float top = max_nan(m.top, m2);
       if (top == -CUDART_INF_F) continue;
       const float f = ex2_approx(m2 - top), g2 = ex2_approx(m.top - top);
       m.top = top;

@@ -467,8 +467,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
       }
       // The row is acc_own * f_own + acc_other * f_other (a tile without keys
-      // reads what was left in tensor memory, and drops it).
-      bool live = l > 0.f;
+      // reads what was left in tensor memory, and drops it).  A sum is 0 only
+      // where no key is seen; a NaN goes through.
+      bool live = l != 0.f;
       float f_own = live ? 1.0f / (l + dl) : 0.f, f_other = 0.f;
       if constexpr (DUAL) {
         // the other row tile's warp has the same rows, in the same lanes of
@@ -488,9 +489,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         const float m2 = stat[(1 - t) * 3 * kRows], l2 = stat[(1 - t) * 3 * kRows + kRows];
         const float dl2 = stat[(1 - t) * 3 * kRows + 2 * kRows];
-        const float m = l > 0.f ? (l2 > 0.f ? fmaxf(m_ref, m2) : m_ref) : m2;
-        const float a = l > 0.f ? ex2_approx(m_ref - m) : 0.f, a2 = l2 > 0.f ? ex2_approx(m2 - m) : 0.f;
-        live = live || l2 > 0.f;
+        const float m = l != 0.f ? (l2 != 0.f ? fmaxf(m_ref, m2) : m_ref) : m2;
+        const float a = l != 0.f ? ex2_approx(m_ref - m) : 0.f, a2 = l2 != 0.f ? ex2_approx(m2 - m) : 0.f;
+        live = live || l2 != 0.f;
         const float inv = live ? 1.0f / (a * (l + dl) + a2 * (l2 + dl2)) : 0.f;
         f_own = a * inv;
         f_other = a2 * inv;
@@ -513,8 +514,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld_wait();
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-          w[i] = f_own > 0.f ? __uint_as_float(x[i]) * f_own : 0.f;
-          if constexpr (DUAL) w[i] += f_other > 0.f ? __uint_as_float(y[i]) * f_other : 0.f;
+          w[i] = f_own != 0.f ? __uint_as_float(x[i]) * f_own : 0.f;
+          if constexpr (DUAL) w[i] += f_other != 0.f ? __uint_as_float(y[i]) * f_other : 0.f;
         }
       };
       constexpr int kShare = DUAL ? 2 : 1;           // warps that write a row
