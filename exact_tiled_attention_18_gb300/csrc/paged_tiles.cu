@@ -51,6 +51,7 @@
 #include <math_constants.h>
 
 #include <atomic>
+#include <cfloat>
 #include <type_traits>
 
 #include "internal.h"
@@ -71,6 +72,7 @@ static_assert(2 * 128 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * kLaunchReg
               "register split exceeds the launch allocation");
 constexpr float kTau = 8.f;
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kNoScore = -FLT_MAX;  // reference maximum before any score: finite, so that -inf less it is -inf
 constexpr int kRows = 128;        // rows and keys a tile
 // Key tiles before a piece's end that the next one is drawn.  (16 heads x 8192
 // tokens 231 us with 2, 230 with 4, 228 with 6, 284 at the piece's beginning; 2 x
@@ -404,9 +406,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c = 0; c < 5; ++c) t3[c] = fmax3(t2[3 * c], t2[3 * c + 1], t2[3 * c + 2]);
         const float mt = fmaxf(fmax3(t3[0], t3[1], t3[2]), fmaxf(t3[3], t3[4])) * scale_log2;
         if (j == 0) {
-          // a row sees a leading range of the piece's keys: if it sees none of
-          // the first tile it sees none at all
-          m_ref = mt == -CUDART_INF_F ? 0.f : mt;
+          // -inf: the row sees a leading range of the piece's keys and so none
+          // at all, or keys whose scores are -inf, behind which any other's
+          // becomes the reference
+          m_ref = fmaxf(mt, kNoScore);
         } else {
           const bool need = mt > m_ref + kTau;
           if (__any_sync(0xffffffffu, need)) {

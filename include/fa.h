@@ -521,7 +521,7 @@ fa_status fa_kv_append(const void* k, long long k_stride_b, long long k_stride_h
  * NaN included; the values of keys that some query of the sequence sees must
  * be finite.  A row with a NaN or +inf score (a NaN in its query or in a key
  * that it sees) has O = NaN and LSE = NaN, however the call is divided; the
- * other rows do not depend on it.
+ * other rows do not depend on it.  A key with a score of -inf has no weight.
  */
 fa_status fa_fwd_paged(const void* q, const void* k_pages, const void* v_pages, int num_pages, int page_size,
                        const int* block_table, long long table_stride, int max_pages, void* o, int o_dtype,

@@ -1,5 +1,5 @@
-"""Scores and lengths at the edges of the paged attention: NaN in keys and
-queries that are seen, in every division of the work."""
+"""Scores at the edges of what the paged attention takes: NaN in keys and
+queries that are seen, in every division of the work, and scores of -inf."""
 
 import numpy as np
 import pytest
@@ -61,3 +61,27 @@ def test_nan_of_a_seen_key_or_query_reaches_its_rows_and_no_others(way, place):
         assert torch.equal(torch.isnan(o), hit[..., None].expand_as(o))
         o[hit], lse[hit] = torch.tensor(ref[0]).to(o_dtype)[hit], torch.tensor(ref[1]).float()[hit]
         check(o, lse, ref, q[some], kp, scale_for(d), bits, way[0])
+
+
+@pytest.mark.parametrize("way", [w for w in WAYS if min(w[8]) - w[4] > 200 or w[0].startswith("prefix")],
+                         ids=lambda w: w[0].replace(" ", "-"))
+def test_keys_of_score_minus_infinity_have_no_weight(way):
+    """The first 200 keys score -inf and the others about -512: rows are the
+    softmax over the others."""
+    _, B, Hq, Hkv, Nq, d, page, prefix, lens, bits = way
+    q, kp, vp, table = make_batch(B, Hq, Hkv, Nq, d, page, lens, seed=Nq + d + B)
+    n = prefix // page
+    prefix_table = table[int(np.argmax(lens)), :n].clone()
+    table[:, :n] = prefix_table
+    q[..., 0], q[..., 1] = 1.0, 64.0
+    kp[..., 1] -= 512 / 64 * d ** 0.5  # (NaN where no key is)
+    clean = kp.clone()
+    for b in range(B):
+        for p in range(200):
+            kp[table[b, p // page], :, p % page, 0] = -float("inf")
+    some = sorted({0, B // 2, B - 1})
+    ref = reference(q[some], kp, vp, table[some], [lens[b] for b in some], None, True)
+    assert np.all(np.isfinite(ref[1])) and ref[1].max() < -300
+    kw = dict(prefix=prefix, prefix_table=prefix_table) if prefix else {}
+    o, lse = run(q, kp, vp, table, lens, **kw)
+    check(o[some], lse[some], ref, q[some], clean, scale_for(d), bits, way[0])
