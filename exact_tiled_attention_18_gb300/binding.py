@@ -112,6 +112,8 @@ def lib() -> ctypes.CDLL:
         L.fa_sync_status.restype = st
         L.fa_test_set_stall.argtypes = [i]
         L.fa_test_set_stall.restype = st
+        L.fa_test_map_encodes.argtypes = []
+        L.fa_test_map_encodes.restype = ll
         L.fa_last_failure.argtypes = [ctypes.POINTER(ctypes.c_int)]
         L.fa_last_failure.restype = st
         L.fa_status_string.argtypes = [st]
@@ -286,6 +288,11 @@ def fa_test_set_stall(unit: int) -> int:
     """Testing hook: from the next call on, CTA 0 leaves one tile of its
     unit-th work unit unloaded (-1: off).  Returns the status."""
     return lib().fa_test_set_stall(int(unit))
+
+
+def fa_test_map_encodes() -> int:
+    """Testing hook: tensor maps encoded by the driver since the library was loaded."""
+    return int(lib().fa_test_map_encodes())
 
 
 def fa_last_failure() -> list:

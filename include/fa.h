@@ -591,6 +591,10 @@ fa_status fa_last_failure(int out[4]);
  */
 fa_status fa_test_set_stall(int unit);
 
+/* Testing hook: how many tensor maps the library has had the driver encode
+ * since it was loaded.  A call on tensors that it has seen adds none. */
+long long fa_test_map_encodes(void);
+
 /* Static, human-readable name of a status code; never NULL. */
 const char* fa_status_string(fa_status s);
 
