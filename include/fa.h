@@ -413,7 +413,10 @@ typedef enum {
  *   factor >= 1 is read for every scaling but NONE; original_len > 0 and
  *   0 <= low < high only for PARTS.
  * Positions multiply these words modulo 2^64, that is modulo a full turn, so
- * the angle is exact to 2^-32 turns at any 32-bit position.
+ * at any 32-bit position the phase is the word's to 2^-32 turns; it is then
+ * rounded to fp32 for the sine and cosine, by at most 2^-26 turns.  The words
+ * of fa_rope_turns carry the roundings of the doubles that they are computed
+ * in, about p * 2^-51 radians at position p.
  */
 fa_status fa_rope_turns(long long* turns, int rot_dim, double base, int scaling, double factor, double original_len,
                         double low, double high);
@@ -442,7 +445,8 @@ fa_status fa_rope_turns(long long* turns, int rot_dim, double base, int scaling,
  *               gradient with respect to x of the forward call with the same
  *               arguments, given dL/dy as x (the rotation is orthogonal, and
  *               amplitude enters both alike).
- * Computed in fp32 from exact angles, rounded once when y is bf16.
+ * Computed in fp32 from the angles that fa_rope_turns describes, rounded once
+ * when y is bf16.
  */
 fa_status fa_rope(const void* x, int x_dtype, long long x_stride_b, long long x_stride_h, long long x_stride_n,
                   void* y, int y_dtype, long long y_stride_b, long long y_stride_h, long long y_stride_n,

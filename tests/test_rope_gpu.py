@@ -403,3 +403,24 @@ def test_append_loop_runs_over_the_end_of_its_table():
     with pytest.raises(fa.FAError):
         fa.sync_status()
     assert torch.equal(kp[:, 0, :, 0].cpu(), want) and torch.equal(vp[:, 0, :, 5].cpu(), want)
+
+
+def test_angles_are_within_the_stated_bound():
+    """Random frequency words and positions of either sign: cosine and sine of
+    the phase, whose error is the cut at 2^-32 turns, the rounding to fp32
+    (2^-26 turns) and sincospif's own (2 steps of at most 2^-23)."""
+    rng = np.random.default_rng(3)
+    N, d = 4096, 128
+    words = rng.integers(-2 ** 63, 2 ** 63, d // 2, dtype=np.int64)
+    words[:4] = [2 ** 63 - 1, -2 ** 63, 2 ** 33 + 1, -1]
+    pos = rng.integers(-2 ** 31, 2 ** 31, N)
+    pos[:4] = [2 ** 31 - 1, -2 ** 31, 0, -1]
+    x = torch.zeros(1, 1, N, d)
+    x[..., :d // 2] = 1.0
+    y = fa.rope_forward(x.cuda(), torch.tensor(words).cuda(), torch.tensor(pos, dtype=torch.int32).cuda())
+    fa.sync_status()
+    phase = (words.astype(np.uint64)[None] * pos.astype(np.int64).astype(np.uint64)[:, None])  # modulo 2^64
+    angle = phase.astype(np.int64).astype(np.float64) / 2.0 ** 64 * 2 * np.pi
+    want = np.concatenate([np.cos(angle), np.sin(angle)], -1)
+    bound = 2 * np.pi * (2.0 ** -26 + 2.0 ** -32) + 2 * 2.0 ** -23
+    assert np.abs(y[0, 0].cpu().double().numpy() - want).max() <= bound
