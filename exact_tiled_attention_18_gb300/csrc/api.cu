@@ -5,6 +5,7 @@
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdint>
@@ -459,6 +460,37 @@ cudaMemPool_t workspace_pool() {
 // size one means nothing and is dropped.
 fa::Strides used_strides(long long sb, long long sh, long long sn, int B, int H, int N) {
   return fa::Strides{B > 1 ? sb : 0, H > 1 ? sh : 0, N > 1 ? sn : 0};
+}
+
+// Whether rows of d elements at b * s.b + h * s.h + n * s.n fall on one
+// another.  Strides that nest, each at least what the smaller ones span, never
+// do; others are looked at difference by difference, the dimension with the
+// most rows solved for (at most 2^22 steps for 2^31 rows).
+bool rows_overlap(const fa::Strides& s, int B, int H, int N, int d) {
+  struct Dim {
+    long long stride, rows;
+  } x[3] = {{s.b, B}, {s.h, H}, {s.n, N}};
+  std::sort(x, x + 3, [](const Dim& a, const Dim& b) { return a.stride < b.stride; });
+  long long span = d;
+  bool nested = true;
+  for (const Dim& i : x) {
+    if (i.rows == 1) continue;
+    nested = nested && i.stride >= span;
+    span += i.stride * (i.rows - 1);
+  }
+  if (nested) return false;
+  std::sort(x, x + 3, [](const Dim& a, const Dim& b) { return a.rows < b.rows; });
+  for (long long i = 0; i < x[0].rows; ++i) {
+    for (long long j = 1 - x[1].rows; j < x[1].rows; ++j) {
+      const long long off = i * x[0].stride + j * x[1].stride, most = x[2].rows - 1;
+      const long long near = x[2].stride > 0 ? -off / x[2].stride : 0;
+      for (long long k = near - 1; k <= near + 1; ++k) {
+        const long long in = std::min(std::max(k, -most), most);
+        if ((i || j || in) && std::llabs(off + in * x[2].stride) < d) return true;
+      }
+    }
+  }
+  return false;
 }
 
 fa_status check_strides(const fa::Strides& s, int elem_bytes) {
@@ -922,12 +954,11 @@ fa_status fa_rope(const void* x, int x_dtype, long long x_stride_b, long long x_
   const int xe = x_dtype == FA_DTYPE_BF16 ? 2 : 4, ye = y_dtype == FA_DTYPE_BF16 ? 2 : 4;
   const fa::Strides xs = used_strides(x_stride_b, x_stride_h, x_stride_n, B, H, N);
   const fa::Strides ys = used_strides(y_stride_b, y_stride_h, y_stride_n, B, H, N);
-  // rows of y that fall on one another would race
-  if ((B > 1 && ys.b < d) || (H > 1 && ys.h < d) || (N > 1 && ys.n < d)) return FA_ERR_INVALID_ARG;
   // in place only element for element
   if (x == y && (x_dtype != y_dtype || xs.b != ys.b || xs.h != ys.h || xs.n != ys.n)) return FA_ERR_INVALID_ARG;
-  if (!aligned(x, 16) || !aligned(y, 16)) return FA_ERR_MISALIGNED;
   if ((st = check_strides(xs, xe)) != FA_OK || (st = check_strides(ys, ye)) != FA_OK) return st;
+  if (rows_overlap(ys, B, H, N, d)) return FA_ERR_INVALID_ARG;  // they would race
+  if (!aligned(x, 16) || !aligned(y, 16)) return FA_ERR_MISALIGNED;
   DeviceInfo di;
   if (device_info(di) != FA_OK) return FA_ERR_LAUNCH;
   fa::RopeArgs a;

@@ -430,8 +430,8 @@ fa_status fa_rope_turns(long long* turns, int rot_dim, double base, int scaling,
  *               d contiguous, the other strides in elements (so that the q or
  *               k part of a fused projection [B][N][heads][d] is read where it
  *               lies); bases 16-byte aligned and rows starting on 16-byte
- *               boundaries, strides >= 0, y's at least d (its rows must not
- *               overlap).  y may be x itself, with its type and strides;
+ *               boundaries, strides >= 0, y's such that its rows do not
+ *               overlap.  y may be x itself, with its type and strides;
  *               otherwise they must not overlap.
  *   positions : device ints, position of token n of sequence b at
  *               positions[b * positions_stride_b + n] (0: one row for all

@@ -205,3 +205,51 @@ def test_oracle_cache_round_trip():
     kv = np.repeat(back, 2, axis=1)
     o2, lse2 = oracle.forward_varlen(q, kv, kv, 0.3, True, [3, 2], [13, 20])
     assert np.array_equal(o, o2) and np.array_equal(lse, lse2) and np.all(mass >= np.abs(o) - 1e-12)
+
+
+# ---------------------------------------------------------------- output rows
+
+
+@pytest.mark.parametrize("ys,bad", [
+    # B, H, N, d = 2, 4, 16, 64; what passes is refused behind it, for a misaligned x
+    ((4096, 1024, 64), False), ((4096, 64, 256), False), ((64, 2048, 128), False), ((1 << 40, 1 << 30, 64), False),
+    ((64, 1024, 64), True),           # two sequences a row apart, where the tokens lie
+    ((4096, 512, 64), True),          # heads that begin inside the one before
+    ((1024, 1024, 64), True),         # every sequence on the other's heads
+    ((4096, 960, 64), True),          # the last token on the next head's first
+    ((192, 128, 1024), False),        # sequences in the gaps between the heads
+    ((160, 128, 1024), True),         # the same, half a row too near
+    ((192, 384, 2048), False),        # sequences three rows apart inside the heads' gaps
+    ((8192, 136, 512), False),        # gaps between the heads
+    ((2048, 136, 512), True),         # the second sequence on the first one's fourth token
+    ((1216, 4096, 128), False),       # not nested, and yet apart: 1216 is between two tokens' rows
+    ((1152, 4096, 128), True),        # nine tokens further
+])
+def test_rope_output_rows_must_not_overlap(fa, ys, bad):
+    """The check against the offsets of all rows, and what fa_rope makes of it."""
+    offs = sorted(b * ys[0] + h * ys[1] + n * ys[2] for b in range(2) for h in range(4) for n in range(16))
+    assert bad == any(b - a < 64 for a, b in zip(offs, offs[1:]))
+    st = call(fa.fa_rope, ROPE, dict(ys=ys, x=FAKE + 8))
+    assert st == (1 if bad else 3), fa.fa_status_string(st)
+
+
+def test_rope_output_rows_of_random_strides(fa):
+    rng = np.random.default_rng(5)
+    seen = [0, 0]
+    for _ in range(3000):
+        B, H, N = (int(n) for n in rng.integers(1, 7, 3))
+        ys = tuple(int(x) * 8 for x in rng.integers(0, 60, 3))
+        used = [s if n > 1 else 0 for s, n in zip(ys, (B, H, N))]
+        offs = sorted(b * used[0] + h * used[1] + n * used[2] for b in range(B) for h in range(H) for n in range(N))
+        bad = any(b - a < 64 for a, b in zip(offs, offs[1:]))
+        seen[bad] += 1
+        st = call(fa.fa_rope, ROPE, dict(ys=ys, x=FAKE + 8, B=B, H=H, N=N))
+        assert st == (1 if bad else 3), (B, H, N, ys)
+    assert min(seen) > 300
+
+
+def test_rope_output_rows_of_many_rows_are_checked_quickly(fa):
+    """Strides that do not nest, with as many rows as a call may have."""
+    many = dict(x=FAKE + 8, B=1023, H=1023, N=1023)
+    assert call(fa.fa_rope, ROPE, dict(many, ys=(1 << 41, (1 << 24) + 64, 1 << 24))) == 3
+    assert call(fa.fa_rope, ROPE, dict(many, ys=(1 << 41, (1 << 24) + 56, 1 << 24))) == 1
