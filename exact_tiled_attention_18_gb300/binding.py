@@ -900,8 +900,11 @@ def forward_shared_prefix(q, k_pages, v_pages, prefix_table, prefix_len: int, bl
 
 
 def sync_status(device=None) -> None:
-    """Synchronise the current stream and raise if a kernel reported a failure."""
-    status = fa_sync_status(_stream_handle(device))
+    """Synchronise the current stream (of ``device``, by default the current
+    one) and raise if a kernel reported a failure there."""
+    import torch
+    with torch.cuda.device(device):  # the status word is the current device's
+        status = fa_sync_status(_stream_handle(device))
     if status != FA_OK:
         detail = fa_last_failure() if status in (FA_ERR_TIMEOUT, FA_ERR_BAD_PAGE) else None
         raise FAError("fa_sync_status", status, fa_status_string(status) + (f" {detail}" if detail else ""))

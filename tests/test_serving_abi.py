@@ -253,3 +253,42 @@ def test_rope_output_rows_of_many_rows_are_checked_quickly(fa):
     many = dict(x=FAKE + 8, B=1023, H=1023, N=1023)
     assert call(fa.fa_rope, ROPE, dict(many, ys=(1 << 41, (1 << 24) + 64, 1 << 24))) == 3
     assert call(fa.fa_rope, ROPE, dict(many, ys=(1 << 41, (1 << 24) + 56, 1 << 24))) == 1
+
+
+# --------------------------------------------------------------------- status
+
+
+def test_sync_status_reads_the_device_it_is_given(fa, monkeypatch):
+    """The status word is the current device's: sync_status makes the given
+    device current around the call (as the calls that may set it do)."""
+    binding = fa.binding
+    current = [0]
+
+    class Device:
+        def __init__(self, device):
+            self.device = device
+
+        def __enter__(self):
+            self.before = current[0]
+            if self.device is not None:
+                current[0] = self.device
+
+        def __exit__(self, *_):
+            current[0] = self.before
+
+    class Stream:
+        def __init__(self, device):
+            self.cuda_stream = 100 + (current[0] if device is None else device)
+
+    seen = []
+
+    def status(stream):
+        seen.append((current[0], stream))
+        return 0
+
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    monkeypatch.setattr(torch.cuda, "current_stream", Stream)
+    monkeypatch.setattr(binding, "fa_sync_status", status)
+    fa.sync_status()
+    fa.sync_status(1)
+    assert seen == [(0, 100), (1, 101)] and current == [0]
