@@ -36,12 +36,14 @@
 // and O is divided by the sum of the rounded weights, so that their rounding
 // does not scale a row; the queries then stay in shared memory instead of
 // registers (8 sequences x 8 heads x 8192 keys: 24 rows 86 us with fragments
-// and pairs, 54 us so; 32 rows 87 and 61).
+// and pairs, 55 us so; 32 rows 87 and 62).
 //
 // Measured (whole calls; HBM read rate of keys and values): 8 sequences x 32
-// heads x 32768 keys, one row a head, 604 to 616 us = 7.0 to 7.1 TB/s; 32 sequences of 100 to
-// 16384 keys, 32 heads on 4, 42 us = 5.3 TB/s, of which 6 us pass before the
-// first tiles are there; one sequence of 1000 keys 6.9 us in a graph.  A pass
+// heads x 32768 keys, one row a head, 604 to 619 us = 6.9 to 7.1 TB/s; 32
+// sequences of 100 to 16384 keys, 32 heads on 4, 42 us = 5.3 TB/s, of which 6 us
+// pass before the first tiles are there; 8 sequences x 8 heads x 8192 keys 48 us =
+// 5.6 TB/s with 1 to 8 rows a head, 50 with 9 to 16, 55 with 24, 62 with 32; one
+// sequence of 1000 keys 6.9 to 7.2 us in a graph.  A pass
 // over a quarter of the first keeps DRAM 85% of its peak busy, the tensor pipe
 // 13%.
 #include <cuda_runtime.h>

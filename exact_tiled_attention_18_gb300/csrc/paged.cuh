@@ -9,9 +9,10 @@
 namespace fa {
 
 // Rows a key head that the step kernel takes; more are the tile kernel's, which
-// takes 128 whether they are there or not.  (8 sequences x 8 heads x 8192 keys: 24
-// rows 54 us here, 64 there; 32 rows 61 and 63; 38 sequences of 512 keys, 32
-// rows, 21 and 37.  64 rows are 65 us there.)
+// takes 128 whether they are there or not.  (8 heads; here and there, us.  8
+// sequences x 8192 keys: 24 rows 55 and 57, 32 rows 62 and 57; 64 x 1000 keys: 57
+// and 77, 65 and 77; 38 x 512 keys: 18 and 29, 21 and 30.  64 rows are 58, 79
+// and 29 there.)
 constexpr int kStepRows = 32;
 constexpr int kLineSequences = 256;    // sequences a launch of the step kernel: the line's table is in shared memory
 constexpr int kLineWords = 528;        // 4-byte words of a line in the workspace, a multiple of 4
@@ -63,8 +64,9 @@ struct PartRef {
   int slot_rows;
   // 1: a unit of the tile kernel has at most 128 rows, so that its tile B would
   // be empty: tile B takes the same rows and every other key tile, and the two
-  // are put together in the CTA.  (8 sequences x 8 heads x 64 rows x 8192 keys:
-  // 65 us, 71 with tile A alone.)
+  // are put together in the CTA.  (64 rows of 8 heads: 8 sequences x 8192 keys
+  // 58 us, 63 with tile A alone, at d = 64 42 and 56; 64 sequences x 1000 keys 79
+  // and 98.)
   int dual;
   int units;
   int heads, pairs, group;  // the tile kernel: (sequence, head)s, row pairs of each, heads dealt out together
@@ -193,9 +195,11 @@ __device__ __forceinline__ uint32_t sw128(int r, int c) {
 // that length need: as quick, with fewer partial results, and units more often
 // cut into equal parts.  (One sequence of 30000 keys, one key head, 469 tiles
 // for 456 CTAs: 14.6 us without, 10.4 with it; 4 chunks of 100 tokens over 1500
-// keys, 32 heads on 8: 33.4 and 28.1 us.  The shared prefix's tiles do without:
-// drafted tokens behind 8208 keys 33.5 us, 34.2 with it, for CTAs that end
-// early make room for the step kernel's.)
+// keys, 32 heads on 8: 33.4 and 28.1 us.  The shared prefix's tiles do
+// without, for CTAs that end early make room for the step kernel's: 24 sequences
+// of 4 drafted tokens behind 8208 keys 30.0 us, 30.5 with it; single tokens of 16
+// behind 4096 21.3 and 21.7, of 64 behind 8192 45 and 47, of 128 behind 16384 107
+// either way.)
 struct Ranges {
   int base, more, total;
 };

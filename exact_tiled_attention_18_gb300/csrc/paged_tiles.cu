@@ -33,8 +33,8 @@
 //
 // Measured (whole calls): a square prompt of 16 heads x 16384 tokens 1574
 // TFLOP/s, 32 heads under the causal rule 1409 to 1442; two chunks of 1000
-// tokens, 32 heads on 8, over 9001 and 16384 keys 320 us = 1250 TFLOP/s; 2048
-// rows of 8 heads behind 32768 shared keys 190 us in this kernel.  The tensor
+// tokens, 32 heads on 8, over 9001 and 16384 keys 323 to 329 us = 1220 to 1240
+// TFLOP/s; 2048 rows of 8 heads behind 32768 shared keys 190 us in this kernel.  The tensor
 // pipe is 54 to 58% busy in the last two, DRAM 9 to 12%.  The smallest call, 64
 // rows of 8 heads over 512 keys, is 12.8 us: 1.7 until the line is there, 1.8 until a
 // piece is worked out, 1.5 until its first scores, 2 for the softmax and the second

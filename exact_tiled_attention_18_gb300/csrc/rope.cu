@@ -22,11 +22,12 @@
 // their 8 sines and cosines once, and walks over heads with them, several
 // heads' loads in flight at a time.
 //
-// Measured: 4 x 16 heads x 8192 tokens, d = 128, bf16, 45.2 us = 5.9 TB/s; 32
-// heads x 16384 tokens from fp32 to bf16, interleaved, 61.8 us = 6.5 TB/s; the
-// append of four prompts of 2048 to 8192 tokens, 16 + 16 + 16 heads, 75.9 us =
-// 6.0 TB/s; a step of 8 sequences 2.1 us (rotation) and 2.5 us (append) a call
-// in a graph.  128 threads a block: 45.2, 61.7 and 79.8 us; half the heads in
+// Measured: 4 x 16 heads x 8192 tokens, d = 128, bf16, out of a fused projection
+// 45.2 us = 5.9 TB/s, contiguous from bf16 to fp32 63 us = 6.4 TB/s, fp32 to
+// fp32 81 us = 6.6 TB/s; 32 heads x 16384 tokens from fp32 to bf16, interleaved,
+// 61.8 us = 6.5 TB/s; the append of four prompts of 2048 to 8192 tokens, 16 + 16
+// + 16 heads, 75.9 us = 6.0 TB/s; a step of 8 sequences 2.1 us (rotation) and 2.5
+// us (append) a call in a graph.  128 threads a block: 45.2, 61.7 and 79.8 us; half the heads in
 // flight 47.3, 63.2, 76.0; twice as many 45.3, 61.9, 75.9; an append of three
 // blocks an SM 86.5.
 #include <cuda_runtime.h>
@@ -291,10 +292,14 @@ __global__ void __launch_bounds__(kRopeThreads) append_kernel(const AppendArgs a
 
 // Heads per thread: as many as leave about a thousand threads for every SM,
 // so that a large call computes each angle for many heads and a call of few
-// tokens spreads its heads over the GPU; at most `most`.  (A rotation of 16
-// heads x 32768 tokens, d = 128, bf16: 47.2 us with 16 heads a thread, 45.7
-// with 8, 46.6 with 4.  The append looks its lengths and page up once a
-// thread: 76 us with 48 heads a thread, 82 with 8.)
+// tokens spreads its heads over the GPU; at most `most`: eight for the rotation,
+// all for the append, which looks its lengths and page up once a thread.  (d =
+// 128, bf16, at most 4 / 8 / 16 heads a thread: rotation of 16 heads x 32768
+// tokens 42.8 / 43.5 / 44.7 us in a graph and 46.6 / 45.7 / 47.2 in eager calls, 8 x
+// 64 heads x 2048 82.0 / 82.6 / 84.0, smaller ones alike.  At most 8 / 16 / all: four
+// prompts of 2048 to 8192 tokens, 48 heads, 82 / - / 76; 4 x 48 heads x 8192
+// 132.9 / 127.1 / 128.5, 2 x 80 heads x 8192 111.1 / 107.3 / 108.3, 24 heads x 16384
+// 37.9 / 39.4 / 39.3, 48 heads x 4096 18.1 / 18.4 / 18.4.)
 int heads_per_thread(long long tokens, int lanes, int heads, int sms, int most) {
   long long n = tokens * lanes * heads / (static_cast<long long>(sms) * 1024);
   if (n < 1) n = 1;

@@ -542,7 +542,10 @@ size_t fa_fwd_paged_workspace_bytes(int B, int Hq, int Hkv, int Nq, int d);
  * sequence's first prefix_len / page_size block-table entries are
  * prefix_table's, but the prefix's keys and values are read once for the rows
  * of all sequences together, not once a sequence; the rest of each sequence
- * is attended on its own and the two are merged by their log-sum-exp.
+ * is attended on its own and the two are merged by their log-sum-exp.  It pays
+ * for many sequences of few rows a key head (Hq / Hkv * Nq, up to about 64)
+ * behind a long prefix; with chunks of a prompt, few sequences or a prefix of
+ * about a thousand keys fa_fwd_paged is as fast or faster.
  *   prefix_table : device ints, the prefix's prefix_len / page_size pages;
  *                  block-table entries below prefix_len / page_size are not
  *                  read by this call (positions stay those of the whole
@@ -550,6 +553,9 @@ size_t fa_fwd_paged_workspace_bytes(int B, int Hq, int Hkv, int Nq, int d);
  *   prefix_len   : a positive multiple of page_size, at most
  *                  max_pages * page_size.  Sequences shorter than it are
  *                  allowed and see their own length's share of the prefix.
+ *   workspace    : with more than 32 rows a key head it holds partial results
+ *                  of 256 rows (130 KB at d = 128) for every key head of every
+ *                  sequence, as many as its rows fill.
  * The prefix's probabilities are bf16, as in fa_fwd, whatever the number of
  * rows.  Other arguments, results and errors as fa_fwd_paged.
  */
