@@ -1,5 +1,5 @@
 """Scores at the edges of what the paged attention takes: NaN in keys and
-queries that are seen, in every division of the work, and scores of -inf."""
+queries that are seen, in every division of the work, and infinite scores."""
 
 import numpy as np
 import pytest
@@ -85,3 +85,35 @@ def test_keys_of_score_minus_infinity_have_no_weight(way):
     kw = dict(prefix=prefix, prefix_table=prefix_table) if prefix else {}
     o, lse = run(q, kp, vp, table, lens, **kw)
     check(o[some], lse[some], ref, q[some], clean, scale_for(d), bits, way[0])
+
+
+@pytest.mark.parametrize("way", WAYS, ids=lambda w: w[0].replace(" ", "-"))
+def test_an_infinite_key_is_nan_or_nothing(way):
+    """One key with +inf in a component that is 1 in some queries and -1 in the
+    others: the first have a score of +inf and are NaN, for the others the key
+    has no weight."""
+    _, B, Hq, Hkv, Nq, d, page, prefix, lens, bits = way
+    q, kp, vp, table = make_batch(B, Hq, Hkv, Nq, d, page, lens, seed=Nq + d + B)
+    n = prefix // page
+    prefix_table = table[int(np.argmax(lens)), :n].clone()
+    table[:, :n] = prefix_table
+    g = torch.Generator().manual_seed(7)
+    up = torch.rand(B, Hq, Nq, generator=g) < 0.4
+    q[..., 7] = torch.where(up, 1.0, -1.0).to(q.dtype)
+    some = sorted({0, B // 2, B - 1})
+    G, sick, head = Hq // Hkv, some[-1], Hkv - 1
+    at = lens[sick] // 3
+    row = table[sick, at // page], head, at % page, 7
+    far, inf = kp.clone(), kp.clone()
+    far[row], inf[row] = 2e4, float("inf")  # 2e4: a weight of exp(-1700) and less, 0 in 64 bits
+    ref = reference(q[some], far, vp, table[some], [lens[b] for b in some], None, True)
+    hit = torch.zeros(len(some), Hq, Nq, dtype=torch.bool)
+    for i, b in enumerate(some):
+        if b == sick or at < prefix:
+            hit[i, head * G:(head + 1) * G, max(0, at - lens[b] + Nq):] = True
+    hit &= up[some]
+    kw = dict(prefix=prefix, prefix_table=prefix_table) if prefix else {}
+    o, lse = (t.cpu()[some] for t in run(q, inf, vp, table, lens, **kw))
+    assert torch.equal(torch.isnan(lse), hit) and torch.equal(torch.isnan(o), hit[..., None].expand_as(o))
+    o[hit], lse[hit] = torch.tensor(ref[0]).float()[hit], torch.tensor(ref[1]).float()[hit]
+    check(o, lse, ref, q[some], kp, scale_for(d), bits, way[0])
