@@ -24,6 +24,7 @@ FA_ERR_BAD_PAGE = 7
 FA_DECODE_MAX_Q = 8
 FA_DTYPE_F32 = 0
 FA_DTYPE_BF16 = 1
+FA_SCALE_TOKENS = 16
 FA_ROPE_HALF = 0
 FA_ROPE_INTERLEAVED = 1
 FA_ROPE_SCALE_NONE = 0
@@ -99,6 +100,15 @@ def lib() -> ctypes.CDLL:
         L.fa_kv_append.argtypes = [vp, ll, ll, ll, vp, ll, ll, ll, vp, ll, ll, ll, vp, vp, vp, i, i, vp, ll, i, vp, vp,
                                    vp, ll, vp, i, i, f, i, i, i, i, i, vp]
         L.fa_kv_append.restype = st
+        L.fa_kv_append_fp8.argtypes = [vp, ll, ll, ll, vp, ll, ll, ll, vp, ll, ll, ll, vp, vp, vp, vp, vp, i, i, vp, ll,
+                                       i, vp, vp, vp, ll, vp, i, i, f, i, i, i, i, i, vp]
+        L.fa_kv_append_fp8.restype = st
+        L.fa_fwd_paged_fp8.argtypes = [vp, vp, vp, vp, vp, i, i, vp, ll, i, vp, i, vp, vp, vp, vp, i, i, i, i, i, f, i,
+                                       vp]
+        L.fa_fwd_paged_fp8.restype = st
+        L.fa_fwd_shared_prefix_fp8.argtypes = [vp, vp, vp, vp, vp, i, i, vp, i, vp, ll, i, vp, i, vp, vp, vp, vp, i, i,
+                                               i, i, i, f, i, vp]
+        L.fa_fwd_shared_prefix_fp8.restype = st
         L.fa_fwd_paged.argtypes = [vp, vp, vp, i, i, vp, ll, i, vp, i, vp, vp, vp, vp, i, i, i, i, i, f, i, vp]
         L.fa_fwd_paged.restype = st
         L.fa_fwd_paged_workspace_bytes.argtypes = [i, i, i, i, i]
@@ -255,6 +265,18 @@ def fa_kv_append(k: int, k_strides: tuple, v: int, v_strides: tuple, q: int, q_s
                               positions_stride_b, turns, rot_dim, layout, amplitude, B, Hq, Hkv, N, d, stream)
 
 
+def fa_kv_append_fp8(k: int, k_strides: tuple, v: int, v_strides: tuple, q: int, q_strides: tuple, q_out: int,
+                     k_pages: int, v_pages: int, k_scales: int, v_scales: int, num_pages: int, page_size: int,
+                     block_table: int, table_stride: int, max_pages: int, seqlens_q: int, seqlens_k: int,
+                     positions: int, positions_stride_b: int, turns: int, rot_dim: int, layout: int, amplitude: float,
+                     B: int, Hq: int, Hkv: int, N: int, d: int, stream: int) -> int:
+    """Raw C call; strides are (b, h, n) triples in elements."""
+    return lib().fa_kv_append_fp8(k, *k_strides, v, *v_strides, q, *q_strides, q_out, k_pages, v_pages, k_scales,
+                                  v_scales, num_pages, page_size, block_table, table_stride, max_pages, seqlens_q,
+                                  seqlens_k, positions, positions_stride_b, turns, rot_dim, layout, amplitude, B, Hq,
+                                  Hkv, N, d, stream)
+
+
 def fa_fwd_paged(q: int, k_pages: int, v_pages: int, num_pages: int, page_size: int, block_table: int,
                  table_stride: int, max_pages: int, o: int, o_dtype: int, lse: int, seqlens_q: int, seqlens_k: int,
                  workspace: int, B: int, Hq: int, Hkv: int, Nq: int, d: int, scale: float, causal: int,
@@ -278,6 +300,25 @@ def fa_fwd_shared_prefix(q: int, k_pages: int, v_pages: int, num_pages: int, pag
 
 def fa_fwd_shared_prefix_workspace_bytes(B: int, Hq: int, Hkv: int, Nq: int, d: int) -> int:
     return lib().fa_fwd_shared_prefix_workspace_bytes(B, Hq, Hkv, Nq, d)
+
+
+def fa_fwd_paged_fp8(q: int, k_pages: int, v_pages: int, k_scales: int, v_scales: int, num_pages: int, page_size: int,
+                     block_table: int, table_stride: int, max_pages: int, o: int, o_dtype: int, lse: int,
+                     seqlens_q: int, seqlens_k: int, workspace: int, B: int, Hq: int, Hkv: int, Nq: int, d: int,
+                     scale: float, causal: int, stream: int) -> int:
+    return lib().fa_fwd_paged_fp8(q, k_pages, v_pages, k_scales, v_scales, num_pages, page_size, block_table,
+                                  table_stride, max_pages, o, o_dtype, lse, seqlens_q, seqlens_k, workspace, B, Hq,
+                                  Hkv, Nq, d, scale, causal, stream)
+
+
+def fa_fwd_shared_prefix_fp8(q: int, k_pages: int, v_pages: int, k_scales: int, v_scales: int, num_pages: int,
+                             page_size: int, prefix_table: int, prefix_len: int, block_table: int, table_stride: int,
+                             max_pages: int, o: int, o_dtype: int, lse: int, seqlens_q: int, seqlens_k: int,
+                             workspace: int, B: int, Hq: int, Hkv: int, Nq: int, d: int, scale: float, causal: int,
+                             stream: int) -> int:
+    return lib().fa_fwd_shared_prefix_fp8(q, k_pages, v_pages, k_scales, v_scales, num_pages, page_size, prefix_table,
+                                          prefix_len, block_table, table_stride, max_pages, o, o_dtype, lse, seqlens_q,
+                                          seqlens_k, workspace, B, Hq, Hkv, Nq, d, scale, causal, stream)
 
 
 def fa_sync_status(stream: int) -> int:
@@ -734,19 +775,32 @@ def rope_backward(dy, turns, positions=None, layout: str = "half", amplitude: fl
     return _rope(dy, turns, positions, layout, amplitude, 1, out, out_dtype)
 
 
-def _page_args(k_pages, v_pages, block_table, B, d, index):
-    """(k_pages, v_pages, num_pages, page_size) and (block_table, its stride,
-    max_pages) of the C calls, and Hkv."""
+def _page_args(k_pages, v_pages, scales, block_table, B, d, index):
+    """(k_pages, v_pages, num_pages, page_size), for a cache in E4M3 with the
+    scales behind the pages, and (block_table, its stride, max_pages) of the
+    C calls, and Hkv."""
     import torch
     shape = k_pages.shape
-    if (len(shape) != 4 or shape[3] != d or v_pages.shape != shape or k_pages.dtype != torch.bfloat16
-            or v_pages.dtype != torch.bfloat16 or not k_pages.is_contiguous() or not v_pages.is_contiguous()
+    dtype = torch.bfloat16 if scales is None else torch.float8_e4m3fn
+    if (len(shape) != 4 or shape[3] != d or v_pages.shape != shape or k_pages.dtype != dtype
+            or v_pages.dtype != dtype or not k_pages.is_contiguous() or not v_pages.is_contiguous()
             or k_pages.get_device() != index or v_pages.get_device() != index):
-        raise ValueError("k_pages and v_pages must be contiguous bf16 [pages, Hkv, page_size, d] on the inputs' device")
+        raise ValueError(f"k_pages and v_pages must be contiguous {dtype} [pages, Hkv, page_size, d] on the inputs' "
+                         "device")
     if (block_table.dim() != 2 or block_table.dtype != torch.int32 or block_table.shape[0] != B
             or block_table.get_device() != index or (block_table.shape[1] != 1 and block_table.stride(1) != 1)):
         raise ValueError("block_table must be int32 [B, max_pages] on the inputs' device with contiguous rows")
-    return ((k_pages.data_ptr(), v_pages.data_ptr(), shape[0], shape[2]),
+    if scales is None:
+        pages = (k_pages.data_ptr(), v_pages.data_ptr(), shape[0], shape[2])
+    else:
+        cells = (shape[0], shape[1], shape[2] // FA_SCALE_TOKENS)
+        for t in scales:
+            if (t.shape != cells or t.dtype != torch.float32 or not t.is_contiguous() or t.get_device() != index):
+                raise ValueError("k_scales and v_scales must be contiguous fp32 [pages, Hkv, page_size / 16] on the "
+                                 "inputs' device")
+        pages = (k_pages.data_ptr(), v_pages.data_ptr(), scales[0].data_ptr(), scales[1].data_ptr(), shape[0],
+                 shape[2])
+    return (pages,
             (block_table.data_ptr(), block_table.stride(0), block_table.shape[1]), shape[1])
 
 
@@ -769,6 +823,22 @@ def kv_append(k, v, k_pages, v_pages, block_table, seqlens_k, seqlens_q=None, tu
     with the new tokens; ``seqlens_q``: int32 [B], its new tokens (default N).
     Tokens past the end of their row of ``block_table`` are not stored, which
     sync_status reports.  Returns q_out, or None without q."""
+    return _append(k, v, k_pages, v_pages, None, block_table, seqlens_k, seqlens_q, turns, layout, amplitude,
+                   positions, q, q_out)
+
+
+def kv_append_fp8(k, v, k_pages, v_pages, k_scales, v_scales, block_table, seqlens_k, seqlens_q=None, turns=None,
+                  layout: str = "half", amplitude: float = 1.0, positions=None, q=None, q_out=None):
+    """kv_append into a cache in E4M3 through fa_kv_append_fp8: pages
+    float8_e4m3fn [pages, Hkv, page_size, d], scales fp32 [pages, Hkv,
+    page_size / 16], a power of two for every 16 tokens of a head (raised, and
+    the older tokens' numbers rounded again, where a new token asks for it)."""
+    return _append(k, v, k_pages, v_pages, (k_scales, v_scales), block_table, seqlens_k, seqlens_q, turns, layout,
+                   amplitude, positions, q, q_out)
+
+
+def _append(k, v, k_pages, v_pages, scales, block_table, seqlens_k, seqlens_q, turns, layout, amplitude, positions, q,
+            q_out):
     import torch
     if k.dim() != 4 or not k.is_cuda:
         raise ValueError("k must be a bf16 CUDA tensor [B, Hkv, N, d] with contiguous d")
@@ -780,7 +850,7 @@ def kv_append(k, v, k_pages, v_pages, block_table, seqlens_k, seqlens_q=None, tu
     vb, vh, vn, v1 = v.stride()
     if (k1 != 1 or v1 != 1 or k.dtype != torch.bfloat16 or v.dtype != torch.bfloat16 or v.get_device() != index):
         raise ValueError("k and v must be bf16 CUDA tensors [B, Hkv, N, d] of one device with contiguous d")
-    pages, table, page_heads = _page_args(k_pages, v_pages, block_table, B, d, index)
+    pages, table, page_heads = _page_args(k_pages, v_pages, scales, block_table, B, d, index)
     if page_heads != Hkv:
         raise ValueError("the pages must have k's heads")
     if seqlens_k is None:
@@ -808,22 +878,23 @@ def kv_append(k, v, k_pages, v_pages, block_table, seqlens_k, seqlens_q=None, tu
               or q_out.get_device() != index):
             raise ValueError("q_out must be contiguous bf16 of q's shape and device")
         qp, op = q.data_ptr(), q_out.data_ptr()
-    st = _call_on(index, (_lib or lib()).fa_kv_append, k.data_ptr(), kb, kh, kn, v.data_ptr(), vb, vh, vn, qp, qb, qh,
+    L = _lib or lib()
+    st = _call_on(index, L.fa_kv_append if scales is None else L.fa_kv_append_fp8, k.data_ptr(), kb, kh, kn, v.data_ptr(), vb, vh, vn, qp, qb, qh,
                   qn, op, *pages, *table, _lens(seqlens_q, B, index), _lens(seqlens_k, B, index), *rope, amplitude, B,
                   Hq, Hkv, N, d)
     if st:
-        _check("fa_kv_append", st)
+        _check("fa_kv_append" if scales is None else "fa_kv_append_fp8", st)
     return q_out
 
 
-def _paged(shared, q, k_pages, v_pages, prefix, block_table, seqlens_k, seqlens_q, causal, scale, o_dtype, workspace,
-           out):
+def _paged(shared, q, k_pages, v_pages, scales, prefix, block_table, seqlens_k, seqlens_q, causal, scale, o_dtype,
+           workspace, out):
     import torch
     if q.dtype != torch.bfloat16 or not q.is_cuda or q.dim() != 4 or not q.is_contiguous():
         raise ValueError("q must be a contiguous bf16 CUDA tensor [B, Hq, Nq, d]")
     B, Hq, Nq, d = q.shape
     index = q.get_device()
-    pages, table, Hkv = _page_args(k_pages, v_pages, block_table, B, d, index)
+    pages, table, Hkv = _page_args(k_pages, v_pages, scales, block_table, B, d, index)
     if out is None:
         if o_dtype is None:
             o_dtype = torch.float32
@@ -856,12 +927,16 @@ def _paged(shared, q, k_pages, v_pages, prefix, block_table, seqlens_k, seqlens_
                 or workspace.numel() < _paged_workspace(L, shared, B, Hq, Hkv, Nq, d)):
             raise ValueError("workspace must be fp32 on q's device, of the call's workspace_bytes(...) bytes")
         ws = workspace.data_ptr()
-    st = _call_on(index, L.fa_fwd_shared_prefix if shared else L.fa_fwd_paged, q.data_ptr(), *pages, *prefix, *table,
+    if scales is None:
+        call = L.fa_fwd_shared_prefix if shared else L.fa_fwd_paged
+    else:
+        call = L.fa_fwd_shared_prefix_fp8 if shared else L.fa_fwd_paged_fp8
+    st = _call_on(index, call, q.data_ptr(), *pages, *prefix, *table,
                   o.data_ptr(), o_dtype == torch.bfloat16, lse.data_ptr(), _lens(seqlens_q, B, index),
                   _lens(seqlens_k, B, index), ws, B, Hq, Hkv, Nq, d, d ** -0.5 if scale is None else scale,
                   bool(causal))
     if st:
-        _check("fa_fwd_shared_prefix" if shared else "fa_fwd_paged", st)
+        _check(("fa_fwd_shared_prefix" if shared else "fa_fwd_paged") + ("" if scales is None else "_fp8"), st)
     return o, lse
 
 
@@ -878,8 +953,17 @@ def forward_paged(q, k_pages, v_pages, block_table, seqlens_k=None, seqlens_q=No
     Hkv.  ``seqlens_k``, ``seqlens_q``: int32 [B] as kv_append.  ``workspace``:
     an fp32 tensor of fa_fwd_paged_workspace_bytes(...) bytes; by default a
     stream-ordered one of the library's."""
-    return _paged(False, q, k_pages, v_pages, (), block_table, seqlens_k, seqlens_q, causal, scale, o_dtype,
+    return _paged(False, q, k_pages, v_pages, None, (), block_table, seqlens_k, seqlens_q, causal, scale, o_dtype,
                   workspace, out)
+
+
+def forward_paged_fp8(q, k_pages, v_pages, k_scales, v_scales, block_table, seqlens_k=None, seqlens_q=None,
+                      causal: bool = True, scale: float | None = None, o_dtype=None, workspace=None, out=None):
+    """forward_paged over a cache in E4M3 (kv_append_fp8) through
+    fa_fwd_paged_fp8: pages float8_e4m3fn, scales fp32 [pages, Hkv,
+    page_size / 16]."""
+    return _paged(False, q, k_pages, v_pages, (k_scales, v_scales), (), block_table, seqlens_k, seqlens_q, causal,
+                  scale, o_dtype, workspace, out)
 
 
 def forward_shared_prefix(q, k_pages, v_pages, prefix_table, prefix_len: int, block_table, seqlens_k=None,
@@ -889,14 +973,28 @@ def forward_shared_prefix(q, k_pages, v_pages, prefix_table, prefix_len: int, bl
     ``prefix_len`` keys (a multiple of the page size), in the pages that
     ``prefix_table`` int32 [prefix_len / page_size] names: that part is
     computed once for all, through fa_fwd_shared_prefix."""
+    return _paged(True, q, k_pages, v_pages, None, _prefix_args(prefix_table, prefix_len, q, k_pages), block_table,
+                  seqlens_k, seqlens_q, causal, scale, o_dtype, workspace, out)
+
+
+def forward_shared_prefix_fp8(q, k_pages, v_pages, k_scales, v_scales, prefix_table, prefix_len: int, block_table,
+                              seqlens_k=None, seqlens_q=None, causal: bool = True, scale: float | None = None,
+                              o_dtype=None, workspace=None, out=None):
+    """forward_shared_prefix over a cache in E4M3 (kv_append_fp8) through
+    fa_fwd_shared_prefix_fp8."""
+    return _paged(True, q, k_pages, v_pages, (k_scales, v_scales),
+                  _prefix_args(prefix_table, prefix_len, q, k_pages), block_table, seqlens_k, seqlens_q, causal, scale,
+                  o_dtype, workspace, out)
+
+
+def _prefix_args(prefix_table, prefix_len, q, k_pages):
     import torch
     if (prefix_table.dtype != torch.int32 or prefix_table.dim() != 1 or not prefix_table.is_contiguous()
             or prefix_table.get_device() != q.get_device() or prefix_len < 1 or k_pages.dim() != 4
             or prefix_table.numel() * k_pages.shape[2] < prefix_len):
         raise ValueError("prefix_table must be contiguous int32 on q's device with an entry for every page of the "
                          "prefix")
-    return _paged(True, q, k_pages, v_pages, (prefix_table.data_ptr(), int(prefix_len)), block_table,
-                  seqlens_k, seqlens_q, causal, scale, o_dtype, workspace, out)
+    return prefix_table.data_ptr(), int(prefix_len)
 
 
 def sync_status(device=None) -> None:

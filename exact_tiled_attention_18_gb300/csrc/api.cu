@@ -118,7 +118,8 @@ bool remember_map(const MapKey& key, const CUtensorMap& m) {
 
 // 3-D map over [heads][rows][inner] elements of `elem_bytes` (2: bf16, 1:
 // E4M3 bytes), box = box_inner x box_rows x 1 with the 128-byte swizzle (the
-// layout the MMA descriptors expect).  Rows past `rows` read as zeros.
+// layout the MMA descriptors expect), or the 64-byte one where the box's rows
+// have 64 bytes.  Rows past `rows` read as zeros.
 // Blocked (bf16): a 4-D map over [heads][inner / 64][rows][64] of the same
 // memory, box = 64 x box_rows x (inner / 64) x 1, so that one load brings the
 // box's rows block by block (blocked = 1), or a 5-D map over
@@ -177,9 +178,9 @@ bool encode_map(CUtensorMap* m, const MapKey& key) {
       return false;
     return remember_map(key, *m);
   }
+  const auto swizzle = key.elem_bytes * key.box_inner == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
   CUresult r = fn(m, key.elem_bytes == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 3,
-                  const_cast<void*>(key.base), dims, strides, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                  const_cast<void*>(key.base), dims, strides, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return false;
   return remember_map(key, *m);
 }
@@ -521,11 +522,17 @@ fa_status check_pages(const void* k_pages, const void* v_pages, int num_pages, i
   return FA_OK;
 }
 
-fa_status paged_common(const void* q, const void* k_pages, const void* v_pages, int num_pages, int page_size,
-                       const int* prefix_table, int prefix_len, const int* block_table, long long table_stride,
-                       int max_pages, void* o, int o_dtype, float* lse, const int* seqlens_q, const int* seqlens_k,
-                       float* workspace, int B, int Hq, int Hkv, int Nq, int d, float scale, int causal,
-                       fa_stream_t stream) {
+fa_status check_scales(const float* k_scales, const float* v_scales) {
+  if (!k_scales || !v_scales) return FA_ERR_INVALID_ARG;
+  return aligned(k_scales, 4) && aligned(v_scales, 4) ? FA_OK : FA_ERR_MISALIGNED;
+}
+
+// k_scales null: a cache in bf16.
+fa_status paged_common(const void* q, const void* k_pages, const void* v_pages, const float* k_scales,
+                       const float* v_scales, int num_pages, int page_size, const int* prefix_table, int prefix_len,
+                       const int* block_table, long long table_stride, int max_pages, void* o, int o_dtype,
+                       float* lse, const int* seqlens_q, const int* seqlens_k, float* workspace, int B, int Hq,
+                       int Hkv, int Nq, int d, float scale, int causal, fa_stream_t stream) {
   if (!q || !o || !lse) return FA_ERR_INVALID_ARG;
   if (o_dtype != FA_DTYPE_F32 && o_dtype != FA_DTYPE_BF16) return FA_ERR_INVALID_ARG;
   fa_status st = check_sizes(B, Hq, Nq, d, causal);
@@ -547,6 +554,8 @@ fa_status paged_common(const void* q, const void* k_pages, const void* v_pages, 
   fa::PagedArgs a;
   std::memset(&a, 0, sizeof(a));
   a.q = static_cast<const uint16_t*>(q);
+  a.k_scales = k_scales;
+  a.v_scales = v_scales;
   a.table = fa::PageTable{block_table, table_stride, max_pages, page_size, num_pages};
   a.prefix_table = prefix_table;
   a.prefix_len = prefix_len;
@@ -567,11 +576,15 @@ fa_status paged_common(const void* q, const void* k_pages, const void* v_pages, 
   a.status = di.status;
   a.wait_limit_ns = wait_limit_ns();
   a.stall_unit = test_stall_unit();
+  const bool fp8 = k_scales != nullptr;
   a.box_rows = page_size % 64 == 0 ? 64 : (page_size % 32 == 0 ? 32 : 16);
+  if (fp8 && page_size % 128 == 0) a.box_rows = 128;  // a tile's rows
   const int page_heads = num_pages * Hkv;
   const bool steps = fa::paged_uses_steps(Hq / Hkv, Nq);
+  if (fp8 && (!steps || prefix_len > 0)) return FA_ERR_INVALID_ARG;
   auto page_map = [&](CUtensorMap* m, const void* pages, int box_rows, int blocked) {
-    return encode_map(m, MapKey{pages, 2, page_heads, page_size, d, 64, box_rows, blocked});
+    return encode_map(m, fp8 ? MapKey{pages, 1, page_heads, page_size, d, d, box_rows}
+                             : MapKey{pages, 2, page_heads, page_size, d, 64, box_rows, blocked});
   };
   if ((!steps || prefix_len > 0) &&
       (!page_map(&a.tm_k, k_pages, a.box_rows, 2) || !page_map(&a.tm_v, v_pages, a.box_rows, 2)))
@@ -979,10 +992,11 @@ fa_status fa_rope(const void* x, int x_dtype, long long x_stride_b, long long x_
   return fa::launch_rope(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
 }
 
-fa_status fa_kv_append(const void* k, long long k_stride_b, long long k_stride_h, long long k_stride_n, const void* v,
-                       long long v_stride_b, long long v_stride_h, long long v_stride_n, const void* q,
-                       long long q_stride_b, long long q_stride_h, long long q_stride_n, void* q_out, void* k_pages,
-                       void* v_pages, int num_pages, int page_size, const int* block_table, long long table_stride,
+// k_scales null: a cache in bf16.
+static fa_status append(const void* k, long long k_stride_b, long long k_stride_h, long long k_stride_n, const void* v,
+                        long long v_stride_b, long long v_stride_h, long long v_stride_n, const void* q,
+                        long long q_stride_b, long long q_stride_h, long long q_stride_n, void* q_out, void* k_pages,
+                        void* v_pages, float* k_scales, float* v_scales, int num_pages, int page_size, const int* block_table, long long table_stride,
                        int max_pages, const int* seqlens_q, const int* seqlens_k, const int* positions,
                        long long positions_stride_b, const long long* turns, int rot_dim, int layout, float amplitude,
                        int B, int Hq, int Hkv, int N, int d, fa_stream_t stream) {
@@ -1026,8 +1040,16 @@ fa_status fa_kv_append(const void* k, long long k_stride_b, long long k_stride_h
   a.ks = ks;
   a.vs = vs;
   a.q_out = static_cast<uint16_t*>(q_out);
-  a.k_pages = static_cast<uint16_t*>(k_pages);
-  a.v_pages = static_cast<uint16_t*>(v_pages);
+  if (k_scales) {
+    a.k_bytes = static_cast<uint8_t*>(k_pages);
+    a.v_bytes = static_cast<uint8_t*>(v_pages);
+    a.k_scales = k_scales;
+    a.v_scales = v_scales;
+    a.key_growth = turns ? static_cast<float>(1.4142135623730951 * std::fabs(static_cast<double>(amplitude))) : 1.f;
+  } else {
+    a.k_pages = static_cast<uint16_t*>(k_pages);
+    a.v_pages = static_cast<uint16_t*>(v_pages);
+  }
   a.table = fa::PageTable{block_table, table_stride, max_pages, page_size, num_pages};
   if (turns)
     a.rope = fa::RopeRef{turns, positions, positions_stride_b, rot_dim, layout == FA_ROPE_INTERLEAVED, amplitude};
@@ -1041,6 +1063,35 @@ fa_status fa_kv_append(const void* k, long long k_stride_b, long long k_stride_h
   a.sms = di.sms;
   a.status = di.status;
   return fa::launch_kv_append(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
+}
+
+fa_status fa_kv_append(const void* k, long long k_stride_b, long long k_stride_h, long long k_stride_n, const void* v,
+                       long long v_stride_b, long long v_stride_h, long long v_stride_n, const void* q,
+                       long long q_stride_b, long long q_stride_h, long long q_stride_n, void* q_out, void* k_pages,
+                       void* v_pages, int num_pages, int page_size, const int* block_table, long long table_stride,
+                       int max_pages, const int* seqlens_q, const int* seqlens_k, const int* positions,
+                       long long positions_stride_b, const long long* turns, int rot_dim, int layout, float amplitude,
+                       int B, int Hq, int Hkv, int N, int d, fa_stream_t stream) {
+  return append(k, k_stride_b, k_stride_h, k_stride_n, v, v_stride_b, v_stride_h, v_stride_n, q, q_stride_b, q_stride_h,
+                q_stride_n, q_out, k_pages, v_pages, nullptr, nullptr, num_pages, page_size, block_table, table_stride,
+                max_pages, seqlens_q, seqlens_k, positions, positions_stride_b, turns, rot_dim, layout, amplitude, B, Hq,
+                Hkv, N, d, stream);
+}
+
+fa_status fa_kv_append_fp8(const void* k, long long k_stride_b, long long k_stride_h, long long k_stride_n, const void* v,
+                           long long v_stride_b, long long v_stride_h, long long v_stride_n, const void* q,
+                           long long q_stride_b, long long q_stride_h, long long q_stride_n, void* q_out,
+                           void* k_pages,
+                           void* v_pages, float* k_scales, float* v_scales, int num_pages, int page_size,
+                           const int* block_table, long long table_stride, int max_pages, const int* seqlens_q, const int* seqlens_k, const int* positions,
+                           long long positions_stride_b, const long long* turns, int rot_dim, int layout,
+                           float amplitude, int B, int Hq, int Hkv, int N, int d, fa_stream_t stream) {
+  const fa_status st = check_scales(k_scales, v_scales);
+  if (st != FA_OK) return st;
+  return append(k, k_stride_b, k_stride_h, k_stride_n, v, v_stride_b, v_stride_h, v_stride_n, q, q_stride_b, q_stride_h,
+                q_stride_n, q_out, k_pages, v_pages, k_scales, v_scales, num_pages, page_size, block_table, table_stride,
+                max_pages, seqlens_q, seqlens_k, positions, positions_stride_b, turns, rot_dim, layout, amplitude, B, Hq,
+                Hkv, N, d, stream);
 }
 
 static size_t paged_workspace_bytes(int B, int Hq, int Hkv, int Nq, int d, bool with_prefix) {
@@ -1057,12 +1108,38 @@ fa_status fa_fwd_paged(const void* q, const void* k_pages, const void* v_pages, 
                        const int* block_table, long long table_stride, int max_pages, void* o, int o_dtype,
                        float* lse, const int* seqlens_q, const int* seqlens_k, float* workspace, int B, int Hq,
                        int Hkv, int Nq, int d, float scale, int causal, fa_stream_t stream) {
-  return paged_common(q, k_pages, v_pages, num_pages, page_size, nullptr, 0, block_table, table_stride, max_pages, o,
-                      o_dtype, lse, seqlens_q, seqlens_k, workspace, B, Hq, Hkv, Nq, d, scale, causal, stream);
+  return paged_common(q, k_pages, v_pages, nullptr, nullptr, num_pages, page_size, nullptr, 0, block_table,
+                      table_stride, max_pages, o, o_dtype, lse, seqlens_q, seqlens_k, workspace, B, Hq, Hkv, Nq, d,
+                      scale, causal, stream);
+}
+
+fa_status fa_fwd_paged_fp8(const void* q, const void* k_pages, const void* v_pages, const float* k_scales,
+                           const float* v_scales, int num_pages, int page_size, const int* block_table,
+                           long long table_stride, int max_pages, void* o, int o_dtype, float* lse,
+                           const int* seqlens_q, const int* seqlens_k, float* workspace, int B, int Hq, int Hkv,
+                           int Nq, int d, float scale, int causal, fa_stream_t stream) {
+  const fa_status st = check_scales(k_scales, v_scales);
+  if (st != FA_OK) return st;
+  return paged_common(q, k_pages, v_pages, k_scales, v_scales, num_pages, page_size, nullptr, 0, block_table,
+                      table_stride, max_pages, o, o_dtype, lse, seqlens_q, seqlens_k, workspace, B, Hq, Hkv, Nq, d,
+                      scale, causal, stream);
 }
 
 size_t fa_fwd_shared_prefix_workspace_bytes(int B, int Hq, int Hkv, int Nq, int d) {
   return paged_workspace_bytes(B, Hq, Hkv, Nq, d, true);
+}
+
+static fa_status shared_prefix(const void* q, const void* k_pages, const void* v_pages, const float* k_scales,
+                               const float* v_scales, int num_pages, int page_size, const int* prefix_table,
+                               int prefix_len, const int* block_table, long long table_stride, int max_pages, void* o,
+                               int o_dtype, float* lse, const int* seqlens_q, const int* seqlens_k, float* workspace,
+                               int B, int Hq, int Hkv, int Nq, int d, float scale, int causal, fa_stream_t stream) {
+  if (!prefix_table || page_size < 16 || prefix_len < page_size || prefix_len % page_size != 0)
+    return FA_ERR_INVALID_ARG;
+  if (prefix_len / page_size > max_pages) return FA_ERR_INVALID_ARG;
+  return paged_common(q, k_pages, v_pages, k_scales, v_scales, num_pages, page_size, prefix_table, prefix_len,
+                      block_table, table_stride, max_pages, o, o_dtype, lse, seqlens_q, seqlens_k, workspace, B, Hq,
+                      Hkv, Nq, d, scale, causal, stream);
 }
 
 fa_status fa_fwd_shared_prefix(const void* q, const void* k_pages, const void* v_pages, int num_pages, int page_size,
@@ -1070,12 +1147,22 @@ fa_status fa_fwd_shared_prefix(const void* q, const void* k_pages, const void* v
                                long long table_stride, int max_pages, void* o, int o_dtype, float* lse,
                                const int* seqlens_q, const int* seqlens_k, float* workspace, int B, int Hq, int Hkv,
                                int Nq, int d, float scale, int causal, fa_stream_t stream) {
-  if (!prefix_table || page_size < 16 || prefix_len < page_size || prefix_len % page_size != 0)
-    return FA_ERR_INVALID_ARG;
-  if (prefix_len / page_size > max_pages) return FA_ERR_INVALID_ARG;
-  return paged_common(q, k_pages, v_pages, num_pages, page_size, prefix_table, prefix_len, block_table, table_stride,
-                      max_pages, o, o_dtype, lse, seqlens_q, seqlens_k, workspace, B, Hq, Hkv, Nq, d, scale, causal,
-                      stream);
+  return shared_prefix(q, k_pages, v_pages, nullptr, nullptr, num_pages, page_size, prefix_table, prefix_len,
+                       block_table, table_stride, max_pages, o, o_dtype, lse, seqlens_q, seqlens_k, workspace, B, Hq,
+                       Hkv, Nq, d, scale, causal, stream);
+}
+
+fa_status fa_fwd_shared_prefix_fp8(const void* q, const void* k_pages, const void* v_pages, const float* k_scales,
+                                   const float* v_scales, int num_pages, int page_size, const int* prefix_table,
+                                   int prefix_len, const int* block_table, long long table_stride, int max_pages,
+                                   void* o, int o_dtype, float* lse, const int* seqlens_q, const int* seqlens_k,
+                                   float* workspace, int B, int Hq, int Hkv, int Nq, int d, float scale, int causal,
+                                   fa_stream_t stream) {
+  const fa_status st = check_scales(k_scales, v_scales);
+  if (st != FA_OK) return st;
+  return shared_prefix(q, k_pages, v_pages, k_scales, v_scales, num_pages, page_size, prefix_table, prefix_len,
+                       block_table, table_stride, max_pages, o, o_dtype, lse, seqlens_q, seqlens_k, workspace, B, Hq,
+                       Hkv, Nq, d, scale, causal, stream);
 }
 
 fa_status fa_sync_status(fa_stream_t stream) {

@@ -61,21 +61,10 @@ namespace fa {
 namespace {
 
 constexpr int kStepKeys = 64;         // keys a tile
-constexpr int kStepWarps = 4;         // compute warps, 16 keys of a tile each
-constexpr int kStepThreads = 32 * (kStepWarps + 1);
 constexpr float kTau = 8.f;           // the reference maximum moves when a row's grows by more than 2^8
 constexpr float kLn2 = 0.6931471805599453f;
 
 enum StepSite : int { SITE_STEP_EMPTY = 73, SITE_STEP_FULL = 74 };
-
-// CTAs an SM: three with up to 8 rows, whose registers and rings (two tiles of
-// 32 KB at d = 128) leave room for it; two with more (three tiles).  The
-// bytes in flight an SM are the same; a third CTA fills the gaps that the
-// others leave between sequences.  (256 sequences of 1 to 1024 keys behind a
-// prefix: 262 us with three, 267 with two; 64 sequences of 300 keys 13.8 and
-// 15.1; one of 4000 keys, where there is less to share, 8.4 and 8.7.)
-template <int RB>
-constexpr int step_ctas_per_sm() { return RB <= 1 ? 3 : 2; }
 
 // RB: blocks of 8 query rows.
 template <int D, int RB>
@@ -103,13 +92,6 @@ struct StepLayout {
   static_assert(step_ctas_per_sm<RB>() * (kSmemBytes + 1024) <= 228 * 1024, "resident CTAs an SM");
 };
 
-__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-
 __device__ __forceinline__ void ldmatrix4_t(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -123,36 +105,6 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], 
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ void st_shared_u32(uint32_t addr, uint32_t v) {
-  asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
-}
-
-__device__ __forceinline__ void store_pair(float* p, float x, float y) {
-  *reinterpret_cast<float2*>(p) = make_float2(x, y);
-}
-
-__device__ __forceinline__ void store_pair(uint16_t* p, float x, float y) {
-  *reinterpret_cast<uint32_t*>(p) = pack_bf16x2(x, y);
-}
-
-// All four compute warps; true if every one of them passed true.
-__device__ __forceinline__ bool warps_agree(bool ok) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.u32 p, %1, 0;\n\t"
-      "barrier.cta.red.and.pred q, 1, %2, p;\n\t"
-      "selp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"(ok ? 1u : 0u), "n"(32 * kStepWarps)
-      : "memory");
-  return r != 0;
-}
-
-__device__ __forceinline__ void warps_sync() {
-  asm volatile("barrier.cta.sync 1, %0;" ::"n"(32 * kStepWarps) : "memory");
 }
 
 template <int D, int RB>
@@ -1081,6 +1033,8 @@ cudaError_t launch_paged_d(const PagedArgs& a, cudaStream_t stream) {
     p.table = a.table;
     p.table.block_table += b0 * a.table.table_stride;
     p.q = a.q + first * D;
+    p.k_scales = a.k_scales;
+    p.v_scales = a.v_scales;
     p.o = static_cast<uint8_t*>(a.o) + first * D * (a.o_bf16 ? 2 : 4);
     p.o_bf16 = a.o_bf16;
     p.lse = a.lse + first;
@@ -1096,7 +1050,8 @@ cudaError_t launch_paged_d(const PagedArgs& a, cudaStream_t stream) {
     p.status = a.status;
     p.wait_limit_ns = a.wait_limit_ns;
     p.stall_unit = a.stall_unit;
-    e = x.rows <= 8    ? launch_steps<D, 1>(a, p, step_ctas, stream)
+    e = a.k_scales     ? launch_steps_fp8(a, p, x.rows, step_ctas, stream)
+        : x.rows <= 8  ? launch_steps<D, 1>(a, p, step_ctas, stream)
         : x.rows <= 16 ? launch_steps<D, 2>(a, p, step_ctas, stream)
         : x.rows <= 24 ? launch_steps<D, 3>(a, p, step_ctas, stream)
                        : launch_steps<D, 4>(a, p, step_ctas, stream);

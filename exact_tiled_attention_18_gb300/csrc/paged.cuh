@@ -4,6 +4,7 @@
 
 #include <cuda_runtime.h>
 
+#include "ptx.cuh"
 #include "serving.h"
 
 namespace fa {
@@ -32,6 +33,20 @@ constexpr int kTileLine = 2 * kMaxTileCtas;  // units of the tile kernel's line
 constexpr int kPairRows = 256;         // query rows a unit of the tile kernel: two 128-row tiles
 static_assert(kLineWords >= kLineSequences + 3 && kLineWords >= kTileLine + 4, "the line's room");
 static_assert(kLineWords % 4 == 0, "what lies behind it is read 16 bytes at a time");
+
+// The step kernels' CTAs: compute warps, which share out a tile's keys, and a TMA
+// warp.
+constexpr int kStepWarps = 4;
+constexpr int kStepThreads = 32 * (kStepWarps + 1);
+
+// CTAs an SM: three with up to 8 rows, whose registers and rings (two tiles of
+// 32 KB at d = 128) leave room for it; two with more (three tiles).  The
+// bytes in flight an SM are the same; a third CTA fills the gaps that the
+// others leave between sequences.  (256 sequences of 1 to 1024 keys behind a
+// prefix: 262 us with three, 267 with two; 64 sequences of 300 keys 13.8 and
+// 15.1; one of 4000 keys, where there is less to share, 8.4 and 8.7.)
+template <int RB>
+constexpr int step_ctas_per_sm() { return RB <= 1 ? 3 : 2; }
 
 struct PagedSeq {
   const int *seqlens_q, *seqlens_k;
@@ -77,6 +92,7 @@ struct PagedStep {
   PagedSeq seq;
   PageTable table;
   const uint16_t* q;
+  const float *k_scales, *v_scales;  // of a cache in E4M3
   void* o;
   int o_bf16;
   float* lse;
@@ -129,6 +145,9 @@ struct PagedCombine {
   float* lse;
 };
 
+// The step kernel over a cache in E4M3 (paged_fp8.cu); rows a key head.
+cudaError_t launch_steps_fp8(const PagedArgs& a, const PagedStep& p, int rows, int ctas, cudaStream_t stream);
+
 cudaError_t launch_tiles(const PagedTiles& p, const CUtensorMap& tm_q, const CUtensorMap& tm_k,
                          const CUtensorMap& tm_v, int d, int ctas, cudaStream_t stream);
 
@@ -177,6 +196,43 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
+}
+
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+
+__device__ __forceinline__ void st_shared_u32(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
+__device__ __forceinline__ void store_pair(float* p, float x, float y) {
+  *reinterpret_cast<float2*>(p) = make_float2(x, y);
+}
+
+__device__ __forceinline__ void store_pair(uint16_t* p, float x, float y) {
+  *reinterpret_cast<uint32_t*>(p) = pack_bf16x2(x, y);
+}
+
+// All four compute warps; true if every one of them passed true.
+__device__ __forceinline__ bool warps_agree(bool ok) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.and.pred q, 1, %2, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(ok ? 1u : 0u), "n"(32 * kStepWarps)
+      : "memory");
+  return r != 0;
+}
+
+__device__ __forceinline__ void warps_sync() {
+  asm volatile("barrier.cta.sync 1, %0;" ::"n"(32 * kStepWarps) : "memory");
 }
 
 __device__ __forceinline__ void seq_lens(const PagedSeq& s, int b, int& lq, int& lk) {

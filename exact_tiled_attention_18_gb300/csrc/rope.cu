@@ -41,6 +41,7 @@ namespace fa {
 namespace {
 
 constexpr int kRopeThreads = 256;
+constexpr int kLowestScale = -32;  // a scale of the append's is at least 2^-32
 
 // A lane's 16 values of a head are RUNS runs of as many bytes as one load
 // takes, spread over the rotated part (or the part behind it) so that
@@ -160,6 +161,13 @@ __device__ __forceinline__ Raw<BF16> pack(const float (&v)[16]) {
       x.w[i] = __float_as_uint(v[i]);
   }
   return x;
+}
+
+// Four E4M3 numbers times r, rounded to E4M3.
+__device__ __forceinline__ uint32_t scale_e4m3x4(uint32_t packed, float r) {
+  float v[4];
+  unpack_e4m3x4(packed, v);
+  return pack_e4m3x4(v[0] * r, v[1] * r, v[2] * r, v[3] * r);
 }
 
 template <bool BF16, int RUNS>
@@ -290,6 +298,158 @@ __global__ void __launch_bounds__(kRopeThreads) append_kernel(const AppendArgs a
   }
 }
 
+// The same into a cache in E4M3, whose cells (16 tokens of a page, one head, keys
+// or values) have one scale: the smallest power of two that brings the new tokens'
+// largest magnitude to at most 448, or the one that the cell has if it holds older
+// tokens and that is larger.  A power of two is as exact as any scale here (E4M3
+// numbers keep four bits wherever they lie), and raising it leaves what is stored
+// as it was but for the numbers that become subnormal.  The largest magnitude is
+// taken before the rotation, times sqrt(2) |amplitude|, which is as far as a pair's
+// values can go: the scale then does not depend on the position.
+//
+// A group of d threads takes a cell of the tokens' heads one after the other, a
+// thread 16 values of a token as in append_kernel; the group's maximum goes
+// through shared memory, once for HEADS heads.
+template <int D>
+__global__ void __launch_bounds__(kRopeThreads) append_fp8_kernel(const AppendArgs a, const int heads_per_thread) {
+  constexpr int LANES = D / 16;
+  constexpr int RUNS = 2, HEADS = 4;
+  constexpr int WARPS = D / 32;                  // of a cell's group
+  constexpr int CELLS = kRopeThreads / D;        // a block
+  constexpr uint32_t kFinite = 0x7f800000u;      // a finite number's magnitude is below it
+  __shared__ uint32_t s_max[2][HEADS][kRopeThreads / 32];
+  grid_trigger();
+  const int group = threadIdx.x / D;
+  const int row_in = threadIdx.x % D / LANES, c = threadIdx.x % LANES;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int per_sequence = (a.N + kScaleTokens - 2) / kScaleTokens + 1;
+  const long long item = static_cast<long long>(blockIdx.x) * CELLS + group;
+  const bool exists = item < static_cast<long long>(a.B) * per_sequence;
+  const int b = exists ? static_cast<int>(item / per_sequence) : 0;
+  int lq, lk;
+  paged_lens(a.seqlens_q, a.seqlens_k, b, a.N, INT_MAX, lq, lk);
+  const int first = lk - lq;                     // the first new token's position; may be negative
+  const long long cell0 = (static_cast<long long>(first >> 4) + (item - static_cast<long long>(b) * per_sequence)) * 16;
+  const bool active = exists && lq > 0 && cell0 < lk;
+  const long long place = cell0 + row_in;
+  const bool fresh = active && place >= first && place < lk;
+  const int t = static_cast<int>(place - first);
+  const int hq = a.q ? a.Hq : 0;
+  const int heads = hq + 2 * a.Hkv;
+  const int h0 = blockIdx.y * heads_per_thread;
+  const int h1 = min(h0 + heads_per_thread, heads);
+  // the cell's first row in its page, or -1: before position 0, past the table's
+  // end or in a page that does not exist
+  long long row = -1, scale_at = 0;
+  if (active && h1 > hq && cell0 >= 0) {
+    if (cell0 >= static_cast<long long>(a.table.max_pages) * a.table.page_size) {
+      if (fresh && c == 0) record_bad_page(a.status, SITE_PAGE_PAST_TABLE, b, static_cast<int>(place));
+    } else {
+      const int page = __ldg(a.table.block_table + b * a.table.table_stride + cell0 / a.table.page_size);
+      if (page >= 0 && page < a.table.num_pages) {
+        const int in = static_cast<int>(cell0 % a.table.page_size);
+        row = static_cast<long long>(page) * a.Hkv * a.table.page_size + in;
+        scale_at = static_cast<long long>(page) * a.Hkv * (a.table.page_size / kScaleTokens) + in / kScaleTokens;
+      } else if (fresh && c == 0) {
+        record_bad_page(a.status, SITE_PAGE_APPEND, b, page);
+      }
+    }
+  }
+  const bool has_old = row >= 0 && cell0 < first;
+  const bool old = has_old && place < first;
+  const bool counts = fresh && place >= 0;       // a token with a place
+  Lane<RUNS> l = make_lane<RUNS>(a.rope, D, c, a.rope.rot_dim > 0);
+  if (fresh && h0 < hq + a.Hkv) {
+    const int position = a.rope.positions ? __ldg(a.rope.positions + b * a.rope.positions_sb + t)
+                                          : static_cast<int>(place);
+    set_angles(l, a.rope, position, 1.f);
+  }
+  int round = 0;
+  for (int h = h0; h < h1; h += HEADS, round ^= 1) {
+    Raw<true> raw[HEADS];
+    float before[HEADS];                         // the cells' scales
+#pragma unroll
+    for (int u = 0; u < HEADS; ++u) {
+      const int g = h + u;
+      before[u] = 0.f;
+      if (g >= h1) continue;
+      const bool value = g >= hq + a.Hkv;
+      const int kh = g - hq - (value ? a.Hkv : 0);
+      if (fresh) {
+        const uint16_t* src = g < hq  ? a.q + b * a.qs.b + g * a.qs.h + t * a.qs.n
+                              : value ? a.v + b * a.vs.b + kh * a.vs.h + t * a.vs.n
+                                      : a.k + b * a.ks.b + kh * a.ks.h + t * a.ks.n;
+        raw[u] = load<true>(src, 0, l);
+      }
+      if (g >= hq && has_old)
+        before[u] = (value ? a.v_scales : a.k_scales)[scale_at + static_cast<long long>(kh) *
+                                                                     (a.table.page_size / kScaleTokens)];
+    }
+#pragma unroll
+    for (int u = 0; u < HEADS; ++u) {
+      uint32_t top = 0;                          // the largest finite magnitude's bits
+      if (counts && h + u < h1) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint32_t x = (raw[u].w[i] << 16) & 0x7fffffffu, y = raw[u].w[i] & 0x7fff0000u;
+          if (x < kFinite) top = max(top, x);
+          if (y < kFinite) top = max(top, y);
+        }
+      }
+      top = __reduce_max_sync(0xffffffffu, top);
+      if (lane == 0) s_max[round][u][warp] = top;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < HEADS; ++u) {
+      const int g = h + u;
+      if (g >= h1) break;
+      const bool value = g >= hq + a.Hkv;
+      float v[16];
+      if (fresh) {
+        unpack<true>(raw[u], v);
+        if (!value) turn(l, a.rope.interleaved, v);
+        if (g < hq) store<true>(a.q_out + ((static_cast<long long>(b) * a.Hq + g) * a.N + t) * D, 0, l, pack<true>(v));
+      }
+      if (g < hq || row < 0) continue;
+      uint32_t top = 0;
+#pragma unroll
+      for (int i = 0; i < WARPS; ++i) top = max(top, s_max[round][u][group * WARPS + i]);
+      const float largest = fminf(__uint_as_float(top) * (value ? 1.f : a.key_growth), 3.4028235e38f);
+      const uint32_t bits = __float_as_uint(largest);
+      // 448 = 1.75 * 2^8
+      const int e = max(static_cast<int>(bits >> 23) - 127 - 8 + ((bits & 0x7fffffu) > 0x600000u), kLowestScale);
+      const float need = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+      const bool raised = has_old && need > before[u];
+      const float scale = has_old && !raised ? before[u] : need;
+      const float inverse = 1.f / scale;
+      const int kh = g - hq - (value ? a.Hkv : 0);
+      uint8_t* dst = (value ? a.v_bytes : a.k_bytes) + (row + static_cast<long long>(kh) * a.table.page_size + row_in) * D;
+      if (fresh) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)  // E4M3 has no infinity
+          v[i] = (__float_as_uint(v[i]) & 0x7fffffffu) < kFinite ? v[i] * inverse : __uint_as_float(0x7fc00000u);
+#pragma unroll
+        for (int k = 0; k < RUNS; ++k)
+          *reinterpret_cast<uint2*>(dst + l.at + k * l.step) =
+              make_uint2(pack_e4m3x4(v[8 * k], v[8 * k + 1], v[8 * k + 2], v[8 * k + 3]),
+                         pack_e4m3x4(v[8 * k + 4], v[8 * k + 5], v[8 * k + 6], v[8 * k + 7]));
+      } else if (old && raised) {
+        const float ratio = before[u] * inverse;
+        uint4 x = *reinterpret_cast<const uint4*>(dst + 16 * c);
+        x.x = scale_e4m3x4(x.x, ratio);
+        x.y = scale_e4m3x4(x.y, ratio);
+        x.z = scale_e4m3x4(x.z, ratio);
+        x.w = scale_e4m3x4(x.w, ratio);
+        *reinterpret_cast<uint4*>(dst + 16 * c) = x;
+      }
+      if (threadIdx.x % D == 0 && (!has_old || raised))
+        (value ? a.v_scales : a.k_scales)[scale_at + static_cast<long long>(kh) * (a.table.page_size / kScaleTokens)] =
+            scale;
+    }
+  }
+}
+
 // Heads per thread: as many as leave about a thousand threads for every SM,
 // so that a large call computes each angle for many heads and a call of few
 // tokens spreads its heads over the GPU; at most `most`: eight for the rotation,
@@ -338,6 +498,17 @@ cudaError_t launch_append_d(const AppendArgs& a, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
+template <int D>
+cudaError_t launch_append_fp8_d(const AppendArgs& a, cudaStream_t stream) {
+  constexpr int CELLS = kRopeThreads / D;
+  const long long cells = static_cast<long long>(a.B) * ((a.N + kScaleTokens - 2) / kScaleTokens + 1);
+  const int heads = (a.q ? a.Hq : 0) + 2 * a.Hkv;
+  const int per = heads_per_thread(cells * kScaleTokens, D / 16, heads, a.sms, heads);
+  const dim3 grid(static_cast<unsigned>((cells + CELLS - 1) / CELLS), (heads + per - 1) / per);
+  append_fp8_kernel<D><<<grid, kRopeThreads, 0, stream>>>(a, per);
+  return cudaGetLastError();
+}
+
 }  // namespace
 
 cudaError_t launch_rope(const RopeArgs& a, cudaStream_t stream) {
@@ -345,6 +516,7 @@ cudaError_t launch_rope(const RopeArgs& a, cudaStream_t stream) {
 }
 
 cudaError_t launch_kv_append(const AppendArgs& a, cudaStream_t stream) {
+  if (a.k_scales) return a.d == 64 ? launch_append_fp8_d<64>(a, stream) : launch_append_fp8_d<128>(a, stream);
   return a.d == 64 ? launch_append_d<64>(a, stream) : launch_append_d<128>(a, stream);
 }
 

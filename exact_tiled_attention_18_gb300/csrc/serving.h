@@ -18,6 +18,9 @@ constexpr int FA_DEV_BAD_PAGE = 7;
 // Sites recorded with FA_DEV_BAD_PAGE.
 enum PageSite : int { SITE_PAGE_APPEND = 71, SITE_PAGE_READ = 72, SITE_PAGE_PAST_TABLE = 81 };
 
+// Tokens of a page that have one scale a head, in the cache in E4M3.
+constexpr int kScaleTokens = 16;
+
 // A [B][H][N][d] tensor with contiguous d: element strides of the others.
 struct Strides {
   long long b, h, n;
@@ -60,6 +63,9 @@ struct AppendArgs {
   Strides qs, ks, vs;
   uint16_t* q_out;            // [B][Hq][N][d]
   uint16_t *k_pages, *v_pages;
+  uint8_t *k_bytes, *v_bytes;   // pages in E4M3, with
+  float *k_scales, *v_scales;   // [num_pages][Hkv][page_size / 16] scales; null: bf16 pages
+  float key_growth;             // how far the rotation can raise a key's largest magnitude
   PageTable table;
   RopeRef rope;               // positions null: the cache position
   const int *seqlens_q, *seqlens_k;
@@ -75,6 +81,7 @@ struct PagedArgs {
   CUtensorMap st_k, st_v;     // step kernel: blocked maps of the same, boxes of box_rows whole rows
   CUtensorMap st_k16, st_v16; // and of 16
   const uint16_t *q;          // [B][Hq][Nq][d]
+  const float *k_scales, *v_scales;  // [num_pages][Hkv][page_size / 16] of a cache in E4M3; null: bf16
   PageTable table;
   const int* prefix_table;    // pages of the shared prefix
   int prefix_len;             // keys of the shared prefix, a multiple of page_size; 0: none

@@ -570,6 +570,63 @@ fa_status fa_fwd_shared_prefix(const void* q, const void* k_pages, const void* v
 size_t fa_fwd_shared_prefix_workspace_bytes(int B, int Hq, int Hkv, int Nq, int d);
 
 /*
+ * The paged cache in E4M3.  Pages hold one byte a value,
+ *   k_pages, v_pages   : E4M3 [num_pages][Hkv][page_size][d], 16-byte aligned,
+ *   k_scales, v_scales : fp32 [num_pages][Hkv][page_size / 16], and a stored
+ *   value stands for its number times the scale of its cell, which is 16 tokens of a
+ *   page, one head, keys or values.
+ * Tables, lengths, positions and errors are those of the cache in bf16.
+ *
+ * fa_kv_append_fp8 is fa_kv_append into that cache: keys are rotated in fp32
+ * and rounded once, to E4M3.  A cell's scale is the smallest power of two, at
+ * least 2^-32, that brings the largest magnitude of its tokens to at most 448:
+ * of the values as they are given and, for keys that are rotated, times
+ * sqrt(2) |amplitude|, as far as a rotation can raise it, so that it does not
+ * depend on the position.  Tokens that come to a cell with older ones (the
+ * rows before theirs, which must be the same sequence's) keep the cell's
+ * scale, or raise it and have the older tokens' numbers rounded again; between
+ * powers of two that changes only those that become subnormal.  A cell whose
+ * first token is new takes nothing from what lay there before.  Infinities and
+ * NaN are stored as NaN and do not count for the scale.  A page must not be
+ * appended to from two sequences: fa_kv_fork gives each its own.
+ */
+fa_status fa_kv_append_fp8(const void* k, long long k_stride_b, long long k_stride_h, long long k_stride_n,
+                           const void* v, long long v_stride_b, long long v_stride_h, long long v_stride_n,
+                           const void* q, long long q_stride_b, long long q_stride_h, long long q_stride_n,
+                           void* q_out, void* k_pages, void* v_pages, float* k_scales, float* v_scales, int num_pages,
+                           int page_size, const int* block_table, long long table_stride, int max_pages,
+                           const int* seqlens_q, const int* seqlens_k, const int* positions,
+                           long long positions_stride_b, const long long* turns, int rot_dim, int layout,
+                           float amplitude, int B, int Hq, int Hkv, int N, int d, fa_stream_t stream);
+
+/*
+ * fa_fwd_paged and fa_fwd_shared_prefix over the cache in E4M3, with the same
+ * workspaces.  Scales may be any positive finite fp32 numbers (of values that
+ * a row sees together, within 2^60 of one another).
+ *   With up to 32 rows a key head both products run on the E4M3 numbers: a query
+ * is split into two of them (exact but for elements below 2^-15 of their row's
+ * largest, which are off by at most 2^-22 of it), a weight into three (up to 16
+ * rows: 12 significand bits) or two (8 bits).  With more rows, and against a
+ * prefix, a query is split without a scale between its two numbers (exact but
+ * for elements below 2^-9 of their row's largest: off by at most 2^-17 of it),
+ * weights are rounded to fp16 and values multiplied as fp16, exactly.
+ *   A query row that holds an infinity or a NaN has O = NaN and LSE = NaN if it
+ * sees a key, as has a row that sees a key stored as NaN.
+ */
+fa_status fa_fwd_paged_fp8(const void* q, const void* k_pages, const void* v_pages, const float* k_scales,
+                           const float* v_scales, int num_pages, int page_size, const int* block_table,
+                           long long table_stride, int max_pages, void* o, int o_dtype, float* lse,
+                           const int* seqlens_q, const int* seqlens_k, float* workspace, int B, int Hq, int Hkv,
+                           int Nq, int d, float scale, int causal, fa_stream_t stream);
+
+fa_status fa_fwd_shared_prefix_fp8(const void* q, const void* k_pages, const void* v_pages, const float* k_scales,
+                                   const float* v_scales, int num_pages, int page_size, const int* prefix_table,
+                                   int prefix_len, const int* block_table, long long table_stride, int max_pages,
+                                   void* o, int o_dtype, float* lse, const int* seqlens_q, const int* seqlens_k,
+                                   float* workspace, int B, int Hq, int Hkv, int Nq, int d, float scale, int causal,
+                                   fa_stream_t stream);
+
+/*
  * Synchronises `stream`, then reads and clears the device status word of the
  * current device.  Returns FA_ERR_DEVICE_FAULT if the stream reported a CUDA
  * error, FA_ERR_TIMEOUT if a kernel wait ran out since the last call,

@@ -1,0 +1,142 @@
+"""Attention over the paged cache in E4M3 (fa_fwd_paged_fp8) and behind a shared
+prefix (fa_fwd_shared_prefix_fp8), against the fp64 oracle on the values that
+the cache stands for."""
+
+import numpy as np
+import pytest
+import torch
+
+import exact_tiled_attention_18_gb300 as fa
+from oracle import serving
+from tests.helpers import scale_for, to64
+from tests.test_paged_gpu import CHUNKS, PREFIXES, STEPS
+from tests.test_rope_gpu import make_cache
+
+pytestmark = pytest.mark.gpu
+
+BF16, F32, E4M3 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
+
+
+class Cache:
+    """Pages of random E4M3 numbers at the sequences' positions and NaN behind
+    them, with a scale of its own (no power of two) for every cell that holds a
+    token and NaN for the others."""
+
+    def __init__(self, B, Hkv, d, page, lens_k, seed=0, spread=0.5):
+        g = torch.Generator().manual_seed(seed)
+        kp, _, self.table = make_cache(B, Hkv, d, page, lens_k, seed=seed)
+        n = kp.shape[0]
+        self.page, self.pages, self.scales, self.values = page, [], [], []
+        live = torch.zeros(n, page, dtype=torch.bool)
+        for b, length in enumerate(lens_k):
+            for i in range((length + page - 1) // page):
+                live[self.table[b, i], :min(page, length - i * page)] = True
+        for _ in range(2):
+            x = (torch.randn(n, Hkv, page, d, generator=g) * 100).clamp(-448, 448).to(E4M3)
+            scale = 0.01 * torch.exp(torch.randn(n, Hkv, page // 16, generator=g) * spread)
+            raw = x.view(torch.uint8)
+            raw[~live[:, None].expand(n, Hkv, page)] = 0x7F
+            scale[~live.view(n, 1, page // 16, 16).any(-1).expand_as(scale)] = float("nan")
+            self.pages.append(x)
+            self.scales.append(scale)
+        self.update()
+
+    def update(self):
+        """The values that the cache stands for, in 64 bits."""
+        self.values = [to64(x.float()) * np.repeat(to64(s), 16, axis=2)[..., None]
+                       for x, s in zip(self.pages, self.scales)]
+
+    def cuda(self):
+        return [t.cuda() for t in (*self.pages, *self.scales, self.table)]
+
+
+def make_batch(B, Hq, Hkv, Nq, d, page, lens_k, seed=0, q_scale=1.0, spread=0.5):
+    g = torch.Generator().manual_seed(seed + 1000)
+    q = (torch.randn(B, Hq, Nq, d, generator=g) * q_scale).to(BF16)
+    return q, Cache(B, Hkv, d, page, lens_k, seed, spread)
+
+
+def reference(q, c, lens_k, lens_q, causal):
+    lq = lens_q if lens_q is not None else [q.shape[2]] * q.shape[0]
+    return serving.paged_forward(to64(q), *c.values, c.table.numpy(), scale_for(q.shape[-1]), causal, lq, lens_k)
+
+
+def run(q, c, lens_k, lens_q=None, causal=True, o_dtype=F32, prefix=0, prefix_table=None, table=None, **kw):
+    k, v, ks, vs, t = c.cuda()
+    t = t if table is None else table.cuda()
+    lk = torch.tensor(lens_k, dtype=torch.int32, device="cuda")
+    lq = torch.tensor(lens_q, dtype=torch.int32, device="cuda") if lens_q is not None else None
+    if prefix:
+        out = fa.forward_shared_prefix_fp8(q.cuda(), k, v, ks, vs, prefix_table.cuda(), prefix, t, lk, lq,
+                                           causal=causal, o_dtype=o_dtype, **kw)
+    else:
+        out = fa.forward_paged_fp8(q.cuda(), k, v, ks, vs, t, lk, lq, causal=causal, o_dtype=o_dtype, **kw)
+    fa.sync_status()
+    return out
+
+
+def check(o, lse, ref, q, c, way, what=""):
+    """way: "steps16", "steps32" (up to 16 and 32 rows a key head) or "tiles".
+
+    A score is off by fp32 sums of d products (each addition half a step of at
+    most sum |q||k|), a few roundings of it and of log2 of a scale, and by what
+    a query's two E4M3 numbers leave: a step of their smallest, 2^-22 (steps: the
+    second is held 32 times larger) or 2^-17 of the row's largest value, for each
+    element.  Exponential, logarithm and sum: 2^-21.
+
+    Weights, relative: three E4M3 numbers 2^-12 (each leaves half a step, 2^-4, of
+    what is left), two 2^-8, fp16 2^-11.  And at least half of the smallest step:
+    2^-10 where a tile's largest weight is 2^8, 2^-18 of it for each of 128 keys.
+    (fp16: the row's reference is at least 2^-8 of its largest weight and 2^-25 the
+    half step: 2^-17 again.)  The tiles' largest weights sum to at most one.
+    """
+    o_ref, lse_ref, mass = ref
+    d = q.shape[-1]
+    qn, kn = np.abs(to64(q)).reshape(-1, d), np.nan_to_num(np.abs(c.values[0])).reshape(-1, d)
+    scale = scale_for(d)
+    top = scale * np.sqrt((qn ** 2).sum(1).max() * (kn ** 2).sum(1).max())
+    logs = np.abs(np.log2(to64(c.scales[1])[np.isfinite(to64(c.scales[1]))])).max(initial=0)
+    left = {"steps16": -22, "steps32": -22, "tiles": -17}[way]
+    e = ((d + 8) * 2.0 ** -24 * top + 2.0 ** -21 + logs * 2.0 ** -23
+         + scale * 2.0 ** left * qn.max() * kn.sum(1).max())
+    rel = 2 * e + 2.0 ** {"steps16": -12, "steps32": -8, "tiles": -11}[way]
+    least = 128 * 2.0 ** (-17 if way == "tiles" else -18) * np.nan_to_num(np.abs(c.values[1])).max()
+    got = o.cpu().double().numpy()
+    assert np.all(np.isfinite(got)), what
+    out = 2.0 ** -8 if o.dtype == BF16 else 2.0 ** -24
+    off = np.abs(got - o_ref)
+    bound = rel * mass + least + out * (np.abs(o_ref) + rel * mass + least) + 1e-30
+    assert (off - bound).max() <= 0, (what, (off - bound).max(), off.max())
+    # the smallest steps leave their bound only where they all fall the same way
+    if o.dtype == F32 and mass.max() > 0:
+        seen = mass > 0
+        assert off[seen].mean() <= rel * mass[seen].mean() + least / 64, (what, off[seen].mean(), mass[seen].mean())
+    lg = lse.cpu().double().numpy()
+    assert np.array_equal(np.isneginf(lg), np.isneginf(lse_ref)), what
+    fin = np.isfinite(lse_ref)
+    assert np.all(np.abs(lg[fin] - lse_ref[fin]) <= e + 2.0 ** -21 * (1 + np.abs(lse_ref[fin]))), what
+
+
+def way_of(Hq, Hkv, Nq, prefix=0):
+    rows = Hq // Hkv * Nq
+    return "tiles" if prefix or rows > 32 else "steps32" if rows > 16 else "steps16"
+
+
+MORE_STEPS = [
+    # B, Hq, Hkv, Nq, d, page, lens_k, lens_q
+    (1, 4, 1, 5, 128, 64, [200], None),                          # 20 rows
+    (2, 2, 1, 16, 64, 16, [16, 333], None),
+    (1, 8, 1, 4, 128, 32, [1000], None),                         # 32 rows
+    (3, 3, 1, 7, 64, 48, [700, 0, 129], [7, 7, 2]),
+    (2, 24, 2, 2, 128, 128, [1500, 127], [2, 1]),
+]
+
+
+@pytest.mark.parametrize("o_dtype", [F32, BF16])
+@pytest.mark.parametrize("case", STEPS + MORE_STEPS, ids=lambda c: "x".join(str(x) for x in c[:6]))
+def test_steps_match_oracle(case, o_dtype):
+    """Single tokens and a few drafted ones (at most 32 rows a key head)."""
+    B, Hq, Hkv, Nq, d, page, lens_k, lens_q = case
+    q, c = make_batch(B, Hq, Hkv, Nq, d, page, lens_k, seed=Nq + d + B, q_scale=0.7)
+    o, lse = run(q, c, lens_k, lens_q, o_dtype=o_dtype)
+    check(o, lse, reference(q, c, lens_k, lens_q, True), q, c, way_of(Hq, Hkv, Nq), case)
