@@ -581,7 +581,6 @@ fa_status paged_common(const void* q, const void* k_pages, const void* v_pages, 
   if (fp8 && page_size % 128 == 0) a.box_rows = 128;  // a tile's rows
   const int page_heads = num_pages * Hkv;
   const bool steps = fa::paged_uses_steps(Hq / Hkv, Nq);
-  if (fp8 && (!steps || prefix_len > 0)) return FA_ERR_INVALID_ARG;
   auto page_map = [&](CUtensorMap* m, const void* pages, int box_rows, int blocked) {
     return encode_map(m, fp8 ? MapKey{pages, 1, page_heads, page_size, d, d, box_rows}
                              : MapKey{pages, 2, page_heads, page_size, d, 64, box_rows, blocked});

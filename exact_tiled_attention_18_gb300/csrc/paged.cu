@@ -970,6 +970,8 @@ cudaError_t launch_paged_d(const PagedArgs& a, cudaStream_t stream) {
     t.seq = all;
     t.table = a.table;
     t.q = a.q;
+    t.k_scales = a.k_scales;
+    t.v_scales = a.v_scales;
     t.o = a.o;
     t.o_bf16 = a.o_bf16;
     t.lse = a.lse;
@@ -989,6 +991,7 @@ cudaError_t launch_paged_d(const PagedArgs& a, cudaStream_t stream) {
     t.stall_unit = a.stall_unit;
     return cut < units ? cudaMemsetAsync(t.counter, 0, sizeof(int), stream) : cudaSuccess;
   };
+  const auto launch = a.k_scales ? launch_tiles_fp8 : launch_tiles;
   PagedCombine c{};
   c.direct = !with_prefix;
   c.o_bf16 = a.o_bf16;
@@ -1001,7 +1004,7 @@ cudaError_t launch_paged_d(const PagedArgs& a, cudaStream_t stream) {
     t.prefix_table = a.prefix_table;
     t.boxed_rows = a.boxed_rows;
     t.wait_first = 1;
-    e = launch_tiles(t, a.tm_qp, a.tm_k, a.tm_v, D, tile_ctas, stream);
+    e = launch(t, a.tm_qp, a.tm_k, a.tm_v, D, tile_ctas, stream);
     if (e != cudaSuccess) return e;
     c.prefix = t.part;
   }
@@ -1013,7 +1016,7 @@ cudaError_t launch_paged_d(const PagedArgs& a, cudaStream_t stream) {
     t.boxed_rows = 1;
     // (behind a memset the launch does not overlap with the prefix's)
     t.wait_first = !with_prefix || t.part.cut < t.part.units;
-    e = launch_tiles(t, a.tm_q, a.tm_k, a.tm_v, D, tile_ctas, stream);
+    e = launch(t, a.tm_q, a.tm_k, a.tm_v, D, tile_ctas, stream);
     if (e != cudaSuccess) return e;
     c.seq = all;
     c.part = t.part;

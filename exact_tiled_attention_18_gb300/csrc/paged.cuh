@@ -116,6 +116,7 @@ struct PagedTiles {
   PageTable table;
   const int* prefix_table;
   const uint16_t* q;
+  const float *k_scales, *v_scales;  // of a cache in E4M3
   void* o;
   int o_bf16;
   float* lse;
@@ -150,6 +151,8 @@ cudaError_t launch_steps_fp8(const PagedArgs& a, const PagedStep& p, int rows, i
 
 cudaError_t launch_tiles(const PagedTiles& p, const CUtensorMap& tm_q, const CUtensorMap& tm_k,
                          const CUtensorMap& tm_v, int d, int ctas, cudaStream_t stream);
+cudaError_t launch_tiles_fp8(const PagedTiles& p, const CUtensorMap& tm_q, const CUtensorMap& tm_k,
+                             const CUtensorMap& tm_v, int d, int ctas, cudaStream_t stream);
 
 #if defined(__CUDACC__)
 // 4-D form of tma_load_3d (ptx.cuh).
@@ -243,6 +246,12 @@ __device__ __forceinline__ void seq_lens(const PagedSeq& s, int b, int& lq, int&
 // (the chunk index is XORed with the row index modulo 8).
 __device__ __forceinline__ uint32_t sw128(int r, int c) {
   return static_cast<uint32_t>(r * 128 + ((c ^ (r & 7)) << 4));
+}
+
+// ... and inside one of 64-byte rows with the 64-byte swizzle: chunk index XOR
+// the row pair's modulo 4.
+__device__ __forceinline__ uint32_t sw64(int r, int c) {
+  return static_cast<uint32_t>(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
 }
 
 // The line's tiles in equal ranges, one a CTA (the first `more` CTAs have one

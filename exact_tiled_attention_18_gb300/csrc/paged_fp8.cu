@@ -82,10 +82,7 @@ struct StepLayout {
 // Byte offset of 16-byte chunk c of key r in a tile.
 template <int D>
 __device__ __forceinline__ uint32_t row_chunk(int r, int c) {
-  if constexpr (D == 128)
-    return sw128(r, c);
-  else  // rows of 64 bytes: the chunk index is XORed with the row pair's modulo 4
-    return static_cast<uint32_t>(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
+  return D == 128 ? sw128(r, c) : sw64(r, c);
 }
 
 // Two 16 x 16 matrices of bytes, transposed: words 0 and 1 of lane 4 c + i are

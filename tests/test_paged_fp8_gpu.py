@@ -86,9 +86,9 @@ def check(o, lse, ref, q, c, way, what=""):
 
     Weights, relative: three E4M3 numbers 2^-12 (each leaves half a step, 2^-4, of
     what is left), two 2^-8, fp16 2^-11.  And at least half of the smallest step:
-    2^-10 where a tile's largest weight is 2^8, 2^-18 of it for each of 128 keys.
-    (fp16: the row's reference is at least 2^-8 of its largest weight and 2^-25 the
-    half step: 2^-17 again.)  The tiles' largest weights sum to at most one.
+    2^-10 where a tile's largest weight is 2^8, 2^-18 of it for each of 128 keys; the
+    tiles' largest weights sum to at most one.  fp16: 2^-25 where the weight of the
+    row's reference, which is one of its keys', is 2^7.
     """
     o_ref, lse_ref, mass = ref
     d = q.shape[-1]
@@ -100,7 +100,8 @@ def check(o, lse, ref, q, c, way, what=""):
     e = ((d + 8) * 2.0 ** -24 * top + 2.0 ** -21 + logs * 2.0 ** -23
          + scale * 2.0 ** left * qn.max() * kn.sum(1).max())
     rel = 2 * e + 2.0 ** {"steps16": -12, "steps32": -8, "tiles": -11}[way]
-    least = 128 * 2.0 ** (-17 if way == "tiles" else -18) * np.nan_to_num(np.abs(c.values[1])).max()
+    least = c.table.numel() * c.page * 2.0 ** -32 if way == "tiles" else 128 * 2.0 ** -18
+    least *= np.nan_to_num(np.abs(c.values[1])).max()
     got = o.cpu().double().numpy()
     assert np.all(np.isfinite(got)), what
     out = 2.0 ** -8 if o.dtype == BF16 else 2.0 ** -24
@@ -140,3 +141,38 @@ def test_steps_match_oracle(case, o_dtype):
     q, c = make_batch(B, Hq, Hkv, Nq, d, page, lens_k, seed=Nq + d + B, q_scale=0.7)
     o, lse = run(q, c, lens_k, lens_q, o_dtype=o_dtype)
     check(o, lse, reference(q, c, lens_k, lens_q, True), q, c, way_of(Hq, Hkv, Nq), case)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("case", CHUNKS, ids=lambda c: "x".join(str(x) for x in c[:6]))
+def test_chunks_match_oracle(case, causal):
+    """Chunks of a prompt against what is cached of it."""
+    B, Hq, Hkv, Nq, d, page, lens_k, lens_q = case
+    q, c = make_batch(B, Hq, Hkv, Nq, d, page, lens_k, seed=Nq + d + B)
+    for o_dtype in (F32, BF16):
+        o, lse = run(q, c, lens_k, lens_q, causal=causal, o_dtype=o_dtype)
+        check(o, lse, reference(q, c, lens_k, lens_q, causal), q, c, way_of(Hq, Hkv, Nq), case)
+
+
+def with_prefix(c, prefix, lens_k):
+    """Every sequence starts with the longest one's pages: their table, and a
+    block table without those entries."""
+    n = prefix // c.page
+    prefix_table = c.table[int(np.argmax(lens_k)), :n].clone()
+    c.table[:, :n] = prefix_table
+    blind = c.table.clone()
+    blind[:, :n] = -1  # entries of the prefix are not read
+    return dict(prefix=prefix, prefix_table=prefix_table, table=blind)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("case", PREFIXES, ids=lambda c: "x".join(str(x) for x in c[:7]))
+def test_shared_prefix_matches_oracle(case, causal):
+    B, Hq, Hkv, Nq, d, page, prefix, lens_k, lens_q = case
+    q, c = make_batch(B, Hq, Hkv, Nq, d, page, lens_k, seed=Nq + d + B)
+    kw = with_prefix(c, prefix, lens_k)
+    ref = reference(q, c, lens_k, lens_q, causal)
+    way = "steps32" if way_of(Hq, Hkv, Nq) == "steps32" else "tiles"
+    for o_dtype in (F32, BF16):
+        o, lse = run(q, c, lens_k, lens_q, causal=causal, o_dtype=o_dtype, **kw)
+        check(o, lse, ref, q, c, way, case)
