@@ -21,6 +21,7 @@ FA_ERR_LAUNCH = 4
 FA_ERR_TIMEOUT = 5
 FA_ERR_DEVICE_FAULT = 6
 FA_ERR_BAD_PAGE = 7
+FA_ERR_NO_PAGES = 8
 FA_DECODE_MAX_Q = 8
 FA_DTYPE_F32 = 0
 FA_DTYPE_BF16 = 1
@@ -34,6 +35,12 @@ FA_ROPE_SCALE_PARTS = 3
 
 _lock = threading.Lock()
 _lib = None
+
+
+class fa_page_tensor(ctypes.Structure):
+    """A tensor whose pages go with the page ids (see include/fa.h)."""
+    _fields_ = [("base", ctypes.c_void_p), ("heads", ctypes.c_int), ("rows", ctypes.c_int),
+                ("row_bytes", ctypes.c_int)]
 
 
 class FAError(RuntimeError):
@@ -118,6 +125,15 @@ def lib() -> ctypes.CDLL:
         L.fa_fwd_shared_prefix.restype = st
         L.fa_fwd_shared_prefix_workspace_bytes.argtypes = [i, i, i, i, i]
         L.fa_fwd_shared_prefix_workspace_bytes.restype = ctypes.c_size_t
+        pt = ctypes.POINTER(fa_page_tensor)
+        L.fa_kv_fork.argtypes = [pt, i, i, i, vp, ll, i, vp, i, vp, vp, i, vp, ll, vp, vp, vp, vp]
+        L.fa_kv_fork.restype = st
+        L.fa_kv_fork_workspace_bytes.argtypes = [i, i]
+        L.fa_kv_fork_workspace_bytes.restype = ctypes.c_size_t
+        L.fa_kv_compact.argtypes = [pt, i, i, i, vp, ll, i, vp, i, vp, vp, ll, vp, vp, vp, vp]
+        L.fa_kv_compact.restype = st
+        L.fa_kv_compact_workspace_bytes.argtypes = [i]
+        L.fa_kv_compact_workspace_bytes.restype = ctypes.c_size_t
         L.fa_sync_status.argtypes = [vp]
         L.fa_sync_status.restype = st
         L.fa_test_set_stall.argtypes = [i]
@@ -319,6 +335,30 @@ def fa_fwd_shared_prefix_fp8(q: int, k_pages: int, v_pages: int, k_scales: int, 
     return lib().fa_fwd_shared_prefix_fp8(q, k_pages, v_pages, k_scales, v_scales, num_pages, page_size, prefix_table,
                                           prefix_len, block_table, table_stride, max_pages, o, o_dtype, lse, seqlens_q,
                                           seqlens_k, workspace, B, Hq, Hkv, Nq, d, scale, causal, stream)
+
+
+def fa_kv_fork(tensors, count: int, num_pages: int, page_size: int, block_table: int, table_stride: int,
+               max_pages: int, seqlens_k: int, B: int, refs: int, sources: int, rows: int, out_table: int,
+               out_stride: int, out_seqlens: int, out_refs: int, workspace: int, stream: int) -> int:
+    """Raw C call; ``tensors``: an array of fa_page_tensor."""
+    return lib().fa_kv_fork(tensors, count, num_pages, page_size, block_table, table_stride, max_pages, seqlens_k, B,
+                            refs, sources, rows, out_table, out_stride, out_seqlens, out_refs, workspace, stream)
+
+
+def fa_kv_fork_workspace_bytes(B: int, rows: int) -> int:
+    return lib().fa_kv_fork_workspace_bytes(B, rows)
+
+
+def fa_kv_compact(tensors, count: int, num_pages: int, page_size: int, block_table: int, table_stride: int,
+                  max_pages: int, seqlens_k: int, B: int, refs: int, out_table: int, out_stride: int, out_refs: int,
+                  new_ids: int, workspace: int, stream: int) -> int:
+    """Raw C call; ``tensors``: an array of fa_page_tensor."""
+    return lib().fa_kv_compact(tensors, count, num_pages, page_size, block_table, table_stride, max_pages, seqlens_k,
+                               B, refs, out_table, out_stride, out_refs, new_ids, workspace, stream)
+
+
+def fa_kv_compact_workspace_bytes(num_pages: int) -> int:
+    return lib().fa_kv_compact_workspace_bytes(num_pages)
 
 
 def fa_sync_status(stream: int) -> int:
@@ -997,6 +1037,114 @@ def _prefix_args(prefix_table, prefix_len, q, k_pages):
     return prefix_table.data_ptr(), int(prefix_len)
 
 
+class PagePool:
+    """A cache's tensors, whose pages go with the same page ids: keys and
+    values of every layer [pages, Hkv, page_size, d], and for a cache in E4M3
+    their scales [pages, Hkv, page_size / 16].  Made once and kept by the
+    program for kv_fork and kv_compact; holds the tensors."""
+
+    def __init__(self, tensors, page_size: int):
+        self.tensors = list(tensors)
+        if not self.tensors:
+            raise ValueError("a pool needs at least one tensor")
+        first = self.tensors[0]
+        self.page_size, self.num_pages, self.index = int(page_size), first.shape[0], first.get_device()
+        if self.page_size < 16 or self.page_size % 16 or not first.is_cuda:
+            raise ValueError("the page size must be a multiple of 16, the tensors on a CUDA device")
+        self.count = len(self.tensors)
+        self.array = (fa_page_tensor * self.count)()
+        for t, x in zip(self.tensors, self.array):
+            if (t.dim() < 3 or t.shape[0] != self.num_pages or not t.is_contiguous() or t.get_device() != self.index
+                    or t.shape[2] < 1 or self.page_size % t.shape[2]):
+                raise ValueError("a pool's tensors must be contiguous [pages, heads, rows, ...] of one device, with "
+                                 "rows that divide the page size")
+            x.base, x.heads, x.rows = t.data_ptr(), t.shape[1], t.shape[2]
+            x.row_bytes = t.element_size() * (t.numel() // max(1, t.shape[0] * t.shape[1] * t.shape[2]))
+
+
+def _table_args(pool, block_table, seqlens_k, refs):
+    import torch
+    index = pool.index
+    if (block_table.dim() != 2 or block_table.dtype != torch.int32 or block_table.get_device() != index
+            or (block_table.shape[1] != 1 and block_table.stride(1) != 1)):
+        raise ValueError("block_table must be int32 [B, max_pages] on the pool's device with contiguous rows")
+    B, width = block_table.shape
+    if seqlens_k is None:
+        raise ValueError("seqlens_k is needed")
+    if refs.shape != (pool.num_pages,) or refs.dtype != torch.int32 or not refs.is_contiguous() or (
+            refs.get_device() != index):
+        raise ValueError("refs must be contiguous int32 [pages] on the pool's device")
+    return B, width, (pool.array, pool.count, pool.num_pages, pool.page_size, block_table.data_ptr(),
+                      block_table.stride(0), width, _lens(seqlens_k, B, index), B, refs.data_ptr())
+
+
+def _out_ints(out, shapes, device, index):
+    """int32 tensors of the shapes, made or checked; the first may have a row stride."""
+    import torch
+    if out is None:
+        return tuple(torch.empty(s, dtype=torch.int32, device=device) for s in shapes)
+    for k, (t, s) in enumerate(zip(out, shapes)):
+        rows = t.dim() == 2 and (s[1] == 1 or t.stride(1) == 1) if k == 0 else t.is_contiguous()
+        if t.shape != s or t.dtype != torch.int32 or t.get_device() != index or not rows:
+            raise ValueError(f"out must be int32 tensors of shapes {shapes} on the pool's device")
+    return out
+
+
+def _int_workspace(workspace, nbytes, device, index):
+    import torch
+    if workspace is None:  # as in the paged attention: a graph keeps a tensor of PyTorch's graph pool
+        if not torch.cuda.is_current_stream_capturing():
+            return None, 0
+        workspace = torch.empty(nbytes // 4, dtype=torch.int32, device=device)
+    elif (workspace.dtype != torch.int32 or not workspace.is_contiguous() or workspace.get_device() != index
+          or workspace.numel() * 4 < nbytes):
+        raise ValueError("workspace must be int32 on the pool's device, of the call's workspace_bytes(...) bytes")
+    return workspace, workspace.data_ptr()
+
+
+def kv_fork(pool, block_table, seqlens_k, refs, sources, workspace=None, out=None):
+    """Forks, drops and reorders sequences through fa_kv_fork: row i of the new
+    batch continues sequence sources[i] (int32 [rows]; outside [0, B): the row
+    is empty).  Full pages are shared, the page that is being filled stays with
+    the first row that continues its sequence and is copied for the others,
+    into the free pages of the lowest ids.  ``refs``: int32 [pages], how many
+    table entries name each page, 0: free.  Returns the new (block_table,
+    seqlens_k, refs), which ``out`` may give; the old ones are left as they
+    were.  sync_status raises if too few pages were free."""
+    import torch
+    B, width, args = _table_args(pool, block_table, seqlens_k, refs)
+    index, device = pool.index, block_table.device
+    if sources.dim() != 1 or sources.dtype != torch.int32 or not sources.is_contiguous() or (
+            sources.get_device() != index):
+        raise ValueError("sources must be contiguous int32 [rows] on the pool's device")
+    rows = sources.numel()
+    out = _out_ints(out, ((rows, width), (rows,), (pool.num_pages,)), device, index)
+    L = _lib or lib()
+    keep, ws = _int_workspace(workspace, L.fa_kv_fork_workspace_bytes(B, rows), device, index)
+    st = _call_on(index, L.fa_kv_fork, *args, sources.data_ptr(), rows, out[0].data_ptr(), out[0].stride(0),
+                  out[1].data_ptr(), out[2].data_ptr(), ws)
+    if st:
+        _check("fa_kv_fork", st)
+    return tuple(out)
+
+
+def kv_compact(pool, block_table, seqlens_k, refs, workspace=None, out=None):
+    """Moves the pages in use together through fa_kv_compact: with n of them,
+    those of ids from n on move into the free ones below.  Returns the new
+    (block_table, refs, new_ids): new_ids int32 [pages] says where each page in
+    use is now (-1 for the others)."""
+    B, width, args = _table_args(pool, block_table, seqlens_k, refs)
+    index, device = pool.index, block_table.device
+    out = _out_ints(out, ((B, width), (pool.num_pages,), (pool.num_pages,)), device, index)
+    L = _lib or lib()
+    keep, ws = _int_workspace(workspace, L.fa_kv_compact_workspace_bytes(pool.num_pages), device, index)
+    st = _call_on(index, L.fa_kv_compact, *args, out[0].data_ptr(), out[0].stride(0), out[1].data_ptr(),
+                  out[2].data_ptr(), ws)
+    if st:
+        _check("fa_kv_compact", st)
+    return tuple(out)
+
+
 def sync_status(device=None) -> None:
     """Synchronise the current stream (of ``device``, by default the current
     one) and raise if a kernel reported a failure there."""
@@ -1004,5 +1152,5 @@ def sync_status(device=None) -> None:
     with torch.cuda.device(device):  # the status word is the current device's
         status = fa_sync_status(_stream_handle(device))
     if status != FA_OK:
-        detail = fa_last_failure() if status in (FA_ERR_TIMEOUT, FA_ERR_BAD_PAGE) else None
+        detail = fa_last_failure() if status in (FA_ERR_TIMEOUT, FA_ERR_BAD_PAGE, FA_ERR_NO_PAGES) else None
         raise FAError("fa_sync_status", status, fa_status_string(status) + (f" {detail}" if detail else ""))

@@ -19,7 +19,7 @@ ROOT = os.path.dirname(PKG)
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libfa.so")
 SOURCES = ["api.cu", "fwd.cu", "fwd_fp8.cu", "bwd.cu", "bwd_rowterm.cu", "decode.cu", "rope.cu", "paged.cu", "paged_fp8.cu",
-           "paged_tiles.cu", "paged_tiles_fp8.cu"]
+           "paged_tiles.cu", "paged_tiles_fp8.cu", "pages.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

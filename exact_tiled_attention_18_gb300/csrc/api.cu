@@ -12,6 +12,7 @@
 #include <cstdlib>
 #include <cstring>
 #include <mutex>
+#include <vector>
 
 #include "../../include/fa.h"
 #include "internal.h"
@@ -457,6 +458,15 @@ cudaMemPool_t workspace_pool() {
   return pools[dev];
 }
 
+// A workspace on the stream, from the pool; a graph's allocations are its own.
+cudaError_t take_workspace(void** p, size_t bytes, cudaStream_t s) {
+  cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+  const cudaError_t e = cudaStreamIsCapturing(s, &capture);
+  if (e != cudaSuccess) return e;
+  cudaMemPool_t pool = capture == cudaStreamCaptureStatusNone ? workspace_pool() : nullptr;
+  return pool ? cudaMallocFromPoolAsync(p, bytes, pool, s) : cudaMallocAsync(p, bytes, s);
+}
+
 // Strides of the dimensions that are walked; the stride of a dimension of
 // size one means nothing and is dropped.
 fa::Strides used_strides(long long sb, long long sh, long long sn, int B, int H, int N) {
@@ -519,6 +529,42 @@ fa_status check_pages(const void* k_pages, const void* v_pages, int num_pages, i
   if (static_cast<long long>(max_pages) * page_size > 1LL << 30) return FA_ERR_INVALID_ARG;
   if (static_cast<long long>(num_pages) * Hkv >= 1LL << 31) return FA_ERR_INVALID_ARG;
   if (!aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(block_table, 4)) return FA_ERR_MISALIGNED;
+  return FA_OK;
+}
+
+// The tables and counts of a fork or a compaction.
+fa_status check_tables(int num_pages, int page_size, const int* block_table, long long table_stride, int max_pages,
+                       const int* seqlens_k, int B, const int* refs, const int* out_table, long long out_stride,
+                       int rows, const int* out_refs) {
+  if (!block_table || !seqlens_k || !refs || !out_table || !out_refs) return FA_ERR_INVALID_ARG;
+  if (num_pages < 1 || max_pages < 1 || page_size < 16 || page_size % 16 != 0 || B < 1 || rows < 1)
+    return FA_ERR_INVALID_ARG;
+  if (static_cast<long long>(max_pages) * page_size > 1LL << 30) return FA_ERR_INVALID_ARG;
+  if (table_stride < 0 || (rows > 1 && out_stride < max_pages)) return FA_ERR_INVALID_ARG;
+  for (const int* p : {block_table, seqlens_k, refs, out_table, out_refs})
+    if (!aligned(p, 4)) return FA_ERR_MISALIGNED;
+  return FA_OK;
+}
+
+bool ranges_meet(const void* a, long long a_words, const void* b, long long b_words) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + 4 * static_cast<uintptr_t>(b_words) && y < x + 4 * static_cast<uintptr_t>(a_words);
+}
+
+// Fills `out` with the tensors of a pool.
+fa_status check_tensors(const fa_page_tensor* tensors, int count, int page_size, std::vector<fa::PageTensor>& out) {
+  if (count < 0 || (count > 0 && !tensors)) return FA_ERR_INVALID_ARG;
+  out.resize(static_cast<size_t>(count));
+  for (int i = 0; i < count; ++i) {
+    const fa_page_tensor& t = tensors[i];
+    if (!t.base || t.heads < 1 || t.rows < 1 || page_size % t.rows != 0 || t.row_bytes < 4 || t.row_bytes % 4 != 0)
+      return FA_ERR_INVALID_ARG;
+    const double bytes = static_cast<double>(t.heads) * t.rows * t.row_bytes;
+    if (bytes >= 2147483648.0) return FA_ERR_INVALID_ARG;
+    if (!aligned(t.base, 16)) return FA_ERR_MISALIGNED;
+    out[static_cast<size_t>(i)] =
+        fa::PageTensor{static_cast<uint8_t*>(t.base), t.heads, t.rows, t.row_bytes, t.row_bytes % 16 == 0, 0};
+  }
   return FA_OK;
 }
 
@@ -604,14 +650,8 @@ fa_status paged_common(const void* q, const void* k_pages, const void* v_pages, 
     return FA_ERR_LAUNCH;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (!workspace) {
-    // (a graph's allocations are its own, not the pool's)
-    cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
-    if (cudaStreamIsCapturing(s, &capture) != cudaSuccess) return FA_ERR_LAUNCH;
-    cudaMemPool_t pool = capture == cudaStreamCaptureStatusNone ? workspace_pool() : nullptr;
     const size_t bytes = sizeof(float) * fa::paged_workspace_floats(B, Hkv, Hq / Hkv, Nq, d, prefix_len > 0);
-    const cudaError_t e = pool ? cudaMallocFromPoolAsync(reinterpret_cast<void**>(&a.part), bytes, pool, s)
-                               : cudaMallocAsync(reinterpret_cast<void**>(&a.part), bytes, s);
-    if (e != cudaSuccess) return FA_ERR_LAUNCH;
+    if (take_workspace(reinterpret_cast<void**>(&a.part), bytes, s) != cudaSuccess) return FA_ERR_LAUNCH;
   }
   cudaError_t e = fa::launch_paged(a, s);
   if (!workspace) {
@@ -1164,6 +1204,107 @@ fa_status fa_fwd_shared_prefix_fp8(const void* q, const void* k_pages, const voi
                        Hkv, Nq, d, scale, causal, stream);
 }
 
+size_t fa_kv_fork_workspace_bytes(int B, int rows) {
+  return B < 1 || rows < 1 ? 0 : sizeof(int) * fa::fork_workspace_words(B, rows);
+}
+
+fa_status fa_kv_fork(const fa_page_tensor* tensors, int count, int num_pages, int page_size, const int* block_table,
+                     long long table_stride, int max_pages, const int* seqlens_k, int B, const int* refs,
+                     const int* sources, int rows, int* out_table, long long out_stride, int* out_seqlens,
+                     int* out_refs, int* workspace, fa_stream_t stream) {
+  fa_status st = check_tables(num_pages, page_size, block_table, table_stride, max_pages, seqlens_k, B, refs, out_table,
+                              out_stride, rows, out_refs);
+  if (st != FA_OK) return st;
+  if (!sources || !out_seqlens) return FA_ERR_INVALID_ARG;
+  if (!aligned(sources, 4) || !aligned(out_seqlens, 4) || (workspace && !aligned(workspace, 16)))
+    return FA_ERR_MISALIGNED;
+  const long long in_words = (B - 1) * table_stride + max_pages, out_words = (rows - 1) * out_stride + max_pages;
+  if (ranges_meet(block_table, in_words, out_table, out_words) || ranges_meet(refs, num_pages, out_refs, num_pages) ||
+      ranges_meet(seqlens_k, B, out_seqlens, rows) || ranges_meet(sources, rows, out_seqlens, rows))
+    return FA_ERR_INVALID_ARG;
+  try {
+    std::vector<fa::PageTensor> list;
+    st = check_tensors(tensors, count, page_size, list);
+    if (st != FA_OK) return st;
+    DeviceInfo di;
+    if (device_info(di) != FA_OK) return FA_ERR_LAUNCH;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    fa::ForkArgs a{};
+    a.table = fa::PageTable{block_table, table_stride, max_pages, page_size, num_pages};
+    a.seqlens = seqlens_k;
+    a.refs = refs;
+    a.sources = sources;
+    a.B = B;
+    a.rows = rows;
+    a.out_table = out_table;
+    a.out_stride = out_stride;
+    a.out_seqlens = out_seqlens;
+    a.out_refs = out_refs;
+    a.workspace = workspace;
+    a.status = di.status;
+    if (!workspace && take_workspace(reinterpret_cast<void**>(&a.workspace), fa_kv_fork_workspace_bytes(B, rows), s) !=
+                          cudaSuccess)
+      return FA_ERR_LAUNCH;
+    cudaError_t e = fa::launch_fork(a, list.data(), count, di.sms, s);
+    if (!workspace) {
+      const cudaError_t e2 = cudaFreeAsync(a.workspace, s);
+      if (e == cudaSuccess) e = e2;
+    }
+    return e == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
+  } catch (...) {  // (host memory)
+    return FA_ERR_LAUNCH;
+  }
+}
+
+size_t fa_kv_compact_workspace_bytes(int num_pages) {
+  return num_pages < 1 ? 0 : sizeof(int) * fa::compact_workspace_words(num_pages);
+}
+
+fa_status fa_kv_compact(const fa_page_tensor* tensors, int count, int num_pages, int page_size, const int* block_table,
+                        long long table_stride, int max_pages, const int* seqlens_k, int B, const int* refs,
+                        int* out_table, long long out_stride, int* out_refs, int* new_ids, int* workspace,
+                        fa_stream_t stream) {
+  fa_status st = check_tables(num_pages, page_size, block_table, table_stride, max_pages, seqlens_k, B, refs, out_table,
+                              out_stride, B, out_refs);
+  if (st != FA_OK) return st;
+  if (!new_ids) return FA_ERR_INVALID_ARG;
+  if (!aligned(new_ids, 4) || (workspace && !aligned(workspace, 16))) return FA_ERR_MISALIGNED;
+  const long long in_words = (B - 1) * table_stride + max_pages, out_words = (B - 1) * out_stride + max_pages;
+  if (ranges_meet(block_table, in_words, out_table, out_words) || ranges_meet(refs, num_pages, out_refs, num_pages) ||
+      ranges_meet(refs, num_pages, new_ids, num_pages) || ranges_meet(out_refs, num_pages, new_ids, num_pages))
+    return FA_ERR_INVALID_ARG;
+  try {
+    std::vector<fa::PageTensor> list;
+    st = check_tensors(tensors, count, page_size, list);
+    if (st != FA_OK) return st;
+    DeviceInfo di;
+    if (device_info(di) != FA_OK) return FA_ERR_LAUNCH;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    fa::CompactArgs a{};
+    a.table = fa::PageTable{block_table, table_stride, max_pages, page_size, num_pages};
+    a.seqlens = seqlens_k;
+    a.refs = refs;
+    a.B = B;
+    a.out_table = out_table;
+    a.out_stride = out_stride;
+    a.out_refs = out_refs;
+    a.new_ids = new_ids;
+    a.workspace = workspace;
+    a.status = di.status;
+    if (!workspace &&
+        take_workspace(reinterpret_cast<void**>(&a.workspace), fa_kv_compact_workspace_bytes(num_pages), s) != cudaSuccess)
+      return FA_ERR_LAUNCH;
+    cudaError_t e = fa::launch_compact(a, list.data(), count, di.sms, s);
+    if (!workspace) {
+      const cudaError_t e2 = cudaFreeAsync(a.workspace, s);
+      if (e == cudaSuccess) e = e2;
+    }
+    return e == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
+  } catch (...) {  // (host memory)
+    return FA_ERR_LAUNCH;
+  }
+}
+
 fa_status fa_sync_status(fa_stream_t stream) {
   if (cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return FA_ERR_DEVICE_FAULT;
   int h[4] = {0, 0, 0, 0};
@@ -1175,7 +1316,8 @@ fa_status fa_sync_status(fa_stream_t stream) {
     }
     const int zero[4] = {0, 0, 0, 0};
     if (cudaMemcpyToSymbol(g_fa_status, zero, sizeof(zero)) != cudaSuccess) return FA_ERR_DEVICE_FAULT;
-    return h[0] == FA_ERR_TIMEOUT || h[0] == FA_ERR_BAD_PAGE ? static_cast<fa_status>(h[0]) : FA_ERR_DEVICE_FAULT;
+    return h[0] == FA_ERR_TIMEOUT || h[0] == FA_ERR_BAD_PAGE || h[0] == FA_ERR_NO_PAGES ? static_cast<fa_status>(h[0])
+                                                                                        : FA_ERR_DEVICE_FAULT;
   }
   return FA_OK;
 }
@@ -1209,6 +1351,7 @@ const char* fa_status_string(fa_status s) {
     case FA_ERR_DEVICE_FAULT: return "FA_ERR_DEVICE_FAULT: the stream reported a CUDA error";
     case FA_ERR_BAD_PAGE:
       return "FA_ERR_BAD_PAGE: a block table names a page outside the cache, or ends before an appended token";
+    case FA_ERR_NO_PAGES: return "FA_ERR_NO_PAGES: a fork needed more pages than are free";
   }
   return "unknown fa_status";
 }

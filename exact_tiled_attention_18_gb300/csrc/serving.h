@@ -14,9 +14,13 @@ namespace fa {
 // Status codes these kernels leave in the device status word, besides the
 // timeout of ptx.cuh.
 constexpr int FA_DEV_BAD_PAGE = 7;
+constexpr int FA_DEV_NO_PAGES = 8;
 
-// Sites recorded with FA_DEV_BAD_PAGE.
-enum PageSite : int { SITE_PAGE_APPEND = 71, SITE_PAGE_READ = 72, SITE_PAGE_PAST_TABLE = 81 };
+// Sites recorded with FA_DEV_BAD_PAGE, and with FA_DEV_NO_PAGES.
+enum PageSite : int {
+  SITE_PAGE_APPEND = 71, SITE_PAGE_READ = 72, SITE_PAGE_PAST_TABLE = 81,
+  SITE_PAGE_FORK = 85, SITE_PAGE_COMPACT = 86, SITE_NO_PAGES = 87,
+};
 
 // Tokens of a page that have one scale a head, in the cache in E4M3.
 constexpr int kScaleTokens = 16;
@@ -101,6 +105,56 @@ struct PagedArgs {
   int stall_unit;
 };
 
+// A tensor whose pages go with the page ids: [num_pages][heads][rows][row_bytes],
+// rows the page's tokens or groups of them.
+struct PageTensor {
+  uint8_t* base;
+  int heads, rows, row_bytes;
+  int wide;        // copied 16 bytes at a time, else 4
+  int slice_end;   // slices of it and of the tensors before it
+};
+
+struct PageCopy {
+  int src, dst, tokens;
+};
+
+constexpr int kCopyTensors = 96;  // of a launch, whose arguments hold them
+
+struct CopyArgs {
+  int* workspace;
+  long long list_a, list_b, first;  // words of its lists
+  int page_size, slices, count;
+  PageTensor t[kCopyTensors];
+};
+static_assert(sizeof(CopyArgs) <= 4000, "a launch's arguments");
+
+struct ForkArgs {
+  PageTable table;
+  const int *seqlens, *refs, *sources;
+  int B, rows;
+  int* out_table;           // [rows][max_pages]
+  long long out_stride;
+  int *out_seqlens, *out_refs;
+  int* workspace;
+  int* status;
+};
+
+struct CompactArgs {
+  PageTable table;
+  const int *seqlens, *refs;
+  int B;
+  int* out_table;           // [B][max_pages]
+  long long out_stride;
+  int *out_refs, *new_ids;
+  int* workspace;
+  int* status;
+};
+
+cudaError_t launch_fork(const ForkArgs& a, const PageTensor* tensors, int count, int sms, cudaStream_t stream);
+cudaError_t launch_compact(const CompactArgs& a, const PageTensor* tensors, int count, int sms, cudaStream_t stream);
+size_t fork_workspace_words(int B, int rows);
+size_t compact_workspace_words(int num_pages);
+
 cudaError_t launch_rope(const RopeArgs& a, cudaStream_t stream);
 cudaError_t launch_kv_append(const AppendArgs& a, cudaStream_t stream);
 cudaError_t launch_paged(const PagedArgs& a, cudaStream_t stream);
@@ -141,16 +195,21 @@ __device__ __forceinline__ void grid_trigger() { asm volatile("griddepcontrol.la
 // which the compiler may move before it.
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
-// Records an entry of a block table that names no page, or a position behind
-// the table's last one (first failure wins).
-__device__ __forceinline__ void record_bad_page(int* status, int site, int sequence, int what) {
-  if (atomicCAS(status, 0, FA_DEV_BAD_PAGE) == 0) {
+// First failure wins.
+__device__ __forceinline__ void record_failure_at(int* status, int code, int site, int sequence, int what) {
+  if (atomicCAS(status, 0, code) == 0) {
     volatile int* s = status;
     s[1] = site;
     s[2] = sequence;
     s[3] = what;
     __threadfence();
   }
+}
+
+// Records an entry of a block table that names no page, or a position behind
+// the table's last one.
+__device__ __forceinline__ void record_bad_page(int* status, int site, int sequence, int what) {
+  record_failure_at(status, FA_DEV_BAD_PAGE, site, sequence, what);
 }
 
 // For a kernel that does not wait for the one before it at its start, because

@@ -69,8 +69,9 @@ typedef enum {
   FA_ERR_LAUNCH = 4,        /* the CUDA runtime refused a launch or an allocation */
   FA_ERR_TIMEOUT = 5,       /* a kernel wait ran past its limit; the kernel returned early */
   FA_ERR_DEVICE_FAULT = 6,  /* the stream reported a CUDA error while synchronising */
-  FA_ERR_BAD_PAGE = 7       /* a block table names a page outside the cache, or ends before an appended token
+  FA_ERR_BAD_PAGE = 7,      /* a block table names a page outside the cache, or ends before an appended token
                                (reported by fa_sync_status) */
+  FA_ERR_NO_PAGES = 8       /* a fork needed more pages than are free (reported by fa_sync_status) */
 } fa_status;
 
 /* Element type of the forward output O (fa_fwd_ex, fa_bwd_ex). */
@@ -627,11 +628,90 @@ fa_status fa_fwd_shared_prefix_fp8(const void* q, const void* k_pages, const voi
                                    fa_stream_t stream);
 
 /*
+ * Pages between sequences.  Several sequences may have a page in common (a
+ * prompt that several samples continue, beams of one request), so every page
+ * has a count of the block-table entries that name it,
+ *   refs : device ints [num_pages]; a page whose count is 0 is free.
+ * Counts are the caller's: a program gives a page to a sequence by writing its
+ * id into the table and 1 into its count; pages that are in use in other ways
+ * (a prefix table of its own) count as well.
+ *
+ * A page id names the same page in every tensor of a cache: keys and values of
+ * all layers, and for a cache in E4M3 their scales.  The calls below take them
+ * as a list, each tensor [num_pages][heads][rows][row_bytes], contiguous, where
+ * `rows` divides page_size: page_size for keys and values, page_size / 16 for
+ * scales.  Bases are 16-byte aligned, row_bytes a multiple of 4, a page of a
+ * tensor below 2^31 bytes.  The list itself is host memory, read during the call.
+ */
+typedef struct {
+  void* base;
+  int heads, rows, row_bytes;
+} fa_page_tensor;
+
+/*
+ * Forks, drops and reorders sequences: row i of the new batch continues
+ * sequence sources[i] of the old one, or is empty where sources[i] is not in [0,
+ * B).  A sequence may be continued by any number of rows, and one that no row
+ * continues lets go of its pages.  So one call is a beam search's reordering,
+ * a prompt's samples, or the end of some sequences.
+ *   - Full pages are shared: the new row names them too.
+ *   - A page that is being filled (the last one, where the length is no
+ *     multiple of page_size) stays with the first row that continues the
+ *     sequence.  Every other such row gets a page of its own, and the page's
+ *     tokens are copied there in every tensor: rows behind them are left as
+ *     they were.
+ *   - Those pages are the free ones of the lowest ids, in the order of the
+ *     rows; pages that this call has freed are among them.
+ * Where too few are free, the rows that come last have -1 in their tables, and
+ * fa_sync_status reports FA_ERR_NO_PAGES.  A used entry outside [0, num_pages) is
+ * reported as FA_ERR_BAD_PAGE, passed on as it is, and counts nothing.
+ *   block_table, seqlens_k : of the old batch [B][max_pages], [B], as
+ *               fa_fwd_paged; only the pages that seqlens_k reaches are read
+ *               (negative: 0, at most max_pages * page_size).
+ *   out_table : [rows][max_pages], stride out_stride >= max_pages; entries behind
+ *               a row's pages are -1.  out_seqlens: [rows]; out_refs:
+ *               [num_pages], refs less the old rows' entries plus the new ones'.
+ *               None may overlap what it comes from, which is left as it was
+ *               but for the pages copied to: a program keeps two sets and
+ *               swaps them.
+ *   workspace : fa_kv_fork_workspace_bytes(B, rows) bytes, 16-byte aligned, used by
+ *               one call at a time; or NULL, as in fa_fwd_paged.
+ */
+fa_status fa_kv_fork(const fa_page_tensor* tensors, int count, int num_pages, int page_size, const int* block_table,
+                     long long table_stride, int max_pages, const int* seqlens_k, int B, const int* refs,
+                     const int* sources, int rows, int* out_table, long long out_stride, int* out_seqlens,
+                     int* out_refs, int* workspace, fa_stream_t stream);
+
+size_t fa_kv_fork_workspace_bytes(int B, int rows);
+
+/*
+ * Moves the pages in use together: with n pages in use, those with ids from n
+ * on move into the free ones below n, the lowest into the lowest, in every
+ * tensor (whole pages); pages from n on are then free, and their memory can be
+ * given back or used otherwise.
+ *   out_table : block_table with the new ids in the entries that seqlens_k
+ *               reaches, the others as they were (stride >= max_pages); an entry
+ *               of a page that is not in use is reported as FA_ERR_BAD_PAGE and
+ *               left as it was.
+ *   out_refs  : [num_pages], the counts by new ids.
+ *   new_ids   : [num_pages], where each page in use is now, -1 for the others:
+ *               what other tables that name pages are to be changed by.
+ *   workspace : fa_kv_compact_workspace_bytes(num_pages) bytes, as fa_kv_fork's.
+ * Outputs may not overlap what they come from.
+ */
+fa_status fa_kv_compact(const fa_page_tensor* tensors, int count, int num_pages, int page_size, const int* block_table,
+                        long long table_stride, int max_pages, const int* seqlens_k, int B, const int* refs,
+                        int* out_table, long long out_stride, int* out_refs, int* new_ids, int* workspace,
+                        fa_stream_t stream);
+
+size_t fa_kv_compact_workspace_bytes(int num_pages);
+
+/*
  * Synchronises `stream`, then reads and clears the device status word of the
  * current device.  Returns FA_ERR_DEVICE_FAULT if the stream reported a CUDA
  * error, FA_ERR_TIMEOUT if a kernel wait ran out since the last call,
- * FA_ERR_BAD_PAGE if a paged call met a table entry that names no page, FA_OK
- * otherwise.
+ * FA_ERR_BAD_PAGE if a paged call met a table entry that names no page,
+ * FA_ERR_NO_PAGES if a fork found too few free pages, FA_OK otherwise.
  */
 fa_status fa_sync_status(fa_stream_t stream);
 
@@ -640,10 +720,11 @@ fa_status fa_sync_status(fa_stream_t stream);
  * out[0] status code, out[1] wait site, out[2] block index, out[3] work unit.
  * Wait sites: 1-7 forward, 11-20 dK/dV, 21-32 dQ, 35-36 decode, 41-47 FP8
  * forward, 51-59 the single-pass row-term pass, 61-63 the single-pass dK/dV
- * sweep, 71-81 the paged calls (each kernel's source names them).  After
+ * sweep, 71-87 the paged calls (each kernel's source names them).  After
  * FA_ERR_BAD_PAGE: out[2] the sequence (0 for a prefix), out[3] the table
  * entry, or where out[1] is 81 the position of an appended token that is
- * behind the table's last one.
+ * behind the table's last one.  After FA_ERR_NO_PAGES: out[2] the first row
+ * without a page, out[3] how many there are.
  * Returns FA_OK, or FA_ERR_INVALID_ARG if out is NULL.
  */
 fa_status fa_last_failure(int out[4]);
