@@ -177,9 +177,9 @@ struct TileLayout {
   static constexpr int kPieceOff = kScratchOff + 64;           // two pieces
   static constexpr int kRowOff = kPieceOff + 2 * 48;           // [2 pieces][256 rows] place in q and o, then last key
   static constexpr int kStatOff = kRowOff + 2 * kPairRows * 8; // [2 row tiles][maximum, sum, correction][128]
-  // [tiles][of keys times `scale`, log2 of values', 1 / of values'][scales of a tile]
+  // [tiles][groups of 16 keys][keys' scale times `scale`, log2 of values', 1 / values', -]
   static constexpr int kScaleOff = (kStatOff + 2 * 3 * kRows * 4 + 15) / 16 * 16;
-  static constexpr int kGrowOff = kScaleOff + (FP8 ? kScaleTiles * 3 * kScales * 4 : 0);  // [128] rows' multipliers
+  static constexpr int kGrowOff = kScaleOff + (FP8 ? kScaleTiles * kScales * 16 : 0);  // [128] rows' multipliers
   static constexpr int kLineOff = kGrowOff + (FP8 && DUAL ? kRows * 4 : 0);
   static constexpr int kSmemBytes = kLineOff + (kTileLine + 1) * 4 + 1024;
   static constexpr uint32_t kColO = 256;
@@ -203,6 +203,12 @@ __device__ __forceinline__ void tma_load_groups(uint32_t dst, const CUtensorMap*
       " [%0], [%1, {%2, %2, %2, %3, %4}], [%5], %6;" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(group), "r"(outer), "r"(bar), "l"(policy)
       : "memory");
+}
+
+__device__ __forceinline__ float2 ld_shared_f2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+  return v;
 }
 
 __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
@@ -450,33 +456,47 @@ __global__ void __launch_bounds__(Launch<FP8>::kThreads, 1)
           ok = tile_wait(BAR(L::Q_RAW + t), qn & 1, wc_idle, SITE_TILE_CONVERT, n);
           if (!ok) break;
           const uint32_t qt = sbase + t * L::kTileBytes;
-          uint32_t raw[D / 8][4];
+          const uint32_t stage = sbase + L::kStageOff + warp * 2048 + lane * 64;
+          auto raw = [&](int c, uint32_t (&x)[4]) { ld_shared_v4(qt + (c >> 3) * 16384 + sw128(r, c & 7), x); };
           uint32_t top = 0;  // the largest magnitude's bits
-#pragma unroll
+#pragma unroll 4
           for (int c = 0; c < D / 8; ++c) {
-            ld_shared_v4(qt + (c >> 3) * 16384 + sw128(r, c & 7), raw[c]);
+            uint32_t x[4];
+            raw(c, x);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              top = max(top, max((raw[c][i] << 16) & 0x7fffffffu, raw[c][i] & 0x7fff0000u));
+            for (int i = 0; i < 4; ++i) top = max(top, max((x[i] << 16) & 0x7fffffffu, x[i] & 0x7fff0000u));
           }
           const uint32_t e = max(top >> 23, 8u);  // the exponent's field
           const float up = __uint_as_float((261u - e) << 23);
           grow = e == 255u ? CUDART_NAN_F : __uint_as_float((e - 7u) << 23);  // (an infinity or a NaN in the row)
-#pragma unroll
-          for (int c = 0; c < D / 16; ++c) {
-            uint32_t hi[4], lo[4];
+          // 16 columns at a time: those of the first block in order and the second's
+          // from behind, with the first block's lo set aside, so that nothing is
+          // written where a value is still to be read
+#pragma unroll 1
+          for (int k = 0; k < D / 16; ++k) {
+            const int c = k < 4 ? k : 11 - k;
+            uint32_t x[8], hi[4], lo[4];
+            raw(2 * c, *reinterpret_cast<uint32_t(*)[4]>(x));
+            raw(2 * c + 1, *reinterpret_cast<uint32_t(*)[4]>(x + 4));
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const uint32_t x = raw[2 * c + i / 2][2 * (i & 1)], y = raw[2 * c + i / 2][2 * (i & 1) + 1];
-              float v[4] = {__uint_as_float(x << 16) * up, __uint_as_float(x & 0xFFFF0000u) * up,
-                            __uint_as_float(y << 16) * up, __uint_as_float(y & 0xFFFF0000u) * up};
-              hi[i] = pack_e4m3x4(v[0], v[1], v[2], v[3]);
+              const float v0 = __uint_as_float(x[2 * i] << 16) * up, v1 = __uint_as_float(x[2 * i] & 0xFFFF0000u) * up;
+              const float v2 = __uint_as_float(x[2 * i + 1] << 16) * up;
+              const float v3 = __uint_as_float(x[2 * i + 1] & 0xFFFF0000u) * up;
+              hi[i] = pack_e4m3x4(v0, v1, v2, v3);
               float u[4];
               unpack_e4m3x4(hi[i], u);
-              lo[i] = pack_e4m3x4(v[0] - u[0], v[1] - u[1], v[2] - u[2], v[3] - u[3]);
+              lo[i] = pack_e4m3x4(v0 - u[0], v1 - u[1], v2 - u[2], v3 - u[3]);
             }
             st_shared_v4(qt + sw128(r, c), hi[0], hi[1], hi[2], hi[3]);
-            st_shared_v4(D == 128 ? qt + 16384 + sw128(r, c) : qt + sw128(r, 4 + c), lo[0], lo[1], lo[2], lo[3]);
+            st_shared_v4(k < 4 ? stage + ((k ^ ((lane >> 1) & 3)) << 4) : qt + 16384 + sw128(r, c), lo[0], lo[1], lo[2],
+                         lo[3]);
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t x[4];
+            ld_shared_v4(stage + ((k ^ ((lane >> 1) & 3)) << 4), x);
+            st_shared_v4(D == 128 ? qt + 16384 + sw128(r, k) : qt + sw128(r, 4 + k), x[0], x[1], x[2], x[3]);
           }
           if constexpr (DUAL) shared_grow[r] = grow;
           fence_proxy_async_smem();
@@ -517,28 +537,27 @@ __global__ void __launch_bounds__(Launch<FP8>::kThreads, 1)
         if (__any_sync(0xffffffffu, lim < kRows)) {
 #pragma unroll
           for (int c = 0; c < 128; ++c) s[c] = (c < lim) ? s[c] : -CUDART_INF_F;
+          if constexpr (FP8) {  // which are read again
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tmem_st32(tS + 32 * c, reinterpret_cast<const uint32_t(&)[32]>(s[32 * c]));
+            tmem_st_wait();
+          }
         }
         float mt;
-        [[maybe_unused]] const float* scales = nullptr;
-        [[maybe_unused]] float ck[kScales], lsv[kScales];
+        [[maybe_unused]] uint32_t scales = 0;
         if constexpr (FP8) {
           const uint32_t at = base + (DUAL ? 2 * j + t : j);
           ok = tile_wait(BAR(L::SCALES + at % kScaleTiles), (at / kScaleTiles) & 1, wc, SITE_TILE_CONVERT, n);
           if (!ok) break;
-          scales = reinterpret_cast<const float*>(smem + L::kScaleOff) + at % kScaleTiles * 3 * kScales;
-#pragma unroll
-          for (int b = 0; b < kScales; b += 4) {
-            *reinterpret_cast<float4*>(ck + b) = *reinterpret_cast<const float4*>(scales + b);
-            *reinterpret_cast<float4*>(lsv + b) = *reinterpret_cast<const float4*>(scales + kScales + b);
-          }
+          scales = sbase + L::kScaleOff + at % kScaleTiles * kScales * 16;
           mt = -CUDART_INF_F;
 #pragma unroll
           for (int b = 0; b < kScales; ++b) {
             const float* x = s + kScaleTokens * b;
             const float t1 = fmax3(fmax3(x[0], x[1], x[2]), fmax3(x[3], x[4], x[5]), fmax3(x[6], x[7], x[8]));
             const float t2 = fmax3(fmax3(x[9], x[10], x[11]), fmax3(x[12], x[13], x[14]), x[15]);
-            ck[b] *= grow;
-            mt = fmaxf(mt, fmaf(fmaxf(t1, t2), ck[b], lsv[b]));
+            const float2 c = ld_shared_f2(scales + 16 * b);
+            mt = fmaxf(mt, fmaf(fmaxf(t1, t2), c.x * grow, c.y));
           }
         } else {
           // row maximum as a log-depth tree of 3-input max
@@ -581,28 +600,38 @@ __global__ void __launch_bounds__(Launch<FP8>::kThreads, 1)
           }
         }
         if constexpr (FP8) {
+          // The scores come from tensor memory once more, 64 columns at a time, so
+          // that the loop over a tile stays small: with all 128 columns' instructions
+          // in a row it is larger than the first-level instruction cache.
+          const float add0 = kShift - m_ref;
+#pragma unroll 1
+          for (int c = 0; c < 2; ++c) {
+            uint32_t x[64], pk[32];
+            tmem_ld32(tS + 64 * c, *reinterpret_cast<uint32_t(*)[32]>(x));
+            tmem_ld32(tS + 64 * c + 32, *reinterpret_cast<uint32_t(*)[32]>(x + 32));
+            tmem_ld_wait();
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t pk[16];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {  // 16 columns of one scale each
-              const int b = 2 * c + h;
-              const float add = lsv[b] + (kShift - m_ref);
-              const uint64_t c2 = f2_pack(ck[b], ck[b]), n2 = f2_pack(add, add);
+            for (int b = 0; b < 4; ++b) {  // 16 columns of one scale each
+              uint32_t k[4];
+              ld_shared_v4(scales + 16 * (4 * c + b), k);
+              const float mul = __uint_as_float(k[0]) * grow, add = __uint_as_float(k[1]) + add0;
+              const uint64_t c2 = f2_pack(mul, mul), n2 = f2_pack(add, add);
               uint64_t sum = f2_pack(0.f, 0.f);
 #pragma unroll
               for (int i = 0; i < 8; ++i) {
                 float x0, x1;
-                f2_unpack(ffma2(f2_pack(s[16 * b + 2 * i], s[16 * b + 2 * i + 1]), c2, n2), x0, x1);
+                f2_unpack(ffma2(f2_pack(__uint_as_float(x[16 * b + 2 * i]), __uint_as_float(x[16 * b + 2 * i + 1])), c2,
+                                n2),
+                          x0, x1);
                 const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
                 sum = fadd2(sum, f2_pack(p0, p1));
-                pk[8 * h + i] = pack_f16x2(p0, p1);
+                pk[8 * b + i] = pack_f16x2(p0, p1);
               }
               float a0, a1;
               f2_unpack(sum, a0, a1);
-              l = fmaf(a0 + a1, scales[2 * kScales + b], l);
+              l = fmaf(a0 + a1, __uint_as_float(k[2]), l);
             }
-            tmem_st16(tS + 16 * c, pk);
+            tmem_st32(tS + 32 * c, pk);
           }
         } else {
           const uint64_t c2 = f2_pack(scale_log2, scale_log2);
@@ -855,14 +884,14 @@ __global__ void __launch_bounds__(Launch<FP8>::kThreads, 1)
             if (loads)
               tma_load_3d_hint(sbase + L::kRawOff + vs * (L::kTileBytes / 2) + offset, &tm_v, BAR(L::RAW_FULL + vs), 0,
                                row, outer, policy);
-            float* scales = reinterpret_cast<float*>(smem + L::kScaleOff) + kvpos % kScaleTiles * 3 * kScales;
+            float* scales = reinterpret_cast<float*>(smem + L::kScaleOff) + (kvpos % kScaleTiles * kScales + group) * 4;
             if (lane < kScales) {
-              scales[lane] = scale * p.scale_log2;
+              scales[0] = scale * p.scale_log2;
             } else if (lane < 2 * kScales) {
               // (the sum takes 2^-log2 of the same rounded logarithm, which drops out)
               const float log = __log2f(scale);
-              scales[lane] = log;
-              scales[kScales + lane] = live ? ex2_approx(-log) : 0.f;
+              scales[1] = log;
+              scales[2] = live ? ex2_approx(-log) : 0.f;
             }
             mbar_arrive_warp(BAR(L::SCALES + kvpos % kScaleTiles));
             ++kvpos;
@@ -917,8 +946,11 @@ __global__ void __launch_bounds__(Launch<FP8>::kThreads, 1)
         const SDesc vdesc0 = sdesc_sw128(sbase + L::kRingOff, 1024, CB * 1024);
         constexpr uint32_t kTileUnits = L::kTileBytes >> 4;
         auto issue_s = [&](int t, uint32_t slot) {
-          const SDesc qd = qdesc0 + static_cast<uint32_t>(DUAL ? 0 : t) * kTileUnits;
-          const SDesc kd = kdesc0 + slot * (FP8 ? kTileUnits / 2 : kTileUnits);
+          SDesc qd = qdesc0 + static_cast<uint32_t>(DUAL ? 0 : t) * kTileUnits;
+          SDesc kd = kdesc0 + slot * (FP8 ? kTileUnits / 2 : kTileUnits);
+          // (each step's own descriptors are an addition here, not registers kept
+          // for all steps of both tiles, of which there are too few)
+          if constexpr (FP8) asm volatile("" : "+r"(qd.lo), "+r"(kd.lo));
           if constexpr (FP8) {
 #pragma unroll
             for (int part = 0; part < 2; ++part)  // hi, lo
@@ -937,7 +969,8 @@ __global__ void __launch_bounds__(Launch<FP8>::kThreads, 1)
           }
         };
         auto issue_pv = [&](int t, uint32_t slot, bool acc) {
-          const SDesc vd = vdesc0 + slot * kTileUnits;
+          SDesc vd = vdesc0 + slot * kTileUnits;
+          if constexpr (FP8) asm volatile("" : "+r"(vd.lo));
 #pragma unroll
           for (int ks = 0; ks < 8; ++ks) {
             umma_ts(tmem + L::kColO + static_cast<uint32_t>(t * D), tmem + static_cast<uint32_t>(t * 128 + ks * 8),
@@ -1149,7 +1182,7 @@ __global__ void __launch_bounds__(Launch<FP8>::kThreads, 1)
               if (!ok) break;
               ++qn[t];
               const uint32_t qt = sbase + t * L::kTileBytes + (chunk >> 3) * 16384;
-              constexpr int RPI = 32 / LPR, IN = 16;  // rows an instruction, instructions looked up at once
+              constexpr int RPI = 32 / LPR, IN = FP8 ? 8 : 16;  // rows an instruction, instructions looked up at once
 #pragma unroll 1
               for (int i0 = lane / LPR; i0 < kRows; i0 += RPI * IN) {
                 uint32_t at[IN];
@@ -1232,31 +1265,31 @@ __global__ void __launch_bounds__(Launch<FP8>::kThreads, 1)
           const uint32_t dst = sbase + L::kRingOff + vs * L::kTileBytes;
           const int left = limit - j * kRows;  // rows behind the last key may hold anything
           constexpr int CHUNKS = D / 16;       // 16-byte chunks of a row
-          constexpr int EACH = kRows * CHUNKS / 128;
+          constexpr int EACH = kRows * CHUNKS / 128, AT_ONCE = 4;
           // eight lanes take a chunk of eight rows, which lie in different banks
           // on both sides
-          uint32_t x[EACH][4];
+#pragma unroll 1
+          for (int i0 = 0; i0 < EACH; i0 += AT_ONCE) {
+            uint32_t x[AT_ONCE][4];
 #pragma unroll
-          for (int i = 0; i < EACH; ++i) {
-            const int item = (sub * EACH + i) * 4 + (lane >> 3);
-            ld_shared_v4(src + byte_chunk<D>(item / CHUNKS * 8 + (lane & 7), item % CHUNKS), x[i]);
+            for (int i = 0; i < AT_ONCE; ++i) {
+              const int item = (sub * EACH + i0 + i) * 4 + (lane >> 3);
+              ld_shared_v4(src + byte_chunk<D>(item / CHUNKS * 8 + (lane & 7), item % CHUNKS), x[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < AT_ONCE; ++i) {
+              const int item = (sub * EACH + i0 + i) * 4 + (lane >> 3);
+              const int row = item / CHUNKS * 8 + (lane & 7), c = item % CHUNKS * 2;
+              const bool live = row < left;
+              uint32_t h[8];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) e4m3x4_to_f16(live ? x[i][k] : 0u, h[2 * k], h[2 * k + 1]);
+              const uint32_t at = dst + ((row >> 3) * CB + (c >> 3)) * 1024;
+              st_shared_v4(at + sw128(row & 7, c & 7), h[0], h[1], h[2], h[3]);
+              st_shared_v4(at + sw128(row & 7, (c & 7) + 1), h[4], h[5], h[6], h[7]);
+            }
           }
           mbar_arrive_warp(BAR(L::RAW_EMPTY + rs));
-#pragma unroll
-          for (int i = 0; i < EACH; ++i) {
-            const int item = (sub * EACH + i) * 4 + (lane >> 3);
-            const int row = item / CHUNKS * 8 + (lane & 7), c = item % CHUNKS * 2;
-            const bool live = row < left;
-            uint32_t h[8];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              e4m3x4_to_f16(x[i][k], h[2 * k], h[2 * k + 1]);
-              if (!live) h[2 * k] = h[2 * k + 1] = 0u;
-            }
-            const uint32_t at = dst + ((row >> 3) * CB + (c >> 3)) * 1024;
-            st_shared_v4(at + sw128(row & 7, c & 7), h[0], h[1], h[2], h[3]);
-            st_shared_v4(at + sw128(row & 7, (c & 7) + 1), h[4], h[5], h[6], h[7]);
-          }
           fence_proxy_async_smem();
           mbar_arrive_warp(BAR(L::V_FULL + vs));
         }
