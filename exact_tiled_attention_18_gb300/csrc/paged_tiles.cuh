@@ -184,10 +184,10 @@ struct TileLayout {
   static constexpr int kSmemBytes = kLineOff + (kTileLine + 1) * 4 + 1024;
   static constexpr uint32_t kColO = 256;
   static_assert(kSmemBytes <= 227 * 1024, "shared memory of a CTA");
-  // Scales are written behind the wait for a raw slot, which is free once the
-  // tile kRawSlots before it is converted, and so the weights of the one
-  // kValueSlots before that are there.
-  static_assert(!FP8 || kRawSlots + kValueSlots <= kScaleTiles, "scales still in use");
+  // Scales are written behind the wait for a key slot, which is free once the
+  // scores of the tile kKeySlots before it are there, and so the weights of the
+  // row tile's one before that (DUAL: two before it).
+  static_assert(!FP8 || kKeySlots + 2 <= kScaleTiles, "scales still in use");
 };
 static_assert(sizeof(Piece) <= 48, "a piece's room");
 
@@ -833,6 +833,19 @@ __global__ void __launch_bounds__(Launch<FP8>::kThreads, 1)
           return i < count && key < last ? pages[key / p.table.page_size] : -1;
         };
         int cur = page_of(lane), next = page_of(32 + lane);
+        // a lane's scale of a tile: of keys' groups of 16, then of values'; 1 for a
+        // group of no page.  Loaded a tile ahead.
+        const int group = lane % kScales;
+        auto scale_of = [&](int j, int pages_of_32) {
+          const int page = __shfl_sync(0xffffffffu, pages_of_32, (j * boxes + group * kScaleTokens / p.box_rows) % 32);
+          const int key = first + j * kRows + group * kScaleTokens;
+          if (lane >= 2 * kScales || j >= tiles || key >= last || page < 0 || page >= p.table.num_pages) return 0.f;
+          const long long cell = (static_cast<long long>(page) * Hkv + head) * (p.table.page_size / kScaleTokens) +
+                                 key % p.table.page_size / kScaleTokens;
+          return (lane < kScales ? p.k_scales : p.v_scales)[cell];
+        };
+        [[maybe_unused]] float scale_ahead = 0.f;
+        if constexpr (FP8) scale_ahead = scale_of(0, cur);
         const int tell = max(0, tiles - kTellTiles);
         for (int j = 0; j < tiles && ok; ++j) {
           if (j == tell && lane == 0) mbar_arrive(BAR(L::LOADED));
@@ -851,19 +864,8 @@ __global__ void __launch_bounds__(Launch<FP8>::kThreads, 1)
           }
           const int row = key % p.table.page_size;
           if constexpr (FP8) {
-            // a lane's scale of the tile: of keys' groups of 16, then of values'; a
-            // group of no page has one of no effect
-            const int group = lane % kScales;
-            const int scale_page = __shfl_sync(0xffffffffu, cur, (j * boxes + group * kScaleTokens / p.box_rows) % 32);
-            const int scale_key = first + j * kRows + group * kScaleTokens;
-            float scale = 1.f;
-            bool live = false;
-            if (lane < 2 * kScales && scale_key < last && scale_page >= 0 && scale_page < p.table.num_pages) {
-              const long long cell = (static_cast<long long>(scale_page) * Hkv + head) * (p.table.page_size / kScaleTokens) +
-                                     scale_key % p.table.page_size / kScaleTokens;
-              scale = (lane < kScales ? p.k_scales : p.v_scales)[cell];
-              live = true;
-            }
+            const float scale = scale_ahead;
+            scale_ahead = scale_of(j + 1, (j + 1) * boxes % 32 == 0 ? next : cur);
             const bool skip = blockIdx.x == 0 && static_cast<int>(n) == p.stall_unit && j == 0;  // testing hook
             const uint32_t ks = kvpos % KSL, vs = kvpos % RSL;
             ok = tile_wait(BAR(L::K_EMPTY + ks), ((kvpos / KSL) & 1) ^ 1, wc, SITE_TILE_LOAD, n);
@@ -877,6 +879,16 @@ __global__ void __launch_bounds__(Launch<FP8>::kThreads, 1)
                                  row, outer, policy);
               __syncwarp();
             }
+            float* scales = reinterpret_cast<float*>(smem + L::kScaleOff) + (kvpos % kScaleTiles * kScales + group) * 4;
+            if (lane < kScales) {
+              scales[0] = (scale != 0.f ? scale : 1.f) * p.scale_log2;
+            } else if (lane < 2 * kScales) {
+              // (the sum takes 2^-log2 of the same rounded logarithm, which drops out)
+              const float log = scale != 0.f ? __log2f(scale) : 0.f;
+              scales[1] = log;
+              scales[2] = scale != 0.f ? ex2_approx(-log) : 0.f;
+            }
+            mbar_arrive_warp(BAR(L::SCALES + kvpos % kScaleTiles));
             ok = tile_wait(BAR(L::RAW_EMPTY + vs), ((kvpos / RSL) & 1) ^ 1, wc, SITE_TILE_LOAD, n);
             if (!ok) break;
             if (lane == 0) mbar_arrive_expect_tx(BAR(L::RAW_FULL + vs), L::kTileBytes / 2);
@@ -884,16 +896,6 @@ __global__ void __launch_bounds__(Launch<FP8>::kThreads, 1)
             if (loads)
               tma_load_3d_hint(sbase + L::kRawOff + vs * (L::kTileBytes / 2) + offset, &tm_v, BAR(L::RAW_FULL + vs), 0,
                                row, outer, policy);
-            float* scales = reinterpret_cast<float*>(smem + L::kScaleOff) + (kvpos % kScaleTiles * kScales + group) * 4;
-            if (lane < kScales) {
-              scales[0] = scale * p.scale_log2;
-            } else if (lane < 2 * kScales) {
-              // (the sum takes 2^-log2 of the same rounded logarithm, which drops out)
-              const float log = __log2f(scale);
-              scales[1] = log;
-              scales[2] = live ? ex2_approx(-log) : 0.f;
-            }
-            mbar_arrive_warp(BAR(L::SCALES + kvpos % kScaleTiles));
             ++kvpos;
           } else {
 #pragma unroll 1
