@@ -3,35 +3,39 @@
 //
 // A stored key or value is its E4M3 number times the scale of its 16 tokens
 // and head.  With scores z_j = scale * sk_j (q . k_j) and weights p_j = 2^z_j the
-// row is O = sum p_j sv_j v_j / sum p_j.  Both products run on E4M3 numbers as they
-// lie in the cache (mma of 32 keys or columns at once, fp32 sums), so nothing of
-// the cache is converted:
+// row is O = sum p_j sv_j v_j / sum p_j.  Both products run on fp16 (mma with fp32
+// sums), in which every E4M3 number is exact, with the scales outside:
 //
-//  - A query row, times a power of two that brings its largest value into [128,
-//    256), is the sum of two E4M3 numbers, q = hi + lo / 32.  hi takes the leading
-//    four significand bits, lo the next four: all eight of a bf16 value down to
-//    2^-21 of the row's largest, whose products are summed apart and put together in fp32.
+//  - A query row is taken times a power of two that brings its largest value into
+//    [2^14, 2^15): exact but for elements below 2^-28 of it.
 //  - The exponent of a weight takes the values' scale in: x_j = z_j + log2 sv_j, and
-//    w_j = 2^(x_j - max x + 8) with the maximum over the tile's 128 keys, so a tile's
-//    largest weight is 2^8 of E4M3's 448.  The weights too are sums of E4M3
-//    numbers: three up to 16 rows (12 significand bits), two with more (8, as the
-//    bf16 weights of the other kernels), and 2^-18 of the tile's largest at the
-//    least.  A tile's product is then scaled into the row's accumulator, which
-//    is in units of 2^(largest x so far).  The sum of the p_j takes w_j / sv_j.
+//    w_j = 2^(x_j - max x + 14) with the maximum over the tile's 128 keys, in 11
+//    significand bits, and 2^-39 of the tile's largest at the least.  The row's
+//    accumulator follows: it is in units of 2^(the last tile's maximum), or of 2^-60
+//    times the largest so far where that is more (what a tile adds below that is
+//    nothing).  The sum of the p_j takes w_j / sv_j.
+//
+// (mma on E4M3 operands is no instruction of this GPU's but a dozen conversions to
+// fp16 around two of fp16, done again for every use of a fragment: 8 sequences x 8
+// heads x 8192 keys 35 us with up to 8 rows and 61 with 16 that way.)
 //
 // paged_steps_fp8_kernel: the work is divided as in paged_steps_kernel (paged.cu),
 // with tiles of 128 keys, the same number of bytes.  Each compute warp multiplies
 // the rows with its 32 keys, the warps agree on the tile's row maxima, exchange
 // the weights through shared memory, and each multiplies all 128 keys with its
 // quarter of the value columns.  The transposed value fragments come by ldmatrix
-// of 16 x 16 bytes.  A lane's four keys of the score product are those of one word
-// of the weights' fragments: key 8 j + (i ^ 2 j), j < 4, of a warp's 32 for line i
-// of the fragments, an order in which the rows that one ldmatrix phase reads lie
-// in different banks for keys and values both.
+// of 16 x 16 bytes.  Fragments are converted where they are: a word holds four
+// numbers in a row, which become two pairs, so an mma's 16 columns are taken in the
+// order 0 1 4 5 8 9 12 13 2 3 6 7 10 11 14 15 on both sides.  A lane's four keys of
+// the score product are those of one word of the value fragments: key 8 j + (i ^
+// 2 j), j < 4, of a warp's 32 for line i of the fragments, an order in which the
+// rows that one ldmatrix phase reads lie in different banks for keys and values
+// both.
 #include <cuda_runtime.h>
 #include <math_constants.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "internal.h"
 #include "paged.cuh"
@@ -56,18 +60,15 @@ struct StepLayout {
   static constexpr int kStage = 2 * kHalf;
   static constexpr bool kMany = RB > 2;   // 17 rows or more
   static constexpr int kStages = (RB == 2 ? 3 : 2) * (128 / D);
-  static constexpr int kTerms = kMany ? 2 : 3;  // E4M3 numbers a weight
-  // weights: [term][8 RB rows][128 keys] and 16 bytes more a row, so that rows
+  // weights: [8 RB rows][128 keys] fp16 and 16 bytes more a row, so that rows
   // begin in different banks
-  static constexpr int kPRow = kKeys + 16;
+  static constexpr int kPRow = 2 * kKeys + 16;
   static constexpr int kPOff = kStages * kStage;
-  static constexpr int kPTerm = 8 * RB * kPRow;
-  // queries (17 rows or more): [hi, lo][8 RB rows][d] and 16 bytes more a row, then
-  // the rows' multipliers
-  static constexpr int kQRow = D + 16;
-  static constexpr int kQOff = kPOff + kTerms * kPTerm;
-  static constexpr int kQTerm = kMany ? 8 * RB * kQRow : 0;
-  static constexpr int kCqOff = kQOff + 2 * kQTerm;
+  // queries (17 rows or more): [8 RB rows][d] fp16 and 16 bytes more a row, then the
+  // rows' multipliers
+  static constexpr int kQRow = 2 * D + 16;
+  static constexpr int kQOff = kPOff + 8 * RB * kPRow;
+  static constexpr int kCqOff = kQOff + (kMany ? 8 * RB * kQRow : 0);
   // a stage's scales: of the keys' groups of 16, then of the values'
   static constexpr int kScaleOff = kCqOff + (kMany ? 8 * RB * 4 : 0);
   static constexpr int kBarOff = kScaleOff + kStages * 2 * kTileScales * 4;  // FULL[s] then EMPTY[s]
@@ -79,7 +80,8 @@ struct StepLayout {
   static_assert(step_ctas_per_sm<RB>() * (kSmemBytes + 1024) <= 228 * 1024, "resident CTAs an SM");
 };
 
-// Byte offset of 16-byte chunk c of key r in a tile.
+// Byte offset of 16-byte chunk c of key r in a tile.  Chunk c's is chunk 0's XOR
+// 16 c, also behind the tile's 1024-byte aligned address.
 template <int D>
 __device__ __forceinline__ uint32_t row_chunk(int r, int c) {
   return D == 128 ? sw128(r, c) : sw64(r, c);
@@ -87,27 +89,26 @@ __device__ __forceinline__ uint32_t row_chunk(int r, int c) {
 
 // Two 16 x 16 matrices of bytes, transposed: words 0 and 1 of lane 4 c + i are
 // bytes c and c + 8 of rows 4 i to 4 i + 3 of the first, 2 and 3 of the second.
+template <int OFF>
 __device__ __forceinline__ void ldmatrix2_t8(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0,%1,%2,%3}, [%4];"
+  asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0,%1,%2,%3}, [%4+%5];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
+               : "r"(addr), "n"(OFF)
                : "memory");
 }
 
-// c (16 x 8, fp32) += a (16 x 32) b (32 x 8), E4M3
-__device__ __forceinline__ void mma_e4m3(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+// c (16 x 8, fp32) += a (16 x 16) b (16 x 8), fp16
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
-      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// v less its four E4M3 numbers in `packed`.
-__device__ __forceinline__ void less_e4m3x4(float (&v)[4], uint32_t packed) {
-  float x[4];
-  unpack_e4m3x4(packed, x);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] -= x[i];
+// The fp16 fragment of 16 columns from words of lines fr and fr + 8.
+__device__ __forceinline__ void widen(uint32_t (&a)[4], uint32_t upper, uint32_t lower) {
+  e4m3x4_to_f16(upper, a[0], a[2]);
+  e4m3x4_to_f16(lower, a[1], a[3]);
 }
 
 // 4 bytes global -> shared without registers; `bytes` 0 writes zeros.
@@ -127,8 +128,7 @@ __global__ void __launch_bounds__(kStepThreads, step_ctas_per_sm<RB>())
                            const __grid_constant__ PagedStep p) {
   using L = StepLayout<D, RB>;
   constexpr int S = L::kStages;
-  constexpr int T = L::kTerms;
-  constexpr int KS = D / 32;       // steps of the score product
+  constexpr int KS = D / 16;       // steps of the score product
   constexpr int MT = D / 64;       // 16-column tiles of a warp's quarter of the values
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -285,74 +285,67 @@ __global__ void __launch_bounds__(kStepThreads, step_ctas_per_sm<RB>())
   const int rows = p.seq.G * p.seq.Nq;
   auto key_at = [](int i, int j) { return 8 * j + (i ^ (2 * j)); };  // of a warp's 32
   // ldmatrix lane addresses: keys (two groups of 16 rows), values
-  uint32_t k_row[2];
+  uint32_t k_off[2];
 #pragma unroll
-  for (int g = 0; g < 2; ++g) k_row[g] = kWarpKeys * warp + key_at(lane & 7, 2 * g + ((lane >> 3) & 1));
-  const int k_half = lane >> 4;
-  const int v_row = key_at(lane >> 2, lane & 3);
+  for (int g = 0; g < 2; ++g)
+    k_off[g] = row_chunk<D>(kWarpKeys * warp + key_at(lane & 7, 2 * g + ((lane >> 3) & 1)), lane >> 4);
   const int v_col = warp * (D / 4);  // first value column of this warp
-  const uint32_t p_at = sbase + L::kPOff;
+  const uint32_t v_off = row_chunk<D>(key_at(lane >> 2, lane & 3), v_col / 16);
+  // weights: where the lane's four keys of row fc go, and 8 keys of a row for the
+  // product
+  const uint32_t p_store = sbase + L::kPOff + fc * L::kPRow + 2 * kWarpKeys * warp + 32 * (fr >> 2) + 4 * (fr & 3);
+  const uint32_t p_load = sbase + L::kPOff + (lane & 7) * L::kPRow + 16 * (lane >> 3);
   constexpr bool MANY = L::kMany;
   constexpr int QB = MANY ? 1 : RB;  // blocks of rows whose queries a warp loads: one, for all warps, or all
-  uint32_t qh[QB][KS][2], ql[QB][KS][2];
-  uint2 raw[QB][KS][2];
+  uint32_t qf[QB][KS][2];
+  uint2 raw[QB][KS];
   float cq[QB][2];                 // what a score of rows fc, fc + 1 is multiplied by
   float* cq_shared = reinterpret_cast<float*>(smem + L::kCqOff);
+  [[maybe_unused]] const uint32_t q_load = sbase + L::kQOff + (lane & 7) * L::kQRow + 16 * (lane >> 3);
   auto load_q = [&](const Walk& x) {
     const uint16_t* base = p.q + (static_cast<size_t>(x.e) * p.seq.Hkv + x.head) * rows * D + 2 * fc;
 #pragma unroll
     for (int m = 0; m < QB; ++m) {
       const int row = 8 * (MANY ? warp : m) + fr;
-      const uint16_t* src = base + min(row, rows - 1) * D;  // rows of the block behind the last see no key
+      const uint16_t* src = base + min(row, rows - 1) * D;  // rows of the block behind the last are not kept
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) raw[m][ks][h] = *reinterpret_cast<const uint2*>(src + 32 * ks + 16 * h);
+      for (int ks = 0; ks < KS; ++ks) raw[m][ks] = *reinterpret_cast<const uint2*>(src + 16 * ks);
     }
   };
-  // hi and lo of the rows, and their multipliers; an infinity or a NaN in a row
-  // makes its multiplier a NaN.  17 rows or more: into shared memory, when every
-  // warp is through with the last ones.
-  auto split_q = [&]() {
+  // the rows in fp16, and their multipliers; an infinity or a NaN in a row makes
+  // its multiplier a NaN.  17 rows or more: into shared memory, when every warp is
+  // through with the last ones.
+  auto scale_q = [&]() {
 #pragma unroll
     for (int m = 0; m < QB; ++m) {
       uint32_t top = 0;            // the largest magnitude's bits
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint2 x = raw[m][ks][h];
-          top = max(top, max(max((x.x << 16) & 0x7fffffffu, x.x & 0x7fff0000u),
-                             max((x.y << 16) & 0x7fffffffu, x.y & 0x7fff0000u)));
-        }
+      for (int ks = 0; ks < KS; ++ks) {
+        const uint2 x = raw[m][ks];
+        top = max(top, max(max((x.x << 16) & 0x7fffffffu, x.x & 0x7fff0000u),
+                           max((x.y << 16) & 0x7fffffffu, x.y & 0x7fff0000u)));
+      }
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      const uint32_t e = max(top >> 23, 8u);  // the exponent's field
-      const float up = __uint_as_float((261u - e) << 23);
-      const float mine = e == 255u ? CUDART_NAN_F : __uint_as_float((e - 7u) << 23) * p.scale_log2;
+      const uint32_t e = max(top >> 23, 15u);  // the exponent's field
+      const float up = __uint_as_float((268u - e) << 23);
+      const float mine = e == 255u ? CUDART_NAN_F : __uint_as_float((e - 14u) << 23) * p.scale_log2;
 #pragma unroll
       for (int i = 0; i < 2; ++i) cq[m][i] = __shfl_sync(0xffffffffu, mine, 4 * (fc + i));
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint2 x = raw[m][ks][h];
-          float v[4] = {__uint_as_float(x.x << 16) * up, __uint_as_float(x.x & 0xFFFF0000u) * up,
-                        __uint_as_float(x.y << 16) * up, __uint_as_float(x.y & 0xFFFF0000u) * up};
-          qh[m][ks][h] = pack_e4m3x4(v[0], v[1], v[2], v[3]);
-          less_e4m3x4(v, qh[m][ks][h]);
-          ql[m][ks][h] = pack_e4m3x4(v[0] * 32.f, v[1] * 32.f, v[2] * 32.f, v[3] * 32.f);
-        }
+      for (int ks = 0; ks < KS; ++ks) {
+        const uint2 x = raw[m][ks];
+        qf[m][ks][0] = pack_f16x2(__uint_as_float(x.x << 16) * up, __uint_as_float(x.x & 0xFFFF0000u) * up);
+        qf[m][ks][1] = pack_f16x2(__uint_as_float(x.y << 16) * up, __uint_as_float(x.y & 0xFFFF0000u) * up);
+      }
       if constexpr (MANY) {
         if (warp < RB) {
           const uint32_t dst = sbase + L::kQOff + (8 * warp + fr) * L::kQRow + 2 * fc;
 #pragma unroll
-          for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              st_shared_u32(dst + 32 * ks + 16 * h, qh[m][ks][h]);
-              st_shared_u32(dst + L::kQTerm + 32 * ks + 16 * h, ql[m][ks][h]);
-            }
+          for (int ks = 0; ks < KS; ++ks) {
+            st_shared_u32(dst + 32 * ks, qf[m][ks][0]);
+            st_shared_u32(dst + 32 * ks + 16, qf[m][ks][1]);
+          }
           if ((lane & 3) == 0) cq_shared[8 * warp + fr] = mine;
         }
         warps_sync();
@@ -371,9 +364,9 @@ __global__ void __launch_bounds__(kStepThreads, step_ctas_per_sm<RB>())
   while (more && ok) {
     const int lq = len_q[w.e], lk = len_k[w.e];
     int kend[RB][2];               // last visible key + 1 of rows fc, fc + 1
-    // the largest x so far; the sum of the p_j and the accumulators, in units of 2^(ref - 8)
+    // the largest x so far; the sum of the p_j and the accumulators, in units of 2^(ref - 14)
     float top[RB][2], ref[RB][2], l[RB][2], acc[RB][MT][4];
-    split_q();
+    scale_q();
 #pragma unroll
     for (int m = 0; m < RB; ++m) {
 #pragma unroll
@@ -388,6 +381,8 @@ __global__ void __launch_bounds__(kStepThreads, step_ctas_per_sm<RB>())
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[m][n][e] = 0.f;
     }
+    // keys that every query of the sequence sees (rows behind the last may see any)
+    const int all_see = lq < p.seq.Nq ? 0 : p.causal ? lk - lq + 1 : lk;
     Walk after = w;
     int after_at = at;
     const bool another = walk_next(after, starts, p.seq.Hkv, after_at, stop);
@@ -397,6 +392,7 @@ __global__ void __launch_bounds__(kStepThreads, step_ctas_per_sm<RB>())
       const uint32_t kb = sbase + s * L::kStage;
       const uint32_t vb = kb + L::kHalf;
       const int key0 = p.seq.prefix_len + t * kKeys;
+      const bool edge = key0 + kKeys > all_see;
       // x of this warp's 32 keys: [group][row block][key line fr of its first (0, 1) and second 8 keys]
       float x[2][RB][4], isv[2];
       if (__all_sync(0xffffffffu, full)) {
@@ -405,33 +401,27 @@ __global__ void __launch_bounds__(kStepThreads, step_ctas_per_sm<RB>())
         const float2 sv = *reinterpret_cast<const float2*>(sc + kTileScales);
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
-          float hi[RB][4], lo[RB][4];
+          float sc[RB][4];
 #pragma unroll
           for (int m = 0; m < RB; ++m)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) hi[m][e] = lo[m][e] = 0.f;
+            for (int e = 0; e < 4; ++e) sc[m][e] = 0.f;
 #pragma unroll
           for (int ks = 0; ks < KS; ks += 2) {
-            uint32_t kf[2][4];
-            ldmatrix4(kf[0], kb + row_chunk<D>(k_row[g], 2 * ks + k_half));
-            ldmatrix4(kf[1], kb + row_chunk<D>(k_row[g], 2 * ks + 2 + k_half));
+            uint32_t w8[4], kf[2][4];
+            ldmatrix4(w8, (kb + k_off[g]) ^ (16 * ks));
+            widen(kf[0], w8[0], w8[1]);
+            widen(kf[1], w8[2], w8[3]);
 #pragma unroll
             for (int m = 0; m < RB; ++m) {
               if constexpr (MANY) {
-                const uint32_t src = sbase + L::kQOff + (8 * m + (lane & 7)) * L::kQRow + 32 * ks + 16 * (lane >> 3);
                 uint32_t qv[4];
-                ldmatrix4(qv, src);
-                mma_e4m3(hi[m], kf[0], qv[0], qv[1]);
-                mma_e4m3(hi[m], kf[1], qv[2], qv[3]);
-                ldmatrix4(qv, src + L::kQTerm);
-                mma_e4m3(lo[m], kf[0], qv[0], qv[1]);
-                mma_e4m3(lo[m], kf[1], qv[2], qv[3]);
+                ldmatrix4(qv, q_load + (8 * m * L::kQRow + 32 * ks));
+                mma_f16(sc[m], kf[0], qv[0], qv[1]);
+                mma_f16(sc[m], kf[1], qv[2], qv[3]);
               } else {
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                  mma_e4m3(hi[m], kf[h], qh[m][ks + h][0], qh[m][ks + h][1]);
-                  mma_e4m3(lo[m], kf[h], ql[m][ks + h][0], ql[m][ks + h][1]);
-                }
+                mma_f16(sc[m], kf[0], qf[m][ks][0], qf[m][ks][1]);
+                mma_f16(sc[m], kf[1], qf[m][ks + 1][0], qf[m][ks + 1][1]);
               }
             }
           }
@@ -448,9 +438,11 @@ __global__ void __launch_bounds__(kStepThreads, step_ctas_per_sm<RB>())
               c = make_float2(cq[m][0], cq[m][1]);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const float z = fmaf(fmaf(lo[m][e], 0.03125f, hi[m][e]), (e & 1 ? c.y : c.x) * kscale, lsv);
-              const int j = key0 + kWarpKeys * warp + key_at(fr, 2 * g + (e >> 1));
-              x[g][m][e] = j < kend[m][e & 1] ? z : -CUDART_INF_F;
+              x[g][m][e] = fmaf(sc[m][e], (e & 1 ? c.y : c.x) * kscale, lsv);
+              if (edge) {
+                const int j = key0 + kWarpKeys * warp + key_at(fr, 2 * g + (e >> 1));
+                if (j >= kend[m][e & 1]) x[g][m][e] = -CUDART_INF_F;
+              }
             }
           }
         }
@@ -500,8 +492,8 @@ __global__ void __launch_bounds__(kStepThreads, step_ctas_per_sm<RB>())
           float sum = 0.f;
 #pragma unroll
           for (int g = 0; g < 2; ++g) {
-            wt[e][2 * g] = ex2_approx(x[g][m][e] - base + 8.f);
-            wt[e][2 * g + 1] = ex2_approx(x[g][m][2 + e] - base + 8.f);
+            wt[e][2 * g] = ex2_approx(x[g][m][e] - base + 14.f);
+            wt[e][2 * g + 1] = ex2_approx(x[g][m][2 + e] - base + 14.f);
             sum = fmaf(wt[e][2 * g] + wt[e][2 * g + 1], isv[g], sum);
           }
           l[m][e] = fmaf(l[m][e], f, sum);
@@ -510,36 +502,38 @@ __global__ void __launch_bounds__(kStepThreads, step_ctas_per_sm<RB>())
             acc[m][n][e] *= f;
             acc[m][n][2 + e] *= f;
           }
-#pragma unroll
-          for (int u = 0; u < T; ++u) {
-            const uint32_t word = pack_e4m3x4(wt[e][0], wt[e][1], wt[e][2], wt[e][3]);
-            st_shared_u32(p_at + u * L::kPTerm + (8 * m + fc + e) * L::kPRow + kWarpKeys * warp + 4 * fr, word);
-            if (u + 1 < T) less_e4m3x4(wt[e], word);
-          }
+          const uint32_t at = p_store + (8 * m + e) * L::kPRow;
+          st_shared_u32(at, pack_f16x2(wt[e][0], wt[e][1]));
+          st_shared_u32(at + 16, pack_f16x2(wt[e][2], wt[e][3]));
         }
       }
       warps_sync();
       // O^T += V^T W^T: all 128 keys, this warp's quarter of the columns
+      auto keys32 = [&](auto tag) {
+        constexpr int KK = decltype(tag)::value;
+        uint32_t vf[MT][2][4];
 #pragma unroll
-      for (int half = 0; half < kKeys / 64; ++half) {
-        uint32_t vf[2][MT][4];
+        for (int n = 0; n < MT; ++n) {
+          uint32_t w8[4];
+          ldmatrix2_t8<32 * KK * D>(w8, (vb + v_off) ^ (16 * n));
+          widen(vf[n][0], w8[0], w8[1]);
+          widen(vf[n][1], w8[2], w8[3]);
+        }
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int m = 0; m < RB; ++m) {
+          uint32_t pf[4];  // 32 keys of eight rows
+          ldmatrix4(pf, p_load + (8 * m * L::kPRow + 64 * KK));
 #pragma unroll
-          for (int n = 0; n < MT; ++n)
-            ldmatrix2_t8(vf[h][n], vb + row_chunk<D>(64 * half + 32 * h + v_row, v_col / 16 + n));
-#pragma unroll
-        for (int m = 0; m < RB; ++m)
-#pragma unroll
-          for (int u = 0; u < T; ++u) {
-            uint32_t pf[4];  // 64 keys of eight rows
-            ldmatrix4(pf, p_at + u * L::kPTerm + (8 * m + (lane & 7)) * L::kPRow + 64 * half + 16 * (lane >> 3));
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-              for (int n = 0; n < MT; ++n) mma_e4m3(acc[m][n], vf[h][n], pf[2 * h], pf[2 * h + 1]);
+          for (int n = 0; n < MT; ++n) {
+            mma_f16(acc[m][n], vf[n][0], pf[0], pf[1]);
+            mma_f16(acc[m][n], vf[n][1], pf[2], pf[3]);
           }
-      }
+        }
+      };
+      keys32(std::integral_constant<int, 0>{});
+      keys32(std::integral_constant<int, 1>{});
+      keys32(std::integral_constant<int, 2>{});
+      keys32(std::integral_constant<int, 3>{});
       __syncwarp();
       if (lane == 0) mbar_arrive(bars + 8 * (S + s));
     }
@@ -591,7 +585,7 @@ __global__ void __launch_bounds__(kStepThreads, step_ctas_per_sm<RB>())
         }
         if (warp == 0 && fr < 2 && valid) {
           const float all = odd ? sum.y : sum.x;
-          lse[r] = all != 0.f ? ((odd ? ref[m][1] : ref[m][0]) - 8.f + __log2f(all)) * unit : -CUDART_INF_F;
+          lse[r] = all != 0.f ? ((odd ? ref[m][1] : ref[m][0]) - 14.f + __log2f(all)) * unit : -CUDART_INF_F;
         }
       }
     };

@@ -604,13 +604,12 @@ fa_status fa_kv_append_fp8(const void* k, long long k_stride_b, long long k_stri
  * fa_fwd_paged and fa_fwd_shared_prefix over the cache in E4M3, with the same
  * workspaces.  Scales may be any positive finite fp32 numbers (of values that
  * a row sees together, within 2^60 of one another).
- *   With up to 32 rows a key head both products run on the E4M3 numbers: a query
- * is split into two of them (exact but for elements below 2^-15 of their row's
- * largest, which are off by at most 2^-22 of it), a weight into three (up to 16
- * rows: 12 significand bits) or two (8 bits).  With more rows, and against a
- * prefix, a query is split without a scale between its two numbers (exact but
- * for elements below 2^-9 of their row's largest: off by at most 2^-17 of it),
- * weights are rounded to fp16 and values multiplied as fp16, exactly.
+ *   With up to 32 rows a key head both products run on fp16, in which the E4M3
+ * numbers are exact, as is a query (taken times a power of two) but for elements
+ * below 2^-28 of their row's largest.  With more rows, and against a prefix, a
+ * query is the sum of two E4M3 numbers: exact but for elements below 2^-9 of their
+ * row's largest, which are off by at most 2^-17 of it.  Weights enter the product
+ * with the values in fp16 (11 significand bits) everywhere.
  *   A query row that holds an infinity or a NaN has O = NaN and LSE = NaN if it
  * sees a key, as has a row that sees a key stored as NaN.
  */
