@@ -32,8 +32,11 @@
 // blocks an SM 86.5.
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <climits>
+#include <type_traits>
 
+#include "internal.h"
 #include "ptx.cuh"
 #include "serving.h"
 
@@ -42,6 +45,8 @@ namespace {
 
 constexpr int kRopeThreads = 256;
 constexpr int kLowestScale = -32;  // a scale of the append's is at least 2^-32
+constexpr int kAppendStages = 6;   // heads whose values are on their way or in use, in the append into E4M3
+constexpr int kAppendStageBytes = 2 * kRopeThreads * 16;
 
 // A lane's 16 values of a head are RUNS runs of as many bytes as one load
 // takes, spread over the rotated part (or the part behind it) so that
@@ -311,13 +316,14 @@ __global__ void __launch_bounds__(kRopeThreads) append_kernel(const AppendArgs a
 // thread 16 values of a token as in append_kernel; the group's maximum goes
 // through shared memory, once for HEADS heads.
 template <int D>
-__global__ void __launch_bounds__(kRopeThreads) append_fp8_kernel(const AppendArgs a, const int heads_per_thread) {
+__global__ void __launch_bounds__(kRopeThreads, 3) append_fp8_kernel(const AppendArgs a, const int heads_per_thread) {
   constexpr int LANES = D / 16;
-  constexpr int RUNS = 2, HEADS = 4;
+  constexpr int RUNS = 2;
   constexpr int WARPS = D / 32;                  // of a cell's group
   constexpr int CELLS = kRopeThreads / D;        // a block
   constexpr uint32_t kFinite = 0x7f800000u;      // a finite number's magnitude is below it
-  __shared__ uint32_t s_max[2][HEADS][kRopeThreads / 32];
+  __shared__ uint32_t s_max[2][kRopeThreads / 32];
+  extern __shared__ __align__(16) uint8_t s_raw[];
   grid_trigger();
   const int group = threadIdx.x / D;
   const int row_in = threadIdx.x % D / LANES, c = threadIdx.x % LANES;
@@ -331,8 +337,9 @@ __global__ void __launch_bounds__(kRopeThreads) append_fp8_kernel(const AppendAr
   const int first = lk - lq;                     // the first new token's position; may be negative
   const long long cell0 = (static_cast<long long>(first >> 4) + (item - static_cast<long long>(b) * per_sequence)) * 16;
   const bool active = exists && lq > 0 && cell0 < lk;
+  if (!active) return;                           // the whole group: a cell behind its sequence's end
   const long long place = cell0 + row_in;
-  const bool fresh = active && place >= first && place < lk;
+  const bool fresh = place >= first && place < lk;
   const int t = static_cast<int>(place - first);
   const int hq = a.q ? a.Hq : 0;
   const int heads = hq + 2 * a.Hkv;
@@ -341,7 +348,7 @@ __global__ void __launch_bounds__(kRopeThreads) append_fp8_kernel(const AppendAr
   // the cell's first row in its page, or -1: before position 0, past the table's
   // end or in a page that does not exist
   long long row = -1, scale_at = 0;
-  if (active && h1 > hq && cell0 >= 0) {
+  if (h1 > hq && cell0 >= 0) {
     if (cell0 >= static_cast<long long>(a.table.max_pages) * a.table.page_size) {
       if (fresh && c == 0) record_bad_page(a.status, SITE_PAGE_PAST_TABLE, b, static_cast<int>(place));
     } else {
@@ -364,102 +371,159 @@ __global__ void __launch_bounds__(kRopeThreads) append_fp8_kernel(const AppendAr
                                           : static_cast<int>(place);
     set_angles(l, a.rope, position, 1.f);
   }
-  int round = 0;
-  for (int h = h0; h < h1; h += HEADS, round ^= 1) {
-    Raw<true> raw[HEADS];
-    float before[HEADS];                         // the cells' scales
-#pragma unroll
-    for (int u = 0; u < HEADS; ++u) {
-      const int g = h + u;
-      before[u] = 0.f;
-      if (g >= h1) continue;
-      const bool value = g >= hq + a.Hkv;
-      const int kh = g - hq - (value ? a.Hkv : 0);
-      if (fresh) {
-        const uint16_t* src = g < hq  ? a.q + b * a.qs.b + g * a.qs.h + t * a.qs.n
-                              : value ? a.v + b * a.vs.b + kh * a.vs.h + t * a.vs.n
-                                      : a.k + b * a.ks.b + kh * a.ks.h + t * a.ks.n;
-        raw[u] = load<true>(src, 0, l);
-      }
-      if (g >= hq && has_old)
-        before[u] = (value ? a.v_scales : a.k_scales)[scale_at + static_cast<long long>(kh) *
-                                                                     (a.table.page_size / kScaleTokens)];
+  // A thread's values of the heads to come are on their way to its own places in
+  // shared memory, up to kAppendStages heads' ahead.  Addresses go from head to
+  // head by additions: this kernel is bound by its instructions.
+  const uint32_t place_at = smem_u32(s_raw) + threadIdx.x * 16;
+  constexpr uint32_t kRing = kAppendStages * kAppendStageBytes;
+  const uint16_t* k0 = a.k + b * a.ks.b + t * a.ks.n + l.at;
+  const uint16_t* v0 = a.v + b * a.vs.b + t * a.vs.n + l.at;
+  const uint16_t* from = nullptr;                // of head f
+  long long from_step = 0;
+  int f = h0;
+  uint32_t in_at = 0;
+  auto begin_fetch = [&](int g) {                // g: the line's head that comes next
+    if (g < hq) {
+      from = a.q + b * a.qs.b + t * a.qs.n + l.at + g * a.qs.h;
+      from_step = a.qs.h;
+    } else if (g < hq + a.Hkv) {
+      from = k0 + (g - hq) * a.ks.h;
+      from_step = a.ks.h;
+    } else {
+      from = v0 + (g - hq - a.Hkv) * a.vs.h;
+      from_step = a.vs.h;
     }
+  };
+  auto fetch = [&]() {
+    if (fresh && f < h1) {
 #pragma unroll
-    for (int u = 0; u < HEADS; ++u) {
-      uint32_t top = 0;                          // the largest finite magnitude's bits
-      if (counts && h + u < h1) {
+      for (int k = 0; k < RUNS; ++k)
+        cp_async16(place_at + in_at + k * kRopeThreads * 16, from + k * l.step, 16u);
+    }
+    cp_async_commit();
+    ++f;
+    from += from_step;
+    if (f == hq || f == hq + a.Hkv) begin_fetch(f);
+    in_at = in_at + kAppendStageBytes == kRing ? 0 : in_at + kAppendStageBytes;
+  };
+  begin_fetch(h0);
+#pragma unroll 1
+  for (int s = 0; s < kAppendStages - 1; ++s) fetch();
+  uint32_t out_at = 0;
+  Raw<true> raw;
+  auto next = [&]() {                            // this thread's values of the next head
+    fetch();
+    cp_async_wait<kAppendStages - 1>();
+#pragma unroll
+    for (int k = 0; k < RUNS; ++k)
+      ld_shared_v4(place_at + out_at + k * kRopeThreads * 16, reinterpret_cast<uint32_t(&)[4]>(raw.w[4 * k]));
+    out_at = out_at + kAppendStageBytes == kRing ? 0 : out_at + kAppendStageBytes;
+  };
+  if (h0 < hq) {
+    uint16_t* to = a.q_out + ((static_cast<long long>(b) * a.Hq + h0) * a.N + t) * D;
+#pragma unroll 1
+    for (int h = h0; h < min(h1, hq); ++h, to += static_cast<long long>(a.N) * D) {
+      next();
+      if (!fresh) continue;
+      float v[16];
+      unpack<true>(raw, v);
+      turn(l, a.rope.interleaved, v);
+      store<true>(to, 0, l, pack<true>(v));
+    }
+  }
+  const int cells_of_page = a.table.page_size / kScaleTokens;
+  int round = 0;
+  // heads [begin, end) of keys or values
+  auto cells = [&](auto value_tag, int begin, int end) {
+    constexpr bool VALUE = decltype(value_tag)::value;
+    float* scale_to = (VALUE ? a.v_scales : a.k_scales) + (row >= 0 ? scale_at + static_cast<long long>(begin) * cells_of_page : 0);
+    uint8_t* to = (VALUE ? a.v_bytes : a.k_bytes) +
+                  (row >= 0 ? (row + row_in + static_cast<long long>(begin) * a.table.page_size) * D : 0);
+    const uint32_t* found = s_max[0] + group * WARPS;
+#pragma unroll 1
+    for (int h = begin; h < end; ++h, round ^= 1, scale_to += cells_of_page, to += a.table.page_size * D) {
+      const float before = has_old ? *scale_to : 0.f;
+      next();
+      uint32_t top = 0;                          // the largest magnitudes' bits, two side by side
+#pragma unroll
+      for (int i = 0; i < 8; ++i) top = __vmaxu2(top, raw.w[i] & 0x7fff7fffu);
+      top = max(top & 0xffff0000u, top << 16);
+      const bool odd = top >= kFinite;           // an infinity or a NaN among this thread's values
+      if (odd) {                                 // the largest finite one
+        top = 0;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const uint32_t x = (raw[u].w[i] << 16) & 0x7fffffffu, y = raw[u].w[i] & 0x7fff0000u;
+          const uint32_t x = (raw.w[i] << 16) & 0x7fffffffu, y = raw.w[i] & 0x7fff0000u;
           if (x < kFinite) top = max(top, x);
           if (y < kFinite) top = max(top, y);
         }
       }
-      top = __reduce_max_sync(0xffffffffu, top);
-      if (lane == 0) s_max[round][u][warp] = top;
-    }
-    __syncthreads();
+      top = __reduce_max_sync(0xffffffffu, counts ? top : 0u);
+      if (lane == 0) s_max[round][warp] = top;
+      // the group's threads
+      asm volatile("barrier.cta.sync %0, %1;" ::"r"(group + 1), "n"(D) : "memory");
+      if (row < 0) continue;
+      top = 0;
 #pragma unroll
-    for (int u = 0; u < HEADS; ++u) {
-      const int g = h + u;
-      if (g >= h1) break;
-      const bool value = g >= hq + a.Hkv;
-      float v[16];
-      if (fresh) {
-        unpack<true>(raw[u], v);
-        if (!value) turn(l, a.rope.interleaved, v);
-        if (g < hq) store<true>(a.q_out + ((static_cast<long long>(b) * a.Hq + g) * a.N + t) * D, 0, l, pack<true>(v));
-      }
-      if (g < hq || row < 0) continue;
-      uint32_t top = 0;
-#pragma unroll
-      for (int i = 0; i < WARPS; ++i) top = max(top, s_max[round][u][group * WARPS + i]);
-      const float largest = fminf(__uint_as_float(top) * (value ? 1.f : a.key_growth), 3.4028235e38f);
+      for (int i = 0; i < WARPS; ++i) top = max(top, found[round * (kRopeThreads / 32) + i]);
+      float largest = __uint_as_float(top);
+      if constexpr (!VALUE) largest = fminf(largest * a.key_growth, 3.4028235e38f);
       const uint32_t bits = __float_as_uint(largest);
-      // 448 = 1.75 * 2^8
-      const int e = max(static_cast<int>(bits >> 23) - 127 - 8 + ((bits & 0x7fffffu) > 0x600000u), kLowestScale);
-      const float need = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
-      const bool raised = has_old && need > before[u];
-      const float scale = has_old && !raised ? before[u] : need;
-      const float inverse = 1.f / scale;
-      const int kh = g - hq - (value ? a.Hkv : 0);
-      uint8_t* dst = (value ? a.v_bytes : a.k_bytes) + (row + static_cast<long long>(kh) * a.table.page_size + row_in) * D;
+      // 448 = 1.75 * 2^8: the exponent's field, one more above 1.75
+      const int e = max(static_cast<int>((bits + 0x1fffffu) >> 23) - 8, kLowestScale + 127);
+      float scale = __uint_as_float(static_cast<uint32_t>(e) << 23);
+      float inverse = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
+      const bool raised = has_old && scale > before;
+      if (has_old && !raised) {
+        scale = before;
+        inverse = __frcp_rn(before);
+      }
       if (fresh) {
+        float v[16];
+        unpack<true>(raw, v);
+        if constexpr (!VALUE) turn(l, a.rope.interleaved, v);
+        if (odd) {                               // E4M3 has no infinity
 #pragma unroll
-        for (int i = 0; i < 16; ++i)  // E4M3 has no infinity
-          v[i] = (__float_as_uint(v[i]) & 0x7fffffffu) < kFinite ? v[i] * inverse : __uint_as_float(0x7fc00000u);
+          for (int i = 0; i < 16; ++i)
+            if ((__float_as_uint(v[i]) & 0x7fffffffu) >= kFinite) v[i] = __uint_as_float(0x7fc00000u);
+        }
 #pragma unroll
-        for (int k = 0; k < RUNS; ++k)
-          *reinterpret_cast<uint2*>(dst + l.at + k * l.step) =
-              make_uint2(pack_e4m3x4(v[8 * k], v[8 * k + 1], v[8 * k + 2], v[8 * k + 3]),
-                         pack_e4m3x4(v[8 * k + 4], v[8 * k + 5], v[8 * k + 6], v[8 * k + 7]));
+        for (int k = 0; k < RUNS; ++k) {
+          const float* x = v + 8 * k;
+          *reinterpret_cast<uint2*>(to + l.at + k * l.step) =
+              make_uint2(pack_e4m3x4(x[0] * inverse, x[1] * inverse, x[2] * inverse, x[3] * inverse),
+                         pack_e4m3x4(x[4] * inverse, x[5] * inverse, x[6] * inverse, x[7] * inverse));
+        }
       } else if (old && raised) {
-        const float ratio = before[u] * inverse;
-        uint4 x = *reinterpret_cast<const uint4*>(dst + 16 * c);
+        const float ratio = before * inverse;
+        uint4 x = *reinterpret_cast<const uint4*>(to + 16 * c);
         x.x = scale_e4m3x4(x.x, ratio);
         x.y = scale_e4m3x4(x.y, ratio);
         x.z = scale_e4m3x4(x.z, ratio);
         x.w = scale_e4m3x4(x.w, ratio);
-        *reinterpret_cast<uint4*>(dst + 16 * c) = x;
+        *reinterpret_cast<uint4*>(to + 16 * c) = x;
       }
-      if (threadIdx.x % D == 0 && (!has_old || raised))
-        (value ? a.v_scales : a.k_scales)[scale_at + static_cast<long long>(kh) * (a.table.page_size / kScaleTokens)] =
-            scale;
+      if (threadIdx.x % D == 0 && (!has_old || raised)) *scale_to = scale;
     }
-  }
+  };
+  const int kv = hq + a.Hkv;
+  cells(std::false_type{}, max(h0, hq) - hq, min(h1, kv) - hq);
+  cells(std::true_type{}, max(h0, kv) - kv, h1 - kv);
+  cp_async_wait<0>();
 }
 
 // Heads per thread: as many as leave about a thousand threads for every SM,
 // so that a large call computes each angle for many heads and a call of few
 // tokens spreads its heads over the GPU; at most `most`: eight for the rotation,
-// all for the append, which looks its lengths and page up once a thread.  (d =
+// all for the append, which looks its lengths and page up once a thread, sixteen
+// for the one into E4M3, whose longer waits want more blocks.  (d =
 // 128, bf16, at most 4 / 8 / 16 heads a thread: rotation of 16 heads x 32768
 // tokens 42.8 / 43.5 / 44.7 us in a graph and 46.6 / 45.7 / 47.2 in eager calls, 8 x
 // 64 heads x 2048 82.0 / 82.6 / 84.0, smaller ones alike.  At most 8 / 16 / all: four
 // prompts of 2048 to 8192 tokens, 48 heads, 82 / - / 76; 4 x 48 heads x 8192
 // 132.9 / 127.1 / 128.5, 2 x 80 heads x 8192 111.1 / 107.3 / 108.3, 24 heads x 16384
-// 37.9 / 39.4 / 39.3, 48 heads x 4096 18.1 / 18.4 / 18.4.)
+// 37.9 / 39.4 / 39.3, 48 heads x 4096 18.1 / 18.4 / 18.4.  Into E4M3 the four
+// prompts 71 with 12 or all, 66 with 16.)
 int heads_per_thread(long long tokens, int lanes, int heads, int sms, int most) {
   long long n = tokens * lanes * heads / (static_cast<long long>(sms) * 1024);
   if (n < 1) n = 1;
@@ -503,9 +567,13 @@ cudaError_t launch_append_fp8_d(const AppendArgs& a, cudaStream_t stream) {
   constexpr int CELLS = kRopeThreads / D;
   const long long cells = static_cast<long long>(a.B) * ((a.N + kScaleTokens - 2) / kScaleTokens + 1);
   const int heads = (a.q ? a.Hq : 0) + 2 * a.Hkv;
-  const int per = heads_per_thread(cells * kScaleTokens, D / 16, heads, a.sms, heads);
+  const int per = heads_per_thread(cells * kScaleTokens, D / 16, heads, a.sms, 16);
   const dim3 grid(static_cast<unsigned>((cells + CELLS - 1) / CELLS), (heads + per - 1) / per);
-  append_fp8_kernel<D><<<grid, kRopeThreads, 0, stream>>>(a, per);
+  auto kern = append_fp8_kernel<D>;
+  static std::atomic<unsigned long long> ready{0};
+  const cudaError_t e = setup_kernel_once(kern, kAppendStages * kAppendStageBytes, 0, ready);
+  if (e != cudaSuccess) return e;
+  kern<<<grid, kRopeThreads, kAppendStages * kAppendStageBytes, stream>>>(a, per);
   return cudaGetLastError();
 }
 
