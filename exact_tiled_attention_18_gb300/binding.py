@@ -1081,7 +1081,7 @@ def _table_args(pool, block_table, seqlens_k, refs):
 def _out_ints(out, shapes, device, index):
     """int32 tensors of the shapes, made or checked; the first may have a row stride."""
     import torch
-    if out is None:
+    if out is None:  # (views of one allocation cost more than three)
         return tuple(torch.empty(s, dtype=torch.int32, device=device) for s in shapes)
     for k, (t, s) in enumerate(zip(out, shapes)):
         rows = t.dim() == 2 and (s[1] == 1 or t.stride(1) == 1) if k == 0 else t.is_contiguous()
