@@ -60,8 +60,8 @@
 //    at twice the rate of bf16.
 //  - Values become fp16, in which they are exact, and so do the weights (11
 //    significand bits, 2^7 at the reference): in E4M3 those far below the largest,
-//    many as they may be, would be lost.  Four more warps (12-15) convert a tile's
-//    values, and zero those behind the last key.
+//    many as they may be, would be lost.  Three more warps (12, 14, 15) convert a
+//    tile's values, and zero those behind the last key.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -87,7 +87,9 @@ struct Launch {
   static constexpr int kRegs = FP8 ? 128 : 168;
   static constexpr int kSoftmaxRegs = FP8 ? 184 : 192;
   static constexpr int kOtherRegs = FP8 ? 72 : 120;
-  static constexpr int kReaders = kThreads / 32 - 1;  // warps that follow the pieces: all but the one that works them out
+  // warps that follow the pieces: all but the one that works them out, and with
+  // E4M3 one that is idle
+  static constexpr int kReaders = kThreads / 32 - 1 - FP8;
   static_assert(2 * 128 * kSoftmaxRegs + (kThreads - 256) * kOtherRegs <= kThreads * kRegs,
                 "register split exceeds the launch allocation");
 };
@@ -102,6 +104,10 @@ constexpr int kTellTiles = 4;
 constexpr int kScales = kRows / kScaleTokens;  // scales of a tile's keys
 constexpr int kScaleTiles = 16;   // tiles whose scales are kept: more than lie between a tile's loads and its weights
 constexpr float kShift = 7.f;     // log2 of an fp16 weight at the reference
+// Warps that convert values: 12, 14 and 15, while 13, which would share the
+// issuer's scheduler, is idle.  (Two chunks of 1000 tokens, 256 sequences behind a
+// prefix, us: 380 and 259 with all four, 377 and 253 so.)
+constexpr int kConverters = 3;
 
 enum TileSite : int {
   SITE_TILE_LOAD = 75,
@@ -276,10 +282,10 @@ __global__ void __launch_bounds__(Launch<FP8>::kThreads, 1)
       }
       for (int s = 0; s < RSL; ++s) {
         mbar_init(bars + 8 * (L::RAW_FULL + s), 1);
-        mbar_init(bars + 8 * (L::RAW_EMPTY + s), 4);
+        mbar_init(bars + 8 * (L::RAW_EMPTY + s), kConverters);
       }
       for (int s = 0; s < VSL; ++s) {
-        mbar_init(bars + 8 * (L::V_FULL + s), 4);
+        mbar_init(bars + 8 * (L::V_FULL + s), kConverters);
         mbar_init(bars + 8 * (L::V_EMPTY + s), 1);
       }
       for (int s = 0; s < kScaleTiles; ++s) mbar_init(bars + 8 * (L::SCALES + s), 1);
@@ -520,6 +526,11 @@ __global__ void __launch_bounds__(Launch<FP8>::kThreads, 1)
       if (FP8 && lim0 <= 0) grow = 1.f;
       float m_ref = 0.f, l = 0.f, dl = 0.f;
       for (int j = 0; j < nt; ++j) {
+        [[maybe_unused]] const uint32_t at = base + (DUAL ? 2 * j + t : j);
+        if constexpr (FP8) {  // (there before the scores are)
+          ok = tile_wait(BAR(L::SCALES + at % kScaleTiles), (at / kScaleTiles) & 1, wc_idle, SITE_TILE_CONVERT, n);
+          if (!ok) break;
+        }
         ok = tile_wait(BAR(L::S_FULL + t), sn & 1, wc_idle, SITE_TILE_S, n);
         if (!ok) break;
         ++sn;
@@ -546,9 +557,6 @@ __global__ void __launch_bounds__(Launch<FP8>::kThreads, 1)
         float mt;
         [[maybe_unused]] uint32_t scales = 0;
         if constexpr (FP8) {
-          const uint32_t at = base + (DUAL ? 2 * j + t : j);
-          ok = tile_wait(BAR(L::SCALES + at % kScaleTiles), (at / kScaleTiles) & 1, wc, SITE_TILE_CONVERT, n);
-          if (!ok) break;
           scales = sbase + L::kScaleOff + at % kScaleTiles * kScales * 16;
           mt = -CUDART_INF_F;
 #pragma unroll
@@ -1253,9 +1261,9 @@ __global__ void __launch_bounds__(Launch<FP8>::kThreads, 1)
     } else if (FP8 && warp >= 12) {
       // ------------------------------------------------- values become fp16
       uint32_t pos = 0;
-      const int sub = warp - 12;
+      const int sub = warp == 12 ? 0 : warp - 13;
       bool ok = true;
-      for (uint32_t n = 0; next_piece(n, ok); ++n) {
+      for (uint32_t n = 0; warp != 13 && next_piece(n, ok); ++n) {
         const int tiles = pieces[n & 1].tiles;
         const int limit = pieces[n & 1].limit - pieces[n & 1].tile * kRows;  // keys from the piece's first on
         for (int j = 0; j < tiles; ++j, ++pos) {
@@ -1266,22 +1274,24 @@ __global__ void __launch_bounds__(Launch<FP8>::kThreads, 1)
           const uint32_t src = sbase + L::kRawOff + rs * (L::kTileBytes / 2);
           const uint32_t dst = sbase + L::kRingOff + vs * L::kTileBytes;
           const int left = limit - j * kRows;  // rows behind the last key may hold anything
-          constexpr int CHUNKS = D / 16;       // 16-byte chunks of a row
-          constexpr int EACH = kRows * CHUNKS / 128, AT_ONCE = 4;
-          // eight lanes take a chunk of eight rows, which lie in different banks
-          // on both sides
+          constexpr int CHUNKS = D / 16;         // 16-byte chunks of a row
+          constexpr int ITEMS = kRows * CHUNKS / 32, AT_ONCE = 4;
+          // an item is four chunks of eight rows: eight lanes take a chunk of eight
+          // rows, which lie in different banks on both sides
 #pragma unroll 1
-          for (int i0 = 0; i0 < EACH; i0 += AT_ONCE) {
+          for (int i0 = sub; i0 < ITEMS; i0 += kConverters * AT_ONCE) {
             uint32_t x[AT_ONCE][4];
 #pragma unroll
             for (int i = 0; i < AT_ONCE; ++i) {
-              const int item = (sub * EACH + i0 + i) * 4 + (lane >> 3);
-              ld_shared_v4(src + byte_chunk<D>(item / CHUNKS * 8 + (lane & 7), item % CHUNKS), x[i]);
+              const int item = i0 + i * kConverters;
+              const int row = item / (CHUNKS / 4) * 8 + (lane & 7), c = item % (CHUNKS / 4) * 4 + (lane >> 3);
+              if (item < ITEMS) ld_shared_v4(src + byte_chunk<D>(row, c), x[i]);
             }
 #pragma unroll
             for (int i = 0; i < AT_ONCE; ++i) {
-              const int item = (sub * EACH + i0 + i) * 4 + (lane >> 3);
-              const int row = item / CHUNKS * 8 + (lane & 7), c = item % CHUNKS * 2;
+              const int item = i0 + i * kConverters;
+              if (item >= ITEMS) break;
+              const int row = item / (CHUNKS / 4) * 8 + (lane & 7), c = (item % (CHUNKS / 4) * 4 + (lane >> 3)) * 2;
               const bool live = row < left;
               uint32_t h[8];
 #pragma unroll
