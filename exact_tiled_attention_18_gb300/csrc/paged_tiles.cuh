@@ -80,13 +80,13 @@ namespace fa {
 namespace {
 
 // registers: the split of the square forward (fwd.cu), 2*128*192 + 128*120 =
-// 384*168; with four more warps 2*128*184 + 2*128*72 = 512*128
+// 384*168; with four more warps 2*128*168 + 2*128*88 = 512*128
 template <bool FP8>
 struct Launch {
   static constexpr int kThreads = FP8 ? 512 : 384;
   static constexpr int kRegs = FP8 ? 128 : 168;
-  static constexpr int kSoftmaxRegs = FP8 ? 184 : 192;
-  static constexpr int kOtherRegs = FP8 ? 72 : 120;
+  static constexpr int kSoftmaxRegs = FP8 ? 168 : 192;
+  static constexpr int kOtherRegs = FP8 ? 88 : 120;
   // warps that follow the pieces: all but the one that works them out, and with
   // E4M3 one that is idle
   static constexpr int kReaders = kThreads / 32 - 1 - FP8;
@@ -525,6 +525,18 @@ __global__ void __launch_bounds__(Launch<FP8>::kThreads, 1)
       // (a row without a key keeps out what its query may hold)
       if (FP8 && lim0 <= 0) grow = 1.f;
       float m_ref = 0.f, l = 0.f, dl = 0.f;
+      auto rescale = [&](float alpha) {
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t v[32];
+          tmem_ld32(tO + 32 * c, v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * alpha);
+          tmem_st32(tO + 32 * c, v);
+        }
+        tmem_st_wait();
+      };
       for (int j = 0; j < nt; ++j) {
         [[maybe_unused]] const uint32_t at = base + (DUAL ? 2 * j + t : j);
         if constexpr (FP8) {  // (there before the scores are)
@@ -535,82 +547,54 @@ __global__ void __launch_bounds__(Launch<FP8>::kThreads, 1)
         if (!ok) break;
         ++sn;
         tc_fence_after();
-        float s[128];
-        {
-          uint32_t sr[128];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(sr + 32 * c));
-          tmem_ld_wait();
-#pragma unroll
-          for (int c = 0; c < 128; ++c) s[c] = __uint_as_float(sr[c]);
-        }
         const int lim = lim0 - j * stride;
-        if (__any_sync(0xffffffffu, lim < kRows)) {
-#pragma unroll
-          for (int c = 0; c < 128; ++c) s[c] = (c < lim) ? s[c] : -CUDART_INF_F;
-          if constexpr (FP8) {  // which are read again
-#pragma unroll
-            for (int c = 0; c < 4; ++c) tmem_st32(tS + 32 * c, reinterpret_cast<const uint32_t(&)[32]>(s[32 * c]));
-            tmem_st_wait();
-          }
-        }
-        float mt;
-        [[maybe_unused]] uint32_t scales = 0;
         if constexpr (FP8) {
-          scales = sbase + L::kScaleOff + at % kScaleTiles * kScales * 16;
-          mt = -CUDART_INF_F;
-#pragma unroll
-          for (int b = 0; b < kScales; ++b) {
-            const float* x = s + kScaleTokens * b;
-            const float t1 = fmax3(fmax3(x[0], x[1], x[2]), fmax3(x[3], x[4], x[5]), fmax3(x[6], x[7], x[8]));
-            const float t2 = fmax3(fmax3(x[9], x[10], x[11]), fmax3(x[12], x[13], x[14]), x[15]);
-            const float2 c = ld_shared_f2(scales + 16 * b);
-            mt = fmaxf(mt, fmaf(fmaxf(t1, t2), c.x * grow, c.y));
-          }
-        } else {
-          // row maximum as a log-depth tree of 3-input max
-          float t1[43];
-#pragma unroll
-          for (int c = 0; c < 42; ++c) t1[c] = fmax3(s[3 * c], s[3 * c + 1], s[3 * c + 2]);
-          t1[42] = fmaxf(s[126], s[127]);
-          float t2[15];
-#pragma unroll
-          for (int c = 0; c < 14; ++c) t2[c] = fmax3(t1[3 * c], t1[3 * c + 1], t1[3 * c + 2]);
-          t2[14] = t1[42];
-          float t3[5];
-#pragma unroll
-          for (int c = 0; c < 5; ++c) t3[c] = fmax3(t2[3 * c], t2[3 * c + 1], t2[3 * c + 2]);
-          mt = fmaxf(fmax3(t3[0], t3[1], t3[2]), fmaxf(t3[3], t3[4])) * scale_log2;
-        }
-        if (j == 0) {
-          // -inf: the row sees a leading range of the piece's keys and so none
-          // at all, or keys whose scores are -inf, behind which any other's
-          // becomes the reference
-          m_ref = fmaxf(mt, kNoScore);
-        } else {
-          const bool need = mt > m_ref + kTau;
-          if (__any_sync(0xffffffffu, need)) {
-            const float m_new = fmaxf(m_ref, mt);
-            const float alpha = ex2_approx(m_ref - m_new);
-            m_ref = m_new;
-            l *= alpha;
-            dl *= alpha;
+          const uint32_t scales = sbase + L::kScaleOff + at % kScaleTiles * kScales * 16;
+          if (__any_sync(0xffffffffu, lim < kRows)) {
 #pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
+            for (int c = 0; c < 4; ++c) {
               uint32_t v[32];
-              tmem_ld32(tO + 32 * c, v);
+              tmem_ld32(tS + 32 * c, v);
               tmem_ld_wait();
 #pragma unroll
-              for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * alpha);
-              tmem_st32(tO + 32 * c, v);
+              for (int i = 0; i < 32; ++i) v[i] = 32 * c + i < lim ? v[i] : 0xff800000u;  // -inf
+              tmem_st32(tS + 32 * c, v);
             }
             tmem_st_wait();
           }
-        }
-        if constexpr (FP8) {
-          // The scores come from tensor memory once more, 64 columns at a time, so
-          // that the loop over a tile stays small: with all 128 columns' instructions
-          // in a row it is larger than the first-level instruction cache.
+          // The scores are read twice, for the maximum and for the weights, 64 columns
+          // at a time, in loops that stay rolled: with all 128 columns' instructions in
+          // a row a tile's are more than the first instruction cache holds, and the
+          // warps wait for them (two chunks of 1000 tokens, us: 415 with the scores in
+          // registers, 377 so).
+          float top = -CUDART_INF_F;
+#pragma unroll 1
+          for (int h = 0; h < 2; ++h) {
+            uint32_t v[64];
+#pragma unroll
+            for (int c = 0; c < 2; ++c) tmem_ld32(tS + 64 * h + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(v + 32 * c));
+            tmem_ld_wait();
+#pragma unroll
+            for (int b = 0; b < kScales / 2; ++b) {
+              auto x = [&](int i) { return __uint_as_float(v[kScaleTokens * b + i]); };
+              const float t1 = fmax3(fmax3(x(0), x(1), x(2)), fmax3(x(3), x(4), x(5)), fmax3(x(6), x(7), x(8)));
+              const float t2 = fmax3(fmax3(x(9), x(10), x(11)), fmax3(x(12), x(13), x(14)), x(15));
+              const float2 k = ld_shared_f2(scales + 16 * (4 * h + b));
+              top = fmaxf(top, fmaf(fmaxf(t1, t2), k.x * grow, k.y));
+            }
+          }
+          if (j == 0) {
+            m_ref = fmaxf(top, kNoScore);  // (as below)
+          } else {
+            const bool need = top > m_ref + kTau;
+            if (__any_sync(0xffffffffu, need)) {
+              const float m_new = fmaxf(m_ref, top);
+              const float alpha = ex2_approx(m_ref - m_new);
+              m_ref = m_new;
+              l *= alpha;
+              rescale(alpha);
+            }
+          }
           const float add0 = kShift - m_ref;
 #pragma unroll 1
           for (int c = 0; c < 2; ++c) {
@@ -642,6 +626,48 @@ __global__ void __launch_bounds__(Launch<FP8>::kThreads, 1)
             tmem_st32(tS + 32 * c, pk);
           }
         } else {
+          float s[128];
+          {
+            uint32_t sr[128];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(sr + 32 * c));
+            tmem_ld_wait();
+#pragma unroll
+            for (int c = 0; c < 128; ++c) s[c] = __uint_as_float(sr[c]);
+          }
+          if (__any_sync(0xffffffffu, lim < kRows)) {
+#pragma unroll
+            for (int c = 0; c < 128; ++c) s[c] = (c < lim) ? s[c] : -CUDART_INF_F;
+          }
+          // row maximum as a log-depth tree of 3-input max
+          float t1[43];
+#pragma unroll
+          for (int c = 0; c < 42; ++c) t1[c] = fmax3(s[3 * c], s[3 * c + 1], s[3 * c + 2]);
+          t1[42] = fmaxf(s[126], s[127]);
+          float t2[15];
+#pragma unroll
+          for (int c = 0; c < 14; ++c) t2[c] = fmax3(t1[3 * c], t1[3 * c + 1], t1[3 * c + 2]);
+          t2[14] = t1[42];
+          float t3[5];
+#pragma unroll
+          for (int c = 0; c < 5; ++c) t3[c] = fmax3(t2[3 * c], t2[3 * c + 1], t2[3 * c + 2]);
+          const float mt = fmaxf(fmax3(t3[0], t3[1], t3[2]), fmaxf(t3[3], t3[4])) * scale_log2;
+          if (j == 0) {
+            // -inf: the row sees a leading range of the piece's keys and so none
+            // at all, or keys whose scores are -inf, behind which any other's
+            // becomes the reference
+            m_ref = fmaxf(mt, kNoScore);
+          } else {
+            const bool need = mt > m_ref + kTau;
+            if (__any_sync(0xffffffffu, need)) {
+              const float m_new = fmaxf(m_ref, mt);
+              const float alpha = ex2_approx(m_ref - m_new);
+              m_ref = m_new;
+              l *= alpha;
+              dl *= alpha;
+              rescale(alpha);
+            }
+          }
           const uint64_t c2 = f2_pack(scale_log2, scale_log2);
           const uint64_t n2 = f2_pack(-m_ref, -m_ref);
           {
@@ -1053,6 +1079,9 @@ __global__ void __launch_bounds__(Launch<FP8>::kThreads, 1)
                 if (nb > 0) {
                   if (!arrived(L::Q_FULL + 1, qb)) return false;
                   ++qb;
+                  // (behind tile A's first weights, so that the two softmaxes begin
+                  // half a step apart: two chunks of 1000 tokens 382 us without, 374)
+                  if (FP8 && na > 0 && !arrived(L::P_FULL + 0, pa)) return false;
                   tc_fence_after();
                   issue_s(1, kvbase % KS);
                   umma_commit(BAR(L::S_FULL + 1));
