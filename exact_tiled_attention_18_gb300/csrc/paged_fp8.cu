@@ -39,7 +39,7 @@
 
 #include "internal.h"
 #include "paged.cuh"
-#include "ptx.cuh"
+#include "ptx_e4m3.cuh"
 #include "serving.h"
 
 namespace fa {

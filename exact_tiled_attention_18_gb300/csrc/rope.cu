@@ -37,7 +37,7 @@
 #include <type_traits>
 
 #include "internal.h"
-#include "ptx.cuh"
+#include "ptx_e4m3.cuh"
 #include "serving.h"
 
 namespace fa {
