@@ -919,9 +919,9 @@ def _append(k, v, k_pages, v_pages, scales, block_table, seqlens_k, seqlens_q, t
             raise ValueError("q_out must be contiguous bf16 of q's shape and device")
         qp, op = q.data_ptr(), q_out.data_ptr()
     L = _lib or lib()
-    st = _call_on(index, L.fa_kv_append if scales is None else L.fa_kv_append_fp8, k.data_ptr(), kb, kh, kn, v.data_ptr(), vb, vh, vn, qp, qb, qh,
-                  qn, op, *pages, *table, _lens(seqlens_q, B, index), _lens(seqlens_k, B, index), *rope, amplitude, B,
-                  Hq, Hkv, N, d)
+    st = _call_on(index, L.fa_kv_append if scales is None else L.fa_kv_append_fp8, k.data_ptr(), kb, kh, kn,
+                  v.data_ptr(), vb, vh, vn, qp, qb, qh, qn, op, *pages, *table, _lens(seqlens_q, B, index),
+                  _lens(seqlens_k, B, index), *rope, amplitude, B, Hq, Hkv, N, d)
     if st:
         _check("fa_kv_append" if scales is None else "fa_kv_append_fp8", st)
     return q_out
@@ -1058,8 +1058,10 @@ class PagePool:
                     or t.shape[2] < 1 or self.page_size % t.shape[2]):
                 raise ValueError("a pool's tensors must be contiguous [pages, heads, rows, ...] of one device, with "
                                  "rows that divide the page size")
-            x.base, x.heads, x.rows = t.data_ptr(), t.shape[1], t.shape[2]
-            x.row_bytes = t.element_size() * (t.numel() // max(1, t.shape[0] * t.shape[1] * t.shape[2]))
+            row_bytes = t.element_size() * (t.numel() // max(1, t.shape[0] * t.shape[1] * t.shape[2]))
+            if self.num_pages > 2 ** 30 or t.shape[1] * t.shape[2] * row_bytes >= 2 ** 31:
+                raise ValueError("a pool has at most 2**30 pages, of less than 2**31 bytes in a tensor")
+            x.base, x.heads, x.rows, x.row_bytes = t.data_ptr(), t.shape[1], t.shape[2], row_bytes
 
 
 def _table_args(pool, block_table, seqlens_k, refs):
@@ -1083,6 +1085,8 @@ def _out_ints(out, shapes, device, index):
     import torch
     if out is None:  # (views of one allocation cost more than three)
         return tuple(torch.empty(s, dtype=torch.int32, device=device) for s in shapes)
+    if len(out) != len(shapes):
+        raise ValueError(f"out must be int32 tensors of shapes {shapes}")
     for k, (t, s) in enumerate(zip(out, shapes)):
         rows = t.dim() == 2 and (s[1] == 1 or t.stride(1) == 1) if k == 0 else t.is_contiguous()
         if t.shape != s or t.dtype != torch.int32 or t.get_device() != index or not rows:

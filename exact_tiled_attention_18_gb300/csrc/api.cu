@@ -11,6 +11,7 @@
 #include <cstdint>
 #include <cstdlib>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 #include <vector>
 
@@ -181,7 +182,8 @@ bool encode_map(CUtensorMap* m, const MapKey& key) {
   }
   const auto swizzle = key.elem_bytes * key.box_inner == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
   CUresult r = fn(m, key.elem_bytes == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 3,
-                  const_cast<void*>(key.base), dims, strides, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                  const_cast<void*>(key.base), dims, strides, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return false;
   return remember_map(key, *m);
 }
@@ -539,16 +541,30 @@ fa_status check_tables(int num_pages, int page_size, const int* block_table, lon
   if (!block_table || !seqlens_k || !refs || !out_table || !out_refs) return FA_ERR_INVALID_ARG;
   if (num_pages < 1 || max_pages < 1 || page_size < 16 || page_size % 16 != 0 || B < 1 || rows < 1)
     return FA_ERR_INVALID_ARG;
-  if (static_cast<long long>(max_pages) * page_size > 1LL << 30) return FA_ERR_INVALID_ARG;
+  if (num_pages > 1 << 30 || static_cast<long long>(max_pages) * page_size > 1LL << 30) return FA_ERR_INVALID_ARG;
   if (table_stride < 0 || (rows > 1 && out_stride < max_pages)) return FA_ERR_INVALID_ARG;
   for (const int* p : {block_table, seqlens_k, refs, out_table, out_refs})
     if (!aligned(p, 4)) return FA_ERR_MISALIGNED;
   return FA_OK;
 }
 
-bool ranges_meet(const void* a, long long a_words, const void* b, long long b_words) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return x < y + 4 * static_cast<uintptr_t>(b_words) && y < x + 4 * static_cast<uintptr_t>(a_words);
+// Device memory that a call reads or writes, in 4-byte words.
+struct Words {
+  const void* base;
+  long long count;
+};
+
+// Whether one of the ranges from the first output on meets any other range.
+bool outputs_meet(std::initializer_list<Words> ranges, int first_output) {
+  const Words* r = ranges.begin();
+  for (int i = first_output; i < static_cast<int>(ranges.size()); ++i) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(r[i].base);
+    for (int j = 0; j < i; ++j) {
+      const uintptr_t y = reinterpret_cast<uintptr_t>(r[j].base);
+      if (x < y + 4 * static_cast<uintptr_t>(r[j].count) && y < x + 4 * static_cast<uintptr_t>(r[i].count)) return true;
+    }
+  }
+  return false;
 }
 
 // Fills `out` with the tensors of a pool.
@@ -1035,10 +1051,11 @@ fa_status fa_rope(const void* x, int x_dtype, long long x_stride_b, long long x_
 static fa_status append(const void* k, long long k_stride_b, long long k_stride_h, long long k_stride_n, const void* v,
                         long long v_stride_b, long long v_stride_h, long long v_stride_n, const void* q,
                         long long q_stride_b, long long q_stride_h, long long q_stride_n, void* q_out, void* k_pages,
-                        void* v_pages, float* k_scales, float* v_scales, int num_pages, int page_size, const int* block_table, long long table_stride,
-                       int max_pages, const int* seqlens_q, const int* seqlens_k, const int* positions,
-                       long long positions_stride_b, const long long* turns, int rot_dim, int layout, float amplitude,
-                       int B, int Hq, int Hkv, int N, int d, fa_stream_t stream) {
+                        void* v_pages, float* k_scales, float* v_scales, int num_pages, int page_size,
+                        const int* block_table, long long table_stride, int max_pages, const int* seqlens_q,
+                        const int* seqlens_k, const int* positions, long long positions_stride_b,
+                        const long long* turns, int rot_dim, int layout, float amplitude, int B, int Hq, int Hkv,
+                        int N, int d, fa_stream_t stream) {
   if (!k || !v || !seqlens_k || (q != nullptr) != (q_out != nullptr)) return FA_ERR_INVALID_ARG;
   fa_status st = check_sizes(B, Hkv, N, d, 0);
   if (st != FA_OK) return st;
@@ -1084,7 +1101,9 @@ static fa_status append(const void* k, long long k_stride_b, long long k_stride_
     a.v_bytes = static_cast<uint8_t*>(v_pages);
     a.k_scales = k_scales;
     a.v_scales = v_scales;
-    a.key_growth = turns ? static_cast<float>(1.4142135623730951 * std::fabs(static_cast<double>(amplitude))) : 1.f;
+    // what a rotation can make of a key's largest value; a part that is not rotated stays as it is
+    const double turned = turns ? 1.4142135623730951 * std::fabs(static_cast<double>(amplitude)) : 1.;
+    a.key_growth = static_cast<float>(rot_dim < d ? std::max(turned, 1.) : turned);
   } else {
     a.k_pages = static_cast<uint16_t*>(k_pages);
     a.v_pages = static_cast<uint16_t*>(v_pages);
@@ -1111,26 +1130,26 @@ fa_status fa_kv_append(const void* k, long long k_stride_b, long long k_stride_h
                        int max_pages, const int* seqlens_q, const int* seqlens_k, const int* positions,
                        long long positions_stride_b, const long long* turns, int rot_dim, int layout, float amplitude,
                        int B, int Hq, int Hkv, int N, int d, fa_stream_t stream) {
-  return append(k, k_stride_b, k_stride_h, k_stride_n, v, v_stride_b, v_stride_h, v_stride_n, q, q_stride_b, q_stride_h,
-                q_stride_n, q_out, k_pages, v_pages, nullptr, nullptr, num_pages, page_size, block_table, table_stride,
-                max_pages, seqlens_q, seqlens_k, positions, positions_stride_b, turns, rot_dim, layout, amplitude, B, Hq,
-                Hkv, N, d, stream);
+  return append(k, k_stride_b, k_stride_h, k_stride_n, v, v_stride_b, v_stride_h, v_stride_n, q, q_stride_b,
+                q_stride_h, q_stride_n, q_out, k_pages, v_pages, nullptr, nullptr, num_pages, page_size, block_table,
+                table_stride, max_pages, seqlens_q, seqlens_k, positions, positions_stride_b, turns, rot_dim, layout,
+                amplitude, B, Hq, Hkv, N, d, stream);
 }
 
-fa_status fa_kv_append_fp8(const void* k, long long k_stride_b, long long k_stride_h, long long k_stride_n, const void* v,
-                           long long v_stride_b, long long v_stride_h, long long v_stride_n, const void* q,
-                           long long q_stride_b, long long q_stride_h, long long q_stride_n, void* q_out,
-                           void* k_pages,
-                           void* v_pages, float* k_scales, float* v_scales, int num_pages, int page_size,
-                           const int* block_table, long long table_stride, int max_pages, const int* seqlens_q, const int* seqlens_k, const int* positions,
+fa_status fa_kv_append_fp8(const void* k, long long k_stride_b, long long k_stride_h, long long k_stride_n,
+                           const void* v, long long v_stride_b, long long v_stride_h, long long v_stride_n,
+                           const void* q, long long q_stride_b, long long q_stride_h, long long q_stride_n,
+                           void* q_out, void* k_pages, void* v_pages, float* k_scales, float* v_scales, int num_pages,
+                           int page_size, const int* block_table, long long table_stride, int max_pages,
+                           const int* seqlens_q, const int* seqlens_k, const int* positions,
                            long long positions_stride_b, const long long* turns, int rot_dim, int layout,
                            float amplitude, int B, int Hq, int Hkv, int N, int d, fa_stream_t stream) {
   const fa_status st = check_scales(k_scales, v_scales);
   if (st != FA_OK) return st;
-  return append(k, k_stride_b, k_stride_h, k_stride_n, v, v_stride_b, v_stride_h, v_stride_n, q, q_stride_b, q_stride_h,
-                q_stride_n, q_out, k_pages, v_pages, k_scales, v_scales, num_pages, page_size, block_table, table_stride,
-                max_pages, seqlens_q, seqlens_k, positions, positions_stride_b, turns, rot_dim, layout, amplitude, B, Hq,
-                Hkv, N, d, stream);
+  return append(k, k_stride_b, k_stride_h, k_stride_n, v, v_stride_b, v_stride_h, v_stride_n, q, q_stride_b,
+                q_stride_h, q_stride_n, q_out, k_pages, v_pages, k_scales, v_scales, num_pages, page_size, block_table,
+                table_stride, max_pages, seqlens_q, seqlens_k, positions, positions_stride_b, turns, rot_dim, layout,
+                amplitude, B, Hq, Hkv, N, d, stream);
 }
 
 static size_t paged_workspace_bytes(int B, int Hq, int Hkv, int Nq, int d, bool with_prefix) {
@@ -1219,8 +1238,9 @@ fa_status fa_kv_fork(const fa_page_tensor* tensors, int count, int num_pages, in
   if (!aligned(sources, 4) || !aligned(out_seqlens, 4) || (workspace && !aligned(workspace, 16)))
     return FA_ERR_MISALIGNED;
   const long long in_words = (B - 1) * table_stride + max_pages, out_words = (rows - 1) * out_stride + max_pages;
-  if (ranges_meet(block_table, in_words, out_table, out_words) || ranges_meet(refs, num_pages, out_refs, num_pages) ||
-      ranges_meet(seqlens_k, B, out_seqlens, rows) || ranges_meet(sources, rows, out_seqlens, rows))
+  const long long space = workspace ? static_cast<long long>(fa_kv_fork_workspace_bytes(B, rows)) / 4 : 0;
+  if (outputs_meet({{block_table, in_words}, {seqlens_k, B}, {refs, num_pages}, {sources, rows}, {out_table, out_words},
+                    {out_seqlens, rows}, {out_refs, num_pages}, {workspace, space}}, 4))
     return FA_ERR_INVALID_ARG;
   try {
     std::vector<fa::PageTensor> list;
@@ -1270,8 +1290,9 @@ fa_status fa_kv_compact(const fa_page_tensor* tensors, int count, int num_pages,
   if (!new_ids) return FA_ERR_INVALID_ARG;
   if (!aligned(new_ids, 4) || (workspace && !aligned(workspace, 16))) return FA_ERR_MISALIGNED;
   const long long in_words = (B - 1) * table_stride + max_pages, out_words = (B - 1) * out_stride + max_pages;
-  if (ranges_meet(block_table, in_words, out_table, out_words) || ranges_meet(refs, num_pages, out_refs, num_pages) ||
-      ranges_meet(refs, num_pages, new_ids, num_pages) || ranges_meet(out_refs, num_pages, new_ids, num_pages))
+  const long long space = workspace ? static_cast<long long>(fa_kv_compact_workspace_bytes(num_pages)) / 4 : 0;
+  if (outputs_meet({{block_table, in_words}, {seqlens_k, B}, {refs, num_pages}, {out_table, out_words},
+                    {out_refs, num_pages}, {new_ids, num_pages}, {workspace, space}}, 3))
     return FA_ERR_INVALID_ARG;
   try {
     std::vector<fa::PageTensor> list;
@@ -1292,7 +1313,8 @@ fa_status fa_kv_compact(const fa_page_tensor* tensors, int count, int num_pages,
     a.workspace = workspace;
     a.status = di.status;
     if (!workspace &&
-        take_workspace(reinterpret_cast<void**>(&a.workspace), fa_kv_compact_workspace_bytes(num_pages), s) != cudaSuccess)
+        take_workspace(reinterpret_cast<void**>(&a.workspace), fa_kv_compact_workspace_bytes(num_pages), s) !=
+            cudaSuccess)
       return FA_ERR_LAUNCH;
     cudaError_t e = fa::launch_compact(a, list.data(), count, di.sms, s);
     if (!workspace) {

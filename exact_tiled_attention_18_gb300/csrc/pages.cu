@@ -182,8 +182,9 @@ __global__ void __cluster_dims__(kPlanCtas) __launch_bounds__(kPlanThreads, 1) f
   cluster_sync();
   // the free pages of the lowest ids, by rank, and the rows' ranks
   const int part = (a.table.num_pages + kPlanCtas - 1) / kPlanCtas;
-  const int begin = min(static_cast<long long>(cta) * part, static_cast<long long>(a.table.num_pages));
-  const int end = static_cast<int>(min(static_cast<long long>(begin) + part, static_cast<long long>(a.table.num_pages)));
+  const long long all = a.table.num_pages;
+  const int begin = static_cast<int>(min(static_cast<long long>(cta) * part, all));
+  const int end = static_cast<int>(min(static_cast<long long>(begin) + part, all));
   auto is_free = [&](int p) { return __ldcg(a.out_refs + p) == 0; };
   const int mine = count_pages(begin, end, scratch, is_free);
   if (threadIdx.x == 0) w.counts[cta] = mine;
@@ -332,7 +333,8 @@ __global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(const __grid_c
     auto copy = [&](auto word) {
       using W = decltype(word);
       constexpr unsigned SIZE = sizeof(W);
-      const unsigned head = static_cast<unsigned>(x.rows) * x.row_bytes / SIZE;  // words of a head (a page's: below 2^31)
+      // words of a head (a page's: below 2^31)
+      const unsigned head = static_cast<unsigned>(x.rows) * x.row_bytes / SIZE;
       const unsigned have = static_cast<unsigned>(rows) * x.row_bytes / SIZE;    // to copy of one
       const unsigned all = have * x.heads;
       const unsigned from = static_cast<unsigned>(static_cast<unsigned long long>(all) * in / of);

@@ -436,7 +436,8 @@ __global__ void __launch_bounds__(kRopeThreads, 3) append_fp8_kernel(const Appen
   // heads [begin, end) of keys or values
   auto cells = [&](auto value_tag, int begin, int end) {
     constexpr bool VALUE = decltype(value_tag)::value;
-    float* scale_to = (VALUE ? a.v_scales : a.k_scales) + (row >= 0 ? scale_at + static_cast<long long>(begin) * cells_of_page : 0);
+    float* scale_to = (VALUE ? a.v_scales : a.k_scales) +
+                      (row >= 0 ? scale_at + static_cast<long long>(begin) * cells_of_page : 0);
     uint8_t* to = (VALUE ? a.v_bytes : a.k_bytes) +
                   (row >= 0 ? (row + row_in + static_cast<long long>(begin) * a.table.page_size) * D : 0);
     const uint32_t* found = s_max[0] + group * WARPS;

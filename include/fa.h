@@ -582,8 +582,8 @@ size_t fa_fwd_shared_prefix_workspace_bytes(int B, int Hq, int Hkv, int Nq, int 
  * and rounded once, to E4M3.  A cell's scale is the smallest power of two, at
  * least 2^-32, that brings the largest magnitude of its tokens to at most 448:
  * of the values as they are given and, for keys that are rotated, times
- * sqrt(2) |amplitude|, as far as a rotation can raise it, so that it does not
- * depend on the position.  Tokens that come to a cell with older ones (the
+ * sqrt(2) |amplitude| (at least 1 where rot_dim < d), as far as a rotation can
+ * raise it, so that it does not depend on the position.  Tokens that come to a cell with older ones (the
  * rows before theirs, which must be the same sequence's) keep the cell's
  * scale, or raise it and have the older tokens' numbers rounded again; between
  * powers of two that changes only those that become subnormal.  A cell whose
@@ -602,8 +602,9 @@ fa_status fa_kv_append_fp8(const void* k, long long k_stride_b, long long k_stri
 
 /*
  * fa_fwd_paged and fa_fwd_shared_prefix over the cache in E4M3, with the same
- * workspaces.  Scales may be any positive finite fp32 numbers (of values that
- * a row sees together, within 2^60 of one another).
+ * workspaces.  Scales of values are fp32 numbers from 2^-32 to 2^60, those that a
+ * row sees together within 2^60 of one another; scales of keys may be any with
+ * which the scores are finite numbers.
  *   With up to 32 rows a key head both products run on fp16, in which the E4M3
  * numbers are exact, as is a query (taken times a power of two) but for elements
  * below 2^-28 of their row's largest.  With more rows, and against a prefix, a
@@ -640,7 +641,7 @@ fa_status fa_fwd_shared_prefix_fp8(const void* q, const void* k_pages, const voi
  * as a list, each tensor [num_pages][heads][rows][row_bytes], contiguous, where
  * `rows` divides page_size: page_size for keys and values, page_size / 16 for
  * scales.  Bases are 16-byte aligned, row_bytes a multiple of 4, a page of a
- * tensor below 2^31 bytes.  The list itself is host memory, read during the call.
+ * tensor below 2^31 bytes; there are at most 2^30 pages.  The list itself is host memory, read during the call.
  */
 typedef struct {
   void* base;
@@ -670,7 +671,7 @@ typedef struct {
  *   out_table : [rows][max_pages], stride out_stride >= max_pages; entries behind
  *               a row's pages are -1.  out_seqlens: [rows]; out_refs:
  *               [num_pages], refs less the old rows' entries plus the new ones'.
- *               None may overlap what it comes from, which is left as it was
+ *               None may overlap another or an input, which is left as it was
  *               but for the pages copied to: a program keeps two sets and
  *               swaps them.
  *   workspace : fa_kv_fork_workspace_bytes(B, rows) bytes, 16-byte aligned, used by
@@ -696,7 +697,7 @@ size_t fa_kv_fork_workspace_bytes(int B, int rows);
  *   new_ids   : [num_pages], where each page in use is now, -1 for the others:
  *               what other tables that name pages are to be changed by.
  *   workspace : fa_kv_compact_workspace_bytes(num_pages) bytes, as fa_kv_fork's.
- * Outputs may not overlap what they come from.
+ * No output may overlap another or an input.
  */
 fa_status fa_kv_compact(const fa_page_tensor* tensors, int count, int num_pages, int page_size, const int* block_table,
                         long long table_stride, int max_pages, const int* seqlens_k, int B, const int* refs,

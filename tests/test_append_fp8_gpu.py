@@ -62,6 +62,8 @@ CASES = [
     (1, 0, 7, 130, 128, 64, [1000], None, 32, "half", 1.0),               # no queries
     (70, 2, 1, 1, 64, 16, [1 + (i * 37) % 50 for i in range(70)], None, 64, "half", 1.0),
     (1, 64, 8, 300, 128, 256, [301], None, 128, "half", 1.0),
+    (2, 3, 3, 50, 128, 32, [50, 77], None, 32, "half", 0.125),           # a part that is larger than the rotated one
+    (1, 2, 2, 50, 64, 32, [60], None, 64, "interleaved", 0.0),            # keys of 0
 ]
 
 
@@ -96,7 +98,7 @@ def test_append_matches_the_definition(case):
     freqs = serving.rope_frequencies(rot) if rot else np.zeros(0)
     x = [to64(t).transpose(0, 2, 1, 3) for t in (k, v, q)]
     turned = [serving.rope(t, place, freqs, layout, amplitude) if rot else t for t in (x[0], x[2])]
-    growth = np.sqrt(2) * amplitude if rot else 1.0
+    growth = max(np.sqrt(2) * amplitude, 1.0 if rot < d else 0.0) if rot else 1.0
     for i, (new, raw, grow) in enumerate([(turned[0], x[0], growth), (x[1], x[1], 1.0)]):
         before = to64(pages[i].view(E4M3).float())
         codes, sc = expected(before, to64(scales[i]), new, raw, grow, table.numpy(), lens_q, lens_k)

@@ -67,10 +67,11 @@ def tensors(fa, *items):
 
 
 FORK = dict(tensors=None, count=0, pages=8, page=16, table=FAKE, stride=4, max_pages=4, lk=FAKE, B=2, refs=FAKE,
-            sources=FAKE, rows=3, out_table=FAKE + 4096, out_stride=4, out_lk=FAKE + 8192, out_refs=FAKE + 12288, ws=FAKE,
-            stream=0)
+            sources=FAKE, rows=3, out_table=FAKE + 4096, out_stride=4, out_lk=FAKE + 8192, out_refs=FAKE + 12288,
+            ws=FAKE + 20480, stream=0)
 COMPACT = dict(tensors=None, count=0, pages=8, page=16, table=FAKE, stride=4, max_pages=4, lk=FAKE, B=2, refs=FAKE,
-               out_table=FAKE + 4096, out_stride=4, out_refs=FAKE + 12288, new_ids=FAKE + 16384, ws=FAKE, stream=0)
+               out_table=FAKE + 4096, out_stride=4, out_refs=FAKE + 12288, new_ids=FAKE + 16384, ws=FAKE + 20480,
+               stream=0)
 TABLE_ERRORS = [
     (dict(table=0), 1), (dict(lk=0), 1), (dict(refs=0), 1), (dict(out_table=0), 1), (dict(out_refs=0), 1),
     (dict(pages=0), 1), (dict(page=0), 1), (dict(page=24), 1), (dict(max_pages=0), 1), (dict(max_pages=BIG), 1),
@@ -78,12 +79,14 @@ TABLE_ERRORS = [
     (dict(table=FAKE + 2), 3), (dict(lk=FAKE + 1), 3), (dict(refs=FAKE + 2), 3), (dict(out_table=FAKE + 4098), 3),
     (dict(out_refs=FAKE + 12289), 3), (dict(ws=FAKE + 8), 3),
     (dict(out_table=FAKE), 1), (dict(out_table=FAKE + 28), 1), (dict(out_refs=FAKE), 1), (dict(out_refs=FAKE + 28), 1),
+    (dict(pages=(1 << 30) + 1), 1), (dict(out_refs=FAKE + 4096), 1), (dict(ws=FAKE + 16), 1), (dict(ws=FAKE + 4096), 1),
+    (dict(lk=FAKE + 4096), 1), (dict(lk=FAKE + 12292), 1),
 ]
 
 
 @pytest.mark.parametrize("change,expect", TABLE_ERRORS + [
-    (dict(sources=0), 1), (dict(out_lk=0), 1), (dict(rows=0), 1), (dict(sources=FAKE + 2), 3), (dict(out_lk=FAKE + 1), 3),
-    (dict(out_lk=FAKE + 4), 1),
+    (dict(sources=0), 1), (dict(out_lk=0), 1), (dict(rows=0), 1), (dict(sources=FAKE + 2), 3),
+    (dict(out_lk=FAKE + 1), 3), (dict(out_lk=FAKE + 4), 1), (dict(sources=FAKE + 4096), 1), (dict(out_lk=FAKE + 12288), 1),
 ])
 def test_fork_argument_errors(fa, change, expect):
     st = call(fa.fa_kv_fork, FORK, change)

@@ -91,6 +91,22 @@ def test_scales_far_apart(Hq, Hkv, Nq):
     check(o, lse, reference(q, c, lens, None, True), q, c, way_of(Hq, Hkv, Nq))
 
 
+@pytest.mark.parametrize("Hq,Hkv,Nq", [(4, 2, 1), (8, 2, 4), (8, 2, 8), (4, 2, 64)])
+@pytest.mark.parametrize("low,high,q_scale", [(-32, 28, 1.0), (0, 60, 1.0), (-32, -32, 1.0), (60, 60, 1.0), (-32, -32, 10.0)])
+def test_scales_of_values_at_their_limits(Hq, Hkv, Nq, low, high, q_scale):
+    """Values' scales of 2^low and 2^high, cells in turn, with scores of +-2 and of
+    +-20 (in units of ln 2 times 10)."""
+    B, d, page = 2, 128, 64
+    lens = [1500, 200 + Nq]
+    q, c = make_batch(B, Hq, Hkv, Nq, d, page, lens, seed=8, q_scale=q_scale)
+    live = torch.isfinite(c.scales[1])
+    at = torch.arange(page // 16) % 2 == 0
+    c.scales[1] = torch.where(live, torch.where(at, 2.0 ** low, 2.0 ** high).float().expand_as(live), c.scales[1])
+    c.update()
+    o, lse = run(q, c, lens)
+    check(o, lse, reference(q, c, lens, None, True), q, c, way_of(Hq, Hkv, Nq))
+
+
 @pytest.mark.parametrize("Hq,Hkv,Nq", [(4, 2, 1), (8, 2, 8), (4, 2, 64), (2, 1, 300)])
 def test_one_large_weight_and_many_small_ones(Hq, Hkv, Nq):
     """The first key takes about half of every row's weight, thousands of others
