@@ -577,9 +577,9 @@ fa_status check_tensors(const fa_page_tensor* tensors, int count, int page_size,
       return FA_ERR_INVALID_ARG;
     const double bytes = static_cast<double>(t.heads) * t.rows * t.row_bytes;
     if (bytes >= 2147483648.0) return FA_ERR_INVALID_ARG;
-    if (!aligned(t.base, 16)) return FA_ERR_MISALIGNED;
-    out[static_cast<size_t>(i)] =
-        fa::PageTensor{static_cast<uint8_t*>(t.base), t.heads, t.rows, t.row_bytes, t.row_bytes % 16 == 0, 0};
+    if (!aligned(t.base, 4)) return FA_ERR_MISALIGNED;
+    out[static_cast<size_t>(i)] = fa::PageTensor{static_cast<uint8_t*>(t.base), t.heads, t.rows, t.row_bytes,
+                                                 t.row_bytes % 16 == 0 && aligned(t.base, 16), 0};
   }
   return FA_OK;
 }

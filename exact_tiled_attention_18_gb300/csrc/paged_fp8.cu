@@ -31,6 +31,16 @@
 // 2 j), j < 4, of a warp's 32 for line i of the fragments, an order in which the
 // rows that one ldmatrix phase reads lie in different banks for keys and values
 // both.
+//
+// Bound by HBM where there are keys enough: 8 sequences x 32 heads x 32768 keys, one
+// row a head, 308 us = 7.0 TB/s of keys and values (a step reads only, the copy that
+// peaks are taken from writes too).  32 sequences of 100 to 16384 keys, 32 heads on 4,
+// 25.1 us, of which about 9 are the start (lengths, page ids, first tiles) and the
+// merge; one sequence of 1000 keys 8.5 us in a graph, all latency.  8 sequences x 8
+// heads x 8192 keys 29.4 us with 1 to 8 rows a head, 35.5 with 16, 42 with 24 and 57
+// with 32 (bf16 48, 50, 55, 62): from 17 rows on the warps' instructions bound it, the
+// conversions and, at 25 and more, accumulators that spill.  Tensor pipe 18%, issue
+// slots 35% in the long case.
 #include <cuda_runtime.h>
 #include <math_constants.h>
 

@@ -12,6 +12,12 @@
 // The copy is bound by HBM (a byte read and a byte written) or, for a few tokens of a
 // few sequences, by launch latency.  It reads the list of pages and its length on
 // the device.
+//
+// Measured, in a graph: 128 samples of two prompts of 1001 and 4000 tokens, each with
+// a page of its own in the tensors of 8 layers, 75 us; about 300 of 1200 pages moved (in E4M3, 8 layers) 106 us =
+// 5.9 TB/s; a beam search's reordering of 16 rows 13.3 us and a small cache's
+// compaction 10.5, of which the tables' passes are about 9 and 7: chains of loads and
+// atomics, a microsecond each.
 #include <cuda_runtime.h>
 
 #include <climits>
@@ -375,7 +381,7 @@ cudaError_t launch_copies(CopyArgs& c, const PageTensor* tensors, int count, lon
     }
     c.slices = slices;
     c.count = n;
-    // (128 samples of two prompts of 1001 and 4000 tokens, and half of 1200 pages
+    // (128 samples of two prompts of 1001 and 4000 tokens, and about 300 of 1200 pages
     // moved, us, with 8 / 16 / 32 CTAs an SM: 83 / 77 / 75 and 114 / 110 / 106; slices of
     // 16 KB 105 and 108; eight loads in flight a thread 89 and 107.)
     const long long items = most * slices, room = 32LL * sms;

@@ -640,8 +640,9 @@ fa_status fa_fwd_shared_prefix_fp8(const void* q, const void* k_pages, const voi
  * all layers, and for a cache in E4M3 their scales.  The calls below take them
  * as a list, each tensor [num_pages][heads][rows][row_bytes], contiguous, where
  * `rows` divides page_size: page_size for keys and values, page_size / 16 for
- * scales.  Bases are 16-byte aligned, row_bytes a multiple of 4, a page of a
- * tensor below 2^31 bytes; there are at most 2^30 pages.  The list itself is host memory, read during the call.
+ * scales.  Bases are 4-byte aligned (16-byte for copies at full speed) and
+ * row_bytes a multiple of 4, a page of a tensor is below 2^31 bytes; there are
+ * at most 2^30 pages.  The list itself is host memory, read during the call.
  */
 typedef struct {
   void* base;

@@ -103,7 +103,7 @@ def test_compact_argument_errors(fa, change, expect):
 
 @pytest.mark.parametrize("item,expect", [
     ((0, 1, 16, 128), 1), ((FAKE, 0, 16, 128), 1), ((FAKE, 1, 0, 128), 1), ((FAKE, 1, 5, 128), 1), ((FAKE, 1, 32, 128), 1),
-    ((FAKE, 1, 16, 0), 1), ((FAKE, 1, 16, 2), 1), ((FAKE, 1, 16, 6), 1), ((FAKE + 8, 1, 16, 128), 3),
+    ((FAKE, 1, 16, 0), 1), ((FAKE, 1, 16, 2), 1), ((FAKE, 1, 16, 6), 1), ((FAKE + 2, 1, 16, 128), 3),
     ((FAKE, 1 << 20, 16, 128), 1),
 ])
 def test_page_tensor_errors(fa, item, expect):

@@ -257,6 +257,39 @@ def test_compact_matches_the_definition(case):
         assert np.array_equal(raw(t), w)
 
 
+def test_layers_of_one_tensor_at_odd_places():
+    """Layers that are slices of one allocation each: scales whose layers begin 4,
+    8 and 12 bytes off a 16-byte boundary, keys 4 bytes off."""
+    page, lens, sources = 16, [40, 7, 33], [0, 0, 1, 2, 1, 2]
+    g = torch.Generator().manual_seed(11)
+    table, refs = make_batch(g, lens, page, 4)
+    n = len(refs) | 1                                            # an odd number of pages
+    refs = np.concatenate([refs, np.zeros(n - len(refs), dtype=np.int32)])
+    scales = torch.randn(4, n, 1, 1, generator=g).cuda()
+    keys = torch.randint(0, 1 << 30, (n * page * 16 + 1,), generator=g, dtype=torch.int32).cuda()[1:].view(n, 1, page, 16)
+    tensors = [*scales.unbind(0), keys]
+    assert {t.data_ptr() % 16 for t in tensors} == {0, 4, 8, 12}
+    out, out_lens, out_refs, copies = fork(table, lens, refs, sources, page)
+    want = moved(tensors, copies, page)
+    pool = fa.PagePool(tensors, page)
+    got = fa.kv_fork(pool, *cuda(table, lens, refs, sources))
+    fa.sync_status()
+    for t, w in zip([*got, *tensors], [out, out_lens, out_refs, *want]):
+        assert np.array_equal(raw(t) if t.dim() > 2 else t.cpu().numpy(), w)
+    gone = out_refs.copy()
+    kept = out.copy()
+    for b in (0, 1):                                             # two rows end
+        for p in kept[b, :-(-out_lens[b] // page)]:
+            gone[p] -= 1
+        out_lens[b] = 0
+    out, out_refs, new_ids, copies = compact(kept, out_lens, gone, page)
+    want = moved(tensors, copies, page)
+    got = fa.kv_compact(pool, *cuda(kept, out_lens, gone))
+    fa.sync_status()
+    for t, w in zip([*got, *tensors], [out, out_refs, new_ids, *want]):
+        assert np.array_equal(raw(t) if t.dim() > 2 else t.cpu().numpy(), w)
+
+
 def test_compact_reports_entries_of_free_pages():
     g = torch.Generator().manual_seed(4)
     tensors = [t.cuda() for t in make_tensors(g, 6, 16, KV8)]
