@@ -76,7 +76,11 @@ __device__ __forceinline__ Lane<RUNS> make_lane(const RopeRef& r, int d, int c, 
   return l;
 }
 
-template <int RUNS>
+// REST: with what the phase's rounding to fp32 leaves, to first order, so that
+// sine and cosine are as near as fp32 holds them.  For keys that are rounded to
+// E4M3 at once, of whose values next to the middle of two numbers fewer go to the
+// farther one (of 30 batches' 96 without, 59 so, 54 with angles in 64 bits).
+template <bool REST = false, int RUNS>
 __device__ __forceinline__ void set_angles(Lane<RUNS>& l, const RopeRef& r, int position, float sign) {
   if (!l.turns) return;
   constexpr int PER = 16 / RUNS;
@@ -87,9 +91,17 @@ __device__ __forceinline__ void set_angles(Lane<RUNS>& l, const RopeRef& r, int 
     const int element = l.at + (e / PER) * l.step + e % PER;
     const unsigned long long f = static_cast<unsigned long long>(__ldg(r.turns + (r.interleaved ? element / 2 : element)));
     const unsigned long long phase = static_cast<unsigned long long>(static_cast<long long>(position)) * f;
-    const float half_turns = static_cast<float>(static_cast<int>(phase >> 32)) * 4.656612873077393e-10f;  // 2^-31
+    const int word = static_cast<int>(phase >> 32);
+    const float rounded = static_cast<float>(word);
+    const float half_turns = rounded * 4.656612873077393e-10f;  // 2^-31
     float s, co;
     sincospif(half_turns, &s, &co);
+    if constexpr (REST) {
+      const float rest = static_cast<float>(word - __float2int_rn(rounded)) * 1.4629180792671596e-9f;  // pi 2^-31
+      const float t = s;
+      s = fmaf(co, rest, s);
+      co = fmaf(-t, rest, co);
+    }
     l.cs[i] = co * r.amplitude;
     l.sn[i] = s * (r.amplitude * sign);
   }
@@ -312,6 +324,11 @@ __global__ void __launch_bounds__(kRopeThreads) append_kernel(const AppendArgs a
 // taken before the rotation, times sqrt(2) |amplitude|, which is as far as a pair's
 // values can go: the scale then does not depend on the position.
 //
+// Measured: four prompts of 2048 to 8192 tokens, 16 + 16 + 16 heads, d = 128, queries
+// rotated too, 65 us = 5.9 TB/s of what has to be read and written (0.87 of the copy
+// rate; issue slots 65% busy, DRAM 68%), a step of 8 sequences 4.2 us a call in a graph.
+// Loads through registers, two heads at a time, 99 us; one after the other 128.
+//
 // A group of d threads takes a cell of the tokens' heads one after the other, a
 // thread 16 values of a token as in append_kernel; the group's maximum goes
 // through shared memory, once for HEADS heads.
@@ -366,11 +383,9 @@ __global__ void __launch_bounds__(kRopeThreads, 3) append_fp8_kernel(const Appen
   const bool old = has_old && place < first;
   const bool counts = fresh && place >= 0;       // a token with a place
   Lane<RUNS> l = make_lane<RUNS>(a.rope, D, c, a.rope.rot_dim > 0);
-  if (fresh && h0 < hq + a.Hkv) {
-    const int position = a.rope.positions ? __ldg(a.rope.positions + b * a.rope.positions_sb + t)
-                                          : static_cast<int>(place);
-    set_angles(l, a.rope, position, 1.f);
-  }
+  const int position = fresh && a.rope.positions ? __ldg(a.rope.positions + b * a.rope.positions_sb + t)
+                                                 : static_cast<int>(place);
+  if (fresh && h0 < hq) set_angles(l, a.rope, position, 1.f);  // (queries: to the bit as fa_rope has them)
   // A thread's values of the heads to come are on their way to its own places in
   // shared memory, up to kAppendStages heads' ahead.  Addresses go from head to
   // head by additions: this kernel is bound by its instructions.
@@ -508,6 +523,7 @@ __global__ void __launch_bounds__(kRopeThreads, 3) append_fp8_kernel(const Appen
     }
   };
   const int kv = hq + a.Hkv;
+  if (fresh && h0 < kv && h1 > hq) set_angles<true>(l, a.rope, position, 1.f);
   cells(std::false_type{}, max(h0, hq) - hq, min(h1, kv) - hq);
   cells(std::true_type{}, max(h0, kv) - kv, h1 - kv);
   cp_async_wait<0>();
