@@ -38,8 +38,8 @@
 // 25.1 us, of which about 9 are the start (lengths, page ids, first tiles) and the
 // merge; one sequence of 1000 keys 8.5 us in a graph, all latency.  8 sequences x 8
 // heads x 8192 keys 29.4 us with 1 to 8 rows a head, 35.5 with 16, 42 with 24 and 57
-// with 32 (bf16 48, 50, 55, 62): from 17 rows on the warps' instructions bound it, the
-// conversions and, at 25 and more, accumulators that spill.  Tensor pipe 18%, issue
+// with 32 (bf16 48, 50, 55, 62): with more rows the warps' instructions bound it, and
+// registers, of which a thread has 168 (100 to 300 bytes spill from 9 rows on).  Tensor pipe 18%, issue
 // slots 35% in the long case.
 #include <cuda_runtime.h>
 #include <math_constants.h>

@@ -326,7 +326,7 @@ __global__ void __launch_bounds__(kRopeThreads) append_kernel(const AppendArgs a
 //
 // Measured: four prompts of 2048 to 8192 tokens, 16 + 16 + 16 heads, d = 128, queries
 // rotated too, 65 us = 5.9 TB/s of what has to be read and written (0.87 of the copy
-// rate; issue slots 65% busy, DRAM 68%), a step of 8 sequences 4.2 us a call in a graph.
+// rate; issue slots and DRAM both 68% busy), a step of 8 sequences 4.2 us a call in a graph.
 // Loads through registers, two heads at a time, 99 us; one after the other 128.
 //
 // A group of d threads takes a cell of the tokens' heads one after the other, a
