@@ -466,7 +466,9 @@ cudaError_t take_workspace(void** p, size_t bytes, cudaStream_t s) {
   const cudaError_t e = cudaStreamIsCapturing(s, &capture);
   if (e != cudaSuccess) return e;
   cudaMemPool_t pool = capture == cudaStreamCaptureStatusNone ? workspace_pool() : nullptr;
-  return pool ? cudaMallocFromPoolAsync(p, bytes, pool, s) : cudaMallocAsync(p, bytes, s);
+  const cudaError_t got = pool ? cudaMallocFromPoolAsync(p, bytes, pool, s) : cudaMallocAsync(p, bytes, s);
+  if (got != cudaSuccess) cudaGetLastError();  // not the next launch's error
+  return got;
 }
 
 // Strides of the dimensions that are walked; the stride of a dimension of
