@@ -181,3 +181,35 @@ def test_tokens_without_a_place():
             pos = torch.arange(lens[b] - N, lens[b], dtype=torch.int32, device="cuda")
             assert torch.equal(got[b:b + 1], fa.rope_forward(q[b:b + 1], turns, pos))
         fa.sync_status()
+
+
+@pytest.mark.parametrize("shared", [True, False])
+@pytest.mark.parametrize("amplitude", [-1.5, 2.0 ** 40])
+def test_given_positions_and_other_amplitudes(shared, amplitude):
+    """Angles from positions of their own (for all sequences, or each its own in
+    a wider tensor), far apart and repeated; an amplitude below 0 and a large one."""
+    B, H, N, d, page = 2, 2, 21, 64, 16
+    g = torch.Generator().manual_seed(9)
+    x = torch.randn(B, H, N, d, generator=g).to(BF16)
+    places = torch.tensor([0, 10 ** 6, 5, 5, 131071, -3, 2 ** 31 - 1] * 9, dtype=torch.int32)
+    places = places[:N] if shared else torch.stack([places[:N + 5], places[1:N + 6]])[:, 2:2 + N]
+    wide = torch.full((B, N + 9), -7, dtype=torch.int32, device="cuda")
+    dev = places.cuda() if shared else wide[:, 4:4 + N].copy_(places)
+    pages = [torch.zeros(5, H, page, d, dtype=torch.uint8, device="cuda").view(E4M3) for _ in range(2)]
+    scales = [torch.zeros(5, H, 1, device="cuda") for _ in range(2)]
+    table = torch.tensor([[3, 1], [0, 4]], dtype=torch.int32)
+    lk = torch.tensor([N, N], dtype=torch.int32, device="cuda")
+    turns = fa.rope_turns(d, device="cuda")
+    fa.kv_append_fp8(x.cuda(), x.cuda(), *pages, *scales, table.cuda(), lk, turns=turns, positions=dev,
+                     amplitude=amplitude)
+    fa.sync_status()
+    at = np.broadcast_to(places.numpy(), (B, N))
+    want = serving.rope(to64(x), at, serving.rope_frequencies(d), "half", amplitude)
+    codes, sc = expected(np.zeros((5, H, page, d)), np.zeros((5, H, 1)), want, to64(x), np.sqrt(2) * abs(amplitude),
+                         table.numpy(), [N] * B, [N] * B)
+    assert np.array_equal(to64(scales[0]), sc)
+    there = to64(pages[0].float())
+    # the table's frequencies are doubles: p * 2^-53 turns, 2^-22 at 2^31, where few values' halves are crossed
+    step = np.maximum(np.exp2(np.floor(np.log2(np.maximum(np.abs(codes), 2.0 ** -6)))) / 8, 2.0 ** -9)
+    assert np.all(np.abs(there - codes) <= step)
+    assert (there != codes).mean() <= 1e-3
