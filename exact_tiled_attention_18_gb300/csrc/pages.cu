@@ -14,10 +14,12 @@
 // the device.
 //
 // Measured, in a graph: 128 samples of two prompts of 1001 and 4000 tokens, each with
-// a page of its own in the tensors of 8 layers, 75 us; about 300 of 1200 pages moved (in E4M3, 8 layers) 106 us =
-// 5.9 TB/s; a beam search's reordering of 16 rows 13.3 us and a small cache's
-// compaction 10.5, of which the tables' passes are about 9 and 7: chains of loads and
-// atomics, a microsecond each.
+// a page of its own in the tensors of 8 layers, 74 us; about 300 of 1200 pages moved
+// (in E4M3, 8 layers) 106 us = 5.9 TB/s; a beam search's reordering of 16 rows 12.2 us
+// and a small cache's compaction 10.5, of which the tables' passes are about 8 and 7:
+// chains of loads and atomics, a microsecond or more each.  One after the other in
+// every thread where they now run side by side, and one more, 13.7; one, two and four
+// CTAs 13.4, 13.2 and 13.1 (128 samples 77.1, 75.7, 75.4).
 #include <cuda_runtime.h>
 
 #include <climits>
@@ -146,59 +148,60 @@ __global__ void __cluster_dims__(kPlanCtas) __launch_bounds__(kPlanThreads, 1) f
   for (unsigned b = tid; b < static_cast<unsigned>(a.B); b += ALL) w.first[b] = INT_MAX;
   cluster_sync();
   // the old rows let go of their pages, the new ones take the full ones
-  for (long long x = tid; x < static_cast<long long>(a.B) * width; x += ALL) {
-    const int b = static_cast<int>(x / width), i = static_cast<int>(x - static_cast<long long>(b) * width);
-    if (i >= used_pages(length(b), page_size)) continue;
-    const int p = entry(b, i, b);
-    if (p >= 0) atomicAdd(a.out_refs + p, -1);
-  }
-  for (long long x = tid; x < static_cast<long long>(a.rows) * width; x += ALL) {
-    const int row = static_cast<int>(x / width), i = static_cast<int>(x - static_cast<long long>(row) * width);
-    const int s = source(row), len = s >= 0 ? length(s) : 0;
-    int out = -1;
-    if (i < used_pages(len, page_size)) {
-      const int p = entry(s, i, -1);
-      out = a.table.block_table[s * a.table.table_stride + i];
-      if (p >= 0 && i < len / page_size) atomicAdd(a.out_refs + p, 1);
-    }
-    a.out_table[row * a.out_stride + i] = out;
-  }
-  for (unsigned row = tid; row < static_cast<unsigned>(a.rows); row += ALL) {
-    const int s = source(row), len = s >= 0 ? length(s) : 0;
-    a.out_seqlens[row] = len;
-    if (s >= 0) atomicMin(w.first + s, static_cast<int>(row));
-  }
-  cluster_sync();
-  // a page that is being filled: the first row that continues the sequence
-  // keeps it, the others need one
-  for (unsigned row = tid; row < static_cast<unsigned>(a.rows); row += ALL) {
-    const int s = source(row), len = s >= 0 ? length(s) : 0;
-    int need = 0;
-    if (len % page_size) {
-      const int p = entry(s, len / page_size, -1);
-      if (p >= 0) {
-        if (__ldcg(w.first + s) == static_cast<int>(row))
-          atomicAdd(a.out_refs + p, 1);
-        else
-          need = 1;
+  // (one walk over all three, so that a small call's threads have one chain of
+  // loads each instead of three)
+  const long long new_from = static_cast<long long>(a.B) * width;
+  const long long rows_from = new_from + static_cast<long long>(a.rows) * width;
+  for (long long x = tid; x < rows_from + a.rows; x += ALL) {
+    if (x < new_from) {
+      const int b = static_cast<int>(x / width), i = static_cast<int>(x - static_cast<long long>(b) * width);
+      if (i >= used_pages(length(b), page_size)) continue;
+      const int p = entry(b, i, b);
+      if (p >= 0) atomicAdd(a.out_refs + p, -1);
+    } else if (x < rows_from) {
+      const long long y = x - new_from;
+      const int row = static_cast<int>(y / width), i = static_cast<int>(y - static_cast<long long>(row) * width);
+      const int s = source(row), len = s >= 0 ? length(s) : 0;
+      int out = -1;
+      if (i < used_pages(len, page_size)) {
+        const int p = entry(s, i, -1);
+        out = a.table.block_table[s * a.table.table_stride + i];
+        if (p >= 0 && i < len / page_size) atomicAdd(a.out_refs + p, 1);
+      }
+      a.out_table[row * a.out_stride + i] = out;
+    } else {
+      const int row = static_cast<int>(x - rows_from);
+      const int s = source(row), len = s >= 0 ? length(s) : 0;
+      a.out_seqlens[row] = len;
+      // a page that is being filled stays with the sequence's first row: one row
+      // counts it, whichever finds that none has been here
+      if (s >= 0 && atomicMin(w.first + s, row) == INT_MAX && len % page_size) {
+        const int p = entry(s, len / page_size, -1);
+        if (p >= 0) atomicAdd(a.out_refs + p, 1);
       }
     }
-    w.list_b[row] = need;
   }
   cluster_sync();
+  // whether a row that is not the first needs a page in its place
+  auto needs = [&](int row) {
+    const int s = source(row), len = s >= 0 ? length(s) : 0;
+    return len % page_size && __ldcg(w.first + s) != row && entry(s, len / page_size, -1) >= 0;
+  };
   // the free pages of the lowest ids, by rank, and the rows' ranks
-  const int part = (a.table.num_pages + kPlanCtas - 1) / kPlanCtas;
+  constexpr int COUNTING = kPlanCtas - 1;  // CTAs; the last one ranks the rows meanwhile
+  const int part = (a.table.num_pages + COUNTING - 1) / COUNTING;
   const long long all = a.table.num_pages;
   const int begin = static_cast<int>(min(static_cast<long long>(cta) * part, all));
   const int end = static_cast<int>(min(static_cast<long long>(begin) + part, all));
   auto is_free = [&](int p) { return __ldcg(a.out_refs + p) == 0; };
-  const int mine = count_pages(begin, end, scratch, is_free);
-  if (threadIdx.x == 0) w.counts[cta] = mine;
-  if (cta == 0) {
+  if (cta < COUNTING) {
+    const int mine = count_pages(begin, end, scratch, is_free);
+    if (threadIdx.x == 0) w.counts[cta] = mine;
+  } else {
     int needed = 0;
     for (int base = 0; base < a.rows; base += kPlanThreads) {
       const int row = base + static_cast<int>(threadIdx.x);
-      const int need = row < a.rows ? __ldcg(w.list_b + row) : 0;
+      const int need = row < a.rows && needs(row);
       int total;
       const int rank = needed + block_scan(need, scratch, total);
       if (row < a.rows) w.list_b[row] = need ? rank : -1;
@@ -208,13 +211,13 @@ __global__ void __cluster_dims__(kPlanCtas) __launch_bounds__(kPlanThreads, 1) f
   }
   cluster_sync();
   int before = 0, found = 0;
-  for (int c = 0; c < kPlanCtas; ++c) {
+  for (int c = 0; c < COUNTING; ++c) {
     const int n = __ldcg(w.counts + c);
     if (c < cta) before += n;
     found += n;
   }
   const int needed = __ldcg(w.pairs);
-  if (before < needed)
+  if (cta < COUNTING && before < needed)
     scan_pages(begin, end, before, scratch, is_free, [&](int p, int rank) {
       if (rank < needed) w.list_a[rank] = p;
     });
