@@ -725,7 +725,7 @@ __global__ void __launch_bounds__(Launch<FP8>::kThreads, 1)
         ++on;
         tc_fence_after();
       }
-      if (!sees) l = 0.f;
+      if (!sees) l = dl = 0.f;  // (dl too: +inf among what it does not see makes a NaN of it)
       // The row is acc_own * f_own + acc_other * f_other (a tile without keys
       // reads what was left in tensor memory, and drops it).  A sum is 0 only
       // where no key is seen; a NaN goes through.
