@@ -889,7 +889,7 @@ __global__ void __launch_bounds__(Launch<FP8>::kThreads, 1)
           return i < count && key < last ? pages[key / p.table.page_size] : -1;
         };
         int cur = page_of(lane), next = page_of(32 + lane);
-        // a lane's scale of a tile: of keys' groups of 16, then of values'; 1 for a
+        // a lane's scale of a tile: of keys' groups of 16, then of values'; 0 for a
         // group of no page.  Loaded a tile ahead.
         const int group = lane % kScales;
         auto scale_of = [&](int j, int pages_of_32) {
@@ -937,7 +937,7 @@ __global__ void __launch_bounds__(Launch<FP8>::kThreads, 1)
             }
             float* scales = reinterpret_cast<float*>(smem + L::kScaleOff) + (kvpos % kScaleTiles * kScales + group) * 4;
             if (lane < kScales) {
-              scales[0] = (scale != 0.f ? scale : 1.f) * p.scale_log2;
+              scales[0] = scale * p.scale_log2;
             } else if (lane < 2 * kScales) {
               // (the sum takes 2^-log2 of the same rounded logarithm, which drops out)
               const float log = scale != 0.f ? __log2f(scale) : 0.f;

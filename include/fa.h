@@ -603,8 +603,8 @@ fa_status fa_kv_append_fp8(const void* k, long long k_stride_b, long long k_stri
 /*
  * fa_fwd_paged and fa_fwd_shared_prefix over the cache in E4M3, with the same
  * workspaces.  Scales of values are fp32 numbers from 2^-32 to 2^60, those that a
- * row sees together within 2^60 of one another; scales of keys may be any with
- * which the scores are finite numbers.
+ * row sees together within 2^60 of one another; scales of keys may be any from 0 on
+ * with which the scores are finite numbers.
  *   With up to 32 rows a key head both products run on fp16, in which the E4M3
  * numbers are exact, as is a query (taken times a power of two) but for elements
  * below 2^-28 of their row's largest.  With more rows, and against a prefix, a

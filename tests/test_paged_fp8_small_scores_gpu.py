@@ -102,3 +102,31 @@ def test_a_batch_of_zeros(case):
         # 2^-22 of the logarithm of at most 2^(32 + 14 + 11), and as much for a merge
         assert ((lse[b, :, :n].cpu().double() - want).abs() <= 2.0 ** -21 * (57 + want)).all()
         assert torch.isneginf(lse[b, :, n:]).all()
+
+
+@pytest.mark.parametrize("q_scale", [0.0, 2.0 ** -60, 1.0, 100.0])
+@pytest.mark.parametrize("case", CASES, ids=ids)
+def test_keys_of_scale_zero(case, q_scale):
+    """Keys whose scales are 0 have scores of 0 whatever their numbers are."""
+    Hq, Hkv, Nq, d, page, prefix, lens_k, lens_q = case
+    q, c = make_batch(len(lens_k), Hq, Hkv, Nq, d, page, lens_k, seed=Nq + d, q_scale=q_scale)
+    live = torch.isfinite(c.scales[0])
+    c.scales[0] = torch.where(live, torch.zeros_like(c.scales[0]), c.scales[0])
+    c.update()
+    go(q, c, case, causal=Nq > 1)
+
+
+@pytest.mark.parametrize("case", CASES, ids=ids)
+def test_cells_of_scale_zero_beside_others(case):
+    """Every third cell of keys has the scale 0, or the smallest that the append
+    gives; every fifth query is zeros."""
+    Hq, Hkv, Nq, d, page, prefix, lens_k, lens_q = case
+    q, c = make_batch(len(lens_k), Hq, Hkv, Nq, d, page, lens_k, seed=3 + Nq + d)
+    q.view(-1, d)[::5] = 0.0
+    flat = c.scales[0].view(-1)
+    live = torch.isfinite(flat)
+    some = torch.arange(flat.numel())
+    flat[live & (some % 3 == 0)] = 0.0
+    flat[live & (some % 3 == 1)] = 2.0 ** -32
+    c.update()
+    go(q, c, case)
