@@ -172,7 +172,8 @@ struct TileLayout {
   static constexpr int V_FULL = RAW_EMPTY + kRawSlots;   // ... and in fp16
   static constexpr int V_EMPTY = V_FULL + kValueSlots;
   static constexpr int SCALES = V_EMPTY + kValueSlots;
-  static constexpr int Q_RAW = SCALES + (FP8 ? kScaleTiles : 0);  // rows in bf16
+  static constexpr int BEGUN = SCALES + (FP8 ? kScaleTiles : 0);  // the pieces' scales before this one are there
+  static constexpr int Q_RAW = BEGUN + (FP8 ? 2 : 0);    // rows in bf16
   static constexpr int Q_FULL = Q_RAW + (FP8 ? 2 : 0);
   static constexpr int Q_IN = FP8 ? Q_RAW : Q_FULL;      // what the loads of rows arrive on
   static constexpr int Q_EMPTY = Q_FULL + 2;
@@ -203,7 +204,8 @@ struct TileLayout {
   static_assert(kSmemBytes <= 227 * 1024, "shared memory of a CTA");
   // Scales are written behind the wait for a key slot, which is free once the
   // scores of the tile kKeySlots before it are there, and so the weights of the
-  // row tile's one before that (DUAL: two before it).
+  // row tile's one before that (DUAL: two before it).  A row tile that has had no
+  // keys waits until the producer has begun its piece (BEGUN).
   static_assert(!FP8 || kKeySlots + 2 <= kScaleTiles, "scales still in use");
 };
 static_assert(sizeof(Piece) <= 48, "a piece's room");
@@ -300,7 +302,10 @@ __global__ void __launch_bounds__(Launch<FP8>::kThreads, 1)
         mbar_init(bars + 8 * (L::V_EMPTY + s), 1);
       }
       for (int s = 0; s < kScaleTiles; ++s) mbar_init(bars + 8 * (L::SCALES + s), 1);
-      for (int t = 0; t < 2; ++t) mbar_init(bars + 8 * (L::Q_RAW + t), 1);
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(bars + 8 * (L::BEGUN + i), 1);
+        mbar_init(bars + 8 * (L::Q_RAW + i), 1);
+      }
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(bars + 8 * (L::Q_FULL + t), FP8 ? 4 : 1);
@@ -541,6 +546,13 @@ __global__ void __launch_bounds__(Launch<FP8>::kThreads, 1)
       const bool sees = lim0 > 0;
       if (!sees) lim0 = INT_MAX / 2;
       float m_ref = 0.f, l = 0.f, dl = 0.f;
+      if constexpr (FP8) {
+        // A row tile may have no keys for many pieces' tiles and come here before the
+        // scales of those tiles: their barriers, which have one bit of count, would
+        // then let it through to the last ones in the same place.
+        ok = tile_wait(BAR(L::BEGUN + (n & 1)), (n >> 1) & 1, wc_idle, SITE_TILE_CONVERT, n);
+        if (!ok) break;
+      }
       auto rescale = [&](float alpha) {
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
@@ -879,6 +891,7 @@ __global__ void __launch_bounds__(Launch<FP8>::kThreads, 1)
       bool ok = true;
       for (uint32_t n = 0; next_piece(n, ok); ++n) {
         const volatile Piece& x = pieces[n & 1];
+        if (FP8 && lane == 0) mbar_arrive(BAR(L::BEGUN + (n & 1)));
         const int head = x.head, b = x.b, tiles = x.tiles;
         const int* pages = PREFIX ? p.prefix_table : p.table.block_table + b * p.table.table_stride;
         const int first = origin + x.tile * kRows;
