@@ -453,11 +453,10 @@ __global__ void __launch_bounds__(kRopeThreads, 3) append_fp8_kernel(const Appen
     constexpr bool VALUE = decltype(value_tag)::value;
     float* scale_to = (VALUE ? a.v_scales : a.k_scales) +
                       (row >= 0 ? scale_at + static_cast<long long>(begin) * cells_of_page : 0);
-    uint8_t* to = (VALUE ? a.v_bytes : a.k_bytes) +
-                  (row >= 0 ? (row + row_in + static_cast<long long>(begin) * a.table.page_size) * D : 0);
+    uint8_t* to0 = (VALUE ? a.v_bytes : a.k_bytes) + (row >= 0 ? (row + row_in) * D : 0);  // of head 0
     const uint32_t* found = s_max[0] + group * WARPS;
 #pragma unroll 1
-    for (int h = begin; h < end; ++h, round ^= 1, scale_to += cells_of_page, to += a.table.page_size * D) {
+    for (int h = begin; h < end; ++h, round ^= 1, scale_to += cells_of_page) {
       const float before = has_old ? *scale_to : 0.f;
       next();
       uint32_t top = 0;                          // the largest magnitudes' bits, two side by side
@@ -494,6 +493,9 @@ __global__ void __launch_bounds__(kRopeThreads, 3) append_fp8_kernel(const Appen
         scale = before;
         inverse = __frcp_rn(before);
       }
+      // (a head of a page may be 2^37 bytes; an addition a head in 64 bits spills)
+      uint8_t* to = to0 + static_cast<unsigned long long>(static_cast<unsigned>(h)) *
+                              static_cast<unsigned>(a.table.page_size) * D;
       if (fresh) {
         float v[16];
         unpack<true>(raw, v);
