@@ -588,8 +588,11 @@ size_t fa_fwd_shared_prefix_workspace_bytes(int B, int Hq, int Hkv, int Nq, int 
  * scale, or raise it and have the older tokens' numbers rounded again; between
  * powers of two that changes only those that become subnormal.  A cell whose
  * first token is new takes nothing from what lay there before.  Infinities and
- * NaN are stored as NaN and do not count for the scale.  A page must not be
- * appended to from two sequences: fa_kv_fork gives each its own.
+ * NaN are stored as NaN and do not count for the scale.  Values above 448 * 2^60
+ * are stored as well, with scales above those that the attention takes.
+ *   A cell is the work of one group of threads: a page must not be appended to
+ * from two sequences (fa_kv_fork gives each its own), nor be named twice by new
+ * tokens of one, or the numbers of either and the scale of the other may stay.
  */
 fa_status fa_kv_append_fp8(const void* k, long long k_stride_b, long long k_stride_h, long long k_stride_n,
                            const void* v, long long v_stride_b, long long v_stride_h, long long v_stride_n,
@@ -602,9 +605,9 @@ fa_status fa_kv_append_fp8(const void* k, long long k_stride_b, long long k_stri
 
 /*
  * fa_fwd_paged and fa_fwd_shared_prefix over the cache in E4M3, with the same
- * workspaces.  Scales of values are fp32 numbers from 2^-32 to 2^60, those that a
- * row sees together within 2^60 of one another; scales of keys may be any from 0 on
- * with which the scores are finite numbers.
+ * workspaces.  Scales of values are fp32 numbers from 2^-32, which the append
+ * gives to zeros, to 2^60; scales of keys may be any from 0 on with which the
+ * scores are finite numbers.
  *   With up to 32 rows a key head both products run on fp16, in which the E4M3
  * numbers are exact, as is a query (taken times a power of two) but for elements
  * below 2^-28 of their row's largest.  With more rows, and against a prefix, a
@@ -661,7 +664,10 @@ typedef struct {
  *     sequence.  Every other such row gets a page of its own, and the page's
  *     tokens are copied there in every tensor: rows behind them are left as
  *     they were.
- *   - Those pages are the free ones of the lowest ids, in the order of the
+ *   - Other old sequences that name the page too are not looked for: where a
+ *     length has been shortened into a page that an earlier fork shared, the
+ *     sequences go on sharing it, and none may be appended to there.
+ *   - The pages for copies are the free ones of the lowest ids, in the order of the
  *     rows; pages that this call has freed are among them.
  * Where too few are free, the rows that come last have -1 in their tables, and
  * fa_sync_status reports FA_ERR_NO_PAGES.  A used entry outside [0, num_pages) is
@@ -672,9 +678,10 @@ typedef struct {
  *   out_table : [rows][max_pages], stride out_stride >= max_pages; entries behind
  *               a row's pages are -1.  out_seqlens: [rows]; out_refs:
  *               [num_pages], refs less the old rows' entries plus the new ones'.
- *               None may overlap another or an input, which is left as it was
- *               but for the pages copied to: a program keeps two sets and
- *               swaps them.
+ *               None may overlap another or an input, from its first entry to
+ *               its last (tables whose rows take turns do).  Inputs are left as
+ *               they were but for the pages copied to: a program keeps two sets
+ *               and swaps them.
  *   workspace : fa_kv_fork_workspace_bytes(B, rows) bytes, 16-byte aligned, used by
  *               one call at a time; or NULL, as in fa_fwd_paged.
  */
@@ -698,7 +705,7 @@ size_t fa_kv_fork_workspace_bytes(int B, int rows);
  *   new_ids   : [num_pages], where each page in use is now, -1 for the others:
  *               what other tables that name pages are to be changed by.
  *   workspace : fa_kv_compact_workspace_bytes(num_pages) bytes, as fa_kv_fork's.
- * No output may overlap another or an input.
+ * No output may overlap another or an input, as there.
  */
 fa_status fa_kv_compact(const fa_page_tensor* tensors, int count, int num_pages, int page_size, const int* block_table,
                         long long table_stride, int max_pages, const int* seqlens_k, int B, const int* refs,

@@ -130,3 +130,23 @@ def test_cells_of_scale_zero_beside_others(case):
     flat[live & (some % 3 == 1)] = 2.0 ** -32
     c.update()
     go(q, c, case)
+
+
+@pytest.mark.parametrize("Hq,Hkv,Nq,prefix", [(4, 2, 1, 0), (8, 2, 4, 0), (8, 2, 8, 0), (4, 2, 40, 0), (4, 2, 100, 0),
+                                              (4, 2, 2, 128)])
+@pytest.mark.parametrize("high", [30, 45, 60])
+@pytest.mark.parametrize("q_scale", [0.0, 1.0, 10.0])
+def test_values_of_the_smallest_scale_beside_large_ones(Hq, Hkv, Nq, prefix, high, q_scale):
+    """Values' cells of 2^-32, which the append gives to zeros, in turn with cells
+    of up to 2^60, one or eight of the small ones at a time."""
+    d, page, lens = 128, 64, [1500, 200 + Nq]
+    for group in (1, 8):
+        q, c = make_batch(2, Hq, Hkv, Nq, d, page, lens, seed=8, q_scale=q_scale)
+        kw = with_prefix(c, prefix, lens) if prefix else {}
+        cells = torch.arange(c.scales[1].numel()).view(c.scales[1].shape)
+        small = cells // group % 2 == 0
+        live = torch.isfinite(c.scales[1])
+        c.scales[1] = torch.where(live, torch.where(small, 2.0 ** -32, 2.0 ** high), c.scales[1])
+        c.update()
+        o, lse = run(q, c, lens, **kw)
+        check_both(o, lse, reference(q, c, lens, None, True), q, c, way_of(Hq, Hkv, Nq, prefix))
