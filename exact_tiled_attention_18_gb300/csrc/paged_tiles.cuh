@@ -578,11 +578,6 @@ __global__ void __launch_bounds__(Launch<FP8>::kThreads, 1)
         const int lim = lim0 - j * stride;
         if constexpr (FP8) {
           const uint32_t scales = sbase + L::kScaleOff + at % kScaleTiles * kScales * 16;
-          // What scores of a group of keys are multiplied by: not 0, for a masked one
-          // is -inf.  (The product underflows for a row of zeros over cells of the
-          // smallest scales; scores are below 2^26, so that the least factor stands
-          // for 0 as well.)
-          auto factor = [&](float k) { return max_nan(k * grow, FLT_MIN); };
           if (__any_sync(0xffffffffu, lim < kRows)) {
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) {
@@ -613,7 +608,7 @@ __global__ void __launch_bounds__(Launch<FP8>::kThreads, 1)
               const float t1 = fmax3(fmax3(x(0), x(1), x(2)), fmax3(x(3), x(4), x(5)), fmax3(x(6), x(7), x(8)));
               const float t2 = fmax3(fmax3(x(9), x(10), x(11)), fmax3(x(12), x(13), x(14)), x(15));
               const float2 k = ld_shared_f2(scales + 16 * (4 * h + b));
-              top = fmaxf(top, fmaf(fmaxf(t1, t2), factor(k.x), k.y));
+              top = fmaxf(top, fmaf(fmaxf(t1, t2), k.x * grow, k.y));  // (-inf * 0 is passed over)
             }
           }
           if (j == 0) {
@@ -639,7 +634,10 @@ __global__ void __launch_bounds__(Launch<FP8>::kThreads, 1)
             for (int b = 0; b < 4; ++b) {  // 16 columns of one scale each
               uint32_t k[4];
               ld_shared_v4(scales + 16 * (4 * c + b), k);
-              const float mul = factor(__uint_as_float(k[0])), add = __uint_as_float(k[1]) + add0;
+              // (not 0, for a masked score is -inf: the product underflows for a row of
+              // zeros over a cell of the smallest scale; scores are below 2^26, so that
+              // the least factor stands for 0 as well)
+              const float mul = max_nan(__uint_as_float(k[0]) * grow, FLT_MIN), add = __uint_as_float(k[1]) + add0;
               const uint64_t c2 = f2_pack(mul, mul), n2 = f2_pack(add, add);
               uint64_t sum = f2_pack(0.f, 0.f);
 #pragma unroll
