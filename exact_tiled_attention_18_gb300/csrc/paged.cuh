@@ -13,7 +13,8 @@ namespace fa {
 // takes 128 whether they are there or not.  (8 heads; here and there, us.  8
 // sequences x 8192 keys: 24 rows 55 and 57, 32 rows 62 and 57; 64 x 1000 keys: 57
 // and 77, 65 and 77; 38 x 512 keys: 18 and 29, 21 and 30.  64 rows are 58, 79
-// and 29 there.)
+// and 29 there.  Over E4M3 24 and 32 rows 42
+// and 53, 57 and 53; 47 and 91, 65 and 91; 15 and 33, 20 and 33.)
 constexpr int kStepRows = 32;
 constexpr int kLineSequences = 256;    // sequences a launch of the step kernel: the line's table is in shared memory
 constexpr int kLineWords = 528;        // 4-byte words of a line in the workspace, a multiple of 4

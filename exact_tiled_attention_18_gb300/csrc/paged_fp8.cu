@@ -15,9 +15,8 @@
 //    times the largest so far where that is more (what a tile adds below that is
 //    nothing).  The sum of the p_j takes w_j / sv_j.
 //
-// (mma on E4M3 operands is no instruction of this GPU's but a dozen conversions to
-// fp16 around two of fp16, done again for every use of a fragment: 8 sequences x 8
-// heads x 8192 keys 35 us with up to 8 rows and 61 with 16 that way.)
+// (With mma on E4M3 operands for the score product instead 8 sequences x 8 heads x
+// 8192 keys were 35 us with up to 8 rows and 61 with 16, the long case below 351.)
 //
 // paged_steps_fp8_kernel: the work is divided as in paged_steps_kernel (paged.cu),
 // with tiles of 128 keys, the same number of bytes.  Each compute warp multiplies
@@ -33,9 +32,9 @@
 // both.
 //
 // Bound by HBM where there are keys enough: 8 sequences x 32 heads x 32768 keys, one
-// row a head, 308 us = 7.0 TB/s of keys and values (a step reads only, the copy that
+// row a head, 308 to 313 us = 6.9 to 7.0 TB/s of keys and values (a step reads only, the copy that
 // peaks are taken from writes too).  32 sequences of 100 to 16384 keys, 32 heads on 4,
-// 25.1 us, of which about 9 are the start (lengths, page ids, first tiles) and the
+// 23.6 to 25.1 us, of which about 9 are the start (lengths, page ids, first tiles) and the
 // merge; one sequence of 1000 keys 8.5 us in a graph, all latency.  8 sequences x 8
 // heads x 8192 keys 29.4 us with 1 to 8 rows a head, 35.5 with 16, 42 with 24 and 57
 // with 32 (bf16 48, 50, 55, 62): with more rows the warps' instructions bound it, and

@@ -64,7 +64,7 @@
 //    tile's values, and zero those behind the last key.
 //
 // Measured: the two chunks 341 us = 1172 TFLOP/s, 256 sequences x 64 heads on 8 behind
-// 32768 shared keys 252 us (218 in this kernel), 24 sequences of 4 drafted tokens
+// 32768 shared keys 254 us (218 in this kernel), 24 sequences of 4 drafted tokens
 // behind 8208 keys 31.6.  A step (a key tile with both row tiles) has 2048 cycles
 // of products, as in bf16, and takes 3270 to 3350 in a long piece (bf16 3060 to 3140):
 // the chain score product - softmax - value product of either row tile bounds it, not

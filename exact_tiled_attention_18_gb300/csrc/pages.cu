@@ -9,13 +9,15 @@
 // continues a sequence, the free pages of the lowest ids), never by which thread
 // comes first: additions to a count are atomic and commute.
 //
-// The copy is bound by HBM (a byte read and a byte written) or, for a few tokens of a
-// few sequences, by launch latency.  It reads the list of pages and its length on
-// the device.
+// The copy of whole pages is bound by HBM (a byte read and a byte written).  Where many
+// rows copy one page it comes from L2, half the bytes go to DRAM, and the instructions
+// bound it (128 samples: issue slots 74% busy, DRAM 46%); a few tokens of a few
+// sequences are launch latency.  It reads the list of pages and its length on the
+// device.
 //
 // Measured, in a graph: 128 samples of two prompts of 1001 and 4000 tokens, each with
-// a page of its own in the tensors of 8 layers, 74 us; about 300 of 1200 pages moved
-// (in E4M3, 8 layers) 106 us = 5.9 TB/s; a beam search's reordering of 16 rows 12.2 us
+// a page of its own in the tensors of 8 layers, 72 to 75 us; about 300 of 1200 pages moved
+// (in E4M3, 8 layers) 106 to 112 us = 5.6 to 5.9 TB/s; a beam search's reordering of 16 rows 12.2 us
 // and a small cache's compaction 10.5, of which the tables' passes are about 8 and 7:
 // chains of loads and atomics, a microsecond or more each.  One after the other in
 // every thread where they now run side by side, and one more, 13.7; one, two and four

@@ -325,7 +325,7 @@ __global__ void __launch_bounds__(kRopeThreads) append_kernel(const AppendArgs a
 // values can go: the scale then does not depend on the position.
 //
 // Measured: four prompts of 2048 to 8192 tokens, 16 + 16 + 16 heads, d = 128, queries
-// rotated too, 65 us = 5.9 TB/s of what has to be read and written (0.87 of the copy
+// rotated too, 66 us = 5.8 TB/s of what has to be read and written (0.86 of the copy
 // rate; issue slots and DRAM both 68% busy), a step of 8 sequences 4.2 us a call in a graph.
 // Loads through registers, two heads at a time, 99 us; one after the other 128.
 //

@@ -671,7 +671,8 @@ typedef struct {
  *     rows; pages that this call has freed are among them.
  * Where too few are free, the rows that come last have -1 in their tables, and
  * fa_sync_status reports FA_ERR_NO_PAGES.  A used entry outside [0, num_pages) is
- * reported as FA_ERR_BAD_PAGE, passed on as it is, and counts nothing.
+ * reported as FA_ERR_BAD_PAGE, passed on as it is, and counts nothing (so the
+ * tables of a batch behind a shared prefix name its pages, too).
  *   block_table, seqlens_k : of the old batch [B][max_pages], [B], as
  *               fa_fwd_paged; only the pages that seqlens_k reaches are read
  *               (negative: 0, at most max_pages * page_size).
