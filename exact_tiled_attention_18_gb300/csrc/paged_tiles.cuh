@@ -34,7 +34,7 @@
 // Measured (whole calls): a square prompt of 16 heads x 16384 tokens 1574
 // TFLOP/s, 32 heads under the causal rule 1409 to 1442; two chunks of 1000
 // tokens, 32 heads on 8, over 9001 and 16384 keys 290 us = 1378
-// TFLOP/s; 2048 rows of 8 heads behind 32768 shared keys 190 us in this kernel.  The tensor
+// TFLOP/s; 2048 rows of 8 heads behind 32768 shared keys 193 us in this kernel.  The tensor
 // pipe is 59 to 61% busy in the last two, DRAM 12 to 14%.  The smallest call, 64
 // rows of 8 heads over 512 keys, is 12.8 us: 1.7 until the line is there, 1.8 until a
 // piece is worked out, 1.5 until its first scores, 2 for the softmax and the second
@@ -64,11 +64,11 @@
 //    tile's values, and zero those behind the last key.
 //
 // Measured: the two chunks 341 us = 1172 TFLOP/s, 256 sequences x 64 heads on 8 behind
-// 32768 shared keys 254 us (218 in this kernel), 24 sequences of 4 drafted tokens
+// 32768 shared keys 254 us (221 in this kernel), 24 sequences of 4 drafted tokens
 // behind 8208 keys 31.6.  A step (a key tile with both row tiles) has 2048 cycles
 // of products, as in bf16, and takes 3270 to 3350 in a long piece (bf16 3060 to 3140):
 // the chain score product - softmax - value product of either row tile bounds it, not
-// the tensor cores (52 to 53% busy) nor DRAM (4 to 5%).  Copies that skip work (two
+// the tensor cores (51 to 52% busy) nor DRAM (4 to 5%).  Copies that skip work (two
 // chunks, 384 us at the time): without the conversion of values 376, with half the
 // score products 394, without exponentials 333.  A piece begins 4700 cycles later for
 // its rows' conversion.
